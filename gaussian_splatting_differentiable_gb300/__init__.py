@@ -1,7 +1,9 @@
 """Tile-based differentiable rasterization of projected 2D Gaussian splats on GB300.
 
 The compute path is libss.so (hand-written CUDA for sm_103a behind the C ABI
-of include/ss.h, include/ss_project.h and include/ss_ssim.h).  This module is its thin Python binding: each ss_* function
+of include/ss.h, include/ss_project.h and include/ss_ssim.h, and of the training
+operators' include/ss_embed.h, include/ss_norm.h and include/ss_clip.h).  This
+module is its thin Python binding: each ss_* function
 here has the C function's name and arguments and only marshals torch tensors
 (device memory) and streams into pointers.  PyTorch provides memory and
 streams; every step of the path runs in the library's kernels.  There is no
@@ -16,8 +18,8 @@ import dataclasses
 import torch
 
 from . import _lib
-from ._lib import (SS_ACCUM_WEIGHT, SS_DISTORTION, SS_ERR_CAPACITY, SS_ERR_DEVICE,  # noqa: F401
-                   SS_ERR_TIMEOUT, SS_MEDIAN_DEPTH, SS_OK, SS_RECORDS_CLEARED, SS_WEIGHT_STATS,
+from ._lib import (SS_ACCUM_WEIGHT, SS_BF16, SS_DISTORTION, SS_ERR_CAPACITY,  # noqa: F401
+                   SS_ERR_DEVICE, SS_ERR_TIMEOUT, SS_F16, SS_F32, SS_MEDIAN_DEPTH, SS_OK, SS_RECORDS_CLEARED, SS_WEIGHT_STATS,
                    STATUS_NAMES, SsGrads, SsSplats)
 
 _L = _lib.load()
@@ -379,6 +381,304 @@ class SsimLoss:
     def __call__(self, img, target, stream=None) -> torch.Tensor:
         ss_ssim_loss(img, target, self.lam, self.loss, self.grad, self.workspace, stream)
         return self.grad
+
+
+# ------------------------------------------------------------------ training operators
+
+DTYPE_CODES = {torch.float32: SS_F32, torch.float16: SS_F16, torch.bfloat16: SS_BF16}
+
+
+def _dtype(t, name: str) -> int:
+    code = DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float32, float16 or bfloat16 (got %s)" % (name, t.dtype))
+    return code
+
+
+def _rows(t, name: str, D: int, n=None):
+    """(pointer, row stride) of a [n, D] device tensor with contiguous rows."""
+    if t.dim() != 2 or t.shape[1] != D or (n is not None and t.shape[0] != n):
+        raise ValueError("%s must be [%s, %d] (got %s)" % (name, "n" if n is None else n, D,
+                                                           tuple(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    rs, cs = t.stride()
+    if cs != 1 and D > 1:
+        raise ValueError("%s must have contiguous rows (column stride %d)" % (name, cs))
+    if t.shape[0] <= 1:
+        rs = max(rs, D)      # no second row: any stride will do
+    if rs < D:
+        raise ValueError("%s has overlapping rows (row stride %d < %d)" % (name, rs, D))
+    return t.data_ptr(), rs
+
+
+def _vector(t, name: str, size: int, dtype=None) -> int:
+    if t.dim() != 1 or t.shape[0] != size or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("%s must be a contiguous CUDA vector of %d (got %s)"
+                         % (name, size, tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    return t.data_ptr()
+
+
+def _ids(ids, n=None):
+    """(pointer, bytes of an id)."""
+    if ids.dtype == torch.int64:
+        size = 8
+    elif ids.dtype == torch.int32:
+        size = 4
+    else:
+        raise ValueError("ids must be int32 or int64 (got %s)" % ids.dtype)
+    if ids.dim() != 1 or not ids.is_cuda or not ids.is_contiguous() or \
+            (n is not None and ids.shape[0] != n):
+        raise ValueError("ids must be a contiguous CUDA vector%s (got %s)"
+                         % ("" if n is None else " of %d" % n, tuple(ids.shape)))
+    return ids.data_ptr(), size
+
+
+def _workspace(nbytes: int, device):
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+# ---- scaled lookup (ss_embed.h)
+
+def ss_embed_workspace_bytes(n: int, V: int, D: int) -> int:
+    return int(_L.ss_embed_workspace_bytes(n, V, D))
+
+
+def ss_embed_fwd(table, ids, scale: float, out, stream=None) -> None:
+    """out[i] = scale * table[ids[i]]; zeros where ids[i] is outside [0, V).
+    table: [V, D], out: [n, D] of the same type; ids: int32 or int64 [n]."""
+    V, D = table.shape
+    code = _dtype(table, "table")
+    if out.dtype != table.dtype:
+        raise ValueError("out must have the table's type")
+    idp, idb = _ids(ids)
+    n = ids.shape[0]
+    tp, ts = _rows(table, "table", D)
+    op, os_ = _rows(out, "out", D, n)
+    st = _L.ss_embed_fwd(tp, code, V, D, ts, idp, idb, n, scale, op, os_, _stream(stream))
+    if st:
+        _check(st, "ss_embed_fwd")
+
+
+def ss_embed_bwd(dout, ids, scale: float, dtable, workspace, stream=None) -> None:
+    """dtable[v] = scale * the sum of the rows of dout whose id is v; every row
+    of dtable [V, D] (dout's type or float32) is overwritten."""
+    V, D = dtable.shape
+    code, gcode = _dtype(dout, "dout"), _dtype(dtable, "dtable")
+    idp, idb = _ids(ids)
+    n = ids.shape[0]
+    dp, ds = _rows(dout, "dout", D, n)
+    gp, gs = _rows(dtable, "dtable", D)
+    st = _L.ss_embed_bwd(dp, code, ds, idp, idb, n, V, D, scale, gp, gcode, gs,
+                         workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st:
+        _check(st, "ss_embed_bwd")
+
+
+class Embedding:
+    """Buffers of the scaled lookup and its gradient for n ids into a table
+    of V rows of D values: `out` [n, D] and `grad` [V, D]."""
+
+    def __init__(self, n: int, V: int, D: int, scale: float = 1.0, dtype=torch.float32,
+                 grad_dtype=None, device="cuda", forward: bool = True, backward: bool = True):
+        d = torch.device(device)
+        self.n, self.V, self.D, self.scale = n, V, D, float(scale)
+        self.out = torch.empty(n, D, dtype=dtype, device=d) if forward else None
+        self.grad = self.workspace = None
+        if backward:
+            nb = ss_embed_workspace_bytes(n, V, D)
+            if nb == 0:
+                raise ValueError("sizes out of range")
+            self.grad = torch.empty(V, D, dtype=grad_dtype or dtype, device=d)
+            self.workspace = _workspace(nb, d)
+
+    def forward(self, table, ids, stream=None) -> torch.Tensor:
+        ss_embed_fwd(table, ids, self.scale, self.out, stream)
+        return self.out
+
+    def backward(self, dout, ids, stream=None) -> torch.Tensor:
+        ss_embed_bwd(dout, ids, self.scale, self.grad, self.workspace, stream)
+        return self.grad
+
+    def check(self, stream=None) -> None:
+        """Raise if the last backward's sort gave up a bounded wait."""
+        _check(_L.ss_embed_status(_ptr(self.workspace), _stream(stream)), "ss_embed_status")
+
+
+# ---- layer norm (ss_norm.h)
+
+def ss_layer_norm_workspace_bytes(n: int, D: int) -> int:
+    return int(_L.ss_layer_norm_workspace_bytes(n, D))
+
+
+def _param(t, name: str, D: int, code: int, dtype) -> tuple:
+    """(pointer, type code) of a parameter vector of the rows' type or float32."""
+    p = _vector(t, name, D)
+    if t.dtype != dtype and t.dtype != torch.float32:
+        raise ValueError("%s must be float32 or the rows' type (got %s)" % (name, t.dtype))
+    return p, (code if t.dtype == dtype else SS_F32)
+
+
+def ss_layer_norm_fwd(x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None) -> None:
+    """y = (x - mean) * rstd * gamma + beta over the rows of x [n, D]; gamma
+    and beta [D] (one type, the rows' or float32) or None; mean, rstd:
+    float32 [n] or None."""
+    n, D = x.shape
+    code = _dtype(x, "x")
+    if y.dtype != x.dtype:
+        raise ValueError("y must have x's type")
+    xp, xs = _rows(x, "x", D)
+    yp, ys = _rows(y, "y", D, n)
+    gp, gc = (None, None) if gamma is None else _param(gamma, "gamma", D, code, x.dtype)
+    bp, bc = (None, None) if beta is None else _param(beta, "beta", D, code, x.dtype)
+    if gc is not None and bc is not None and gc != bc:
+        raise ValueError("gamma and beta must have one type")
+    pc = gc if gc is not None else (bc if bc is not None else SS_F32)
+    mp = None if mean is None else _vector(mean, "mean", n, torch.float32)
+    rp = None if rstd is None else _vector(rstd, "rstd", n, torch.float32)
+    st = _L.ss_layer_norm_fwd(xp, code, xs, n, D, gp, bp, pc, eps, yp, ys, mp, rp,
+                              _stream(stream))
+    if st:
+        _check(st, "ss_layer_norm_fwd")
+
+
+def ss_layer_norm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace,
+                      stream=None) -> None:
+    """dx [n, D], and dgamma, dbeta [D] (both or neither) from dy, the
+    forward's x, gamma, mean and rstd; dx may be dy or x."""
+    n, D = x.shape
+    code = _dtype(x, "x")
+    if dy.dtype != x.dtype or dx.dtype != x.dtype:
+        raise ValueError("dy and dx must have x's type")
+    dyp, dys = _rows(dy, "dy", D, n)
+    xp, xs = _rows(x, "x", D)
+    dxp, dxs = _rows(dx, "dx", D, n)
+    gp, pc = (None, None) if gamma is None else _param(gamma, "gamma", D, code, x.dtype)
+    dgp = dbp = None
+    for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
+        if t is None:
+            continue
+        p, c = _param(t, name, D, code, x.dtype)
+        if pc is not None and c != pc:
+            raise ValueError("gamma, dgamma and dbeta must have one type")
+        pc = c
+        if name == "dgamma":
+            dgp = p
+        else:
+            dbp = p
+    mp = _vector(mean, "mean", n, torch.float32)
+    rp = _vector(rstd, "rstd", n, torch.float32)
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    st = _L.ss_layer_norm_bwd(dyp, dys, xp, xs, code, n, D, gp, SS_F32 if pc is None else pc, mp,
+                              rp, dxp, dxs, dgp, dbp, wp, wb, _stream(stream))
+    if st:
+        _check(st, "ss_layer_norm_bwd")
+
+
+class LayerNorm:
+    """Buffers of the layer norm of n rows of D values: `y`, `mean`, `rstd`
+    of the forward, `dx` and `grads` (dgamma, dbeta) of the backward."""
+
+    def __init__(self, n: int, D: int, eps: float = 1e-5, dtype=torch.float32,
+                 param_dtype=torch.float32, device="cuda", forward: bool = True,
+                 backward: bool = True):
+        d = torch.device(device)
+        self.n, self.D, self.eps = n, D, float(eps)
+        self.y = self.mean = self.rstd = self.dx = self.grads = self.workspace = None
+        if forward:
+            self.y = torch.empty(n, D, dtype=dtype, device=d)
+            self.mean = torch.empty(n, dtype=torch.float32, device=d)
+            self.rstd = torch.empty(n, dtype=torch.float32, device=d)
+        if backward:
+            nb = ss_layer_norm_workspace_bytes(n, D)
+            if nb == 0:
+                raise ValueError("sizes out of range")
+            self.dx = torch.empty(n, D, dtype=dtype, device=d)
+            self.grads = {k: torch.empty(D, dtype=param_dtype, device=d)
+                          for k in ("dgamma", "dbeta")}
+            self.workspace = _workspace(nb, d)
+
+    def forward(self, x, gamma=None, beta=None, stream=None) -> torch.Tensor:
+        ss_layer_norm_fwd(x, gamma, beta, self.eps, self.y, self.mean, self.rstd, stream)
+        return self.y
+
+    def backward(self, dy, x, gamma=None, mean=None, rstd=None, stream=None) -> torch.Tensor:
+        """mean, rstd: the forward's, this object's own if not given."""
+        ss_layer_norm_bwd(dy, x, gamma, self.mean if mean is None else mean,
+                          self.rstd if rstd is None else rstd, self.dx, self.grads["dgamma"],
+                          self.grads["dbeta"], self.workspace, stream)
+        return self.dx
+
+
+# ---- gradient norm and clipping (ss_clip.h)
+
+def ss_clip_workspace_bytes(n_tensors: int) -> int:
+    return int(_L.ss_clip_workspace_bytes(n_tensors))
+
+
+def _tensor_list(grads, outs):
+    """The host array of ss_tensor for `grads`, results into `outs` (None: in place)."""
+    if outs is not None and len(outs) != len(grads):
+        raise ValueError("%d outputs for %d gradients" % (len(outs), len(grads)))
+    arr = (_lib.SsTensor * max(len(grads), 1))()
+    for k, g in enumerate(grads):
+        o = g if outs is None else outs[k]
+        code = _dtype(g, "gradient %d" % k)
+        if not g.is_cuda or not g.is_contiguous():
+            raise ValueError("gradient %d must be a contiguous CUDA tensor" % k)
+        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or
+                           not o.is_contiguous()):
+            raise ValueError("output %d must be a contiguous CUDA tensor like its gradient" % k)
+        arr[k] = _lib.SsTensor(g.data_ptr(), o.data_ptr(), g.numel(), code, 0)
+    return arr
+
+
+def ss_grad_clip(tensors, n: int, max_norm: float, eps: float, result, workspace,
+                 stream=None) -> None:
+    """tensors: the ctypes array of SsTensor (see GradClip); result: float32[2]
+    device tensor, (norm, coefficient)."""
+    st = _L.ss_grad_clip(tensors, n, max_norm, eps, result.data_ptr(), workspace.data_ptr(),
+                         workspace.nbytes, _stream(stream))
+    if st:
+        _check(st, "ss_grad_clip")
+
+
+def ss_grad_norm(tensors, n: int, result, workspace, stream=None) -> None:
+    st = _L.ss_grad_norm(tensors, n, result.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                         _stream(stream))
+    if st:
+        _check(st, "ss_grad_norm")
+
+
+class GradClip:
+    """The gradients of a step, clipped together: clip(max_norm) scales them
+    in place, or into `outs`, by min(1, max_norm / (norm + eps)) and returns
+    `result`, the device float32[2] (norm, coefficient); the coefficient is 0
+    and nothing is scaled where the norm is not finite.  The lists are read
+    once, here: their tensors must stay where they are."""
+
+    def __init__(self, grads, outs=None, eps: float = 1e-6, device="cuda"):
+        d = torch.device(device)
+        self.grads, self.outs = list(grads), None if outs is None else list(outs)
+        self.eps = float(eps)
+        self.n = len(self.grads)
+        nb = ss_clip_workspace_bytes(self.n)
+        if nb == 0:
+            raise ValueError("too many tensors")
+        self._list = _tensor_list(self.grads, self.outs)
+        self.result = torch.zeros(2, dtype=torch.float32, device=d)
+        self.workspace = _workspace(nb, d)
+
+    def __call__(self, max_norm: float, stream=None) -> torch.Tensor:
+        ss_grad_clip(self._list, self.n, max_norm, self.eps, self.result, self.workspace, stream)
+        return self.result
+
+    def norm(self, stream=None) -> torch.Tensor:
+        """result = (norm, 1 if it is finite else 0); scales nothing."""
+        ss_grad_norm(self._list, self.n, self.result, self.workspace, stream)
+        return self.result
 
 
 # ------------------------------------------------------------------ whole path

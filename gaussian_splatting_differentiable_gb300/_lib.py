@@ -1,5 +1,6 @@
 """ctypes prototypes of libss.so (the C ABI declared in include/ss.h,
-include/ss_project.h and include/ss_ssim.h).
+include/ss_project.h and include/ss_ssim.h, and the training operators of
+include/ss_embed.h, include/ss_norm.h and include/ss_clip.h).
 
 Loading fails with an ImportError when the library has not been built: there
 is no fallback implementation behind this package.
@@ -24,6 +25,7 @@ SS_MEDIAN_DEPTH = 2
 SS_WEIGHT_STATS = 4
 SS_DISTORTION = 8
 SS_RECORDS_CLEARED = 16   # bwd: the forward already cleared the gradient records
+SS_F32, SS_F16, SS_BF16 = range(3)   # ss_dtype
 
 
 class SsSplats(ctypes.Structure):
@@ -92,6 +94,30 @@ PROTOTYPES = {
     "ss_ssim_loss": (ctypes.c_int, [P, P, I32, I32, I32, ctypes.c_float, P, P, P, SZ, P]),
 }
 
+
+
+class SsTensor(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+# the training operators: ss_embed.h, ss_norm.h, ss_clip.h
+F32 = ctypes.c_float
+TRAIN_PROTOTYPES = {
+    "ss_embed_fwd": (ctypes.c_int, [P, I32, I64, I32, I64, P, I32, I64, F32, P, I64, P]),
+    "ss_embed_workspace_bytes": (SZ, [I64, I64, I32]),
+    "ss_embed_bwd": (ctypes.c_int, [P, I32, I64, P, I32, I64, I64, I32, F32, P, I32, I64, P, SZ,
+                                    P]),
+    "ss_embed_status": (ctypes.c_int, [P, P]),
+    "ss_layer_norm_fwd": (ctypes.c_int, [P, I32, I64, I64, I32, P, P, I32, F32, P, I64, P, P, P]),
+    "ss_layer_norm_workspace_bytes": (SZ, [I64, I32]),
+    "ss_layer_norm_bwd": (ctypes.c_int, [P, I64, P, I64, I32, I64, I32, P, I32, P, P, P, I64, P,
+                                         P, P, SZ, P]),
+    "ss_clip_workspace_bytes": (SZ, [I32]),
+    "ss_grad_clip": (ctypes.c_int, [P, I32, F32, F32, P, P, SZ, P]),
+    "ss_grad_norm": (ctypes.c_int, [P, I32, P, P, SZ, P]),
+}
+
 _lib = None
 
 
@@ -105,7 +131,7 @@ def load(path: str | None = None):
         raise ImportError("libss.so is not built (%s); run "
                           "`python -c 'import __graft_entry__ as g; g.build()'`" % p)
     lib = ctypes.CDLL(p)
-    for name, (res, args) in PROTOTYPES.items():
+    for name, (res, args) in {**PROTOTYPES, **TRAIN_PROTOTYPES}.items():
         f = getattr(lib, name)
         f.restype = res
         f.argtypes = args
