@@ -277,8 +277,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__
             for (int u = 0; u < kBatch; ++u) w[u] = i + u < hi ? __ldg(p.words + i + u) : ~0ull;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-#pragma unroll
-                for (int k = 0; k < N; ++k) x[u].v[k] = from_float<T>(0.0f);
+                x[u].clear();
                 const uint32_t pos = uint32_t(w[u]);
                 if (uint32_t(w[u] >> 32) < p.V && int64_t(pos) < p.n)
                     x[u] = load_vec<T, N>(dout + int64_t(pos) * p.in_stride + int64_t(col) * N);
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__
                     for (int k = 0; k < N; ++k) acc[k] = 0.0f;
                 }
 #pragma unroll
-                for (int k = 0; k < N; ++k) acc[k] += to_float(x[u].v[k]);
+                for (int k = 0; k < N; ++k) acc[k] += x[u].get(k);
             }
         }
         if (open) {

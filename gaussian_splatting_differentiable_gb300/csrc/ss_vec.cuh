@@ -29,29 +29,73 @@ __device__ __forceinline__ __half from_float<__half>(float v) { return __float2h
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// N elements of T, loaded and stored as one access (N * sizeof(T) <= 16
-// bytes, address aligned to it) or, with 32 bytes, as two.
+// N elements of T as they lie in memory: one of them, or 16 bytes held as four
+// words (an array of 16-bit class types would be loaded element by element).
 template <typename T, int N>
-struct alignas(N * sizeof(T) > 16 ? 16 : N * sizeof(T)) Vec {
-    T v[N];
+struct Vec {
+    static_assert(N * sizeof(T) == 16, "a vector is 16 bytes");
+    uint32_t w[4];
+    __device__ __forceinline__ float get(int i) const { return get_as(i, T()); }
+    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+
+  private:
+    __device__ __forceinline__ float get_as(int i, float) const { return __uint_as_float(w[i]); }
+    __device__ __forceinline__ float get_as(int i, __nv_bfloat16) const {
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    __device__ __forceinline__ float get_as(int i, __half) const {
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu)));
+    }
+};
+template <typename T>
+struct Vec<T, 1> {
+    T v;
+    __device__ __forceinline__ float get(int) const { return to_float(v); }
+    __device__ __forceinline__ void clear() { v = from_float<T>(0.0f); }
 };
 
 template <typename T, int N>
 __device__ __forceinline__ Vec<T, N> load_vec(const T *p) {
-    return *reinterpret_cast<const Vec<T, N> *>(p);
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_vec(T *p, const Vec<T, N> &x) {
-    *reinterpret_cast<Vec<T, N> *>(p) = x;
+    Vec<T, N> x;
+    if constexpr (N == 1) {
+        x.v = *p;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        x.w[0] = u.x, x.w[1] = u.y, x.w[2] = u.z, x.w[3] = u.w;
+    }
+    return x;
 }
 
-// Stores N floats rounded to T.
+// Two floats rounded to T, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return uint32_t(__half_as_ushort(__low2half(h))) | uint32_t(__half_as_ushort(__high2half(h))) << 16;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return uint32_t(__bfloat16_as_ushort(__low2bfloat16(h))) | uint32_t(__bfloat16_as_ushort(__high2bfloat16(h))) << 16;
+}
+
+// Stores N floats rounded to T: one of them, or 16-byte pieces.
 template <typename T, int N>
 __device__ __forceinline__ void store_floats(T *p, const float (&f)[N]) {
-    Vec<T, N> x;
+    if constexpr (N == 1) {
+        *p = from_float<T>(f[0]);
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) x.v[k] = from_float<T>(f[k]);
-    store_vec<T, N>(p, x);
+        for (int k = 0; k < N; k += 4)
+            *reinterpret_cast<float4 *>(p + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; k += 8)
+            *reinterpret_cast<uint4 *>(p + k) =
+                make_uint4(pack2<T>(f[k], f[k + 1]), pack2<T>(f[k + 2], f[k + 3]), pack2<T>(f[k + 4], f[k + 5]),
+                           pack2<T>(f[k + 6], f[k + 7]));
+    }
 }
 
 // One element of a parameter vector whose type is known at run time.
