@@ -1,6 +1,7 @@
 // Layer normalisation of rows and its gradient (model: include/ss_norm.h).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -16,109 +17,338 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int32_t kMaxD = 65536;
 
-// A row's place in the threads: `lanes` threads share it, thread l of them
-// holding vectors l, l + lanes, ... (NV of VEC elements) in registers, so the
+// A row's place in the threads.  `lanes` threads share it, thread l of them
+// holding 16-byte vectors l, l + lanes, ... (NV of them) in registers, so the
 // row is read once for the mean, the centred squares and the result.  Narrow
 // rows (MULTI false) take a power of two of lanes inside a warp and reduce by
-// shuffles; wide ones take a CTA and reduce through shared memory.  The next
-// row's loads are issued before this row's reduction waits.
+// shuffles; wide ones take whole warps and reduce through shared memory and a
+// barrier of their own.
+//
+// Rows arrive through a ring in shared memory, asynchronously, kStages - 1
+// rows ahead: every thread copies into slots of its own and reads only
+// those, so the ring needs no barrier and the copies in flight no registers.
+//
+// Rows need not start on 16-byte boundaries (SHIFT): vectors lie on the
+// boundaries, and element i of vector v is column 8 v + i - mis (4 v + i - mis
+// in float32), mis the row start's distance from the boundary before it.  A
+// group of lanes takes every step-th row with step a multiple of the period
+// after which rows start alike, so its mis, and with it its columns, stay
+// fixed.  Only a vector that would leave the tensor's own span is loaded
+// element by element; a vector that holds other rows' or unused values is
+// loaded whole, masked, and stored element by element (in place, a neighbour
+// may be storing those values: whichever arrive, they are not used).
 constexpr int kPerThread = 16;       // elements of a row in one thread
-constexpr int kMaxRowThreads = 512;  // x 16 = the widest row held in registers
-constexpr int32_t kMaxRegD = kPerThread * kMaxRowThreads;
+constexpr int kMaxRowThreads = 512;
+constexpr int kMaxGroups = 8;        // of two warps at least
+  // x 16 = the widest row held in registers
 
 struct Place {
     int lanes, shift;   // lanes = 1 << shift where !MULTI
-    int vecs;           // vectors of a row
+    int vecs;           // vectors that a row may touch
+    int groups;         // rows side by side in a CTA
 };
 
+// Rows of one tensor; `same`: they start as far from a boundary as x's.
+template <typename T>
+struct Rows {
+    T *base;
+    int64_t stride;
+    bool same;
+};
+
+// Rows ahead by what they take: 16 bytes a vector, thread and tensor.
+constexpr int stages_of(int vectors) { return vectors <= 4 ? 4 : 3; }
+
+__device__ __forceinline__ void copy16(void *smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(smem))), "l"(gmem)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Sums K values over the row's lanes; every lane gets the same sums (one
-// fixed order).  MULTI alternates two buffers, so one barrier a sum is enough.
+// fixed order).  MULTI alternates two buffers, so one barrier a sum is enough;
+// their slots past the row's warps hold zeros.
+constexpr int kRowWarps = kMaxRowThreads / 32;
 template <int K, bool MULTI>
-__device__ __forceinline__ void row_sum(float (&v)[K], const Place &pl, float (*s_red)[K][16], int &flip) {
-    const int top = MULTI ? 16 : pl.lanes >> 1;
-    for (int o = top; o > 0; o >>= 1)
+__device__ __forceinline__ void row_sum(float (&v)[K], const Place &pl, int group, int lane,
+                                        float (*s_red)[K][kRowWarps], int &flip) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    for (int o = 16; o > 0; o >>= 1)
+        if (MULTI || o < pl.lanes)
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     if (!MULTI) return;
-    const int warps = pl.lanes >> 5, warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0)
+    if ((lane & 31) == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) s_red[flip][k][warp] = v[k];
-    __syncthreads();
+        for (int k = 0; k < K; ++k) s_red[flip][k][lane >> 5] = v[k];
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(pl.lanes) : "memory");
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+        const float4 *q = reinterpret_cast<const float4 *>(s_red[flip][k]);
         v[k] = 0.0f;
-        for (int w = 0; w < warps; ++w) v[k] += s_red[flip][k][w];
+        for (int w = 0; w < pl.lanes; w += 128) {
+            const float4 t = q[w >> 7];
+            v[k] += (t.x + t.y) + (t.z + t.w);
+        }
     }
     flip ^= 1;
 }
 
-template <typename T, int VEC, int NV>
-__device__ __forceinline__ void load_row(Vec<T, VEC> (&r)[NV], const T *p, int lane, const Place &pl) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-        if (lane + k * pl.lanes < pl.vecs) r[k] = load_vec<T, VEC>(p + size_t(lane + k * pl.lanes) * VEC);
+template <int K>
+__device__ __forceinline__ void clear_sums(float *s_red, int count) {
+    for (int e = threadIdx.x; e < count * 2 * K * kRowWarps; e += blockDim.x) s_red[e] = 0.0f;
 }
 
-template <typename T, int VEC, int NV, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads)
-    k_norm_fwd(const T *x, int64_t xs, int64_t n, int32_t D, Place pl, const void *gamma, const void *beta, int pdt,
-               float eps, T *y, int64_t ys, float *mean, float *rstd) {
-    __shared__ float s_red[2][1][16];
-    const int lane = MULTI ? threadIdx.x : threadIdx.x & (pl.lanes - 1);
-    const int rows = MULTI ? 1 : 32 >> pl.shift;                    // of a warp (or CTA)
-    const int64_t step = MULTI ? int64_t(gridDim.x) : int64_t(gridDim.x) * (kThreads / 32) * rows;
-    const int sub = MULTI ? 0 : (threadIdx.x & 31) >> pl.shift;
-    const int64_t row0 = MULTI ? int64_t(blockIdx.x)
-                               : (int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * rows;
-    const float inv = 1.0f / float(D);
-    float g[NV][VEC], b[NV][VEC];
+// Where a thread's vectors lie: its lane, and the row's distance from a
+// boundary (SHIFT).
+struct Cols {
+    int lane, lanes, vecs, mis;
+    int32_t D;
+};
+
+// Starts the copies of a row's vectors into this thread's slots (slots `apart`
+// vectors from one another).  p: the row's start; before, after: elements of
+// the tensor's span on either side of it (SHIFT).
+template <typename T, int VEC, int NV, bool SHIFT>
+__device__ __forceinline__ void fetch_row(uint4 *slot, int apart, const T *p, bool same, int64_t before, int64_t after,
+                                          const Cols &c) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = c.lane + k * c.lanes;
+        if (v >= c.vecs) continue;
+        if (!SHIFT) {
+            copy16(slot + k * apart, p + v * VEC);
+            continue;
+        }
+        const int j = v * VEC - c.mis;
+        if (same && j + before >= 0 && j + VEC <= after) {
+            copy16(slot + k * apart, p + j);
+        } else {
+            Vec<T, VEC> r;
+            r.clear();
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (j + i >= 0 && j + i < c.D) r.set(i, p[j + i]);
+            slot[k * apart] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        }
+    }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> from_slot(const uint4 *slot) {
+    const uint4 u = *slot;
+    Vec<T, VEC> x;
+    x.w[0] = u.x, x.w[1] = u.y, x.w[2] = u.z, x.w[3] = u.w;
+    return x;
+}
+
+// Whether element i of vector v belongs to the row; whether all of them do.
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ bool in_row(const Cols &c, int v, int i) {
+    return SHIFT ? uint32_t(v * VEC + i - c.mis) < uint32_t(c.D) : v < c.vecs;
+}
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ bool all_in_row(const Cols &c, int v) {
+    return SHIFT ? v * VEC >= c.mis && v * VEC - c.mis + VEC <= c.D : v < c.vecs;
+}
+
+// Zeros what of a vector does not belong to the row.
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ void mask(F2 (&f)[VEC / 2], const Cols &c, int v) {
+    if (all_in_row<VEC, SHIFT>(c, v)) return;
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+        const float2 q = get_f2(f[i / 2]);
+        f[i / 2] = make_f2(in_row<VEC, SHIFT>(c, v, i) ? q.x : 0.0f, in_row<VEC, SHIFT>(c, v, i + 1) ? q.y : 0.0f);
+    }
+}
+
+template <typename T, int VEC, bool SHIFT>
+__device__ __forceinline__ void store_row(T *p, bool same, int v, const Cols &c, const F2 (&o)[VEC / 2]) {
+    if (!SHIFT) {
+        store_pairs<T, VEC>(p + v * VEC, o);
+        return;
+    }
+    const int j = v * VEC - c.mis;
+    if (same && all_in_row<VEC, SHIFT>(c, v)) {
+        store_pairs<T, VEC>(p + j, o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const float2 q = get_f2(o[i / 2]);
+            if (j + i >= 0 && j + i < c.D) p[j + i] = from_float<T>(q.x);
+            if (j + i + 1 >= 0 && j + i + 1 < c.D) p[j + i + 1] = from_float<T>(q.y);
+        }
+    }
+}
+
+// Elements from a 16-byte boundary to row `row`.
+template <typename T>
+__device__ __forceinline__ int row_mis(const Rows<const T> &t, int64_t row) {
+    return int((reinterpret_cast<uintptr_t>(t.base + row * t.stride) & 15) / sizeof(T));
+}
+
+// A thread's weights, in float32 registers; `absent` where there are none.
+// All its loads are in flight together.
+template <int VEC, int NV, bool SHIFT, typename P>
+__device__ __forceinline__ void load_weights_as(F2 (&g)[NV][VEC / 2], const P *w, float absent, const Cols &c) {
+    constexpr int kVec = 16 / sizeof(P);
+    if constexpr (VEC % kVec == 0)
+    if (w && !SHIFT && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+        Vec<P, kVec> q[NV][VEC / kVec];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC / kVec; ++i) {
+                q[k][i].clear();
+                if (c.lane + k * c.lanes < c.vecs) q[k][i] = load_vec<P, kVec>(w + (c.lane + k * c.lanes) * VEC + i * kVec);
+            }
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; i += 2)
+                g[k][i / 2] = make_f2(q[k][i / kVec].get(i % kVec), q[k][i / kVec].get(i % kVec + 1));
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int v = lane + k * pl.lanes;
-            g[k][i] = gamma && v < pl.vecs ? load_param(gamma, pdt, int64_t(v) * VEC + i) : 1.0f;
-            b[k][i] = beta && v < pl.vecs ? load_param(beta, pdt, int64_t(v) * VEC + i) : 0.0f;
+        for (int i = 0; i < VEC; i += 2) {
+            float q[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int v = c.lane + k * c.lanes;
+                q[u] = w && in_row<VEC, SHIFT>(c, v, i + u) ? to_float(w[v * VEC + i + u - c.mis]) : absent;
+            }
+            g[k][i / 2] = make_f2(q[0], q[1]);
         }
-    Vec<T, VEC> next[NV];
-    if (row0 + sub < n) load_row<T, VEC, NV>(next, x + (row0 + sub) * xs, lane, pl);
-    int flip = 0;
-    for (int64_t base = row0; base < n; base += step) {
-        const int64_t row = base + sub;
-        float f[NV][VEC], sum[1] = {0.0f};
+}
+
+template <int VEC, int NV, bool SHIFT>
+__device__ __forceinline__ void load_weights(F2 (&g)[NV][VEC / 2], const void *w, int pdt, float absent, const Cols &c) {
+    if (pdt == SS_F32)
+        load_weights_as<VEC, NV, SHIFT>(g, static_cast<const float *>(w), absent, c);
+    else if (pdt == SS_F16)
+        load_weights_as<VEC, NV, SHIFT>(g, static_cast<const __half *>(w), absent, c);
+    else
+        load_weights_as<VEC, NV, SHIFT>(g, static_cast<const __nv_bfloat16 *>(w), absent, c);
+}
+
+// The backward has no registers left for gamma: a thread's vectors lie in
+// shared memory, one plane for every four columns of a vector, so that the
+// lanes of a warp read side by side (as two vectors of one thread, one after
+// the other, they would meet in the banks).
+template <int VEC, int NV>
+__device__ __forceinline__ void put_weights(float4 *plane, int apart, const F2 (&g)[NV][VEC / 2]) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                f[k][i] = row < n && lane + k * pl.lanes < pl.vecs ? next[k].get(i) : 0.0f;
-                sum[0] += f[k][i];
-            }
-        if (row + step < n) load_row<T, VEC, NV>(next, x + (row + step) * xs, lane, pl);
-        row_sum<1, MULTI>(sum, pl, s_red, flip);
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float2 a = get_f2(g[k][2 * i]), b = get_f2(g[k][2 * i + 1]);
+            plane[(k * (VEC / 4) + i) * apart] = make_float4(a.x, a.y, b.x, b.y);
+        }
+}
+template <int VEC>
+__device__ __forceinline__ void weights_of(F2 (&g)[VEC / 2], const float4 *plane, int apart, int k) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+        const float4 q = plane[(k * (VEC / 4) + i) * apart];
+        g[2 * i] = make_f2(q.x, q.y), g[2 * i + 1] = make_f2(q.z, q.w);
+    }
+}
+
+template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : 3)
+    k_norm_fwd(Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, const void *beta, int pdt, float eps,
+               Rows<T> y, float *mean, float *rstd) {
+    extern __shared__ uint4 s_ring[];    // [stages][NV][threads]
+    __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][1][kRowWarps];
+    constexpr int kStages = stages_of(NV), kHalf = VEC / 2;
+    const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
+    Cols c;
+    c.lanes = pl.lanes, c.vecs = pl.vecs, c.D = D;
+    c.lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
+    const int64_t step = int64_t(gridDim.x) * pl.groups;
+    const int64_t row0 = int64_t(blockIdx.x) * pl.groups + group;
+    c.mis = SHIFT ? row_mis(x, row0) : 0;
+    const int apart = blockDim.x;
+    uint4 *slot = s_ring + threadIdx.x;
+    const T *px = x.base + row0 * x.stride;
+    const int64_t xstep = step * x.stride, end = (n - 1) * x.stride + D;
+    int64_t at = row0 * x.stride;          // where the row to fetch starts
+#pragma unroll
+    for (int q = 0; q < kStages; ++q) {
+        if (q < kStages - 1) {
+            if (row0 + q * step < n)
+                fetch_row<T, VEC, NV, SHIFT>(slot + q * NV * apart, apart, px, true, at, end - at, c);
+            copies_commit();
+            px += xstep, at += xstep;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k)       // slots that no copy fills stay zero
+            if (c.lane + k * c.lanes >= c.vecs) slot[(q * NV + k) * apart] = make_uint4(0, 0, 0, 0);
+    }
+    F2 g[NV][kHalf], b[NV][kHalf];
+    load_weights<VEC, NV, SHIFT>(g, gamma, pdt, 1.0f, c);
+    load_weights<VEC, NV, SHIFT>(b, beta, pdt, 0.0f, c);
+    if (MULTI) clear_sums<1>(&s_red[0][0][0][0], kMaxGroups);
+    __syncthreads();
+    const float inv = 1.0f / float(D);
+    int flip = 0, stage = 0;
+    T *py = y.base + row0 * y.stride;
+    const int64_t ystep = step * y.stride;
+    // a warp's lanes leave together: they shuffle with one another; a row past
+    // the last is worked on as it lies in the ring and not stored
+    const int64_t lead = MULTI ? row0 : row0 - ((threadIdx.x & 31) >> pl.shift);
+    for (int64_t base = lead; base < n; base += step, py += ystep) {
+        const int64_t row = base + (row0 - lead);
+        copies_wait<kStages - 2>();
+        F2 f[NV][kHalf], acc = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            widen<T, VEC>(f[k], from_slot<T, VEC>(slot + (stage * NV + k) * apart));
+            if (SHIFT) mask<VEC, SHIFT>(f[k], c, c.lane + k * pl.lanes);
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) acc = add2(acc, f[k][i]);
+        }
+        const int last = stage == 0 ? kStages - 1 : stage - 1;   // the slots read one row ago
+        if (row + (kStages - 1) * step < n)
+            fetch_row<T, VEC, NV, SHIFT>(slot + last * NV * apart, apart, px, true, at, end - at, c);
+        copies_commit();
+        px += xstep, at += xstep;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        float sum[1] = {sum_of(acc)};
+        row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
         const float mu = sum[0] * inv;
-        sum[0] = 0.0f;
+        const F2 neg = both(-mu);
+        acc = both(0.0f);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (lane + k * pl.lanes < pl.vecs)
+        for (int k = 0; k < NV; ++k) {
+            const int v = c.lane + k * pl.lanes;
+            if (v < pl.vecs) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    f[k][i] -= mu;
-                    sum[0] = fmaf(f[k][i], f[k][i], sum[0]);
-                }
-        row_sum<1, MULTI>(sum, pl, s_red, flip);
-        const float r = 1.0f / sqrtf(fmaf(sum[0], inv, eps));
-        if (row >= n) continue;
-        T *out = y + row * ys;
+                for (int i = 0; i < kHalf; ++i) f[k][i] = add2(f[k][i], neg);
+                if (SHIFT) mask<VEC, SHIFT>(f[k], c, v);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (lane + k * pl.lanes < pl.vecs) {
-                float o[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = fmaf(f[k][i] * r, g[k][i], b[k][i]);
-                store_floats<T, VEC>(out + size_t(lane + k * pl.lanes) * VEC, o);
+                for (int i = 0; i < kHalf; ++i) acc = fma2(f[k][i], f[k][i], acc);
             }
-        if (lane == 0) {
+        }
+        sum[0] = sum_of(acc);
+        row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
+        const float r = __frsqrt_rn(fmaf(sum[0], inv, eps));
+        if (row >= n) continue;
+        const F2 rr = both(r);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = c.lane + k * pl.lanes;
+            if (v >= pl.vecs) continue;
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) f[k][i] = fma2(mul2(f[k][i], rr), g[k][i], b[k][i]);
+            store_row<T, VEC, SHIFT>(py, y.same, v, c, f[k]);
+        }
+        if (c.lane == 0) {
             if (mean) mean[row] = mu;
             if (rstd) rstd[row] = r;
         }
@@ -128,102 +358,146 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads)
 // As the forward, with dy and x of a row in registers; the weights' sums stay
 // in the threads' registers over all of a CTA's rows and leave one partial
 // sum a CTA in `part` [CTAs][2][D] (none where part is NULL).
-template <typename T, int VEC, int NV, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI || NV * VEC > 12 ? 1 : 2)
-    k_norm_bwd(const T *dy, int64_t dys, const T *x, int64_t xs, int64_t n, int32_t D, Place pl, const void *gamma,
-               int pdt, const float *mean, const float *rstd, T *dx, int64_t dxs, float *part) {
-    extern __shared__ float s_dyn[];     // !MULTI: [8 warps][2][D]
-    __shared__ float s_red[2][2][16];
-    const int lane = MULTI ? threadIdx.x : threadIdx.x & (pl.lanes - 1);
-    const int rows = MULTI ? 1 : 32 >> pl.shift;
-    const int64_t step = MULTI ? int64_t(gridDim.x) : int64_t(gridDim.x) * (kThreads / 32) * rows;
-    const int sub = MULTI ? 0 : (threadIdx.x & 31) >> pl.shift;
-    const int64_t row0 = MULTI ? int64_t(blockIdx.x)
-                               : (int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * rows;
+template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : 2)
+    k_norm_bwd(Rows<const T> dy, Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, int pdt,
+               const float *mean, const float *rstd, Rows<T> dx, float *part) {
+    extern __shared__ uint4 s_ring[];    // [stages][dy | x][NV][threads], then gamma; at the end the sums
+    __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][2][kRowWarps];
+    constexpr int kStages = stages_of(2 * NV), kHalf = VEC / 2;
+    const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
+    Cols c;
+    c.lanes = pl.lanes, c.vecs = pl.vecs, c.D = D;
+    c.lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
+    const int64_t step = int64_t(gridDim.x) * pl.groups;
+    const int64_t row0 = int64_t(blockIdx.x) * pl.groups + group;
+    c.mis = SHIFT ? row_mis(x, row0) : 0;
+    const int apart = blockDim.x;
+    uint4 *slot = s_ring + threadIdx.x;
+    // Row `row` of both tensors into a stage; a row past the last as zeros.
+    auto fetch = [&](int stage, int64_t row) {
+        uint4 *sd = slot + stage * 2 * NV * apart, *sx = sd + NV * apart;
+        if (row < n) {
+            const int64_t ad = row * dy.stride, ax = row * x.stride;
+            fetch_row<T, VEC, NV, SHIFT>(sd, apart, dy.base + ad, dy.same, ad, (n - 1 - row) * dy.stride + D, c);
+            fetch_row<T, VEC, NV, SHIFT>(sx, apart, x.base + ax, true, ax, (n - 1 - row) * x.stride + D, c);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2 * NV; ++k) sd[k * apart] = make_uint4(0, 0, 0, 0);
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int q = 0; q < kStages - 1; ++q) fetch(q, row0 + q * step);
+    float mu = 0.0f, r = 0.0f;
+    if (row0 < n) mu = mean[row0], r = rstd[row0];
+    float4 *plane = reinterpret_cast<float4 *>(s_ring + kStages * 2 * NV * apart) + threadIdx.x;
+    {
+        F2 g[NV][kHalf];
+        load_weights<VEC, NV, SHIFT>(g, gamma, pdt, 1.0f, c);
+        put_weights<VEC, NV>(plane, apart, g);
+    }
+    if (MULTI) clear_sums<2>(&s_red[0][0][0][0], kMaxGroups);
+    __syncthreads();
     const float inv = 1.0f / float(D);
-    float g[NV][VEC], dg[NV][VEC], db[NV][VEC];
+    F2 dg[NV][kHalf], db[NV][kHalf];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int v = lane + k * pl.lanes;
-            g[k][i] = gamma && v < pl.vecs ? load_param(gamma, pdt, int64_t(v) * VEC + i) : 1.0f;
-            dg[k][i] = db[k][i] = 0.0f;
-        }
-    Vec<T, VEC> nx[NV], nd[NV];
-    float mu = 0.0f, r = 0.0f;
-    if (row0 + sub < n) {
-        load_row<T, VEC, NV>(nd, dy + (row0 + sub) * dys, lane, pl);
-        load_row<T, VEC, NV>(nx, x + (row0 + sub) * xs, lane, pl);
-        mu = mean[row0 + sub], r = rstd[row0 + sub];
-    }
-    int flip = 0;
-    for (int64_t base = row0; base < n; base += step) {
-        const int64_t row = base + sub;
-        float a[NV][VEC], h[NV][VEC], sum[2] = {0.0f, 0.0f};
+        for (int i = 0; i < kHalf; ++i) dg[k][i] = db[k][i] = both(0.0f);
+    int flip = 0, stage = 0;
+    T *pdx = dx.base + row0 * dx.stride;
+    const int64_t dxstep = step * dx.stride;
+    const int64_t lead = MULTI ? row0 : row0 - ((threadIdx.x & 31) >> pl.shift);
+    for (int64_t base = lead; base < n; base += step, pdx += dxstep) {
+        const int64_t row = base + (row0 - lead);
+        copies_wait<kStages - 2>();
+        F2 a[NV][kHalf], h[NV][kHalf], s0 = both(0.0f), s1 = both(0.0f);
+        const F2 neg = both(-mu), rr = both(r);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k) {
+            const int v = c.lane + k * pl.lanes;
+            if (v < pl.vecs) {
+                F2 g[kHalf];
+                widen<T, VEC>(a[k], from_slot<T, VEC>(slot + (stage * 2 * NV + k) * apart));
+                widen<T, VEC>(h[k], from_slot<T, VEC>(slot + ((stage * 2 + 1) * NV + k) * apart));
+                weights_of<VEC>(g, plane, apart, k);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const bool ok = row < n && lane + k * pl.lanes < pl.vecs;
-                const float d = ok ? nd[k].get(i) : 0.0f;
-                h[k][i] = ok ? (nx[k].get(i) - mu) * r : 0.0f;
-                a[k][i] = d * g[k][i];
-                dg[k][i] = fmaf(d, h[k][i], dg[k][i]);
-                db[k][i] += d;
-                sum[0] += a[k][i];
-                sum[1] = fmaf(a[k][i], h[k][i], sum[1]);
+                for (int i = 0; i < kHalf; ++i) h[k][i] = mul2(add2(h[k][i], neg), rr);
+                if (SHIFT) mask<VEC, SHIFT>(a[k], c, v), mask<VEC, SHIFT>(h[k], c, v);
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) {
+                    dg[k][i] = fma2(a[k][i], h[k][i], dg[k][i]);
+                    db[k][i] = add2(db[k][i], a[k][i]);
+                    a[k][i] = mul2(a[k][i], g[i]);
+                    s0 = add2(s0, a[k][i]);
+                    s1 = fma2(a[k][i], h[k][i], s1);
+                }
             }
-        const float rr = r;
-        if (row + step < n) {
-            load_row<T, VEC, NV>(nd, dy + (row + step) * dys, lane, pl);
-            load_row<T, VEC, NV>(nx, x + (row + step) * xs, lane, pl);
-            mu = mean[row + step], r = rstd[row + step];
         }
-        row_sum<2, MULTI>(sum, pl, s_red, flip);
+        mu = r = 0.0f;
+        if (row + step < n) mu = mean[row + step], r = rstd[row + step];
+        fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);   // the slots read one row ago
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        float sum[2] = {sum_of(s0), sum_of(s1)};
+        row_sum<2, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
         if (row >= n) continue;
-        const float ma = sum[0] * inv, mah = sum[1] * inv;
-        T *out = dx + row * dxs;
+        const F2 ma = both(-sum[0] * inv), mah = both(-sum[1] * inv);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (lane + k * pl.lanes < pl.vecs) {
-                float o[VEC];
+        for (int k = 0; k < NV; ++k) {
+            const int v = c.lane + k * pl.lanes;
+            if (v >= pl.vecs) continue;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = rr * (a[k][i] - ma - h[k][i] * mah);
-                store_floats<T, VEC>(out + size_t(lane + k * pl.lanes) * VEC, o);
-            }
+            for (int i = 0; i < kHalf; ++i) a[k][i] = mul2(fma2(h[k][i], mah, add2(a[k][i], ma)), rr);
+            store_row<T, VEC, SHIFT>(pdx, dx.same, v, c, a[k]);
+        }
     }
     if (!part) return;
+    // The CTA's sum, in fixed order: the rows of a warp are joined by shuffles
+    // first where they start alike (!MULTI, !SHIFT), then the warps or groups
+    // in turn, in the ring's place.
     part += size_t(blockIdx.x) * 2 * D;
-    if (MULTI) {
+    const bool fold = !MULTI && !SHIFT;
+    const int slots = fold ? kThreads / 32 : pl.groups;
+    const int mine_at = fold ? threadIdx.x >> 5 : group;
+    copies_wait<0>();
+    __syncthreads();                       // the last rows' slots and gamma have been read
+    float *s_sum = reinterpret_cast<float *>(s_ring);
+    const bool direct = MULTI && !SHIFT && slots == 1;   // whole vectors, straight to their place
+    float *mine = direct ? part : s_sum + size_t(mine_at) * 2 * D;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (lane + k * pl.lanes < pl.vecs) {
-                store_floats<float, VEC>(part + size_t(lane + k * pl.lanes) * VEC, dg[k]);
-                store_floats<float, VEC>(part + D + size_t(lane + k * pl.lanes) * VEC, db[k]);
-            }
-        return;
-    }
-    // the warp's rows, then the CTA's warps, in fixed order
-    float *mine = s_dyn + size_t(threadIdx.x >> 5) * 2 * D;
+    for (int k = 0; k < NV; ++k) {
+        const int v = c.lane + k * pl.lanes;
+        float tg[VEC], tb[VEC];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            for (int o = pl.lanes; o < 32; o <<= 1) {
-                dg[k][i] += __shfl_xor_sync(0xffffffffu, dg[k][i], o);
-                db[k][i] += __shfl_xor_sync(0xffffffffu, db[k][i], o);
-            }
-            const int v = lane + k * pl.lanes;
-            if (sub == 0 && v < pl.vecs) {
-                mine[v * VEC + i] = dg[k][i];
-                mine[D + v * VEC + i] = db[k][i];
-            }
+        for (int i = 0; i < VEC; i += 2) {
+            const float2 qg = get_f2(dg[k][i / 2]), qb = get_f2(db[k][i / 2]);
+            tg[i] = qg.x, tg[i + 1] = qg.y, tb[i] = qb.x, tb[i + 1] = qb.y;
         }
+        if (fold)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                for (int o = pl.lanes; o < 32; o <<= 1) {
+                    tg[i] += __shfl_xor_sync(0xffffffffu, tg[i], o);
+                    tb[i] += __shfl_xor_sync(0xffffffffu, tb[i], o);
+                }
+        if (fold && (threadIdx.x & 31) >= pl.lanes) continue;
+        if (!SHIFT) {
+            if (v < pl.vecs) {
+                store_floats<float, VEC>(mine + v * VEC, tg);
+                store_floats<float, VEC>(mine + D + v * VEC, tb);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (in_row<VEC, SHIFT>(c, v, i)) mine[v * VEC + i - c.mis] = tg[i], mine[D + v * VEC + i - c.mis] = tb[i];
+        }
+    }
+    if (direct) return;
     __syncthreads();
-    for (int j = threadIdx.x; j < 2 * D; j += kThreads) {
+    for (int j = threadIdx.x; j < 2 * D; j += blockDim.x) {
         float t = 0.0f;
-        for (int w = 0; w < kThreads / 32; ++w) t += s_dyn[size_t(w) * 2 * D + j];
+        for (int w = 0; w < slots; ++w) t += s_sum[size_t(w) * 2 * D + j];
         part[j] = t;
     }
 }
@@ -277,7 +551,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_fwd_wide(const T *__restrict_
             const float c = to_float(xr[j]) - mu;
             s += c * c;
         }
-        const float r = 1.0f / sqrtf(block_sum(s, s_red) / float(D) + eps);
+        const float r = __frsqrt_rn(block_sum(s, s_red) / float(D) + eps);
         for (int j = threadIdx.x; j < D; j += kThreads) {
             const float g = gamma ? load_param(gamma, pdt, j) : 1.0f;
             const float b = beta ? load_param(beta, pdt, j) : 0.0f;
@@ -332,14 +606,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows_wide(const T *dy, in
     }
 }
 
-// CTAs of a launch over n rows, so many rows at a time in each.
-int grid_of(int64_t n, int rows, int per_sm, int sms) {
-    const int64_t want = (n + rows - 1) / rows, most = int64_t(sms) * per_sm;
-    return int(want < 1 ? 1 : (want < most ? want : most));
-}
-
-constexpr int kMaxParts = 1024;      // partial sums of the weights' gradients
-int64_t weight_parts(int64_t n) { return n < 1 ? 1 : (n < kMaxParts ? n : kMaxParts); }
+// Partial sums of the weights' gradients that the workspace has room for: at
+// most one for each row, and up to kMaxPeriod - 1 more where the grid is rounded up
+// to a multiple of the period of the rows' starts.
+constexpr int kMaxPeriod = 8, kMaxParts = 1024;
+int64_t weight_parts(int64_t n) { return n + kMaxPeriod < kMaxParts ? n + kMaxPeriod : kMaxParts; }
 
 int pow2_at_least(int v) {
     int p = 1;
@@ -347,27 +618,56 @@ int pow2_at_least(int v) {
     return p;
 }
 
-// Lanes of a row of `vecs` vectors of `vec` elements: a power of two up to a
-// warp while 16 elements a thread hold the row, else whole warps.  At least
-// 4 lanes of 16-byte vectors (16 of single elements), so that a load touches
-// whole sectors.
-Place place_of(int32_t D, int vec, bool *multi) {
+// Lanes of a row of D elements in vectors of `vec`: a power of two up to a
+// warp while 16 elements a thread hold the row, else whole warps.  At least 4
+// lanes, so that a load touches whole sectors.  Several wide rows share a CTA
+// of about `threads`.
+Place place_of(int32_t D, int vec, int threads, bool shift, bool *multi) {
     Place pl{};
-    pl.vecs = D / vec;
+    pl.vecs = (D + (shift ? vec - 1 : 0) + vec - 1) / vec;
     const int nv = kPerThread / vec;
     const int need = (pl.vecs + nv - 1) / nv;
     *multi = need > 32;
     if (*multi) {
         pl.lanes = (need + 31) / 32 * 32;
+        pl.groups = pl.lanes < threads ? threads / pl.lanes : 1;
     } else {
-        const int least = vec > 1 ? 4 : 16, most = pow2_at_least(pl.vecs);
+        const int most = pow2_at_least(pl.vecs);
         pl.lanes = pow2_at_least(need);
-        if (pl.lanes < least) pl.lanes = least;
-        if (pl.lanes > most) pl.lanes = most;
-        if (pl.lanes > 32) pl.lanes = 32;
+        if (pl.lanes < 4) pl.lanes = most < 4 ? most : 4;
+        pl.groups = kThreads / pl.lanes;
     }
     while ((1 << pl.shift) < pl.lanes) ++pl.shift;
     return pl;
+}
+
+// Rows after which row starts repeat their distance from a 16-byte boundary.
+int period_of(int64_t stride, int bytes) {
+    const int r = int((stride * bytes) & 15);
+    return r == 0 ? 1 : 16 / (r & -r);
+}
+
+// As many CTAs as fit the device at once, and no more than share the rows
+// evenly; a multiple of the period where rows start differently.
+template <typename Tag, typename K>
+int grid_of(K kernel, int threads, size_t smem, int64_t n, int groups, int period, int most, int sms) {
+    // the last answer, by what it depends on (one kernel, one architecture)
+    static std::atomic<unsigned long long> known{0};
+    const unsigned long long key = (unsigned long long)(threads) << 40 | (unsigned long long)(smem) << 8;
+    const unsigned long long k = known.load(std::memory_order_relaxed);
+    int per_sm = int(k & 255);
+    if ((k ^ key) >> 8) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+            per_sm = 1;
+        known.store(key | per_sm, std::memory_order_relaxed);
+    }
+    int64_t fit = int64_t(sms) * per_sm;
+    if (fit > most) fit = most;
+    const int64_t turns = (n + fit * groups - 1) / (fit * groups);
+    int64_t grid = (n + turns * groups - 1) / (turns * groups);
+    const int p = groups % period == 0 ? 1 : period;
+    grid = (grid + p - 1) / p * p;
+    return int(grid < 1 ? 1 : grid);
 }
 
 bool sizes_ok(int64_t n, int32_t D) { return n >= 0 && n < (int64_t(1) << 31) && D >= 1 && D <= kMaxD; }
@@ -423,104 +723,132 @@ struct BwdArgs {
     float *part;
 };
 
-template <typename T, int VEC, int NV, bool MULTI>
-void fwd_kernel(const FwdArgs &a, const Place &pl, int sms, cudaStream_t s) {
-    const int rows = MULTI ? 1 : kThreads / pl.lanes, threads = MULTI ? pl.lanes : kThreads;
-    const int grid = grid_of(a.n, rows, MULTI ? 2048 / threads : 8, sms);
-    SS_LAUNCH("k_norm_fwd", s,
-              k_norm_fwd<T, VEC, NV, MULTI><<<grid, threads, 0, s>>>(static_cast<const T *>(a.x), a.xs, a.n, a.D, pl,
-                                                                     a.gamma, a.beta, a.pdt, a.eps,
-                                                                     static_cast<T *>(a.y), a.ys, a.mean, a.rstd));
+template <typename T>
+bool same_start(const void *a, int64_t as, const void *b, int64_t bs) {
+    return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0 &&
+           (((as - bs) * int64_t(sizeof(T))) & 15) == 0;
 }
 
-template <typename T, int VEC, int NV, bool MULTI>
-void bwd_kernel(const BwdArgs &a, const Place &pl, int sms, cudaStream_t s) {
-    const int rows = MULTI ? 1 : kThreads / pl.lanes, threads = MULTI ? pl.lanes : kThreads;
-    int per_sm = MULTI ? 512 / threads : 2;
-    if (per_sm > 6) per_sm = 6;      // kMaxParts / SMs
-    int grid = grid_of(a.n, rows, per_sm, sms);
-    if (grid > kMaxParts) grid = kMaxParts;
-    const size_t smem = MULTI || !a.dgamma ? 0 : size_t(kThreads / 32) * 2 * a.D * sizeof(float);
+constexpr int kMaxSmem = 225 * 1024;   // 227 KB less 2 KB of static buffers
+
+template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+struct FwdTag {};
+template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+struct BwdTag {};
+
+template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+ss_status fwd_kernel(const FwdArgs &a, const Place &pl, int sms, cudaStream_t s) {
+    const int threads = MULTI ? pl.lanes * pl.groups : kThreads;
+    const size_t smem = size_t(stages_of(NV)) * NV * threads * 16;
+    auto kernel = k_norm_fwd<T, VEC, NV, MULTI, SHIFT>;
+    static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
+    const void *fn = (const void *)kernel;
+    const ss_status st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "ss_layer_norm_fwd");
+    if (st != SS_OK) return st;
+    const int grid = grid_of<FwdTag<T, VEC, NV, MULTI, SHIFT>>(kernel, threads, smem, a.n, pl.groups,
+                                                               period_of(a.xs, sizeof(T)), 1 << 30, sms);
+    const Rows<const T> x{static_cast<const T *>(a.x), a.xs, true};
+    const Rows<T> y{static_cast<T *>(a.y), a.ys, same_start<T>(a.x, a.xs, a.y, a.ys)};
+    SS_LAUNCH("k_norm_fwd", s,
+              kernel<<<grid, threads, smem, s>>>(x, a.n, a.D, pl, a.gamma, a.beta, a.pdt, a.eps, y, a.mean, a.rstd));
+    return SS_OK;
+}
+
+template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+ss_status bwd_kernel(const BwdArgs &a, const Place &pl, int sms, cudaStream_t s) {
+    const int threads = MULTI ? pl.lanes * pl.groups : kThreads;
+    size_t smem = size_t(stages_of(2 * NV)) * 2 * NV * threads * 16 +
+                  size_t(NV) * VEC * threads * sizeof(float);   // the ring and gamma
+    const int slots = MULTI || SHIFT ? pl.groups : kThreads / 32;
+    const size_t sums = a.dgamma && !(MULTI && !SHIFT && slots == 1) ? size_t(slots) * 2 * a.D * sizeof(float) : 0;
+    if (smem < sums) smem = sums;
+    auto kernel = k_norm_bwd<T, VEC, NV, MULTI, SHIFT>;
+    static std::atomic<unsigned long long> smem_ctx[kMaxDevices];
+    const void *fn = (const void *)kernel;
+    const ss_status st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "ss_layer_norm_bwd");
+    if (st != SS_OK) return st;
+    const int grid = grid_of<BwdTag<T, VEC, NV, MULTI, SHIFT>>(kernel, threads, smem, a.n, pl.groups,
+                                                               period_of(a.xs, sizeof(T)), kMaxParts - kMaxPeriod, sms);
+    const Rows<const T> x{static_cast<const T *>(a.x), a.xs, true};
+    const Rows<const T> dy{static_cast<const T *>(a.dy), a.dys, same_start<T>(a.x, a.xs, a.dy, a.dys)};
+    const Rows<T> dx{static_cast<T *>(a.dx), a.dxs, same_start<T>(a.x, a.xs, a.dx, a.dxs)};
     SS_LAUNCH("k_norm_bwd", s,
-              k_norm_bwd<T, VEC, NV, MULTI><<<grid, threads, smem, s>>>(
-                  static_cast<const T *>(a.dy), a.dys, static_cast<const T *>(a.x), a.xs, a.n, a.D, pl, a.gamma,
-                  a.pdt, a.mean, a.rstd, static_cast<T *>(a.dx), a.dxs, a.dgamma ? a.part : nullptr));
+              kernel<<<grid, threads, smem, s>>>(dy, x, a.n, a.D, pl, a.gamma, a.pdt, a.mean, a.rstd, dx,
+                                                 a.dgamma ? a.part : nullptr));
     if (a.dgamma)
         SS_LAUNCH("k_norm_bwd_final", s,
                   k_norm_bwd_final<<<(2 * a.D + 31) / 32, 1024, 0, s>>>(a.part, grid, a.D, a.dgamma, a.dbeta, a.pdt));
+    return SS_OK;
 }
 
 // Picks the vectors a thread holds: all of them for wide rows, just enough
 // for narrow ones.
-template <typename T, int VEC, typename Args>
-void pick_nv(const Args &a, int sms, cudaStream_t s) {
-    constexpr int kNv = kPerThread / VEC;
+template <typename T, bool SHIFT, typename Args>
+ss_status pick_nv(const Args &a, int sms, cudaStream_t s) {
+    constexpr int kVec = 16 / sizeof(T), kNv = kPerThread / kVec;
     bool multi;
-    const Place pl = place_of(a.D, VEC, &multi);
+    const Place pl = place_of(a.D, kVec, std::is_same<Args, FwdArgs>::value ? kThreads : kMaxRowThreads, SHIFT, &multi);
     const int nv = (pl.vecs + pl.lanes - 1) / pl.lanes;
     auto go = [&](auto NV, auto MULTI) {
         if constexpr (std::is_same<Args, FwdArgs>::value)
-            fwd_kernel<T, VEC, decltype(NV)::value, decltype(MULTI)::value>(a, pl, sms, s);
+            return fwd_kernel<T, kVec, decltype(NV)::value, decltype(MULTI)::value, SHIFT>(a, pl, sms, s);
         else
-            bwd_kernel<T, VEC, decltype(NV)::value, decltype(MULTI)::value>(a, pl, sms, s);
+            return bwd_kernel<T, kVec, decltype(NV)::value, decltype(MULTI)::value, SHIFT>(a, pl, sms, s);
     };
     if (multi) return go(std::integral_constant<int, kNv>{}, std::true_type{});
     if (nv <= 1) return go(std::integral_constant<int, 1>{}, std::false_type{});
-    if (nv <= 2) return go(std::integral_constant<int, 2>{}, std::false_type{});
     if constexpr (kNv == 4) {
         if (nv == 3) return go(std::integral_constant<int, 3>{}, std::false_type{});
+        if (nv == 4) return go(std::integral_constant<int, 4>{}, std::false_type{});
     }
-    if constexpr (kNv >= 4) {
-        if (nv <= 4) return go(std::integral_constant<int, 4>{}, std::false_type{});
-    }
-    if constexpr (kNv == 16) {
-        if (nv <= 8) return go(std::integral_constant<int, 8>{}, std::false_type{});
-        go(std::integral_constant<int, 16>{}, std::false_type{});
-    }
+    return go(std::integral_constant<int, 2>{}, std::false_type{});
+}
+
+// The widest row that 512 threads hold, whatever its start.
+template <typename T>
+bool too_wide(int32_t D, bool shift) {
+    constexpr int kVec = 16 / sizeof(T);
+    return (D + (shift ? kVec - 1 : 0) + kVec - 1) / kVec > kMaxRowThreads * (kPerThread / kVec);
+}
+
+int wide_grid(int64_t n, int sms) { return int(n < int64_t(sms) * 8 ? n : int64_t(sms) * 8); }
+
+template <typename T>
+ss_status launch_fwd(const FwdArgs &a, int sms, cudaStream_t s) {
+    constexpr int kVec = 16 / sizeof(T);
+    const bool shift = !(a.D % kVec == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) && a.xs % kVec == 0 &&
+                         a.ys % kVec == 0);
+    if (!too_wide<T>(a.D, shift)) return shift ? pick_nv<T, true>(a, sms, s) : pick_nv<T, false>(a, sms, s);
+    SS_LAUNCH("k_norm_fwd_wide", s,
+              k_norm_fwd_wide<T><<<wide_grid(a.n, sms), kThreads, 0, s>>>(
+                  static_cast<const T *>(a.x), a.xs, a.n, a.D, a.gamma, a.beta, a.pdt, a.eps, static_cast<T *>(a.y),
+                  a.ys, a.mean, a.rstd));
+    return SS_OK;
 }
 
 template <typename T>
-void launch_fwd(const FwdArgs &a, int sms, cudaStream_t s) {
+ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
     constexpr int kVec = 16 / sizeof(T);
-    if (a.D > kMaxRegD) {
-        const int grid = grid_of(a.n, 1, 8, sms);
-        SS_LAUNCH("k_norm_fwd_wide", s,
-                  k_norm_fwd_wide<T><<<grid, kThreads, 0, s>>>(static_cast<const T *>(a.x), a.xs, a.n, a.D, a.gamma,
-                                                               a.beta, a.pdt, a.eps, static_cast<T *>(a.y), a.ys,
-                                                               a.mean, a.rstd));
-    } else if (a.D % kVec == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) && a.xs % kVec == 0 && a.ys % kVec == 0) {
-        pick_nv<T, kVec>(a, sms, s);
-    } else {
-        pick_nv<T, 1>(a, sms, s);
+    const bool shift = !(a.D % kVec == 0 && aligned_to(a.dy, 16) && aligned_to(a.x, 16) && aligned_to(a.dx, 16) &&
+                         a.dys % kVec == 0 && a.xs % kVec == 0 && a.dxs % kVec == 0);
+    if (a.n > 0 && !too_wide<T>(a.D, shift)) return shift ? pick_nv<T, true>(a, sms, s) : pick_nv<T, false>(a, sms, s);
+    // the weights first: dx may overwrite dy or x
+    if (a.dgamma) {
+        const dim3 g((a.D + kThreads - 1) / kThreads, unsigned(a.n < 64 ? (a.n < 1 ? 1 : a.n) : 64));
+        SS_LAUNCH("k_norm_bwd_weights_wide", s,
+                  k_norm_bwd_weights_wide<T><<<g, kThreads, 0, s>>>(static_cast<const T *>(a.dy), a.dys,
+                                                                    static_cast<const T *>(a.x), a.xs, a.n, a.D,
+                                                                    a.mean, a.rstd, a.part));
+        SS_LAUNCH("k_norm_bwd_final", s,
+                  k_norm_bwd_final<<<(2 * a.D + 31) / 32, 1024, 0, s>>>(a.part, int(g.y), a.D, a.dgamma, a.dbeta,
+                                                                        a.pdt));
     }
-}
-
-template <typename T>
-void launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
-    constexpr int kVec = 16 / sizeof(T);
-    if (a.D > kMaxRegD || a.n == 0) {
-        // the weights first: dx may overwrite dy or x
-        if (a.dgamma) {
-            const dim3 g((a.D + kThreads - 1) / kThreads, unsigned(a.n < 64 ? (a.n < 1 ? 1 : a.n) : 64));
-            SS_LAUNCH("k_norm_bwd_weights_wide", s,
-                      k_norm_bwd_weights_wide<T><<<g, kThreads, 0, s>>>(static_cast<const T *>(a.dy), a.dys,
-                                                                        static_cast<const T *>(a.x), a.xs, a.n, a.D,
-                                                                        a.mean, a.rstd, a.part));
-            SS_LAUNCH("k_norm_bwd_final", s,
-                      k_norm_bwd_final<<<(2 * a.D + 31) / 32, 1024, 0, s>>>(a.part, int(g.y), a.D, a.dgamma, a.dbeta,
-                                                                            a.pdt));
-        }
-        if (a.n == 0) return;
-        SS_LAUNCH("k_norm_bwd_rows_wide", s,
-                  k_norm_bwd_rows_wide<T><<<grid_of(a.n, 1, 8, sms), kThreads, 0, s>>>(
-                      static_cast<const T *>(a.dy), a.dys, static_cast<const T *>(a.x), a.xs, a.n, a.D, a.gamma, a.pdt,
-                      a.mean, a.rstd, static_cast<T *>(a.dx), a.dxs));
-    } else if (a.D % kVec == 0 && aligned_to(a.dy, 16) && aligned_to(a.x, 16) && aligned_to(a.dx, 16) &&
-               a.dys % kVec == 0 && a.xs % kVec == 0 && a.dxs % kVec == 0) {
-        pick_nv<T, kVec>(a, sms, s);
-    } else {
-        pick_nv<T, 1>(a, sms, s);
-    }
+    if (a.n == 0) return SS_OK;
+    SS_LAUNCH("k_norm_bwd_rows_wide", s,
+              k_norm_bwd_rows_wide<T><<<wide_grid(a.n, sms), kThreads, 0, s>>>(
+                  static_cast<const T *>(a.dy), a.dys, static_cast<const T *>(a.x), a.xs, a.n, a.D, a.gamma, a.pdt,
+                  a.mean, a.rstd, static_cast<T *>(a.dx), a.dxs));
+    return SS_OK;
 }
 
 }  // namespace
@@ -550,11 +878,12 @@ ss_status ss_layer_norm_fwd(const void *x, ss_dtype dtype, int64_t x_stride, int
     cudaStream_t s = (cudaStream_t)stream;
     const FwdArgs a{x, x_stride, n, D, gamma, beta, int(param_dtype), eps, y, y_stride, mean, rstd};
     if (dtype == SS_F32)
-        launch_fwd<float>(a, sms, s);
+        st = launch_fwd<float>(a, sms, s);
     else if (dtype == SS_F16)
-        launch_fwd<__half>(a, sms, s);
+        st = launch_fwd<__half>(a, sms, s);
     else
-        launch_fwd<__nv_bfloat16>(a, sms, s);
+        st = launch_fwd<__nv_bfloat16>(a, sms, s);
+    if (st != SS_OK) return st;
     return check_launch(who);
 }
 
@@ -597,11 +926,12 @@ ss_status ss_layer_norm_bwd(const void *dy, int64_t dy_stride, const void *x, in
     const BwdArgs a{dy, dy_stride, x, x_stride, n, D, gamma, int(param_dtype), mean, rstd, dx, dx_stride, dgamma,
                     dbeta, static_cast<float *>(workspace)};
     if (dtype == SS_F32)
-        launch_bwd<float>(a, sms, s);
+        st = launch_bwd<float>(a, sms, s);
     else if (dtype == SS_F16)
-        launch_bwd<__half>(a, sms, s);
+        st = launch_bwd<__half>(a, sms, s);
     else
-        launch_bwd<__nv_bfloat16>(a, sms, s);
+        st = launch_bwd<__nv_bfloat16>(a, sms, s);
+    if (st != SS_OK) return st;
     return check_launch(who);
 }
 

@@ -37,8 +37,17 @@ struct Vec {
     uint32_t w[4];
     __device__ __forceinline__ float get(int i) const { return get_as(i, T()); }
     __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    // Puts element i in place (after clear()).
+    __device__ __forceinline__ void set(int i, T v) { set_as(i, v); }
 
   private:
+    __device__ __forceinline__ void set_as(int i, float v) { w[i] = __float_as_uint(v); }
+    __device__ __forceinline__ void set_as(int i, __nv_bfloat16 v) {
+        w[i >> 1] |= uint32_t(__bfloat16_as_ushort(v)) << (16 * (i & 1));
+    }
+    __device__ __forceinline__ void set_as(int i, __half v) {
+        w[i >> 1] |= uint32_t(__half_as_ushort(v)) << (16 * (i & 1));
+    }
     __device__ __forceinline__ float get_as(int i, float) const { return __uint_as_float(w[i]); }
     __device__ __forceinline__ float get_as(int i, __nv_bfloat16) const {
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
@@ -71,13 +80,15 @@ template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <>
 __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return uint32_t(__half_as_ushort(__low2half(h))) | uint32_t(__half_as_ushort(__high2half(h))) << 16;
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
 }
 template <>
 __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return uint32_t(__bfloat16_as_ushort(__low2bfloat16(h))) | uint32_t(__bfloat16_as_ushort(__high2bfloat16(h))) << 16;
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
 }
 
 // Stores N floats rounded to T: one of them, or 16-byte pieces.
@@ -96,6 +107,59 @@ __device__ __forceinline__ void store_floats(T *p, const float (&f)[N]) {
                 make_uint4(pack2<T>(f[k], f[k + 1]), pack2<T>(f[k + 2], f[k + 3]), pack2<T>(f[k + 4], f[k + 5]),
                            pack2<T>(f[k + 6], f[k + 7]));
     }
+}
+
+// Two float32 values in a register pair; sums, products and fused products
+// of pairs take one instruction each (PTX add / mul / fma .f32x2).
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 make_f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 get_f2(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 both(float a) { return make_f2(a, a); }
+__device__ __forceinline__ float sum_of(F2 a) {
+    const float2 q = get_f2(a);
+    return q.x + q.y;
+}
+
+// The four words of a vector as pairs of floats, and back.
+template <typename T, int N>
+__device__ __forceinline__ void widen(F2 (&f)[N / 2], const Vec<T, N> &x) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) f[i / 2] = make_f2(x.get(i), x.get(i + 1));
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_pairs(T *p, const F2 (&f)[N / 2]) {
+    float o[N];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 q = get_f2(f[i / 2]);
+        o[i] = q.x, o[i + 1] = q.y;
+    }
+    store_floats<T, N>(p, o);
 }
 
 // One element of a parameter vector whose type is known at run time.
