@@ -1,6 +1,21 @@
 // The norm of all gradients and their scaling by it (model: include/ss_clip.h).
+//
+// Bound by memory: every gradient has to be read for the norm and again to be
+// scaled, and the scaled values written.  One cooperative launch does both:
+// its CTAs sweep the tensors' 32 KB tiles from the first to the last adding
+// squares, meet at a grid barrier, add everybody's partial sums in the same
+// order, and sweep back from the last tile to the first, so that what the
+// first sweep read last is still in L2 (129 MB) when the second begins.
+// A few small tensors never leave the registers of one cluster.
+// Tiles that the second sweep will not find there, and all that it reads and
+// writes, are marked to leave L2 first.  The list of tensors travels in the
+// launch's parameters: nothing is copied to the device, and a captured graph
+// keeps its own list.  Lists too long for one launch's parameters take a
+// launch for each part of the list and sweep.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -12,107 +27,416 @@
 namespace ss {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBatch = 64;           // tensors in one launch's parameters
-constexpr int kGrid = 512;
-constexpr int kTile = kThreads * 16; // elements of one CTA's step
+constexpr int kThreads = 512;
+constexpr int kPer = 4;                          // 16-byte vectors of a tile in one thread
+constexpr int kTile = kThreads * kPer * 16;      // bytes
+constexpr int kMaxGrid = 1024;                   // partial sums of one launch
+constexpr int kSmallList = 24, kLongList = 1000; // tensors in one launch's parameters
 constexpr int32_t kMaxTensors = 65536;
+// What of the first sweep's bytes the second is let find in L2: a part of its
+// 129 MB, so that lines of the two memories' halves do not crowd one another out.
+constexpr int64_t kKeep = 80 << 20;
 
+template <int CAP>
 struct Table {
-    const void *in[kBatch];
-    void *out[kBatch];
-    int64_t numel[kBatch];
-    int64_t first[kBatch + 1];   // first tile of each tensor
-    int dtype[kBatch];
-    int count;
+    const void *in[CAP];
+    void *out[CAP];
+    int64_t numel[CAP];
+    int32_t first[CAP + 1];      // first tile of each tensor
+    uint8_t dtype[CAP];
+    int32_t count, keep;         // tensors; tiles from `keep` on stay in L2
 };
 
-template <typename T>
-__device__ float tile_squares(const T *p, int64_t lo, int64_t hi) {
-    float s = 0.0f;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-        const float v = to_float(p[i]);
-        s = fmaf(v, v, s);
+// The tensor of a tile (tensors without elements have no tile).
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const Table<CAP> &t, int tile) {
+    int a = 0, b = t.count;
+    while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (t.first[m] <= tile) a = m; else b = m;
     }
+    return a;
+}
+
+template <typename T>
+using Vector = Vec<T, 16 / int(sizeof(T))>;
+
+template <typename T>
+__device__ __forceinline__ float squares_of(const Vector<T> &x) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16 / int(sizeof(T)); ++i) s = fmaf(x.get(i), x.get(i), s);
     return s;
 }
 
+// c x, rounded to T; by 1 the bits as they are (a product would change a NaN's).
 template <typename T>
-__device__ void tile_scale(const T *in, T *out, int64_t lo, int64_t hi, float c) {
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) out[i] = c == 1.0f ? in[i] : from_float<T>(to_float(in[i]) * c);
+__device__ __forceinline__ Vector<T> scaled(Vector<T> x, float c) {
+    if (c == 1.0f) return x;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.w[i] = __float_as_uint(x.get(i) * c);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack2<T>(x.get(2 * i) * c, x.get(2 * i + 1) * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.w[i] = w[i];
+    }
+    return x;
 }
 
-__global__ void __launch_bounds__(kThreads) k_clip_squares(Table t, double *part) {
-    __shared__ double s_red[kThreads / 32];
-    double sum = 0.0;
-    int k = 0;
-    for (int64_t tile = blockIdx.x; tile < t.first[t.count]; tile += gridDim.x) {
-        while (tile >= t.first[k + 1]) ++k;
-        const int64_t lo = (tile - t.first[k]) * kTile;
-        const int64_t hi = lo + kTile < t.numel[k] ? lo + kTile : t.numel[k];
-        float s;
+// One tensor.  Its 16-byte vectors lie on 16-byte boundaries; the first and
+// the last may hold elements that are not its own, and go one by one.
+template <typename E>
+struct Flat {
+    using T = E;
+    static constexpr int kVec = 16 / sizeof(T);
+    const T *in;
+    T *out;
+    int64_t numel;
+
+    template <int CAP>
+    __device__ __forceinline__ Flat(const Table<CAP> &t, int k)
+        : in(static_cast<const T *>(t.in[k])), out(static_cast<T *>(t.out[k])), numel(t.numel[k]) {}
+    // Elements before the first 16-byte boundary.
+    __device__ __forceinline__ int head() const {
+        const int h = int((16 - (reinterpret_cast<uintptr_t>(in) & 15)) & 15) / int(sizeof(T));
+        return h < numel ? h : int(numel);
+    }
+    // The i-th of the elements before and after the body (past numel: none).
+    __device__ __forceinline__ int64_t lone(int h, int64_t body, int i) const { return i < h ? i : i + body * kVec; }
+    // Element at which vector v starts, counting from the boundary before the
+    // tensor (negative: before the tensor).
+    __device__ __forceinline__ int64_t start(int64_t v) const {
+        return v * kVec - int((reinterpret_cast<uintptr_t>(in) & 15) / sizeof(T));
+    }
+    __device__ __forceinline__ bool whole(int64_t e) const { return e >= 0 && e + kVec <= numel; }
+    __device__ __forceinline__ bool alike() const {
+        return ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    }
+    // The vector at element e, zeros in the place of what is not the tensor's.
+    __device__ __forceinline__ Vector<T> load(int64_t e) const {
+        if (whole(e)) return load_vec<T, kVec>(in + e);
+        Vector<T> x;
+        x.clear();
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (e + i >= 0 && e + i < numel) x.set(i, in[e + i]);
+        return x;
+    }
+    __device__ __forceinline__ void store(int64_t e, const Vector<T> &x) const {
+        if (whole(e) && alike()) {
+            *reinterpret_cast<uint4 *>(out + e) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (e + i >= 0 && e + i < numel) out[e + i] = x.elem(i);
+        }
+    }
+};
+
+// A tensor's body, from its first 16-byte boundary on, is cut into tiles of
+// vectors, kPer a thread and all in flight; the few elements before and after
+// the body go with its first tile, one a thread.
+template <int CAP, typename T>
+__device__ __forceinline__ float tile_squares(const Table<CAP> &t, int k, int tile) {
+    const Flat<T> a(t, k);
+    constexpr int kVec = Flat<T>::kVec;
+    const int head = a.head();
+    const int64_t body = (a.numel - head) / kVec, v0 = int64_t(tile - t.first[k]) * (kThreads * kPer) + threadIdx.x;
+    const T *p = a.in + head + v0 * kVec;
+    constexpr int kStep = kThreads * kVec;
+    Vector<T> x[kPer];
+    if (v0 - threadIdx.x + kThreads * kPer <= body) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u)
+            x[u] = tile < t.keep ? load_vec_cs<T, kVec>(p + u * kStep) : load_vec<T, kVec>(p + u * kStep);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            x[u].clear();
+            if (v0 + u * kThreads < body) x[u] = load_vec<T, kVec>(p + u * kStep);
+        }
+    }
+    float sum = 0.0f;
+    const int64_t lone = a.lone(head, body, threadIdx.x);
+    if (tile == t.first[k] && lone < a.numel) {
+        const float f = to_float(a.in[lone]);
+        sum = f * f;
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) sum += squares_of<T>(x[u]);
+    return sum;
+}
+
+template <int CAP, typename T>
+__device__ __forceinline__ void tile_scale(const Table<CAP> &t, int k, int tile, float c) {
+    const Flat<T> a(t, k);
+    constexpr int kVec = Flat<T>::kVec;
+    const int head = a.head();
+    const int64_t body = (a.numel - head) / kVec, v0 = int64_t(tile - t.first[k]) * (kThreads * kPer) + threadIdx.x;
+    const int64_t lone = a.lone(head, body, threadIdx.x);
+    if (tile == t.first[k] && lone < a.numel)
+        a.out[lone] = c == 1.0f ? a.in[lone] : from_float<T>(to_float(a.in[lone]) * c);
+    const T *p = a.in + head + v0 * kVec;
+    T *o = a.out + head + v0 * kVec;
+    constexpr int kStep = kThreads * kVec;
+    if (a.alike()) {
+        Vector<T> x[kPer];
+        if (v0 - threadIdx.x + kThreads * kPer <= body) {
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) x[u] = load_vec_cs<T, kVec>(p + u * kStep);
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) store_vec_cs<T, kVec>(o + u * kStep, scaled<T>(x[u], c));
+        } else {
+#pragma unroll
+            for (int u = 0; u < kPer; ++u)
+                if (v0 + u * kThreads < body) x[u] = load_vec<T, kVec>(p + u * kStep);
+#pragma unroll
+            for (int u = 0; u < kPer; ++u)
+                if (v0 + u * kThreads < body) store_vec_cs<T, kVec>(o + u * kStep, scaled<T>(x[u], c));
+        }
+    } else {                             // the results lie otherwise: element by element
+        const T *q = a.in + head;
+        T *r = a.out + head;
+        int64_t i = (v0 - threadIdx.x) * kVec + threadIdx.x, end = (v0 - threadIdx.x + kThreads * kPer) * kVec;
+        if (end > body * kVec) end = body * kVec;
+#pragma unroll 4
+        for (; i < end; i += kThreads) r[i] = c == 1.0f ? q[i] : from_float<T>(to_float(q[i]) * c);
+    }
+}
+
+// A sum of float32 values with the rounding errors of its additions beside
+// it: about 46 bits, at float32's rate (float64 additions of every thread
+// would take longer than a small list's memory traffic).  An infinity or a
+// NaN stays in `hi`.
+struct Sum {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum plus(Sum a, Sum b) {
+    const float s = a.hi + b.hi, v = s - a.hi;
+    return Sum{s, a.lo + b.lo + ((a.hi - (s - v)) + (b.hi - v))};
+}
+__device__ __forceinline__ Sum plus(Sum a, float b) { return plus(a, Sum{b, 0.0f}); }
+__device__ __forceinline__ float value_of(Sum a) { return isfinite(a.hi) ? a.hi + a.lo : a.hi; }
+template <int FROM>
+__device__ __forceinline__ Sum warp_sum(Sum v) {
+#pragma unroll
+    for (int o = FROM; o > 0; o >>= 1)
+        v = plus(v, Sum{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+    return v;
+}
+
+// Sum over the CTA, the same value in every thread (fixed order).
+constexpr int kWarps = kThreads / 32;
+__device__ __forceinline__ Sum block_sum(Sum v, Sum *s_red) {
+    v = warp_sum<16>(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum<kWarps / 2>(s_red[threadIdx.x & (kWarps - 1)]);
+}
+
+// This CTA's squares: plain float32 over a thread's vectors of a tile (at
+// most 33 elements), with the errors from there on.
+template <int CAP>
+__device__ __forceinline__ Sum sweep_squares(const Table<CAP> &t, Sum *s_red) {
+    Sum sum{0.0f, 0.0f};
+    const int tiles = t.first[t.count];
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int k = tensor_of(t, tile);
         if (t.dtype[k] == SS_F32)
-            s = tile_squares(static_cast<const float *>(t.in[k]), lo, hi);
+            sum = plus(sum, tile_squares<CAP, float>(t, k, tile));
         else if (t.dtype[k] == SS_F16)
-            s = tile_squares(static_cast<const __half *>(t.in[k]), lo, hi);
+            sum = plus(sum, tile_squares<CAP, __half>(t, k, tile));
         else
-            s = tile_squares(static_cast<const __nv_bfloat16 *>(t.in[k]), lo, hi);
-        sum += s;
+            sum = plus(sum, tile_squares<CAP, __nv_bfloat16>(t, k, tile));
     }
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) sum += s_red[w];
-        part[blockIdx.x] = sum;
-    }
+    return block_sum(sum, s_red);
 }
 
-__global__ void __launch_bounds__(kThreads) k_clip_result(const double *part, int parts, float max_norm, float eps,
-                                                          bool clip, float *result) {
-    __shared__ double s_red[kThreads / 32];
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kThreads) sum += part[i];
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) sum += s_red[w];
-        const float norm = float(sqrt(sum));
-        const bool fine = isfinite(norm);
-        result[0] = norm;
-        result[1] = !fine ? 0.0f : (clip ? fminf(1.0f, max_norm / (norm + eps)) : 1.0f);
+// (norm, coefficient).
+__device__ __forceinline__ float2 result_of(Sum squares, float max_norm, float eps, bool clip) {
+    const float norm = sqrtf(value_of(squares));
+    const float coef = !isfinite(norm) ? 0.0f : (clip ? fminf(1.0f, max_norm / (norm + eps)) : 1.0f);
+    return make_float2(norm, coef);
+}
+__device__ __forceinline__ Sum sum_parts(const float2 *part, int parts, Sum *s_red) {
+    Sum sum{0.0f, 0.0f};
+    for (int i = threadIdx.x; i < parts; i += kThreads) {
+        const float2 q = __ldcg(part + i);
+        sum = plus(sum, Sum{q.x, q.y});
     }
+    return block_sum(sum, s_red);
 }
 
-__global__ void __launch_bounds__(kThreads) k_clip_scale(Table t, const float *result) {
-    const bool fine = isfinite(result[0]);
-    const float c = fine ? result[1] : 1.0f;
-    int k = 0;
-    for (int64_t tile = blockIdx.x; tile < t.first[t.count]; tile += gridDim.x) {
-        while (tile >= t.first[k + 1]) ++k;
+template <int CAP>
+__device__ __forceinline__ void sweep_scale(const Table<CAP> &t, float2 r) {
+    const float c = isfinite(r.x) ? r.y : 1.0f;      // nothing is scaled by a norm that is not finite
+    const int tiles = t.first[t.count], mine = tiles - int(blockIdx.x);
+    if (mine <= 0) return;
+    for (int tile = int(blockIdx.x) + (mine - 1) / int(gridDim.x) * int(gridDim.x); tile >= 0; tile -= gridDim.x) {
+        const int k = tensor_of(t, tile);
         if (c == 1.0f && t.in[k] == t.out[k]) continue;
-        const int64_t lo = (tile - t.first[k]) * kTile;
-        const int64_t hi = lo + kTile < t.numel[k] ? lo + kTile : t.numel[k];
         if (t.dtype[k] == SS_F32)
-            tile_scale(static_cast<const float *>(t.in[k]), static_cast<float *>(t.out[k]), lo, hi, c);
+            tile_scale<CAP, float>(t, k, tile, c);
         else if (t.dtype[k] == SS_F16)
-            tile_scale(static_cast<const __half *>(t.in[k]), static_cast<__half *>(t.out[k]), lo, hi, c);
+            tile_scale<CAP, __half>(t, k, tile, c);
         else
-            tile_scale(static_cast<const __nv_bfloat16 *>(t.in[k]), static_cast<__nv_bfloat16 *>(t.out[k]), lo, hi, c);
+            tile_scale<CAP, __nv_bfloat16>(t, k, tile, c);
     }
 }
 
-int batches(int32_t n) { return n < 1 ? 1 : (n + kBatch - 1) / kBatch; }
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 2) k_clip(const __grid_constant__ Table<CAP> t, float max_norm, float eps,
+                                                   float2 *part, float *result) {
+    __shared__ Sum s_red[kWarps];
+    const Sum sum = sweep_squares(t, s_red);
+    if (threadIdx.x == 0) part[blockIdx.x] = make_float2(sum.hi, sum.lo);
+    cooperative_groups::this_grid().sync();
+    const float2 r = result_of(sum_parts(part, gridDim.x, s_red), max_norm, eps, true);
+    if (blockIdx.x == 0 && threadIdx.x == 0) result[0] = r.x, result[1] = r.y;
+    sweep_scale(t, r);
+}
 
-void fill(Table *t, const ss_tensor *h, int32_t n, int b) {
+// Gradients of up to half a megabyte: one cluster of CTAs holds them in
+// registers between the norm and the scaling, so they are read once and the
+// CTAs meet at the cluster's barrier, which costs a fraction of a grid's.
+// (Tiles here are 8 KB, one vector a thread.)
+constexpr int kCluster = 8, kHeld = 8;
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+    k_clip_small(const __grid_constant__ Table<kSmallList> t, float max_norm, float eps, float *result) {
+    __shared__ Sum s_red[kWarps], s_part[kCluster];
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int tiles = t.first[t.count], rank = int(cluster.block_rank());
+    uint4 held[kHeld];
+    auto at = [&](int u, auto f) {       // f on this thread's vector of the CTA's u-th tile
+        const int tile = u * kCluster + rank;
+        if (tile >= tiles) return;
+        const int k = tensor_of(t, tile);
+        const int64_t v = int64_t(tile - t.first[k]) * kThreads + threadIdx.x;
+        if (t.dtype[k] == SS_F32)
+            f(Flat<float>(t, k), v);
+        else if (t.dtype[k] == SS_F16)
+            f(Flat<__half>(t, k), v);
+        else
+            f(Flat<__nv_bfloat16>(t, k), v);
+    };
+    auto vector_of = [&](auto a, int u) {
+        Vector<typename decltype(a)::T> x;
+        x.w[0] = held[u].x, x.w[1] = held[u].y, x.w[2] = held[u].z, x.w[3] = held[u].w;
+        return x;
+    };
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+        at(u, [&](auto a, int64_t v) {
+            const auto x = a.load(a.start(v));
+            held[u] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+        });
+    Sum sum{0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+        at(u, [&](auto a, int64_t) { sum = plus(sum, squares_of<typename decltype(a)::T>(vector_of(a, u))); });
+    sum = block_sum(sum, s_red);
+    if (threadIdx.x < kCluster) *cluster.map_shared_rank(&s_part[rank], threadIdx.x) = sum;
+    cluster.sync();
+    sum = s_part[0];
+#pragma unroll
+    for (int q = 1; q < kCluster; ++q) sum = plus(sum, s_part[q]);
+    const float2 r = result_of(sum, max_norm, eps, true);
+    if (rank == 0 && threadIdx.x == 0) result[0] = r.x, result[1] = r.y;
+    const float c = isfinite(r.x) ? r.y : 1.0f;      // nothing is scaled by a norm that is not finite
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+        at(u, [&](auto a, int64_t v) {
+            if (c == 1.0f && static_cast<const void *>(a.in) == a.out) return;
+            a.store(a.start(v), scaled<typename decltype(a)::T>(vector_of(a, u), c));
+        });
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) k_clip_squares(const __grid_constant__ Table<CAP> t, float2 *part) {
+    __shared__ Sum s_red[kWarps];
+    const Sum sum = sweep_squares(t, s_red);
+    if (threadIdx.x == 0) part[blockIdx.x] = make_float2(sum.hi, sum.lo);
+}
+
+__global__ void __launch_bounds__(kThreads) k_clip_result(const float2 *part, int parts, float max_norm, float eps,
+                                                          bool clip, float *result) {
+    __shared__ Sum s_red[kWarps];
+    const float2 r = result_of(sum_parts(part, parts, s_red), max_norm, eps, clip);
+    if (threadIdx.x == 0) result[0] = r.x, result[1] = r.y;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) k_clip_scale(const __grid_constant__ Table<kLongList> t,
+                                                         const float *result) {
+    sweep_scale(t, make_float2(result[0], result[1]));
+}
+
+// ------------------------------------------------------------------ host
+
+// Tiles of a tensor with elements, counting from the boundary before it: at
+// least as many as its body takes.
+int64_t tiles_of(const ss_tensor &t, int tile) {
+    const int64_t bytes = t.numel * int64_t(dtype_bytes(t.dtype)) + int64_t(reinterpret_cast<uintptr_t>(t.in) & 15);
+    return (bytes + tile - 1) / tile;
+}
+
+// Tensors [from, to) that have elements into a launch's table.
+template <int CAP>
+void fill(Table<CAP> *t, const ss_tensor *h, int32_t from, int32_t to, int tile = kTile) {
     t->count = 0;
     t->first[0] = 0;
-    for (int32_t i = b * kBatch; i < n && i < (b + 1) * kBatch; ++i) {
+    for (int32_t i = from; i < to; ++i) {
+        if (h[i].numel == 0) continue;
         const int k = t->count++;
-        t->in[k] = h[i].in, t->out[k] = h[i].out, t->numel[k] = h[i].numel, t->dtype[k] = h[i].dtype;
-        t->first[k + 1] = t->first[k] + (h[i].numel + kTile - 1) / kTile;
+        t->in[k] = h[i].in, t->out[k] = h[i].out, t->numel[k] = h[i].numel, t->dtype[k] = uint8_t(h[i].dtype);
+        t->first[k + 1] = t->first[k] + int32_t(tiles_of(h[i], tile));
     }
+    const int64_t keep = t->first[t->count] - kKeep / tile;
+    t->keep = keep > 0 ? int32_t(keep) : 0;
+}
+
+// CTAs that are on the device together.
+template <typename K>
+int resident(K kernel, int sms) {
+    static std::atomic<int> known{0};
+    int per_sm = known.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0) != cudaSuccess || per_sm < 1)
+            per_sm = 1;
+        known.store(per_sm, std::memory_order_relaxed);
+    }
+    return sms * per_sm < kMaxGrid ? sms * per_sm : kMaxGrid;
+}
+
+int parts_of(int32_t n) { return (n + kLongList - 1) / kLongList; }
+
+template <int CAP>
+ss_status clip_once(const ss_tensor *h, int32_t n, float max_norm, float eps, float *result, float2 *part, int sms,
+                    cudaStream_t s) {
+    Table<CAP> t;
+    fill(&t, h, 0, n);
+    auto kernel = k_clip<CAP>;
+    const int most = resident(kernel, sms), tiles = t.first[t.count];
+    const int grid = tiles < 1 ? 1 : (tiles < most ? tiles : most);
+    void *args[] = {&t, &max_norm, &eps, &part, &result};
+    SS_LAUNCH("k_clip", s, cudaLaunchCooperativeKernel((const void *)kernel, dim3(grid), dim3(kThreads), args, 0, s));
+    return check_launch("ss_grad_clip");
+}
+
+// A launch for each part of the list.
+template <int CAP>
+int squares(const ss_tensor *h, int32_t from, int32_t to, float2 *part, int sms, cudaStream_t s) {
+    Table<CAP> t;
+    fill(&t, h, from, to);
+    auto kernel = k_clip_squares<CAP>;
+    const int most = resident(kernel, sms), tiles = t.first[t.count];
+    const int grid = tiles < 1 ? 1 : (tiles < most ? tiles : most);
+    SS_LAUNCH("k_clip_squares", s, kernel<<<grid, kThreads, 0, s>>>(t, part));
+    return grid;
 }
 
 ss_status run(const char *who, const ss_tensor *h, int32_t n, bool clip, float max_norm, float eps, float *result,
@@ -141,18 +465,36 @@ ss_status run(const char *who, const ss_tensor *h, int32_t n, bool clip, float m
         return fail(SS_ERR_INVALID_ARG, "%s: workspace NULL or not 256-byte aligned", who);
     const size_t need = ss_clip_workspace_bytes(n);
     if (bytes < need) return fail(SS_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu", who, bytes, need);
-    double *part = static_cast<double *>(workspace);
-    Table t;
-    for (int b = 0; b < batches(n); ++b) {
-        fill(&t, h, n, b);
-        SS_LAUNCH("k_clip_squares", s, k_clip_squares<<<kGrid, kThreads, 0, s>>>(t, part + size_t(b) * kGrid));
+    int dev = 0, sms = 0;
+    ss_status st = current_device(&dev, &sms, who);
+    if (st != SS_OK) return st;
+    float2 *part = static_cast<float2 *>(workspace);
+    if (clip && n <= kSmallList && total <= kCluster * kHeld * (kThreads * 8)) {   // 16 bytes hold 8 at most
+        Table<kSmallList> t;
+        fill(&t, h, 0, n, kThreads * 16);
+        if (t.first[t.count] <= kCluster * kHeld) {
+            SS_LAUNCH("k_clip_small", s,
+                      k_clip_small<<<kCluster, kThreads, 0, s>>>(t, max_norm, eps, result));
+            return check_launch(who);
+        }
     }
-    SS_LAUNCH("k_clip_result", s,
-              k_clip_result<<<1, kThreads, 0, s>>>(part, batches(n) * kGrid, max_norm, eps, clip, result));
+    if (clip && n <= kSmallList) return clip_once<kSmallList>(h, n, max_norm, eps, result, part, sms, s);
+    if (clip && n <= kLongList) return clip_once<kLongList>(h, n, max_norm, eps, result, part, sms, s);
+    int parts = 0;
+    if (n <= kSmallList)
+        parts = squares<kSmallList>(h, 0, n, part, sms, s);
+    else
+        for (int32_t from = 0; from < n; from += kLongList)
+            parts += squares<kLongList>(h, from, from + kLongList < n ? from + kLongList : n, part + parts, sms, s);
+    SS_LAUNCH("k_clip_result", s, k_clip_result<<<1, kThreads, 0, s>>>(part, parts, max_norm, eps, clip, result));
     if (clip)
-        for (int b = 0; b < batches(n); ++b) {
-            fill(&t, h, n, b);
-            SS_LAUNCH("k_clip_scale", s, k_clip_scale<<<kGrid, kThreads, 0, s>>>(t, result));
+        for (int32_t from = 0; from < n; from += kLongList) {
+            Table<kLongList> t;
+            fill(&t, h, from, from + kLongList < n ? from + kLongList : n);
+            const int tiles = t.first[t.count], most = resident(k_clip_scale, sms);
+            if (tiles > 0)
+                SS_LAUNCH("k_clip_scale", s,
+                          k_clip_scale<<<tiles < most ? tiles : most, kThreads, 0, s>>>(t, result));
         }
     return check_launch(who);
 }
@@ -166,7 +508,7 @@ extern "C" {
 
 size_t ss_clip_workspace_bytes(int32_t n_tensors) {
     if (n_tensors < 0 || n_tensors > kMaxTensors) return 0;
-    return size_t(batches(n_tensors)) * kGrid * sizeof(double);
+    return size_t(n_tensors < 1 ? 1 : parts_of(n_tensors)) * kMaxGrid * sizeof(float2);
 }
 
 ss_status ss_grad_clip(const ss_tensor *h_tensors, int32_t n_tensors, float max_norm, float eps, float *result,

@@ -37,10 +37,19 @@ struct Vec {
     uint32_t w[4];
     __device__ __forceinline__ float get(int i) const { return get_as(i, T()); }
     __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    // Element i as it is.
+    __device__ __forceinline__ T elem(int i) const { return elem_as(i, T()); }
     // Puts element i in place (after clear()).
     __device__ __forceinline__ void set(int i, T v) { set_as(i, v); }
 
   private:
+    __device__ __forceinline__ float elem_as(int i, float) const { return __uint_as_float(w[i]); }
+    __device__ __forceinline__ __nv_bfloat16 elem_as(int i, __nv_bfloat16) const {
+        return __ushort_as_bfloat16(static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1))));
+    }
+    __device__ __forceinline__ __half elem_as(int i, __half) const {
+        return __ushort_as_half(static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1))));
+    }
     __device__ __forceinline__ void set_as(int i, float v) { w[i] = __float_as_uint(v); }
     __device__ __forceinline__ void set_as(int i, __nv_bfloat16 v) {
         w[i >> 1] |= uint32_t(__bfloat16_as_ushort(v)) << (16 * (i & 1));
@@ -73,6 +82,19 @@ __device__ __forceinline__ Vec<T, N> load_vec(const T *p) {
         x.w[0] = u.x, x.w[1] = u.y, x.w[2] = u.z, x.w[3] = u.w;
     }
     return x;
+}
+
+// The same, and a store of it, marked to leave the caches first.
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> load_vec_cs(const T *p) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
+    Vec<T, N> x;
+    x.w[0] = u.x, x.w[1] = u.y, x.w[2] = u.z, x.w[3] = u.w;
+    return x;
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_vec_cs(T *p, const Vec<T, N> &x) {
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]));
 }
 
 // Two floats rounded to T, the first in the low half.

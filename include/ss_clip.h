@@ -7,14 +7,15 @@
  *   out  = coef * x
  *
  * A norm that is not finite (an infinity or a NaN among the gradients, or
- * squares past float64) scales nothing: coef is reported as 0, gradients
+ * squares that add up past float32) scales nothing: coef is reported as 0, gradients
  * clipped in place keep their values and separate outputs receive copies, so
  * that the caller can see which step to skip.  Where coef is 1, in-place
  * gradients are not written.
  *
  * Squares are summed in float32 over at most a few dozen values and from
- * there on in float64, along splits that depend on the sizes alone: the same
- * inputs give the same bits.  Conventions are those of ss.h.
+ * there on in pairs of float32 that keep the additions' rounding errors,
+ * along splits that depend on the sizes and alignments alone: the same inputs
+ * give the same bits.  Conventions are those of ss.h.
  */
 #ifndef SS_CLIP_H
 #define SS_CLIP_H
