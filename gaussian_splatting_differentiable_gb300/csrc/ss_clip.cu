@@ -1,17 +1,13 @@
 // The norm of all gradients and their scaling by it (model: include/ss_clip.h).
 //
 // Bound by memory: every gradient has to be read for the norm and again to be
-// scaled, and the scaled values written.  One cooperative launch does both:
-// its CTAs sweep the tensors' 32 KB tiles from the first to the last adding
-// squares, meet at a grid barrier, add everybody's partial sums in the same
-// order, and sweep back from the last tile to the first, so that what the
-// first sweep read last is still in L2 (129 MB) when the second begins.
-// A few small tensors never leave the registers of one cluster.
-// Tiles that the second sweep will not find there, and all that it reads and
-// writes, are marked to leave L2 first.  The list of tensors travels in the
-// launch's parameters: nothing is copied to the device, and a captured graph
-// keeps its own list.  Lists too long for one launch's parameters take a
-// launch for each part of the list and sweep.
+// scaled, and the scaled values written.  A sweep over the tensors' tiles,
+// from the first to the last, adds squares; a second goes back from the last
+// tile to the first, so that what the first read last is still in L2 (129 MB).
+// Tiles that it will not find there, and all that it reads and writes itself,
+// are marked to leave L2 first.  A few small tensors take one launch and never
+// leave the registers of one cluster.  The list of tensors travels in the launches' parameters: nothing is copied to
+// the device, and a captured graph keeps its own list.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -21,16 +17,17 @@
 
 #include "ss_clip.h"
 #include "ss_internal.h"
+#include "ss_launch.cuh"
 #include "ss_profile.h"
 #include "ss_vec.cuh"
 
 namespace ss {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kPer = 4;                          // 16-byte vectors of a tile in one thread
 constexpr int kTile = kThreads * kPer * 16;      // bytes
-constexpr int kMaxGrid = 1024;                   // partial sums of one launch
+constexpr int kMaxGrid = 2048;                   // partial sums of one launch
 constexpr int kSmallList = 24, kLongList = 1000; // tensors in one launch's parameters
 constexpr int32_t kMaxTensors = 65536;
 // What of the first sweep's bytes the second is let find in L2: a part of its
@@ -272,32 +269,15 @@ __device__ __forceinline__ Sum sum_parts(const float2 *part, int parts, Sum *s_r
 }
 
 template <int CAP>
-__device__ __forceinline__ void sweep_scale(const Table<CAP> &t, float2 r) {
-    const float c = isfinite(r.x) ? r.y : 1.0f;      // nothing is scaled by a norm that is not finite
-    const int tiles = t.first[t.count], mine = tiles - int(blockIdx.x);
-    if (mine <= 0) return;
-    for (int tile = int(blockIdx.x) + (mine - 1) / int(gridDim.x) * int(gridDim.x); tile >= 0; tile -= gridDim.x) {
-        const int k = tensor_of(t, tile);
-        if (c == 1.0f && t.in[k] == t.out[k]) continue;
-        if (t.dtype[k] == SS_F32)
-            tile_scale<CAP, float>(t, k, tile, c);
-        else if (t.dtype[k] == SS_F16)
-            tile_scale<CAP, __half>(t, k, tile, c);
-        else
-            tile_scale<CAP, __nv_bfloat16>(t, k, tile, c);
-    }
-}
-
-template <int CAP>
-__global__ void __launch_bounds__(kThreads, 2) k_clip(const __grid_constant__ Table<CAP> t, float max_norm, float eps,
-                                                   float2 *part, float *result) {
-    __shared__ Sum s_red[kWarps];
-    const Sum sum = sweep_squares(t, s_red);
-    if (threadIdx.x == 0) part[blockIdx.x] = make_float2(sum.hi, sum.lo);
-    cooperative_groups::this_grid().sync();
-    const float2 r = result_of(sum_parts(part, gridDim.x, s_red), max_norm, eps, true);
-    if (blockIdx.x == 0 && threadIdx.x == 0) result[0] = r.x, result[1] = r.y;
-    sweep_scale(t, r);
+__device__ __forceinline__ void scale_tile(const Table<CAP> &t, int tile, float c) {
+    const int k = tensor_of(t, tile);
+    if (c == 1.0f && t.in[k] == t.out[k]) return;
+    if (t.dtype[k] == SS_F32)
+        tile_scale<CAP, float>(t, k, tile, c);
+    else if (t.dtype[k] == SS_F16)
+        tile_scale<CAP, __half>(t, k, tile, c);
+    else
+        tile_scale<CAP, __nv_bfloat16>(t, k, tile, c);
 }
 
 // Gradients of up to half a megabyte: one cluster of CTAs holds them in
@@ -356,9 +336,11 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
         });
 }
 
+// CTAs that stay on the device and share the tiles out.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) k_clip_squares(const __grid_constant__ Table<CAP> t, float2 *part) {
     __shared__ Sum s_red[kWarps];
+    start_dependents();
     const Sum sum = sweep_squares(t, s_red);
     if (threadIdx.x == 0) part[blockIdx.x] = make_float2(sum.hi, sum.lo);
 }
@@ -366,13 +348,19 @@ __global__ void __launch_bounds__(kThreads) k_clip_squares(const __grid_constant
 __global__ void __launch_bounds__(kThreads) k_clip_result(const float2 *part, int parts, float max_norm, float eps,
                                                           bool clip, float *result) {
     __shared__ Sum s_red[kWarps];
+    start_dependents();
+    wait_for_previous();
     const float2 r = result_of(sum_parts(part, parts, s_red), max_norm, eps, clip);
     if (threadIdx.x == 0) result[0] = r.x, result[1] = r.y;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) k_clip_scale(const __grid_constant__ Table<kLongList> t,
-                                                         const float *result) {
-    sweep_scale(t, make_float2(result[0], result[1]));
+// A CTA for each tile, the last tiles first: the device hands them out as
+// CTAs finish, which keeps the two memories' halves evenly busy.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 4) k_clip_scale(const __grid_constant__ Table<CAP> t, const float *result) {
+    wait_for_previous();
+    const float norm = result[0], coef = result[1];
+    scale_tile(t, t.first[t.count] - 1 - int(blockIdx.x), isfinite(norm) ? coef : 1.0f);
 }
 
 // ------------------------------------------------------------------ host
@@ -412,31 +400,36 @@ int resident(K kernel, int sms) {
     return sms * per_sm < kMaxGrid ? sms * per_sm : kMaxGrid;
 }
 
-int parts_of(int32_t n) { return (n + kLongList - 1) / kLongList; }
-
+// Squares of the table's tensors; parts: how many partial sums there are.
 template <int CAP>
-ss_status clip_once(const ss_tensor *h, int32_t n, float max_norm, float eps, float *result, float2 *part, int sms,
-                    cudaStream_t s) {
-    Table<CAP> t;
-    fill(&t, h, 0, n);
-    auto kernel = k_clip<CAP>;
-    const int most = resident(kernel, sms), tiles = t.first[t.count];
-    const int grid = tiles < 1 ? 1 : (tiles < most ? tiles : most);
-    void *args[] = {&t, &max_norm, &eps, &part, &result};
-    SS_LAUNCH("k_clip", s, cudaLaunchCooperativeKernel((const void *)kernel, dim3(grid), dim3(kThreads), args, 0, s));
-    return check_launch("ss_grad_clip");
+void launch_squares(const Table<CAP> &t, float2 *part, int *parts, int sms, cudaStream_t s) {
+    auto kernel = k_clip_squares<CAP>;
+    const int most = resident(kernel, sms), tiles = t.first[t.count], grid = tiles < 1 ? 1 : (tiles < most ? tiles : most);
+    SS_LAUNCH("k_clip_squares", s, kernel<<<grid, kThreads, 0, s>>>(t, part + *parts));
+    *parts += grid;
 }
 
-// A launch for each part of the list.
+void launch_result(const float2 *part, int parts, float max_norm, float eps, bool clip, float *result, cudaStream_t s) {
+    SS_LAUNCH("k_clip_result", s,
+              launch_after(k_clip_result, dim3(1), kThreads, 0, s, part, parts, max_norm, eps, clip, result));
+}
+
 template <int CAP>
-int squares(const ss_tensor *h, int32_t from, int32_t to, float2 *part, int sms, cudaStream_t s) {
+void launch_scale(const Table<CAP> &t, const float *result, cudaStream_t s) {
+    if (t.first[t.count] > 0)
+        SS_LAUNCH("k_clip_scale", s, launch_after(k_clip_scale<CAP>, dim3(t.first[t.count]), kThreads, 0, s, t, result));
+}
+
+// A list that fits one launch's parameters.
+template <int CAP>
+void clip_list(const ss_tensor *h, int32_t n, bool clip, float max_norm, float eps, float *result, float2 *part, int sms,
+               cudaStream_t s) {
     Table<CAP> t;
-    fill(&t, h, from, to);
-    auto kernel = k_clip_squares<CAP>;
-    const int most = resident(kernel, sms), tiles = t.first[t.count];
-    const int grid = tiles < 1 ? 1 : (tiles < most ? tiles : most);
-    SS_LAUNCH("k_clip_squares", s, kernel<<<grid, kThreads, 0, s>>>(t, part));
-    return grid;
+    int parts = 0;
+    fill(&t, h, 0, n);
+    launch_squares(t, part, &parts, sms, s);
+    launch_result(part, parts, max_norm, eps, clip, result, s);
+    if (clip) launch_scale(t, result, s);
 }
 
 ss_status run(const char *who, const ss_tensor *h, int32_t n, bool clip, float max_norm, float eps, float *result,
@@ -478,24 +471,23 @@ ss_status run(const char *who, const ss_tensor *h, int32_t n, bool clip, float m
             return check_launch(who);
         }
     }
-    if (clip && n <= kSmallList) return clip_once<kSmallList>(h, n, max_norm, eps, result, part, sms, s);
-    if (clip && n <= kLongList) return clip_once<kLongList>(h, n, max_norm, eps, result, part, sms, s);
-    int parts = 0;
-    if (n <= kSmallList)
-        parts = squares<kSmallList>(h, 0, n, part, sms, s);
-    else
-        for (int32_t from = 0; from < n; from += kLongList)
-            parts += squares<kLongList>(h, from, from + kLongList < n ? from + kLongList : n, part + parts, sms, s);
-    SS_LAUNCH("k_clip_result", s, k_clip_result<<<1, kThreads, 0, s>>>(part, parts, max_norm, eps, clip, result));
-    if (clip)
+    if (n <= kSmallList) {
+        clip_list<kSmallList>(h, n, clip, max_norm, eps, result, part, sms, s);
+    } else if (n <= kLongList) {
+        clip_list<kLongList>(h, n, clip, max_norm, eps, result, part, sms, s);
+    } else {                             // a launch for each part of the list
+        Table<kLongList> t;
+        int parts = 0;
         for (int32_t from = 0; from < n; from += kLongList) {
-            Table<kLongList> t;
             fill(&t, h, from, from + kLongList < n ? from + kLongList : n);
-            const int tiles = t.first[t.count], most = resident(k_clip_scale, sms);
-            if (tiles > 0)
-                SS_LAUNCH("k_clip_scale", s,
-                          k_clip_scale<<<tiles < most ? tiles : most, kThreads, 0, s>>>(t, result));
+            launch_squares(t, part, &parts, sms, s);
         }
+        launch_result(part, parts, max_norm, eps, clip, result, s);
+        for (int32_t from = 0; clip && from < n; from += kLongList) {
+            fill(&t, h, from, from + kLongList < n ? from + kLongList : n);
+            launch_scale(t, result, s);
+        }
+    }
     return check_launch(who);
 }
 
@@ -508,7 +500,7 @@ extern "C" {
 
 size_t ss_clip_workspace_bytes(int32_t n_tensors) {
     if (n_tensors < 0 || n_tensors > kMaxTensors) return 0;
-    return size_t(n_tensors < 1 ? 1 : parts_of(n_tensors)) * kMaxGrid * sizeof(float2);
+    return size_t(n_tensors < 1 ? 1 : (n_tensors + kLongList - 1) / kLongList) * kMaxGrid * sizeof(float2);
 }
 
 ss_status ss_grad_clip(const ss_tensor *h_tensors, int32_t n_tensors, float max_norm, float eps, float *result,

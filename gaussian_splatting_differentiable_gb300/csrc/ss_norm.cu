@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "ss_internal.h"
+#include "ss_launch.cuh"
 #include "ss_norm.h"
 #include "ss_profile.h"
 #include "ss_vec.cuh"
@@ -452,6 +453,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
             store_row<T, VEC, SHIFT>(pdx, dx.same, v, c, a[k]);
         }
     }
+    start_dependents();
     if (!part) return;
     // The CTA's sum, in fixed order: the rows of a warp are joined by shuffles
     // first where they start alike (!MULTI, !SHIFT), then the warps or groups
@@ -507,6 +509,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
 __global__ void __launch_bounds__(1024) k_norm_bwd_final(const float *part, int parts, int32_t D, void *dgamma,
                                                          void *dbeta, int pdt) {
     __shared__ float s_t[32][33];
+    wait_for_previous();
     const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + c;
     float t = 0.0f;
@@ -777,7 +780,8 @@ ss_status bwd_kernel(const BwdArgs &a, const Place &pl, int sms, cudaStream_t s)
                                                  a.dgamma ? a.part : nullptr));
     if (a.dgamma)
         SS_LAUNCH("k_norm_bwd_final", s,
-                  k_norm_bwd_final<<<(2 * a.D + 31) / 32, 1024, 0, s>>>(a.part, grid, a.D, a.dgamma, a.dbeta, a.pdt));
+                  launch_after(k_norm_bwd_final, dim3((2 * a.D + 31) / 32), 1024, 0, s, a.part, grid, a.D, a.dgamma,
+                               a.dbeta, a.pdt));
     return SS_OK;
 }
 
@@ -840,8 +844,8 @@ ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
                                                                     static_cast<const T *>(a.x), a.xs, a.n, a.D,
                                                                     a.mean, a.rstd, a.part));
         SS_LAUNCH("k_norm_bwd_final", s,
-                  k_norm_bwd_final<<<(2 * a.D + 31) / 32, 1024, 0, s>>>(a.part, int(g.y), a.D, a.dgamma, a.dbeta,
-                                                                        a.pdt));
+                  launch_after(k_norm_bwd_final, dim3((2 * a.D + 31) / 32), 1024, 0, s, a.part, int(g.y), a.D,
+                               a.dgamma, a.dbeta, a.pdt));
     }
     if (a.n == 0) return SS_OK;
     SS_LAUNCH("k_norm_bwd_rows_wide", s,
