@@ -502,10 +502,6 @@ class Embedding:
         ss_embed_bwd(dout, ids, self.scale, self.grad, self.workspace, stream)
         return self.grad
 
-    def check(self, stream=None) -> None:
-        """Raise if the last backward's sort gave up a bounded wait."""
-        _check(_L.ss_embed_status(_ptr(self.workspace), _stream(stream)), "ss_embed_status")
-
 
 # ---- layer norm (ss_norm.h)
 

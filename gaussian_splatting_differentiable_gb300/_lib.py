@@ -108,7 +108,6 @@ TRAIN_PROTOTYPES = {
     "ss_embed_workspace_bytes": (SZ, [I64, I64, I32]),
     "ss_embed_bwd": (ctypes.c_int, [P, I32, I64, P, I32, I64, I64, I32, F32, P, I32, I64, P, SZ,
                                     P]),
-    "ss_embed_status": (ctypes.c_int, [P, P]),
     "ss_layer_norm_fwd": (ctypes.c_int, [P, I32, I64, I64, I32, P, P, I32, F32, P, I64, P, P, P]),
     "ss_layer_norm_workspace_bytes": (SZ, [I64, I32]),
     "ss_layer_norm_bwd": (ctypes.c_int, [P, I64, P, I64, I32, I64, I32, P, I32, P, P, P, I64, P,

@@ -1,20 +1,20 @@
 // Rows of a learned table looked up by id, and the table's gradient (model:
 // include/ss_embed.h).
 //
-// Backward.  k_embed_hist counts the ids' digits and clears dtable;
-// k_embed_pass is one stable onesweep pass over an 8-bit digit of the id
-// (words id << 32 | position; an id outside [0, V) becomes V and sorts past
-// every row); k_embed_sum walks fixed chunks of the sorted words and adds
-// dout rows: an id whose words lie inside one chunk is finished there, one
-// that crosses chunks leaves a partial sum at each end of each chunk that
-// k_embed_join adds in chunk order.
+// Backward.  (id, position) words are sorted by id (k_embed_sort_small, or
+// k_embed_count / k_embed_scan / k_embed_move for each digit), while CTAs
+// beside the sort's clear dtable; k_embed_sum walks fixed chunks of the sorted
+// words and adds dout rows, and k_embed_join adds up the ids that cross chunks.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "ss_embed.h"
 #include "ss_internal.h"
+#include "ss_launch.cuh"
 #include "ss_profile.h"
 #include "ss_vec.cuh"
 
@@ -23,37 +23,68 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int32_t kMaxD = 65536;
-constexpr int kPart = 4096;              // words of one sort partition
-constexpr int kKpt = kPart / kThreads;
-constexpr int kMaxPasses = 4;
-constexpr uint32_t kFlagAgg = 1u << 30, kFlagInc = 2u << 30, kValMask = kFlagAgg - 1;
-constexpr uint32_t kSpinLimit = 1u << 22;
 
 // ------------------------------------------------------------------ forward
 
-template <typename T, typename I>
-__global__ void __launch_bounds__(kThreads) k_embed_fwd(const T *__restrict__ table, int64_t ts, int64_t V, int32_t D,
+// `lanes` threads take a row, NV vectors each (N elements a vector: as many as
+// every row's start and end are aligned to), and ROWS rows at a time so that
+// the ids' loads, and then the rows', wait together.  Bound by the writes of
+// out (and the table's reads where it does not stay in L2).
+template <typename T, typename I, int N, int NV, int ROWS>
+__global__ void __launch_bounds__(kThreads) k_embed_fwd(const T *__restrict__ table, int64_t ts, int64_t V,
                                                         const I *__restrict__ ids, int64_t n, float scale, T *out,
-                                                        int64_t os) {
-    const int64_t total = n * D, stride = int64_t(gridDim.x) * kThreads;
-    for (int64_t e = int64_t(blockIdx.x) * kThreads + threadIdx.x; e < total; e += stride) {
-        const int64_t i = e / D;
-        const int j = int(e - i * D);
-        const int64_t id = int64_t(ids[i]);
-        const float v = id >= 0 && id < V ? to_float(table[id * ts + j]) * scale : 0.0f;
-        out[i * os + j] = from_float<T>(v);
+                                                        int64_t os, int shift, int vecs) {
+    const int lanes = 1 << shift, lane = threadIdx.x & (lanes - 1);
+    const int64_t row0 = int64_t(blockIdx.x) * ((kThreads >> shift) * ROWS) + (threadIdx.x >> shift);
+    const int rstep = kThreads >> shift;
+    int64_t id[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) id[r] = row0 + r * rstep < n ? int64_t(ids[row0 + r * rstep]) : -1;
+    for (int v0 = lane; v0 < vecs; v0 += lanes * NV) {
+        Vec<T, N> x[ROWS][NV];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                x[r][k].clear();
+                if (id[r] >= 0 && id[r] < V && v0 + k * lanes < vecs)
+                    x[r][k] = load_vec<T, N>(table + id[r] * ts + (v0 + k * lanes) * N);
+            }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (row0 + r * rstep >= n || v0 + k * lanes >= vecs) continue;
+                const bool here = id[r] >= 0 && id[r] < V;    // no row: zeros, not 0 times the scale
+                float f[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] = here ? x[r][k].get(i) * scale : 0.0f;
+                store_floats<T, N>(out + (row0 + r * rstep) * os + (v0 + k * lanes) * N, f);
+            }
     }
 }
 
 // ------------------------------------------------------------------ sort
 
+constexpr int kPart = 4096;              // ids of one sort partition
+constexpr int kKpt = kPart / kThreads;
+constexpr int kMaxBits = 10;             // of a digit: at most 1024 bins
+constexpr int kSmallN = 8192;            // ids that one CTA sorts by itself
+constexpr int kSmallThreads = 1024, kSmallKpt = kSmallN / kSmallThreads;
+
+struct SortState {
+    int64_t count;                       // ids that name a row
+};
+
+// The id as a key, V where it names no row.
 template <typename I>
 __device__ __forceinline__ uint32_t id_key(const I *ids, int64_t i, uint32_t V) {
     const int64_t id = int64_t(ids[i]);
     return id >= 0 && id < int64_t(V) ? uint32_t(id) : V;
 }
 
-__device__ __forceinline__ uint32_t excl_scan256(uint32_t v, uint32_t *s_warp) {
+// Exclusive scan of one value a thread over the CTA; s_warp: a word a warp.
+__device__ __forceinline__ uint32_t excl_scan(uint32_t v, uint32_t *s_warp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t x = v;
 #pragma unroll
@@ -69,177 +100,337 @@ __device__ __forceinline__ uint32_t excl_scan256(uint32_t v, uint32_t *s_warp) {
     return base + x - v;
 }
 
-struct SortState {
-    uint32_t status;                       // kDevErrTimeout
-    uint32_t done;                         // histogram CTAs done
-    uint32_t ticket[kMaxPasses];
-    uint32_t hist[kMaxPasses][256];
-    uint32_t start[kMaxPasses][256];       // exclusive digit starts
+__device__ __forceinline__ uint32_t lanes_below() {
+    uint32_t m;
+    asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));
+    return m;
+}
+
+// The table's gradient, cleared by the CTAs that a sort kernel has beside its
+// own: the sort waits on latency, not on bandwidth, and the clearing, the
+// larger part of the work for a large vocabulary, goes on meanwhile.  Each
+// launch of the sort clears its share.
+template <typename G>
+struct Clearing {
+    G *p;
+    int64_t rows, stride;
+    int32_t D;
+    int share, shares;                   // this launch's
+};
+template <typename G>
+__device__ __forceinline__ void clear_share(const Clearing<G> &c, int cta, int ctas) {
+    const int64_t part = int64_t(c.share) * ctas + cta, parts = int64_t(c.shares) * ctas;
+    if (c.stride == c.D) {               // one run of values, 16 bytes at a time
+        const int64_t total = c.rows * c.D;
+        int64_t head = int64_t((16 - (reinterpret_cast<uintptr_t>(c.p) & 15)) & 15) / int64_t(sizeof(G));
+        if (head > total) head = total;
+        constexpr int kVec = 16 / sizeof(G);
+        const int64_t body = (total - head) / kVec, each = (body + parts - 1) / parts;
+        const int64_t lo = part * each, hi = lo + each < body ? lo + each : body;
+        uint4 *q = reinterpret_cast<uint4 *>(c.p + head);
+#pragma unroll 4
+        for (int64_t v = lo + threadIdx.x; v < hi; v += blockDim.x) q[v] = make_uint4(0, 0, 0, 0);
+        if (part == 0) {
+            for (int64_t e = threadIdx.x; e < head; e += blockDim.x) c.p[e] = from_float<G>(0.0f);
+            for (int64_t e = head + body * kVec + threadIdx.x; e < total; e += blockDim.x) c.p[e] = from_float<G>(0.0f);
+        }
+        return;
+    }
+    const int64_t each = (c.rows + parts - 1) / parts;
+    const int64_t lo = part * each, hi = lo + each < c.rows ? lo + each : c.rows;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    for (int64_t r = lo + warp; r < hi; r += warps)
+        for (int j = threadIdx.x & 31; j < c.D; j += 32) c.p[r * c.stride + j] = from_float<G>(0.0f);
+}
+
+// Up to kSmallN ids: one CTA sorts them in its shared memory, 8 bits a pass,
+// the others clear.
+template <typename I, typename G>
+__global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__restrict__ ids, int n, uint32_t V,
+                                                                    int passes, uint64_t *words, SortState *st,
+                                                                    Clearing<G> clear) {
+    constexpr int kWarps = kSmallThreads / 32;
+    extern __shared__ uint32_t s_small[];
+    uint32_t *s_key = s_small;                                            // [kSmallN]
+    uint16_t *s_pos = reinterpret_cast<uint16_t *>(s_key + kSmallN);      // [kSmallN]
+    uint16_t (*s_hist)[256] = reinterpret_cast<uint16_t (*)[256]>(s_pos + kSmallN);   // [kWarps][256]
+    __shared__ uint32_t s_warp[kWarps], s_start[256], s_count;
+    start_dependents();
+    if (blockIdx.x > 0) {
+        clear_share(clear, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s_count = 0;
+    const uint32_t lt = lanes_below();
+    uint32_t key[kSmallKpt], pos[kSmallKpt];
+    uint32_t named = 0;
+#pragma unroll
+    for (int j = 0; j < kSmallKpt; ++j) {
+        const int i = warp * (kSmallKpt * 32) + j * 32 + lane;
+        key[j] = i < n ? id_key(ids, i, V) : 0u;
+        pos[j] = uint32_t(i);
+        named += i < n && key[j] < V;
+    }
+    __syncthreads();
+    named = __reduce_add_sync(0xffffffffu, named);
+    if (lane == 0 && named) atomicAdd(&s_count, named);
+    for (int d = 0; d < passes; ++d) {
+        for (int e = tid; e < kWarps * 128; e += kSmallThreads) reinterpret_cast<uint32_t *>(&s_hist[0][0])[e] = 0u;
+        __syncthreads();
+        uint32_t rank[kSmallKpt];
+#pragma unroll
+        for (int j = 0; j < kSmallKpt; ++j) {
+            const bool ok = warp * (kSmallKpt * 32) + j * 32 + lane < n;
+            const uint32_t dig = ok ? (key[j] >> (8 * d)) & 255u : 256u + lane;
+            const uint32_t peers = __match_any_sync(0xffffffffu, dig);
+            const uint32_t before = __popc(peers & lt);
+            const uint32_t cur = ok ? s_hist[warp][dig] : 0u;
+            rank[j] = cur + before;
+            __syncwarp();
+            if (ok && before == 0) s_hist[warp][dig] = uint16_t(cur + __popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        uint32_t total = 0;
+        if (tid < 256)
+#pragma unroll 8
+            for (int w = 0; w < kWarps; ++w) {
+                const uint32_t c = s_hist[w][tid];
+                s_hist[w][tid] = uint16_t(total);
+                total += c;
+            }
+        const uint32_t start = excl_scan(total, s_warp);
+        if (tid < 256) s_start[tid] = start;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSmallKpt; ++j)
+            if (warp * (kSmallKpt * 32) + j * 32 + lane < n) {
+                const uint32_t dig = (key[j] >> (8 * d)) & 255u;
+                const uint32_t to = s_start[dig] + s_hist[warp][dig] + rank[j];
+                s_key[to] = key[j];
+                s_pos[to] = uint16_t(pos[j]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSmallKpt; ++j) {
+            const int i = warp * (kSmallKpt * 32) + j * 32 + lane;
+            if (i < n) key[j] = s_key[i], pos[j] = s_pos[i];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kSmallKpt; ++j) {
+        const int i = warp * (kSmallKpt * 32) + j * 32 + lane;
+        if (i < n) words[i] = uint64_t(key[j]) << 32 | pos[j];
+    }
+    if (tid == 0) st->count = int64_t(s_count);
+}
+
+// More ids: stable passes over digits of the key, least significant first,
+// each a count of every partition's digits, a scan of the counts over the
+// partitions, and a move.  Partitions do not wait on one another (a look-back
+// from partition to partition is a chain of L2 round trips: with a few
+// hundred partitions that start together it took twice the three launches'
+// time).  Ids that name no row are not moved by the first pass.
+struct PassParams {
+    const uint64_t *in;
+    uint64_t *out;
+    int64_t n;               // ids
+    uint32_t V;
+    int shift, bits;         // the digit
+    int parts;
+    bool first;
+    uint32_t *counts;        // [bins][parts]: of the digit in each partition, then their exclusive sums
+    uint32_t *totals;        // [bins]
+    SortState *st;
 };
 
-template <typename I, typename G>
-__global__ void __launch_bounds__(kThreads) k_embed_hist(const I *__restrict__ ids, int64_t n, uint32_t V, int passes,
-                                                         SortState *st, G *dtable, int64_t ds, int32_t D) {
-    __shared__ uint32_t s_h[kMaxPasses][256];
-    __shared__ uint32_t s_warp[8], s_last;
-    for (int k = threadIdx.x; k < kMaxPasses * 256; k += kThreads) (&s_h[0][0])[k] = 0;
-    __syncthreads();
-    const int64_t stride = int64_t(gridDim.x) * kThreads;
-    const int64_t first = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    for (int64_t i = first; i < n; i += stride) {
-        const uint32_t key = id_key(ids, i, V);
-        for (int d = 0; d < passes; ++d) atomicAdd(&s_h[d][(key >> (8 * d)) & 255u], 1u);
-    }
-    __syncthreads();
-    for (int k = threadIdx.x; k < passes * 256; k += kThreads) {
-        const uint32_t v = (&s_h[0][0])[k];
-        if (v) atomicAdd(&st->hist[0][0] + k, v);
-    }
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(&st->done, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (s_last) {
-        __threadfence();
-        for (int d = 0; d < passes; ++d)
-            st->start[d][threadIdx.x] = excl_scan256(__ldcg(&st->hist[d][threadIdx.x]), s_warp);
-    }
-    const int64_t total = int64_t(V) * D;
-    for (int64_t e = first; e < total; e += stride) {
-        const int64_t v = e / D;
-        dtable[v * ds + (e - v * D)] = from_float<G>(0.0f);
-    }
-}
+// Words of a pass: the ids themselves in the first, else what the first moved.
+__device__ __forceinline__ int64_t pass_size(const PassParams &p) { return p.first ? p.n : p.st->count; }
 
-__device__ __forceinline__ uint32_t ld_relaxed(const uint32_t *p) {
-    uint32_t v;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_relaxed(uint32_t *p, uint32_t v) {
-    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// One stable pass over digit d.  Partitions are taken by ticket, so every
-// partition that one waits on has been started; a wait that runs out sets
-// the status and goes on with the counts that it has (every write stays
-// inside the n words).
 template <typename I>
-__global__ void __launch_bounds__(kThreads) k_embed_pass(const I *__restrict__ ids, const uint64_t *__restrict__ win,
-                                                         uint64_t *__restrict__ wout, int64_t n, uint32_t V, int d,
-                                                         SortState *st, uint32_t *lookback) {
-    __shared__ uint32_t s_whist[8][256];
-    __shared__ uint32_t s_lstart[256], s_gbase[256], s_warp[8], s_part;
-    __shared__ uint64_t s_words[kPart];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) s_part = atomicAdd(&st->ticket[d], 1u);
-    for (int k = tid; k < 8 * 256; k += kThreads) (&s_whist[0][0])[k] = 0;
+__device__ __forceinline__ uint64_t word_at(const PassParams &p, const I *ids, int64_t i) {
+    return p.first ? uint64_t(id_key(ids, i, p.V)) << 32 | uint32_t(i) : p.in[i];
+}
+
+template <typename I, typename G>
+__global__ void __launch_bounds__(kThreads) k_embed_count(const I *__restrict__ ids, PassParams p, Clearing<G> clear) {
+    __shared__ uint32_t s_hist[1 << kMaxBits];
+    start_dependents();
+    if (int(blockIdx.x) >= p.parts) {
+        wait_for_previous();
+        clear_share(clear, blockIdx.x - p.parts, gridDim.x - p.parts);
+        return;
+    }
+    const int bins = 1 << p.bits;
+    for (int k = threadIdx.x; k < bins; k += kThreads) s_hist[k] = 0u;
+    wait_for_previous();
     __syncthreads();
-    const int64_t part = s_part, base = part * kPart, wbase = base + warp * (kKpt * 32);
-    const int shift = 32 + 8 * d;
+    const int64_t n = pass_size(p), base = int64_t(blockIdx.x) * kPart;
+    uint32_t key[kKpt];
+#pragma unroll
+    for (int j = 0; j < kKpt; ++j) {
+        const int64_t i = base + j * kThreads + threadIdx.x;
+        key[j] = i < n ? uint32_t(word_at(p, ids, i) >> 32) : p.V;
+    }
+    const uint32_t lt = lanes_below();
+#pragma unroll
+    for (int j = 0; j < kKpt; ++j) {
+        const bool ok = key[j] < p.V;      // equal digits of a warp add once
+        const uint32_t dig = ok ? (key[j] >> p.shift) & uint32_t(bins - 1) : 0xffffffffu;
+        const uint32_t peers = __match_any_sync(0xffffffffu, dig);
+        if (ok && (peers & lt) == 0) atomicAdd(&s_hist[dig], uint32_t(__popc(peers)));
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < bins; k += kThreads) p.counts[int64_t(k) * p.parts + blockIdx.x] = s_hist[k];
+}
+
+// A warp for each bin: exclusive sums of its counts over the partitions.
+template <typename G>
+__global__ void __launch_bounds__(kThreads) k_embed_scan(PassParams p, int scanning, Clearing<G> clear) {
+    start_dependents();
+    wait_for_previous();
+    if (int(blockIdx.x) >= scanning) {
+        clear_share(clear, blockIdx.x - scanning, gridDim.x - scanning);
+        return;
+    }
+    const int lane = threadIdx.x & 31, bin = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (bin >= 1 << p.bits) return;
+    uint32_t *c = p.counts + int64_t(bin) * p.parts;
+    uint32_t run = 0;
+    for (int q0 = 0; q0 < p.parts; q0 += 128) {
+        uint32_t v[4], mine = 0;           // four neighbours a lane
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int q = q0 + lane * 4 + u;
+            v[u] = q < p.parts ? c[q] : 0u;
+            mine += v[u];
+        }
+        uint32_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        uint32_t at = run + x - mine;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int q = q0 + lane * 4 + u;
+            if (q < p.parts) c[q] = at;
+            at += v[u];
+        }
+        run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) p.totals[bin] = run;
+}
+
+template <typename I, typename G>
+__global__ void __launch_bounds__(kThreads) k_embed_move(const I *__restrict__ ids, PassParams p, Clearing<G> clear) {
+    extern __shared__ uint64_t s_words[];                                        // [kPart]
+    uint16_t *s_hist = reinterpret_cast<uint16_t *>(s_words + kPart);            // [8 warps][bins]
+    const int bins = 1 << p.bits;
+    uint32_t *s_lstart = reinterpret_cast<uint32_t *>(s_hist + 8 * bins);        // [bins] starts in this partition
+    uint32_t *s_gbase = s_lstart + bins;                                         // [bins] destinations less starts
+    __shared__ uint32_t s_warp[8];
+    start_dependents();
+    if (int(blockIdx.x) >= p.parts) {
+        wait_for_previous();
+        clear_share(clear, blockIdx.x - p.parts, gridDim.x - p.parts);
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int k = tid; k < 4 * bins; k += kThreads) reinterpret_cast<uint32_t *>(s_hist)[k] = 0u;
+    wait_for_previous();
+    __syncthreads();
+    const int64_t n = pass_size(p), base = int64_t(blockIdx.x) * kPart, wbase = base + warp * (kKpt * 32);
+    const int shift = 32 + p.shift;
+    const uint32_t mask = uint32_t(bins - 1);
     uint64_t word[kKpt];
-    uint32_t rank[kKpt];
 #pragma unroll
     for (int j = 0; j < kKpt; ++j) {
         const int64_t i = wbase + j * 32 + lane;
-        word[j] = ~0ull;
-        if (i < n) word[j] = d == 0 ? uint64_t(id_key(ids, i, V)) << 32 | uint32_t(i) : win[i];
+        word[j] = i < n ? word_at(p, ids, i) : ~0ull;
     }
-    uint32_t lt;
-    asm("mov.u32 %0, %%lanemask_lt;" : "=r"(lt));
+    const uint32_t lt = lanes_below();
+    uint16_t *mine = s_hist + warp * bins;
+    uint32_t rank[kKpt];
 #pragma unroll
     for (int j = 0; j < kKpt; ++j) {
-        const bool ok = wbase + j * 32 + lane < n;
-        const uint32_t dig = ok ? uint32_t(word[j] >> shift) & 255u : 256u + lane;
+        const bool ok = uint32_t(word[j] >> 32) < p.V;
+        const uint32_t dig = ok ? uint32_t(word[j] >> shift) & mask : 0xffffffffu - lane;
         const uint32_t peers = __match_any_sync(0xffffffffu, dig);
         const uint32_t before = __popc(peers & lt);
-        const uint32_t cur = ok ? s_whist[warp][dig] : 0u;
+        const uint32_t cur = ok ? mine[dig] : 0u;
         rank[j] = cur + before;
         __syncwarp();
-        if (ok && before == 0) s_whist[warp][dig] = cur + __popc(peers);
+        if (ok && before == 0) mine[dig] = uint16_t(cur + __popc(peers));
         __syncwarp();
     }
     __syncthreads();
-    uint32_t total = 0;
+    // bins: the warps' starts in each, the partition's start, the destination
+    uint32_t local = 0, global = 0;        // running sums over the bins done so far
+    for (int k0 = 0; k0 < bins; k0 += kThreads) {
+        const int k = k0 + tid;
+        uint32_t total = 0, all = 0, earlier = 0;
+        if (k < bins) {
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        const uint32_t c = s_whist[w][tid];
-        s_whist[w][tid] = total;
-        total += c;
-    }
-    uint32_t *my = lookback + part * 256 + tid;
-    st_relaxed(my, (part == 0 ? kFlagInc : kFlagAgg) | total);
-    s_lstart[tid] = excl_scan256(total, s_warp);
-    uint32_t excl = 0;
-    if (part > 0) {
-        uint32_t spins = 0;
-        for (int64_t q = part - 1;;) {
-            const uint32_t w = ld_relaxed(lookback + q * 256 + tid);
-            if (w < kFlagAgg) {
-                if (++spins > kSpinLimit) {
-                    atomicOr(&st->status, kDevErrTimeout);
-                    break;
-                }
-                continue;
+            for (int w = 0; w < 8; ++w) {
+                const uint32_t c = s_hist[w * bins + k];
+                s_hist[w * bins + k] = uint16_t(total);
+                total += c;
             }
-            excl += w & kValMask;
-            if (w >= kFlagInc || q == 0) break;
-            --q;
-            spins = 0;
+            all = p.totals[k];
+            earlier = p.counts[int64_t(k) * p.parts + blockIdx.x];
         }
-        st_relaxed(my, kFlagInc | (excl + total));
+        const uint32_t ls = local + excl_scan(total, s_warp), gs = global + excl_scan(all, s_warp);
+        if (k < bins) s_lstart[k] = ls, s_gbase[k] = gs + earlier - ls;
+        // the last thread has the sums of all of them
+        __syncthreads();
+        if (tid == kThreads - 1) s_warp[0] = ls + total, s_warp[1] = gs + all;
+        __syncthreads();
+        local = s_warp[0], global = s_warp[1];
     }
-    s_gbase[tid] = st->start[d][tid] + excl;
+    if (p.first && blockIdx.x == 0 && tid == 0) p.st->count = int64_t(global);
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kKpt; ++j) {
-        if (wbase + j * 32 + lane < n) {
-            const uint32_t dig = uint32_t(word[j] >> shift) & 255u;
-            s_words[s_lstart[dig] + s_whist[warp][dig] + rank[j]] = word[j];
+    for (int j = 0; j < kKpt; ++j)
+        if (uint32_t(word[j] >> 32) < p.V) {
+            const uint32_t dig = uint32_t(word[j] >> shift) & mask;
+            s_words[s_lstart[dig] + mine[dig] + rank[j]] = word[j];
         }
-    }
     __syncthreads();
-    const int cnt = int(n - base < kPart ? n - base : kPart);
-    for (int i = tid; i < cnt; i += kThreads) {
+    for (int i = tid; i < int(local); i += kThreads) {
         const uint64_t w = s_words[i];
-        const uint32_t dig = uint32_t(w >> shift) & 255u;
-        const uint32_t g = s_gbase[dig] + uint32_t(i) - s_lstart[dig];
-        if (int64_t(g) < n) wout[g] = w;
+        p.out[s_gbase[uint32_t(w >> shift) & mask] + uint32_t(i)] = w;
     }
 }
 
 // ------------------------------------------------------------------ sums
 
+// Chunks of the sorted words, one a CTA: `groups` walks side by side, each by
+// `cols` threads that own a vector of columns.  An id that lies inside one
+// walk is finished there.  One that goes on over walks leaves a sum in shared
+// memory at the end of each, which the thread of the walk where it begins
+// adds in order; one that goes on over chunks leaves them in `head` and
+// `tail`, for k_embed_join.
+enum : uint32_t { kIn = 1u, kOn = 2u, kWhole = 4u };   // of a walk or chunk: its first id
+                                                        // began before it, its last goes on
+                                                        // after it, one id fills it and does both
 struct SumParams {
     const uint64_t *words;   // sorted id << 32 | position
-    int64_t n, chunk;        // words of a CTA = groups * walk
+    const SortState *st;
+    int64_t n, chunk;        // ids; words of a CTA = groups * walk
     uint32_t V;
     int32_t D;
-    int walk;                // words of one thread group
-    int groups, cols;        // blockDim = groups * cols, a thread owns one vector of columns
-    int vecs;                // vectors of a row
+    int walk, groups, cols, vecs;
     int64_t in_stride, out_stride;
     float scale;
-    float *head, *tail;      // [chunks][D] partial sums of ids that cross a chunk's ends
+    float *head, *tail;      // [chunks][D]
+    uint32_t *flags;         // [chunks]
 };
 
-__device__ __forceinline__ uint32_t key_at(const SumParams &p, int64_t i) {
-    return uint32_t(__ldg(p.words + i) >> 32);
-}
-
-// Chunk [lo, hi) as seen from its ends: `in` its first id began before it,
-// `on` its last id goes on after it, `whole` one id fills it and does both.
-struct Ends {
-    bool in, on, whole;
-};
-__device__ __forceinline__ Ends ends_of(const SumParams &p, int64_t lo, int64_t hi) {
-    Ends e;
-    const uint32_t a = key_at(p, lo), b = key_at(p, hi - 1);
-    e.in = lo > 0 && key_at(p, lo - 1) == a;
-    e.on = hi < p.n && key_at(p, hi) == b;
-    e.whole = e.in && e.on && a == b;
-    return e;
-}
+__device__ __forceinline__ uint32_t key_at(const SumParams &p, int64_t i) { return uint32_t(p.words[i] >> 32); }
 
 template <typename G, int N>
 __device__ __forceinline__ void finish_row(const SumParams &p, G *dtable, uint32_t key, int col, const float (&acc)[N]) {
@@ -252,49 +443,57 @@ __device__ __forceinline__ void finish_row(const SumParams &p, G *dtable, uint32
 
 template <typename T, typename G, int N>
 __global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__restrict__ dout, G *dtable) {
-    extern __shared__ float s_part[];      // head then tail: [groups][cols][N]
-    constexpr int kBatch = 8;
+    extern __shared__ float s_part[];      // head then tail: [groups][cols][N], then flags [groups]
+    constexpr int kBatch = N >= 4 ? 8 : 16;
     const int g = threadIdx.x / p.cols, c = threadIdx.x - g * p.cols;
     const int col = blockIdx.y * p.cols + c;
-    const bool live = col < p.vecs;
-    const int64_t cbase = int64_t(blockIdx.x) * p.chunk;
-    const int64_t lo = cbase + int64_t(g) * p.walk;
-    const int64_t hi = lo + p.walk < p.n ? lo + p.walk : p.n;
     float *head = s_part + size_t(threadIdx.x) * N;
-    float *tail = head + size_t(p.groups) * p.cols * N;
-    Ends e{false, false, false};
+    float *tail = head + size_t(blockDim.x) * N;
+    uint32_t *s_flags = reinterpret_cast<uint32_t *>(s_part + size_t(blockDim.x) * N * 2);
+    start_dependents();
+    wait_for_previous();
+    const int64_t n = p.st->count < p.n ? p.st->count : p.n;
+    const int64_t lo = int64_t(blockIdx.x) * p.chunk + int64_t(g) * p.walk;
+    const int64_t hi = lo + p.walk < n ? lo + p.walk : n;
+    uint32_t flags = 0, cur = 0;
     float acc[N];
-    if (live && lo < hi) {
-        e = ends_of(p, lo, hi);
-        uint32_t cur = key_at(p, lo);
-        bool open = e.in;                 // the current id began before this walk
 #pragma unroll
-        for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+    for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+    if (lo < hi) {
+        const bool live = col < p.vecs;
+        const T *base = dout + int64_t(live ? col : 0) * N;
+        uint64_t w[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) w[u] = lo + u < hi ? p.words[lo + u] : ~0ull;
+        cur = uint32_t(w[0] >> 32);
+        bool open = lo > 0 && key_at(p, lo - 1) == cur;   // the current id began before this walk
+        const uint32_t after = hi < n ? key_at(p, hi) : p.V;
+        flags = open ? kIn : 0u;
         for (int64_t i = lo; i < hi; i += kBatch) {
-            uint64_t w[kBatch];
             Vec<T, N> x[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) w[u] = i + u < hi ? __ldg(p.words + i + u) : ~0ull;
+            uint32_t key[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                x[u].clear();
                 const uint32_t pos = uint32_t(w[u]);
-                if (uint32_t(w[u] >> 32) < p.V && int64_t(pos) < p.n)
-                    x[u] = load_vec<T, N>(dout + int64_t(pos) * p.in_stride + int64_t(col) * N);
+                key[u] = uint32_t(w[u] >> 32);
+                x[u].clear();
+                if (key[u] < p.V && int64_t(pos) < p.n) x[u] = load_vec<T, N>(base + int64_t(pos) * p.in_stride);
             }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)              // the next words, while the rows arrive
+                w[u] = i + kBatch + u < hi ? p.words[i + kBatch + u] : ~0ull;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 if (i + u >= hi) break;
-                const uint32_t key = uint32_t(w[u] >> 32);
-                if (key != cur) {
+                if (key[u] != cur) {
                     if (open) {
 #pragma unroll
                         for (int k = 0; k < N; ++k) head[k] = acc[k];
-                    } else {
+                    } else if (live) {
                         finish_row<G, N>(p, dtable, cur, col, acc);
                     }
                     open = false;
-                    cur = key;
+                    cur = key[u];
 #pragma unroll
                     for (int k = 0; k < N; ++k) acc[k] = 0.0f;
                 }
@@ -302,83 +501,108 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__
                 for (int k = 0; k < N; ++k) acc[k] += x[u].get(k);
             }
         }
+        const bool on = hi < n && after == cur;
+        flags |= (on ? kOn : 0u) | (open && on ? kWhole : 0u);
         if (open) {
 #pragma unroll
             for (int k = 0; k < N; ++k) head[k] = acc[k];
-        } else if (!e.on) {
-            finish_row<G, N>(p, dtable, cur, col, acc);
+        } else if (!on) {
+            if (live) finish_row<G, N>(p, dtable, cur, col, acc);
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k) tail[k] = acc[k];
         }
     }
+    if (c == 0) s_flags[g] = flags;
     __syncthreads();
-    if (!live || lo >= hi) return;
-    // Joins the groups of this chunk.  The thread of the group where an id
-    // begins (or of group 0 for the id that the chunk before began) adds the
-    // groups that follow, in order.
-    const int64_t chi = cbase + p.chunk < p.n ? cbase + p.chunk : p.n;
+    if (lo >= hi) return;
     for (int pass = 0; pass < 2; ++pass) {
-        const bool incoming = pass == 0;
-        if (incoming ? !(g == 0 && e.in) : !(e.on && !e.whole)) continue;
+        const bool incoming = pass == 0;   // the id that the chunk before began: walk 0's threads
+        if (incoming ? !(g == 0 && (flags & kIn)) : (flags & (kOn | kWhole)) != kOn) continue;
         float *own = incoming ? head : tail;
 #pragma unroll
         for (int k = 0; k < N; ++k) acc[k] = own[k];
-        bool on = incoming ? e.whole : true;
-        const uint32_t key = incoming ? key_at(p, lo) : key_at(p, hi - 1);
-        int64_t q = hi;                    // first word of the next group
-        int h = 1;
-        while (on && q < chi) {
-            const int64_t qe = q + p.walk < chi ? q + p.walk : chi;
+        bool on = incoming ? (flags & kWhole) != 0 : true;
+        for (int h = 1; on && g + h < p.groups; ++h) {
 #pragma unroll
             for (int k = 0; k < N; ++k) acc[k] += head[size_t(h) * p.cols * N + k];
-            on = key_at(p, qe - 1) == key && qe < p.n && key_at(p, qe) == key;
-            q = qe;
-            ++h;
+            on = (s_flags[g + h] & kWhole) != 0;
         }
-        if (incoming || on) {
-            float *dst = (incoming ? p.head : p.tail) + size_t(blockIdx.x) * p.D + size_t(col) * N;
-#pragma unroll
-            for (int k = 0; k < N; ++k) dst[k] = acc[k];
-        } else {
-            finish_row<G, N>(p, dtable, key, col, acc);
-        }
+        if (col >= p.vecs) continue;
+        if (incoming || on)
+            store_floats<float, N>((incoming ? p.head : p.tail) + size_t(blockIdx.x) * p.D + size_t(col) * N, acc);
+        else
+            finish_row<G, N>(p, dtable, cur, col, acc);
+    }
+    if (c == 0 && blockIdx.y == 0 && (hi == n || g == p.groups - 1)) {
+        // the chunk's last walk: one id fills the chunk if every walk is whole
+        bool whole = true;
+        for (int h = 0; h <= g; ++h) whole = whole && (s_flags[h] & kWhole);
+        p.flags[blockIdx.x] = (s_flags[0] & kIn) | (flags & kOn) | (whole ? kWhole : 0u);
     }
 }
 
-// One CTA per chunk (and slice of columns): if an id begins in the chunk and
-// goes on after it, adds its partial sums, groups of threads taking every
+// One CTA for each chunk (and slice of columns): if an id begins in the chunk
+// and goes on after it, adds its sums, walks of threads taking every
 // groups-th chunk and then joining in order.
-template <typename G>
-__global__ void __launch_bounds__(kThreads) k_embed_join(SumParams p, G *dtable) {
-    __shared__ float s_acc[kThreads];
-    const int64_t lo = int64_t(blockIdx.x) * p.chunk, hi = lo + p.chunk;
-    if (hi >= p.n) return;                 // the last chunk: nothing follows
-    const Ends e = ends_of(p, lo, hi);
+template <typename G, int N>
+__global__ void __launch_bounds__(kThreads) k_embed_join(SumParams p, int chunks, G *dtable) {
+    __shared__ float s_acc[kThreads * N];
+    start_dependents();
+    wait_for_previous();
+    const int64_t n = p.st->count < p.n ? p.st->count : p.n;
+    const int64_t hi = (int64_t(blockIdx.x) + 1) * p.chunk;
+    if (hi >= n) return;                   // nothing follows
+    if ((p.flags[blockIdx.x] & (kOn | kWhole)) != kOn) return;
     const uint32_t key = key_at(p, hi - 1);
-    if (!e.on || e.whole || key >= p.V) return;
-    // the id's last chunk: the chunk of its last word
-    int64_t a = hi, b = p.n;               // words[a] has the id, words[b] (if any) has not
-    while (b - a > 1) {
-        const int64_t m = a + (b - a) / 2;
-        if (key_at(p, m) == key) a = m; else b = m;
+    int last = blockIdx.x + 1;             // the first of the chunks after this one that the id does not fill
+    for (;;) {
+        const int q = last + int(threadIdx.x);
+        const bool ends = q >= chunks || !(p.flags[q] & kWhole);
+        const int first = __syncthreads_or(ends) ? 1 : 0;
+        if (first) {
+            // the lowest thread that says so
+            __shared__ int s_first;
+            if (threadIdx.x == 0) s_first = kThreads;
+            __syncthreads();
+            if (ends) atomicMin(&s_first, int(threadIdx.x));
+            __syncthreads();
+            last += s_first;
+            if (last >= chunks) last = chunks - 1;
+            break;
+        }
+        last += int(blockDim.x);
     }
-    const int64_t last = a / p.chunk;
-    const int cols = p.D < kThreads ? p.D : kThreads, groups = kThreads / cols;
+    const int vecs = p.D / N;
+    const int cols = vecs < kThreads ? vecs : kThreads, groups = kThreads / cols;
     const int g = threadIdx.x / cols, c = threadIdx.x - g * cols;
-    for (int col0 = blockIdx.y * cols; col0 < p.D; col0 += gridDim.y * cols) {
+    for (int col0 = blockIdx.y * cols; col0 < vecs; col0 += gridDim.y * cols) {
         const int col = col0 + c;
-        float acc = 0.0f;
-        if (g < groups && col < p.D) {
-            if (g == 0) acc = p.tail[size_t(blockIdx.x) * p.D + col];
-            for (int64_t q = blockIdx.x + 1 + g; q <= last; q += groups) acc += p.head[size_t(q) * p.D + col];
+        float acc[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+        if (g < groups && col < vecs) {
+            if (g == 0)
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc[k] = p.tail[size_t(blockIdx.x) * p.D + col * N + k];
+#pragma unroll 4
+            for (int q = blockIdx.x + 1 + g; q <= last; q += groups) {
+                const Vec<float, N> x = load_vec<float, N>(p.head + size_t(q) * p.D + col * N);
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc[k] += x.get(k);
+            }
         }
         __syncthreads();
-        s_acc[threadIdx.x] = acc;
+#pragma unroll
+        for (int k = 0; k < N; ++k) s_acc[threadIdx.x * N + k] = acc[k];
         __syncthreads();
-        if (g == 0 && col < p.D) {
-            for (int h = 1; h < groups; ++h) acc += s_acc[h * cols + c];
-            dtable[int64_t(key) * p.out_stride + col] = from_float<G>(acc * p.scale);
+        if (g == 0 && col < vecs) {
+            for (int h = 1; h < groups; ++h)
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc[k] += s_acc[(h * cols + c) * N + k];
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                dtable[int64_t(key) * p.out_stride + col * N + k] = from_float<G>(acc[k] * p.scale);
         }
     }
 }
@@ -389,10 +613,17 @@ bool sizes_ok(int64_t n, int64_t V, int32_t D) {
     return n >= 0 && n < (int64_t(1) << 30) && V >= 1 && V < (int64_t(1) << 31) && D >= 1 && D <= kMaxD;
 }
 
-int sort_passes(int64_t V) {               // keys 0..V
-    int b = 1;
-    while (b < 32 && (int64_t(1) << b) <= V) ++b;
-    return (b + 7) / 8;
+int bits_of(int64_t v) {                   // of the numbers below v
+    int b = 0;
+    while (b < 32 && (int64_t(1) << b) < v) ++b;
+    return b;
+}
+
+// Passes over `bits` bits of the key, and the bits of each.
+int passes_of(int bits) { return bits < 1 ? 1 : (bits + kMaxBits - 1) / kMaxBits; }
+int digit_of(int bits) {
+    const int p = passes_of(bits), b = (bits + p - 1) / p;
+    return b < 1 ? 1 : b;
 }
 
 struct SumShape {
@@ -400,9 +631,8 @@ struct SumShape {
     int64_t chunk, chunks;
 };
 
-// Columns over threads: a row's vectors side by side, as many rows as fit in
-// a CTA.  The walk (words added by one thread in turn) is as long as leaves
-// about eight CTAs an SM.
+// Columns over threads: a row's vectors side by side, as many walks as fit in
+// a CTA.  A walk is as long as leaves about eight CTAs an SM.
 SumShape sum_shape(int64_t n, int32_t D, int vec) {
     SumShape s;
     s.vecs = D / vec;
@@ -419,25 +649,25 @@ SumShape sum_shape(int64_t n, int32_t D, int vec) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct BwdLayout {
-    size_t lookback, zero_end, words, head, tail, total;
-    int64_t parts;
-    int passes;
+    size_t totals, counts, words, flags, head, tail, total;
+    int parts;
 };
 
 BwdLayout bwd_layout(int64_t n, int64_t V, int32_t D) {
     BwdLayout L;
-    L.parts = (n + kPart - 1) / kPart;
-    L.passes = sort_passes(V);
-    L.lookback = align256(sizeof(SortState));
-    L.zero_end = align256(L.lookback + size_t(L.passes) * L.parts * 256 * 4);
-    L.words = L.zero_end;
-    L.head = align256(L.words + size_t(n) * 16);
+    const size_t bins = size_t(1) << digit_of(bits_of(V));
+    L.parts = int((n + kPart - 1) / kPart);
+    L.totals = align256(sizeof(SortState));
+    L.counts = align256(L.totals + bins * 4);
+    L.words = align256(L.counts + (n > kSmallN ? bins * L.parts * 4 : 0));
+    L.flags = align256(L.words + size_t(n) * 16);
     int64_t chunks = 0;                    // of whichever vector width the pointers allow
-    for (int vec : {1, 4, 8})
+    for (int vec = 1; vec <= 8; vec *= 2)
         if (D % vec == 0) {
             const SumShape s = sum_shape(n, D, vec);
             if (s.chunks > chunks) chunks = s.chunks;
         }
+    L.head = align256(L.flags + size_t(chunks) * 4);
     L.tail = align256(L.head + size_t(chunks) * D * 4);
     L.total = align256(L.tail + size_t(chunks) * D * 4);
     return L;
@@ -463,15 +693,45 @@ ss_status check_common(const char *who, int64_t n, int64_t V, int32_t D, int dty
     return SS_OK;
 }
 
+// The most elements that one access may take: every row of both tensors
+// starts and ends on such a boundary.
+int access_bytes(const void *a, int64_t a_row, const void *b, int64_t b_row, int64_t row) {
+    const uint64_t all = reinterpret_cast<uintptr_t>(a) | uint64_t(a_row) | reinterpret_cast<uintptr_t>(b) |
+                         uint64_t(b_row) | uint64_t(row);
+    return all % 16 == 0 ? 16 : (all % 8 == 0 ? 8 : (all % 4 == 0 ? 4 : 2));
+}
+
+template <typename T, typename I, int N>
+void launch_fwd_n(const void *table, int64_t ts, int64_t V, int32_t D, const void *ids, int64_t n, float scale,
+                  void *out, int64_t os, cudaStream_t s) {
+    const int vecs = D / N;
+    int shift = 0;                         // up to four vectors a lane, at least 4 lanes, at most a warp
+    while ((1 << shift) < 32 && (1 << shift) * 4 < vecs) ++shift;
+    while (shift < 2 && (1 << shift) < vecs) ++shift;
+    const int nv = (vecs + (1 << shift) - 1) >> shift;
+    auto go = [&](auto NV, auto ROWS) {
+        constexpr int kNv = decltype(NV)::value, kRows = decltype(ROWS)::value;
+        const int64_t per = int64_t(kThreads >> shift) * kRows;
+        SS_LAUNCH("k_embed_fwd", s,
+                  k_embed_fwd<T, I, N, kNv, kRows><<<unsigned((n + per - 1) / per), kThreads, 0, s>>>(
+                      static_cast<const T *>(table), ts, V, static_cast<const I *>(ids), n, scale,
+                      static_cast<T *>(out), os, shift, vecs));
+    };
+    if (nv == 1) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+    else if (nv == 2) go(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+    else if (nv == 3) go(std::integral_constant<int, 3>{}, std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+}
+
 template <typename T, typename I>
 void launch_fwd(const void *table, int64_t ts, int64_t V, int32_t D, const void *ids, int64_t n, float scale,
-                void *out, int64_t os, int sms, cudaStream_t s) {
-    const int64_t want = (n * D + kThreads - 1) / kThreads;
-    const int grid = int(want < int64_t(sms) * 32 ? want : int64_t(sms) * 32);
-    SS_LAUNCH("k_embed_fwd", s,
-              k_embed_fwd<T, I><<<grid, kThreads, 0, s>>>(static_cast<const T *>(table), ts, V, D,
-                                                          static_cast<const I *>(ids), n, scale,
-                                                          static_cast<T *>(out), os));
+                void *out, int64_t os, cudaStream_t s) {
+    const int b = access_bytes(table, ts * sizeof(T), out, os * sizeof(T), int64_t(D) * sizeof(T));
+    constexpr int E = sizeof(T);
+    if (b == 16) launch_fwd_n<T, I, 16 / E>(table, ts, V, D, ids, n, scale, out, os, s);
+    else if (b == 8) launch_fwd_n<T, I, 8 / E>(table, ts, V, D, ids, n, scale, out, os, s);
+    else if (b == 4 && E == 2) launch_fwd_n<T, I, E == 2 ? 2 : 1>(table, ts, V, D, ids, n, scale, out, os, s);
+    else launch_fwd_n<T, I, 1>(table, ts, V, D, ids, n, scale, out, os, s);
 }
 
 template <typename T, typename G, int N>
@@ -479,9 +739,15 @@ void launch_sums(const SumParams &p, const SumShape &sh, const T *dout, G *dtabl
     const dim3 grid(unsigned(sh.chunks), unsigned(sh.slices));
     const int threads = sh.groups * sh.cols;
     SS_LAUNCH("k_embed_sum", s,
-              k_embed_sum<T, G, N><<<grid, threads, size_t(threads) * N * 8, s>>>(p, dout, dtable));
-    if (sh.chunks > 1)
-        SS_LAUNCH("k_embed_join", s, k_embed_join<G><<<dim3(unsigned(sh.chunks)), kThreads, 0, s>>>(p, dtable));
+              launch_after(k_embed_sum<T, G, N>, grid, threads, size_t(threads) * N * 8 + sh.groups * 4, s, p, dout,
+                           dtable));
+    if (sh.chunks > 1) {
+        constexpr int kJoin = N < 4 ? N : 4;
+        const int vecs = p.D / kJoin, cols = vecs < kThreads ? vecs : kThreads;
+        SS_LAUNCH("k_embed_join", s,
+                  launch_after(k_embed_join<G, kJoin>, dim3(unsigned(sh.chunks), unsigned((vecs + cols - 1) / cols)),
+                               kThreads, 0, s, p, int(sh.chunks), dtable));
+    }
 }
 
 template <typename T, typename G, typename I>
@@ -489,32 +755,83 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
                      void *dtable, int64_t out_stride, char *ws, int sms, cudaStream_t s) {
     const BwdLayout L = bwd_layout(n, V, D);
     SortState *st = reinterpret_cast<SortState *>(ws);
-    ss_status e = check_cuda(cudaMemsetAsync(ws, 0, L.zero_end, s), "ss_embed_bwd: memset");
-    if (e != SS_OK) return e;
     const I *id = static_cast<const I *>(ids);
     G *dt = static_cast<G *>(dtable);
-    SS_LAUNCH("k_embed_hist", s,
-              k_embed_hist<I, G><<<sms * 4, kThreads, 0, s>>>(id, n, uint32_t(V), L.passes, st, dt, out_stride, D));
-    if (n == 0) return SS_OK;
     uint64_t *w[2] = {reinterpret_cast<uint64_t *>(ws + L.words), reinterpret_cast<uint64_t *>(ws + L.words) + n};
-    for (int d = 0; d < L.passes; ++d)
-        SS_LAUNCH("k_embed_pass", s,
-                  k_embed_pass<I><<<unsigned(L.parts), kThreads, 0, s>>>(
-                      id, w[(d + 1) & 1], w[d & 1], n, uint32_t(V), d, st,
-                      reinterpret_cast<uint32_t *>(ws + L.lookback) + size_t(d) * L.parts * 256));
-    constexpr int kVec = 16 / sizeof(T);
-    const bool vec = D % kVec == 0 && aligned_to(dout, 16) && in_stride % kVec == 0 &&
-                     aligned_to(dtable, 16) && (out_stride * sizeof(G)) % 16 == 0;
-    const SumShape sh = sum_shape(n, D, vec ? kVec : 1);
-    SumParams p{};
-    p.words = w[(L.passes - 1) & 1];
-    p.n = n, p.chunk = sh.chunk, p.V = uint32_t(V), p.D = D, p.walk = sh.walk, p.groups = sh.groups, p.cols = sh.cols;
-    p.vecs = sh.vecs, p.in_stride = in_stride, p.out_stride = out_stride, p.scale = scale;
-    p.head = reinterpret_cast<float *>(ws + L.head), p.tail = reinterpret_cast<float *>(ws + L.tail);
-    if (vec)
-        launch_sums<T, G, kVec>(p, sh, static_cast<const T *>(dout), dt, s);
-    else
-        launch_sums<T, G, 1>(p, sh, static_cast<const T *>(dout), dt, s);
+    Clearing<G> clear{dt, V, out_stride, D, 0, 1};
+    // CTAs that clear: enough to draw on the whole bandwidth where there is much to clear
+    const int64_t bytes = V * D * int64_t(sizeof(G));
+    const uint64_t *sorted = w[0];
+    if (n <= kSmallN) {
+        const int want = int(bytes / (64 * 1024)) + 1, ctas = want < sms * 2 ? want : sms * 2;
+        constexpr int kSmem = kSmallN * 6 + kSmallThreads / 32 * 512;
+        auto kernel = k_embed_sort_small<I, G>;
+        static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
+        const void *fn = (const void *)kernel;
+        const ss_status e = ensure_dyn_smem(smem_ctx, &fn, 1, kSmem, "ss_embed_bwd");
+        if (e != SS_OK) return e;
+        SS_LAUNCH("k_embed_sort_small", s,
+                  kernel<<<1 + ctas, kSmallThreads, kSmem, s>>>(id, int(n), uint32_t(V), (bits_of(V + 1) + 7) / 8, w[0],
+                                                                st, clear));
+    } else {
+        const int bits = bits_of(V), passes = passes_of(bits);
+        PassParams p{};
+        p.n = n, p.V = uint32_t(V), p.bits = digit_of(bits), p.parts = L.parts;
+        p.counts = reinterpret_cast<uint32_t *>(ws + L.counts), p.totals = reinterpret_cast<uint32_t *>(ws + L.totals);
+        p.st = st;
+        clear.shares = 3 * passes;
+        const int64_t share = bytes / clear.shares;
+        const int want = int(share / (32 * 1024) < 1 << 20 ? share / (32 * 1024) : 1 << 20) + 1;
+        const int ctas = want < sms * 4 ? want : sms * 4;
+        const int scanning = ((1 << p.bits) + kThreads / 32 - 1) / (kThreads / 32);
+        const size_t smem = size_t(kPart) * 8 + (size_t(8) << p.bits) * 2 + (size_t(2) << p.bits) * 4;
+        auto move = k_embed_move<I, G>;
+        static std::atomic<unsigned long long> smem_ctx[kMaxDevices];
+        const void *fn = (const void *)move;
+        const ss_status e = ensure_dyn_smem(smem_ctx, &fn, 1, kPart * 8 + (8 << kMaxBits) * 2 + (2 << kMaxBits) * 4,
+                                            "ss_embed_bwd");
+        if (e != SS_OK) return e;
+        for (int d = 0; d < passes; ++d) {
+            p.first = d == 0, p.shift = d * p.bits, p.in = w[(d + 1) & 1], p.out = w[d & 1];
+            if (d == 0)
+                SS_LAUNCH("k_embed_count", s,
+                          k_embed_count<I, G><<<p.parts + ctas, kThreads, 0, s>>>(id, p, clear));
+            else
+                SS_LAUNCH("k_embed_count", s,
+                          launch_after(k_embed_count<I, G>, dim3(p.parts + ctas), kThreads, 0, s, id, p, clear));
+            ++clear.share;
+            SS_LAUNCH("k_embed_scan", s,
+                      launch_after(k_embed_scan<G>, dim3(scanning + ctas), kThreads, 0, s, p, scanning, clear));
+            ++clear.share;
+            SS_LAUNCH("k_embed_move", s,
+                      launch_after(move, dim3(p.parts + ctas), kThreads, smem, s, id, p, clear));
+            ++clear.share;
+        }
+        sorted = w[(passes - 1) & 1];
+    }
+    if (n == 0) return SS_OK;
+    constexpr int E = sizeof(T);
+    int b = access_bytes(dout, in_stride * E, dout, in_stride * E, int64_t(D) * E);
+    // the gradient's rows are written in the same vectors (of 32 bytes in two halves)
+    for (; b > E; b /= 2) {
+        const int64_t a = int64_t(b) / E * int64_t(sizeof(G)) < 16 ? int64_t(b) / E * int64_t(sizeof(G)) : 16;
+        if (aligned_to(dtable, size_t(a)) && (out_stride * int64_t(sizeof(G))) % a == 0) break;
+    }
+    auto go = [&](auto NE) {
+        constexpr int kN = decltype(NE)::value;
+        const SumShape sh = sum_shape(n, D, kN);
+        SumParams p{};
+        p.words = sorted, p.st = st;
+        p.n = n, p.chunk = sh.chunk, p.V = uint32_t(V), p.D = D, p.walk = sh.walk, p.groups = sh.groups;
+        p.cols = sh.cols, p.vecs = sh.vecs, p.in_stride = in_stride, p.out_stride = out_stride, p.scale = scale;
+        p.head = reinterpret_cast<float *>(ws + L.head), p.tail = reinterpret_cast<float *>(ws + L.tail);
+        p.flags = reinterpret_cast<uint32_t *>(ws + L.flags);
+        launch_sums<T, G, kN>(p, sh, static_cast<const T *>(dout), dt, s);
+    };
+    if (b == 16) go(std::integral_constant<int, 16 / E>{});
+    else if (b == 8) go(std::integral_constant<int, 8 / E>{});
+    else if (b == 4 && E == 2) go(std::integral_constant<int, E == 2 ? 2 : 1>{});
+    else go(std::integral_constant<int, 1>{});
     return SS_OK;
 }
 
@@ -540,12 +857,10 @@ ss_status ss_embed_fwd(const void *table, ss_dtype dtype, int64_t V, int32_t D, 
     if (st != SS_OK || n == 0) return st;
     if ((st = check_rows(who, "table", table, table_stride, D, dtype)) != SS_OK) return st;
     if ((st = check_rows(who, "out", out, out_stride, D, dtype)) != SS_OK) return st;
-    int dev = 0, sms = 0;
-    if ((st = current_device(&dev, &sms, "ss_embed_fwd: device query")) != SS_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
 #define SS_FWD(T)                                                                                             \
-    (id_bytes == 4 ? launch_fwd<T, int32_t>(table, table_stride, V, D, ids, n, scale, out, out_stride, sms, s) \
-                   : launch_fwd<T, int64_t>(table, table_stride, V, D, ids, n, scale, out, out_stride, sms, s))
+    (id_bytes == 4 ? launch_fwd<T, int32_t>(table, table_stride, V, D, ids, n, scale, out, out_stride, s) \
+                   : launch_fwd<T, int64_t>(table, table_stride, V, D, ids, n, scale, out, out_stride, s))
     if (dtype == SS_F32) SS_FWD(float);
     else if (dtype == SS_F16) SS_FWD(__half);
     else SS_FWD(__nv_bfloat16);
@@ -584,20 +899,6 @@ ss_status ss_embed_bwd(const void *dout, ss_dtype dtype, int64_t dout_stride, co
     else st = grad_dtype == SS_F32 ? SS_BWD(__nv_bfloat16, float) : SS_BWD(__nv_bfloat16, __nv_bfloat16);
 #undef SS_BWD
     return st != SS_OK ? st : check_launch(who);
-}
-
-ss_status ss_embed_status(const void *workspace, ss_stream_t stream) {
-    clear_error();
-    if (!workspace) return fail(SS_ERR_INVALID_ARG, "ss_embed_status: workspace is NULL");
-    uint32_t word = 0;
-    ss_status st = check_cuda(cudaMemcpyAsync(&word, workspace, 4, cudaMemcpyDeviceToHost, (cudaStream_t)stream),
-                              "ss_embed_status: cudaMemcpyAsync");
-    if (st != SS_OK) return st;
-    st = check_cuda(cudaStreamSynchronize((cudaStream_t)stream), "ss_embed_status: synchronize");
-    if (st != SS_OK) return st;
-    if (word & kDevErrTimeout)
-        return fail(SS_ERR_TIMEOUT, "ss_embed_bwd: a look-back wait gave up (status 0x%x)", word);
-    return SS_OK;
 }
 
 }  // extern "C"

@@ -29,14 +29,19 @@ __device__ __forceinline__ __half from_float<__half>(float v) { return __float2h
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// N elements of T as they lie in memory: one of them, or 16 bytes held as four
-// words (an array of 16-bit class types would be loaded element by element).
+// N elements of T as they lie in memory: one of them, or 4, 8 or 16 bytes held
+// as words (an array of 16-bit class types would be loaded element by
+// element).
 template <typename T, int N>
 struct Vec {
-    static_assert(N * sizeof(T) == 16, "a vector is 16 bytes");
-    uint32_t w[4];
+    static constexpr int kWords = N * int(sizeof(T)) / 4;
+    static_assert(kWords == 1 || kWords == 2 || kWords == 4, "a vector is 4, 8 or 16 bytes");
+    uint32_t w[kWords];
     __device__ __forceinline__ float get(int i) const { return get_as(i, T()); }
-    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
     // Element i as it is.
     __device__ __forceinline__ T elem(int i) const { return elem_as(i, T()); }
     // Puts element i in place (after clear()).
@@ -77,6 +82,11 @@ __device__ __forceinline__ Vec<T, N> load_vec(const T *p) {
     Vec<T, N> x;
     if constexpr (N == 1) {
         x.v = *p;
+    } else if constexpr (Vec<T, N>::kWords == 1) {
+        x.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (Vec<T, N>::kWords == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        x.w[0] = u.x, x.w[1] = u.y;
     } else {
         const uint4 u = *reinterpret_cast<const uint4 *>(p);
         x.w[0] = u.x, x.w[1] = u.y, x.w[2] = u.z, x.w[3] = u.w;
@@ -113,11 +123,17 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
     return r;
 }
 
-// Stores N floats rounded to T: one of them, or 16-byte pieces.
+// Stores N floats rounded to T: one of them, 4 or 8 bytes, or 16-byte pieces.
 template <typename T, int N>
 __device__ __forceinline__ void store_floats(T *p, const float (&f)[N]) {
     if constexpr (N == 1) {
         *p = from_float<T>(f[0]);
+    } else if constexpr (N == 2 && sizeof(T) == 4) {
+        *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<uint32_t *>(p) = pack2<T>(f[0], f[1]);
+    } else if constexpr (N == 4 && sizeof(T) == 2) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int k = 0; k < N; k += 4)

@@ -50,11 +50,6 @@ ss_status ss_embed_bwd(const void *dout, ss_dtype dtype, int64_t dout_stride, co
                        void *dtable, ss_dtype grad_dtype, int64_t dtable_stride, void *workspace,
                        size_t workspace_bytes, ss_stream_t stream);
 
-/* Synchronizes `stream` and reports the last ss_embed_bwd on this workspace:
- * SS_OK, or SS_ERR_TIMEOUT if a bounded wait of its sort gave up (the
- * gradient is then wrong). */
-ss_status ss_embed_status(const void *workspace, ss_stream_t stream);
-
 #ifdef __cplusplus
 }
 #endif

@@ -155,7 +155,6 @@ def test_infinities_and_nan_stay_in_their_rows(ss):
     assert (out[0] == 1).all() and torch.isinf(out[1]).all() and torch.isnan(out[2]).all() and (out[3] == 0).all()
     g = e.backward(out, torch.tensor([3, 2, 1, 1], device="cuda"))
     assert (g[0] == 0).all() and torch.isnan(g[1]).all() and torch.isinf(g[2]).all() and (g[3] == 1).all()
-    e.check()
 
 
 def test_another_stream_and_a_captured_graph(ss):

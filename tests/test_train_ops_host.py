@@ -71,7 +71,6 @@ def test_lookup_gradient_refusals(lib):
     assert f(ds=3) == BAD and f(gs=3) == BAD and f(g=0x1002) == BAD
     assert f(ws=None) == BAD and f(ws=0x1010) == BAD and f(nb=need - 1) == BAD
     assert "workspace" in lib.ss_last_error().decode()
-    assert lib.ss_embed_status(None, None) == BAD
 
 
 def test_norm_refusals(lib):
