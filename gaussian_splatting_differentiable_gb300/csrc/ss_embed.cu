@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_fwd(const T *__restrict__ ta
 
 // ------------------------------------------------------------------ sort
 
-constexpr int kPart = 4096;              // ids of one sort partition
+constexpr int kPart = 2048;              // ids of one sort partition
 constexpr int kKpt = kPart / kThreads;
 constexpr int kMaxBits = 10;             // of a digit: at most 1024 bins
 constexpr int kSmallN = 8192;            // ids that one CTA sorts by itself
@@ -84,20 +84,39 @@ __device__ __forceinline__ uint32_t id_key(const I *ids, int64_t i, uint32_t V) 
 }
 
 // Exclusive scan of one value a thread over the CTA; s_warp: a word a warp.
-__device__ __forceinline__ uint32_t excl_scan(uint32_t v, uint32_t *s_warp) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x) {   // inclusive
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
+    return x;
+}
+__device__ __forceinline__ uint32_t excl_scan(uint32_t v, uint32_t *s_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint32_t x = warp_scan(v);
     __syncthreads();
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
-    uint32_t base = 0;
-    for (int w = 0; w < warp; ++w) base += s_warp[w];
-    return base + x - v;
+    const uint32_t sums = warp_scan(lane < warps ? s_warp[lane] : 0u);
+    const uint32_t before = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+    return (warp > 0 ? before : 0u) + x - v;
+}
+
+// The lanes whose digit of BITS bits is this lane's (of those with `ok`): a
+// vote for each bit.  (A match instruction took several times as long: 2M ids
+// of 12 bits, 155 us for the whole gradient against 132.)
+template <int BITS>
+__device__ __forceinline__ uint32_t same_digit(uint32_t dig, bool ok) {
+    uint32_t peers = __ballot_sync(0xffffffffu, ok);
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
+        const bool one = (dig >> b) & 1u;
+        const uint32_t v = __ballot_sync(0xffffffffu, one);
+        peers &= one ? v : ~v;
+    }
+    return peers;
 }
 
 __device__ __forceinline__ uint32_t lanes_below() {
@@ -163,11 +182,14 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s_count = 0;
     const uint32_t lt = lanes_below();
+    // every warp has as many ids in turn, and no more than there are: a few
+    // hundred take one step of eight
+    const int per = (n + kSmallThreads - 1) / kSmallThreads * 32, used = per > 0 ? (n + per - 1) / per : 0;
     uint32_t key[kSmallKpt], pos[kSmallKpt];
     uint32_t named = 0;
 #pragma unroll
     for (int j = 0; j < kSmallKpt; ++j) {
-        const int i = warp * (kSmallKpt * 32) + j * 32 + lane;
+        const int i = j * 32 < per ? warp * per + j * 32 + lane : n;
         key[j] = i < n ? id_key(ids, i, V) : 0u;
         pos[j] = uint32_t(i);
         named += i < n && key[j] < V;
@@ -176,14 +198,15 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
     named = __reduce_add_sync(0xffffffffu, named);
     if (lane == 0 && named) atomicAdd(&s_count, named);
     for (int d = 0; d < passes; ++d) {
-        for (int e = tid; e < kWarps * 128; e += kSmallThreads) reinterpret_cast<uint32_t *>(&s_hist[0][0])[e] = 0u;
+        for (int e = tid; e < used * 128; e += kSmallThreads) reinterpret_cast<uint32_t *>(&s_hist[0][0])[e] = 0u;
         __syncthreads();
         uint32_t rank[kSmallKpt];
 #pragma unroll
         for (int j = 0; j < kSmallKpt; ++j) {
-            const bool ok = warp * (kSmallKpt * 32) + j * 32 + lane < n;
-            const uint32_t dig = ok ? (key[j] >> (8 * d)) & 255u : 256u + lane;
-            const uint32_t peers = __match_any_sync(0xffffffffu, dig);
+            if (j * 32 >= per || warp >= used) break;
+            const bool ok = warp * per + j * 32 + lane < n;
+            const uint32_t dig = (key[j] >> (8 * d)) & 255u;
+            const uint32_t peers = same_digit<8>(dig, ok);
             const uint32_t before = __popc(peers & lt);
             const uint32_t cur = ok ? s_hist[warp][dig] : 0u;
             rank[j] = cur + before;
@@ -195,7 +218,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
         uint32_t total = 0;
         if (tid < 256)
 #pragma unroll 8
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < used; ++w) {
                 const uint32_t c = s_hist[w][tid];
                 s_hist[w][tid] = uint16_t(total);
                 total += c;
@@ -205,7 +228,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kSmallKpt; ++j)
-            if (warp * (kSmallKpt * 32) + j * 32 + lane < n) {
+            if (j * 32 < per && warp * per + j * 32 + lane < n) {
                 const uint32_t dig = (key[j] >> (8 * d)) & 255u;
                 const uint32_t to = s_start[dig] + s_hist[warp][dig] + rank[j];
                 s_key[to] = key[j];
@@ -214,14 +237,14 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kSmallKpt; ++j) {
-            const int i = warp * (kSmallKpt * 32) + j * 32 + lane;
+            const int i = j * 32 < per ? warp * per + j * 32 + lane : n;
             if (i < n) key[j] = s_key[i], pos[j] = s_pos[i];
         }
         __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < kSmallKpt; ++j) {
-        const int i = warp * (kSmallKpt * 32) + j * 32 + lane;
+        const int i = j * 32 < per ? warp * per + j * 32 + lane : n;
         if (i < n) words[i] = uint64_t(key[j]) << 32 | pos[j];
     }
     if (tid == 0) st->count = int64_t(s_count);
@@ -274,62 +297,55 @@ __global__ void __launch_bounds__(kThreads) k_embed_count(const I *__restrict__ 
         const int64_t i = base + j * kThreads + threadIdx.x;
         key[j] = i < n ? uint32_t(word_at(p, ids, i) >> 32) : p.V;
     }
-    const uint32_t lt = lanes_below();
 #pragma unroll
-    for (int j = 0; j < kKpt; ++j) {
-        const bool ok = key[j] < p.V;      // equal digits of a warp add once
-        const uint32_t dig = ok ? (key[j] >> p.shift) & uint32_t(bins - 1) : 0xffffffffu;
-        const uint32_t peers = __match_any_sync(0xffffffffu, dig);
-        if (ok && (peers & lt) == 0) atomicAdd(&s_hist[dig], uint32_t(__popc(peers)));
-    }
+    for (int j = 0; j < kKpt; ++j)
+        if (key[j] < p.V) atomicAdd(&s_hist[(key[j] >> p.shift) & uint32_t(bins - 1)], 1u);
     __syncthreads();
     for (int k = threadIdx.x; k < bins; k += kThreads) p.counts[int64_t(k) * p.parts + blockIdx.x] = s_hist[k];
 }
 
-// A warp for each bin: exclusive sums of its counts over the partitions.
+// A CTA for each bin: exclusive sums of its counts over the partitions.
 template <typename G>
-__global__ void __launch_bounds__(kThreads) k_embed_scan(PassParams p, int scanning, Clearing<G> clear) {
+__global__ void __launch_bounds__(kThreads) k_embed_scan(PassParams p, Clearing<G> clear) {
+    __shared__ uint32_t s_warp[kThreads / 32];
+    const int bins = 1 << p.bits;
     start_dependents();
     wait_for_previous();
-    if (int(blockIdx.x) >= scanning) {
-        clear_share(clear, blockIdx.x - scanning, gridDim.x - scanning);
+    if (int(blockIdx.x) >= bins) {
+        clear_share(clear, blockIdx.x - bins, gridDim.x - bins);
         return;
     }
-    const int lane = threadIdx.x & 31, bin = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (bin >= 1 << p.bits) return;
-    uint32_t *c = p.counts + int64_t(bin) * p.parts;
+    uint32_t *c = p.counts + int64_t(blockIdx.x) * p.parts;
     uint32_t run = 0;
-    for (int q0 = 0; q0 < p.parts; q0 += 128) {
-        uint32_t v[4], mine = 0;           // four neighbours a lane
+    for (int q0 = 0; q0 < p.parts; q0 += kThreads * 4) {
+        uint32_t v[4], mine = 0;           // four neighbours a thread
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int q = q0 + lane * 4 + u;
+            const int q = q0 + threadIdx.x * 4 + u;
             v[u] = q < p.parts ? c[q] : 0u;
             mine += v[u];
         }
-        uint32_t x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        uint32_t at = run + x - mine;
+        const uint32_t before = excl_scan(mine, s_warp);
+        uint32_t at = run + before;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int q = q0 + lane * 4 + u;
+            const int q = q0 + threadIdx.x * 4 + u;
             if (q < p.parts) c[q] = at;
             at += v[u];
         }
-        run += __shfl_sync(0xffffffffu, x, 31);
+        __syncthreads();
+        if (threadIdx.x == kThreads - 1) s_warp[0] = before + mine;
+        __syncthreads();
+        run += s_warp[0];
     }
-    if (lane == 0) p.totals[bin] = run;
+    if (threadIdx.x == 0) p.totals[blockIdx.x] = run;
 }
 
-template <typename I, typename G>
+template <typename I, typename G, int BITS>
 __global__ void __launch_bounds__(kThreads) k_embed_move(const I *__restrict__ ids, PassParams p, Clearing<G> clear) {
     extern __shared__ uint64_t s_words[];                                        // [kPart]
     uint16_t *s_hist = reinterpret_cast<uint16_t *>(s_words + kPart);            // [8 warps][bins]
-    const int bins = 1 << p.bits;
+    constexpr int bins = 1 << BITS;
     uint32_t *s_lstart = reinterpret_cast<uint32_t *>(s_hist + 8 * bins);        // [bins] starts in this partition
     uint32_t *s_gbase = s_lstart + bins;                                         // [bins] destinations less starts
     __shared__ uint32_t s_warp[8];
@@ -345,7 +361,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_move(const I *__restrict__ i
     __syncthreads();
     const int64_t n = pass_size(p), base = int64_t(blockIdx.x) * kPart, wbase = base + warp * (kKpt * 32);
     const int shift = 32 + p.shift;
-    const uint32_t mask = uint32_t(bins - 1);
+    constexpr uint32_t mask = uint32_t(bins - 1);
     uint64_t word[kKpt];
 #pragma unroll
     for (int j = 0; j < kKpt; ++j) {
@@ -358,8 +374,8 @@ __global__ void __launch_bounds__(kThreads) k_embed_move(const I *__restrict__ i
 #pragma unroll
     for (int j = 0; j < kKpt; ++j) {
         const bool ok = uint32_t(word[j] >> 32) < p.V;
-        const uint32_t dig = ok ? uint32_t(word[j] >> shift) & mask : 0xffffffffu - lane;
-        const uint32_t peers = __match_any_sync(0xffffffffu, dig);
+        const uint32_t dig = uint32_t(word[j] >> shift) & mask;
+        const uint32_t peers = same_digit<BITS>(dig, ok);
         const uint32_t before = __popc(peers & lt);
         const uint32_t cur = ok ? mine[dig] : 0u;
         rank[j] = cur + before;
@@ -621,9 +637,9 @@ int bits_of(int64_t v) {                   // of the numbers below v
 
 // Passes over `bits` bits of the key, and the bits of each.
 int passes_of(int bits) { return bits < 1 ? 1 : (bits + kMaxBits - 1) / kMaxBits; }
-int digit_of(int bits) {
+int digit_of(int bits) {                   // 6, 8 or 10
     const int p = passes_of(bits), b = (bits + p - 1) / p;
-    return b < 1 ? 1 : b;
+    return b <= 6 ? 6 : (b <= 8 ? 8 : 10);
 }
 
 struct SumShape {
@@ -632,7 +648,8 @@ struct SumShape {
 };
 
 // Columns over threads: a row's vectors side by side, as many walks as fit in
-// a CTA.  A walk is as long as leaves about eight CTAs an SM.
+// a CTA.  A walk is as long as leaves about eight CTAs an SM, or a little
+// longer where that spares the join.
 SumShape sum_shape(int64_t n, int32_t D, int vec) {
     SumShape s;
     s.vecs = D / vec;
@@ -641,6 +658,7 @@ SumShape sum_shape(int64_t n, int32_t D, int vec) {
     s.groups = kThreads / s.cols;
     int64_t w = n * s.slices / (int64_t(s.groups) * 152 * 8);
     s.walk = int(w < 8 ? 8 : (w > 64 ? 64 : (w + 7) / 8 * 8));
+    if (n <= int64_t(s.groups) * 16 && n > int64_t(s.groups) * s.walk) s.walk = 16;   // one chunk: nothing to join
     s.chunk = int64_t(s.groups) * s.walk;
     s.chunks = (n + s.chunk - 1) / s.chunk;
     return s;
@@ -783,12 +801,12 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
         const int64_t share = bytes / clear.shares;
         const int want = int(share / (32 * 1024) < 1 << 20 ? share / (32 * 1024) : 1 << 20) + 1;
         const int ctas = want < sms * 4 ? want : sms * 4;
-        const int scanning = ((1 << p.bits) + kThreads / 32 - 1) / (kThreads / 32);
         const size_t smem = size_t(kPart) * 8 + (size_t(8) << p.bits) * 2 + (size_t(2) << p.bits) * 4;
-        auto move = k_embed_move<I, G>;
+        auto move = p.bits == 6 ? k_embed_move<I, G, 6> : (p.bits == 8 ? k_embed_move<I, G, 8> : k_embed_move<I, G, 10>);
         static std::atomic<unsigned long long> smem_ctx[kMaxDevices];
-        const void *fn = (const void *)move;
-        const ss_status e = ensure_dyn_smem(smem_ctx, &fn, 1, kPart * 8 + (8 << kMaxBits) * 2 + (2 << kMaxBits) * 4,
+        const void *fns[] = {(const void *)k_embed_move<I, G, 6>, (const void *)k_embed_move<I, G, 8>,
+                             (const void *)k_embed_move<I, G, 10>};
+        const ss_status e = ensure_dyn_smem(smem_ctx, fns, 3, kPart * 8 + (8 << kMaxBits) * 2 + (2 << kMaxBits) * 4,
                                             "ss_embed_bwd");
         if (e != SS_OK) return e;
         for (int d = 0; d < passes; ++d) {
@@ -801,7 +819,7 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
                           launch_after(k_embed_count<I, G>, dim3(p.parts + ctas), kThreads, 0, s, id, p, clear));
             ++clear.share;
             SS_LAUNCH("k_embed_scan", s,
-                      launch_after(k_embed_scan<G>, dim3(scanning + ctas), kThreads, 0, s, p, scanning, clear));
+                      launch_after(k_embed_scan<G>, dim3((1 << p.bits) + ctas), kThreads, 0, s, p, clear));
             ++clear.share;
             SS_LAUNCH("k_embed_move", s,
                       launch_after(move, dim3(p.parts + ctas), kThreads, smem, s, id, p, clear));
