@@ -68,12 +68,14 @@ __global__ void __launch_bounds__(kThreads) k_embed_fwd(const T *__restrict__ ta
 
 constexpr int kPart = 2048;              // ids of one sort partition
 constexpr int kKpt = kPart / kThreads;
-constexpr int kMaxBits = 10;             // of a digit: at most 1024 bins
+constexpr int kMaxBits = 8;              // of a digit: at most 256 bins
+constexpr int kFewParts = 32;            // partitions whose counts the move adds up itself
 constexpr int kSmallN = 8192;            // ids that one CTA sorts by itself
 constexpr int kSmallThreads = 1024, kSmallKpt = kSmallN / kSmallThreads;
 
 struct SortState {
     int64_t count;                       // ids that name a row
+    uint32_t joins;                      // ids that cross chunks of the sorted words
 };
 
 // The id as a key, V where it names no row.
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
         const int i = j * 32 < per ? warp * per + j * 32 + lane : n;
         if (i < n) words[i] = uint64_t(key[j]) << 32 | pos[j];
     }
-    if (tid == 0) st->count = int64_t(s_count);
+    if (tid == 0) st->count = int64_t(s_count), st->joins = 0;
 }
 
 // More ids: stable passes over digits of the key, least significant first,
@@ -264,7 +266,9 @@ struct PassParams {
     int shift, bits;         // the digit
     int parts;
     bool first;
-    uint32_t *counts;        // [bins][parts]: of the digit in each partition, then their exclusive sums
+    uint32_t *counts;        // [bins][parts, to a multiple of 4]: of the digit in each partition; where there
+                             // are more than kFewParts, k_embed_scan makes them exclusive sums
+    int row;                 // of counts
     uint32_t *totals;        // [bins]
     SortState *st;
 };
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_count(const I *__restrict__ 
     for (int j = 0; j < kKpt; ++j)
         if (key[j] < p.V) atomicAdd(&s_hist[(key[j] >> p.shift) & uint32_t(bins - 1)], 1u);
     __syncthreads();
-    for (int k = threadIdx.x; k < bins; k += kThreads) p.counts[int64_t(k) * p.parts + blockIdx.x] = s_hist[k];
+    for (int k = threadIdx.x; k < bins; k += kThreads) p.counts[int64_t(k) * p.row + blockIdx.x] = s_hist[k];
 }
 
 // A CTA for each bin: exclusive sums of its counts over the partitions.
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_scan(PassParams p, Clearing<
         clear_share(clear, blockIdx.x - bins, gridDim.x - bins);
         return;
     }
-    uint32_t *c = p.counts + int64_t(blockIdx.x) * p.parts;
+    uint32_t *c = p.counts + int64_t(blockIdx.x) * p.row;
     uint32_t run = 0;
     for (int q0 = 0; q0 < p.parts; q0 += kThreads * 4) {
         uint32_t v[4], mine = 0;           // four neighbours a thread
@@ -384,31 +388,40 @@ __global__ void __launch_bounds__(kThreads) k_embed_move(const I *__restrict__ i
         __syncwarp();
     }
     __syncthreads();
-    // bins: the warps' starts in each, the partition's start, the destination
-    uint32_t local = 0, global = 0;        // running sums over the bins done so far
-    for (int k0 = 0; k0 < bins; k0 += kThreads) {
-        const int k = k0 + tid;
-        uint32_t total = 0, all = 0, earlier = 0;
-        if (k < bins) {
+    // a thread a bin: the warps' starts in it, the partition's start, the destination
+    uint32_t total = 0, all = 0, earlier = 0;
+    if (tid < bins) {
+        const uint32_t *c = p.counts + int64_t(tid) * p.row;
+        if (p.parts <= kFewParts) {
+            uint4 v[kFewParts / 4];
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const uint32_t c = s_hist[w * bins + k];
-                s_hist[w * bins + k] = uint16_t(total);
-                total += c;
+            for (int q = 0; q < kFewParts; q += 4)
+                v[q / 4] = q < p.parts ? *reinterpret_cast<const uint4 *>(c + q) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < kFewParts; ++q) {
+                const uint4 f = v[q / 4];
+                const uint32_t x = q % 4 == 0 ? f.x : (q % 4 == 1 ? f.y : (q % 4 == 2 ? f.z : f.w));
+                if (q < p.parts) all += x;
+                if (q < int(blockIdx.x)) earlier += x;
             }
-            all = p.totals[k];
-            earlier = p.counts[int64_t(k) * p.parts + blockIdx.x];
+        } else {
+            all = p.totals[tid];
+            earlier = c[blockIdx.x];
         }
-        const uint32_t ls = local + excl_scan(total, s_warp), gs = global + excl_scan(all, s_warp);
-        if (k < bins) s_lstart[k] = ls, s_gbase[k] = gs + earlier - ls;
-        // the last thread has the sums of all of them
-        __syncthreads();
-        if (tid == kThreads - 1) s_warp[0] = ls + total, s_warp[1] = gs + all;
-        __syncthreads();
-        local = s_warp[0], global = s_warp[1];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const uint32_t m = s_hist[w * bins + tid];
+            s_hist[w * bins + tid] = uint16_t(total);
+            total += m;
+        }
     }
-    if (p.first && blockIdx.x == 0 && tid == 0) p.st->count = int64_t(global);
+    const uint32_t ls = excl_scan(total, s_warp), gs = excl_scan(all, s_warp);
+    if (tid < bins) s_lstart[tid] = ls, s_gbase[tid] = gs + earlier - ls;
     __syncthreads();
+    if (tid == kThreads - 1) s_warp[0] = ls + total, s_warp[1] = gs + all;   // the sums of all bins
+    __syncthreads();
+    const uint32_t local = s_warp[0], global = s_warp[1];
+    if (p.first && blockIdx.x == 0 && tid == 0) p.st->count = int64_t(global), p.st->joins = 0;
 #pragma unroll
     for (int j = 0; j < kKpt; ++j)
         if (uint32_t(word[j] >> 32) < p.V) {
@@ -435,49 +448,66 @@ enum : uint32_t { kIn = 1u, kOn = 2u, kWhole = 4u };   // of a walk or chunk: it
                                                         // after it, one id fills it and does both
 struct SumParams {
     const uint64_t *words;   // sorted id << 32 | position
-    const SortState *st;
+    SortState *st;
     int64_t n, chunk;        // ids; words of a CTA = groups * walk
     uint32_t V;
     int32_t D;
-    int walk, groups, cols, vecs;
+    int walk, groups, cols;
+    int vecs;                // vectors of a row; a thread owns every cols-th of its CTA's slice
     int64_t in_stride, out_stride;
     float scale;
     float *head, *tail;      // [chunks][D]
     uint32_t *flags;         // [chunks]
+    uint32_t *list;          // chunks whose last id goes on after them and began in them
 };
 
 __device__ __forceinline__ uint32_t key_at(const SumParams &p, int64_t i) { return uint32_t(p.words[i] >> 32); }
 
-template <typename G, int N>
-__device__ __forceinline__ void finish_row(const SumParams &p, G *dtable, uint32_t key, int col, const float (&acc)[N]) {
+// Vector k of a thread: column col0 + k * cols (in vectors).
+template <typename G, int N, int K>
+__device__ __forceinline__ void finish_row(const SumParams &p, G *dtable, uint32_t key, int col0, const float (&acc)[K][N]) {
     if (key >= p.V) return;
-    float f[N];
+    G *row = dtable + int64_t(key) * p.out_stride;
 #pragma unroll
-    for (int k = 0; k < N; ++k) f[k] = acc[k] * p.scale;
-    store_floats<G, N>(dtable + int64_t(key) * p.out_stride + int64_t(col) * N, f);
+    for (int k = 0; k < K; ++k) {
+        if (col0 + k * p.cols >= p.vecs) continue;
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = acc[k][i] * p.scale;
+        store_floats<G, N>(row + (col0 + k * p.cols) * N, f);
+    }
 }
 
-template <typename T, typename G, int N>
-__global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__restrict__ dout, G *dtable) {
-    extern __shared__ float s_part[];      // head then tail: [groups][cols][N], then flags [groups]
-    constexpr int kBatch = N >= 4 ? 8 : 16;
+template <typename T, typename G, int N, int K>
+__global__ void __launch_bounds__(kThreads, 4) k_embed_sum(SumParams p, const T *__restrict__ dout, G *dtable) {
+    extern __shared__ float s_part[];      // head then tail: [K * N][threads], then flags [groups]
+    constexpr int kBatch = 4;
     const int g = threadIdx.x / p.cols, c = threadIdx.x - g * p.cols;
-    const int col = blockIdx.y * p.cols + c;
-    float *head = s_part + size_t(threadIdx.x) * N;
-    float *tail = head + size_t(blockDim.x) * N;
-    uint32_t *s_flags = reinterpret_cast<uint32_t *>(s_part + size_t(blockDim.x) * N * 2);
+    const int col0 = blockIdx.y * p.cols * K + c, threads = blockDim.x;
+    float *head = s_part + threadIdx.x;
+    float *tail = head + size_t(threads) * K * N;
+    uint32_t *s_flags = reinterpret_cast<uint32_t *>(s_part + size_t(threads) * K * N * 2);
+    auto put = [&](float *to, const float (&v)[K][N]) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) to[(k * N + i) * threads] = v[k][i];
+    };
     start_dependents();
     wait_for_previous();
     const int64_t n = p.st->count < p.n ? p.st->count : p.n;
     const int64_t lo = int64_t(blockIdx.x) * p.chunk + int64_t(g) * p.walk;
     const int64_t hi = lo + p.walk < n ? lo + p.walk : n;
     uint32_t flags = 0, cur = 0;
-    float acc[N];
+    float acc[K][N];
+    auto clear = [&] {
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[k][i] = 0.0f;
+    };
+    clear();
     if (lo < hi) {
-        const bool live = col < p.vecs;
-        const T *base = dout + int64_t(live ? col : 0) * N;
         uint64_t w[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) w[u] = lo + u < hi ? p.words[lo + u] : ~0ull;
@@ -486,14 +516,19 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__
         const uint32_t after = hi < n ? key_at(p, hi) : p.V;
         flags = open ? kIn : 0u;
         for (int64_t i = lo; i < hi; i += kBatch) {
-            Vec<T, N> x[kBatch];
+            Vec<T, N> x[kBatch][K];
             uint32_t key[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const uint32_t pos = uint32_t(w[u]);
                 key[u] = uint32_t(w[u] >> 32);
-                x[u].clear();
-                if (key[u] < p.V && int64_t(pos) < p.n) x[u] = load_vec<T, N>(base + int64_t(pos) * p.in_stride);
+                const T *row = dout + int64_t(pos) * p.in_stride + col0 * N;
+                const bool here = key[u] < p.V && int64_t(pos) < p.n;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    x[u][k].clear();
+                    if (here && col0 + k * p.cols < p.vecs) x[u][k] = load_vec<T, N>(row + k * p.cols * N);
+                }
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)              // the next words, while the rows arrive
@@ -502,32 +537,28 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__
             for (int u = 0; u < kBatch; ++u) {
                 if (i + u >= hi) break;
                 if (key[u] != cur) {
-                    if (open) {
-#pragma unroll
-                        for (int k = 0; k < N; ++k) head[k] = acc[k];
-                    } else if (live) {
-                        finish_row<G, N>(p, dtable, cur, col, acc);
-                    }
+                    if (open)
+                        put(head, acc);
+                    else
+                        finish_row<G, N, K>(p, dtable, cur, col0, acc);
                     open = false;
                     cur = key[u];
-#pragma unroll
-                    for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+                    clear();
                 }
 #pragma unroll
-                for (int k = 0; k < N; ++k) acc[k] += x[u].get(k);
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) acc[k][e] += x[u][k].get(e);
             }
         }
         const bool on = hi < n && after == cur;
         flags |= (on ? kOn : 0u) | (open && on ? kWhole : 0u);
-        if (open) {
-#pragma unroll
-            for (int k = 0; k < N; ++k) head[k] = acc[k];
-        } else if (!on) {
-            if (live) finish_row<G, N>(p, dtable, cur, col, acc);
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k) tail[k] = acc[k];
-        }
+        if (open)
+            put(head, acc);
+        else if (on)
+            put(tail, acc);
+        else
+            finish_row<G, N, K>(p, dtable, cur, col0, acc);
     }
     if (c == 0) s_flags[g] = flags;
     __syncthreads();
@@ -535,20 +566,28 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__
     for (int pass = 0; pass < 2; ++pass) {
         const bool incoming = pass == 0;   // the id that the chunk before began: walk 0's threads
         if (incoming ? !(g == 0 && (flags & kIn)) : (flags & (kOn | kWhole)) != kOn) continue;
-        float *own = incoming ? head : tail;
+        const float *own = incoming ? head : tail;
 #pragma unroll
-        for (int k = 0; k < N; ++k) acc[k] = own[k];
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[k][e] = own[(k * N + e) * threads];
         bool on = incoming ? (flags & kWhole) != 0 : true;
         for (int h = 1; on && g + h < p.groups; ++h) {
 #pragma unroll
-            for (int k = 0; k < N; ++k) acc[k] += head[size_t(h) * p.cols * N + k];
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < N; ++e) acc[k][e] += head[(k * N + e) * threads + h * p.cols];
             on = (s_flags[g + h] & kWhole) != 0;
         }
-        if (col >= p.vecs) continue;
-        if (incoming || on)
-            store_floats<float, N>((incoming ? p.head : p.tail) + size_t(blockIdx.x) * p.D + size_t(col) * N, acc);
-        else
-            finish_row<G, N>(p, dtable, cur, col, acc);
+        if (incoming || on) {
+            float *to = (incoming ? p.head : p.tail) + size_t(blockIdx.x) * p.D;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (col0 + k * p.cols < p.vecs) store_floats<float, N>(to + (col0 + k * p.cols) * N, acc[k]);
+            if (!incoming && c == 0 && blockIdx.y == 0) p.list[atomicAdd(&p.st->joins, 1u)] = blockIdx.x;
+        } else {
+            finish_row<G, N, K>(p, dtable, cur, col0, acc);
+        }
     }
     if (c == 0 && blockIdx.y == 0 && (hi == n || g == p.groups - 1)) {
         // the chunk's last walk: one id fills the chunk if every walk is whole
@@ -558,68 +597,65 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumParams p, const T *__
     }
 }
 
-// One CTA for each chunk (and slice of columns): if an id begins in the chunk
-// and goes on after it, adds its sums, walks of threads taking every
-// groups-th chunk and then joining in order.
+// The ids that cross chunks (in whatever order the sums found them: each is
+// its own task, and so is each slice of its columns).  A task's walks of
+// threads take every groups-th chunk and then join in order.
 template <typename G, int N>
-__global__ void __launch_bounds__(kThreads) k_embed_join(SumParams p, int chunks, G *dtable) {
-    __shared__ float s_acc[kThreads * N];
-    start_dependents();
+__global__ void __launch_bounds__(kThreads) k_embed_join(SumParams p, int chunks, int cols, int slices, G *dtable) {
+    __shared__ float s_acc[N][kThreads];
+    __shared__ int s_first;
     wait_for_previous();
-    const int64_t n = p.st->count < p.n ? p.st->count : p.n;
-    const int64_t hi = (int64_t(blockIdx.x) + 1) * p.chunk;
-    if (hi >= n) return;                   // nothing follows
-    if ((p.flags[blockIdx.x] & (kOn | kWhole)) != kOn) return;
-    const uint32_t key = key_at(p, hi - 1);
-    int last = blockIdx.x + 1;             // the first of the chunks after this one that the id does not fill
-    for (;;) {
-        const int q = last + int(threadIdx.x);
-        const bool ends = q >= chunks || !(p.flags[q] & kWhole);
-        const int first = __syncthreads_or(ends) ? 1 : 0;
-        if (first) {
-            // the lowest thread that says so
-            __shared__ int s_first;
+    const int64_t tasks = int64_t(p.st->joins) * slices;
+    const int vecs = p.D / N, groups = kThreads / cols;
+    const int g = threadIdx.x / cols, c = threadIdx.x - g * cols;
+    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const int chunk = int(p.list[task / slices]), col = int(task % slices) * cols + c;
+        const uint32_t key = key_at(p, (int64_t(chunk) + 1) * p.chunk - 1);
+        int last = chunk + 1;              // the first of the chunks after this one that the id does not fill
+        for (;; last += kThreads) {
+            const int q = last + int(threadIdx.x);
+            const bool ends = q >= chunks || !(p.flags[q] & kWhole);
             if (threadIdx.x == 0) s_first = kThreads;
             __syncthreads();
             if (ends) atomicMin(&s_first, int(threadIdx.x));
             __syncthreads();
-            last += s_first;
-            if (last >= chunks) last = chunks - 1;
-            break;
+            const int first = s_first;
+            __syncthreads();
+            if (first < kThreads) {
+                last += first;
+                break;
+            }
         }
-        last += int(blockDim.x);
-    }
-    const int vecs = p.D / N;
-    const int cols = vecs < kThreads ? vecs : kThreads, groups = kThreads / cols;
-    const int g = threadIdx.x / cols, c = threadIdx.x - g * cols;
-    for (int col0 = blockIdx.y * cols; col0 < vecs; col0 += gridDim.y * cols) {
-        const int col = col0 + c;
+        if (last >= chunks) last = chunks - 1;
+        const bool live = g < groups && col < vecs;
         float acc[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) acc[k] = 0.0f;
-        if (g < groups && col < vecs) {
-            if (g == 0)
+        if (live) {
+            if (g == 0) {
+                const Vec<float, N> x = load_vec<float, N>(p.tail + size_t(chunk) * p.D + col * N);
 #pragma unroll
-                for (int k = 0; k < N; ++k) acc[k] = p.tail[size_t(blockIdx.x) * p.D + col * N + k];
-#pragma unroll 4
-            for (int q = blockIdx.x + 1 + g; q <= last; q += groups) {
+                for (int k = 0; k < N; ++k) acc[k] = x.get(k);
+            }
+#pragma unroll 8
+            for (int q = chunk + 1 + g; q <= last; q += groups) {
                 const Vec<float, N> x = load_vec<float, N>(p.head + size_t(q) * p.D + col * N);
 #pragma unroll
                 for (int k = 0; k < N; ++k) acc[k] += x.get(k);
             }
         }
-        __syncthreads();
 #pragma unroll
-        for (int k = 0; k < N; ++k) s_acc[threadIdx.x * N + k] = acc[k];
+        for (int k = 0; k < N; ++k) s_acc[k][threadIdx.x] = acc[k];
         __syncthreads();
-        if (g == 0 && col < vecs) {
+        if (live && g == 0) {
             for (int h = 1; h < groups; ++h)
 #pragma unroll
-                for (int k = 0; k < N; ++k) acc[k] += s_acc[(h * cols + c) * N + k];
+                for (int k = 0; k < N; ++k) acc[k] += s_acc[k][h * cols + c];
 #pragma unroll
             for (int k = 0; k < N; ++k)
                 dtable[int64_t(key) * p.out_stride + col * N + k] = from_float<G>(acc[k] * p.scale);
         }
+        __syncthreads();
     }
 }
 
@@ -637,9 +673,9 @@ int bits_of(int64_t v) {                   // of the numbers below v
 
 // Passes over `bits` bits of the key, and the bits of each.
 int passes_of(int bits) { return bits < 1 ? 1 : (bits + kMaxBits - 1) / kMaxBits; }
-int digit_of(int bits) {                   // 6, 8 or 10
-    const int p = passes_of(bits), b = (bits + p - 1) / p;
-    return b <= 6 ? 6 : (b <= 8 ? 8 : 10);
+int digit_of(int bits) {                   // 6 or 8 (10 would spare a pass of 17 to 20 bits, and takes
+    const int p = passes_of(bits);         // twice the time in each: 2M ids, 27 us against 14)
+    return (bits + p - 1) / p <= 6 ? 6 : 8;
 }
 
 struct SumShape {
@@ -650,11 +686,16 @@ struct SumShape {
 // Columns over threads: a row's vectors side by side, as many walks as fit in
 // a CTA.  A walk is as long as leaves about eight CTAs an SM, or a little
 // longer where that spares the join.
+// Vectors of a row in one thread, so that what each word costs beside its
+// values (its key, its place) is spread over a few of them.
+constexpr int vectors_of(int vec) { return vec >= 4 ? 1 : (vec == 2 ? 2 : 4); }
+
 SumShape sum_shape(int64_t n, int32_t D, int vec) {
     SumShape s;
     s.vecs = D / vec;
-    s.slices = (s.vecs + kThreads - 1) / kThreads;
-    s.cols = (s.vecs + s.slices - 1) / s.slices;
+    const int most = kThreads * vectors_of(vec), own = vectors_of(vec);
+    s.slices = (s.vecs + most - 1) / most;
+    s.cols = ((s.vecs + s.slices - 1) / s.slices + own - 1) / own;
     s.groups = kThreads / s.cols;
     int64_t w = n * s.slices / (int64_t(s.groups) * 152 * 8);
     s.walk = int(w < 8 ? 8 : (w > 64 ? 64 : (w + 7) / 8 * 8));
@@ -667,7 +708,7 @@ SumShape sum_shape(int64_t n, int32_t D, int vec) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct BwdLayout {
-    size_t totals, counts, words, flags, head, tail, total;
+    size_t totals, counts, words, flags, list, head, tail, total;
     int parts;
 };
 
@@ -677,7 +718,7 @@ BwdLayout bwd_layout(int64_t n, int64_t V, int32_t D) {
     L.parts = int((n + kPart - 1) / kPart);
     L.totals = align256(sizeof(SortState));
     L.counts = align256(L.totals + bins * 4);
-    L.words = align256(L.counts + (n > kSmallN ? bins * L.parts * 4 : 0));
+    L.words = align256(L.counts + (n > kSmallN ? bins * ((L.parts + 3) / 4 * 4) * 4 : 0));
     L.flags = align256(L.words + size_t(n) * 16);
     int64_t chunks = 0;                    // of whichever vector width the pointers allow
     for (int vec = 1; vec <= 8; vec *= 2)
@@ -685,7 +726,8 @@ BwdLayout bwd_layout(int64_t n, int64_t V, int32_t D) {
             const SumShape s = sum_shape(n, D, vec);
             if (s.chunks > chunks) chunks = s.chunks;
         }
-    L.head = align256(L.flags + size_t(chunks) * 4);
+    L.list = align256(L.flags + size_t(chunks) * 4);
+    L.head = align256(L.list + size_t(chunks) * 4);
     L.tail = align256(L.head + size_t(chunks) * D * 4);
     L.total = align256(L.tail + size_t(chunks) * D * 4);
     return L;
@@ -753,18 +795,21 @@ void launch_fwd(const void *table, int64_t ts, int64_t V, int32_t D, const void 
 }
 
 template <typename T, typename G, int N>
-void launch_sums(const SumParams &p, const SumShape &sh, const T *dout, G *dtable, cudaStream_t s) {
+void launch_sums(const SumParams &p, const SumShape &sh, const T *dout, G *dtable, int sms, cudaStream_t s) {
     const dim3 grid(unsigned(sh.chunks), unsigned(sh.slices));
     const int threads = sh.groups * sh.cols;
+    constexpr int kOwn = vectors_of(N);
     SS_LAUNCH("k_embed_sum", s,
-              launch_after(k_embed_sum<T, G, N>, grid, threads, size_t(threads) * N * 8 + sh.groups * 4, s, p, dout,
-                           dtable));
+              launch_after(k_embed_sum<T, G, N, kOwn>, grid, threads, size_t(threads) * N * kOwn * 8 + sh.groups * 4, s,
+                           p, dout, dtable));
     if (sh.chunks > 1) {
+        // slices of half a kilobyte: a long chain of sums is spread over eight walks at least
         constexpr int kJoin = N < 4 ? N : 4;
-        const int vecs = p.D / kJoin, cols = vecs < kThreads ? vecs : kThreads;
+        const int vecs = p.D / kJoin, cols = vecs < 32 ? vecs : 32, slices = (vecs + cols - 1) / cols;
+        const int64_t most = sh.chunks * slices;
         SS_LAUNCH("k_embed_join", s,
-                  launch_after(k_embed_join<G, kJoin>, dim3(unsigned(sh.chunks), unsigned((vecs + cols - 1) / cols)),
-                               kThreads, 0, s, p, int(sh.chunks), dtable));
+                  launch_after(k_embed_join<G, kJoin>, dim3(unsigned(most < sms * 8 ? most : sms * 8)), kThreads, 0, s, p,
+                               int(sh.chunks), cols, slices, dtable));
     }
 }
 
@@ -794,19 +839,19 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
     } else {
         const int bits = bits_of(V), passes = passes_of(bits);
         PassParams p{};
-        p.n = n, p.V = uint32_t(V), p.bits = digit_of(bits), p.parts = L.parts;
+        p.n = n, p.V = uint32_t(V), p.bits = digit_of(bits), p.parts = L.parts, p.row = (L.parts + 3) / 4 * 4;
         p.counts = reinterpret_cast<uint32_t *>(ws + L.counts), p.totals = reinterpret_cast<uint32_t *>(ws + L.totals);
         p.st = st;
-        clear.shares = 3 * passes;
+        const bool scan = p.parts > kFewParts;
+        clear.shares = (scan ? 3 : 2) * passes;
         const int64_t share = bytes / clear.shares;
         const int want = int(share / (32 * 1024) < 1 << 20 ? share / (32 * 1024) : 1 << 20) + 1;
         const int ctas = want < sms * 4 ? want : sms * 4;
         const size_t smem = size_t(kPart) * 8 + (size_t(8) << p.bits) * 2 + (size_t(2) << p.bits) * 4;
-        auto move = p.bits == 6 ? k_embed_move<I, G, 6> : (p.bits == 8 ? k_embed_move<I, G, 8> : k_embed_move<I, G, 10>);
+        auto move = p.bits == 6 ? k_embed_move<I, G, 6> : k_embed_move<I, G, 8>;
         static std::atomic<unsigned long long> smem_ctx[kMaxDevices];
-        const void *fns[] = {(const void *)k_embed_move<I, G, 6>, (const void *)k_embed_move<I, G, 8>,
-                             (const void *)k_embed_move<I, G, 10>};
-        const ss_status e = ensure_dyn_smem(smem_ctx, fns, 3, kPart * 8 + (8 << kMaxBits) * 2 + (2 << kMaxBits) * 4,
+        const void *fns[] = {(const void *)k_embed_move<I, G, 6>, (const void *)k_embed_move<I, G, 8>};
+        const ss_status e = ensure_dyn_smem(smem_ctx, fns, 2, kPart * 8 + (8 << kMaxBits) * 2 + (2 << kMaxBits) * 4,
                                             "ss_embed_bwd");
         if (e != SS_OK) return e;
         for (int d = 0; d < passes; ++d) {
@@ -818,9 +863,11 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
                 SS_LAUNCH("k_embed_count", s,
                           launch_after(k_embed_count<I, G>, dim3(p.parts + ctas), kThreads, 0, s, id, p, clear));
             ++clear.share;
-            SS_LAUNCH("k_embed_scan", s,
-                      launch_after(k_embed_scan<G>, dim3((1 << p.bits) + ctas), kThreads, 0, s, p, clear));
-            ++clear.share;
+            if (scan) {
+                SS_LAUNCH("k_embed_scan", s,
+                          launch_after(k_embed_scan<G>, dim3((1 << p.bits) + ctas), kThreads, 0, s, p, clear));
+                ++clear.share;
+            }
             SS_LAUNCH("k_embed_move", s,
                       launch_after(move, dim3(p.parts + ctas), kThreads, smem, s, id, p, clear));
             ++clear.share;
@@ -843,8 +890,8 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
         p.n = n, p.chunk = sh.chunk, p.V = uint32_t(V), p.D = D, p.walk = sh.walk, p.groups = sh.groups;
         p.cols = sh.cols, p.vecs = sh.vecs, p.in_stride = in_stride, p.out_stride = out_stride, p.scale = scale;
         p.head = reinterpret_cast<float *>(ws + L.head), p.tail = reinterpret_cast<float *>(ws + L.tail);
-        p.flags = reinterpret_cast<uint32_t *>(ws + L.flags);
-        launch_sums<T, G, kN>(p, sh, static_cast<const T *>(dout), dt, s);
+        p.flags = reinterpret_cast<uint32_t *>(ws + L.flags), p.list = reinterpret_cast<uint32_t *>(ws + L.list);
+        launch_sums<T, G, kN>(p, sh, static_cast<const T *>(dout), dt, sms, s);
     };
     if (b == 16) go(std::integral_constant<int, 16 / E>{});
     else if (b == 8) go(std::integral_constant<int, 8 / E>{});
