@@ -70,8 +70,10 @@ constexpr int kPart = 2048;              // ids of one sort partition
 constexpr int kKpt = kPart / kThreads;
 constexpr int kMaxBits = 8;              // of a digit: at most 256 bins
 constexpr int kFewParts = 32;            // partitions whose counts the move adds up itself
-constexpr int kSmallN = 8192;            // ids that one CTA sorts by itself
-constexpr int kSmallThreads = 1024, kSmallKpt = kSmallN / kSmallThreads;
+constexpr int kSmallThreads = 1024;      // of the one CTA that sorts a small batch
+constexpr int kSmallN = 4 * kSmallThreads;         // ids up to which it does,
+constexpr int kSmallMost = 8 * kSmallThreads;      // and up to which it does beside a long clearing
+constexpr int64_t kLongClearing = 32 << 20;        // bytes
 
 struct SortState {
     int64_t count;                       // ids that name a row
@@ -164,17 +166,17 @@ __device__ __forceinline__ void clear_share(const Clearing<G> &c, int cta, int c
         for (int j = threadIdx.x & 31; j < c.D; j += 32) c.p[r * c.stride + j] = from_float<G>(0.0f);
 }
 
-// Up to kSmallN ids: one CTA sorts them in its shared memory, 8 bits a pass,
+// One CTA sorts up to KPT ids a thread in its shared memory, 8 bits a pass,
 // the others clear.
-template <typename I, typename G>
+template <typename I, typename G, int KPT>
 __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__restrict__ ids, int n, uint32_t V,
                                                                     int passes, uint64_t *words, SortState *st,
                                                                     Clearing<G> clear) {
     constexpr int kWarps = kSmallThreads / 32;
     extern __shared__ uint32_t s_small[];
-    uint32_t *s_key = s_small;                                            // [kSmallN]
-    uint16_t *s_pos = reinterpret_cast<uint16_t *>(s_key + kSmallN);      // [kSmallN]
-    uint16_t (*s_hist)[256] = reinterpret_cast<uint16_t (*)[256]>(s_pos + kSmallN);   // [kWarps][256]
+    uint32_t *s_key = s_small;                                            // [KPT * kSmallThreads]
+    uint16_t *s_pos = reinterpret_cast<uint16_t *>(s_key + KPT * kSmallThreads);      // [KPT * kSmallThreads]
+    uint16_t (*s_hist)[256] = reinterpret_cast<uint16_t (*)[256]>(s_pos + KPT * kSmallThreads);   // [kWarps][256]
     __shared__ uint32_t s_warp[kWarps], s_start[256], s_count;
     start_dependents();
     if (blockIdx.x > 0) {
@@ -187,10 +189,10 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
     // every warp has as many ids in turn, and no more than there are: a few
     // hundred take one step of eight
     const int per = (n + kSmallThreads - 1) / kSmallThreads * 32, used = per > 0 ? (n + per - 1) / per : 0;
-    uint32_t key[kSmallKpt], pos[kSmallKpt];
+    uint32_t key[KPT], pos[KPT];
     uint32_t named = 0;
 #pragma unroll
-    for (int j = 0; j < kSmallKpt; ++j) {
+    for (int j = 0; j < KPT; ++j) {
         const int i = j * 32 < per ? warp * per + j * 32 + lane : n;
         key[j] = i < n ? id_key(ids, i, V) : 0u;
         pos[j] = uint32_t(i);
@@ -202,9 +204,9 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
     for (int d = 0; d < passes; ++d) {
         for (int e = tid; e < used * 128; e += kSmallThreads) reinterpret_cast<uint32_t *>(&s_hist[0][0])[e] = 0u;
         __syncthreads();
-        uint32_t rank[kSmallKpt];
+        uint32_t rank[KPT];
 #pragma unroll
-        for (int j = 0; j < kSmallKpt; ++j) {
+        for (int j = 0; j < KPT; ++j) {
             if (j * 32 >= per || warp >= used) break;
             const bool ok = warp * per + j * 32 + lane < n;
             const uint32_t dig = (key[j] >> (8 * d)) & 255u;
@@ -218,18 +220,21 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
         }
         __syncthreads();
         uint32_t total = 0;
-        if (tid < 256)
-#pragma unroll 8
-            for (int w = 0; w < used; ++w) {
-                const uint32_t c = s_hist[w][tid];
-                s_hist[w][tid] = uint16_t(total);
-                total += c;
+        if (tid < 256) {
+            uint32_t c[kWarps];            // all of a bin's counts at once, not one behind the other
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) c[w] = w < used ? s_hist[w][tid] : 0u;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < used) s_hist[w][tid] = uint16_t(total);
+                total += c[w];
             }
+        }
         const uint32_t start = excl_scan(total, s_warp);
         if (tid < 256) s_start[tid] = start;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kSmallKpt; ++j)
+        for (int j = 0; j < KPT; ++j)
             if (j * 32 < per && warp * per + j * 32 + lane < n) {
                 const uint32_t dig = (key[j] >> (8 * d)) & 255u;
                 const uint32_t to = s_start[dig] + s_hist[warp][dig] + rank[j];
@@ -238,14 +243,14 @@ __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__r
             }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kSmallKpt; ++j) {
+        for (int j = 0; j < KPT; ++j) {
             const int i = j * 32 < per ? warp * per + j * 32 + lane : n;
             if (i < n) key[j] = s_key[i], pos[j] = s_pos[i];
         }
         __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < kSmallKpt; ++j) {
+    for (int j = 0; j < KPT; ++j) {
         const int i = j * 32 < per ? warp * per + j * 32 + lane : n;
         if (i < n) words[i] = uint64_t(key[j]) << 32 | pos[j];
     }
@@ -825,17 +830,25 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
     // CTAs that clear: enough to draw on the whole bandwidth where there is much to clear
     const int64_t bytes = V * D * int64_t(sizeof(G));
     const uint64_t *sorted = w[0];
-    if (n <= kSmallN) {
+    if (n <= kSmallN || (n <= kSmallMost && bytes >= kLongClearing)) {
+        // (8000 ids: 22 us in one CTA, 17 in several launches; but 35 against 39 beside 131 MB of clearing)
         const int want = int(bytes / (64 * 1024)) + 1, ctas = want < sms * 2 ? want : sms * 2;
-        constexpr int kSmem = kSmallN * 6 + kSmallThreads / 32 * 512;
-        auto kernel = k_embed_sort_small<I, G>;
-        static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
-        const void *fn = (const void *)kernel;
-        const ss_status e = ensure_dyn_smem(smem_ctx, &fn, 1, kSmem, "ss_embed_bwd");
+        auto go = [&](auto KPT) {
+            constexpr int kKpts = decltype(KPT)::value, kSmem = kKpts * kSmallThreads * 6 + kSmallThreads / 32 * 512;
+            auto kernel = k_embed_sort_small<I, G, kKpts>;
+            static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
+            const void *fn = (const void *)kernel;
+            const ss_status e = ensure_dyn_smem(smem_ctx, &fn, 1, kSmem, "ss_embed_bwd");
+            if (e != SS_OK) return e;
+            SS_LAUNCH("k_embed_sort_small", s,
+                      kernel<<<1 + ctas, kSmallThreads, kSmem, s>>>(id, int(n), uint32_t(V), (bits_of(V + 1) + 7) / 8,
+                                                                    w[0], st, clear));
+            return SS_OK;
+        };
+        const ss_status e = n <= kSmallThreads ? go(std::integral_constant<int, 1>{})
+                                               : (n <= kSmallN ? go(std::integral_constant<int, kSmallN / kSmallThreads>{})
+                                                               : go(std::integral_constant<int, kSmallMost / kSmallThreads>{}));
         if (e != SS_OK) return e;
-        SS_LAUNCH("k_embed_sort_small", s,
-                  kernel<<<1 + ctas, kSmallThreads, kSmem, s>>>(id, int(n), uint32_t(V), (bits_of(V + 1) + 7) / 8, w[0],
-                                                                st, clear));
     } else {
         const int bits = bits_of(V), passes = passes_of(bits);
         PassParams p{};
