@@ -41,9 +41,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it: 0.2 us of host
+# time against 2.9 us, a third of a small call.
+_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -397,23 +402,24 @@ def _dtype(t, name: str) -> int:
 
 def _rows(t, name: str, D: int, n=None):
     """(pointer, row stride) of a [n, D] device tensor with contiguous rows."""
-    if t.dim() != 2 or t.shape[1] != D or (n is not None and t.shape[0] != n):
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != D or (n is not None and shape[0] != n):
         raise ValueError("%s must be [%s, %d] (got %s)" % (name, "n" if n is None else n, D,
-                                                           tuple(t.shape)))
+                                                           tuple(shape)))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     rs, cs = t.stride()
     if cs != 1 and D > 1:
         raise ValueError("%s must have contiguous rows (column stride %d)" % (name, cs))
-    if t.shape[0] <= 1:
-        rs = max(rs, D)      # no second row: any stride will do
     if rs < D:
-        raise ValueError("%s has overlapping rows (row stride %d < %d)" % (name, rs, D))
+        if shape[0] > 1:
+            raise ValueError("%s has overlapping rows (row stride %d < %d)" % (name, rs, D))
+        rs = D               # no second row: any stride will do
     return t.data_ptr(), rs
 
 
 def _vector(t, name: str, size: int, dtype=None) -> int:
-    if t.dim() != 1 or t.shape[0] != size or not t.is_contiguous() or not t.is_cuda:
+    if t.shape != (size,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA vector of %d (got %s)"
                          % (name, size, tuple(t.shape)))
     if dtype is not None and t.dtype != dtype:
