@@ -484,9 +484,9 @@ __device__ __forceinline__ void finish_row(const SumParams &p, G *dtable, uint32
 }
 
 template <typename T, typename G, int N, int K>
-__global__ void __launch_bounds__(kThreads, 4) k_embed_sum(SumParams p, const T *__restrict__ dout, G *dtable) {
+__global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T *__restrict__ dout, G *dtable) {
     extern __shared__ float s_part[];      // head then tail: [K * N][threads], then flags [groups]
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 8;
     const int g = threadIdx.x / p.cols, c = threadIdx.x - g * p.cols;
     const int col0 = blockIdx.y * p.cols * K + c, threads = blockDim.x;
     float *head = s_part + threadIdx.x;
@@ -689,8 +689,9 @@ struct SumShape {
 };
 
 // Columns over threads: a row's vectors side by side, as many walks as fit in
-// a CTA.  A walk is as long as leaves about eight CTAs an SM, or a little
-// longer where that spares the join.
+// a CTA.  A walk is as long as gives every SM its two CTAs once (2M x 48: 120 us
+// for the whole gradient; with walks of a quarter, several CTAs after one
+// another, 127), or a little longer where that spares the join.
 // Vectors of a row in one thread, so that what each word costs beside its
 // values (its key, its place) is spread over a few of them.
 constexpr int vectors_of(int vec) { return vec >= 4 ? 1 : (vec == 2 ? 2 : 4); }
@@ -702,8 +703,8 @@ SumShape sum_shape(int64_t n, int32_t D, int vec) {
     s.slices = (s.vecs + most - 1) / most;
     s.cols = ((s.vecs + s.slices - 1) / s.slices + own - 1) / own;
     s.groups = kThreads / s.cols;
-    int64_t w = n * s.slices / (int64_t(s.groups) * 152 * 8);
-    s.walk = int(w < 8 ? 8 : (w > 64 ? 64 : (w + 7) / 8 * 8));
+    const int64_t w = n * s.slices / (int64_t(s.groups) * 152 * 2);
+    s.walk = int(w < 8 ? 8 : (w > 512 ? 512 : (w + 7) / 8 * 8));
     if (n <= int64_t(s.groups) * 16 && n > int64_t(s.groups) * s.walk) s.walk = 16;   // one chunk: nothing to join
     s.chunk = int64_t(s.groups) * s.walk;
     s.chunks = (n + s.chunk - 1) / s.chunk;
