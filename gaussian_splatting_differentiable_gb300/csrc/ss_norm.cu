@@ -58,7 +58,7 @@ struct Rows {
 };
 
 // Rows ahead by what they take: 16 bytes a vector, thread and tensor.
-constexpr int stages_of(int vectors) { return vectors <= 4 ? 4 : 3; }
+constexpr int stages_of(int vectors) { return vectors <= 2 ? 4 : 3; }
 
 __device__ __forceinline__ void copy16(void *smem, const void *gmem) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(smem))), "l"(gmem)
@@ -261,7 +261,7 @@ __device__ __forceinline__ void weights_of(F2 (&g)[VEC / 2], const float4 *plane
 }
 
 template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
-__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : 3)
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : (SHIFT ? 2 : 3))
     k_norm_fwd(Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, const void *beta, int pdt, float eps,
                Rows<T> y, float *mean, float *rstd) {
     extern __shared__ uint4 s_ring[];    // [stages][NV][threads]
@@ -651,9 +651,12 @@ int period_of(int64_t stride, int bytes) {
 }
 
 // As many CTAs as fit the device at once, and no more than share the rows
-// evenly; a multiple of the period where rows start differently.
+// evenly; a multiple of the period where rows start differently.  `waves`
+// times as many where each would have many rows of few values: the device
+// hands out the later ones as the first end, which evens out what the
+// memory's two halves take (2M x 48 float32: 115 us, 131 in one wave).
 template <typename Tag, typename K>
-int grid_of(K kernel, int threads, size_t smem, int64_t n, int groups, int period, int most, int sms) {
+int grid_of(K kernel, int threads, size_t smem, int64_t n, int groups, int period, int waves, int most, int sms) {
     // the last answer, by what it depends on (one kernel, one architecture)
     static std::atomic<unsigned long long> known{0};
     const unsigned long long key = (unsigned long long)(threads) << 40 | (unsigned long long)(smem) << 8;
@@ -665,6 +668,7 @@ int grid_of(K kernel, int threads, size_t smem, int64_t n, int groups, int perio
         known.store(key | per_sm, std::memory_order_relaxed);
     }
     int64_t fit = int64_t(sms) * per_sm;
+    if (n >= fit * groups * 48) fit *= waves;
     if (fit > most) fit = most;
     const int64_t turns = (n + fit * groups - 1) / (fit * groups);
     int64_t grid = (n + turns * groups - 1) / (turns * groups);
@@ -749,7 +753,7 @@ ss_status fwd_kernel(const FwdArgs &a, const Place &pl, int sms, cudaStream_t s)
     const ss_status st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "ss_layer_norm_fwd");
     if (st != SS_OK) return st;
     const int grid = grid_of<FwdTag<T, VEC, NV, MULTI, SHIFT>>(kernel, threads, smem, a.n, pl.groups,
-                                                               period_of(a.xs, sizeof(T)), 1 << 30, sms);
+                                                               period_of(a.xs, sizeof(T)), MULTI ? 1 : 8, 1 << 30, sms);
     const Rows<const T> x{static_cast<const T *>(a.x), a.xs, true};
     const Rows<T> y{static_cast<T *>(a.y), a.ys, same_start<T>(a.x, a.xs, a.y, a.ys)};
     SS_LAUNCH("k_norm_fwd", s,
@@ -771,7 +775,8 @@ ss_status bwd_kernel(const BwdArgs &a, const Place &pl, int sms, cudaStream_t s)
     const ss_status st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "ss_layer_norm_bwd");
     if (st != SS_OK) return st;
     const int grid = grid_of<BwdTag<T, VEC, NV, MULTI, SHIFT>>(kernel, threads, smem, a.n, pl.groups,
-                                                               period_of(a.xs, sizeof(T)), kMaxParts - kMaxPeriod, sms);
+                                                               period_of(a.xs, sizeof(T)), 1, kMaxParts - kMaxPeriod,
+                                                               sms);
     const Rows<const T> x{static_cast<const T *>(a.x), a.xs, true};
     const Rows<const T> dy{static_cast<const T *>(a.dy), a.dys, same_start<T>(a.x, a.xs, a.dy, a.dys)};
     const Rows<T> dx{static_cast<T *>(a.dx), a.dxs, same_start<T>(a.x, a.xs, a.dx, a.dxs)};
