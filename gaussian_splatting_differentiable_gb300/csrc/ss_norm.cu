@@ -30,22 +30,17 @@ constexpr int32_t kMaxD = 65536;
 // those, so the ring needs no barrier and the copies in flight no registers.
 //
 // Rows need not start on 16-byte boundaries (SHIFT): vectors lie on the
-// boundaries, and element i of vector v is column 8 v + i - mis (4 v + i - mis
-// in float32), mis the row start's distance from the boundary before it.  A
-// group of lanes takes every step-th row with step a multiple of the period
-// after which rows start alike, so its mis, and with it its columns, stay
-// fixed.  Only a vector that would leave the tensor's own span is loaded
-// element by element; a vector that holds other rows' or unused values is
-// loaded whole, masked, and stored element by element (in place, a neighbour
-// may be storing those values: whichever arrive, they are not used).
-constexpr int kPerThread = 16;       // elements of a row in one thread
-constexpr int kMaxRowThreads = 512;
+// boundaries, and the few elements of a row before its first and after its
+// last vector go one to a lane (`extra`).  A group of lanes takes every
+// step-th row with step a multiple of the period after which rows start
+// alike, so its columns stay fixed.
+constexpr int kPerThread = 16;       // elements of a row in one thread's vectors
+constexpr int kMaxRowThreads = 512;  // x 16 = the widest row held in registers
 constexpr int kMaxGroups = 8;        // of two warps at least
-  // x 16 = the widest row held in registers
 
 struct Place {
     int lanes, shift;   // lanes = 1 << shift where !MULTI
-    int vecs;           // vectors that a row may touch
+    int vecs;           // vectors of a row, where it starts on a boundary
     int groups;         // rows side by side in a CTA
 };
 
@@ -102,36 +97,44 @@ __device__ __forceinline__ void clear_sums(float *s_red, int count) {
     for (int e = threadIdx.x; e < count * 2 * K * kRowWarps; e += blockDim.x) s_red[e] = 0.0f;
 }
 
-// Where a thread's vectors lie: its lane, and the row's distance from a
-// boundary (SHIFT).
+// Where a thread's columns lie: vectors lane, lane + lanes, ... of the `vecs`
+// whole ones that begin after `head` elements, and the column `extra` (none:
+// -1).
 struct Cols {
-    int lane, lanes, vecs, mis;
+    int lane, lanes, vecs, head, extra;
     int32_t D;
 };
 
+template <typename T, int VEC, bool SHIFT>
+__device__ __forceinline__ Cols cols_of(const Rows<const T> &x, int64_t row, int lane, const Place &pl, int32_t D) {
+    Cols c{lane, pl.lanes, pl.vecs, 0, -1, D};
+    if (SHIFT) {
+        const int h = int((16 - (reinterpret_cast<uintptr_t>(x.base + row * x.stride) & 15)) & 15) / int(sizeof(T));
+        c.head = h < D ? h : D;
+        c.vecs = (D - c.head) / VEC;
+        const int tail = D - c.head - c.vecs * VEC;
+        c.extra = lane < c.head ? lane : (lane < c.head + tail ? D - tail + lane - c.head : -1);
+    }
+    return c;
+}
+
 // Starts the copies of a row's vectors into this thread's slots (slots `apart`
-// vectors from one another).  p: the row's start; before, after: elements of
-// the tensor's span on either side of it (SHIFT).
+// vectors from one another).  p: the row's start.  A tensor whose rows start
+// otherwise than x's is read element by element.
 template <typename T, int VEC, int NV, bool SHIFT>
-__device__ __forceinline__ void fetch_row(uint4 *slot, int apart, const T *p, bool same, int64_t before, int64_t after,
-                                          const Cols &c) {
+__device__ __forceinline__ void fetch_row(uint4 *slot, int apart, const T *p, bool same, const Cols &c) {
+    if (SHIFT) p += c.head;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int v = c.lane + k * c.lanes;
         if (v >= c.vecs) continue;
-        if (!SHIFT) {
+        if (!SHIFT || same) {
             copy16(slot + k * apart, p + v * VEC);
-            continue;
-        }
-        const int j = v * VEC - c.mis;
-        if (same && j + before >= 0 && j + VEC <= after) {
-            copy16(slot + k * apart, p + j);
         } else {
             Vec<T, VEC> r;
             r.clear();
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (j + i >= 0 && j + i < c.D) r.set(i, p[j + i]);
+            for (int i = 0; i < VEC; ++i) r.set(i, p[v * VEC + i]);
             slot[k * apart] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
         }
     }
@@ -145,50 +148,18 @@ __device__ __forceinline__ Vec<T, VEC> from_slot(const uint4 *slot) {
     return x;
 }
 
-// Whether element i of vector v belongs to the row; whether all of them do.
-template <int VEC, bool SHIFT>
-__device__ __forceinline__ bool in_row(const Cols &c, int v, int i) {
-    return SHIFT ? uint32_t(v * VEC + i - c.mis) < uint32_t(c.D) : v < c.vecs;
-}
-template <int VEC, bool SHIFT>
-__device__ __forceinline__ bool all_in_row(const Cols &c, int v) {
-    return SHIFT ? v * VEC >= c.mis && v * VEC - c.mis + VEC <= c.D : v < c.vecs;
-}
-
-// Zeros what of a vector does not belong to the row.
-template <int VEC, bool SHIFT>
-__device__ __forceinline__ void mask(F2 (&f)[VEC / 2], const Cols &c, int v) {
-    if (all_in_row<VEC, SHIFT>(c, v)) return;
-#pragma unroll
-    for (int i = 0; i < VEC; i += 2) {
-        const float2 q = get_f2(f[i / 2]);
-        f[i / 2] = make_f2(in_row<VEC, SHIFT>(c, v, i) ? q.x : 0.0f, in_row<VEC, SHIFT>(c, v, i + 1) ? q.y : 0.0f);
-    }
-}
-
 template <typename T, int VEC, bool SHIFT>
 __device__ __forceinline__ void store_row(T *p, bool same, int v, const Cols &c, const F2 (&o)[VEC / 2]) {
-    if (!SHIFT) {
-        store_pairs<T, VEC>(p + v * VEC, o);
-        return;
-    }
-    const int j = v * VEC - c.mis;
-    if (same && all_in_row<VEC, SHIFT>(c, v)) {
-        store_pairs<T, VEC>(p + j, o);
+    p += (SHIFT ? c.head : 0) + v * VEC;
+    if (!SHIFT || same) {
+        store_pairs<T, VEC>(p, o);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
             const float2 q = get_f2(o[i / 2]);
-            if (j + i >= 0 && j + i < c.D) p[j + i] = from_float<T>(q.x);
-            if (j + i + 1 >= 0 && j + i + 1 < c.D) p[j + i + 1] = from_float<T>(q.y);
+            p[i] = from_float<T>(q.x), p[i + 1] = from_float<T>(q.y);
         }
     }
-}
-
-// Elements from a 16-byte boundary to row `row`.
-template <typename T>
-__device__ __forceinline__ int row_mis(const Rows<const T> &t, int64_t row) {
-    return int((reinterpret_cast<uintptr_t>(t.base + row * t.stride) & 15) / sizeof(T));
 }
 
 // A thread's weights, in float32 registers; `absent` where there are none.
@@ -221,7 +192,7 @@ __device__ __forceinline__ void load_weights_as(F2 (&g)[NV][VEC / 2], const P *w
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int v = c.lane + k * c.lanes;
-                q[u] = w && in_row<VEC, SHIFT>(c, v, i + u) ? to_float(w[v * VEC + i + u - c.mis]) : absent;
+                q[u] = w && v < c.vecs ? to_float(w[c.head + v * VEC + i + u]) : absent;
             }
             g[k][i / 2] = make_f2(q[0], q[1]);
         }
@@ -235,6 +206,11 @@ __device__ __forceinline__ void load_weights(F2 (&g)[NV][VEC / 2], const void *w
         load_weights_as<VEC, NV, SHIFT>(g, static_cast<const __half *>(w), absent, c);
     else
         load_weights_as<VEC, NV, SHIFT>(g, static_cast<const __nv_bfloat16 *>(w), absent, c);
+}
+
+// The weight of the column `extra`.
+__device__ __forceinline__ float extra_weight(const void *w, int pdt, float absent, const Cols &c) {
+    return w && c.extra >= 0 ? load_param(w, pdt, c.extra) : absent;
 }
 
 // The backward has no registers left for gamma: a thread's vectors lie in
@@ -268,28 +244,30 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][1][kRowWarps];
     constexpr int kStages = stages_of(NV), kHalf = VEC / 2;
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
-    Cols c;
-    c.lanes = pl.lanes, c.vecs = pl.vecs, c.D = D;
-    c.lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
+    const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
     const int64_t step = int64_t(gridDim.x) * pl.groups;
     const int64_t row0 = int64_t(blockIdx.x) * pl.groups + group;
-    c.mis = SHIFT ? row_mis(x, row0) : 0;
+    const Cols c = cols_of<T, VEC, SHIFT>(x, row0, lane, pl, D);
     const int apart = blockDim.x;
     uint4 *slot = s_ring + threadIdx.x;
-    const T *px = x.base + row0 * x.stride;
-    const int64_t xstep = step * x.stride, end = (n - 1) * x.stride + D;
-    int64_t at = row0 * x.stride;          // where the row to fetch starts
+    const T *px = x.base + row0 * x.stride, *pe = px + c.extra;   // the rows to fetch next, whole and its extra
+    const int64_t xstep = step * x.stride;
 #pragma unroll
     for (int q = 0; q < kStages; ++q) {
         if (q < kStages - 1) {
-            if (row0 + q * step < n)
-                fetch_row<T, VEC, NV, SHIFT>(slot + q * NV * apart, apart, px, true, at, end - at, c);
+            if (row0 + q * step < n) fetch_row<T, VEC, NV, SHIFT>(slot + q * NV * apart, apart, px, true, c);
             copies_commit();
-            px += xstep, at += xstep;
+            px += xstep;
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k)       // slots that no copy fills stay zero
             if (c.lane + k * c.lanes >= c.vecs) slot[(q * NV + k) * apart] = make_uint4(0, 0, 0, 0);
+    }
+    float e = 0.0f, ge = 1.0f, be = 0.0f;
+    if (SHIFT) {
+        if (c.extra >= 0 && row0 < n) e = to_float(*pe);
+        ge = extra_weight(gamma, pdt, 1.0f, c), be = extra_weight(beta, pdt, 0.0f, c);
+        pe += xstep;
     }
     F2 g[NV][kHalf], b[NV][kHalf];
     load_weights<VEC, NV, SHIFT>(g, gamma, pdt, 1.0f, c);
@@ -310,33 +288,40 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             widen<T, VEC>(f[k], from_slot<T, VEC>(slot + (stage * NV + k) * apart));
-            if (SHIFT) mask<VEC, SHIFT>(f[k], c, c.lane + k * pl.lanes);
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) acc = add2(acc, f[k][i]);
         }
         const int last = stage == 0 ? kStages - 1 : stage - 1;   // the slots read one row ago
         if (row + (kStages - 1) * step < n)
-            fetch_row<T, VEC, NV, SHIFT>(slot + last * NV * apart, apart, px, true, at, end - at, c);
+            fetch_row<T, VEC, NV, SHIFT>(slot + last * NV * apart, apart, px, true, c);
         copies_commit();
-        px += xstep, at += xstep;
+        px += xstep;
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        float sum[1] = {sum_of(acc)};
+        float sum[1] = {sum_of(acc)}, ec = e;
+        if (SHIFT) {
+            sum[0] += e;
+            if (c.extra >= 0 && row + step < n) e = to_float(*pe);
+            pe += xstep;
+        }
         row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
         const float mu = sum[0] * inv;
         const F2 neg = both(-mu);
         acc = both(0.0f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int v = c.lane + k * pl.lanes;
-            if (v < pl.vecs) {
+            if (c.lane + k * pl.lanes < c.vecs) {
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) f[k][i] = add2(f[k][i], neg);
-                if (SHIFT) mask<VEC, SHIFT>(f[k], c, v);
-#pragma unroll
-                for (int i = 0; i < kHalf; ++i) acc = fma2(f[k][i], f[k][i], acc);
+                for (int i = 0; i < kHalf; ++i) {
+                    f[k][i] = add2(f[k][i], neg);
+                    acc = fma2(f[k][i], f[k][i], acc);
+                }
             }
         }
         sum[0] = sum_of(acc);
+        if (SHIFT && c.extra >= 0) {
+            ec -= mu;
+            sum[0] = fmaf(ec, ec, sum[0]);
+        }
         row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
         const float r = __frsqrt_rn(fmaf(sum[0], inv, eps));
         if (row >= n) continue;
@@ -344,11 +329,12 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = c.lane + k * pl.lanes;
-            if (v >= pl.vecs) continue;
+            if (v >= c.vecs) continue;
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) f[k][i] = fma2(mul2(f[k][i], rr), g[k][i], b[k][i]);
             store_row<T, VEC, SHIFT>(py, y.same, v, c, f[k]);
         }
+        if (SHIFT && c.extra >= 0) py[c.extra] = from_float<T>(fmaf(ec * r, ge, be));
         if (c.lane == 0) {
             if (mean) mean[row] = mu;
             if (rstd) rstd[row] = r;
@@ -367,21 +353,18 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][2][kRowWarps];
     constexpr int kStages = stages_of(2 * NV), kHalf = VEC / 2;
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
-    Cols c;
-    c.lanes = pl.lanes, c.vecs = pl.vecs, c.D = D;
-    c.lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
+    const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
     const int64_t step = int64_t(gridDim.x) * pl.groups;
     const int64_t row0 = int64_t(blockIdx.x) * pl.groups + group;
-    c.mis = SHIFT ? row_mis(x, row0) : 0;
+    const Cols c = cols_of<T, VEC, SHIFT>(x, row0, lane, pl, D);
     const int apart = blockDim.x;
     uint4 *slot = s_ring + threadIdx.x;
     // Row `row` of both tensors into a stage; a row past the last as zeros.
     auto fetch = [&](int stage, int64_t row) {
         uint4 *sd = slot + stage * 2 * NV * apart, *sx = sd + NV * apart;
         if (row < n) {
-            const int64_t ad = row * dy.stride, ax = row * x.stride;
-            fetch_row<T, VEC, NV, SHIFT>(sd, apart, dy.base + ad, dy.same, ad, (n - 1 - row) * dy.stride + D, c);
-            fetch_row<T, VEC, NV, SHIFT>(sx, apart, x.base + ax, true, ax, (n - 1 - row) * x.stride + D, c);
+            fetch_row<T, VEC, NV, SHIFT>(sd, apart, dy.base + row * dy.stride, dy.same, c);
+            fetch_row<T, VEC, NV, SHIFT>(sx, apart, x.base + row * x.stride, true, c);
         } else {
 #pragma unroll
             for (int k = 0; k < 2 * NV; ++k) sd[k * apart] = make_uint4(0, 0, 0, 0);
@@ -390,8 +373,19 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
     };
 #pragma unroll
     for (int q = 0; q < kStages - 1; ++q) fetch(q, row0 + q * step);
-    float mu = 0.0f, r = 0.0f;
-    if (row0 < n) mu = mean[row0], r = rstd[row0];
+    // what a row needs beside its vectors, a row ahead
+    float mu, r, ed = 0.0f, ex = 0.0f;
+    auto load = [&](int64_t row) {
+        mu = r = 0.0f;
+        if (SHIFT) ed = ex = 0.0f;
+        if (row >= n) return;
+        mu = mean[row], r = rstd[row];
+        if (SHIFT && c.extra >= 0)
+            ed = to_float(dy.base[row * dy.stride + c.extra]), ex = to_float(x.base[row * x.stride + c.extra]);
+    };
+    load(row0);
+    const float ge = SHIFT ? extra_weight(gamma, pdt, 1.0f, c) : 1.0f;
+    float dge = 0.0f, dbe = 0.0f;
     float4 *plane = reinterpret_cast<float4 *>(s_ring + kStages * 2 * NV * apart) + threadIdx.x;
     {
         F2 g[NV][kHalf];
@@ -417,15 +411,13 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
         const F2 neg = both(-mu), rr = both(r);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int v = c.lane + k * pl.lanes;
-            if (v < pl.vecs) {
+            if (c.lane + k * pl.lanes < c.vecs) {
                 F2 g[kHalf];
                 widen<T, VEC>(a[k], from_slot<T, VEC>(slot + (stage * 2 * NV + k) * apart));
                 widen<T, VEC>(h[k], from_slot<T, VEC>(slot + ((stage * 2 + 1) * NV + k) * apart));
                 weights_of<VEC>(g, plane, apart, k);
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i) h[k][i] = mul2(add2(h[k][i], neg), rr);
-                if (SHIFT) mask<VEC, SHIFT>(a[k], c, v), mask<VEC, SHIFT>(h[k], c, v);
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i) {
                     dg[k][i] = fma2(a[k][i], h[k][i], dg[k][i]);
@@ -436,22 +428,29 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
                 }
             }
         }
-        mu = r = 0.0f;
-        if (row + step < n) mu = mean[row + step], r = rstd[row + step];
+        float sum[2] = {sum_of(s0), sum_of(s1)}, ae = 0.0f, he = 0.0f;
+        const float r0 = r;
+        if (SHIFT && c.extra >= 0) {
+            he = (ex - mu) * r;
+            dge = fmaf(ed, he, dge), dbe += ed;
+            ae = ed * ge;
+            sum[0] += ae, sum[1] = fmaf(ae, he, sum[1]);
+        }
+        load(row + step);
         fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);   // the slots read one row ago
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        float sum[2] = {sum_of(s0), sum_of(s1)};
         row_sum<2, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
         if (row >= n) continue;
         const F2 ma = both(-sum[0] * inv), mah = both(-sum[1] * inv);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = c.lane + k * pl.lanes;
-            if (v >= pl.vecs) continue;
+            if (v >= c.vecs) continue;
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) a[k][i] = mul2(fma2(h[k][i], mah, add2(a[k][i], ma)), rr);
             store_row<T, VEC, SHIFT>(pdx, dx.same, v, c, a[k]);
         }
+        if (SHIFT && c.extra >= 0) pdx[c.extra] = from_float<T>(r0 * (ae - sum[0] * inv - he * (sum[1] * inv)));
     }
     start_dependents();
     if (!part) return;
@@ -485,16 +484,17 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
                 }
         if (fold && (threadIdx.x & 31) >= pl.lanes) continue;
         if (!SHIFT) {
-            if (v < pl.vecs) {
+            if (v < c.vecs) {
                 store_floats<float, VEC>(mine + v * VEC, tg);
                 store_floats<float, VEC>(mine + D + v * VEC, tb);
             }
-        } else {
+        } else if (v < c.vecs) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (in_row<VEC, SHIFT>(c, v, i)) mine[v * VEC + i - c.mis] = tg[i], mine[D + v * VEC + i - c.mis] = tb[i];
+                mine[c.head + v * VEC + i] = tg[i], mine[D + c.head + v * VEC + i] = tb[i];
         }
     }
+    if (SHIFT && c.extra >= 0) mine[c.extra] = dge, mine[D + c.extra] = dbe;
     if (direct) return;
     __syncthreads();
     for (int j = threadIdx.x; j < 2 * D; j += blockDim.x) {
@@ -540,7 +540,7 @@ __device__ __forceinline__ float block_sum(float v, float *s_red) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_norm_fwd_wide(const T *__restrict__ x, int64_t xs, int64_t n, int32_t D,
+__global__ void __launch_bounds__(kThreads) k_norm_fwd_wide(const T *x, int64_t xs, int64_t n, int32_t D,
                                                        const void *gamma, const void *beta, int pdt, float eps, T *y,
                                                        int64_t ys, float *mean, float *rstd) {
     __shared__ float s_red[kThreads / 32];
@@ -623,11 +623,12 @@ int pow2_at_least(int v) {
 
 // Lanes of a row of D elements in vectors of `vec`: a power of two up to a
 // warp while 16 elements a thread hold the row, else whole warps.  At least 4
-// lanes, so that a load touches whole sectors.  Several wide rows share a CTA
-// of about `threads`.
+// lanes, so that a load touches whole sectors, or, where rows start anywhere,
+// one for each element outside the vectors (6 of 32 bits, 14 of 16).
+// Several wide rows share a CTA of about `threads`.
 Place place_of(int32_t D, int vec, int threads, bool shift, bool *multi) {
     Place pl{};
-    pl.vecs = (D + (shift ? vec - 1 : 0) + vec - 1) / vec;
+    pl.vecs = D / vec;
     const int nv = kPerThread / vec;
     const int need = (pl.vecs + nv - 1) / nv;
     *multi = need > 32;
@@ -635,9 +636,10 @@ Place place_of(int32_t D, int vec, int threads, bool shift, bool *multi) {
         pl.lanes = (need + 31) / 32 * 32;
         pl.groups = pl.lanes < threads ? threads / pl.lanes : 1;
     } else {
-        const int most = pow2_at_least(pl.vecs);
+        const int most = pow2_at_least(pl.vecs), most_extra = D < 2 * vec - 2 ? D : 2 * vec - 2,
+                  least = shift ? pow2_at_least(most_extra) : (most < 4 ? most : 4);
         pl.lanes = pow2_at_least(need);
-        if (pl.lanes < 4) pl.lanes = most < 4 ? most : 4;
+        if (pl.lanes < least) pl.lanes = least;
         pl.groups = kThreads / pl.lanes;
     }
     while ((1 << pl.shift) < pl.lanes) ++pl.shift;
@@ -815,9 +817,9 @@ ss_status pick_nv(const Args &a, int sms, cudaStream_t s) {
 
 // The widest row that 512 threads hold, whatever its start.
 template <typename T>
-bool too_wide(int32_t D, bool shift) {
+bool too_wide(int32_t D) {
     constexpr int kVec = 16 / sizeof(T);
-    return (D + (shift ? kVec - 1 : 0) + kVec - 1) / kVec > kMaxRowThreads * (kPerThread / kVec);
+    return D / kVec > kMaxRowThreads * (kPerThread / kVec);
 }
 
 int wide_grid(int64_t n, int sms) { return int(n < int64_t(sms) * 8 ? n : int64_t(sms) * 8); }
@@ -827,7 +829,7 @@ ss_status launch_fwd(const FwdArgs &a, int sms, cudaStream_t s) {
     constexpr int kVec = 16 / sizeof(T);
     const bool shift = !(a.D % kVec == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) && a.xs % kVec == 0 &&
                          a.ys % kVec == 0);
-    if (!too_wide<T>(a.D, shift)) return shift ? pick_nv<T, true>(a, sms, s) : pick_nv<T, false>(a, sms, s);
+    if (!too_wide<T>(a.D)) return shift ? pick_nv<T, true>(a, sms, s) : pick_nv<T, false>(a, sms, s);
     SS_LAUNCH("k_norm_fwd_wide", s,
               k_norm_fwd_wide<T><<<wide_grid(a.n, sms), kThreads, 0, s>>>(
                   static_cast<const T *>(a.x), a.xs, a.n, a.D, a.gamma, a.beta, a.pdt, a.eps, static_cast<T *>(a.y),
@@ -840,7 +842,7 @@ ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
     constexpr int kVec = 16 / sizeof(T);
     const bool shift = !(a.D % kVec == 0 && aligned_to(a.dy, 16) && aligned_to(a.x, 16) && aligned_to(a.dx, 16) &&
                          a.dys % kVec == 0 && a.xs % kVec == 0 && a.dxs % kVec == 0);
-    if (a.n > 0 && !too_wide<T>(a.D, shift)) return shift ? pick_nv<T, true>(a, sms, s) : pick_nv<T, false>(a, sms, s);
+    if (a.n > 0 && !too_wide<T>(a.D)) return shift ? pick_nv<T, true>(a, sms, s) : pick_nv<T, false>(a, sms, s);
     // the weights first: dx may overwrite dy or x
     if (a.dgamma) {
         const dim3 g((a.D + kThreads - 1) / kThreads, unsigned(a.n < 64 ? (a.n < 1 ? 1 : a.n) : 64));

@@ -200,6 +200,19 @@ __device__ __forceinline__ void store_pairs(T *p, const F2 (&f)[N / 2]) {
     store_floats<T, N>(p, o);
 }
 
+// The same marked to leave the caches first (16-byte pieces; others as they are).
+template <typename T, int N>
+__device__ __forceinline__ void store_floats_cs(T *p, const float (&f)[N]) {
+    if constexpr (N * sizeof(T) == 16 && sizeof(T) == 4) {
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
+    } else if constexpr (N * sizeof(T) == 16) {
+        __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
+                                                        pack2<T>(f[6], f[7])));
+    } else {
+        store_floats<T, N>(p, f);
+    }
+}
+
 // One element of a parameter vector whose type is known at run time.
 __device__ __forceinline__ float load_param(const void *p, int dtype, int64_t i) {
     if (dtype == SS_F32) return static_cast<const float *>(p)[i];

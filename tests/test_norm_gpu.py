@@ -181,6 +181,41 @@ def test_backward_without_weights(ss):
     bwd_case(ss, 77, 48, "f32", "f32", 0, 0, affine=False)
 
 
+@pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [1, 9, 48, 257, 1000, 3001])
+def test_tensors_that_start_differently(ss, D, t):
+    """Each tensor with its own offset and stride: the same values as from
+    tensors that all start on boundaries."""
+    import torch
+    r = np.random.default_rng(D)
+    n = 45
+    xv, dv = r.normal(size=(n, D)), r.normal(size=(n, D))
+    plain = [rows(v, t)[0] for v in (xv, dv)]
+    ln = ss.LayerNorm(n, D, dtype=dtype(t))
+    g = torch.as_tensor(1 + 0.3 * r.normal(size=D), device="cuda").float()
+    y = ln.forward(plain[0], g)
+    dx = ln.backward(plain[1], plain[0], g)
+    want = [f64(v) for v in (y, dx, ln.grads["dgamma"], ln.grads["dbeta"])]
+    (_, _, _), (ey, _, _) = fwd_tolerances(f64(plain[0]), f64(g), None, 1e-5, t)
+    x, _ = rows(xv, t, pad=3, offset=1)
+    dy, _ = rows(dv, t, pad=1, offset=2)
+    out, buf = rows(np.zeros((n, D)), t, pad=5, offset=3, fill=-7.0)
+    ss.ss_layer_norm_fwd(x, g, None, ln.eps, out)
+    assert_close(out, want[0], 2 * ey, "y")
+    dg, db = torch.empty_like(g), torch.empty_like(g)
+    ss.ss_layer_norm_bwd(dy, x, g, ln.mean, ln.rstd, out, dg, db, ln.workspace)
+    # two float32 evaluations of sums of at most max(n, D) terms, and two roundings to the type
+    h = (D / 32 + 80) * U32
+    scale = np.abs(f64(ln.rstd))[:, None] * (np.abs(dv) + np.abs(dv).mean(1, keepdims=True)) * 4 * \
+        (1 + np.abs(f64(plain[0])) ** 2)
+    assert_close(out, want[1], 2 * h * scale + 2 * uT(t) * np.abs(want[1]) + TINY[t], "dx")
+    hh = np.abs((f64(plain[0]) - f64(ln.mean)[:, None]) * f64(ln.rstd)[:, None])
+    assert_close(dg, want[2], 2 * (n + 4) * U32 * (np.abs(dv) * hh).sum(0) * 1.01, "dgamma")
+    assert_close(db, want[3], 2 * (n + 4) * U32 * np.abs(dv).sum(0) * 1.01, "dbeta")
+    out.zero_()
+    assert ((buf == 0) | (buf == -7.0)).all()
+
+
 @pytest.mark.parametrize("D", [5, 48, 1001])
 def test_gradient_against_differences(ss, D):
     """The kernel's gradients along a direction against central differences of
