@@ -453,9 +453,11 @@ __global__ void __launch_bounds__(kThreads) k_embed_move(const I *__restrict__ i
 // memory at the end of each, which the thread of the walk where it begins
 // adds in order; one that goes on over chunks leaves them in `head` and
 // `tail`, for k_embed_join.
-enum : uint32_t { kIn = 1u, kOn = 2u, kWhole = 4u };   // of a walk or chunk: its first id
-                                                        // began before it, its last goes on
-                                                        // after it, one id fills it and does both
+// Flags of a walk or chunk: its first id began before it, its last goes on
+// after it, one id fills it and does both; of every kBlock-th walk: one id
+// fills it and the walks up to the next of those.
+enum : uint32_t { kIn = 1u, kOn = 2u, kWhole = 4u, kFilled = 8u };
+constexpr int kBlock = 16;
 struct SumParams {
     const uint64_t *words;   // sorted id << 32 | position
     SortState *st;
@@ -490,13 +492,15 @@ __device__ __forceinline__ void finish_row(const SumParams &p, G *dtable, uint32
 
 template <typename T, typename G, int N, int K>
 __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T *__restrict__ dout, G *dtable) {
-    extern __shared__ float s_part[];      // head then tail: [K * N][threads], then flags [groups]
+    extern __shared__ float s_part[];      // head then tail: [K * N][threads], blocks [K * N][blocks * cols], flags [groups]
     constexpr int kBatch = 8;
     const int g = threadIdx.x / p.cols, c = threadIdx.x - g * p.cols;
     const int col0 = blockIdx.y * p.cols * K + c, threads = blockDim.x;
     float *head = s_part + threadIdx.x;
     float *tail = head + size_t(threads) * K * N;
-    uint32_t *s_flags = reinterpret_cast<uint32_t *>(s_part + size_t(threads) * K * N * 2);
+    const int blocks = (p.groups + kBlock - 1) / kBlock, across = blocks * p.cols;
+    float *s_block = s_part + size_t(threads) * K * N * 2;
+    uint32_t *s_flags = reinterpret_cast<uint32_t *>(s_block + size_t(across) * K * N);
     auto put = [&](float *to, const float (&v)[K][N]) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -572,6 +576,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
     }
     if (c == 0) s_flags[g] = flags;
     __syncthreads();
+    if (p.groups > kBlock) {               // sums of the blocks of walks that one id fills
+        if (g % kBlock == 0 && g + kBlock <= p.groups) {
+            bool whole = true;
+            clear();
+            for (int h = 0; h < kBlock; ++h) {
+                whole = whole && (s_flags[g + h] & kWhole);
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) acc[k][e] += head[(k * N + e) * threads + h * p.cols];
+            }
+            float *to = s_block + g / kBlock * p.cols + c;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < N; ++e) to[(k * N + e) * across] = acc[k][e];
+            if (whole) flags |= kFilled;
+        }
+        __syncthreads();
+        if (c == 0 && (flags & kFilled)) s_flags[g] = flags;
+        __syncthreads();
+    }
     if (lo >= hi) return;
     for (int pass = 0; pass < 2; ++pass) {
         const bool incoming = pass == 0;   // the id that the chunk before began: walk 0's threads
@@ -582,12 +608,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[k][e] = own[(k * N + e) * threads];
         bool on = incoming ? (flags & kWhole) != 0 : true;
-        for (int h = 1; on && g + h < p.groups; ++h) {
+        for (int h = g + 1; on && h < p.groups;) {
+            const uint32_t f = s_flags[h];
+            const bool all = (f & kFilled) != 0;         // a block at a time
+            const float *from = all ? s_block + h / kBlock * p.cols + c : s_part + h * p.cols + c;
+            const int apart = all ? across : threads;
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[k][e] += head[(k * N + e) * threads + h * p.cols];
-            on = (s_flags[g + h] & kWhole) != 0;
+                for (int e = 0; e < N; ++e) acc[k][e] += from[(k * N + e) * apart];
+            on = (f & kWhole) != 0;
+            h += all ? kBlock : 1;
         }
         if (incoming || on) {
             float *to = (incoming ? p.head : p.tail) + size_t(blockIdx.x) * p.D;
@@ -710,7 +741,8 @@ SumShape sum_shape(int64_t n, int32_t D, int vec) {
     s.groups = kThreads / s.cols;
     const int64_t w = n * s.slices / (int64_t(s.groups) * 152 * 2);
     s.walk = int(w < 8 ? 8 : (w > 512 ? 512 : (w + 7) / 8 * 8));
-    if (n <= int64_t(s.groups) * 16 && n > int64_t(s.groups) * s.walk) s.walk = 16;   // one chunk: nothing to join
+    if (n <= int64_t(s.groups) * 32) s.walk = int((n + s.groups * 8 - 1) / (s.groups * 8)) * 8;   // one chunk: no join
+    if (s.walk < 8) s.walk = 8;
     s.chunk = int64_t(s.groups) * s.walk;
     s.chunks = (n + s.chunk - 1) / s.chunk;
     return s;
@@ -812,8 +844,10 @@ void launch_sums(const SumParams &p, const SumShape &sh, const T *dout, G *dtabl
     const dim3 grid(unsigned(sh.chunks), unsigned(sh.slices));
     const int threads = sh.groups * sh.cols;
     constexpr int kOwn = vectors_of(N);
+    const size_t smem = (size_t(threads) * 2 + size_t((sh.groups + kBlock - 1) / kBlock) * sh.cols) * N * kOwn * 4 +
+                        sh.groups * 4;
     SS_LAUNCH("k_embed_sum", s,
-              launch_after(k_embed_sum<T, G, N, kOwn>, grid, threads, size_t(threads) * N * kOwn * 8 + sh.groups * 4, s,
+              launch_after(k_embed_sum<T, G, N, kOwn>, grid, threads, smem, s,
                            p, dout, dtable));
     if (sh.chunks > 1) {
         // slices of half a kilobyte: a long chain of sums is spread over eight walks at least
