@@ -156,8 +156,7 @@ __device__ __forceinline__ void store_row(T *p, bool same, int v, const Cols &c,
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
-            const float2 q = get_f2(o[i / 2]);
-            p[i] = from_float<T>(q.x), p[i + 1] = from_float<T>(q.y);
+            p[i] = from_float<T>(o[i / 2].x), p[i + 1] = from_float<T>(o[i / 2].y);
         }
     }
 }
@@ -181,7 +180,7 @@ __device__ __forceinline__ void load_weights_as(F2 (&g)[NV][VEC / 2], const P *w
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int i = 0; i < VEC; i += 2)
-                g[k][i / 2] = make_f2(q[k][i / kVec].get(i % kVec), q[k][i / kVec].get(i % kVec + 1));
+                g[k][i / 2] = make_float2(q[k][i / kVec].get(i % kVec), q[k][i / kVec].get(i % kVec + 1));
         return;
     }
 #pragma unroll
@@ -194,7 +193,7 @@ __device__ __forceinline__ void load_weights_as(F2 (&g)[NV][VEC / 2], const P *w
                 const int v = c.lane + k * c.lanes;
                 q[u] = w && v < c.vecs ? to_float(w[c.head + v * VEC + i + u]) : absent;
             }
-            g[k][i / 2] = make_f2(q[0], q[1]);
+            g[k][i / 2] = make_float2(q[0], q[1]);
         }
 }
 
@@ -223,7 +222,7 @@ __device__ __forceinline__ void put_weights(float4 *plane, int apart, const F2 (
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i) {
-            const float2 a = get_f2(g[k][2 * i]), b = get_f2(g[k][2 * i + 1]);
+            const F2 a = g[k][2 * i], b = g[k][2 * i + 1];
             plane[(k * (VEC / 4) + i) * apart] = make_float4(a.x, a.y, b.x, b.y);
         }
 }
@@ -232,7 +231,7 @@ __device__ __forceinline__ void weights_of(F2 (&g)[VEC / 2], const float4 *plane
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
         const float4 q = plane[(k * (VEC / 4) + i) * apart];
-        g[2 * i] = make_f2(q.x, q.y), g[2 * i + 1] = make_f2(q.z, q.w);
+        g[2 * i] = make_float2(q.x, q.y), g[2 * i + 1] = make_float2(q.z, q.w);
     }
 }
 
@@ -472,8 +471,8 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
         float tg[VEC], tb[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
-            const float2 qg = get_f2(dg[k][i / 2]), qb = get_f2(db[k][i / 2]);
-            tg[i] = qg.x, tg[i + 1] = qg.y, tb[i] = qb.x, tb[i + 1] = qb.y;
+            tg[i] = dg[k][i / 2].x, tg[i + 1] = dg[k][i / 2].y;
+            tb[i] = db[k][i / 2].x, tb[i + 1] = db[k][i / 2].y;
         }
         if (fold)
 #pragma unroll

@@ -148,54 +148,28 @@ __device__ __forceinline__ void store_floats(T *p, const float (&f)[N]) {
 }
 
 // Two float32 values in a register pair; sums, products and fused products
-// of pairs take one instruction each (PTX add / mul / fma .f32x2).
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 make_f2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 get_f2(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 both(float a) { return make_f2(a, a); }
+// of pairs take one instruction each.
+using F2 = float2;
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ F2 both(float a) { return make_float2(a, a); }
 __device__ __forceinline__ float sum_of(F2 a) {
-    const float2 q = get_f2(a);
-    return q.x + q.y;
+    return a.x + a.y;
 }
 
 // The four words of a vector as pairs of floats, and back.
 template <typename T, int N>
 __device__ __forceinline__ void widen(F2 (&f)[N / 2], const Vec<T, N> &x) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) f[i / 2] = make_f2(x.get(i), x.get(i + 1));
+    for (int i = 0; i < N; i += 2) f[i / 2] = make_float2(x.get(i), x.get(i + 1));
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_pairs(T *p, const F2 (&f)[N / 2]) {
     float o[N];
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        const float2 q = get_f2(f[i / 2]);
-        o[i] = q.x, o[i + 1] = q.y;
+        o[i] = f[i / 2].x, o[i + 1] = f[i / 2].y;
     }
     store_floats<T, N>(p, o);
 }
