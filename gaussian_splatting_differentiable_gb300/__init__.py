@@ -422,23 +422,21 @@ def _vector(t, name: str, size: int, dtype=None) -> int:
     if t.shape != (size,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA vector of %d (got %s)"
                          % (name, size, tuple(t.shape)))
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
     return t.data_ptr()
 
 
 def _ids(ids, n=None):
     """(pointer, bytes of an id)."""
-    if ids.dtype == torch.int64:
-        size = 8
-    elif ids.dtype == torch.int32:
-        size = 4
-    else:
+    size = 8 if ids.dtype is torch.int64 else 4
+    if size == 4 and ids.dtype is not torch.int32:
         raise ValueError("ids must be int32 or int64 (got %s)" % ids.dtype)
-    if ids.dim() != 1 or not ids.is_cuda or not ids.is_contiguous() or \
-            (n is not None and ids.shape[0] != n):
+    shape = ids.shape
+    if len(shape) != 1 or (n is not None and shape[0] != n) or not ids.is_cuda or \
+            not ids.is_contiguous():
         raise ValueError("ids must be a contiguous CUDA vector%s (got %s)"
-                         % ("" if n is None else " of %d" % n, tuple(ids.shape)))
+                         % ("" if n is None else " of %d" % n, tuple(shape)))
     return ids.data_ptr(), size
 
 
@@ -485,28 +483,54 @@ def ss_embed_bwd(dout, ids, scale: float, dtable, workspace, stream=None) -> Non
 
 class Embedding:
     """Buffers of the scaled lookup and its gradient for n ids into a table
-    of V rows of D values: `out` [n, D] and `grad` [V, D]."""
+    of V rows of D values: `out` [n, D] and `grad` [V, D].  They belong to
+    one stream at a time: calls on different streams are the caller's to order.
+    (The methods check what they are given; their own buffers they made.)"""
 
     def __init__(self, n: int, V: int, D: int, scale: float = 1.0, dtype=torch.float32,
                  grad_dtype=None, device="cuda", forward: bool = True, backward: bool = True):
         d = torch.device(device)
         self.n, self.V, self.D, self.scale = n, V, D, float(scale)
-        self.out = torch.empty(n, D, dtype=dtype, device=d) if forward else None
-        self.grad = self.workspace = None
+        self.dtype, self._code = dtype, DTYPE_CODES[dtype]
+        self._out = torch.empty(n, D, dtype=dtype, device=d) if forward else None
+        self._grad = self._workspace = None
         if backward:
             nb = ss_embed_workspace_bytes(n, V, D)
             if nb == 0:
                 raise ValueError("sizes out of range")
-            self.grad = torch.empty(V, D, dtype=grad_dtype or dtype, device=d)
-            self.workspace = _workspace(nb, d)
+            self._grad = torch.empty(V, D, dtype=grad_dtype or dtype, device=d)
+            self._grad_code = DTYPE_CODES[self._grad.dtype]
+            self._workspace = _workspace(nb, d)
+
+    out = property(lambda self: self._out)
+    grad = property(lambda self: self._grad)
+    workspace = property(lambda self: self._workspace)
+
+    def _input(self, t, name: str, rows: int):
+        if t.dtype is not self.dtype:
+            raise ValueError("%s must be %s (got %s)" % (name, self.dtype, t.dtype))
+        return _rows(t, name, self.D, rows)
 
     def forward(self, table, ids, stream=None) -> torch.Tensor:
-        ss_embed_fwd(table, ids, self.scale, self.out, stream)
-        return self.out
+        tp, ts = self._input(table, "table", self.V)
+        idp, idb = _ids(ids, self.n)
+        out = self._out
+        st = _L.ss_embed_fwd(tp, self._code, self.V, self.D, ts, idp, idb, self.n, self.scale,
+                             out.data_ptr(), self.D, _stream(stream))
+        if st:
+            _check(st, "ss_embed_fwd")
+        return out
 
     def backward(self, dout, ids, stream=None) -> torch.Tensor:
-        ss_embed_bwd(dout, ids, self.scale, self.grad, self.workspace, stream)
-        return self.grad
+        dp, ds = self._input(dout, "dout", self.n)
+        idp, idb = _ids(ids, self.n)
+        grad, ws = self._grad, self._workspace
+        st = _L.ss_embed_bwd(dp, self._code, ds, idp, idb, self.n, self.V, self.D, self.scale,
+                             grad.data_ptr(), self._grad_code, self.D, ws.data_ptr(), ws.nbytes,
+                             _stream(stream))
+        if st:
+            _check(st, "ss_embed_bwd")
+        return grad
 
 
 # ---- layer norm (ss_norm.h)
@@ -581,37 +605,74 @@ def ss_layer_norm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace,
 
 class LayerNorm:
     """Buffers of the layer norm of n rows of D values: `y`, `mean`, `rstd`
-    of the forward, `dx` and `grads` (dgamma, dbeta) of the backward."""
+    of the forward, `dx` and `grads` (dgamma, dbeta) of the backward.  They
+    belong to one stream at a time, as Embedding's do.  param_dtype is that of
+    gamma, beta and their gradients."""
 
     def __init__(self, n: int, D: int, eps: float = 1e-5, dtype=torch.float32,
                  param_dtype=torch.float32, device="cuda", forward: bool = True,
                  backward: bool = True):
         d = torch.device(device)
         self.n, self.D, self.eps = n, D, float(eps)
-        self.y = self.mean = self.rstd = self.dx = self.grads = self.workspace = None
+        self.dtype, self._code = dtype, DTYPE_CODES[dtype]
+        self.param_dtype, self._param_code = param_dtype, DTYPE_CODES[param_dtype]
+        if param_dtype != dtype and param_dtype != torch.float32:
+            raise ValueError("param_dtype must be float32 or the rows' type")
+        self._y = self._mean = self._rstd = self._dx = self._workspace = self.grads = None
         if forward:
-            self.y = torch.empty(n, D, dtype=dtype, device=d)
-            self.mean = torch.empty(n, dtype=torch.float32, device=d)
-            self.rstd = torch.empty(n, dtype=torch.float32, device=d)
+            self._y = torch.empty(n, D, dtype=dtype, device=d)
+            self._mean = torch.empty(n, dtype=torch.float32, device=d)
+            self._rstd = torch.empty(n, dtype=torch.float32, device=d)
         if backward:
             nb = ss_layer_norm_workspace_bytes(n, D)
             if nb == 0:
                 raise ValueError("sizes out of range")
-            self.dx = torch.empty(n, D, dtype=dtype, device=d)
-            self.grads = {k: torch.empty(D, dtype=param_dtype, device=d)
-                          for k in ("dgamma", "dbeta")}
-            self.workspace = _workspace(nb, d)
+            self._dx = torch.empty(n, D, dtype=dtype, device=d)
+            self._dgamma, self._dbeta = (torch.empty(D, dtype=param_dtype, device=d)
+                                         for _ in range(2))
+            self.grads = {"dgamma": self._dgamma, "dbeta": self._dbeta}
+            self._workspace = _workspace(nb, d)
+
+    y = property(lambda self: self._y)
+    mean = property(lambda self: self._mean)
+    rstd = property(lambda self: self._rstd)
+    dx = property(lambda self: self._dx)
+    workspace = property(lambda self: self._workspace)
+
+    def _input(self, t, name: str):
+        if t.dtype is not self.dtype:
+            raise ValueError("%s must be %s (got %s)" % (name, self.dtype, t.dtype))
+        return _rows(t, name, self.D, self.n)
 
     def forward(self, x, gamma=None, beta=None, stream=None) -> torch.Tensor:
-        ss_layer_norm_fwd(x, gamma, beta, self.eps, self.y, self.mean, self.rstd, stream)
-        return self.y
+        xp, xs = self._input(x, "x")
+        D, p = self.D, self.param_dtype
+        gp = None if gamma is None else _vector(gamma, "gamma", D, p)
+        bp = None if beta is None else _vector(beta, "beta", D, p)
+        y = self._y
+        st = _L.ss_layer_norm_fwd(xp, self._code, xs, self.n, D, gp, bp, self._param_code,
+                                  self.eps, y.data_ptr(), D, self._mean.data_ptr(),
+                                  self._rstd.data_ptr(), _stream(stream))
+        if st:
+            _check(st, "ss_layer_norm_fwd")
+        return y
 
     def backward(self, dy, x, gamma=None, mean=None, rstd=None, stream=None) -> torch.Tensor:
         """mean, rstd: the forward's, this object's own if not given."""
-        ss_layer_norm_bwd(dy, x, gamma, self.mean if mean is None else mean,
-                          self.rstd if rstd is None else rstd, self.dx, self.grads["dgamma"],
-                          self.grads["dbeta"], self.workspace, stream)
-        return self.dx
+        dyp, dys = self._input(dy, "dy")
+        xp, xs = self._input(x, "x")
+        n, D = self.n, self.D
+        gp = None if gamma is None else _vector(gamma, "gamma", D, self.param_dtype)
+        mp = self._mean.data_ptr() if mean is None else _vector(mean, "mean", n, torch.float32)
+        rp = self._rstd.data_ptr() if rstd is None else _vector(rstd, "rstd", n, torch.float32)
+        dx, ws = self._dx, self._workspace
+        st = _L.ss_layer_norm_bwd(dyp, dys, xp, xs, self._code, n, D, gp, self._param_code, mp, rp,
+                                  dx.data_ptr(), D, self._dgamma.data_ptr(),
+                                  self._dbeta.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                  _stream(stream))
+        if st:
+            _check(st, "ss_layer_norm_bwd")
+        return dx
 
 
 # ---- gradient norm and clipping (ss_clip.h)

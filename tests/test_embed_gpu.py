@@ -180,6 +180,24 @@ def test_another_stream_and_a_captured_graph(ss):
         assert torch.equal(e.grad, 2 * want)
 
 
+def test_profile_names_the_kernels(ss):
+    """Per-kernel timing sees the launches that overlap as well."""
+    import torch
+    e = ss.Embedding(6000, 50, 16)
+    ids = torch.as_tensor(make_ids(6000, 50, "log", 1), device="cuda")
+    dout = torch.ones(6000, 16, device="cuda")
+    want = e.backward(dout, ids).clone()
+    ss.ss_profile_enable(True)
+    ss.ss_profile_collect()
+    try:
+        e.backward(dout, ids)
+        names = ss.ss_profile_collect()
+    finally:
+        ss.ss_profile_enable(False)
+    assert {"k_embed_count", "k_embed_move", "k_embed_sum"} <= set(names)
+    assert torch.equal(e.grad, want)
+
+
 def test_gradient_against_differences(ss):
     """The lookup is linear: its slope along a direction, through the kernels."""
     import torch
@@ -208,6 +226,12 @@ def test_binding_checks_shapes(ss):
         ss.ss_embed_fwd(torch.zeros(8, 3, device="cuda").t(), ids, 1.0, e.out)
     with pytest.raises(ValueError, match="dout"):
         e.backward(torch.zeros(3, 8, device="cuda"), ids)
+    with pytest.raises(ValueError, match="float32"):
+        e.forward(torch.zeros(3, 8, device="cuda").half(), ids)
+    with pytest.raises(ValueError, match="table"):
+        e.forward(torch.zeros(4, 8, device="cuda"), ids)
+    with pytest.raises(ValueError, match="ids"):
+        e.forward(torch.zeros(3, 8, device="cuda"), ids[:2])
     with pytest.raises(ss.SSError, match="workspace"):
         ss.ss_embed_bwd(torch.zeros(4, 8, device="cuda"), ids, 1.0, e.grad, e.workspace[:256])
     assert dtype("f32") == e.out.dtype

@@ -295,3 +295,16 @@ def test_binding_checks(ss):
                              1e-5, torch.empty_like(h))
     with pytest.raises(ValueError, match="mean"):
         ss.ss_layer_norm_fwd(x, None, None, 1e-5, torch.empty_like(x), torch.zeros(3, device="cuda"))
+    ln = ss.LayerNorm(4, 8)
+    with pytest.raises(ValueError, match="x must be"):
+        ln.forward(x[:3])
+    with pytest.raises(ValueError, match="x must be torch.float32"):
+        ln.forward(x.half())
+    with pytest.raises(ValueError, match="gamma must be torch.float32"):
+        ln.forward(x, torch.zeros(8, device="cuda").half())
+    with pytest.raises(ValueError, match="dy must be"):
+        ln.backward(torch.zeros(4, 7, device="cuda"), x)
+    with pytest.raises(ValueError, match="mean"):
+        ln.backward(x, x, mean=torch.zeros(5, device="cuda"))
+    with pytest.raises(ValueError, match="param_dtype"):
+        ss.LayerNorm(4, 8, dtype=torch.float16, param_dtype=torch.bfloat16)
