@@ -393,11 +393,15 @@ class SsimLoss:
 DTYPE_CODES = {torch.float32: SS_F32, torch.float16: SS_F16, torch.bfloat16: SS_BF16}
 
 
-def _dtype(t, name: str) -> int:
-    code = DTYPE_CODES.get(t.dtype)
+def _code(dtype, name: str) -> int:
+    code = DTYPE_CODES.get(dtype)
     if code is None:
-        raise ValueError("%s must be float32, float16 or bfloat16 (got %s)" % (name, t.dtype))
+        raise ValueError("%s must be float32, float16 or bfloat16 (got %s)" % (name, dtype))
     return code
+
+
+def _dtype(t, name: str) -> int:
+    return _code(t.dtype, name)
 
 
 def _rows(t, name: str, D: int, n=None):
@@ -491,7 +495,7 @@ class Embedding:
                  grad_dtype=None, device="cuda", forward: bool = True, backward: bool = True):
         d = torch.device(device)
         self.n, self.V, self.D, self.scale = n, V, D, float(scale)
-        self.dtype, self._code = dtype, DTYPE_CODES[dtype]
+        self.dtype, self._code = dtype, _code(dtype, "dtype")
         self._out = torch.empty(n, D, dtype=dtype, device=d) if forward else None
         self._grad = self._workspace = None
         if backward:
@@ -499,7 +503,7 @@ class Embedding:
             if nb == 0:
                 raise ValueError("sizes out of range")
             self._grad = torch.empty(V, D, dtype=grad_dtype or dtype, device=d)
-            self._grad_code = DTYPE_CODES[self._grad.dtype]
+            self._grad_code = _code(self._grad.dtype, "grad_dtype")
             self._workspace = _workspace(nb, d)
 
     out = property(lambda self: self._out)
@@ -614,8 +618,8 @@ class LayerNorm:
                  backward: bool = True):
         d = torch.device(device)
         self.n, self.D, self.eps = n, D, float(eps)
-        self.dtype, self._code = dtype, DTYPE_CODES[dtype]
-        self.param_dtype, self._param_code = param_dtype, DTYPE_CODES[param_dtype]
+        self.dtype, self._code = dtype, _code(dtype, "dtype")
+        self.param_dtype, self._param_code = param_dtype, _code(param_dtype, "param_dtype")
         if param_dtype != dtype and param_dtype != torch.float32:
             raise ValueError("param_dtype must be float32 or the rows' type")
         self._y = self._mean = self._rstd = self._dx = self._workspace = self.grads = None

@@ -350,11 +350,12 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
 
 // As the forward, with dy and x of a row in registers; the weights' sums stay
 // in the threads' registers over all of a CTA's rows and leave one partial
-// sum a CTA in `part` [CTAs][2][D] (none where part is NULL).
+// sum a CTA in `part` [CTAs][2][D] (none where part is NULL), or, where one
+// CTA has all rows, the gradients themselves.
 template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : (NV == 1 ? 3 : 2))
     k_norm_bwd(Rows<const T> dy, Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, int pdt,
-               const float *mean, const float *rstd, Rows<T> dx, float *part) {
+               const float *mean, const float *rstd, Rows<T> dx, float *part, void *dgamma, void *dbeta) {
     extern __shared__ uint4 s_ring[];    // [stages][dy | x][NV][threads], then gamma; at the end the sums
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][2][kRowWarps];
     constexpr int kStages = stages_of(2 * NV), kHalf = VEC / 2;
@@ -501,12 +502,16 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
         }
     }
     if (SHIFT && c.extra >= 0) mine[c.extra] = dge, mine[D + c.extra] = dbe;
-    if (direct) return;
     __syncthreads();
+    if (direct && !dgamma) return;
     for (int j = threadIdx.x; j < 2 * D; j += blockDim.x) {
-        float t = 0.0f;
-        for (int w = 0; w < slots; ++w) t += s_sum[size_t(w) * 2 * D + j];
-        part[j] = t;
+        float t = direct ? part[j] : 0.0f;
+        if (!direct)
+            for (int w = 0; w < slots; ++w) t += s_sum[size_t(w) * 2 * D + j];
+        if (dgamma)
+            store_param(j < D ? dgamma : dbeta, pdt, j < D ? j : j - D, t);
+        else
+            part[j] = t;
     }
 }
 
@@ -782,16 +787,21 @@ ss_status bwd_kernel(const BwdArgs &a, const Place &pl, int sms, cudaStream_t s)
     const void *fn = (const void *)kernel;
     const ss_status st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "ss_layer_norm_bwd");
     if (st != SS_OK) return st;
-    const int grid = grid_of<BwdTag<T, VEC, NV, MULTI, SHIFT>>(kernel, threads, smem, a.n, pl.groups,
-                                                               period_of(a.xs, sizeof(T)), 1, kMaxParts - kMaxPeriod,
-                                                               sms);
+    // what one CTA takes at once needs no launch that adds up several CTAs' sums (four turns of one
+    // CTA take longer than that launch: 4 x 8192, 16 us against 8)
+    const bool alone = a.n <= pl.groups;
+    const int grid = alone ? 1
+                           : grid_of<BwdTag<T, VEC, NV, MULTI, SHIFT>>(kernel, threads, smem, a.n, pl.groups,
+                                                                       period_of(a.xs, sizeof(T)), 1,
+                                                                       kMaxParts - kMaxPeriod, sms);
     const Rows<const T> x{static_cast<const T *>(a.x), a.xs, true};
     const Rows<const T> dy{static_cast<const T *>(a.dy), a.dys, same_start<T>(a.x, a.xs, a.dy, a.dys)};
     const Rows<T> dx{static_cast<T *>(a.dx), a.dxs, same_start<T>(a.x, a.xs, a.dx, a.dxs)};
     SS_LAUNCH("k_norm_bwd", s,
               kernel<<<grid, threads, smem, s>>>(dy, x, a.n, a.D, pl, a.gamma, a.pdt, a.mean, a.rstd, dx,
-                                                 a.dgamma ? a.part : nullptr));
-    if (a.dgamma)
+                                                 a.dgamma ? a.part : nullptr, alone ? a.dgamma : nullptr,
+                                                 alone ? a.dbeta : nullptr));
+    if (a.dgamma && !alone)
         SS_LAUNCH("k_norm_bwd_final", s,
                   launch_after(k_norm_bwd_final, dim3((2 * a.D + 31) / 32), 1024, 0, s, a.part, grid, a.D, a.dgamma,
                                a.dbeta, a.pdt));
