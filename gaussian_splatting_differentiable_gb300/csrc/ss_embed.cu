@@ -471,9 +471,11 @@ struct SumParams {
     float *head, *tail;      // [chunks][D]
     uint32_t *flags;         // [chunks]
     uint32_t *list;          // chunks whose last id goes on after them and began in them
+    const void *ids;         // a tiny batch's, sorted by the sum's own CTAs (else NULL)
+    int id_bytes;
 };
 
-__device__ __forceinline__ uint32_t key_at(const SumParams &p, int64_t i) { return uint32_t(p.words[i] >> 32); }
+__device__ __forceinline__ uint32_t key_of(const uint64_t *words, int64_t i) { return uint32_t(words[i] >> 32); }
 
 // Vector k of a thread: column col0 + k * cols (in vectors).
 template <typename G, int N, int K>
@@ -488,6 +490,50 @@ __device__ __forceinline__ void finish_row(const SumParams &p, G *dtable, uint32
         for (int i = 0; i < N; ++i) f[i] = acc[k][i] * p.scale;
         store_floats<G, N>(row + (col0 + k * p.cols) * N, f);
     }
+}
+
+// A tiny batch, one id a thread at most: every CTA of the sum (a slice of the
+// columns) puts the words in order by itself, each word's place being the
+// number of smaller ones, and clears its columns of dtable; the sort's launch
+// and its end are spared.
+constexpr int kTinyN = kThreads;
+constexpr int64_t kTinyClearing = 64 << 10;            // bytes of a slice (192 KB: 13 us against 8)
+template <typename G, int N, int K>
+__device__ __forceinline__ int tiny_sort(const SumParams &p, uint64_t *s_sorted, G *dtable, int g, int col0) {
+    __shared__ uint64_t s_raw[kTinyN];
+    const int t = threadIdx.x, n = int(p.n);
+    uint32_t mine = 0;
+    for (int i = t; i < kTinyN; i += blockDim.x) {      // the CTA may have fewer threads
+        uint64_t w = ~0ull;
+        if (i < n) {
+            const uint32_t key = p.id_bytes == 4 ? id_key(static_cast<const int32_t *>(p.ids), i, p.V)
+                                                 : id_key(static_cast<const int64_t *>(p.ids), i, p.V);
+            w = uint64_t(key) << 32 | uint32_t(i);
+            mine += key < p.V;
+        }
+        s_raw[i] = w;
+    }
+    for (int64_t r = g; r < int64_t(p.V); r += p.groups)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (col0 + k * p.cols < p.vecs) {
+                const float zero[N] = {};
+                store_floats<G, N>(dtable + r * p.out_stride + (col0 + k * p.cols) * N, zero);
+            }
+    __syncthreads();                       // the words are there, and the rows cleared before any is summed
+    for (int i = t; i < n; i += blockDim.x) {
+        const uint64_t w = s_raw[i];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) place += s_raw[j] < w;
+        s_sorted[place] = w;
+    }
+    __shared__ int s_count;
+    if (t == 0) s_count = 0;
+    __syncthreads();
+    if (mine) atomicAdd(&s_count, int(mine));
+    __syncthreads();
+    return s_count;
 }
 
 template <typename T, typename G, int N, int K>
@@ -507,9 +553,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
 #pragma unroll
             for (int i = 0; i < N; ++i) to[(k * N + i) * threads] = v[k][i];
     };
-    start_dependents();
-    wait_for_previous();
-    const int64_t n = p.st->count < p.n ? p.st->count : p.n;
+    __shared__ uint64_t s_sorted[kTinyN];
+    const uint64_t *words = p.words;
+    int64_t n;
+    if (p.ids) {
+        n = tiny_sort<G, N, K>(p, s_sorted, dtable, g, col0);
+        words = s_sorted;
+    } else {
+        start_dependents();
+        wait_for_previous();
+        n = p.st->count < p.n ? p.st->count : p.n;
+    }
     const int64_t lo = int64_t(blockIdx.x) * p.chunk + int64_t(g) * p.walk;
     const int64_t hi = lo + p.walk < n ? lo + p.walk : n;
     uint32_t flags = 0, cur = 0;
@@ -524,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
     if (lo < hi) {
         uint64_t w[kBatch];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) w[u] = lo + u < hi ? p.words[lo + u] : ~0ull;
+        for (int u = 0; u < kBatch; ++u) w[u] = lo + u < hi ? words[lo + u] : ~0ull;
         cur = uint32_t(w[0] >> 32);
-        bool open = lo > 0 && key_at(p, lo - 1) == cur;   // the current id began before this walk
-        const uint32_t after = hi < n ? key_at(p, hi) : p.V;
+        bool open = lo > 0 && key_of(words, lo - 1) == cur;   // the current id began before this walk
+        const uint32_t after = hi < n ? key_of(words, hi) : p.V;
         flags = open ? kIn : 0u;
         for (int64_t i = lo; i < hi; i += kBatch) {
             Vec<T, N> x[kBatch][K];
@@ -546,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)              // the next words, while the rows arrive
-                w[u] = i + kBatch + u < hi ? p.words[i + kBatch + u] : ~0ull;
+                w[u] = i + kBatch + u < hi ? words[i + kBatch + u] : ~0ull;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 if (i + u >= hi) break;
@@ -630,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
             finish_row<G, N, K>(p, dtable, cur, col0, acc);
         }
     }
-    if (c == 0 && blockIdx.y == 0 && (hi == n || g == p.groups - 1)) {
+    if (c == 0 && blockIdx.y == 0 && !p.ids && (hi == n || g == p.groups - 1)) {
         // the chunk's last walk: one id fills the chunk if every walk is whole
         bool whole = true;
         for (int h = 0; h <= g; ++h) whole = whole && (s_flags[h] & kWhole);
@@ -651,7 +705,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(SumParams p, int chunks
     const int g = threadIdx.x / cols, c = threadIdx.x - g * cols;
     for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
         const int chunk = int(p.list[task / slices]), col = int(task % slices) * cols + c;
-        const uint32_t key = key_at(p, (int64_t(chunk) + 1) * p.chunk - 1);
+        const uint32_t key = key_of(p.words, (int64_t(chunk) + 1) * p.chunk - 1);
         int last = chunk + 1;              // the first of the chunks after this one that the id does not fill
         for (;; last += kThreads) {
             const int q = last + int(threadIdx.x);
@@ -855,6 +909,10 @@ void launch_sums(const SumParams &p, const SumShape &sh, const T *dout, G *dtabl
     constexpr int kOwn = vectors_of(N, sizeof(T));
     const size_t smem = (size_t(threads) * 2 + size_t((sh.groups + kBlock - 1) / kBlock) * sh.cols) * N * kOwn * 4 +
                         sh.groups * 4;
+    if (p.ids) {                           // waits for all that is before it: it has no sort to overlap
+        SS_LAUNCH("k_embed_sum", s, k_embed_sum<T, G, N, kOwn><<<grid, threads, smem, s>>>(p, dout, dtable));
+        return;
+    }
     SS_LAUNCH("k_embed_sum", s,
               launch_after(k_embed_sum<T, G, N, kOwn>, grid, threads, smem, s,
                            p, dout, dtable));
@@ -878,6 +936,40 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
     G *dt = static_cast<G *>(dtable);
     uint64_t *w[2] = {reinterpret_cast<uint64_t *>(ws + L.words), reinterpret_cast<uint64_t *>(ws + L.words) + n};
     Clearing<G> clear{dt, V, out_stride, D, 0, 1};
+    // the gradient's rows are written in the vectors that dout's are read in (of 32 bytes in two halves)
+    constexpr int E = sizeof(T);
+    int b = access_bytes(dout, in_stride * E, dout, in_stride * E, int64_t(D) * E);
+    for (; b > E; b /= 2) {
+        const int64_t a = int64_t(b) / E * int64_t(sizeof(G)) < 16 ? int64_t(b) / E * int64_t(sizeof(G)) : 16;
+        if (aligned_to(dtable, size_t(a)) && (out_stride * int64_t(sizeof(G))) % a == 0) break;
+    }
+    auto with_vector = [&](auto f) {
+        if (b == 16) return f(std::integral_constant<int, 16 / E>{});
+        if (b == 8) return f(std::integral_constant<int, 8 / E>{});
+        if (b == 4 && E == 2) return f(std::integral_constant<int, E == 2 ? 2 : 1>{});
+        return f(std::integral_constant<int, 1>{});
+    };
+    auto sums = [&](const uint64_t *sorted, bool tiny) {
+        return with_vector([&](auto NE) {
+            constexpr int kN = decltype(NE)::value;
+            const SumShape sh = sum_shape(n, D, kN, E);
+            SumParams p{};
+            p.words = sorted, p.st = st;
+            p.n = n, p.chunk = sh.chunk, p.V = uint32_t(V), p.D = D, p.walk = sh.walk, p.groups = sh.groups;
+            p.cols = sh.cols, p.vecs = sh.vecs, p.in_stride = in_stride, p.out_stride = out_stride, p.scale = scale;
+            p.head = reinterpret_cast<float *>(ws + L.head), p.tail = reinterpret_cast<float *>(ws + L.tail);
+            p.flags = reinterpret_cast<uint32_t *>(ws + L.flags), p.list = reinterpret_cast<uint32_t *>(ws + L.list);
+            p.ids = tiny ? ids : nullptr, p.id_bytes = sizeof(I);
+            launch_sums<T, G, kN>(p, sh, static_cast<const T *>(dout), dt, sms, s);
+            return SS_OK;
+        });
+    };
+    if (n > 0 && n <= kTinyN && with_vector([&](auto NE) {
+            const SumShape sh = sum_shape(n, D, decltype(NE)::value, E);
+            const int64_t width = int64_t(sh.cols) * vectors_of(decltype(NE)::value, E) * decltype(NE)::value;
+            return sh.chunks == 1 && V * width * int64_t(sizeof(G)) <= kTinyClearing;
+        }))
+        return sums(nullptr, true);
     // CTAs that clear: enough to draw on the whole bandwidth where there is much to clear
     const int64_t bytes = V * D * int64_t(sizeof(G));
     const uint64_t *sorted = w[0];
@@ -939,29 +1031,7 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
         sorted = w[(passes - 1) & 1];
     }
     if (n == 0) return SS_OK;
-    constexpr int E = sizeof(T);
-    int b = access_bytes(dout, in_stride * E, dout, in_stride * E, int64_t(D) * E);
-    // the gradient's rows are written in the same vectors (of 32 bytes in two halves)
-    for (; b > E; b /= 2) {
-        const int64_t a = int64_t(b) / E * int64_t(sizeof(G)) < 16 ? int64_t(b) / E * int64_t(sizeof(G)) : 16;
-        if (aligned_to(dtable, size_t(a)) && (out_stride * int64_t(sizeof(G))) % a == 0) break;
-    }
-    auto go = [&](auto NE) {
-        constexpr int kN = decltype(NE)::value;
-        const SumShape sh = sum_shape(n, D, kN, E);
-        SumParams p{};
-        p.words = sorted, p.st = st;
-        p.n = n, p.chunk = sh.chunk, p.V = uint32_t(V), p.D = D, p.walk = sh.walk, p.groups = sh.groups;
-        p.cols = sh.cols, p.vecs = sh.vecs, p.in_stride = in_stride, p.out_stride = out_stride, p.scale = scale;
-        p.head = reinterpret_cast<float *>(ws + L.head), p.tail = reinterpret_cast<float *>(ws + L.tail);
-        p.flags = reinterpret_cast<uint32_t *>(ws + L.flags), p.list = reinterpret_cast<uint32_t *>(ws + L.list);
-        launch_sums<T, G, kN>(p, sh, static_cast<const T *>(dout), dt, sms, s);
-    };
-    if (b == 16) go(std::integral_constant<int, 16 / E>{});
-    else if (b == 8) go(std::integral_constant<int, 8 / E>{});
-    else if (b == 4 && E == 2) go(std::integral_constant<int, E == 2 ? 2 : 1>{});
-    else go(std::integral_constant<int, 1>{});
-    return SS_OK;
+    return sums(sorted, false);
 }
 
 template <typename T, typename G>

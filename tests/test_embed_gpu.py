@@ -114,7 +114,11 @@ BWD = [(0, 5, 8, "f32", "f32", "int64", "uniform", 0, 0),
        (100000, 4096, 16, "f32", "f32", "int64", "same", 0, 0),
        (300000, 4096, 12, "f32", "f32", "int32", "log", 0, 0),
        (120000, 100, 48, "bf16", "f32", "int64", "one", 0, 0),
-       (5, 3, 65536, "f32", "f32", "int64", "uniform", 0, 0)]
+       (5, 3, 65536, "f32", "f32", "int64", "uniform", 0, 0),
+       (256, 5, 8, "f16", "f32", "int32", "absent", 0, 0), (255, 700, 3, "bf16", "bf16", "int64", "one", 2, 1),
+       (257, 700, 3, "bf16", "bf16", "int64", "one", 2, 1), (33, 60, 4096, "f32", "f32", "int64", "log", 0, 0),
+       (32, 7, 4096, "bf16", "bf16", "int64", "same", 0, 0), (100, 16000, 1, "f32", "f32", "int32", "log", 0, 0),
+       (100, 30000, 2, "f16", "f16", "int32", "uniform", 0, 0), (17, 2, 1001, "f16", "f32", "int64", "none", 0, 1)]
 
 
 @pytest.mark.parametrize("case", BWD, ids=lambda c: "-".join(map(str, c)))
