@@ -31,7 +31,7 @@ constexpr int32_t kMaxD = 65536;
 //
 // Rows need not start on 16-byte boundaries (SHIFT): vectors lie on the
 // boundaries, and the few elements of a row before its first and after its
-// last vector go one to a lane (`extra`).  A group of lanes takes every
+// last vector go to the lanes, X at most to each.  A group of lanes takes every
 // step-th row with step a multiple of the period after which rows start
 // alike, so its columns stay fixed.
 constexpr int kPerThread = 16;       // elements of a row in one thread's vectors
@@ -98,22 +98,25 @@ __device__ __forceinline__ void clear_sums(float *s_red, int count) {
 }
 
 // Where a thread's columns lie: vectors lane, lane + lanes, ... of the `vecs`
-// whole ones that begin after `head` elements, and the column `extra` (none:
-// -1).
+// whole ones that begin after `head` elements, and, of the elements before
+// and after them, lane, lane + lanes, ... (column extra(u), -1: none).
 struct Cols {
-    int lane, lanes, vecs, head, extra;
+    int lane, lanes, vecs, head, tail;
     int32_t D;
+    __device__ __forceinline__ int extra(int u) const {
+        const int q = lane + u * lanes;
+        return q < head ? q : (q < head + tail ? D - tail + q - head : -1);
+    }
 };
 
 template <typename T, int VEC, bool SHIFT>
 __device__ __forceinline__ Cols cols_of(const Rows<const T> &x, int64_t row, int lane, const Place &pl, int32_t D) {
-    Cols c{lane, pl.lanes, pl.vecs, 0, -1, D};
+    Cols c{lane, pl.lanes, pl.vecs, 0, 0, D};
     if (SHIFT) {
         const int h = int((16 - (reinterpret_cast<uintptr_t>(x.base + row * x.stride) & 15)) & 15) / int(sizeof(T));
         c.head = h < D ? h : D;
         c.vecs = (D - c.head) / VEC;
-        const int tail = D - c.head - c.vecs * VEC;
-        c.extra = lane < c.head ? lane : (lane < c.head + tail ? D - tail + lane - c.head : -1);
+        c.tail = D - c.head - c.vecs * VEC;
     }
     return c;
 }
@@ -207,9 +210,9 @@ __device__ __forceinline__ void load_weights(F2 (&g)[NV][VEC / 2], const void *w
         load_weights_as<VEC, NV, SHIFT>(g, static_cast<const __nv_bfloat16 *>(w), absent, c);
 }
 
-// The weight of the column `extra`.
-__device__ __forceinline__ float extra_weight(const void *w, int pdt, float absent, const Cols &c) {
-    return w && c.extra >= 0 ? load_param(w, pdt, c.extra) : absent;
+// The weight of a column (-1: none).
+__device__ __forceinline__ float weight_of(const void *w, int pdt, float absent, int col) {
+    return w && col >= 0 ? load_param(w, pdt, col) : absent;
 }
 
 // The backward has no registers left for gamma: a thread's vectors lie in
@@ -238,17 +241,18 @@ __device__ __forceinline__ void weights_of(F2 (&g)[VEC / 2], const float4 *plane
 // CTAs an SM that the registers are held down for: a row's chain of sums is
 // long, and more rows at a time hide it while nothing spills (700,000 x 87
 // bfloat16: 158 us with two, 116 with four).
-constexpr int fwd_ctas(int vec, int nv, bool multi, bool shift) {
-    return multi ? 1 : (nv == 1 ? 4 : (shift && nv * vec > 8 ? 2 : 3));
+constexpr int fwd_ctas(int vec, int nv, bool multi, int x) {
+    return multi ? 1 : (nv == 1 && x <= 2 ? 4 : (x > 0 && nv * vec > 8 ? 2 : 3));
 }
 
-template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
-__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VEC, NV, MULTI, SHIFT))
+template <typename T, int VEC, int NV, bool MULTI, int X>
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VEC, NV, MULTI, X))
     k_norm_fwd(Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, const void *beta, int pdt, float eps,
                Rows<T> y, float *mean, float *rstd) {
     extern __shared__ uint4 s_ring[];    // [stages][NV][threads]
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][1][kRowWarps];
-    constexpr int kStages = stages_of(NV), kHalf = VEC / 2;
+    constexpr bool SHIFT = X > 0;
+    constexpr int kStages = stages_of(NV), kHalf = VEC / 2, kX = SHIFT ? X : 1;
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
     const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
     const int64_t step = int64_t(gridDim.x) * pl.groups;
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
     const Cols c = cols_of<T, VEC, SHIFT>(x, row0, lane, pl, D);
     const int apart = blockDim.x;
     uint4 *slot = s_ring + threadIdx.x;
-    const T *px = x.base + row0 * x.stride, *pe = px + c.extra;   // the rows to fetch next, whole and its extra
+    const T *px = x.base + row0 * x.stride, *pe = px;   // the rows to fetch next: its vectors, its other elements
     const int64_t xstep = step * x.stride;
 #pragma unroll
     for (int q = 0; q < kStages; ++q) {
@@ -269,12 +273,16 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
         for (int k = 0; k < NV; ++k)       // slots that no copy fills stay zero
             if (c.lane + k * c.lanes >= c.vecs) slot[(q * NV + k) * apart] = make_uint4(0, 0, 0, 0);
     }
-    float e = 0.0f, ge = 1.0f, be = 0.0f;
-    if (SHIFT) {
-        if (c.extra >= 0 && row0 < n) e = to_float(*pe);
-        ge = extra_weight(gamma, pdt, 1.0f, c), be = extra_weight(beta, pdt, 0.0f, c);
-        pe += xstep;
+    float e[kX], ge[kX], be[kX];
+    int col[kX];
+#pragma unroll
+    for (int u = 0; u < kX; ++u) {
+        col[u] = SHIFT ? c.extra(u) : -1;
+        e[u] = SHIFT && col[u] >= 0 && row0 < n ? to_float(pe[col[u]]) : 0.0f;
+        ge[u] = SHIFT ? weight_of(gamma, pdt, 1.0f, col[u]) : 1.0f;
+        be[u] = SHIFT ? weight_of(beta, pdt, 0.0f, col[u]) : 0.0f;
     }
+    pe += xstep;
     F2 g[NV][kHalf], b[NV][kHalf];
     load_weights<VEC, NV, SHIFT>(g, gamma, pdt, 1.0f, c);
     load_weights<VEC, NV, SHIFT>(b, beta, pdt, 0.0f, c);
@@ -303,10 +311,14 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
         copies_commit();
         px += xstep;
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        float sum[1] = {sum_of(acc)}, ec = e;
+        float sum[1] = {sum_of(acc)}, ec[kX];
         if (SHIFT) {
-            sum[0] += e;
-            if (c.extra >= 0 && row + step < n) e = to_float(*pe);
+#pragma unroll
+            for (int u = 0; u < kX; ++u) {
+                ec[u] = e[u];
+                sum[0] += e[u];
+                if (col[u] >= 0 && row + step < n) e[u] = to_float(pe[col[u]]);
+            }
             pe += xstep;
         }
         row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
@@ -324,10 +336,12 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
             }
         }
         sum[0] = sum_of(acc);
-        if (SHIFT && c.extra >= 0) {
-            ec -= mu;
-            sum[0] = fmaf(ec, ec, sum[0]);
-        }
+        if (SHIFT)
+#pragma unroll
+            for (int u = 0; u < kX; ++u) {
+                ec[u] = col[u] >= 0 ? ec[u] - mu : 0.0f;
+                sum[0] = fmaf(ec[u], ec[u], sum[0]);
+            }
         row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
         const float r = __frsqrt_rn(fmaf(sum[0], inv, eps));
         if (row >= n) continue;
@@ -340,7 +354,10 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
             for (int i = 0; i < kHalf; ++i) f[k][i] = fma2(mul2(f[k][i], rr), g[k][i], b[k][i]);
             store_row<T, VEC, SHIFT>(py, y.same, v, c, f[k]);
         }
-        if (SHIFT && c.extra >= 0) py[c.extra] = from_float<T>(fmaf(ec * r, ge, be));
+        if (SHIFT)
+#pragma unroll
+            for (int u = 0; u < kX; ++u)
+                if (col[u] >= 0) py[col[u]] = from_float<T>(fmaf(ec[u] * r, ge[u], be[u]));
         if (c.lane == 0) {
             if (mean) mean[row] = mu;
             if (rstd) rstd[row] = r;
@@ -352,13 +369,14 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
 // in the threads' registers over all of a CTA's rows and leave one partial
 // sum a CTA in `part` [CTAs][2][D] (none where part is NULL), or, where one
 // CTA has all rows, the gradients themselves.
-template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
-__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : (NV == 1 ? 3 : 2))
+template <typename T, int VEC, int NV, bool MULTI, int X>
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : (NV == 1 && X <= 1 ? 3 : 2))
     k_norm_bwd(Rows<const T> dy, Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, int pdt,
                const float *mean, const float *rstd, Rows<T> dx, float *part, void *dgamma, void *dbeta) {
     extern __shared__ uint4 s_ring[];    // [stages][dy | x][NV][threads], then gamma; at the end the sums
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][2][kRowWarps];
-    constexpr int kStages = stages_of(2 * NV), kHalf = VEC / 2;
+    constexpr bool SHIFT = X > 0;
+    constexpr int kStages = stages_of(2 * NV), kHalf = VEC / 2, kX = SHIFT ? X : 1;
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
     const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
     const int64_t step = int64_t(gridDim.x) * pl.groups;
@@ -381,18 +399,25 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
 #pragma unroll
     for (int q = 0; q < kStages - 1; ++q) fetch(q, row0 + q * step);
     // what a row needs beside its vectors, a row ahead
-    float mu, r, ed = 0.0f, ex = 0.0f;
+    float mu, r, ed[kX], ex[kX], ge[kX], dge[kX], dbe[kX];
+    int col[kX];
+#pragma unroll
+    for (int u = 0; u < kX; ++u) {
+        col[u] = SHIFT ? c.extra(u) : -1;
+        ge[u] = SHIFT ? weight_of(gamma, pdt, 1.0f, col[u]) : 1.0f;
+        dge[u] = dbe[u] = 0.0f;
+    }
     auto load = [&](int64_t row) {
-        mu = r = 0.0f;
-        if (SHIFT) ed = ex = 0.0f;
-        if (row >= n) return;
-        mu = mean[row], r = rstd[row];
-        if (SHIFT && c.extra >= 0)
-            ed = to_float(dy.base[row * dy.stride + c.extra]), ex = to_float(x.base[row * x.stride + c.extra]);
+        const bool here = row < n;
+        mu = here ? mean[row] : 0.0f, r = here ? rstd[row] : 0.0f;
+        if (SHIFT)
+#pragma unroll
+            for (int u = 0; u < kX; ++u) {
+                ed[u] = here && col[u] >= 0 ? to_float(dy.base[row * dy.stride + col[u]]) : 0.0f;
+                ex[u] = here && col[u] >= 0 ? to_float(x.base[row * x.stride + col[u]]) : 0.0f;
+            }
     };
     load(row0);
-    const float ge = SHIFT ? extra_weight(gamma, pdt, 1.0f, c) : 1.0f;
-    float dge = 0.0f, dbe = 0.0f;
     float4 *plane = reinterpret_cast<float4 *>(s_ring + kStages * 2 * NV * apart) + threadIdx.x;
     {
         F2 g[NV][kHalf];
@@ -435,14 +460,16 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
                 }
             }
         }
-        float sum[2] = {sum_of(s0), sum_of(s1)}, ae = 0.0f, he = 0.0f;
+        float sum[2] = {sum_of(s0), sum_of(s1)}, ae[kX], he[kX];
         const float r0 = r;
-        if (SHIFT && c.extra >= 0) {
-            he = (ex - mu) * r;
-            dge = fmaf(ed, he, dge), dbe += ed;
-            ae = ed * ge;
-            sum[0] += ae, sum[1] = fmaf(ae, he, sum[1]);
-        }
+        if (SHIFT)
+#pragma unroll
+            for (int u = 0; u < kX; ++u) {
+                he[u] = col[u] >= 0 ? (ex[u] - mu) * r : 0.0f;
+                dge[u] = fmaf(ed[u], he[u], dge[u]), dbe[u] += ed[u];
+                ae[u] = ed[u] * ge[u];
+                sum[0] += ae[u], sum[1] = fmaf(ae[u], he[u], sum[1]);
+            }
         load(row + step);
         fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);   // the slots read one row ago
         stage = stage == kStages - 1 ? 0 : stage + 1;
@@ -457,7 +484,10 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
             for (int i = 0; i < kHalf; ++i) a[k][i] = mul2(fma2(h[k][i], mah, add2(a[k][i], ma)), rr);
             store_row<T, VEC, SHIFT>(pdx, dx.same, v, c, a[k]);
         }
-        if (SHIFT && c.extra >= 0) pdx[c.extra] = from_float<T>(r0 * (ae - sum[0] * inv - he * (sum[1] * inv)));
+        if (SHIFT)
+#pragma unroll
+            for (int u = 0; u < kX; ++u)
+                if (col[u] >= 0) pdx[col[u]] = from_float<T>(r0 * (ae[u] - sum[0] * inv - he[u] * (sum[1] * inv)));
     }
     start_dependents();
     if (!part) return;
@@ -501,7 +531,10 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
                 mine[c.head + v * VEC + i] = tg[i], mine[D + c.head + v * VEC + i] = tb[i];
         }
     }
-    if (SHIFT && c.extra >= 0) mine[c.extra] = dge, mine[D + c.extra] = dbe;
+    if (SHIFT)
+#pragma unroll
+        for (int u = 0; u < kX; ++u)
+            if (col[u] >= 0) mine[col[u]] = dge[u], mine[D + col[u]] = dbe[u];
     __syncthreads();
     if (direct && !dgamma) return;
     for (int j = threadIdx.x; j < 2 * D; j += blockDim.x) {
@@ -634,10 +667,9 @@ int pow2_at_least(int v) {
 
 // Lanes of a row of D elements in vectors of `vec`: a power of two up to a
 // warp while 16 elements a thread hold the row, else whole warps.  At least 4
-// lanes, so that a load touches whole sectors, or, where rows start anywhere,
-// one for each element outside the vectors (6 of 32 bits, 14 of 16).
+// lanes, so that a load touches whole sectors.
 // Several wide rows share a CTA of about `threads`.
-Place place_of(int32_t D, int vec, int threads, bool shift, bool *multi) {
+Place place_of(int32_t D, int vec, int threads, bool *multi) {
     Place pl{};
     pl.vecs = D / vec;
     const int nv = kPerThread / vec;
@@ -647,8 +679,7 @@ Place place_of(int32_t D, int vec, int threads, bool shift, bool *multi) {
         pl.lanes = (need + 31) / 32 * 32;
         pl.groups = pl.lanes < threads ? threads / pl.lanes : 1;
     } else {
-        const int most = pow2_at_least(pl.vecs), most_extra = D < 2 * vec - 2 ? D : 2 * vec - 2,
-                  least = shift ? pow2_at_least(most_extra) : (most < 4 ? most : 4);
+        const int least = D < 4 ? pow2_at_least(D) : 4;
         pl.lanes = pow2_at_least(need);
         if (pl.lanes < least) pl.lanes = least;
         pl.groups = kThreads / pl.lanes;
@@ -751,21 +782,21 @@ bool same_start(const void *a, int64_t as, const void *b, int64_t bs) {
 
 constexpr int kMaxSmem = 225 * 1024;   // 227 KB less 2 KB of static buffers
 
-template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+template <typename T, int VEC, int NV, bool MULTI, int X>
 struct FwdTag {};
-template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+template <typename T, int VEC, int NV, bool MULTI, int X>
 struct BwdTag {};
 
-template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+template <typename T, int VEC, int NV, bool MULTI, int X>
 ss_status fwd_kernel(const FwdArgs &a, const Place &pl, int sms, cudaStream_t s) {
     const int threads = MULTI ? pl.lanes * pl.groups : kThreads;
     const size_t smem = size_t(stages_of(NV)) * NV * threads * 16;
-    auto kernel = k_norm_fwd<T, VEC, NV, MULTI, SHIFT>;
+    auto kernel = k_norm_fwd<T, VEC, NV, MULTI, X>;
     static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
     const void *fn = (const void *)kernel;
     const ss_status st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "ss_layer_norm_fwd");
     if (st != SS_OK) return st;
-    const int grid = grid_of<FwdTag<T, VEC, NV, MULTI, SHIFT>>(kernel, threads, smem, a.n, pl.groups,
+    const int grid = grid_of<FwdTag<T, VEC, NV, MULTI, X>>(kernel, threads, smem, a.n, pl.groups,
                                                                period_of(a.xs, sizeof(T)), MULTI ? 1 : 8, 1 << 30, sms);
     const Rows<const T> x{static_cast<const T *>(a.x), a.xs, true};
     const Rows<T> y{static_cast<T *>(a.y), a.ys, same_start<T>(a.x, a.xs, a.y, a.ys)};
@@ -774,15 +805,16 @@ ss_status fwd_kernel(const FwdArgs &a, const Place &pl, int sms, cudaStream_t s)
     return SS_OK;
 }
 
-template <typename T, int VEC, int NV, bool MULTI, bool SHIFT>
+template <typename T, int VEC, int NV, bool MULTI, int X>
 ss_status bwd_kernel(const BwdArgs &a, const Place &pl, int sms, cudaStream_t s) {
     const int threads = MULTI ? pl.lanes * pl.groups : kThreads;
     size_t smem = size_t(stages_of(2 * NV)) * 2 * NV * threads * 16 +
                   size_t(NV) * VEC * threads * sizeof(float);   // the ring and gamma
+    constexpr bool SHIFT = X > 0;
     const int slots = MULTI || SHIFT ? pl.groups : kThreads / 32;
     const size_t sums = a.dgamma && !(MULTI && !SHIFT && slots == 1) ? size_t(slots) * 2 * a.D * sizeof(float) : 0;
     if (smem < sums) smem = sums;
-    auto kernel = k_norm_bwd<T, VEC, NV, MULTI, SHIFT>;
+    auto kernel = k_norm_bwd<T, VEC, NV, MULTI, X>;
     static std::atomic<unsigned long long> smem_ctx[kMaxDevices];
     const void *fn = (const void *)kernel;
     const ss_status st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "ss_layer_norm_bwd");
@@ -791,7 +823,7 @@ ss_status bwd_kernel(const BwdArgs &a, const Place &pl, int sms, cudaStream_t s)
     // CTA take longer than that launch: 4 x 8192, 16 us against 8)
     const bool alone = a.n <= pl.groups;
     const int grid = alone ? 1
-                           : grid_of<BwdTag<T, VEC, NV, MULTI, SHIFT>>(kernel, threads, smem, a.n, pl.groups,
+                           : grid_of<BwdTag<T, VEC, NV, MULTI, X>>(kernel, threads, smem, a.n, pl.groups,
                                                                        period_of(a.xs, sizeof(T)), 1,
                                                                        kMaxParts - kMaxPeriod, sms);
     const Rows<const T> x{static_cast<const T *>(a.x), a.xs, true};
@@ -814,21 +846,34 @@ template <typename T, bool SHIFT, typename Args>
 ss_status pick_nv(const Args &a, int sms, cudaStream_t s) {
     constexpr int kVec = 16 / sizeof(T), kNv = kPerThread / kVec;
     bool multi;
-    const Place pl = place_of(a.D, kVec, std::is_same<Args, FwdArgs>::value ? kThreads : kMaxRowThreads, SHIFT, &multi);
+    const Place pl = place_of(a.D, kVec, std::is_same<Args, FwdArgs>::value ? kThreads : kMaxRowThreads, &multi);
     const int nv = (pl.vecs + pl.lanes - 1) / pl.lanes;
-    auto go = [&](auto NV, auto MULTI) {
+    // elements outside the vectors, at most, and how many of them fall to a lane
+    const int others = a.D < 2 * kVec - 2 ? a.D : 2 * kVec - 2, x = (others + pl.lanes - 1) / pl.lanes;
+    auto go = [&](auto NV, auto MULTI, auto X) {
         if constexpr (std::is_same<Args, FwdArgs>::value)
-            return fwd_kernel<T, kVec, decltype(NV)::value, decltype(MULTI)::value, SHIFT>(a, pl, sms, s);
+            return fwd_kernel<T, kVec, decltype(NV)::value, decltype(MULTI)::value, decltype(X)::value>(a, pl, sms, s);
         else
-            return bwd_kernel<T, kVec, decltype(NV)::value, decltype(MULTI)::value, SHIFT>(a, pl, sms, s);
+            return bwd_kernel<T, kVec, decltype(NV)::value, decltype(MULTI)::value, decltype(X)::value>(a, pl, sms, s);
     };
-    if (multi) return go(std::integral_constant<int, kNv>{}, std::true_type{});
-    if (nv <= 1) return go(std::integral_constant<int, 1>{}, std::false_type{});
+    auto narrow = [&](auto NV) {
+        if constexpr (!SHIFT) {
+            return go(NV, std::false_type{}, std::integral_constant<int, 0>{});
+        } else {
+            if (x <= 1) return go(NV, std::false_type{}, std::integral_constant<int, 1>{});
+            if constexpr (kVec == 8) {      // 14 on 4 lanes
+                if (x > 2) return go(NV, std::false_type{}, std::integral_constant<int, 4>{});
+            }
+            return go(NV, std::false_type{}, std::integral_constant<int, 2>{});
+        }
+    };
+    if (multi) return go(std::integral_constant<int, kNv>{}, std::true_type{}, std::integral_constant<int, SHIFT ? 1 : 0>{});
+    if (nv <= 1) return narrow(std::integral_constant<int, 1>{});
     if constexpr (kNv == 4) {
-        if (nv == 3) return go(std::integral_constant<int, 3>{}, std::false_type{});
-        if (nv == 4) return go(std::integral_constant<int, 4>{}, std::false_type{});
+        if (nv == 3) return narrow(std::integral_constant<int, 3>{});
+        if (nv == 4) return narrow(std::integral_constant<int, 4>{});
     }
-    return go(std::integral_constant<int, 2>{}, std::false_type{});
+    return narrow(std::integral_constant<int, 2>{});
 }
 
 // The widest row that 512 threads hold, whatever its start.
