@@ -164,11 +164,18 @@ __device__ __forceinline__ void clear_share(const Clearing<G> &c, int cta, int c
         }
         return;
     }
+    // rows apart from one another: whole rows to a CTA, their elements to its threads in turn
     const int64_t each = (c.rows + parts - 1) / parts;
     const int64_t lo = part * each, hi = lo + each < c.rows ? lo + each : c.rows;
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    for (int64_t r = lo + warp; r < hi; r += warps)
-        for (int j = threadIdx.x & 31; j < c.D; j += 32) c.p[r * c.stride + j] = from_float<G>(0.0f);
+    if (lo >= hi) return;
+    const int dr = int(blockDim.x) / c.D, dj = int(blockDim.x) - dr * c.D;   // a step of blockDim.x elements
+    int64_t r = lo + int(threadIdx.x) / c.D;
+    int j = int(threadIdx.x) % c.D;
+    while (r < hi) {
+        c.p[r * c.stride + j] = from_float<G>(0.0f);
+        r += dr, j += dj;
+        if (j >= c.D) j -= c.D, ++r;
+    }
 }
 
 // One CTA sorts up to KPT ids a thread in its shared memory, 8 bits a pass,
@@ -868,6 +875,9 @@ void launch_fwd_n(const void *table, int64_t ts, int64_t V, int32_t D, const voi
     int shift = 0;                         // up to four vectors a lane, at least 4 lanes, at most a warp
     while ((1 << shift) < 32 && (1 << shift) * 4 < vecs) ++shift;
     while (shift < 2 && (1 << shift) < vecs) ++shift;
+    // too few rows to fill the device so: more lanes, and a row at a time
+    const bool few = (n << shift) < int64_t(kThreads) * 152 * 4;
+    while (few && (1 << shift) < kThreads && (1 << shift) < vecs) ++shift;
     const int nv = (vecs + (1 << shift) - 1) >> shift;
     // what L2 could not keep anyway leaves room in it for the table (2M x 48 float32: 66 us, 72 without)
     const bool leave = n * D * int64_t(sizeof(T)) > kManyBytes;
@@ -883,6 +893,7 @@ void launch_fwd_n(const void *table, int64_t ts, int64_t V, int32_t D, const voi
     // little (700,000 x 87 bfloat16: 120 us with one row, 107 with eight)
     auto rows = [&](auto NV) {
         constexpr int kBytes = decltype(NV)::value * N * int(sizeof(T));
+        if (few) return go(NV, std::integral_constant<int, 1>{});
         go(NV, std::integral_constant<int, (kBytes >= 48 ? 1 : (kBytes >= 24 ? 2 : (kBytes >= 12 ? 4 : 8)))>{});
     };
     if (nv == 1) rows(std::integral_constant<int, 1>{});
@@ -971,7 +982,7 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
         }))
         return sums(nullptr, true);
     // CTAs that clear: enough to draw on the whole bandwidth where there is much to clear
-    const int64_t bytes = V * D * int64_t(sizeof(G));
+    const int64_t row_bytes = int64_t(D) * sizeof(G), bytes = V * (out_stride == D || row_bytes > 64 ? row_bytes : 64);
     const uint64_t *sorted = w[0];
     if (n <= kSmallN || (n <= kSmallMost && bytes >= kLongClearing)) {
         // (8000 ids: 22 us in one CTA, 17 in several launches; but 35 against 39 beside 131 MB of clearing)
