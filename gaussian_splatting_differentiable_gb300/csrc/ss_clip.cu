@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     const int tiles = t.first[t.count], rank = int(cluster.block_rank());
+    auto all_here = cluster.barrier_arrive();       // waited for before a CTA writes into another
     uint4 held[kHeld];
     auto at = [&](int u, auto f) {       // f on this thread's vector of the CTA's u-th tile
         const int tile = u * kCluster + rank;
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     for (int u = 0; u < kHeld; ++u)
         at(u, [&](auto a, int64_t) { sum = plus(sum, squares_of<typename decltype(a)::T>(vector_of(a, u))); });
     sum = block_sum(sum, s_red);
+    cluster.barrier_wait(static_cast<decltype(all_here) &&>(all_here));
     if (threadIdx.x < kCluster) *cluster.map_shared_rank(&s_part[rank], threadIdx.x) = sum;
     cluster.sync();
     sum = s_part[0];
