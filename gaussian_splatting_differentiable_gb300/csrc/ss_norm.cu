@@ -245,6 +245,11 @@ constexpr int fwd_ctas(int vec, int nv, bool multi, int x) {
     return multi ? 1 : (nv == 1 && x <= 2 ? 4 : (x > 0 && nv * vec > 8 ? 2 : 3));
 }
 
+// mean, centred squares and result of a row from registers.  Bound by memory:
+// 2M x 48 float32 (768 MB and the statistics) 114 us, at copy bandwidth (116);
+// 8191 x 4096 bfloat16 29 (20); 8191 x 8192 float32 83 (79); 1,731,207 x 35
+// bfloat16 89 (38: seven of eight rows start off a 16-byte boundary, and their
+// three or four vectors leave up to 14 elements that are loaded one by one).
 template <typename T, int VEC, int NV, bool MULTI, int X>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VEC, NV, MULTI, X))
     k_norm_fwd(Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, const void *beta, int pdt, float eps,
@@ -368,7 +373,11 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
 // As the forward, with dy and x of a row in registers; the weights' sums stay
 // in the threads' registers over all of a CTA's rows and leave one partial
 // sum a CTA in `part` [CTAs][2][D] (none where part is NULL), or, where one
-// CTA has all rows, the gradients themselves.
+// CTA has all rows, the gradients themselves.  8191 x 4096 bfloat16 (201 MB):
+// 42 us, 30 at copy bandwidth; two rows of 256 threads are all that the
+// registers of an SM hold (x, dy and two sums a column, 127 a thread), and 16
+// warps issue every other cycle.  1M x 48 float32 (576 MB): 89 us (86).
+// 76,363 x 48: 10.2, of which the last launch takes 3.
 template <typename T, int VEC, int NV, bool MULTI, int X>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : (NV == 1 && X <= 1 ? 3 : 2))
     k_norm_bwd(Rows<const T> dy, Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, int pdt,
@@ -549,7 +558,8 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
 }
 
 // The CTAs' partial sums of 32 columns of [dgamma | dbeta]: 32 slices of the
-// CTAs side by side, then the slices in order.
+// CTAs side by side, then the slices in order.  Its launch begins while
+// k_norm_bwd ends; bound by latency.
 __global__ void __launch_bounds__(1024) k_norm_bwd_final(const float *part, int parts, int32_t D, void *dgamma,
                                                          void *dbeta, int pdt) {
     __shared__ float s_t[32][33];
@@ -583,6 +593,9 @@ __device__ __forceinline__ float block_sum(float v, float *s_red) {
     return t;
 }
 
+// A CTA a row, which is read three times (the second and third from L1 or L2),
+// an element a thread: rows of more than 8,191 elements have work enough for
+// their latency.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_norm_fwd_wide(const T *x, int64_t xs, int64_t n, int32_t D,
                                                        const void *gamma, const void *beta, int pdt, float eps, T *y,
@@ -629,6 +642,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_weights_wide(const T *__r
     part[size_t(blockIdx.y) * 2 * D + D + j] = db;
 }
 
+// A CTA a row, as in the forward.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows_wide(const T *dy, int64_t dys, const T *x, int64_t xs,
                                                             int64_t n, int32_t D, const void *gamma, int pdt,
