@@ -234,12 +234,13 @@ __device__ __forceinline__ Sum warp_sum(Sum v) {
 
 // Sum over the CTA, the same value in every thread (fixed order).
 constexpr int kWarps = kThreads / 32;
+template <int WARPS = kWarps>
 __device__ __forceinline__ Sum block_sum(Sum v, Sum *s_red) {
     v = warp_sum<16>(v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
     __syncthreads();
-    return warp_sum<kWarps / 2>(s_red[threadIdx.x & (kWarps - 1)]);
+    return warp_sum<WARPS / 2>(s_red[threadIdx.x & (WARPS - 1)]);
 }
 
 // This CTA's squares: plain float32 over a thread's vectors of a tile (at
@@ -290,23 +291,27 @@ __device__ __forceinline__ void scale_tile(const Table<CAP> &t, int tile, float 
 // Gradients of up to 256 KB: one cluster of CTAs holds them in
 // registers between the norm and the scaling, so they are read once and the
 // CTAs meet at the cluster's barrier, which costs a fraction of a grid's.
-// Tiles here are 4 KB, one vector a thread.  Bound by latency, one trip to
-// memory, one over the CTAs' shared memories: 256 splats' gradients, 60 KB,
-// 3.9 us; the three launches of the larger lists took 8.
-constexpr int kCluster = 8, kHeld = 8;
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+// Tiles here are 4 KB, a vector in each thread of a team, and all of a CTA's
+// tiles are on their way at once (in teams of one, with eight tiles after one
+// another, 236 KB took 7.8 us).  Bound by latency, a trip to memory and one
+// over the CTAs' shared memories: 60 KB 3.7 us, 236 KB 5.1; the three launches
+// of larger lists take 4.7, but a call of theirs from Python 7.7, and of this
+// one 6.2.
+constexpr int kCluster = 8, kTeams = 4, kHeld = 2;
+constexpr int kMostHeld = kCluster * kTeams * kHeld;      // tiles
+__global__ void __launch_bounds__(kTeams *kThreads) __cluster_dims__(kCluster, 1, 1)
     k_clip_small(const __grid_constant__ Table<kSmallList> t, float max_norm, float eps, float *result) {
-    __shared__ Sum s_red[kWarps], s_part[kCluster];
+    __shared__ Sum s_red[kTeams * kWarps], s_part[kCluster];
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int tiles = t.first[t.count], rank = int(cluster.block_rank());
+    const int tiles = t.first[t.count], rank = int(cluster.block_rank()), team = threadIdx.x / kThreads;
     auto all_here = cluster.barrier_arrive();       // waited for before a CTA writes into another
     uint4 held[kHeld];
-    auto at = [&](int u, auto f) {       // f on this thread's vector of the CTA's u-th tile
-        const int tile = u * kCluster + rank;
+    auto at = [&](int u, auto f) {       // f on this thread's vector of its team's u-th tile
+        const int tile = (u * kTeams + team) * kCluster + rank;
         if (tile >= tiles) return;
         const int k = tensor_of(t, tile);
-        const int64_t v = int64_t(tile - t.first[k]) * kThreads + threadIdx.x;
+        const int64_t v = int64_t(tile - t.first[k]) * kThreads + threadIdx.x % kThreads;
         if (t.dtype[k] == SS_F32)
             f(Flat<float>(t, k), v);
         else if (t.dtype[k] == SS_F16)
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
 #pragma unroll
     for (int u = 0; u < kHeld; ++u)
         at(u, [&](auto a, int64_t) { sum = plus(sum, squares_of<typename decltype(a)::T>(vector_of(a, u))); });
-    sum = block_sum(sum, s_red);
+    sum = block_sum<kTeams * kWarps>(sum, s_red);
     cluster.barrier_wait(static_cast<decltype(all_here) &&>(all_here));
     if (threadIdx.x < kCluster) *cluster.map_shared_rank(&s_part[rank], threadIdx.x) = sum;
     cluster.sync();
@@ -475,12 +480,12 @@ ss_status run(const char *who, const ss_tensor *h, int32_t n, bool clip, float m
     ss_status st = current_device(&dev, &sms, who);
     if (st != SS_OK) return st;
     float2 *part = static_cast<float2 *>(workspace);
-    if (clip && n <= kSmallList && total <= kCluster * kHeld * (kThreads * 8)) {   // 16 bytes hold 8 at most
+    if (clip && n <= kSmallList && total <= kMostHeld * (kThreads * 8)) {   // 16 bytes hold 8 at most
         Table<kSmallList> t;
         fill(&t, h, 0, n, kThreads * 16);
-        if (t.first[t.count] <= kCluster * kHeld) {
+        if (t.first[t.count] <= kMostHeld) {
             SS_LAUNCH("k_clip_small", s,
-                      k_clip_small<<<kCluster, kThreads, 0, s>>>(t, max_norm, eps, result));
+                      k_clip_small<<<kCluster, kTeams * kThreads, 0, s>>>(t, max_norm, eps, result));
             return check_launch(who);
         }
     }
