@@ -31,42 +31,65 @@ constexpr int64_t kManyBytes = 64 << 20;   // of output, half of L2
 // every row's start and end are aligned to), and ROWS rows at a time so that
 // the ids' loads, and then the rows', wait together.  Bound by the writes of
 // out (and the table's reads where it does not stay in L2): 2M x 48 float32
-// out of 4096 rows (400 MB) 67 us, 61 at copy bandwidth.
-template <typename T, typename I, int N, int NV, int ROWS>
-__global__ void __launch_bounds__(kThreads) k_embed_fwd(const T *__restrict__ table, int64_t ts, int64_t V,
-                                                        const I *__restrict__ ids, int64_t n, float scale, T *out,
-                                                        int64_t os, int shift, int vecs, bool leave) {
-    const int lanes = 1 << shift, lane = threadIdx.x & (lanes - 1);
-    const int64_t row0 = int64_t(blockIdx.x) * ((kThreads >> shift) * ROWS) + (threadIdx.x >> shift);
-    const int rstep = kThreads >> shift;
+// out of 4096 rows (400 MB) 67 to 68 us, 61 at copy bandwidth.
+//
+// Where rows allow only narrow vectors the instructions bound it: a row's
+// pointers and limits are made once, and WARP (a row to a warp) leaves the
+// vectors' distances to the instructions (700,000 x 87 bfloat16: 107 us with
+// all of that worked out for each value, 58 so; in pairs on 4-byte boundaries
+// 80, for the registers and instructions that the rows' ends take).  The
+// registers are held down, or too few rows are on their way at a time (2M x 48
+// float32: 80 us with 45 registers, 68 with 32).
+constexpr int fwd_ctas(int rows, int bytes) { return rows == 1 ? (bytes > 48 ? 6 : 8) : (rows == 2 ? 5 : 4); }
+
+template <typename T, typename I, int N, int NV, int ROWS, bool WARP>
+__global__ void __launch_bounds__(kThreads, fwd_ctas(ROWS, NV * N * int(sizeof(T))))
+    k_embed_fwd(const T *__restrict__ table, int64_t ts, int64_t V, const I *__restrict__ ids, int64_t n, float scale,
+                T *out, int64_t os, int shift, int vecs, bool leave) {
+    const int lanes = WARP ? 32 : 1 << shift, lane = threadIdx.x & (lanes - 1);
+    const int rstep = WARP ? kThreads / 32 : kThreads >> shift;
+    const int64_t row0 = int64_t(blockIdx.x) * (rstep * ROWS) + threadIdx.x / lanes;
     int64_t id[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) id[r] = row0 + r * rstep < n ? int64_t(ids[row0 + r * rstep]) : -1;
-    for (int v0 = lane; v0 < vecs; v0 += lanes * NV) {
+    const T *from[ROWS];
+    T *const to = out + row0 * os + lane * N;
+    const int64_t apart = rstep * os;
+    int named[ROWS];                       // vectors to read of the row: none where the id names no row,
+    float s[ROWS];                         // and zeros times 0, not times the scale
+    const int mine = vecs - lane, left = n - row0 < ROWS * rstep ? int(n - row0) : ROWS * rstep;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const bool here = id[r] >= 0 && id[r] < V;
+        from[r] = table + (here ? id[r] : 0) * ts + lane * N;
+        named[r] = here ? mine : 0;
+        s[r] = here ? scale : 0.0f;
+    }
+    for (int v0 = 0; v0 < mine; v0 += lanes * NV) {
         Vec<T, N> x[ROWS][NV];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 x[r][k].clear();
-                if (id[r] >= 0 && id[r] < V && v0 + k * lanes < vecs)
-                    x[r][k] = load_vec<T, N>(table + id[r] * ts + (v0 + k * lanes) * N);
+                if (v0 + k * lanes < named[r]) x[r][k] = load_vec<T, N>(from[r] + (v0 + k * lanes) * N);
             }
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r)
+        for (int r = 0; r < ROWS; ++r) {
+            if (r * rstep >= left) break;
+            T *row = to + r * apart;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                if (row0 + r * rstep >= n || v0 + k * lanes >= vecs) continue;
-                const bool here = id[r] >= 0 && id[r] < V;    // no row: zeros, not 0 times the scale
                 float f[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = here ? x[r][k].get(i) * scale : 0.0f;
-                T *to = out + (row0 + r * rstep) * os + (v0 + k * lanes) * N;
-                if (leave)
-                    store_floats_cs<T, N>(to, f);
+                for (int i = 0; i < N; ++i) f[i] = x[r][k].get(i) * s[r];
+                if (v0 + k * lanes >= mine) continue;
+                if (N * sizeof(T) == 16 && leave)
+                    store_floats_cs<T, N>(row + (v0 + k * lanes) * N, f);
                 else
-                    store_floats<T, N>(to, f);
+                    store_floats<T, N>(row + (v0 + k * lanes) * N, f);
             }
+        }
     }
 }
 
@@ -906,17 +929,20 @@ void launch_fwd_n(const void *table, int64_t ts, int64_t V, int32_t D, const voi
     auto go = [&](auto NV, auto ROWS) {
         constexpr int kNv = decltype(NV)::value, kRows = decltype(ROWS)::value;
         const int64_t per = int64_t(kThreads >> shift) * kRows;
+        // (a row of a warp that has few of them has three or four vectors a lane)
+        auto kernel = kNv >= 3 && shift == 5 ? k_embed_fwd<T, I, N, kNv, kRows, (kNv >= 3)>
+                                             : k_embed_fwd<T, I, N, kNv, kRows, false>;
         SS_LAUNCH("k_embed_fwd", s,
-                  k_embed_fwd<T, I, N, kNv, kRows><<<unsigned((n + per - 1) / per), kThreads, 0, s>>>(
+                  kernel<<<unsigned((n + per - 1) / per), kThreads, 0, s>>>(
                       static_cast<const T *>(table), ts, V, static_cast<const I *>(ids), n, scale,
                       static_cast<T *>(out), os, shift, vecs, leave));
     };
-    // as many rows at a time as bring a thread some 48 bytes: fewer leave it waiting on the ids for
-    // little (700,000 x 87 bfloat16: 120 us with one row, 107 with eight)
+    // several rows at a time where one brings a thread little to wait for (1M x 33 float16: 53 us with
+    // two; with four, and more registers, 67)
     auto rows = [&](auto NV) {
         constexpr int kBytes = decltype(NV)::value * N * int(sizeof(T));
         if (few) return go(NV, std::integral_constant<int, 1>{});
-        go(NV, std::integral_constant<int, (kBytes >= 48 ? 1 : (kBytes >= 24 ? 2 : (kBytes >= 12 ? 4 : 8)))>{});
+        go(NV, std::integral_constant<int, (kBytes >= 24 ? 1 : (kBytes >= 12 ? 2 : 4))>{});
     };
     if (nv == 1) rows(std::integral_constant<int, 1>{});
     else if (nv == 2) rows(std::integral_constant<int, 2>{});
@@ -931,7 +957,7 @@ void launch_fwd(const void *table, int64_t ts, int64_t V, int32_t D, const void 
     constexpr int E = sizeof(T);
     if (b == 16) launch_fwd_n<T, I, 16 / E>(table, ts, V, D, ids, n, scale, out, os, s);
     else if (b == 8) launch_fwd_n<T, I, 8 / E>(table, ts, V, D, ids, n, scale, out, os, s);
-    else if (b == 4 && E == 2) launch_fwd_n<T, I, E == 2 ? 2 : 1>(table, ts, V, D, ids, n, scale, out, os, s);
+    else if (b == 4) launch_fwd_n<T, I, 4 / E>(table, ts, V, D, ids, n, scale, out, os, s);
     else launch_fwd_n<T, I, 1>(table, ts, V, D, ids, n, scale, out, os, s);
 }
 
