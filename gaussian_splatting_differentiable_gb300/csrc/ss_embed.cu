@@ -594,6 +594,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
     constexpr int kBatch = 8;
     const int g = threadIdx.x / p.cols, c = threadIdx.x - g * p.cols;
     const int col0 = blockIdx.y * p.cols * K + c, threads = blockDim.x;
+    // where a thread's several vectors are read: one past the row's end reads another in its place, and
+    // what it adds up is never stored (with a test for each load 20,000 x 2503 bfloat16 took 88 us, 81 so)
+    const int first = col0 < p.vecs ? col0 * N : 0;
+    int ahead[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) ahead[k] = col0 + k * p.cols < p.vecs ? k * p.cols * N : 0;
     float *head = s_part + threadIdx.x;
     float *tail = head + size_t(threads) * K * N;
     const int blocks = (p.groups + kBlock - 1) / kBlock, across = blocks * p.cols;
@@ -642,12 +648,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
             for (int u = 0; u < kBatch; ++u) {
                 const uint32_t pos = uint32_t(w[u]);
                 key[u] = uint32_t(w[u] >> 32);
-                const T *row = dout + int64_t(pos) * p.in_stride + col0 * N;
+                const T *row = dout + int64_t(pos) * p.in_stride + (K == 1 ? col0 * N : first);
                 const bool here = key[u] < p.V && int64_t(pos) < p.n;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     x[u][k].clear();
-                    if (here && col0 + k * p.cols < p.vecs) x[u][k] = load_once<T, N>(row + k * p.cols * N);
+                    if constexpr (K == 1) {
+                        if (here && col0 < p.vecs) x[u][0] = load_once<T, N>(row);
+                    } else {
+                        if (here) x[u][k] = load_once<T, N>(row + ahead[k]);
+                    }
                 }
             }
 #pragma unroll
