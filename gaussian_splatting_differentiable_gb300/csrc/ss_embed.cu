@@ -547,9 +547,12 @@ __device__ __forceinline__ void finish_row(const SumParams &p, G *dtable, uint32
 // A tiny batch, one id a thread at most: every CTA of the sum (a slice of the
 // columns) puts the words in order by itself, each word's place being the
 // number of smaller ones, and clears its columns of dtable; the sort's launch
-// and its end are spared.
+// and its end are spared (256 x 48 float32 into 1000 rows: 8.3 us with a sort,
+// 6.5 so; 200 x 700 into 1000 rows: 9.8 and 6.1).  The slices are narrow, for
+// short walks and little to clear, but no narrower than a sector.
 constexpr int kTinyN = kThreads;
-constexpr int64_t kTinyClearing = 64 << 10;            // bytes of a slice (192 KB: 13 us against 8)
+constexpr int64_t kTinyClearing = 16 << 10;    // bytes of a slice, if it can be that narrow,
+constexpr int64_t kTinyMost = 64 << 10;        // and at most (128 KB: 10.3 us a call against 9.7; 192 KB: 13 against 8)
 template <typename G, int N, int K>
 __device__ __forceinline__ int tiny_sort(const SumParams &p, uint64_t *s_sorted, G *dtable, int g, int col0) {
     __shared__ uint64_t s_raw[kTinyN];
@@ -576,7 +579,7 @@ __device__ __forceinline__ int tiny_sort(const SumParams &p, uint64_t *s_sorted,
     for (int i = t; i < n; i += blockDim.x) {
         const uint64_t w = s_raw[i];
         int place = 0;
-#pragma unroll 4
+#pragma unroll 16
         for (int j = 0; j < n; ++j) place += s_raw[j] < w;
         s_sorted[place] = w;
     }
@@ -850,11 +853,12 @@ constexpr int vectors_of(int vec, int bytes) {
     return vec >= 4 ? 1 : (vec == 2 && bytes == 4 ? 2 : 4);
 }
 
-SumShape sum_shape(int64_t n, int32_t D, int vec, int bytes) {
+SumShape sum_shape(int64_t n, int32_t D, int vec, int bytes, int slices = 1) {
     SumShape s;
     s.vecs = D / vec;
     const int own = vectors_of(vec, bytes), most = kThreads * own;
     s.slices = (s.vecs + most - 1) / most;
+    if (s.slices < slices) s.slices = slices;
     s.cols = ((s.vecs + s.slices - 1) / s.slices + own - 1) / own;
     s.groups = kThreads / s.cols;
     const int64_t w = n * s.slices / (int64_t(s.groups) * 152 * 2);
@@ -1018,10 +1022,10 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
         if (b == 4 && E == 2) return f(std::integral_constant<int, E == 2 ? 2 : 1>{});
         return f(std::integral_constant<int, 1>{});
     };
-    auto sums = [&](const uint64_t *sorted, bool tiny) {
+    auto sums = [&](const uint64_t *sorted, int tiny) {
         return with_vector([&](auto NE) {
             constexpr int kN = decltype(NE)::value;
-            const SumShape sh = sum_shape(n, D, kN, E);
+            const SumShape sh = sum_shape(n, D, kN, E, tiny);
             SumParams p{};
             p.words = sorted, p.st = st;
             p.n = n, p.chunk = sh.chunk, p.V = uint32_t(V), p.D = D, p.walk = sh.walk, p.groups = sh.groups;
@@ -1033,12 +1037,23 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
             return SS_OK;
         });
     };
-    if (n > 0 && n <= kTinyN && with_vector([&](auto NE) {
-            const SumShape sh = sum_shape(n, D, decltype(NE)::value, E);
-            const int64_t width = int64_t(sh.cols) * vectors_of(decltype(NE)::value, E) * decltype(NE)::value;
-            return sh.chunks == 1 && V * width * int64_t(sizeof(G)) <= kTinyClearing;
-        }))
-        return sums(nullptr, true);
+    if (n > 0 && n <= kTinyN) {
+        // slices of the columns, or 0 where a CTA would have too much to clear
+        const int slices = with_vector([&](auto NE) {
+            constexpr int kN = decltype(NE)::value, kOwn = vectors_of(kN, E);
+            constexpr int64_t kBytes = kN * int64_t(sizeof(G)), kLeast = (32 + kBytes - 1) / kBytes;
+            const int64_t vecs = D / kN;
+            int64_t own = kTinyClearing / (V * kBytes);    // vectors of a slice that its CTA clears,
+            if (own > 2048 / n * kOwn) own = 2048 / n * kOwn;      // and that leave a walk of eight ids
+            if (own < (vecs + sms - 1) / sms) own = (vecs + sms - 1) / sms;
+            if (own < kLeast) own = kLeast;
+            own = (own + kOwn - 1) / kOwn * kOwn;
+            if (own > vecs) own = vecs;
+            const int slices = int((vecs + own - 1) / own);
+            return V * own * kBytes <= kTinyMost && sum_shape(n, D, kN, E, slices).chunks == 1 ? slices : 0;
+        });
+        if (slices > 0) return sums(nullptr, slices);
+    }
     // CTAs that clear: enough to draw on the whole bandwidth where there is much to clear
     const int64_t row_bytes = int64_t(D) * sizeof(G), bytes = V * (out_stride == D || row_bytes > 64 ? row_bytes : 64);
     const uint64_t *sorted = w[0];
@@ -1100,7 +1115,7 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
         sorted = w[(passes - 1) & 1];
     }
     if (n == 0) return SS_OK;
-    return sums(sorted, false);
+    return sums(sorted, 0);
 }
 
 template <typename T, typename G>

@@ -126,6 +126,19 @@ def test_backward(ss, case):
     bwd_case(ss, *case)
 
 
+# Up to 256 ids: every slice of the columns sorts and clears for itself.
+FEW = [(200, 1000, 700, "bf16", "f32", "int64", "log", 0, 0), (256, 100, 8190, "f32", "f32", "int64", "same", 0, 0),
+       (150, 4096, 256, "f32", "f32", "int32", "log", 0, 0), (256, 20, 5, "f16", "f16", "int64", "one", 0, 0),
+       (60, 300, 1111, "bf16", "f32", "int64", "absent", 3, 1), (256, 1000, 333, "f32", "f32", "int32", "uniform", 1, 1),
+       (2, 2048, 24, "f16", "f16", "int64", "same", 8, 0), (128, 30, 65536, "bf16", "bf16", "int64", "log", 0, 0),
+       (255, 40, 1002, "f32", "f32", "int64", "none", 2, 0)]
+
+
+@pytest.mark.parametrize("case", FEW, ids=lambda c: "-".join(map(str, c)))
+def test_backward_of_few_ids(ss, case):
+    bwd_case(ss, *case)
+
+
 def test_offsets_past_32_bits(ss):
     """Rows a billion values apart: the last starts past 2^32 bytes and 2^31 values."""
     import torch
