@@ -203,8 +203,8 @@ __device__ __forceinline__ void clear_share(const Clearing<G> &c, int cta, int c
 }
 
 // One CTA sorts up to KPT ids a thread in its shared memory, 8 bits a pass,
-// the others clear.  The sort waits on its barriers (256 ids 4 us, 8,191 some
-// 20), the clearing on the stores' bandwidth: 131 MB in 25 us, 5.3 TB/s.
+// the others clear.  The sort waits on its barriers and on shared memory, the
+// clearing on the stores' bandwidth: 8191 ids and 131 MB together 25 us.
 template <typename I, typename G, int KPT>
 __global__ void __launch_bounds__(kSmallThreads) k_embed_sort_small(const I *__restrict__ ids, int n, uint32_t V,
                                                                     int passes, uint64_t *words, SortState *st,

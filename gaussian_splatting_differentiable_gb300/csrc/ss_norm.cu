@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
 // 42 us, 30 at copy bandwidth; two rows of 256 threads are all that the
 // registers of an SM hold (x, dy and two sums a column, 127 a thread), and 16
 // warps issue every other cycle.  1M x 48 float32 (576 MB): 89 us (86).
-// 76,363 x 48: 10.2, of which the last launch takes 3.
+// 76,363 x 48 (44 MB): 10.2 with the last launch, both bound by latency.
 template <typename T, int VEC, int NV, bool MULTI, int X>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : (NV == 1 && X <= 1 ? 3 : 2))
     k_norm_bwd(Rows<const T> dy, Rows<const T> x, int64_t n, int32_t D, Place pl, const void *gamma, int pdt,
