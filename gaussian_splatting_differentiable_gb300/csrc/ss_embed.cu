@@ -31,19 +31,15 @@ constexpr int64_t kManyBytes = 64 << 20;   // of output, half of L2
 // every row's start and end are aligned to), and ROWS rows at a time so that
 // the ids' loads, and then the rows', wait together.  Bound by the writes of
 // out (and the table's reads where it does not stay in L2): 2M x 48 float32
-// out of 4096 rows (400 MB) 67 to 68 us, 61 at copy bandwidth.
+// out of 65,536 rows (412 MB) 67 us, 61 at copy bandwidth.
 //
 // Where rows allow only narrow vectors the instructions bound it: a row's
 // pointers and limits are made once, and WARP (a row to a warp) leaves the
 // vectors' distances to the instructions (700,000 x 87 bfloat16: 107 us with
 // all of that worked out for each value, 58 so; in pairs on 4-byte boundaries
-// 80, for the registers and instructions that the rows' ends take).  The
-// registers are held down, or too few rows are on their way at a time (2M x 48
-// float32: 80 us with 45 registers, 68 with 32).
-constexpr int fwd_ctas(int rows, int bytes) { return rows == 1 ? (bytes > 48 ? 6 : 8) : (rows == 2 ? 5 : 4); }
-
+// 80, for the registers and instructions that the rows' ends take).
 template <typename T, typename I, int N, int NV, int ROWS, bool WARP>
-__global__ void __launch_bounds__(kThreads, fwd_ctas(ROWS, NV * N * int(sizeof(T))))
+__global__ void __launch_bounds__(kThreads)
     k_embed_fwd(const T *__restrict__ table, int64_t ts, int64_t V, const I *__restrict__ ids, int64_t n, float scale,
                 T *out, int64_t os, int shift, int vecs, bool leave) {
     const int lanes = WARP ? 32 : 1 << shift, lane = threadIdx.x & (lanes - 1);
@@ -65,6 +61,7 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas(ROWS, NV * N * int(sizeof(T
         named[r] = here ? mine : 0;
         s[r] = here ? scale : 0.0f;
     }
+#pragma unroll 1                           // most rows take one turn (unrolled, 45 registers: 2M x 48, 80 us for 67)
     for (int v0 = 0; v0 < mine; v0 += lanes * NV) {
         Vec<T, N> x[ROWS][NV];
 #pragma unroll
