@@ -1,10 +1,11 @@
 // Rows of a learned table looked up by id, and the table's gradient (model:
 // include/ss_embed.h).
 //
-// Backward.  (id, position) words are sorted by id (k_embed_sort_small, or
-// k_embed_count / k_embed_scan / k_embed_move for each digit), while CTAs
-// beside the sort's clear dtable; k_embed_sum walks fixed chunks of the sorted
-// words and adds dout rows, and k_embed_join adds up the ids that cross chunks.
+// Backward.  (id, position) words are sorted by id: a few in k_embed_sum
+// itself, more in k_embed_sort_small, else by k_embed_count / k_embed_scan /
+// k_embed_move for each digit, while CTAs beside the sort's clear dtable.
+// k_embed_sum walks fixed chunks of the sorted words and adds dout rows, and
+// k_embed_join adds up the ids that cross chunks.
 #include <cuda_runtime.h>
 
 #include <atomic>
