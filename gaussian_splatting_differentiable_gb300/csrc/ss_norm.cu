@@ -92,6 +92,25 @@ __device__ __forceinline__ void row_sum(float (&v)[K], const Place &pl, int grou
     flip ^= 1;
 }
 
+// Rounding of the mean.  1 / sqrt(var + eps) multiplies it: a row of one value
+// 1e4 and a mean one unit of its last place off give y = 0.3 for 0.
+// A float32 sum of 16-bit values that are all alike is exact (in float16 up to
+// 8192 of them), so there the quotient sum / D is rounded once and no more.
+// Sums of float32 values are not; where the mean is `far` from the row's spread
+// the deviations from it, which are nearly exact there, are averaged and the
+// average taken off.  Nearer, a few units of the mean's last place are no more
+// than a few roundings of a result of that size.
+constexpr float kFar = 8.0f;
+// v = var + eps: by the squares, so that it need not wait for the root.
+__device__ __forceinline__ bool far_off(float mu, float v) { return mu * mu > kFar * kFar * v; }
+// a / width, correctly rounded, from inv = 1 / width: the product, and its
+// remainder, which a fused product gives exactly, times inv (P. Markstein, IBM
+// J. Res. Dev. 34, 1990).
+__device__ __forceinline__ float quotient(float a, float width, float inv) {
+    const float q = a * inv, r = fmaf(-q, width, a);
+    return isfinite(q) ? fmaf(r, inv, q) : q;
+}
+
 template <int K>
 __device__ __forceinline__ void clear_sums(float *s_red, int count) {
     for (int e = threadIdx.x; e < count * 2 * K * kRowWarps; e += blockDim.x) s_red[e] = 0.0f;
@@ -245,7 +264,10 @@ constexpr int fwd_ctas(int vec, int nv, bool multi, int x) {
     return multi ? 1 : (nv == 1 && x <= 2 ? 4 : (x > 0 && nv * vec > 8 ? 2 : 3));
 }
 
-// mean, centred squares and result of a row from registers.  Bound by memory:
+// mean, centred squares and result of a row from registers.  Float32 rows whose
+// mean is far_off take one sum more, and one branch for every row: 2M x 48
+// 113.8 -> 114.0 us, 2M x 3 47 -> 50 (in 16 bits, where the quotient does, the
+// branch would cost 1 to 5 us of 20 to 100).  Bound by memory:
 // 2M x 48 float32 (768 MB and the statistics) 114 us, at copy bandwidth (116);
 // 8191 x 4096 bfloat16 29 (20); 8191 x 8192 float32 83 (79); 1,731,207 x 35
 // bfloat16 89 (38: seven of eight rows start off a 16-byte boundary, and their
@@ -257,6 +279,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
     extern __shared__ uint4 s_ring[];    // [stages][NV][threads]
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][1][kRowWarps];
     constexpr bool SHIFT = X > 0;
+    constexpr bool kAgain = sizeof(T) == 4;
     constexpr int kStages = stages_of(NV), kHalf = VEC / 2, kX = SHIFT ? X : 1;
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
     const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
@@ -293,7 +316,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
     load_weights<VEC, NV, SHIFT>(b, beta, pdt, 0.0f, c);
     if (MULTI) clear_sums<1>(&s_red[0][0][0][0], kMaxGroups);
     __syncthreads();
-    const float inv = 1.0f / float(D);
+    const float width = float(D), inv = 1.0f / width;
     int flip = 0, stage = 0;
     T *py = y.base + row0 * y.stride;
     const int64_t ystep = step * y.stride;
@@ -327,7 +350,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
             pe += xstep;
         }
         row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
-        const float mu = sum[0] * inv;
+        float mu = kAgain ? sum[0] * inv : quotient(sum[0], width, inv);
         const F2 neg = both(-mu);
         acc = both(0.0f);
 #pragma unroll
@@ -348,8 +371,37 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
                 sum[0] = fmaf(ec[u], ec[u], sum[0]);
             }
         row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
-        const float r = __frsqrt_rn(fmaf(sum[0], inv, eps));
-        if (row >= n) continue;
+        float v = fmaf(sum[0], inv, eps);
+        const bool again = kAgain && far_off(mu, v);
+        // (a row's lanes agree; and one branch for what few rows are)
+        if (kAgain && (MULTI ? again : __any_sync(0xffffffffu, again || row >= n))) {
+            const float var = sum[0] * inv;
+            acc = both(0.0f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (c.lane + k * c.lanes < c.vecs)
+#pragma unroll
+                    for (int i = 0; i < kHalf; ++i) acc = add2(acc, f[k][i]);
+            sum[0] = sum_of(acc);
+            if (SHIFT)
+#pragma unroll
+                for (int u = 0; u < kX; ++u) sum[0] += ec[u];
+            row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
+            const float off = again ? sum[0] / width : 0.0f;    // (a product with 1 / D would leave a rounding)
+            if (again) v = fmaxf(fmaf(-off, off, var), 0.0f) + eps;
+            mu += off;
+            const F2 less = both(-off);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) f[k][i] = add2(f[k][i], less);
+            if (SHIFT)
+#pragma unroll
+                for (int u = 0; u < kX; ++u) ec[u] -= off;
+            if (!MULTI && row >= n) continue;
+        }
+        const float r = __frsqrt_rn(v);
+        if (!kAgain && row >= n) continue;
         const F2 rr = both(r);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -595,31 +647,67 @@ __device__ __forceinline__ float block_sum(float v, float *s_red) {
 
 // A CTA a row, which is read three times (the second and third from L1 or L2),
 // an element a thread: rows of more than 8,191 elements have work enough for
-// their latency.
+// their latency.  FAR: a row whose mean is far_off, as in k_norm_fwd.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_norm_fwd_wide(const T *x, int64_t xs, int64_t n, int32_t D,
+struct WideRow {
+    const T *x;
+    T *y;
+    int32_t D;
+    const void *gamma, *beta;
+    int pdt;
+    float eps, mu, off, v, r;      // v = var + eps
+    template <bool FAR>
+    __device__ __forceinline__ float centred(int j) const {
+        const float c = to_float(x[j]) - mu;
+        return FAR ? c - off : c;
+    }
+    template <bool FAR>
+    __device__ __forceinline__ void statistics(float *s_red) {
+        float s = 0.0f;
+        for (int j = threadIdx.x; j < D; j += kThreads) {
+            const float c = centred<FAR>(j);
+            s += c * c;
+        }
+        v = block_sum(s, s_red) / float(D) + eps;
+        r = __frsqrt_rn(v);
+    }
+    template <bool FAR>
+    __device__ __forceinline__ void result() const {
+        for (int j = threadIdx.x; j < D; j += kThreads) {
+            const float g = gamma ? load_param(gamma, pdt, j) : 1.0f;
+            const float b = beta ? load_param(beta, pdt, j) : 0.0f;
+            y[j] = from_float<T>(centred<FAR>(j) * r * g + b);
+        }
+    }
+};
+template <typename T>
+__device__ __noinline__ float2 far_row(WideRow<T> w, float *s_red) {   // its (mean, rstd)
+    float s = 0.0f;
+    for (int j = threadIdx.x; j < w.D; j += kThreads) s += w.template centred<false>(j);
+    w.off = block_sum(s, s_red) / float(w.D);
+    w.template statistics<true>(s_red);
+    w.template result<true>();
+    return make_float2(w.mu + w.off, w.r);
+}
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 8) k_norm_fwd_wide(const T *x, int64_t xs, int64_t n, int32_t D,
                                                        const void *gamma, const void *beta, int pdt, float eps, T *y,
                                                        int64_t ys, float *mean, float *rstd) {
     __shared__ float s_red[kThreads / 32];
     for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
-        const T *xr = x + row * xs;
+        WideRow<T> w{x + row * xs, y + row * ys, D, gamma, beta, pdt, eps, 0.0f, 0.0f, 0.0f, 0.0f};
         float s = 0.0f;
-        for (int j = threadIdx.x; j < D; j += kThreads) s += to_float(xr[j]);
-        const float mu = block_sum(s, s_red) / float(D);
-        s = 0.0f;
-        for (int j = threadIdx.x; j < D; j += kThreads) {
-            const float c = to_float(xr[j]) - mu;
-            s += c * c;
-        }
-        const float r = __frsqrt_rn(block_sum(s, s_red) / float(D) + eps);
-        for (int j = threadIdx.x; j < D; j += kThreads) {
-            const float g = gamma ? load_param(gamma, pdt, j) : 1.0f;
-            const float b = beta ? load_param(beta, pdt, j) : 0.0f;
-            y[row * ys + j] = from_float<T>((to_float(xr[j]) - mu) * r * g + b);
-        }
+        for (int j = threadIdx.x; j < D; j += kThreads) s += to_float(w.x[j]);
+        w.mu = block_sum(s, s_red) / float(D);
+        w.template statistics<false>(s_red);
+        float2 m = make_float2(w.mu, w.r);
+        if (far_off(w.mu, w.v))           // the same in every thread
+            m = far_row(w, s_red);
+        else
+            w.template result<false>();
         if (threadIdx.x == 0) {
-            if (mean) mean[row] = mu;
-            if (rstd) rstd[row] = r;
+            if (mean) mean[row] = m.x;
+            if (rstd) rstd[row] = m.y;
         }
     }
 }

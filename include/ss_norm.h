@@ -10,8 +10,10 @@
  *
  * The variance is taken from the centred values (a second look at the row,
  * held in registers), never as a difference of moments.  Statistics and sums
- * are float32; the weights' sums run along splits that depend on the sizes
- * alone, so the same inputs give the same bits.
+ * are float32; where mu is far from the row's spread its rounding is averaged
+ * out of the centred values, so that a row of one value gives y = beta.
+ * The weights' sums run along splits that depend on the sizes alone, so the
+ * same inputs give the same bits.
  *
  * Conventions are those of ss.h; rows and strides those of ss_embed.h.
  */
