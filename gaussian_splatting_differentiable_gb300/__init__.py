@@ -448,6 +448,21 @@ def _workspace(nbytes: int, device):
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+def _device(device):
+    """The device of an object's own buffers: the kernels take their pointers as they are."""
+    d = torch.device(device)
+    if d.type != "cuda":
+        raise ValueError("device must be a CUDA device (got %s)" % d)
+    return d
+
+
+def _scratch(workspace):
+    """(pointer, bytes) of a caller's workspace."""
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.nbytes
+
+
 # ---- scaled lookup (ss_embed.h)
 
 def ss_embed_workspace_bytes(n: int, V: int, D: int) -> int:
@@ -479,8 +494,9 @@ def ss_embed_bwd(dout, ids, scale: float, dtable, workspace, stream=None) -> Non
     n = ids.shape[0]
     dp, ds = _rows(dout, "dout", D, n)
     gp, gs = _rows(dtable, "dtable", D)
-    st = _L.ss_embed_bwd(dp, code, ds, idp, idb, n, V, D, scale, gp, gcode, gs,
-                         workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    wp, wb = _scratch(workspace)
+    st = _L.ss_embed_bwd(dp, code, ds, idp, idb, n, V, D, scale, gp, gcode, gs, wp, wb,
+                         _stream(stream))
     if st:
         _check(st, "ss_embed_bwd")
 
@@ -493,7 +509,7 @@ class Embedding:
 
     def __init__(self, n: int, V: int, D: int, scale: float = 1.0, dtype=torch.float32,
                  grad_dtype=None, device="cuda", forward: bool = True, backward: bool = True):
-        d = torch.device(device)
+        d = _device(device)
         self.n, self.V, self.D, self.scale = n, V, D, float(scale)
         self.dtype, self._code = dtype, _code(dtype, "dtype")
         self._out = torch.empty(n, D, dtype=dtype, device=d) if forward else None
@@ -600,7 +616,7 @@ def ss_layer_norm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace,
             dbp = p
     mp = _vector(mean, "mean", n, torch.float32)
     rp = _vector(rstd, "rstd", n, torch.float32)
-    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    wp, wb = (None, 0) if workspace is None else _scratch(workspace)
     st = _L.ss_layer_norm_bwd(dyp, dys, xp, xs, code, n, D, gp, SS_F32 if pc is None else pc, mp,
                               rp, dxp, dxs, dgp, dbp, wp, wb, _stream(stream))
     if st:
@@ -616,7 +632,7 @@ class LayerNorm:
     def __init__(self, n: int, D: int, eps: float = 1e-5, dtype=torch.float32,
                  param_dtype=torch.float32, device="cuda", forward: bool = True,
                  backward: bool = True):
-        d = torch.device(device)
+        d = _device(device)
         self.n, self.D, self.eps = n, D, float(eps)
         self.dtype, self._code = dtype, _code(dtype, "dtype")
         self.param_dtype, self._param_code = param_dtype, _code(param_dtype, "param_dtype")
@@ -702,19 +718,32 @@ def _tensor_list(grads, outs):
     return arr
 
 
+def _clip_args(tensors, n: int, result, workspace):
+    """Pointers and sizes, after checking that the list holds n tensors and the
+    result two values (plain pointers cross the C ABI)."""
+    if not isinstance(tensors, ctypes.Array) or tensors._type_ is not _lib.SsTensor:
+        raise ValueError("tensors must be a ctypes array of SsTensor")
+    if n > len(tensors):
+        raise ValueError("%d tensors in a list of %d" % (n, len(tensors)))
+    if result.dtype != torch.float32 or result.numel() < 2 or not result.is_cuda or \
+            not result.is_contiguous():
+        raise ValueError("result must be a contiguous float32 CUDA tensor of 2")
+    return (result.data_ptr(), *_scratch(workspace))
+
+
 def ss_grad_clip(tensors, n: int, max_norm: float, eps: float, result, workspace,
                  stream=None) -> None:
     """tensors: the ctypes array of SsTensor (see GradClip); result: float32[2]
     device tensor, (norm, coefficient)."""
-    st = _L.ss_grad_clip(tensors, n, max_norm, eps, result.data_ptr(), workspace.data_ptr(),
-                         workspace.nbytes, _stream(stream))
+    rp, wp, wb = _clip_args(tensors, n, result, workspace)
+    st = _L.ss_grad_clip(tensors, n, max_norm, eps, rp, wp, wb, _stream(stream))
     if st:
         _check(st, "ss_grad_clip")
 
 
 def ss_grad_norm(tensors, n: int, result, workspace, stream=None) -> None:
-    st = _L.ss_grad_norm(tensors, n, result.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                         _stream(stream))
+    rp, wp, wb = _clip_args(tensors, n, result, workspace)
+    st = _L.ss_grad_norm(tensors, n, rp, wp, wb, _stream(stream))
     if st:
         _check(st, "ss_grad_norm")
 
@@ -727,25 +756,37 @@ class GradClip:
     once, here: their tensors must stay where they are."""
 
     def __init__(self, grads, outs=None, eps: float = 1e-6, device="cuda"):
-        d = torch.device(device)
         self.grads, self.outs = list(grads), None if outs is None else list(outs)
         self.eps = float(eps)
-        self.n = len(self.grads)
-        nb = ss_clip_workspace_bytes(self.n)
+        self._n = len(self.grads)
+        nb = ss_clip_workspace_bytes(self._n)
         if nb == 0:
             raise ValueError("too many tensors")
         self._list = _tensor_list(self.grads, self.outs)
-        self.result = torch.zeros(2, dtype=torch.float32, device=d)
-        self.workspace = _workspace(nb, d)
+        d = _device(device)
+        self._result = torch.zeros(2, dtype=torch.float32, device=d)
+        self._workspace = _workspace(nb, d)
+
+    n = property(lambda self: self._n)
+    result = property(lambda self: self._result)
+    workspace = property(lambda self: self._workspace)
 
     def __call__(self, max_norm: float, stream=None) -> torch.Tensor:
-        ss_grad_clip(self._list, self.n, max_norm, self.eps, self.result, self.workspace, stream)
-        return self.result
+        result, ws = self._result, self._workspace
+        st = _L.ss_grad_clip(self._list, self._n, max_norm, self.eps, result.data_ptr(),
+                             ws.data_ptr(), ws.nbytes, _stream(stream))
+        if st:
+            _check(st, "ss_grad_clip")
+        return result
 
     def norm(self, stream=None) -> torch.Tensor:
         """result = (norm, 1 if it is finite else 0); scales nothing."""
-        ss_grad_norm(self._list, self.n, self.result, self.workspace, stream)
-        return self.result
+        result, ws = self._result, self._workspace
+        st = _L.ss_grad_norm(self._list, self._n, result.data_ptr(), ws.data_ptr(), ws.nbytes,
+                             _stream(stream))
+        if st:
+            _check(st, "ss_grad_norm")
+        return result
 
 
 # ------------------------------------------------------------------ whole path

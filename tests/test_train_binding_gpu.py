@@ -1,0 +1,47 @@
+"""The training operators' binding on the device: buffers of the wrong place,
+type or size are refused before the library is called."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ss():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import gaussian_splatting_differentiable_gb300 as m
+    return m
+
+
+def test_clip_result_and_workspace(ss):
+    import torch
+    c = ss.GradClip([torch.ones(10, device="cuda")])
+    arr, ws, ok = c._list, c.workspace, c.result
+    for bad in (torch.zeros(2), torch.zeros(1, device="cuda"), torch.zeros(2, device="cuda").double(),
+                torch.zeros(4, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="result"):
+            ss.ss_grad_clip(arr, 1, 1.0, 1e-6, bad, ws)
+        with pytest.raises(ValueError, match="result"):
+            ss.ss_grad_norm(arr, 1, bad, ws)
+    for bad in (ws.cpu(), torch.zeros(1 << 16, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError, match="workspace"):
+            ss.ss_grad_clip(arr, 1, 1.0, 1e-6, ok, bad)
+        with pytest.raises(ValueError, match="workspace"):
+            ss.ss_grad_norm(arr, 1, ok, bad)
+    ss.ss_grad_norm(arr, 1, ok, ws)
+    assert float(ok[0]) == pytest.approx(10 ** 0.5, rel=1e-6)
+    assert c.result is ok and float(c(1.0)[0]) == float(ok[0])
+
+
+def test_gradients_workspaces(ss):
+    import torch
+    e, x = ss.Embedding(4, 3, 8), torch.zeros(4, 8, device="cuda")
+    ids = torch.zeros(4, dtype=torch.int64, device="cuda")
+    ln = ss.LayerNorm(4, 8)
+    g = ln.grads
+    for ws in (lambda t: t.cpu(), lambda t: torch.zeros(t.numel(), 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError, match="workspace"):
+            ss.ss_embed_bwd(x, ids, 1.0, e.grad, ws(e.workspace))
+        with pytest.raises(ValueError, match="workspace"):
+            ss.ss_layer_norm_bwd(x, x, None, ln.mean, ln.rstd, ln.dx, g["dgamma"], g["dbeta"], ws(ln.workspace))
