@@ -535,6 +535,8 @@ class Embedding:
         tp, ts = self._input(table, "table", self.V)
         idp, idb = _ids(ids, self.n)
         out = self._out
+        if out is None:
+            raise ValueError("this Embedding was made without forward=True")
         st = _L.ss_embed_fwd(tp, self._code, self.V, self.D, ts, idp, idb, self.n, self.scale,
                              out.data_ptr(), self.D, _stream(stream))
         if st:
@@ -545,6 +547,8 @@ class Embedding:
         dp, ds = self._input(dout, "dout", self.n)
         idp, idb = _ids(ids, self.n)
         grad, ws = self._grad, self._workspace
+        if grad is None:
+            raise ValueError("this Embedding was made without backward=True")
         st = _L.ss_embed_bwd(dp, self._code, ds, idp, idb, self.n, self.V, self.D, self.scale,
                              grad.data_ptr(), self._grad_code, self.D, ws.data_ptr(), ws.nbytes,
                              _stream(stream))
@@ -670,6 +674,8 @@ class LayerNorm:
         gp = None if gamma is None else _vector(gamma, "gamma", D, p)
         bp = None if beta is None else _vector(beta, "beta", D, p)
         y = self._y
+        if y is None:
+            raise ValueError("this LayerNorm was made without forward=True")
         st = _L.ss_layer_norm_fwd(xp, self._code, xs, self.n, D, gp, bp, self._param_code,
                                   self.eps, y.data_ptr(), D, self._mean.data_ptr(),
                                   self._rstd.data_ptr(), _stream(stream))
@@ -683,9 +689,13 @@ class LayerNorm:
         xp, xs = self._input(x, "x")
         n, D = self.n, self.D
         gp = None if gamma is None else _vector(gamma, "gamma", D, self.param_dtype)
+        dx, ws = self._dx, self._workspace
+        if dx is None:
+            raise ValueError("this LayerNorm was made without backward=True")
+        if self._mean is None and (mean is None or rstd is None):
+            raise ValueError("mean and rstd must be given to a LayerNorm made without forward=True")
         mp = self._mean.data_ptr() if mean is None else _vector(mean, "mean", n, torch.float32)
         rp = self._rstd.data_ptr() if rstd is None else _vector(rstd, "rstd", n, torch.float32)
-        dx, ws = self._dx, self._workspace
         st = _L.ss_layer_norm_bwd(dyp, dys, xp, xs, self._code, n, D, gp, self._param_code, mp, rp,
                                   dx.data_ptr(), D, self._dgamma.data_ptr(),
                                   self._dbeta.data_ptr(), ws.data_ptr(), ws.nbytes,

@@ -45,3 +45,22 @@ def test_gradients_workspaces(ss):
             ss.ss_embed_bwd(x, ids, 1.0, e.grad, ws(e.workspace))
         with pytest.raises(ValueError, match="workspace"):
             ss.ss_layer_norm_bwd(x, x, None, ln.mean, ln.rstd, ln.dx, g["dgamma"], g["dbeta"], ws(ln.workspace))
+
+
+def test_a_direction_without_buffers(ss):
+    import torch
+    t, x = torch.zeros(3, 8, device="cuda"), torch.zeros(4, 8, device="cuda")
+    ids, stat = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.ones(4, device="cuda")
+    with pytest.raises(ValueError, match="forward=True"):
+        ss.Embedding(4, 3, 8, forward=False).forward(t, ids)
+    with pytest.raises(ValueError, match="backward=True"):
+        ss.Embedding(4, 3, 8, backward=False).backward(x, ids)
+    with pytest.raises(ValueError, match="forward=True"):
+        ss.LayerNorm(4, 8, forward=False).forward(x)
+    with pytest.raises(ValueError, match="backward=True"):
+        ss.LayerNorm(4, 8, backward=False).backward(x, x)
+    ln = ss.LayerNorm(4, 8, forward=False)
+    for given in ({}, {"mean": stat}, {"rstd": stat}):
+        with pytest.raises(ValueError, match="mean and rstd"):
+            ln.backward(x, x, **given)
+    assert (ln.backward(x, x, mean=stat, rstd=stat) == 0).all()
