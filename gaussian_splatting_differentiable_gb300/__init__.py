@@ -42,8 +42,16 @@ def _ptr(t):
 
 
 # The current stream's handle without a Stream object around it: 0.2 us of host
-# time against 2.9 us, a third of a small call.
-_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# time against 2.9 us, a third of a small call.  These names are PyTorch's own;
+# one that lacks them (built without CUDA, say) takes the public way.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+if _current_stream is None or _current_device is None:
+    def _current_device():
+        return None
+
+    def _current_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _stream(stream):

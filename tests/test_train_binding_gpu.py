@@ -1,5 +1,10 @@
 """The training operators' binding on the device: buffers of the wrong place,
 type or size are refused before the library is called."""
+import os
+import subprocess
+import sys
+import textwrap
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +69,23 @@ def test_a_direction_without_buffers(ss):
         with pytest.raises(ValueError, match="mean and rstd"):
             ln.backward(x, x, **given)
     assert (ln.backward(x, x, mean=stat, rstd=stat) == 0).all()
+
+
+def test_the_current_stream_by_its_public_name(ss):
+    """What a PyTorch without the handle's own name takes gives the same stream."""
+    prog = textwrap.dedent("""
+        import torch
+        del torch._C._cuda_getCurrentRawStream
+        import gaussian_splatting_differentiable_gb300 as ss
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            assert ss._stream(None) == s.cuda_stream
+        assert ss._stream(None) == torch.cuda.current_stream().cuda_stream
+    """)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", prog], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    import torch
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        assert ss._stream(None) == s.cuda_stream

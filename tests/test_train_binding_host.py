@@ -1,9 +1,15 @@
 """The training operators' binding refuses what the library would read or
-write outside of, or what is not on the device, before it calls the library
-(no GPU)."""
+write outside of, or what is not on the device, before it calls the library;
+and the package loads whatever the installed PyTorch has of CUDA (no GPU)."""
+import os
+import subprocess
+import sys
+import textwrap
+
 import pytest
 
 torch = pytest.importorskip("torch")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -41,3 +47,17 @@ def test_buffers_are_made_on_the_device(ss):
                  lambda: ss.GradClip([], device="cpu")):
         with pytest.raises(ValueError, match="CUDA device"):
             make()
+
+
+def test_import_without_the_cuda_names_of_torch(ss):
+    """A PyTorch without CUDA has none of them; streams given as handles still work."""
+    prog = textwrap.dedent("""
+        import torch
+        for name in [n for n in dir(torch._C) if n.startswith("_cuda_getCurrent") or n == "_cuda_getDevice"]:
+            delattr(torch._C, name)
+        import gaussian_splatting_differentiable_gb300 as ss
+        assert ss._stream(7) == 7
+        assert ss.ss_embed_workspace_bytes(4, 3, 8) > 0
+    """)
+    r = subprocess.run([sys.executable, "-c", prog], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
