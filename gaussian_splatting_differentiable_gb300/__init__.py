@@ -733,7 +733,27 @@ def _tensor_list(grads, outs):
                            not o.is_contiguous()):
             raise ValueError("output %d must be a contiguous CUDA tensor like its gradient" % k)
         arr[k] = _lib.SsTensor(g.data_ptr(), o.data_ptr(), g.numel(), code, 0)
+    _no_overlaps([(a.inp, a.out, g.nbytes) for a, g in zip(arr, grads) if a.numel])
     return arr
+
+
+def _no_overlaps(spans):
+    """Refuses results that share memory with one another or with a gradient
+    other than their own: a gradient listed twice in place would be scaled twice,
+    by whichever threads come first."""
+    pieces = []
+    for i, o, nbytes in spans:
+        pieces.append((o, o + nbytes, True))
+        if i != o:
+            pieces.append((i, i + nbytes, False))
+    read_to = written_to = 0
+    for start, end, written in sorted(pieces):
+        if start < written_to or (written and start < read_to):
+            raise ValueError("a result overlaps another result or a gradient (a tensor listed twice?)")
+        if written:
+            written_to = max(written_to, end)
+        else:
+            read_to = max(read_to, end)
 
 
 def _clip_args(tensors, n: int, result, workspace):

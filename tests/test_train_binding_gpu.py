@@ -89,3 +89,27 @@ def test_the_current_stream_by_its_public_name(ss):
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
         assert ss._stream(None) == s.cuda_stream
+
+
+def test_clip_refuses_results_that_overlap(ss):
+    import torch
+    buf = torch.arange(100.0, device="cuda")
+    a, b = buf[:40], buf[40:90]
+    inner, across = buf[10:20], buf[30:50]
+    out = torch.zeros(100, device="cuda")
+    for grads, outs in (([a, a], None), ([a, b, inner], None), ([a, across], None), ([buf, b], None),
+                        ([a, b], [out[:40], out[39:89]]),          # result on result
+                        ([a, b], [b[:40], out[:50]]),              # result on another gradient
+                        ([buf[:10], b], [buf[1:11], out[:50]]),    # result shifted against its gradient
+                        ([a, a], [out[:40], out[:40]])):
+        with pytest.raises(ValueError, match="overlaps"):
+            ss.GradClip(grads, outs)
+    empty = buf[5:5]
+    ss.GradClip([a, b, empty, empty])
+    ss.GradClip([], [])
+    c = ss.GradClip([a, a, inner], [out[:40], out[40:80], out[80:90]])   # gradients may
+    n2 = float((2 * (a ** 2).sum() + (inner ** 2).sum()))
+    assert float(c(1e9)[0]) == pytest.approx(n2 ** 0.5, rel=1e-6)
+    assert torch.equal(out[:40], a) and torch.equal(out[40:80], a) and torch.equal(out[80:90], inner)
+    in_place = ss.GradClip([a, b], [a, b])
+    in_place(float("inf"))
