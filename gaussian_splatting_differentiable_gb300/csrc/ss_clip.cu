@@ -21,6 +21,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "ss_clip.h"
 #include "ss_internal.h"
@@ -71,6 +72,20 @@ __device__ __forceinline__ float squares_of(const Vector<T> &x) {
 #pragma unroll
     for (int i = 0; i < 16 / int(sizeof(T)); ++i) s = fmaf(x.get(i), x.get(i), s);
     return s;
+}
+
+template <typename T>
+__device__ __forceinline__ float squares_of(const Vector<T> &x, float by) {   // of the values times `by`
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16 / int(sizeof(T)); ++i) s = fmaf(x.get(i) * by, x.get(i) * by, s);
+    return s;
+}
+
+// Whether there is a value other than 0 in it.
+template <typename T>
+__device__ __forceinline__ bool any_of(const Vector<T> &x) {
+    return ((x.w[0] | x.w[1] | x.w[2] | x.w[3]) & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) != 0u;
 }
 
 // c x, rounded to T; by 1 the bits as they are (a product would change a NaN's).
@@ -142,9 +157,10 @@ struct Flat {
 
 // A tensor's body, from its first 16-byte boundary on, is cut into tiles of
 // vectors, kPer a thread and all in flight; the few elements before and after
-// the body go with its first tile, one a thread.
+// the body go with its first tile, one a thread.  lost: set where values other
+// than 0 have squares that add up to 0.
 template <int CAP, typename T>
-__device__ __forceinline__ float tile_squares(const Table<CAP> &t, int k, int tile) {
+__device__ __forceinline__ float tile_squares(const Table<CAP> &t, int k, int tile, bool *lost) {
     const Flat<T> a(t, k);
     constexpr int kVec = Flat<T>::kVec;
     const int head = a.head();
@@ -171,6 +187,30 @@ __device__ __forceinline__ float tile_squares(const Table<CAP> &t, int k, int ti
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) sum += squares_of<T>(x[u]);
+    if (!std::is_same<T, __half>::value && sum == 0.0f) {
+        bool any = tile == t.first[k] && lone < a.numel && to_float(a.in[lone]) != 0.0f;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) any = any || any_of<T>(x[u]);
+        *lost = *lost || any;
+    }
+    return sum;
+}
+
+// The same of the values times `by`, a vector at a time: few sums need it, and
+// the others are not to hold registers for it.
+template <int CAP, typename T>
+__device__ __forceinline__ float tile_squares(const Table<CAP> &t, int k, int tile, float by) {
+    const Flat<T> a(t, k);
+    constexpr int kVec = Flat<T>::kVec;
+    const int head = a.head();
+    const int64_t body = (a.numel - head) / kVec, v0 = int64_t(tile - t.first[k]) * (kThreads * kPer);
+    const int64_t end = v0 + kThreads * kPer < body ? v0 + kThreads * kPer : body;
+    const int64_t lone = a.lone(head, body, threadIdx.x);
+    const float f = tile == t.first[k] && lone < a.numel ? to_float(a.in[lone]) * by : 0.0f;
+    float sum = f * f;
+#pragma unroll 1
+    for (int64_t v = v0 + threadIdx.x; v < end; v += kThreads)
+        sum += squares_of<T>(load_vec<T, kVec>(a.in + head + v * kVec), by);
     return sum;
 }
 
@@ -244,36 +284,64 @@ __device__ __forceinline__ Sum block_sum(Sum v, Sum *s_red) {
 }
 
 // This CTA's squares: plain float32 over a thread's vectors of a tile (at
-// most 33 elements), with the errors from there on.
-template <int CAP>
-__device__ __forceinline__ Sum sweep_squares(const Table<CAP> &t, Sum *s_red) {
+// most 33 elements), with the errors from there on.  how: `lost` or `by`.
+template <int CAP, typename How>
+__device__ __forceinline__ Sum sweep_squares(const Table<CAP> &t, Sum *s_red, How how) {
     Sum sum{0.0f, 0.0f};
     const int tiles = t.first[t.count];
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int k = tensor_of(t, tile);
         if (t.dtype[k] == SS_F32)
-            sum = plus(sum, tile_squares<CAP, float>(t, k, tile));
+            sum = plus(sum, tile_squares<CAP, float>(t, k, tile, how));
         else if (t.dtype[k] == SS_F16)
-            sum = plus(sum, tile_squares<CAP, __half>(t, k, tile));
+            sum = plus(sum, tile_squares<CAP, __half>(t, k, tile, how));
         else
-            sum = plus(sum, tile_squares<CAP, __nv_bfloat16>(t, k, tile));
+            sum = plus(sum, tile_squares<CAP, __nv_bfloat16>(t, k, tile, how));
     }
     return block_sum(sum, s_red);
 }
 
+// Squares of float32 and bfloat16 values may leave float32's range where their
+// root does not.  A CTA's sum from kLeast to kMost has lost nothing to underflow
+// that its rounding does not (2^30 values lose 2^-119 at most), and those of all
+// CTAs add up to no infinity; nor has one of zeros.  Any other is taken again, of
+// the values times 2^96 or 2^-96: its kind is kLow or kHigh.
+constexpr float kLeast = 0x1p-90f, kMost = 0x1p100f, kUp = 0x1p96f, kDown = 0x1p-96f;
+enum Kind { kLow = -1, kMiddle = 0, kHigh = 1 };
+
+// The root of all squares, of each kind; what is not of the largest scarcely counts.
+__device__ __forceinline__ float root_of(Sum low, Sum middle, Sum high) {
+    const float h = value_of(high), m = value_of(middle);
+    if (h != 0.0f) return sqrtf(h + m * kDown * kDown) * kUp;
+    if (m != 0.0f) return sqrtf(m + value_of(low) * kDown * kDown);
+    return sqrtf(value_of(low)) * kDown;
+}
+
 // (norm, coefficient).
-__device__ __forceinline__ float2 result_of(Sum squares, float max_norm, float eps, bool clip) {
-    const float norm = sqrtf(value_of(squares));
+__device__ __forceinline__ float2 result_of(float norm, float max_norm, float eps, bool clip) {
     const float coef = !isfinite(norm) ? 0.0f : (clip ? fminf(1.0f, max_norm / (norm + eps)) : 1.0f);
     return make_float2(norm, coef);
 }
-__device__ __forceinline__ Sum sum_parts(const float2 *part, int parts, Sum *s_red) {
-    Sum sum{0.0f, 0.0f};
+// part: (hi, lo, kind) of each CTA.
+__device__ __forceinline__ float root_of_parts(const float4 *part, int parts, Sum *s_red) {
+    Sum low{0.0f, 0.0f}, middle = low, high = low;
+    bool some = false;                   // of other kinds
     for (int i = threadIdx.x; i < parts; i += kThreads) {
-        const float2 q = __ldcg(part + i);
-        sum = plus(sum, Sum{q.x, q.y});
+        const float4 q = __ldcg(part + i);
+        const bool here = q.z == kMiddle;
+        middle = plus(middle, Sum{here ? q.x : 0.0f, here ? q.y : 0.0f});
+        some = some || !here;
     }
-    return block_sum(sum, s_red);
+    middle = block_sum(middle, s_red);
+    if (__syncthreads_or(some)) {
+        for (int i = threadIdx.x; i < parts; i += kThreads) {
+            const float4 q = __ldcg(part + i);
+            if (q.z == kLow) low = plus(low, Sum{q.x, q.y});
+            if (q.z == kHigh) high = plus(high, Sum{q.x, q.y});
+        }
+        low = block_sum(low, s_red), high = block_sum(high, s_red);
+    }
+    return root_of(low, middle, high);
 }
 
 template <int CAP>
@@ -301,7 +369,7 @@ constexpr int kCluster = 8, kTeams = 4, kHeld = 2;
 constexpr int kMostHeld = kCluster * kTeams * kHeld;      // tiles
 __global__ void __launch_bounds__(kTeams *kThreads) __cluster_dims__(kCluster, 1, 1)
     k_clip_small(const __grid_constant__ Table<kSmallList> t, float max_norm, float eps, float *result) {
-    __shared__ Sum s_red[kTeams * kWarps], s_part[kCluster];
+    __shared__ Sum s_red[kTeams * kWarps], s_part[2][kCluster];
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     const int tiles = t.first[t.count], rank = int(cluster.block_rank()), team = threadIdx.x / kThreads;
@@ -334,14 +402,27 @@ __global__ void __launch_bounds__(kTeams *kThreads) __cluster_dims__(kCluster, 1
 #pragma unroll
     for (int u = 0; u < kHeld; ++u)
         at(u, [&](auto a, int64_t) { sum = plus(sum, squares_of<typename decltype(a)::T>(vector_of(a, u))); });
-    sum = block_sum<kTeams * kWarps>(sum, s_red);
     cluster.barrier_wait(static_cast<decltype(all_here) &&>(all_here));
-    if (threadIdx.x < kCluster) *cluster.map_shared_rank(&s_part[rank], threadIdx.x) = sum;
-    cluster.sync();
-    sum = s_part[0];
+    auto over_cluster = [&](Sum v, Sum *s_to) {      // the same in every thread
+        v = block_sum<kTeams * kWarps>(v, s_red);
+        if (threadIdx.x < kCluster) *cluster.map_shared_rank(&s_to[rank], threadIdx.x) = v;
+        cluster.sync();
+        v = s_to[0];
 #pragma unroll
-    for (int q = 1; q < kCluster; ++q) sum = plus(sum, s_part[q]);
-    const float2 r = result_of(sum, max_norm, eps, true);
+        for (int q = 1; q < kCluster; ++q) v = plus(v, s_to[q]);
+        return v;
+    };
+    sum = over_cluster(sum, s_part[0]);
+    float norm = sqrtf(value_of(sum));
+    if (!(value_of(sum) >= kLeast && value_of(sum) <= kMost)) {      // scaled, as in k_clip_squares
+        const float by = norm < 1.0f ? kUp : kDown;
+        sum = Sum{0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u)
+            at(u, [&](auto a, int64_t) { sum = plus(sum, squares_of<typename decltype(a)::T>(vector_of(a, u), by)); });
+        norm = sqrtf(value_of(over_cluster(sum, s_part[1]))) * (norm < 1.0f ? kDown : kUp);
+    }
+    const float2 r = result_of(norm, max_norm, eps, true);
     if (rank == 0 && threadIdx.x == 0) result[0] = r.x, result[1] = r.y;
     const float c = isfinite(r.x) ? r.y : 1.0f;      // nothing is scaled by a norm that is not finite
 #pragma unroll
@@ -355,19 +436,26 @@ __global__ void __launch_bounds__(kTeams *kThreads) __cluster_dims__(kCluster, 1
 // CTAs that stay on the device and share the tiles out: 6.3 TB/s, the copy's
 // bandwidth within a tenth (239 MB, 38 us).
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) k_clip_squares(const __grid_constant__ Table<CAP> t, float2 *part) {
+__global__ void __launch_bounds__(kThreads, 8) k_clip_squares(const __grid_constant__ Table<CAP> t, float4 *part) {
     __shared__ Sum s_red[kWarps];
     start_dependents();
-    const Sum sum = sweep_squares(t, s_red);
-    if (threadIdx.x == 0) part[blockIdx.x] = make_float2(sum.hi, sum.lo);
+    bool lost = false;
+    Sum sum = sweep_squares(t, s_red, &lost);
+    int kind = kMiddle;
+    const float v = value_of(sum);                   // the same in every thread
+    if (!(v >= kLeast && v <= kMost) && (v != 0.0f || __syncthreads_or(lost))) {
+        kind = v < kLeast ? kLow : kHigh;
+        sum = sweep_squares(t, s_red, kind == kLow ? kUp : kDown);
+    }
+    if (threadIdx.x == 0) part[blockIdx.x] = make_float4(sum.hi, sum.lo, float(kind), 0.0f);
 }
 
-__global__ void __launch_bounds__(kThreads) k_clip_result(const float2 *part, int parts, float max_norm, float eps,
+__global__ void __launch_bounds__(kThreads) k_clip_result(const float4 *part, int parts, float max_norm, float eps,
                                                           bool clip, float *result) {
     __shared__ Sum s_red[kWarps];
     start_dependents();
     wait_for_previous();
-    const float2 r = result_of(sum_parts(part, parts, s_red), max_norm, eps, clip);
+    const float2 r = result_of(root_of_parts(part, parts, s_red), max_norm, eps, clip);
     if (threadIdx.x == 0) result[0] = r.x, result[1] = r.y;
 }
 
@@ -420,14 +508,14 @@ int resident(K kernel, int sms) {
 
 // Squares of the table's tensors; parts: how many partial sums there are.
 template <int CAP>
-void launch_squares(const Table<CAP> &t, float2 *part, int *parts, int sms, cudaStream_t s) {
+void launch_squares(const Table<CAP> &t, float4 *part, int *parts, int sms, cudaStream_t s) {
     auto kernel = k_clip_squares<CAP>;
     const int most = resident(kernel, sms), tiles = t.first[t.count], grid = tiles < 1 ? 1 : (tiles < most ? tiles : most);
     SS_LAUNCH("k_clip_squares", s, kernel<<<grid, kThreads, 0, s>>>(t, part + *parts));
     *parts += grid;
 }
 
-void launch_result(const float2 *part, int parts, float max_norm, float eps, bool clip, float *result, cudaStream_t s) {
+void launch_result(const float4 *part, int parts, float max_norm, float eps, bool clip, float *result, cudaStream_t s) {
     SS_LAUNCH("k_clip_result", s,
               launch_after(k_clip_result, dim3(1), kThreads, 0, s, part, parts, max_norm, eps, clip, result));
 }
@@ -440,7 +528,7 @@ void launch_scale(const Table<CAP> &t, const float *result, cudaStream_t s) {
 
 // A list that fits one launch's parameters.
 template <int CAP>
-void clip_list(const ss_tensor *h, int32_t n, bool clip, float max_norm, float eps, float *result, float2 *part, int sms,
+void clip_list(const ss_tensor *h, int32_t n, bool clip, float max_norm, float eps, float *result, float4 *part, int sms,
                cudaStream_t s) {
     Table<CAP> t;
     int parts = 0;
@@ -479,7 +567,7 @@ ss_status run(const char *who, const ss_tensor *h, int32_t n, bool clip, float m
     int dev = 0, sms = 0;
     ss_status st = current_device(&dev, &sms, who);
     if (st != SS_OK) return st;
-    float2 *part = static_cast<float2 *>(workspace);
+    float4 *part = static_cast<float4 *>(workspace);
     if (clip && n <= kSmallList && total <= kMostHeld * (kThreads * 8)) {   // 16 bytes hold 8 at most
         Table<kSmallList> t;
         fill(&t, h, 0, n, kThreads * 16);
@@ -518,7 +606,7 @@ extern "C" {
 
 size_t ss_clip_workspace_bytes(int32_t n_tensors) {
     if (n_tensors < 0 || n_tensors > kMaxTensors) return 0;
-    return size_t(n_tensors < 1 ? 1 : (n_tensors + kLongList - 1) / kLongList) * kMaxGrid * sizeof(float2);
+    return size_t(n_tensors < 1 ? 1 : (n_tensors + kLongList - 1) / kLongList) * kMaxGrid * sizeof(float4);
 }
 
 ss_status ss_grad_clip(const ss_tensor *h_tensors, int32_t n_tensors, float max_norm, float eps, float *result,

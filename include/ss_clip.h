@@ -6,11 +6,13 @@
  *   coef = min(1, max_norm / (norm + eps))
  *   out  = coef * x
  *
- * A norm that is not finite (an infinity or a NaN among the gradients, or
- * squares that add up past float32) scales nothing: coef is reported as 0, gradients
+ * A norm that is not finite (an infinity or a NaN among the gradients, or a
+ * norm past float32's 3.4e38) scales nothing: coef is reported as 0, gradients
  * clipped in place keep their values and separate outputs receive copies, so
  * that the caller can see which step to skip.  Where coef is 1, in-place
- * gradients are not written.
+ * gradients are not written.  Squares that leave float32's range, above or
+ * below, are taken of scaled values: a second look at the gradients, which
+ * takes half as long again.
  *
  * Squares are summed in float32 over at most a few dozen values and from
  * there on in pairs of float32 that keep the additions' rounding errors,
