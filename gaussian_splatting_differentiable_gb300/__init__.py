@@ -791,7 +791,9 @@ class GradClip:
     in place, or into `outs`, by min(1, max_norm / (norm + eps)) and returns
     `result`, the device float32[2] (norm, coefficient); the coefficient is 0
     and nothing is scaled where the norm is not finite.  The lists are read
-    once, here: their tensors must stay where they are."""
+    once, here: their tensors must stay where they are, and gradients that are
+    new tensors each step need a new object each step.  No result may share
+    memory with another, or with a gradient other than its own."""
 
     def __init__(self, grads, outs=None, eps: float = 1e-6, device="cuda"):
         self.grads, self.outs = list(grads), None if outs is None else list(outs)

@@ -10,11 +10,14 @@
 // launches' parameters: nothing is copied to the device, and a captured graph
 // keeps its own list.
 //
-// The 14 gradients of 2M splats, 472 MB: 204 us, of which 139 are one read and
-// one write at copy bandwidth and 209 would be two reads from DRAM.  Three
-// launches, each begun while the one before it ends, rather than one that
-// waits on its whole grid: that one took 225 us (the tiles' registers spilled
-// beside both sweeps).  300 tensors of mixed types, 115 MB: 52 us (34; 51).
+// The five gradients of 2M splats, 472 MB: 204 us, of which 139 are one read and
+// one write at copy bandwidth and 209 would be two reads from DRAM; the second
+// sweep finds 65 MB in L2.  Three launches, each begun while the one before it
+// ends, rather than one that waits on its whole grid: that one took 225 us (the
+// tiles' registers spilled beside both sweeps).  300 tensors of mixed types, 115
+// MB: 52 us (34; 51); the second sweep finds 60 MB, and both run at 4.8 TB/s of
+// DRAM traffic, the first with 61 % of its issue slots (16-bit values widened,
+// tiles that end inside).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -757,7 +757,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(SumParams p, const T 
 
 // The ids that cross chunks (in whatever order the sums found them: each is
 // its own task, and so is each slice of its columns).  A task's walks of
-// threads take every groups-th chunk and then join in order.
+// threads take every groups-th chunk and then join in order.  (Four columns a
+// thread spill 8 bytes.)
 template <typename G, int N>
 __global__ void __launch_bounds__(kThreads) k_embed_join(SumParams p, int chunks, int cols, int slices, G *dtable) {
     __shared__ float s_acc[N][kThreads];
@@ -1056,7 +1057,9 @@ ss_status launch_bwd(const void *dout, int64_t in_stride, const void *ids, int64
     const int64_t row_bytes = int64_t(D) * sizeof(G), bytes = V * (out_stride == D || row_bytes > 64 ? row_bytes : 64);
     const uint64_t *sorted = w[0];
     if (n <= kSmallN || (n <= kSmallMost && bytes >= kLongClearing)) {
-        // (8000 ids: 22 us in one CTA, 17 in several launches; but 35 against 39 beside 131 MB of clearing)
+        // (the whole gradient, one CTA against several launches: 8000 ids, 24.6 us and 20.3 beside 2 MB of
+        // clearing, 25.5 and 23.8 beside 16, 25.9 and 27.2 beside 25, 34 and 38 beside 131; 4200 ids, 18.8 and
+        // 18.3 beside 2 MB, 18.9 and 21.8 beside 16, so that fewer ids would gain from 8 MB on)
         const int want = int(bytes / (64 * 1024)) + 1, ctas = want < sms * 2 ? want : sms * 2;
         auto go = [&](auto KPT) {
             constexpr int kKpts = decltype(KPT)::value, kSmem = kKpts * kSmallThreads * 6 + kSmallThreads / 32 * 512;

@@ -258,8 +258,10 @@ __device__ __forceinline__ void weights_of(F2 (&g)[VEC / 2], const float4 *plane
 }
 
 // CTAs an SM that the registers are held down for: a row's chain of sums is
-// long, and more rows at a time hide it while nothing spills (700,000 x 87
-// bfloat16: 158 us with two, 116 with four).
+// long, and more rows at a time hide it while they leave the rows' own registers
+// alone (1.5M x 7 bfloat16: 58 us with two or three, 45 with four; 1.73M x 35: 112
+// with two, 89 with three, 104 with four; 500,000 x 50 float32: 37 with two, 38
+// with three, 47 with four).
 constexpr int fwd_ctas(int vec, int nv, bool multi, int x) {
     return multi ? 1 : (nv == 1 && x <= 2 ? 4 : (x > 0 && nv * vec > 8 ? 2 : 3));
 }
@@ -428,7 +430,9 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
 // CTA has all rows, the gradients themselves.  8191 x 4096 bfloat16 (201 MB):
 // 42 us, 30 at copy bandwidth; two rows of 256 threads are all that the
 // registers of an SM hold (x, dy and two sums a column, 127 a thread), and 16
-// warps issue every other cycle.  1M x 48 float32 (576 MB): 89 us (86).
+// warps issue every other cycle.  (16-bit rows of 40 to 71 elements that start off
+// 16-byte boundaries, with up to four elements a lane outside two vectors, spill
+// 148 bytes.)  1M x 48 float32 (576 MB): 89 us (86).
 // 76,363 x 48 (44 MB): 10.2 with the last launch, both bound by latency.
 template <typename T, int VEC, int NV, bool MULTI, int X>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 : (NV == 1 && X <= 1 ? 3 : 2))
@@ -646,8 +650,8 @@ __device__ __forceinline__ float block_sum(float v, float *s_red) {
 }
 
 // A CTA a row, which is read three times (the second and third from L1 or L2),
-// an element a thread: rows of more than 8,191 elements have work enough for
-// their latency.  FAR: a row whose mean is far_off, as in k_norm_fwd.
+// an element a thread: rows past too_wide() have work enough for
+// their latency (2000 x 16,384 bfloat16: 70 us, 19 at copy bandwidth).  FAR: a row whose mean is far_off, as in k_norm_fwd.
 template <typename T>
 struct WideRow {
     const T *x;
@@ -978,7 +982,8 @@ ss_status pick_nv(const Args &a, int sms, cudaStream_t s) {
     return narrow(std::integral_constant<int, 2>{});
 }
 
-// The widest row that 512 threads hold, whatever its start.
+// Wider than 512 threads hold, whatever the row's start: from 8196 elements on in
+// float32, from 8200 in 16 bits.
 template <typename T>
 bool too_wide(int32_t D) {
     constexpr int kVec = 16 / sizeof(T);

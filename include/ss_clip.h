@@ -16,8 +16,9 @@
  *
  * Squares are summed in float32 over at most a few dozen values and from
  * there on in pairs of float32 that keep the additions' rounding errors,
- * along splits that depend on the sizes and alignments alone: the same inputs
- * give the same bits.  Conventions are those of ss.h.
+ * along splits that depend on the sizes, the alignments and the device: with
+ * those the same, the same inputs give the same bits.  Conventions are those of
+ * ss.h.
  */
 #ifndef SS_CLIP_H
 #define SS_CLIP_H

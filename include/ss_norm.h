@@ -12,8 +12,9 @@
  * held in registers), never as a difference of moments.  Statistics and sums
  * are float32; where mu is far from the row's spread its rounding is averaged
  * out of the centred values, so that a row of one value gives y = beta.
- * The weights' sums run along splits that depend on the sizes alone, so the
- * same inputs give the same bits.
+ * The weights' sums run along splits that depend on the sizes, on how the rows
+ * are aligned and on the device: with those the same, the same inputs give the
+ * same bits.
  *
  * Conventions are those of ss.h; rows and strides those of ss_embed.h.
  */
@@ -27,7 +28,7 @@
 extern "C" {
 #endif
 
-/* x, y: device [n][D] of `dtype` (y may be x); gamma, beta: device [D] of
+/* x, y: device [n][D] of `dtype` (y may be x, row for row); gamma, beta: device [D] of
  * param_dtype (SS_F32 or `dtype`), NULL for 1 and 0; mean, rstd: device float
  * [n], each NULL if not wanted.  n = 0 does nothing.
  * Errors: SS_ERR_UNSUPPORTED unless 0 <= n < 2^31 and 1 <= D <= 65536;
@@ -41,7 +42,7 @@ ss_status ss_layer_norm_fwd(const void *x, ss_dtype dtype, int64_t x_stride, int
 /* Bytes of workspace ss_layer_norm_bwd needs; 0 for sizes outside the limits. */
 size_t ss_layer_norm_workspace_bytes(int64_t n, int32_t D);
 
-/* dy, x, dx: device [n][D] of `dtype` (dx may be dy or x); mean, rstd: the
+/* dy, x, dx: device [n][D] of `dtype` (dx may be dy or x, row for row); mean, rstd: the
  * forward's; dgamma, dbeta: device [D] of param_dtype, overwritten (n = 0:
  * with zeros), both NULL if not wanted; workspace: device, 256-byte aligned,
  * >= ss_layer_norm_workspace_bytes (not read where dgamma and dbeta are
