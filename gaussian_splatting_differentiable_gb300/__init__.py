@@ -2,7 +2,8 @@
 
 The compute path is libss.so (hand-written CUDA for sm_103a behind the C ABI
 of include/ss.h, include/ss_project.h and include/ss_ssim.h, and of the training
-operators' include/ss_embed.h, include/ss_norm.h and include/ss_clip.h).  This
+operators' include/ss_embed.h, include/ss_norm.h, include/ss_clip.h,
+include/ss_rows8.h, include/ss_rms.h and include/ss_dense.h).  This
 module is its thin Python binding: each ss_* function
 here has the C function's name and arguments and only marshals torch tensors
 (device memory) and streams into pointers.  PyTorch provides memory and
@@ -18,8 +19,9 @@ import dataclasses
 import torch
 
 from . import _lib
-from ._lib import (SS_ACCUM_WEIGHT, SS_BF16, SS_DISTORTION, SS_ERR_CAPACITY,  # noqa: F401
-                   SS_ERR_DEVICE, SS_ERR_TIMEOUT, SS_F16, SS_F32, SS_MEDIAN_DEPTH, SS_OK, SS_RECORDS_CLEARED, SS_WEIGHT_STATS,
+from ._lib import (SS_ACCUM_WEIGHT, SS_BF16, SS_DISTORTION, SS_E4M3, SS_ERR_CAPACITY,  # noqa: F401
+                   SS_ERR_DEVICE, SS_ERR_TIMEOUT, SS_F16, SS_F32, SS_INT8,
+                   SS_MEDIAN_DEPTH, SS_OK, SS_RECORDS_CLEARED, SS_WEIGHT_STATS,
                    STATUS_NAMES, SsGrads, SsSplats)
 
 _L = _lib.load()
@@ -692,10 +694,15 @@ class LayerNorm:
         return y
 
     def backward(self, dy, x, gamma=None, mean=None, rstd=None, stream=None) -> torch.Tensor:
-        """mean, rstd: the forward's, this object's own if not given."""
+        """x: the forward's, or the Rows8 that keeps it in 8 bits; mean, rstd: the
+        forward's, this object's own if not given."""
         dyp, dys = self._input(dy, "dy")
-        xp, xs = self._input(x, "x")
         n, D = self.n, self.D
+        in8 = isinstance(x, Rows8)
+        if in8:
+            x._sized(n, D, "x")
+        else:
+            xp, xs = self._input(x, "x")
         gp = None if gamma is None else _vector(gamma, "gamma", D, self.param_dtype)
         dx, ws = self._dx, self._workspace
         if dx is None:
@@ -704,6 +711,14 @@ class LayerNorm:
             raise ValueError("mean and rstd must be given to a LayerNorm made without forward=True")
         mp = self._mean.data_ptr() if mean is None else _vector(mean, "mean", n, torch.float32)
         rp = self._rstd.data_ptr() if rstd is None else _vector(rstd, "rstd", n, torch.float32)
+        if in8:
+            st = _L.ss_layer_norm_bwd8(dyp, dys, x.c, self._code, n, D, gp, self._param_code, mp,
+                                       rp, dx.data_ptr(), D, self._dgamma.data_ptr(),
+                                       self._dbeta.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                       _stream(stream))
+            if st:
+                _check(st, "ss_layer_norm_bwd8")
+            return dx
         st = _L.ss_layer_norm_bwd(dyp, dys, xp, xs, self._code, n, D, gp, self._param_code, mp, rp,
                                   dx.data_ptr(), D, self._dgamma.data_ptr(),
                                   self._dbeta.data_ptr(), ws.data_ptr(), ws.nbytes,
@@ -711,6 +726,313 @@ class LayerNorm:
         if st:
             _check(st, "ss_layer_norm_bwd")
         return dx
+
+
+# ---- rows in 8 bits (ss_rows8.h)
+
+FORMAT_CODES = {torch.int8: SS_INT8, torch.float8_e4m3fn: SS_E4M3}
+
+
+def _format(format) -> int:
+    code = FORMAT_CODES.get(format)
+    if code is None:
+        raise ValueError("format must be int8 or float8_e4m3fn (got %s)" % format)
+    return code
+
+
+def _rows8(r, name: str, n: int, D: int):
+    """The C struct of a Rows8 of n rows of D, None for None."""
+    if r is None:
+        return None
+    if not isinstance(r, Rows8):
+        raise ValueError("%s must be a Rows8 (got %s)" % (name, type(r).__name__))
+    r._sized(n, D, name)
+    return r.c
+
+
+class Rows8:
+    """n rows of D values in 8 bits, with a power-of-two scale for every 32
+    columns: `q` [n, D] (int8 or float8_e4m3fn; its rows start on 8-byte
+    boundaries) and `scales` uint8 [n, (D + 31) // 32], biased exponents.
+    Element (i, j) reads as q[i, j] * 2^(scales[i, j // 32] - 127), and as NaN
+    where that byte is 255.  The rows belong to one stream at a time."""
+
+    def __init__(self, n: int, D: int, format=torch.int8, device="cuda"):
+        d = _device(device)
+        code = _format(format)
+        if not (0 <= n < 1 << 31 and 1 <= D <= 65536):
+            raise ValueError("sizes out of range")
+        self._n, self._D, self._format = n, D, format
+        stride, groups = (D + 7) // 8 * 8, (D + 31) // 32
+        self._buf = torch.empty(n, stride, dtype=torch.uint8, device=d)
+        self._q = self._buf.view(format)[:, :D]
+        self._scales = torch.empty(n, groups, dtype=torch.uint8, device=d)
+        self._c = _lib.SsRows8(self._buf.data_ptr(), stride, self._scales.data_ptr(), groups, code,
+                               0)
+
+    n = property(lambda self: self._n)
+    D = property(lambda self: self._D)
+    format = property(lambda self: self._format)
+    q = property(lambda self: self._q)
+    scales = property(lambda self: self._scales)
+    c = property(lambda self: self._c)
+
+    def _sized(self, n: int, D: int, name: str):
+        if self._n != n or self._D != D:
+            raise ValueError("%s must be %d rows of %d (got %d of %d)"
+                             % (name, n, D, self._n, self._D))
+
+    def pack(self, x, stream=None) -> "Rows8":
+        """x [n, D] rounded into these rows; returns this object."""
+        code = _dtype(x, "x")
+        xp, xs = _rows(x, "x", self._D, self._n)
+        st = _L.ss_rows8_pack(xp, code, xs, self._n, self._D, self._c, _stream(stream))
+        if st:
+            _check(st, "ss_rows8_pack")
+        return self
+
+    def unpack(self, out, stream=None) -> torch.Tensor:
+        """out [n, D] overwritten with what the rows hold; returns it."""
+        code = _dtype(out, "out")
+        op, os_ = _rows(out, "out", self._D, self._n)
+        st = _L.ss_rows8_unpack(self._c, self._n, self._D, op, code, os_, _stream(stream))
+        if st:
+            _check(st, "ss_rows8_unpack")
+        return out
+
+
+# ---- root-mean-square norm (ss_rms.h)
+
+def ss_rms_norm_workspace_bytes(n: int, D: int) -> int:
+    return int(_L.ss_rms_norm_workspace_bytes(n, D))
+
+
+def ss_rms_norm_fwd(x, residual, gamma, eps: float, sum=None, y=None, out=None, kept=None,
+                    rstd=None, stream=None) -> None:
+    """sum = x + residual (both or neither), y = sum * rstd * gamma over the rows
+    of x [n, D]; out: a Rows8 for y in 8 bits; kept: a Rows8 for sum (x without a
+    residual) in 8 bits; rstd: float32 [n]; gamma [D] or None."""
+    n, D = x.shape
+    code = _dtype(x, "x")
+    xp, xs = _rows(x, "x", D)
+    ptrs = []
+    for t, name in ((residual, "residual"), (sum, "sum"), (y, "y")):
+        if t is not None and t.dtype != x.dtype:
+            raise ValueError("%s must have x's type" % name)
+        ptrs += (None, 0) if t is None else _rows(t, name, D, n)
+    gp, gc = (None, SS_F32) if gamma is None else _param(gamma, "gamma", D, code, x.dtype)
+    rp = None if rstd is None else _vector(rstd, "rstd", n, torch.float32)
+    st = _L.ss_rms_norm_fwd(xp, code, xs, ptrs[0], ptrs[1], n, D, gp, gc, eps, *ptrs[2:],
+                            _rows8(out, "out", n, D), _rows8(kept, "kept", n, D), rp,
+                            _stream(stream))
+    if st:
+        _check(st, "ss_rms_norm_fwd")
+
+
+def ss_rms_norm_bwd(dy, h, gamma, rstd, dsum, dx, dgamma, workspace, stream=None) -> None:
+    """dx [n, D], and dgamma [D] unless it is None, from dy, the forward's sum h
+    (rows, or the Rows8 that keeps them), gamma, rstd and the gradient dsum of the
+    sum's other use (None for none); dx may be dy, dsum or h."""
+    n, D = dy.shape
+    code = _dtype(dy, "dy")
+    dyp, dys = _rows(dy, "dy", D)
+    in8 = isinstance(h, Rows8)
+    ptrs = []
+    for t, name in ((None if in8 else h, "h"), (dsum, "dsum"), (dx, "dx")):
+        if t is not None and t.dtype != dy.dtype:
+            raise ValueError("%s must have dy's type" % name)
+        ptrs += (None, 0) if t is None else _rows(t, name, D, n)
+    gp, pc = (None, None) if gamma is None else _param(gamma, "gamma", D, code, dy.dtype)
+    dgp = None
+    if dgamma is not None:
+        dgp, c = _param(dgamma, "dgamma", D, code, dy.dtype)
+        if pc is not None and c != pc:
+            raise ValueError("gamma and dgamma must have one type")
+        pc = c
+    rp = _vector(rstd, "rstd", n, torch.float32)
+    wp, wb = (None, 0) if workspace is None else _scratch(workspace)
+    st = _L.ss_rms_norm_bwd(dyp, dys, ptrs[0], ptrs[1], _rows8(h, "h", n, D) if in8 else None, code,
+                            n, D, gp, SS_F32 if pc is None else pc, rp, *ptrs[2:], dgp, wp, wb,
+                            _stream(stream))
+    if st:
+        _check(st, "ss_rms_norm_bwd")
+
+
+class RMSNorm:
+    """Buffers of the root-mean-square norm of n rows of D values.  The forward's:
+    `sum` (x + residual, where residual=True), `y` or, where `out` names a format
+    (int8 or float8_e4m3fn), the Rows8 `out`; the Rows8 `kept` (the sum, or x, in 8
+    bits) where `keep` names one; `rstd`.  The backward's: `dx` and `grads`
+    (dgamma).  They belong to one stream at a time, as Embedding's do.  param_dtype
+    is that of gamma and its gradient."""
+
+    def __init__(self, n: int, D: int, eps: float = 1e-5, dtype=torch.float32,
+                 param_dtype=torch.float32, device="cuda", forward: bool = True,
+                 backward: bool = True, residual: bool = False, out=None, keep=None):
+        d = _device(device)
+        self.n, self.D, self.eps = n, D, float(eps)
+        self.dtype, self._code = dtype, _code(dtype, "dtype")
+        self.param_dtype, self._param_code = param_dtype, _code(param_dtype, "param_dtype")
+        if param_dtype != dtype and param_dtype != torch.float32:
+            raise ValueError("param_dtype must be float32 or the rows' type")
+        nb = ss_rms_norm_workspace_bytes(n, D)
+        if nb == 0:
+            raise ValueError("sizes out of range")
+        if not forward and (residual or out is not None or keep is not None):
+            raise ValueError("residual, out and keep are the forward's")
+        self._forward, self._residual = forward, bool(residual)
+        self._sum = self._y = self._out = self._kept = self._rstd = None
+        self._dx = self._workspace = self.grads = None
+        if forward:
+            if residual:
+                self._sum = torch.empty(n, D, dtype=dtype, device=d)
+            if out is None:
+                self._y = torch.empty(n, D, dtype=dtype, device=d)
+            else:
+                self._out = Rows8(n, D, out, d)
+            if keep is not None:
+                self._kept = Rows8(n, D, keep, d)
+            self._rstd = torch.empty(n, dtype=torch.float32, device=d)
+        if backward:
+            self._dx = torch.empty(n, D, dtype=dtype, device=d)
+            self._dgamma = torch.empty(D, dtype=param_dtype, device=d)
+            self.grads = {"dgamma": self._dgamma}
+            self._workspace = _workspace(nb, d)
+
+    sum = property(lambda self: self._sum)
+    y = property(lambda self: self._y)
+    out = property(lambda self: self._out)
+    kept = property(lambda self: self._kept)
+    rstd = property(lambda self: self._rstd)
+    dx = property(lambda self: self._dx)
+    workspace = property(lambda self: self._workspace)
+
+    def _input(self, t, name: str):
+        if t.dtype is not self.dtype:
+            raise ValueError("%s must be %s (got %s)" % (name, self.dtype, t.dtype))
+        return _rows(t, name, self.D, self.n)
+
+    def forward(self, x, gamma=None, residual=None, stream=None):
+        """`out` where the output is in 8 bits, else `y`."""
+        if not self._forward:
+            raise ValueError("this RMSNorm was made without forward=True")
+        if (residual is not None) != self._residual:
+            raise ValueError("this RMSNorm was made with residual=%s" % self._residual)
+        D = self.D
+        xp, xs = self._input(x, "x")
+        rp, rs = (None, 0) if residual is None else self._input(residual, "residual")
+        gp = None if gamma is None else _vector(gamma, "gamma", D, self.param_dtype)
+        h, y, o, k = self._sum, self._y, self._out, self._kept
+        st = _L.ss_rms_norm_fwd(xp, self._code, xs, rp, rs, self.n, D, gp, self._param_code,
+                                self.eps, None if h is None else h.data_ptr(), D,
+                                None if y is None else y.data_ptr(), D,
+                                None if o is None else o._c, None if k is None else k._c,
+                                self._rstd.data_ptr(), _stream(stream))
+        if st:
+            _check(st, "ss_rms_norm_fwd")
+        return y if o is None else o
+
+    def backward(self, dy, x=None, gamma=None, dsum=None, rstd=None, stream=None) -> torch.Tensor:
+        """x: the forward's sum (x without a residual) as rows or as the Rows8 that
+        keeps it, this object's own `kept` or else `sum` if not given; dsum: the
+        gradient of the sum's other use, None for none; rstd: the forward's, this
+        object's own if not given."""
+        n, D = self.n, self.D
+        dx, ws = self._dx, self._workspace
+        if dx is None:
+            raise ValueError("this RMSNorm was made without backward=True")
+        if x is None:
+            x = self._sum if self._kept is None else self._kept
+            if x is None:
+                raise ValueError("x must be given to an RMSNorm that keeps neither its sum nor rows in 8 bits")
+        if rstd is None and self._rstd is None:
+            raise ValueError("rstd must be given to an RMSNorm made without forward=True")
+        dyp, dys = self._input(dy, "dy")
+        if isinstance(x, Rows8):
+            x._sized(n, D, "x")
+            xp, xs, kp = None, 0, x._c
+        else:
+            xp, xs = self._input(x, "x")
+            kp = None
+        gp = None if gamma is None else _vector(gamma, "gamma", D, self.param_dtype)
+        sp, ss_ = (None, 0) if dsum is None else self._input(dsum, "dsum")
+        rp = self._rstd.data_ptr() if rstd is None else _vector(rstd, "rstd", n, torch.float32)
+        st = _L.ss_rms_norm_bwd(dyp, dys, xp, xs, kp, self._code, n, D, gp, self._param_code, rp,
+                                sp, ss_, dx.data_ptr(), D, self._dgamma.data_ptr(), ws.data_ptr(),
+                                ws.nbytes, _stream(stream))
+        if st:
+            _check(st, "ss_rms_norm_bwd")
+        return dx
+
+
+# ---- weight gradient of a dense layer (ss_dense.h)
+
+def ss_dense_grad8_workspace_bytes(n: int, N: int, D: int) -> int:
+    return int(_L.ss_dense_grad8_workspace_bytes(n, N, D))
+
+
+def ss_dense_grad8(dy, x, dweight, dbias, workspace, stream=None) -> None:
+    """dweight [N, D] and, unless it is None, dbias [N] from dy [n, N] and the
+    layer's input x, a Rows8 of n rows of D."""
+    n, N = dy.shape
+    code = _dtype(dy, "dy")
+    dyp, dys = _rows(dy, "dy", N)
+    D = dweight.shape[-1]
+    if dweight.dtype not in (dy.dtype, torch.float32):
+        raise ValueError("dweight must be float32 or dy's type (got %s)" % dweight.dtype)
+    wp, wstride = _rows(dweight, "dweight", D, N)
+    bp = None if dbias is None else _vector(dbias, "dbias", N, dweight.dtype)
+    if x is None:
+        raise ValueError("x must be a Rows8")
+    xc = _rows8(x, "x", n, D)
+    sp, sb = _scratch(workspace)
+    st = _L.ss_dense_grad8(dyp, code, dys, xc, n, N, D, wp, wstride, bp, DTYPE_CODES[dweight.dtype],
+                           sp, sb, _stream(stream))
+    if st:
+        _check(st, "ss_dense_grad8")
+
+
+class DenseGrad:
+    """Buffers of the weight gradient of a dense layer y = x W^T + b over n rows,
+    W [N, D], whose input was kept in 8 bits: `grads` (dweight [N, D], dbias [N]
+    unless bias=False).  They belong to one stream at a time, as Embedding's do."""
+
+    def __init__(self, n: int, N: int, D: int, dtype=torch.float32, grad_dtype=torch.float32,
+                 bias: bool = True, device="cuda"):
+        d = _device(device)
+        self.n, self.N, self.D = n, N, D
+        self.dtype, self._code = dtype, _code(dtype, "dtype")
+        self.grad_dtype, self._grad_code = grad_dtype, _code(grad_dtype, "grad_dtype")
+        if grad_dtype != dtype and grad_dtype != torch.float32:
+            raise ValueError("grad_dtype must be float32 or the rows' type")
+        nb = ss_dense_grad8_workspace_bytes(n, N, D)
+        if nb == 0:
+            raise ValueError("sizes out of range")
+        self._dweight = torch.empty(N, D, dtype=grad_dtype, device=d)
+        self._dbias = torch.empty(N, dtype=grad_dtype, device=d) if bias else None
+        self.grads = {"dweight": self._dweight}
+        if bias:
+            self.grads["dbias"] = self._dbias
+        self._workspace = _workspace(nb, d)
+
+    workspace = property(lambda self: self._workspace)
+
+    def backward(self, dy, x, stream=None) -> torch.Tensor:
+        """dweight from dy [n, N] and the Rows8 x [n, D]; dbias beside it."""
+        if dy.dtype is not self.dtype:
+            raise ValueError("dy must be %s (got %s)" % (self.dtype, dy.dtype))
+        n, N, D = self.n, self.N, self.D
+        dyp, dys = _rows(dy, "dy", N, n)
+        if not isinstance(x, Rows8):
+            raise ValueError("x must be a Rows8 (got %s)" % type(x).__name__)
+        x._sized(n, D, "x")
+        b, ws = self._dbias, self._workspace
+        st = _L.ss_dense_grad8(dyp, self._code, dys, x._c, n, N, D, self._dweight.data_ptr(), D,
+                               None if b is None else b.data_ptr(), self._grad_code, ws.data_ptr(),
+                               ws.nbytes, _stream(stream))
+        if st:
+            _check(st, "ss_dense_grad8")
+        return self._dweight
 
 
 # ---- gradient norm and clipping (ss_clip.h)

@@ -1,6 +1,8 @@
 """ctypes prototypes of libss.so (the C ABI declared in include/ss.h,
 include/ss_project.h and include/ss_ssim.h, and the training operators of
-include/ss_embed.h, include/ss_norm.h and include/ss_clip.h).
+include/ss_embed.h, include/ss_norm.h and include/ss_clip.h, and those for
+activations in 8 bits, include/ss_rows8.h, include/ss_rms.h and
+include/ss_dense.h).
 
 Loading fails with an ImportError when the library has not been built: there
 is no fallback implementation behind this package.
@@ -26,6 +28,7 @@ SS_WEIGHT_STATS = 4
 SS_DISTORTION = 8
 SS_RECORDS_CLEARED = 16   # bwd: the forward already cleared the gradient records
 SS_F32, SS_F16, SS_BF16 = range(3)   # ss_dtype
+SS_INT8, SS_E4M3 = range(2)   # ss_format8
 
 
 class SsSplats(ctypes.Structure):
@@ -117,6 +120,31 @@ TRAIN_PROTOTYPES = {
     "ss_grad_norm": (ctypes.c_int, [P, I32, P, P, SZ, P]),
 }
 
+
+
+class SsRows8(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("scale_stride", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+# activations in 8 bits: ss_rows8.h, ss_rms.h, ss_dense.h
+R8 = ctypes.POINTER(SsRows8)
+ROWS8_PROTOTYPES = {
+    "ss_rows8_pack": (ctypes.c_int, [P, I32, I64, I64, I32, R8, P]),
+    "ss_rows8_unpack": (ctypes.c_int, [R8, I64, I32, P, I32, I64, P]),
+    "ss_rms_norm_fwd": (ctypes.c_int, [P, I32, I64, P, I64, I64, I32, P, I32, F32, P, I64, P, I64,
+                                       R8, R8, P, P]),
+    "ss_rms_norm_workspace_bytes": (SZ, [I64, I32]),
+    "ss_layer_norm_bwd8_workspace_bytes": (SZ, [I64, I32]),
+    "ss_rms_norm_bwd": (ctypes.c_int, [P, I64, P, I64, R8, I32, I64, I32, P, I32, P, P, I64, P,
+                                       I64, P, P, SZ, P]),
+    "ss_layer_norm_bwd8": (ctypes.c_int, [P, I64, R8, I32, I64, I32, P, I32, P, P, P, I64, P, P,
+                                          P, SZ, P]),
+    "ss_dense_grad8_workspace_bytes": (SZ, [I64, I32, I32]),
+    "ss_dense_grad8": (ctypes.c_int, [P, I32, I64, R8, I64, I32, I32, P, I64, P, I32, P, SZ, P]),
+}
+
 _lib = None
 
 
@@ -130,7 +158,7 @@ def load(path: str | None = None):
         raise ImportError("libss.so is not built (%s); run "
                           "`python -c 'import __graft_entry__ as g; g.build()'`" % p)
     lib = ctypes.CDLL(p)
-    for name, (res, args) in {**PROTOTYPES, **TRAIN_PROTOTYPES}.items():
+    for name, (res, args) in {**PROTOTYPES, **TRAIN_PROTOTYPES, **ROWS8_PROTOTYPES}.items():
         f = getattr(lib, name)
         f.restype = res
         f.argtypes = args

@@ -1,0 +1,155 @@
+// Rows in 8 bits (model: include/ss_rows8.h): scales, encoding and decoding on
+// the device, and the checks of arguments that their entry points share.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ss_internal.h"
+#include "ss_rows8.h"
+#include "ss_vec.cuh"
+
+namespace ss {
+
+constexpr int kGroup = SS_ROWS8_GROUP;
+constexpr uint32_t kLeastExponent = 16;    // 2^-111: what q s can be stays clear of subnormals
+constexpr uint32_t kNanExponent = 255;
+
+// An ss_rows8 as kernels take it.
+struct Rows8 {
+    uint8_t *q;
+    int64_t stride;
+    uint8_t *scales;
+    int64_t scale_stride;
+};
+inline Rows8 rows8_of(const ss_rows8 *r) {
+    return r ? Rows8{static_cast<uint8_t *>(r->q), r->q_stride, r->scales, r->scale_stride} : Rows8{};
+}
+__host__ __device__ inline int groups_of(int32_t D) { return (D + kGroup - 1) / kGroup; }
+
+// The biased exponent of a group's scale, from the bits of its largest
+// magnitude: the bits' exponent less Q's, one more where the mantissa is above
+// Q's (which the addition carries into the exponent).
+template <int FMT>
+__device__ __forceinline__ uint32_t exponent_of(uint32_t bits) {
+    constexpr uint32_t carry = FMT == SS_INT8 ? 0x7fffffu - 0x7e0000u : 0x7fffffu - 0x600000u;   // 127 = 1.984375 2^6, 448 = 1.75 2^8
+    constexpr int top = FMT == SS_INT8 ? 6 : 8;
+    const int e = int((bits + carry) >> 23) - top;
+    return bits >= 0x7f800000u ? kNanExponent : uint32_t(e < int(kLeastExponent) ? int(kLeastExponent) : e);
+}
+
+// 1 / s for a scale that exponent_of gave and is not NaN's.
+__device__ __forceinline__ float inverse_of(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+// s for any byte.
+__device__ __forceinline__ float scale_of(uint32_t e) {
+    return __uint_as_float(e == kNanExponent ? 0x7fffffffu : (e == 0 ? 0x400000u : e << 23));
+}
+
+// Four values, already divided by their scale, as bytes.  SS_INT8: 1.5 2^23 added in
+// float32 rounds to a whole number, to nearest even, and leaves it in the low
+// byte as two's complement.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    if (FMT == SS_INT8) {
+        const float m = 12582912.0f;
+        const uint32_t u = __byte_perm(__float_as_uint(__fadd_rn(a, m)), __float_as_uint(__fadd_rn(b, m)), 0x0040);
+        const uint32_t v = __byte_perm(__float_as_uint(__fadd_rn(c, m)), __float_as_uint(__fadd_rn(d, m)), 0x0040);
+        return __byte_perm(u, v, 0x5410);
+    }
+    uint16_t u, v;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(u) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(d), "f"(c));
+    return uint32_t(u) | uint32_t(v) << 16;
+}
+
+// Four bytes as the float32 values that they hold before their scale.
+// SS_INT8: the byte plus 128 below 2^23's exponent is 2^23 + q + 128.
+template <int FMT>
+__device__ __forceinline__ void decode4(F2 &a, F2 &b, uint32_t w) {
+    if (FMT == SS_INT8) {
+        const uint32_t u = w ^ 0x80808080u;
+        const F2 off = both(-8388736.0f);
+        a = add2(make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)),
+                             __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441))), off);
+        b = add2(make_float2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)),
+                             __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443))), off);
+        return;
+    }
+    uint32_t lo, hi;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(uint16_t(w)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(uint16_t(w >> 16)));
+    a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+}
+
+template <int FMT>
+__device__ __forceinline__ float decode1(uint8_t q) {
+    F2 a, b;
+    decode4<FMT>(a, b, q);
+    return a.x;
+}
+
+// ------------------------------------------------------------------ checks
+
+constexpr int32_t kMaxWidth = 65536;
+inline bool row_sizes_ok(int64_t n, int32_t D) { return n >= 0 && n < (int64_t(1) << 31) && D >= 1 && D <= kMaxWidth; }
+
+inline ss_status check_row_sizes(const char *who, int64_t n, int32_t D) {
+    if (!row_sizes_ok(n, D))
+        return fail(SS_ERR_UNSUPPORTED, "%s: %lld rows of %d outside 0..2^31-1 x 1..%d", who, (long long)n, D, kMaxWidth);
+    return SS_OK;
+}
+inline ss_status check_row_types(const char *who, int dtype, int pdt) {
+    if (!dtype_known(dtype)) return fail(SS_ERR_INVALID_ARG, "%s: unknown dtype %d", who, dtype);
+    if (pdt != SS_F32 && pdt != dtype)
+        return fail(SS_ERR_INVALID_ARG, "%s: type %d of the weights is neither SS_F32 nor the rows' type", who, pdt);
+    return SS_OK;
+}
+inline ss_status check_row_tensor(const char *who, const char *what, const void *p, int64_t stride, int32_t D, int dtype) {
+    if (!p) return fail(SS_ERR_INVALID_ARG, "%s: %s is NULL", who, what);
+    if (!aligned_to(p, dtype_bytes(dtype)))
+        return fail(SS_ERR_INVALID_ARG, "%s: %s is not aligned to its type", who, what);
+    if (stride < D || stride > (int64_t(1) << 31))
+        return fail(SS_ERR_INVALID_ARG, "%s: %s stride %lld below %d or above 2^31", who, what, (long long)stride, D);
+    return SS_OK;
+}
+inline ss_status check_aligned(const char *who, const char *what, const void *p, int dtype) {
+    if (p && !aligned_to(p, dtype_bytes(dtype)))
+        return fail(SS_ERR_INVALID_ARG, "%s: %s is not aligned to its type", who, what);
+    return SS_OK;
+}
+inline ss_status check_rows8(const char *who, const char *what, const ss_rows8 *r, int32_t D) {
+    if (!r) return fail(SS_ERR_INVALID_ARG, "%s: %s is NULL", who, what);
+    if (r->format != SS_INT8 && r->format != SS_E4M3)
+        return fail(SS_ERR_INVALID_ARG, "%s: %s has the unknown format %d", who, what, r->format);
+    if (r->reserved != 0) return fail(SS_ERR_INVALID_ARG, "%s: %s: reserved is not 0", who, what);
+    if (!r->q || !r->scales) return fail(SS_ERR_INVALID_ARG, "%s: %s: q or scales is NULL", who, what);
+    if (!aligned_to(r->q, 8)) return fail(SS_ERR_INVALID_ARG, "%s: %s: q is not 8-byte aligned", who, what);
+    if (r->q_stride % 8 != 0 || r->q_stride < (D + 7) / 8 * 8 || r->q_stride > (int64_t(1) << 31))
+        return fail(SS_ERR_INVALID_ARG, "%s: %s: q_stride %lld is no multiple of 8 that holds %d, or above 2^31", who,
+                    what, (long long)r->q_stride, D);
+    if (r->scale_stride < groups_of(D) || r->scale_stride > (int64_t(1) << 31))
+        return fail(SS_ERR_INVALID_ARG, "%s: %s: scale_stride %lld below %d or above 2^31", who, what,
+                    (long long)r->scale_stride, groups_of(D));
+    return SS_OK;
+}
+inline ss_status check_workspace(const char *who, const void *ws, size_t have, size_t need) {
+    if (!ws || !aligned_to(ws, 256))
+        return fail(SS_ERR_INVALID_ARG, "%s: workspace NULL or not 256-byte aligned", who);
+    if (have < need) return fail(SS_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu", who, have, need);
+    return SS_OK;
+}
+
+// f(T{}, integral_constant<FMT>) for run-time codes.
+template <typename F>
+void with_type(int dtype, F &&f) {
+    if (dtype == SS_F32)
+        f(float());
+    else if (dtype == SS_F16)
+        f(__half());
+    else
+        f(__nv_bfloat16());
+}
+
+}  // namespace ss

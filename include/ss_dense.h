@@ -1,0 +1,43 @@
+/*
+ * ss_dense.h -- C ABI of libss.so, part 9: the weight gradient of a dense
+ * layer y = x W^T + b whose input x was kept in 8 bits (ss_rows8.h).
+ *
+ *   dW[i][j] = sum over rows m of dy[m][i] x[m][j],   db[i] = sum of dy[m][i]
+ *
+ * x[m][j] is q s as it is held; every product is exact in the sums' terms
+ * (x in bfloat16, dy as the sum of one, two or three bfloat16 values), and sums are float32 along
+ * splits of the rows that depend on the sizes: with those the same, the same inputs
+ * give the same bits.
+ *
+ * Conventions are those of ss.h; rows and strides those of ss_embed.h.
+ */
+#ifndef SS_DENSE_H
+#define SS_DENSE_H
+
+#include "ss.h"
+#include "ss_dtype.h"
+#include "ss_rows8.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Bytes of workspace ss_dense_grad8 needs; 0 for sizes outside the limits. */
+size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D);
+
+/* dy: device [n][N] of `dtype`; *x: n rows of D; dweight: device [N][D] of
+ * grad_dtype (SS_F32 or `dtype`), dbias: device [N] of grad_dtype, NULL if not
+ * wanted; both are overwritten (n = 0: with zeros).  workspace: device, 256-byte
+ * aligned, >= ss_dense_grad8_workspace_bytes.
+ * Errors: SS_ERR_UNSUPPORTED unless 0 <= n < 2^31, 1 <= N <= 65536 and
+ * 1 <= D <= 65536; SS_ERR_INVALID_ARG for a NULL or misaligned pointer, an unknown type or
+ * format, a stride too small, a small or misaligned workspace. */
+ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x,
+                         int64_t n, int32_t N, int32_t D, void *dweight, int64_t dweight_stride,
+                         void *dbias, ss_dtype grad_dtype, void *workspace,
+                         size_t workspace_bytes, ss_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* SS_DENSE_H */
