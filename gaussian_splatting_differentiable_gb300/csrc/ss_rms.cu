@@ -2,6 +2,7 @@
 // bits (model: include/ss_rms.h).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -11,6 +12,7 @@
 #include "ss_profile.h"
 #include "ss_rms.h"
 #include "ss_rows8.cuh"
+#include "ss_unit.cuh"
 
 namespace ss {
 namespace {
@@ -22,6 +24,104 @@ struct Rows {
     T *base;
     int64_t stride;
 };
+
+// A row's place in the threads.  `lanes` threads share it, thread l of them
+// holding units l, l + lanes, ... (NV of them) in registers, so the row is read
+// once.  Narrow rows (MULTI false) take a power of two of lanes inside a warp, four at
+// least, and reduce by shuffles; wide ones take whole warps and reduce through
+// shared memory and a barrier of their own.  Groups of 32 columns are four lanes side
+// by side in both.
+constexpr int kMaxRowThreads = 512;    // x 2 units = 8192 columns, the widest row held in registers
+constexpr int kMaxGroups = 4;          // rows of several warps side by side in a CTA: of two warps at least
+constexpr int kRowWarps = kMaxRowThreads / 32;
+
+struct Place {
+    int lanes, shift;   // lanes = 1 << shift where !MULTI
+    int units;          // of a row
+    int groups;         // rows side by side in a CTA
+};
+
+bool in_registers(int32_t D) { return D <= kMaxRowThreads * 2 * kUnit; }
+
+// Up to 32 lanes a unit each; a warp with two units a lane up to 64; from there on
+// whole warps.
+Place place_of(int32_t D, int *nv, bool *multi) {
+    Place pl{};
+    pl.units = units_of(D);
+    *nv = pl.units <= 32 ? 1 : 2;
+    *multi = pl.units > 64;
+    if (*multi) {
+        pl.lanes = (pl.units + 63) / 64 * 32;
+        pl.groups = pl.lanes < kThreads ? kThreads / pl.lanes : 1;
+    } else {
+        pl.lanes = 4, pl.shift = 2;
+        while (pl.lanes * *nv < pl.units) pl.lanes <<= 1, ++pl.shift;
+        pl.groups = kThreads / pl.lanes;
+    }
+    return pl;
+}
+
+// Sums K values over the row's lanes; every lane gets the same sums (one
+// fixed order).  MULTI alternates two buffers, so one barrier a sum is enough;
+// their slots past the row's warps hold zeros.
+template <int K, bool MULTI>
+__device__ __forceinline__ void row_sum(float (&v)[K], const Place &pl, int group, int lane,
+                                        float (*s_red)[K][kRowWarps], int &flip) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (MULTI || o < pl.lanes)
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    if (!MULTI) return;
+    if ((lane & 31) == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k) s_red[flip][k][lane >> 5] = v[k];
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(pl.lanes) : "memory");
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const float4 *q = reinterpret_cast<const float4 *>(s_red[flip][k]);
+        v[k] = 0.0f;
+        for (int w = 0; w < pl.lanes; w += 128) {
+            const float4 t = q[w >> 7];
+            v[k] += (t.x + t.y) + (t.z + t.w);
+        }
+    }
+    flip ^= 1;
+}
+
+// Where a thread's units lie.
+struct Units {
+    int lane, lanes;
+    int32_t D;
+    bool first, last;    // of the lanes of a warp that share a row
+    __device__ __forceinline__ int at(int k) const { return lane + k * lanes; }
+    // Elements of unit k that are a row's.
+    __device__ __forceinline__ int count(int k) const {
+        const int c = D - at(k) * kUnit;
+        return c <= 0 ? 0 : (c < kUnit ? c : kUnit);
+    }
+    __device__ __forceinline__ bool prev() const { return !first; }
+    __device__ __forceinline__ bool next(int k) const { return !last && (at(k) + 1) * kUnit < D; }
+};
+template <bool MULTI>
+__device__ __forceinline__ Units units_at(int lane, const Place &pl, int32_t D) {
+    const int l = MULTI ? lane & 31 : lane;
+    return Units{lane, pl.lanes, D, l == 0, l == (MULTI ? 31 : pl.lanes - 1)};
+}
+
+// A thread's weights in float32 (1 where there are none, and past the row).
+template <int NV>
+__device__ __forceinline__ void load_weights(F2 (&g)[NV][4], const void *w, int pdt, const Units &c) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        float f[kUnit];
+        const int j = c.at(k) * kUnit, n = w ? c.count(k) : 0;
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) f[i] = i < n ? load_param(w, pdt, j + i) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[k][i] = make_float2(f[2 * i], f[2 * i + 1]);
+    }
+}
 
 // Sum over the CTA, the same value in every thread (fixed order).
 __device__ __forceinline__ float block_sum(float v, float *s_red) {
@@ -51,6 +151,24 @@ __device__ __forceinline__ void put_group(int fmt, const Rows8 &out, int64_t row
         put_group<SS_E4M3>(out, row, j, held, v);
 }
 
+// A unit into 8 bits; all lanes of a warp together.  What lies past the row is whatever the
+// unit has there, and counts for nothing.
+template <int FMT>
+__device__ __forceinline__ void put_held(const Rows8 &out, int64_t row, int u, int count, const F2 (&v)[4]) {
+    F2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = make_float2(2 * i < count ? v[i].x : 0.0f, 2 * i + 1 < count ? v[i].y : 0.0f);
+    const uint32_t e = group_exponent<FMT>(f);
+    if (count > 0) put_unit<FMT>(out, row, u, e, f);
+}
+__device__ __forceinline__ void put_held(int fmt, const Rows8 &out, int64_t row, int u, int count, const F2 (&v)[4]) {
+    if (fmt == SS_INT8)
+        put_held<SS_INT8>(out, row, u, count, v);
+    else
+        put_held<SS_E4M3>(out, row, u, count, v);
+}
+
 struct FwdArgs {
     const void *x;
     int64_t xs;
@@ -68,6 +186,80 @@ struct FwdArgs {
     int out_fmt, kept_fmt;     // -1: not wanted
     float *rstd;
 };
+
+// A row from registers: its sum with the residual, its square's mean, and every
+// output that is wanted.  The next row's loads are in flight meanwhile.
+template <typename T, int NV, bool MULTI, bool ALIGNED, bool RES>
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_rms_fwd(FwdArgs a, Place pl) {
+    __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][1][kRowWarps];
+    const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
+    const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
+    const Units c = units_at<MULTI>(lane, pl, a.D);
+    const int64_t step = int64_t(gridDim.x) * pl.groups, row0 = int64_t(blockIdx.x) * pl.groups + group;
+    int count[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) count[k] = c.count(k);
+    Raw<T> x[NV], res[NV];
+    auto load = [&](int64_t row) {
+        const T *px = static_cast<const T *>(a.x) + row * a.xs, *pr = static_cast<const T *>(a.residual) + row * a.rs;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int n = row < a.n ? count[k] : 0;
+            x[k] = load_unit<T, ALIGNED>(px + c.at(k) * kUnit, n);
+            if (RES) res[k] = load_unit<T, ALIGNED>(pr + c.at(k) * kUnit, n);
+        }
+    };
+    load(row0);
+    F2 g[NV][4];
+    load_weights<NV>(g, a.gamma, a.pdt, c);
+    if (MULTI) {
+        for (int e = threadIdx.x; e < kMaxGroups * 2 * kRowWarps; e += blockDim.x) (&s_red[0][0][0][0])[e] = 0.0f;
+        __syncthreads();
+    }
+    const float width = float(a.D);
+    int flip = 0;
+    // a warp's lanes leave together: they shuffle with one another; a row past the
+    // last is zeros, and not stored
+    const int64_t lead = MULTI ? row0 : row0 - ((threadIdx.x & 31) >> pl.shift);
+    for (int64_t base = lead; base < a.n; base += step) {
+        const int64_t row = base + (row0 - lead);
+        const bool here = row < a.n;
+        F2 h[NV][4], acc = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            floats_of(h[k], x[k]);
+            if (RES) {
+                F2 q[4];
+                floats_of(q, res[k]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[k][i] = add2(h[k][i], q[i]);
+                const Raw<T> r = raw_of<T>(h[k]);
+                store_unit<T, ALIGNED>(static_cast<T *>(a.sum) + row * a.ss_ + c.at(k) * kUnit, r, here ? count[k] : 0,
+                                       c.prev(), c.next(k));
+                floats_of(h[k], r);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc = fma2(h[k][i], h[k][i], acc);
+        }
+        load(row + step);
+        float sum[1] = {sum_of(acc)};
+        row_sum<1, MULTI>(sum, pl, group, lane, s_red[MULTI ? group : 0], flip);
+        const float r = __frsqrt_rn(__fdiv_rn(sum[0], width) + a.eps);
+        const F2 rr = both(r);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int n = here ? count[k] : 0;
+            if (a.kept_fmt >= 0) put_held(a.kept_fmt, a.kept, row, c.at(k), n, h[k]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[k][i] = mul2(mul2(h[k][i], rr), g[k][i]);
+            if (a.y)
+                store_unit<T, ALIGNED>(static_cast<T *>(a.y) + row * a.ys + c.at(k) * kUnit, raw_of<T>(h[k]), n,
+                                       c.prev(), c.next(k));
+            if (a.out_fmt >= 0) put_held(a.out_fmt, a.out, row, c.at(k), n, h[k]);
+        }
+        if (here && lane == 0 && a.rstd) a.rstd[row] = r;
+    }
+}
 
 // A CTA a row, an element a thread, the row read again for its result.
 template <typename T>
@@ -142,8 +334,9 @@ __global__ void __launch_bounds__(kThreads) k_norm8_bwd_weights_wide(BwdArgs a) 
         dg = fmaf(d, (kept_value<T>(a, row, j) - mu) * a.rstd[row], dg);
         db += d;
     }
-    a.part[size_t(blockIdx.y) * 2 * a.D + j] = dg;
-    a.part[size_t(blockIdx.y) * 2 * a.D + a.D + j] = db;
+    const int cols = a.centred ? 2 * a.D : a.D;
+    a.part[size_t(blockIdx.y) * cols + j] = dg;
+    if (a.centred) a.part[size_t(blockIdx.y) * cols + a.D + j] = db;
 }
 
 template <typename T>
@@ -170,51 +363,334 @@ __global__ void __launch_bounds__(kThreads) k_norm8_bwd_rows_wide(BwdArgs a) {
     }
 }
 
+// A row's dy and h (HELD: kept in 8 bits) from registers, as they were loaded: widened once
+// for the sums and once more for the result, they take half the registers.  The next
+// row's loads are in flight meanwhile.  The weights' sums stay in registers over all of a
+// CTA's rows and leave one partial sum a CTA in a.part (none where it is NULL), or, where one CTA
+// has all rows, the gradients themselves.
+template <typename T, int NV, bool MULTI, bool ALIGNED, bool CENTRED, bool HELD>
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd(BwdArgs a, Place pl, bool alone) {
+    constexpr int kSums = CENTRED ? 2 : 1;
+    extern __shared__ float4 s_gamma[];      // [2 NV][threads]; at the end the sums
+    __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][kSums][kRowWarps];
+    const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
+    const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
+    const Units c = units_at<MULTI>(lane, pl, a.D);
+    const int64_t step = int64_t(gridDim.x) * pl.groups, row0 = int64_t(blockIdx.x) * pl.groups + group;
+    int count[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) count[k] = c.count(k);
+    struct Row {
+        Raw<T> dy[NV], dsum[NV], x[HELD ? 1 : NV];
+        Held q[HELD ? NV : 1];
+        float mu, r;
+    };
+    auto load = [&](Row &w, int64_t row) {
+        const bool here = row < a.n;
+        const T *pd = static_cast<const T *>(a.dy) + row * a.dys, *ps = static_cast<const T *>(a.dsum) + row * a.dss,
+                *px = static_cast<const T *>(a.h) + row * a.hs;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int n = here ? count[k] : 0, j = c.at(k) * kUnit;
+            w.dy[k] = load_unit<T, ALIGNED>(pd + j, n);
+            if (!CENTRED && a.dsum) w.dsum[k] = load_unit<T, ALIGNED>(ps + j, n);
+            if constexpr (HELD)
+                w.q[k].load(a.kept, row, c.at(k), n > 0);
+            else
+                w.x[k] = load_unit<T, ALIGNED>(px + j, n);
+        }
+        w.mu = CENTRED && here ? a.mean[row] : 0.0f;
+        w.r = here ? a.rstd[row] : 0.0f;
+    };
+    // g = (h - mean) r of unit k, zeros past the row
+    auto normed = [&](F2 (&g)[4], const Row &w, int k) {
+        if constexpr (HELD) {
+            if (a.fmt == SS_INT8)
+                w.q[k].template values<SS_INT8>(g);
+            else
+                w.q[k].template values<SS_E4M3>(g);
+        } else {
+            floats_of(g, w.x[k]);
+        }
+        const F2 rr = both(w.r), neg = both(-w.mu);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = mul2(CENTRED ? add2(g[i], neg) : g[i], rr);
+    };
+    Row w, ahead;
+    load(ahead, row0);
+    float4 *plane = s_gamma + threadIdx.x;
+    const int apart = blockDim.x;
+    {
+        F2 g[NV][4];
+        load_weights<NV>(g, a.gamma, a.pdt, c);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                plane[(2 * k + i) * apart] = make_float4(g[k][2 * i].x, g[k][2 * i].y, g[k][2 * i + 1].x, g[k][2 * i + 1].y);
+    }
+    auto weights = [&](F2 (&g)[4], int k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 q = plane[(2 * k + i) * apart];
+            g[2 * i] = make_float2(q.x, q.y), g[2 * i + 1] = make_float2(q.z, q.w);
+        }
+    };
+    if (MULTI) {
+        for (int e = threadIdx.x; e < kMaxGroups * 2 * kSums * kRowWarps; e += blockDim.x) (&s_red[0][0][0][0])[e] = 0.0f;
+        __syncthreads();
+    }
+    const float inv = 1.0f / float(a.D);
+    F2 dg[NV][4], db[NV][4];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = both(0.0f);
+    int flip = 0;
+    const int64_t lead = MULTI ? row0 : row0 - ((threadIdx.x & 31) >> pl.shift);
+    for (int64_t base = lead; base < a.n; base += step) {
+        const int64_t row = base + (row0 - lead);
+        w = ahead;
+        load(ahead, row + step);
+        F2 s0 = both(0.0f), s1 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            F2 d[4], g[4], wt[4];
+            floats_of(d, w.dy[k]);
+            normed(g, w, k);
+            weights(wt, k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dg[k][i] = fma2(d[i], g[i], dg[k][i]);
+                if (CENTRED) db[k][i] = add2(db[k][i], d[i]);
+                d[i] = mul2(d[i], wt[i]);
+                if (CENTRED) s1 = add2(s1, d[i]);
+                s0 = fma2(d[i], g[i], s0);
+            }
+        }
+        float sum[kSums];
+        sum[0] = sum_of(s0);
+        if (CENTRED) sum[kSums - 1] = sum_of(s1);
+        row_sum<kSums, MULTI>(sum, pl, group, lane, s_red[MULTI ? group : 0], flip);
+        const F2 mag = both(-sum[0] * inv), ma = both(CENTRED ? -sum[kSums - 1] * inv : 0.0f), rr = both(w.r);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            F2 d[4], g[4], wt[4];
+            floats_of(d, w.dy[k]);
+            normed(g, w, k);
+            weights(wt, k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                d[i] = mul2(d[i], wt[i]);
+                if (CENTRED) d[i] = add2(d[i], ma);
+                d[i] = mul2(fma2(g[i], mag, d[i]), rr);
+            }
+            if (!CENTRED && a.dsum) {
+                F2 u[4];
+                floats_of(u, w.dsum[k]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = add2(d[i], u[i]);
+            }
+            store_unit<T, ALIGNED>(static_cast<T *>(a.dx) + row * a.dxs + c.at(k) * kUnit, raw_of<T>(d),
+                                   row < a.n ? count[k] : 0, c.prev(), c.next(k));
+        }
+    }
+    start_dependents();
+    if (!a.part) return;
+    // The CTA's sums, in fixed order: the rows of a warp are joined by shuffles
+    // (!MULTI), then the warps or groups in turn, in gamma's place.
+    __syncthreads();                       // gamma has been read
+    const int cols = kSums * a.D;
+    const int slots = MULTI ? pl.groups : kThreads / 32;
+    float *s_sum = reinterpret_cast<float *>(s_gamma);
+    float *part = a.part + size_t(blockIdx.x) * cols;
+    const bool direct = slots == 1 && !alone;
+    float *mine = direct ? part : s_sum + size_t(MULTI ? group : threadIdx.x >> 5) * cols;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int q = 0; q < kSums; ++q)
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) {
+                const F2 t = q ? db[k][i / 2] : dg[k][i / 2];
+                float v = i & 1 ? t.y : t.x;
+                if (!MULTI)
+                    for (int o = pl.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (i < count[k] && (MULTI || (threadIdx.x & 31) < pl.lanes)) mine[q * a.D + c.at(k) * kUnit + i] = v;
+            }
+    if (direct) return;
+    __syncthreads();
+    for (int j = threadIdx.x; j < cols; j += blockDim.x) {
+        float t = 0.0f;
+        for (int v = 0; v < slots; ++v) t += s_sum[size_t(v) * cols + j];
+        if (!alone)
+            part[j] = t;
+        else if (j < a.D)
+            store_param(a.dgamma, a.pdt, j, t);
+        else
+            store_param(a.dbeta, a.pdt, j - a.D, t);
+    }
+}
+
 // The partial sums of 32 columns of [dgamma | dbeta]: 32 slices of them side by
 // side, then the slices in order.
-__global__ void __launch_bounds__(1024) k_norm8_bwd_final(const float *part, int parts, int32_t D, void *dgamma,
-                                                          void *dbeta, int pdt) {
+__global__ void __launch_bounds__(1024) k_norm8_bwd_final(const float *part, int parts, int32_t D, int cols,
+                                                          void *dgamma, void *dbeta, int pdt) {
     __shared__ float s_t[32][33];
     wait_for_previous();
     const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + c;
     float t = 0.0f;
-    if (j < 2 * D)
+    if (j < cols)
 #pragma unroll 4
-        for (int p = q; p < parts; p += 32) t += part[size_t(p) * 2 * D + j];
+        for (int p = q; p < parts; p += 32) t += part[size_t(p) * cols + j];
     s_t[q][c] = t;
     __syncthreads();
     t = s_t[c][q];                         // column q of the 32, slice c
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     const int col = blockIdx.x * 32 + q;
-    if (c != 0 || col >= 2 * D) return;
+    if (c != 0 || col >= cols) return;
     if (col < D)
         store_param(dgamma, pdt, col, t);
-    else if (dbeta)
+    else
         store_param(dbeta, pdt, col - D, t);
 }
 
 // Partial sums of the weights' gradients that the workspace has room for.
+constexpr int kMaxSmem = 200 * 1024;
 constexpr int kMaxParts = 1024;
 int64_t weight_parts(int64_t n) { return n < 1 ? 1 : (n < kMaxParts ? n : kMaxParts); }
 int wide_grid(int64_t n, int sms) { return int(n < int64_t(sms) * 8 ? n : int64_t(sms) * 8); }
 
-ss_status backward(const char *who, const BwdArgs &a, int dtype, int sms, cudaStream_t s) {
-    with_type(dtype, [&](auto t) {
-        using T = decltype(t);
+// As many CTAs as fit the device at once (times `waves` where each would have many
+// rows of few values: the later ones even out what the memory's two halves
+// take), and no more than share the rows evenly.
+template <typename K>
+int grid_of(std::atomic<unsigned long long> *known, K kernel, int threads, size_t smem, int64_t n, int groups, int waves,
+            int most, int sms) {
+    // the last answer, by what it depends on (one kernel, one architecture)
+    const unsigned long long key = (unsigned long long)(threads) << 40 | (unsigned long long)(smem) << 8;
+    const unsigned long long k = known->load(std::memory_order_relaxed);
+    int per_sm = int(k & 255);
+    if ((k ^ key) >> 8) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+            per_sm = 1;
+        known->store(key | per_sm, std::memory_order_relaxed);
+    }
+    int64_t fit = int64_t(sms) * per_sm;
+    if (n >= fit * groups * 48) fit *= waves;
+    if (fit > most) fit = most;
+    const int64_t turns = (n + fit * groups - 1) / (fit * groups);
+    const int64_t grid = (n + turns * groups - 1) / (turns * groups);
+    return int(grid < 1 ? 1 : grid);
+}
+
+// f(NV, MULTI) of a place, as constants.
+template <typename F>
+void with_place(int nv, bool multi, F &&f) {
+    if (multi)
+        f(std::integral_constant<int, 2>(), std::true_type());
+    else if (nv == 2)
+        f(std::integral_constant<int, 2>(), std::false_type());
+    else
+        f(std::integral_constant<int, 1>(), std::false_type());
+}
+template <typename F>
+void with_flag(bool b, F &&f) {
+    if (b)
+        f(std::true_type());
+    else
+        f(std::false_type());
+}
+
+template <typename T>
+void launch_fwd(const FwdArgs &a, int sms, cudaStream_t s) {
+    if (!in_registers(a.D)) {
+        SS_LAUNCH("k_rms_fwd_wide", s, k_rms_fwd_wide<T><<<wide_grid(a.n, sms), kThreads, 0, s>>>(a));
+        return;
+    }
+    const bool aligned = units_aligned<T>(a.x, a.xs) &&
+                         (!a.residual || (units_aligned<T>(a.residual, a.rs) && units_aligned<T>(a.sum, a.ss_))) &&
+                         (!a.y || units_aligned<T>(a.y, a.ys));
+    int nv;
+    bool multi;
+    const Place pl = place_of(a.D, &nv, &multi);
+    const int threads = multi ? pl.lanes * pl.groups : kThreads;
+    with_place(nv, multi, [&](auto NV, auto MULTI) {
+        with_flag(aligned, [&](auto ALIGNED) {
+            with_flag(a.residual != nullptr, [&](auto RES) {
+                auto kernel = k_rms_fwd<T, NV(), MULTI(), ALIGNED(), RES()>;
+                static std::atomic<unsigned long long> known{0};
+                const int grid = grid_of(&known, kernel, threads, 0, a.n, pl.groups, multi ? 1 : 8, 1 << 30, sms);
+                SS_LAUNCH("k_rms_fwd", s, kernel<<<grid, threads, 0, s>>>(a, pl));
+            });
+        });
+    });
+}
+
+template <typename T, bool CENTRED, bool HELD>
+ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
+    const int cols = CENTRED ? 2 * a.D : a.D;
+    const dim3 final_grid((cols + 31) / 32);
+    if (a.n == 0 || !in_registers(a.D)) {
         // the weights first: dx may overwrite dy, dsum or h
         if (a.dgamma) {
             const dim3 g((a.D + kThreads - 1) / kThreads, unsigned(a.n < 64 ? (a.n < 1 ? 1 : a.n) : 64));
             SS_LAUNCH("k_norm8_bwd_weights_wide", s, k_norm8_bwd_weights_wide<T><<<g, kThreads, 0, s>>>(a));
             SS_LAUNCH("k_norm8_bwd_final", s,
-                      launch_after(k_norm8_bwd_final, dim3((2 * a.D + 31) / 32), 1024, 0, s, a.part, int(g.y), a.D,
-                                   a.dgamma, a.dbeta, a.pdt));
+                      launch_after(k_norm8_bwd_final, final_grid, 1024, 0, s, a.part, int(g.y), a.D, cols, a.dgamma,
+                                   a.dbeta, a.pdt));
         }
         if (a.n > 0)
             SS_LAUNCH("k_norm8_bwd_rows_wide", s, k_norm8_bwd_rows_wide<T><<<wide_grid(a.n, sms), kThreads, 0, s>>>(a));
+        return SS_OK;
+    }
+    const bool aligned = units_aligned<T>(a.dy, a.dys) && units_aligned<T>(a.dx, a.dxs) &&
+                         (HELD || units_aligned<T>(a.h, a.hs)) && (!a.dsum || units_aligned<T>(a.dsum, a.dss));
+    int nv;
+    bool multi;
+    const Place pl = place_of(a.D, &nv, &multi);
+    const int threads = multi ? pl.lanes * pl.groups : kThreads;
+    // what one CTA takes at once needs no launch that adds up several CTAs' sums
+    const bool alone = a.n <= pl.groups;
+    ss_status st = SS_OK;
+    with_place(nv, multi, [&](auto NV, auto MULTI) {
+        with_flag(aligned, [&](auto ALIGNED) {
+            auto kernel = k_norm8_bwd<T, NV(), MULTI(), ALIGNED(), CENTRED, HELD>;
+            const int slots = MULTI() ? pl.groups : kThreads / 32;
+            size_t smem = size_t(2 * NV()) * threads * sizeof(float4);
+            const size_t sums = a.dgamma && (slots > 1 || alone) ? size_t(slots) * cols * sizeof(float) : 0;
+            if (smem < sums) smem = sums;
+            static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
+            const void *fn = (const void *)kernel;
+            if ((st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "k_norm8_bwd")) != SS_OK) return;
+            static std::atomic<unsigned long long> known{0};
+            const int grid = alone ? 1 : grid_of(&known, kernel, threads, smem, a.n, pl.groups, 1, kMaxParts, sms);
+            BwdArgs b = a;
+            if (!a.dgamma) b.part = nullptr;
+            SS_LAUNCH("k_norm8_bwd", s, kernel<<<grid, threads, smem, s>>>(b, pl, alone));
+            if (a.dgamma && !alone)
+                SS_LAUNCH("k_norm8_bwd_final", s,
+                          launch_after(k_norm8_bwd_final, final_grid, 1024, 0, s, a.part, grid, a.D, cols, a.dgamma,
+                                       a.dbeta, a.pdt));
+        });
     });
-    return check_launch(who);
+    return st;
+}
+
+ss_status backward(const char *who, const BwdArgs &a, int dtype, int sms, cudaStream_t s) {
+    ss_status st = SS_OK;
+    with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        if (a.centred)
+            st = launch_bwd<T, true, true>(a, sms, s);
+        else if (a.fmt >= 0)
+            st = launch_bwd<T, false, true>(a, sms, s);
+        else
+            st = launch_bwd<T, false, false>(a, sms, s);
+    });
+    return st != SS_OK ? st : check_launch(who);
 }
 
 }  // namespace
@@ -254,10 +730,7 @@ ss_status ss_rms_norm_fwd(const void *x, ss_dtype dtype, int64_t x_stride, const
     cudaStream_t s = (cudaStream_t)stream;
     const FwdArgs a{x, x_stride, residual, residual_stride, n, D, gamma, int(param_dtype), eps, sum, sum_stride, y,
                     y_stride, rows8_of(out), rows8_of(kept), out ? out->format : -1, kept ? kept->format : -1, rstd};
-    with_type(dtype, [&](auto t) {
-        using T = decltype(t);
-        SS_LAUNCH("k_rms_fwd_wide", s, k_rms_fwd_wide<T><<<wide_grid(n, sms), kThreads, 0, s>>>(a));
-    });
+    with_type(dtype, [&](auto t) { launch_fwd<decltype(t)>(a, sms, s); });
     return check_launch(who);
 }
 

@@ -7,44 +7,100 @@
 #include "ss_internal.h"
 #include "ss_profile.h"
 #include "ss_rows8.cuh"
+#include "ss_unit.cuh"
 
 namespace ss {
 namespace {
 
 constexpr int kThreads = 256;
 
-// A warp a group, a lane a column.
-template <typename T, int FMT>
+// A thread a unit at a time.  A row takes whole groups of four lanes (its last lanes may
+// have no unit), so that a group's maximum is two shuffles.  The units of all rows lie
+// one after the other along the threads of the grid; a thread's next unit is a grid's
+// threads on, and its row and column follow by additions.
+struct Walk {
+    int64_t n, row, rows;       // rows: whole rows in a grid's threads
+    int per_row, u, more;       // more: and units beyond them
+    __device__ __forceinline__ Walk(int64_t n_, int32_t D) : n(n_) {
+        per_row = groups_of(D) * (kGroup / kUnit);
+        const int64_t k = int64_t(blockIdx.x) * kThreads + threadIdx.x, step = int64_t(gridDim.x) * kThreads;
+        row = k / per_row, u = int(k - row * per_row);
+        rows = step / per_row, more = int(step - rows * per_row);
+    }
+    __device__ __forceinline__ void next() {
+        row += rows, u += more;
+        if (u >= per_row) u -= per_row, ++row;
+    }
+    // Elements of this unit that are a row's.
+    __device__ __forceinline__ int count(int32_t D) const {
+        const int c = D - u * kUnit;
+        return row >= n || c <= 0 ? 0 : (c < kUnit ? c : kUnit);
+    }
+};
+
+// Bound by memory.  AHEAD units' loads are in flight in a thread.
+template <typename T, int FMT, bool ALIGNED, int AHEAD>
 __global__ void __launch_bounds__(kThreads) k_rows8_pack(const T *x, int64_t xs, int64_t n, int32_t D, Rows8 out) {
-    const int G = groups_of(D), lane = threadIdx.x & 31;
-    const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
-    const int32_t held = (D + 7) / 8 * 8;
-    for (int64_t k = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); k < n * G; k += warps) {
-        const int64_t row = k / G;
-        const int g = int(k - row * G), j = g * kGroup + lane;
-        const float v = j < D ? to_float(x[row * xs + j]) : 0.0f;
-        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
-        const uint32_t e = exponent_of<FMT>(most);
-        const float z = e == kNanExponent ? 0.0f : v * inverse_of(e);
-        if (j < held) out.q[row * out.stride + j] = uint8_t(encode4<FMT>(z, 0.0f, 0.0f, 0.0f));
-        if (lane == 0) out.scales[row * out.scale_stride + g] = uint8_t(e);
+    Walk w(n, D);
+    while (__any_sync(0xffffffffu, w.row < n)) {
+        Raw<T> r[AHEAD];
+        int64_t row[AHEAD];
+        int u[AHEAD], count[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            row[k] = w.row, u[k] = w.u, count[k] = w.count(D);
+            r[k] = load_unit<T, ALIGNED>(x + row[k] * xs + u[k] * kUnit, count[k]);
+            w.next();
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            F2 f[4];
+            floats_of(f, r[k]);
+            const uint32_t e = group_exponent<FMT>(f);
+            if (count[k] > 0) put_unit<FMT>(out, row[k], u[k], e, f);
+        }
     }
 }
 
 template <typename T>
-__device__ __forceinline__ T held_to(float v) { return from_float<T>(v); }
+__device__ __forceinline__ F2 held_to(F2 v) { return v; }
 // Finite values stay finite.
 template <>
-__device__ __forceinline__ __half held_to<__half>(float v) {
-    return __float2half_rn(isnan(v) ? v : fminf(fmaxf(v, -65504.0f), 65504.0f));
+__device__ __forceinline__ F2 held_to<__half>(F2 v) {
+    return make_float2(isnan(v.x) ? v.x : fminf(fmaxf(v.x, -65504.0f), 65504.0f),
+                       isnan(v.y) ? v.y : fminf(fmaxf(v.y, -65504.0f), 65504.0f));
 }
 
-template <typename T, int FMT>
+template <typename T, int FMT, bool ALIGNED, int AHEAD>
 __global__ void __launch_bounds__(kThreads) k_rows8_unpack(Rows8 in, int64_t n, int32_t D, T *x, int64_t xs) {
-    for (int64_t row = blockIdx.x; row < n; row += gridDim.x)
-        for (int j = threadIdx.x; j < D; j += kThreads)
-            x[row * xs + j] = held_to<T>(decode1<FMT>(in.q[row * in.stride + j]) *
-                                         scale_of(in.scales[row * in.scale_stride + j / kGroup]));
+    Walk w(n, D);
+    const int lane = threadIdx.x & 31;
+    while (__any_sync(0xffffffffu, w.row < n)) {
+        Held h[AHEAD];
+        T *p[AHEAD];
+        int u[AHEAD], count[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            u[k] = w.u, count[k] = w.count(D);
+            h[k].load(in, w.row, u[k], count[k] > 0);
+            p[k] = x + w.row * xs + u[k] * kUnit;
+            w.next();
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            F2 f[4];
+            h[k].template values<FMT>(f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = held_to<T>(f[i]);
+            store_unit<T, ALIGNED>(p[k], raw_of<T>(f), count[k], u[k] > 0 && lane > 0,
+                                   (u[k] + 1) * kUnit < D && lane < 31);
+        }
+    }
+}
+
+int grid_for(int64_t n, int32_t D, int sms, int per_sm) {
+    const int64_t ctas = (n * groups_of(D) * (kGroup / kUnit) + kThreads - 1) / kThreads;
+    return int(ctas < int64_t(sms) * per_sm ? ctas : int64_t(sms) * per_sm);
 }
 
 }  // namespace
@@ -67,13 +123,19 @@ ss_status ss_rows8_pack(const void *x, ss_dtype dtype, int64_t x_stride, int64_t
     int dev = 0, sms = 0;
     if ((st = current_device(&dev, &sms, "ss_rows8_pack: device query")) != SS_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    const int64_t ctas = (n * groups_of(D) + kThreads / 32 - 1) / (kThreads / 32);
-    const int grid = int(ctas < int64_t(sms) * 8 ? ctas : int64_t(sms) * 8);
+    const Rows8 o = rows8_of(out);
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        SS_LAUNCH("k_rows8_pack", s,
-                  (out->format == SS_INT8 ? k_rows8_pack<T, SS_INT8> : k_rows8_pack<T, SS_E4M3>)<<<grid, kThreads, 0, s>>>(
-                      static_cast<const T *>(x), x_stride, n, D, rows8_of(out)));
+        const T *p = static_cast<const T *>(x);
+        const int grid = grid_for(n, D, sms, 16);
+        const bool aligned = units_aligned<T>(x, x_stride);
+        with_format(out->format, [&](auto F) {
+            constexpr int FMT = decltype(F)::value;
+            if (aligned)
+                SS_LAUNCH("k_rows8_pack", s, k_rows8_pack<T, FMT, true, 2><<<grid, kThreads, 0, s>>>(p, x_stride, n, D, o));
+            else
+                SS_LAUNCH("k_rows8_pack", s, k_rows8_pack<T, FMT, false, 2><<<grid, kThreads, 0, s>>>(p, x_stride, n, D, o));
+        });
     });
     return check_launch(who);
 }
@@ -91,12 +153,19 @@ ss_status ss_rows8_unpack(const ss_rows8 *in, int64_t n, int32_t D, void *x, ss_
     int dev = 0, sms = 0;
     if ((st = current_device(&dev, &sms, "ss_rows8_unpack: device query")) != SS_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    const int grid = int(n < int64_t(sms) * 8 ? n : int64_t(sms) * 8);
+    const Rows8 r = rows8_of(in);
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        SS_LAUNCH("k_rows8_unpack", s,
-                  (in->format == SS_INT8 ? k_rows8_unpack<T, SS_INT8> : k_rows8_unpack<T, SS_E4M3>)<<<grid, kThreads, 0, s>>>(
-                      rows8_of(in), n, D, static_cast<T *>(x), x_stride));
+        T *p = static_cast<T *>(x);
+        const int grid = grid_for(n, D, sms, 16);
+        const bool aligned = units_aligned<T>(x, x_stride);
+        with_format(in->format, [&](auto F) {
+            constexpr int FMT = decltype(F)::value;
+            if (aligned)
+                SS_LAUNCH("k_rows8_unpack", s, k_rows8_unpack<T, FMT, true, 4><<<grid, kThreads, 0, s>>>(r, n, D, p, x_stride));
+            else
+                SS_LAUNCH("k_rows8_unpack", s, k_rows8_unpack<T, FMT, false, 2><<<grid, kThreads, 0, s>>>(r, n, D, p, x_stride));
+        });
     });
     return check_launch(who);
 }

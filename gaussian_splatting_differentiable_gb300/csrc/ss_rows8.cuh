@@ -5,9 +5,11 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ss_internal.h"
 #include "ss_rows8.h"
+#include "ss_unit.cuh"
 #include "ss_vec.cuh"
 
 namespace ss {
@@ -90,6 +92,55 @@ __device__ __forceinline__ float decode1(uint8_t q) {
     return a.x;
 }
 
+// Of a group whose 32 values four lanes side by side hold, 8 each (zeros past the row): the biased
+// exponent of its scale, in all four.
+template <int FMT>
+__device__ __forceinline__ uint32_t group_exponent(const F2 (&f)[4]) {
+    // as whole numbers: NaN is the largest magnitude of all
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = max(m, max(__float_as_uint(f[i].x) & 0x7fffffffu, __float_as_uint(f[i].y) & 0x7fffffffu));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return exponent_of<FMT>(m);
+}
+
+// Unit u of a row into 8 bits, with its group's exponent beside the first of the group.
+template <int FMT>
+__device__ __forceinline__ void put_unit(const Rows8 &out, int64_t row, int u, uint32_t e, const F2 (&f)[4]) {
+    uint2 q = make_uint2(0u, 0u);
+    if (e != kNanExponent) {
+        const F2 inv = both(inverse_of(e));
+        F2 z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = mul2(f[i], inv);
+        q = make_uint2(encode4<FMT>(z[0].x, z[0].y, z[1].x, z[1].y), encode4<FMT>(z[2].x, z[2].y, z[3].x, z[3].y));
+    }
+    *reinterpret_cast<uint2 *>(out.q + row * out.stride + u * kUnit) = q;
+    if (u % (kGroup / kUnit) == 0) out.scales[row * out.scale_stride + u / (kGroup / kUnit)] = uint8_t(e);
+}
+
+// A unit as it is held.
+struct Held {
+    uint2 q;
+    uint32_t e;
+    __device__ __forceinline__ void load(const Rows8 &in, int64_t row, int u, bool here) {
+        q = make_uint2(0u, 0u), e = 127u;
+        if (!here) return;
+        q = *reinterpret_cast<const uint2 *>(in.q + row * in.stride + u * kUnit);
+        e = in.scales[row * in.scale_stride + u / (kGroup / kUnit)];
+    }
+    template <int FMT>
+    __device__ __forceinline__ void values(F2 (&f)[4]) const {
+        decode4<FMT>(f[0], f[1], q.x);
+        decode4<FMT>(f[2], f[3], q.y);
+        const F2 s = both(scale_of(e));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], s);
+    }
+};
+
 // ------------------------------------------------------------------ checks
 
 constexpr int32_t kMaxWidth = 65536;
@@ -141,7 +192,7 @@ inline ss_status check_workspace(const char *who, const void *ws, size_t have, s
     return SS_OK;
 }
 
-// f(T{}, integral_constant<FMT>) for run-time codes.
+// f of a type, of a format, for run-time codes.
 template <typename F>
 void with_type(int dtype, F &&f) {
     if (dtype == SS_F32)
@@ -150,6 +201,14 @@ void with_type(int dtype, F &&f) {
         f(__half());
     else
         f(__nv_bfloat16());
+}
+
+template <typename F>
+void with_format(int format, F &&f) {
+    if (format == SS_INT8)
+        f(std::integral_constant<int, SS_INT8>());
+    else
+        f(std::integral_constant<int, SS_E4M3>());
 }
 
 }  // namespace ss
