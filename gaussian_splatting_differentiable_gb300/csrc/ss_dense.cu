@@ -2,6 +2,7 @@
 // include/ss_dense.h).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -9,13 +10,45 @@
 #include "ss_internal.h"
 #include "ss_profile.h"
 #include "ss_rows8.cuh"
+#include "ss_unit.cuh"
 
 namespace ss {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSide = 64;       // of a CTA's tile of the weight
-constexpr int kDepth = 16;      // rows at a time
+// dW = dy^T x on the tensor cores, the rows being the sum's index: both operands
+// lie in memory with their columns side by side ("MN-major"), and go into shared memory
+// as they lie, 64 columns (128 bytes) to a row of a swizzled 8-row atom of 1 KB.
+// x becomes bfloat16 on the way, which holds it exactly.  dy is one bfloat16, or is cut into
+// as many as hold it exactly: hi, mid and lo of a float32's 24 bits, hi and lo of
+// a float16's 11; a product of each with x goes into the same float32 sums.
+//
+// A CTA has a tile TI x TJ of dW over a range of rows.  Its loader warps keep
+// AHEAD stages of kRows rows on their way in registers, convert them and store them into
+// a ring in shared memory; one thread of the last warp issues the products; at the end the
+// loaders read the sums out of the tensor memory.
+constexpr int kRows = 32;              // of a stage
+constexpr int kStep = 16;              // of one product
+constexpr int kBlock = kRows * 128;    // bytes of 64 columns of a stage
+
+template <typename T>
+constexpr int parts_of() { return sizeof(T) == 4 ? 3 : (std::is_same<T, __half>::value ? 2 : 1); }
+
+template <typename T, int TI, int TJ>
+struct Config {
+    static constexpr int kParts = parts_of<T>();
+    static constexpr bool kLarge = TI == 256;
+    static constexpr int kLoaders = kLarge ? 512 : 256;
+    static constexpr int kThreads = kLoaders + 32;
+    static constexpr int kABytes = TI / 64 * kBlock, kBBytes = TJ / 64 * kBlock;
+    static constexpr int kStageBytes = kParts * kABytes + kBBytes;
+    static constexpr int kStages = kLarge ? (kParts == 3 ? 3 : (kParts == 2 ? 4 : 6)) : 2;
+    static constexpr int kSmem = kStages * kStageBytes + 1024;      // and up to the first 1 KB boundary
+    static constexpr int kAhead = 2;
+    static constexpr int kTurnsA = kRows * (TI / kUnit) / kLoaders;
+    static constexpr int kTurnsB = kRows * (TJ / kUnit) / kLoaders < 1 ? 1 : kRows * (TJ / kUnit) / kLoaders;
+    static constexpr int kColumns = TI / 128 * TJ;                  // of tensor memory
+    static constexpr int kMinCtas = kLarge ? 1 : 2;
+};
 
 struct DenseArgs {
     const void *dy;
@@ -25,73 +58,421 @@ struct DenseArgs {
     int64_t n;
     int32_t N, D;
     int64_t rows;         // of a split
-    float *part;          // [splits][N][D], then [splits][N]
+    int splits;
+    float *part;          // [splits][N][D], then [splits][N]; not used where splits = 1
     float *part_bias;
+    void *dw;
+    int64_t dws;
+    void *db;
+    int gdt;
 };
 
-// CTA (tile of D, tile of N, split): 4 x 4 values a thread, in float32.
-template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads) k_dense_part(DenseArgs a) {
-    __shared__ float s_d[kDepth][kSide], s_x[kDepth][kSide];
-    const int i0 = blockIdx.y * kSide, j0 = blockIdx.x * kSide;
-    const int ti = threadIdx.x >> 4, tj = threadIdx.x & 15;
-    float acc[4][4] = {}, bias = 0.0f;
-    const int64_t first = int64_t(blockIdx.z) * a.rows, last = first + a.rows < a.n ? first + a.rows : a.n;
-    for (int64_t m0 = first; m0 < last; m0 += kDepth) {
-        __syncthreads();
-        for (int k = threadIdx.x; k < kDepth * kSide; k += kThreads) {
-            const int r = k / kSide, c = k % kSide;
-            const int64_t m = m0 + r;
-            s_d[r][c] = m < last && i0 + c < a.N ? to_float(static_cast<const T *>(a.dy)[m * a.dys + i0 + c]) : 0.0f;
-            s_x[r][c] = m < last && j0 + c < a.D
-                            ? decode1<FMT>(a.x.q[m * a.x.stride + j0 + c]) *
-                                  scale_of(a.x.scales[m * a.x.scale_stride + (j0 + c) / kGroup])
-                            : 0.0f;
-        }
-        __syncthreads();
-        if (threadIdx.x < kSide)
-            for (int r = 0; r < kDepth; ++r) bias += s_d[r][threadIdx.x];
-        for (int r = 0; r < kDepth; ++r)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(s_d[r][ti + 16 * u], s_x[r][tj + 16 * v], acc[u][v]);
+// ---- tensor core and barrier instructions
+
+__device__ __forceinline__ uint32_t smem_of(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void barrier_init(uint64_t *b, uint32_t count) {
+    asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(smem_of(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint64_t *b) {
+    asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(smem_of(b)) : "memory");
+}
+// Waits for the phase of that parity to end; false after some seconds, when something has gone
+// wrong.
+__device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity) {
+    for (uint32_t k = 0; k < (1u << 22); ++k) {
+        uint32_t done;
+        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done) : "r"(smem_of(b)), "r"(parity) : "memory");
+        if (done) return true;
     }
-    float *part = a.part + size_t(blockIdx.z) * a.N * a.D;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int i = i0 + ti + 16 * u, j = j0 + tj + 16 * v;
-            if (i < a.N && j < a.D) part[size_t(i) * a.D + j] = acc[u][v];
-        }
-    if (blockIdx.x == 0 && threadIdx.x < kSide && i0 + threadIdx.x < a.N)
-        a.part_bias[size_t(blockIdx.z) * a.N + i0 + threadIdx.x] = bias;
+    return false;
+}
+__device__ __forceinline__ void writes_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 64 columns of 128 bytes a row, swizzled, columns side by side: blocks of 64
+// columns kBlock apart, groups of 8 rows 1 KB apart.
+__device__ __forceinline__ uint64_t operand_at(uint32_t smem) {
+    return uint64_t((smem & 0x3ffff) >> 4) | uint64_t(kBlock >> 4) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
+           uint64_t(2) << 61;
+}
+// bfloat16 x bfloat16 into float32, both operands MN-major, 128 x n.
+__device__ __forceinline__ uint32_t product_of(int n) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | uint32_t(n >> 3) << 17 | uint32_t(128 >> 4) << 24;
+}
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(what),
+                 "r"(uint32_t(add)) : "memory");
+}
+__device__ __forceinline__ void products_arrive(uint64_t *b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(b)) : "memory");
+}
+__device__ __forceinline__ void tensor_load16(uint32_t (&v)[16], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// The splits' sums in order; [N][D], then the bias.
-__global__ void __launch_bounds__(kThreads) k_dense_join(DenseArgs a, int splits, void *dw, int64_t dws, void *db,
-                                                         int gdt) {
-    const int64_t all = int64_t(a.N) * a.D, count = all + (db ? a.N : 0);
-    for (int64_t k = int64_t(blockIdx.x) * kThreads + threadIdx.x; k < count; k += int64_t(gridDim.x) * kThreads) {
+// ---- conversion
+
+// The part of a float32 that a bfloat16's bits hold, and the rest, which is exact; an infinity
+// has no rest.
+__device__ __forceinline__ float rest_of(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const float r = x - __uint_as_float(u & 0xffff0000u);
+    return (u & 0x7fffffffu) == 0x7f800000u ? 0.0f : r;
+}
+__device__ __forceinline__ uint32_t tops(F2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
+
+__device__ __forceinline__ void store16(uint32_t at, const uint32_t (&w)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+template <int APART>
+__device__ __forceinline__ void store_parts(uint32_t at, const Raw<__nv_bfloat16> &r) { store16(at, r.w); }
+template <int APART>
+__device__ __forceinline__ void store_parts(uint32_t at, const Raw<__half> &r) {
+    F2 f[4];
+    floats_of(f, r);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi[i] = tops(f[i]);
+        lo[i] = tops(make_float2(rest_of(f[i].x), rest_of(f[i].y)));
+    }
+    store16(at, hi);
+    store16(at + APART, lo);
+}
+template <int APART>
+__device__ __forceinline__ void store_parts(uint32_t at, const Raw<float> &r) {
+    F2 f[4];
+    floats_of(f, r);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = tops(f[i]);
+        f[i] = make_float2(rest_of(f[i].x), rest_of(f[i].y));
+    }
+    store16(at, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = tops(f[i]);
+        f[i] = make_float2(f[i].x - __uint_as_float(__float_as_uint(f[i].x) & 0xffff0000u),
+                           f[i].y - __uint_as_float(__float_as_uint(f[i].y) & 0xffff0000u));
+    }
+    store16(at + APART, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = tops(f[i]);
+    store16(at + 2 * APART, w);
+}
+__device__ __forceinline__ void store_held(uint32_t at, const Held &h, int fmt) {
+    F2 f[4];
+    if (fmt == SS_INT8)
+        h.values<SS_INT8>(f);
+    else
+        h.values<SS_E4M3>(f);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<__nv_bfloat16>(f[i].x, f[i].y);
+    store16(at, w);
+}
+
+// Where a thread's units of a stage lie: `valid` units a row, the threads one
+// after the other along them, rows after rows.
+struct Turns {
+    int unit, row, rows;     // rows: of a turn; unit < 0: none
+    __device__ __forceinline__ Turns(int threads, int valid) {
+        rows = threads / valid;
+        row = threadIdx.x / valid, unit = threadIdx.x - row * valid;
+        if (row >= rows) unit = -1, row = 0;
+    }
+};
+
+template <typename T, int TI, int TJ, bool ALIGNED>
+__global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>::kMinCtas) k_dense(DenseArgs a) {
+    using C = Config<T, TI, TJ>;
+    extern __shared__ uint8_t s_raw[];
+    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages], s_done;
+    __shared__ uint32_t s_tensor, s_failed;
+    const uint32_t ring = (smem_of(s_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = s_raw + (ring - smem_of(s_raw));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int i0 = blockIdx.z * TI, j0 = blockIdx.y * TJ;
+    const int ni = a.N - i0 < TI ? a.N - i0 : TI, nj = a.D - j0 < TJ ? a.D - j0 : TJ;
+    const int64_t first = int64_t(blockIdx.x) * a.rows;
+    const int64_t last = first + a.rows < a.n ? first + a.rows : a.n;
+    const int stages = last > first ? int((last - first + kRows - 1) / kRows) : 0;
+    const bool bias = blockIdx.y == 0 && a.db;
+
+    if (threadIdx.x == 0) {
+        s_failed = 0;
+        for (int k = 0; k < C::kStages; ++k) barrier_init(&s_full[k], C::kLoaders / 32), barrier_init(&s_empty[k], 1);
+        barrier_init(&s_done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == C::kLoaders / 32) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&s_tensor)),
+                     "n"(C::kColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // columns past the matrices stay zeros
+    if (ni < TI || nj < TJ)
+        for (int k = threadIdx.x; k < C::kStages * C::kStageBytes / 16; k += C::kThreads)
+            reinterpret_cast<uint4 *>(ring_ptr)[k] = make_uint4(0u, 0u, 0u, 0u);
+    writes_to_async();
+    asm volatile("tcgen05.fence::before_thread_sync;");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;");
+    const uint32_t tensor = s_tensor;
+
+    F2 sums[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[i] = both(0.0f);
+    const Turns ta(C::kLoaders, (ni + kUnit - 1) / kUnit), tb(C::kLoaders, (nj + kUnit - 1) / kUnit);
+
+    if (warp < C::kLoaders / 32) {
+        Raw<T> ra[C::kAhead][C::kTurnsA];
+        Held rb[C::kAhead][C::kTurnsB];
+        const int ca = ta.unit < 0 ? 0 : (ni - ta.unit * kUnit < kUnit ? ni - ta.unit * kUnit : kUnit);
+        const T *pa = static_cast<const T *>(a.dy) + i0 + ta.unit * kUnit;
+        auto load = [&](Raw<T> (&va)[C::kTurnsA], Held (&vb)[C::kTurnsB], int stage) {
+            const int64_t m0 = first + int64_t(stage) * kRows;
+#pragma unroll
+            for (int k = 0; k < C::kTurnsA; ++k) {
+                const int r = ta.row + k * ta.rows;
+                const bool here = r < kRows && m0 + r < last && stage < stages;
+                va[k] = load_unit<T, ALIGNED>(pa + (m0 + r) * a.dys, here ? ca : 0);
+            }
+#pragma unroll
+            for (int k = 0; k < C::kTurnsB; ++k) {
+                const int r = tb.row + k * tb.rows;
+                const bool here = tb.unit >= 0 && r < kRows && m0 + r < last && stage < stages;
+                vb[k].load(a.x, m0 + r, j0 / kUnit + tb.unit, here);
+            }
+        };
+#pragma unroll
+        for (int q = 0; q < C::kAhead; ++q) load(ra[q], rb[q], q);
+        int slot = 0;
+        uint32_t parity = 1;
+        bool ok = true;
+        for (int base = 0; base < stages && ok; base += C::kAhead) {
+#pragma unroll
+            for (int q = 0; q < C::kAhead; ++q) {
+                const int stage = base + q;
+                if (stage >= stages) break;
+                if (!barrier_wait(&s_empty[slot], parity)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = ring + slot * C::kStageBytes;
+#pragma unroll
+                for (int k = 0; k < C::kTurnsA; ++k) {
+                    const int r = ta.row + k * ta.rows;
+                    if (ta.unit < 0 || r >= kRows) continue;
+                    store_parts<C::kABytes>(at + (ta.unit >> 3) * kBlock + r * 128 + (((ta.unit ^ r) & 7) << 4), ra[q][k]);
+                    if (bias) {
+                        F2 f[4];
+                        floats_of(f, ra[q][k]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sums[i] = add2(sums[i], f[i]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < C::kTurnsB; ++k) {
+                    const int r = tb.row + k * tb.rows;
+                    if (tb.unit < 0 || r >= kRows) continue;
+                    store_held(at + C::kParts * C::kABytes + (tb.unit >> 3) * kBlock + r * 128 + (((tb.unit ^ r) & 7) << 4),
+                               rb[q][k], a.fmt);
+                }
+                writes_to_async();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(&s_full[slot]);
+                load(ra[q], rb[q], stage + C::kAhead);
+                if (++slot == C::kStages) slot = 0, parity ^= 1;
+            }
+        }
+        if (!ok) s_failed = 1;
+        if (!barrier_wait(&s_done, 0)) s_failed = 1;
+    } else {
+        if (lane == 0) {
+            const uint32_t what = product_of((nj + 15) / 16 * 16);
+            int slot = 0;
+            uint32_t parity = 0;
+            for (int stage = 0; stage < stages; ++stage) {
+                if (!barrier_wait(&s_full[slot], parity)) {
+                    s_failed = 1;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;");
+                const uint32_t at = ring + slot * C::kStageBytes, bt = at + C::kParts * C::kABytes;
+#pragma unroll
+                for (int k = 0; k < kRows / kStep; ++k)
+#pragma unroll
+                    for (int p = 0; p < C::kParts; ++p)
+#pragma unroll
+                        for (int h = 0; h < TI / 128; ++h)
+                            if (h * 128 < ni)
+                                product(tensor + h * TJ, operand_at(at + p * C::kABytes + h * 2 * kBlock + k * kStep * 128),
+                                        operand_at(bt + k * kStep * 128), what, stage > 0 || k > 0 || p > 0);
+                products_arrive(&s_empty[slot]);
+                if (++slot == C::kStages) slot = 0, parity ^= 1;
+            }
+            products_arrive(&s_done);
+            if (!barrier_wait(&s_done, 0)) s_failed = 1;    // the tensor memory is freed after them
+        }
+        __syncwarp();
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;");
+
+    if (warp < C::kLoaders / 32) {
+        // a warp reads the 32 lanes (rows of dW) of its quarter, warps of a quarter 16 columns in turn
+        const bool zeros = stages == 0, failed = s_failed != 0;
+        const int quarter = warp & 3;
+#pragma unroll
+        for (int h = 0; h < TI / 128; ++h) {
+            if (h * 128 >= ni) break;
+            const int i = i0 + h * 128 + quarter * 32 + lane;
+            for (int c = (warp >> 2) * 16; c < nj; c += C::kLoaders / 128 * 16) {
+                uint32_t v[16];
+                __syncwarp();
+                tensor_load16(v, tensor + (uint32_t(quarter * 32) << 16) + h * TJ + c);
+                if (zeros || failed)      // a wait that ran out leaves NaN
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = failed ? 0x7fffffffu : 0u;
+                if (i >= a.N) continue;
+                const int count = nj - c < 16 ? nj - c : 16;
+                if (a.splits > 1) {
+                    float *p = a.part + (size_t(blockIdx.x) * a.N + i) * a.D + j0 + c;
+                    if (count == 16 && (reinterpret_cast<uintptr_t>(p) & 15) == 0)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            reinterpret_cast<uint4 *>(p)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    else
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (k < count) p[k] = __uint_as_float(v[k]);
+                } else {
+                    const int64_t e = int64_t(i) * a.dws + j0 + c;
+                    const uintptr_t p = reinterpret_cast<uintptr_t>(a.dw) + e * (a.gdt == SS_F32 ? 4 : 2);
+                    if (count == 16 && (p & 15) == 0 && a.gdt != SS_F32) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float x = __uint_as_float(v[2 * k]), y = __uint_as_float(v[2 * k + 1]);
+                            w[k] = a.gdt == SS_F16 ? pack2<__half>(x, y) : pack2<__nv_bfloat16>(x, y);
+                        }
+                        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else if (count == 16 && (p & 15) == 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            reinterpret_cast<uint4 *>(p)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (k < count) store_param(a.dw, a.gdt, e + k, __uint_as_float(v[k]));
+                    }
+                }
+            }
+        }
+    }
+    if (bias) {
+        // the threads' sums of a column, in the order of their rows
+        float *s = reinterpret_cast<float *>(ring_ptr);
+        const int width = (ni + kUnit - 1) / kUnit * kUnit;
+        if (warp < C::kLoaders / 32 && ta.unit >= 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<float2 *>(s + size_t(ta.row) * width + ta.unit * kUnit)[i] = sums[i];
+        __syncthreads();
+        for (int j = threadIdx.x; j < ni; j += C::kThreads) {
+            float t = 0.0f;
+            for (int r = 0; r < ta.rows; ++r) t += s[size_t(r) * width + j];
+            if (a.splits > 1)
+                a.part_bias[size_t(blockIdx.x) * a.N + i0 + j] = t;
+            else
+                store_param(a.db, a.gdt, i0 + j, t);
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;");
+    __syncthreads();
+    if (warp == C::kLoaders / 32)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(C::kColumns));
+}
+
+// The splits' sums: 32 values of [N][D], then of the bias, by 32 slices of the splits side by
+// side, then the slices in order.
+__global__ void __launch_bounds__(1024) k_dense_join(DenseArgs a) {
+    __shared__ float s_t[32][33];
+    const int64_t all = int64_t(a.N) * a.D, count = all + (a.db ? a.N : 0);
+    const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
+    for (int64_t base = int64_t(blockIdx.x) * 32; base < count; base += int64_t(gridDim.x) * 32) {
+        const int64_t k = base + c;
         float t = 0.0f;
-        for (int p = 0; p < splits; ++p) t += k < all ? a.part[size_t(p) * all + k] : a.part_bias[size_t(p) * a.N + (k - all)];
-        if (k < all)
-            store_param(dw, gdt, k / a.D * dws + k % a.D, t);
+        if (k < count) {
+            const float *p = k < all ? a.part + k : a.part_bias + (k - all);
+            const int64_t apart = k < all ? all : a.N;
+#pragma unroll 4
+            for (int v = q; v < a.splits; v += 32) t += p[v * apart];
+        }
+        __syncthreads();
+        s_t[q][c] = t;
+        __syncthreads();
+        t = s_t[c][q];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        const int64_t e = base + q;
+        if (c != 0 || e >= count) continue;
+        if (e < all)
+            store_param(a.dw, a.gdt, e / a.D * a.dws + e % a.D, t);
         else
-            store_param(db, gdt, k - all, t);
+            store_param(a.db, a.gdt, e - all, t);
     }
 }
 
-// How many ranges of rows have sums of their own: as many as give the device's
-// SMs two tiles each, of 256 rows at least.
-constexpr int kWanted = 304;
+// The tile's sides for a weight's.
+struct Tile {
+    int i, j, ctas;    // ctas: of an SM
+};
+Tile tile_of(int32_t N, int32_t D) {
+    if (N <= 128 && D <= 64) return {128, 64, 3};
+    if (N <= 128 && D <= 128) return {128, 128, 2};
+    return {256, 256, 1};
+}
+
+// Rows that a split's sum may have: the tensor core's sums lose more than float32's with
+// each addition.
+constexpr int64_t kMaxRows = 4096;
+constexpr int kSms = 152;
+
+// How many ranges of rows have sums of their own: as many as fill the device, of eight stages
+// at least, and none longer than kMaxRows.
 int splits_of(int64_t n, int32_t N, int32_t D) {
-    const int64_t tiles = int64_t((N + kSide - 1) / kSide) * ((D + kSide - 1) / kSide);
-    int64_t s = (kWanted + tiles - 1) / tiles;
-    const int64_t most = (n + 255) / 256;
+    const Tile t = tile_of(N, D);
+    const int64_t tiles = int64_t((N + t.i - 1) / t.i) * ((D + t.j - 1) / t.j);
+    int64_t s = kSms * t.ctas / tiles;
+    const int64_t most = (n + 8 * kRows - 1) / (8 * kRows), least = (n + kMaxRows - 1) / kMaxRows;
     if (s > most) s = most;
+    if (s < least) s = least;
     return int(s < 1 ? 1 : s);
+}
+
+template <typename T, int TI, int TJ>
+ss_status launch(const DenseArgs &a, cudaStream_t s) {
+    using C = Config<T, TI, TJ>;
+    const dim3 grid(a.splits, (a.D + TJ - 1) / TJ, (a.N + TI - 1) / TI);
+    const bool aligned = units_aligned<T>(a.dy, a.dys);
+    auto kernel = aligned ? k_dense<T, TI, TJ, true> : k_dense<T, TI, TJ, false>;
+    static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
+    const void *fn[2] = {(const void *)k_dense<T, TI, TJ, true>, (const void *)k_dense<T, TI, TJ, false>};
+    const ss_status st = ensure_dyn_smem(smem_ctx, fn, 2, C::kSmem, "k_dense");
+    if (st != SS_OK) return st;
+    SS_LAUNCH("k_dense", s, kernel<<<grid, C::kThreads, C::kSmem, s>>>(a));
+    return SS_OK;
 }
 
 bool dense_sizes_ok(int64_t n, int32_t N, int32_t D) { return row_sizes_ok(n, D) && N >= 1 && N <= kMaxWidth; }
@@ -105,7 +486,8 @@ extern "C" {
 
 size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D) {
     if (!dense_sizes_ok(n, N, D)) return 0;
-    return size_t(splits_of(n, N, D)) * N * (size_t(D) + 1) * sizeof(float);
+    const int splits = splits_of(n, N, D);
+    return splits > 1 ? size_t(splits) * N * (size_t(D) + 1) * sizeof(float) : 256;
 }
 
 ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n, int32_t N,
@@ -132,18 +514,23 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
     const int splits = splits_of(n, N, D);
     float *part = static_cast<float *>(workspace);
     const int64_t each = (n + splits - 1) / splits;
-    const DenseArgs a{dy, dy_stride, rows8_of(x), x ? x->format : 0, n, N, D, (each + kDepth - 1) / kDepth * kDepth,
-                      part, part + size_t(splits) * N * D};
-    const dim3 grid((D + kSide - 1) / kSide, (N + kSide - 1) / kSide, splits);
+    const DenseArgs a{dy, dy_stride, rows8_of(x), x ? x->format : 0, n, N, D, (each + kRows - 1) / kRows * kRows, splits,
+                      part, part + size_t(splits) * N * D, dweight, dweight_stride, dbias, int(grad_dtype)};
+    const Tile tile = tile_of(N, D);
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        SS_LAUNCH("k_dense_part", s,
-                  (a.fmt == SS_INT8 ? k_dense_part<T, SS_INT8> : k_dense_part<T, SS_E4M3>)<<<grid, kThreads, 0, s>>>(a));
+        if (tile.i == 256)
+            st = launch<T, 256, 256>(a, s);
+        else if (tile.j == 128)
+            st = launch<T, 128, 128>(a, s);
+        else
+            st = launch<T, 128, 64>(a, s);
     });
-    const int64_t ctas = (int64_t(N) * D + N + kThreads - 1) / kThreads;
-    SS_LAUNCH("k_dense_join", s,
-              k_dense_join<<<int(ctas < sms * 8 ? ctas : sms * 8), kThreads, 0, s>>>(a, splits, dweight, dweight_stride,
-                                                                                    dbias, grad_dtype));
+    if (st != SS_OK) return st;
+    if (splits > 1) {
+        const int64_t ctas = (int64_t(N) * D + N + 31) / 32;
+        SS_LAUNCH("k_dense_join", s, k_dense_join<<<int(ctas < sms * 16 ? ctas : sms * 16), 1024, 0, s>>>(a));
+    }
     return check_launch(who);
 }
 
