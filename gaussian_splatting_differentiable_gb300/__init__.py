@@ -967,8 +967,10 @@ class RMSNorm:
 
 # ---- weight gradient of a dense layer (ss_dense.h)
 
-def ss_dense_grad8_workspace_bytes(n: int, N: int, D: int) -> int:
-    return int(_L.ss_dense_grad8_workspace_bytes(n, N, D))
+def ss_dense_grad8_workspace_bytes(n: int, N: int, D: int, dtype=torch.float32,
+                                   grad_dtype=torch.float32) -> int:
+    return int(_L.ss_dense_grad8_workspace_bytes(n, N, D, _code(dtype, "dtype"),
+                                                 _code(grad_dtype, "grad_dtype")))
 
 
 def ss_dense_grad8(dy, x, dweight, dbias, workspace, stream=None) -> None:
@@ -1005,7 +1007,7 @@ class DenseGrad:
         self.grad_dtype, self._grad_code = grad_dtype, _code(grad_dtype, "grad_dtype")
         if grad_dtype != dtype and grad_dtype != torch.float32:
             raise ValueError("grad_dtype must be float32 or the rows' type")
-        nb = ss_dense_grad8_workspace_bytes(n, N, D)
+        nb = ss_dense_grad8_workspace_bytes(n, N, D, dtype, grad_dtype)
         if nb == 0:
             raise ValueError("sizes out of range")
         self._dweight = torch.empty(N, D, dtype=grad_dtype, device=d)

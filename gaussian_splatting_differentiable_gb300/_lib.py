@@ -141,7 +141,7 @@ ROWS8_PROTOTYPES = {
                                        I64, P, P, SZ, P]),
     "ss_layer_norm_bwd8": (ctypes.c_int, [P, I64, R8, I32, I64, I32, P, I32, P, P, P, I64, P, P,
                                           P, SZ, P]),
-    "ss_dense_grad8_workspace_bytes": (SZ, [I64, I32, I32]),
+    "ss_dense_grad8_workspace_bytes": (SZ, [I64, I32, I32, I32, I32]),
     "ss_dense_grad8": (ctypes.c_int, [P, I32, I64, R8, I64, I32, I32, P, I64, P, I32, P, SZ, P]),
 }
 

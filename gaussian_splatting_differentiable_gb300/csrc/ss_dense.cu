@@ -20,12 +20,16 @@ namespace {
 // as they lie, 64 columns (128 bytes) to a row of a swizzled 8-row atom of 1 KB.
 // x becomes bfloat16 on the way, which holds it exactly.  dy is one bfloat16, or is cut into
 // as many as hold it exactly: hi, mid and lo of a float32's 24 bits, hi and lo of
-// a float16's 11; a product of each with x goes into the same float32 sums.
+// a float16's 11.  The tensor cores cut every addition off at float32's last place, towards
+// zero, so a long chain of them loses a little of each sum: after 2048 rows 5e-7 of it.
+// So the products of mid and lo have sums of their own (with hi's they would cut those off
+// three times as often), and where dW is float32 the sums leave the tensor memory every
+// kChain32 rows and are added in float32.
 //
 // A CTA has a tile TI x TJ of dW over a range of rows.  Its loader warps keep
 // AHEAD stages of kRows rows on their way in registers, convert them and store them into
-// a ring in shared memory; one thread of the last warp issues the products; at the end the
-// loaders read the sums out of the tensor memory.
+// a ring in shared memory; one thread of the last warp issues the products; at the end of a
+// chain the loaders read the sums out of the tensor memory.
 constexpr int kRows = 32;              // of a stage
 constexpr int kStep = 16;              // of one product
 constexpr int kBlock = kRows * 128;    // bytes of 64 columns of a stage
@@ -36,17 +40,19 @@ constexpr int parts_of() { return sizeof(T) == 4 ? 3 : (std::is_same<T, __half>:
 template <typename T, int TI, int TJ>
 struct Config {
     static constexpr int kParts = parts_of<T>();
-    static constexpr bool kLarge = TI == 256;
+    static constexpr bool kLarge = TJ == 256;
+    static constexpr int kSums = kParts > 1 ? 2 : 1;
     static constexpr int kLoaders = kLarge ? 512 : 256;
     static constexpr int kThreads = kLoaders + 32;
     static constexpr int kABytes = TI / 64 * kBlock, kBBytes = TJ / 64 * kBlock;
     static constexpr int kStageBytes = kParts * kABytes + kBBytes;
-    static constexpr int kStages = kLarge ? (kParts == 3 ? 3 : (kParts == 2 ? 4 : 6)) : 2;
+    static constexpr int kStages = kLarge ? 200 * 1024 / kStageBytes : 2;
     static constexpr int kSmem = kStages * kStageBytes + 1024;      // and up to the first 1 KB boundary
     static constexpr int kAhead = 2;
     static constexpr int kTurnsA = kRows * (TI / kUnit) / kLoaders;
     static constexpr int kTurnsB = kRows * (TJ / kUnit) / kLoaders < 1 ? 1 : kRows * (TJ / kUnit) / kLoaders;
-    static constexpr int kColumns = TI / 128 * TJ;                  // of tensor memory
+    static constexpr int kTile = TI / 128 * TJ;                     // columns of tensor memory for one set of sums
+    static constexpr int kColumns = kSums * kTile;
     static constexpr int kMinCtas = kLarge ? 1 : 2;
 };
 
@@ -59,7 +65,8 @@ struct DenseArgs {
     int32_t N, D;
     int64_t rows;         // of a split
     int splits;
-    float *part;          // [splits][N][D], then [splits][N]; not used where splits = 1
+    int chain;            // stages of a chain of sums, a multiple of kAhead
+    float *part;          // [splits][N][D], then [splits][N]; not used by one split of one chain
     float *part_bias;
     void *dw;
     int64_t dws;
@@ -79,7 +86,7 @@ __device__ __forceinline__ void barrier_arrive(uint64_t *b) {
 // Waits for the phase of that parity to end; false after some seconds, when something has gone
 // wrong.
 __device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity) {
-    for (uint32_t k = 0; k < (1u << 22); ++k) {
+    for (uint32_t k = 0; k < (1u << 20); ++k) {
         uint32_t done;
         asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
                      : "=r"(done) : "r"(smem_of(b)), "r"(parity) : "memory");
@@ -190,11 +197,64 @@ struct Turns {
     }
 };
 
+// 16 sums of a row of the tile (`count` of them the weight's): added to what is in
+// part at `p` (if there is something), and stored there, or, at `e`, as dW.
+__device__ __forceinline__ void put_sums(const DenseArgs &a, size_t p, int64_t e, int count, uint32_t (&v)[16], bool add,
+                                         bool result) {
+    float *part = a.part + p;
+    const bool vectors = count == 16 && (reinterpret_cast<uintptr_t>(part) & 15) == 0;
+    if (add) {
+        if (vectors)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 q = reinterpret_cast<const float4 *>(part)[k];
+                v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) + q.x);
+                v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) + q.y);
+                v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) + q.z);
+                v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) + q.w);
+            }
+        else
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (k < count) v[k] = __float_as_uint(__uint_as_float(v[k]) + part[k]);
+    }
+    if (!result) {
+        if (vectors)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                reinterpret_cast<uint4 *>(part)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        else
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (k < count) part[k] = __uint_as_float(v[k]);
+        return;
+    }
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.dw) + e * (a.gdt == SS_F32 ? 4 : 2);
+    if (count < 16 || (at & 15) != 0) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (k < count) store_param(a.dw, a.gdt, e + k, __uint_as_float(v[k]));
+    } else if (a.gdt == SS_F32) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            reinterpret_cast<uint4 *>(at)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float x = __uint_as_float(v[2 * k]), y = __uint_as_float(v[2 * k + 1]);
+            w[k] = a.gdt == SS_F16 ? pack2<__half>(x, y) : pack2<__nv_bfloat16>(x, y);
+        }
+        reinterpret_cast<uint4 *>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 template <typename T, int TI, int TJ, bool ALIGNED>
 __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>::kMinCtas) k_dense(DenseArgs a) {
     using C = Config<T, TI, TJ>;
     extern __shared__ uint8_t s_raw[];
-    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages], s_done;
+    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages], s_done, s_drained;
     __shared__ uint32_t s_tensor, s_failed;
     const uint32_t ring = (smem_of(s_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = s_raw + (ring - smem_of(s_raw));
@@ -210,6 +270,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         s_failed = 0;
         for (int k = 0; k < C::kStages; ++k) barrier_init(&s_full[k], C::kLoaders / 32), barrier_init(&s_empty[k], 1);
         barrier_init(&s_done, 1);
+        barrier_init(&s_drained, C::kLoaders / 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == C::kLoaders / 32) {
@@ -232,6 +293,36 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
     for (int i = 0; i < 4; ++i) sums[i] = both(0.0f);
     const Turns ta(C::kLoaders, (ni + kUnit - 1) / kUnit), tb(C::kLoaders, (nj + kUnit - 1) / kUnit);
 
+    // The sums of a chain out of the tensor memory: added to what the chains before left, and to their
+    // place if it is the last.  A warp reads the 32 lanes (rows of dW) of its quarter, the warps of a
+    // quarter 16 columns in turn.
+    auto drain = [&](bool first_chain, bool last_chain) {
+        const int quarter = warp & 3;
+        const bool failed = *static_cast<volatile uint32_t *>(&s_failed) != 0;
+#pragma unroll 1
+        for (int h = 0; h < TI / 128 && h * 128 < ni; ++h) {
+            const int i = i0 + h * 128 + quarter * 32 + lane;
+#pragma unroll 1
+            for (int c = (warp >> 2) * 16; c < nj; c += C::kLoaders / 128 * 16) {
+                uint32_t v[16];
+                const uint32_t at = tensor + (uint32_t(quarter * 32) << 16) + h * TJ + c;
+                __syncwarp();
+                tensor_load16(v, at);
+                if (C::kSums > 1) {
+                    uint32_t w[16];
+                    tensor_load16(w, at + C::kTile);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
+                }
+                if (stages == 0 || failed)      // a wait that ran out leaves NaN
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = failed ? 0x7fffffffu : 0u;
+                if (i < a.N)
+                    put_sums(a, (size_t(blockIdx.x) * a.N + i) * a.D + j0 + c, int64_t(i) * a.dws + j0 + c,
+                             nj - c < 16 ? nj - c : 16, v, !first_chain, last_chain && a.splits == 1);
+            }
+        }
+    };
     if (warp < C::kLoaders / 32) {
         Raw<T> ra[C::kAhead][C::kTurnsA];
         Held rb[C::kAhead][C::kTurnsB];
@@ -254,10 +345,11 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         };
 #pragma unroll
         for (int q = 0; q < C::kAhead; ++q) load(ra[q], rb[q], q);
-        int slot = 0;
+        int slot = 0, chains = 0;
         uint32_t parity = 1;
-        bool ok = true;
-        for (int base = 0; base < stages && ok; base += C::kAhead) {
+        bool ok = true, end;
+        int base = 0;
+        do {
 #pragma unroll
             for (int q = 0; q < C::kAhead; ++q) {
                 const int stage = base + q;
@@ -292,13 +384,22 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                 load(ra[q], rb[q], stage + C::kAhead);
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
             }
-        }
-        if (!ok) s_failed = 1;
-        if (!barrier_wait(&s_done, 0)) s_failed = 1;
+            base += C::kAhead;
+            end = !ok || base >= stages;
+            if (end || base % a.chain == 0) {
+                if (!ok || !barrier_wait(&s_done, chains & 1)) s_failed = 1;
+                asm volatile("tcgen05.fence::after_thread_sync;");
+                drain(chains == 0, end);
+                asm volatile("tcgen05.fence::before_thread_sync;");
+                __syncwarp();
+                if (lane == 0) barrier_arrive(&s_drained);
+                ++chains;
+            }
+        } while (!end);
     } else {
         if (lane == 0) {
             const uint32_t what = product_of((nj + 15) / 16 * 16);
-            int slot = 0;
+            int slot = 0, chains = 0, link = 0;
             uint32_t parity = 0;
             for (int stage = 0; stage < stages; ++stage) {
                 if (!barrier_wait(&s_full[slot], parity)) {
@@ -314,72 +415,25 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
 #pragma unroll
                         for (int h = 0; h < TI / 128; ++h)
                             if (h * 128 < ni)
-                                product(tensor + h * TJ, operand_at(at + p * C::kABytes + h * 2 * kBlock + k * kStep * 128),
-                                        operand_at(bt + k * kStep * 128), what, stage > 0 || k > 0 || p > 0);
+                                product(tensor + (p > 0 ? C::kTile : 0) + h * TJ, operand_at(at + p * C::kABytes + h * 2 * kBlock + k * kStep * 128),
+                                        operand_at(bt + k * kStep * 128), what, link > 0 || k > 0 || p > 1);
                 products_arrive(&s_empty[slot]);
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
+                if (++link == a.chain && stage + 1 < stages) {
+                    products_arrive(&s_done);
+                    if (!barrier_wait(&s_drained, chains & 1)) {
+                        s_failed = 1;
+                        break;
+                    }
+                    link = 0, ++chains;
+                }
             }
             products_arrive(&s_done);
-            if (!barrier_wait(&s_done, 0)) s_failed = 1;    // the tensor memory is freed after them
+            if (!barrier_wait(&s_done, chains & 1)) s_failed = 1;    // the tensor memory is freed after them
         }
         __syncwarp();
     }
-    asm volatile("tcgen05.fence::before_thread_sync;");
     __syncthreads();
-    asm volatile("tcgen05.fence::after_thread_sync;");
-
-    if (warp < C::kLoaders / 32) {
-        // a warp reads the 32 lanes (rows of dW) of its quarter, warps of a quarter 16 columns in turn
-        const bool zeros = stages == 0, failed = s_failed != 0;
-        const int quarter = warp & 3;
-#pragma unroll
-        for (int h = 0; h < TI / 128; ++h) {
-            if (h * 128 >= ni) break;
-            const int i = i0 + h * 128 + quarter * 32 + lane;
-            for (int c = (warp >> 2) * 16; c < nj; c += C::kLoaders / 128 * 16) {
-                uint32_t v[16];
-                __syncwarp();
-                tensor_load16(v, tensor + (uint32_t(quarter * 32) << 16) + h * TJ + c);
-                if (zeros || failed)      // a wait that ran out leaves NaN
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = failed ? 0x7fffffffu : 0u;
-                if (i >= a.N) continue;
-                const int count = nj - c < 16 ? nj - c : 16;
-                if (a.splits > 1) {
-                    float *p = a.part + (size_t(blockIdx.x) * a.N + i) * a.D + j0 + c;
-                    if (count == 16 && (reinterpret_cast<uintptr_t>(p) & 15) == 0)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            reinterpret_cast<uint4 *>(p)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                    else
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (k < count) p[k] = __uint_as_float(v[k]);
-                } else {
-                    const int64_t e = int64_t(i) * a.dws + j0 + c;
-                    const uintptr_t p = reinterpret_cast<uintptr_t>(a.dw) + e * (a.gdt == SS_F32 ? 4 : 2);
-                    if (count == 16 && (p & 15) == 0 && a.gdt != SS_F32) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float x = __uint_as_float(v[2 * k]), y = __uint_as_float(v[2 * k + 1]);
-                            w[k] = a.gdt == SS_F16 ? pack2<__half>(x, y) : pack2<__nv_bfloat16>(x, y);
-                        }
-                        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    } else if (count == 16 && (p & 15) == 0) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            reinterpret_cast<uint4 *>(p)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (k < count) store_param(a.dw, a.gdt, e + k, __uint_as_float(v[k]));
-                    }
-                }
-            }
-        }
-    }
     if (bias) {
         // the threads' sums of a column, in the order of their rows
         float *s = reinterpret_cast<float *>(ring_ptr);
@@ -404,9 +458,28 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(C::kColumns));
 }
 
-// The splits' sums: 32 values of [N][D], then of the bias, by 32 slices of the splits side by
-// side, then the slices in order.
-__global__ void __launch_bounds__(1024) k_dense_join(DenseArgs a) {
+__device__ __forceinline__ void put_result(const DenseArgs &a, int64_t all, int64_t k, float t) {
+    if (k < all)
+        store_param(a.dw, a.gdt, k / a.D * a.dws + k % a.D, t);
+    else
+        store_param(a.db, a.gdt, k - all, t);
+}
+
+// The splits' sums, of [N][D] and then of the bias.  Few splits: a thread a value.
+__global__ void __launch_bounds__(256) k_dense_join(DenseArgs a) {
+    const int64_t all = int64_t(a.N) * a.D, count = all + (a.db ? a.N : 0);
+    for (int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x; k < count; k += int64_t(gridDim.x) * 256) {
+        const float *p = k < all ? a.part + k : a.part_bias + (k - all);
+        const int64_t apart = k < all ? all : a.N;
+        float t = 0.0f;
+#pragma unroll 4
+        for (int v = 0; v < a.splits; ++v) t += p[v * apart];
+        put_result(a, all, k, t);
+    }
+}
+
+// Many splits: 32 values by 32 slices of the splits side by side, then the slices in order.
+__global__ void __launch_bounds__(1024) k_dense_join_many(DenseArgs a) {
     __shared__ float s_t[32][33];
     const int64_t all = int64_t(a.N) * a.D, count = all + (a.db ? a.N : 0);
     const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
@@ -426,11 +499,7 @@ __global__ void __launch_bounds__(1024) k_dense_join(DenseArgs a) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
         const int64_t e = base + q;
-        if (c != 0 || e >= count) continue;
-        if (e < all)
-            store_param(a.dw, a.gdt, e / a.D * a.dws + e % a.D, t);
-        else
-            store_param(a.db, a.gdt, e - all, t);
+        if (c == 0 && e < count) put_result(a, all, e, t);
     }
 }
 
@@ -438,27 +507,30 @@ __global__ void __launch_bounds__(1024) k_dense_join(DenseArgs a) {
 struct Tile {
     int i, j, ctas;    // ctas: of an SM
 };
-Tile tile_of(int32_t N, int32_t D) {
+Tile tile_of(int32_t N, int32_t D, int dtype) {
     if (N <= 128 && D <= 64) return {128, 64, 3};
     if (N <= 128 && D <= 128) return {128, 128, 2};
-    return {256, 256, 1};
+    if (dtype == SS_BF16) return {256, 256, 1};
+    return {128, 256, 1};      // two sets of sums
 }
 
-// Rows that a split's sum may have: the tensor core's sums lose more than float32's with
-// each addition.
-constexpr int64_t kMaxRows = 4096;
+// How the rows are shared out: ranges with sums of their own, as many as fill the device, of
+// eight stages at least; and the chains of sums within a range.
 constexpr int kSms = 152;
-
-// How many ranges of rows have sums of their own: as many as fill the device, of eight stages
-// at least, and none longer than kMaxRows.
-int splits_of(int64_t n, int32_t N, int32_t D) {
-    const Tile t = tile_of(N, D);
+constexpr int kChain32 = 2048, kChain16 = 16384;    // rows; dW in float32, in 16 bits
+struct Shares {
+    int splits, chain;
+    bool part;         // sums leave the tensor memory before they are done
+};
+Shares shares_of(int64_t n, int32_t N, int32_t D, int dtype, int gdt) {
+    const Tile t = tile_of(N, D, dtype);
     const int64_t tiles = int64_t((N + t.i - 1) / t.i) * ((D + t.j - 1) / t.j);
     int64_t s = kSms * t.ctas / tiles;
-    const int64_t most = (n + 8 * kRows - 1) / (8 * kRows), least = (n + kMaxRows - 1) / kMaxRows;
+    const int64_t most = (n + 8 * kRows - 1) / (8 * kRows);
     if (s > most) s = most;
-    if (s < least) s = least;
-    return int(s < 1 ? 1 : s);
+    if (s < 1) s = 1;
+    const int rows = gdt == SS_F32 ? kChain32 : kChain16;
+    return {int(s), rows / kRows, s > 1 || n > rows};
 }
 
 template <typename T, int TI, int TJ>
@@ -484,10 +556,10 @@ using namespace ss;
 
 extern "C" {
 
-size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D) {
-    if (!dense_sizes_ok(n, N, D)) return 0;
-    const int splits = splits_of(n, N, D);
-    return splits > 1 ? size_t(splits) * N * (size_t(D) + 1) * sizeof(float) : 256;
+size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D, ss_dtype dtype, ss_dtype grad_dtype) {
+    if (!dense_sizes_ok(n, N, D) || !dtype_known(dtype) || (grad_dtype != SS_F32 && grad_dtype != dtype)) return 0;
+    const Shares sh = shares_of(n, N, D, dtype, grad_dtype);
+    return sh.part ? size_t(sh.splits) * N * (size_t(D) + 1) * sizeof(float) : 256;
 }
 
 ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n, int32_t N,
@@ -506,30 +578,39 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
     }
     if ((st = check_row_tensor(who, "dweight", dweight, dweight_stride, D, grad_dtype)) != SS_OK) return st;
     if ((st = check_aligned(who, "dbias", dbias, grad_dtype)) != SS_OK) return st;
-    if ((st = check_workspace(who, workspace, workspace_bytes, ss_dense_grad8_workspace_bytes(n, N, D))) != SS_OK)
+    if ((st = check_workspace(who, workspace, workspace_bytes, ss_dense_grad8_workspace_bytes(n, N, D, dtype, grad_dtype))) != SS_OK)
         return st;
     int dev = 0, sms = 0;
     if ((st = current_device(&dev, &sms, "ss_dense_grad8: device query")) != SS_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    const int splits = splits_of(n, N, D);
+    const Shares sh = shares_of(n, N, D, dtype, grad_dtype);
     float *part = static_cast<float *>(workspace);
-    const int64_t each = (n + splits - 1) / splits;
-    const DenseArgs a{dy, dy_stride, rows8_of(x), x ? x->format : 0, n, N, D, (each + kRows - 1) / kRows * kRows, splits,
-                      part, part + size_t(splits) * N * D, dweight, dweight_stride, dbias, int(grad_dtype)};
-    const Tile tile = tile_of(N, D);
+    const int64_t each = (n + sh.splits - 1) / sh.splits;
+    const DenseArgs a{dy, dy_stride, rows8_of(x), x ? x->format : 0, n, N, D, (each + kRows - 1) / kRows * kRows,
+                      sh.splits, sh.chain, part, part + size_t(sh.splits) * N * D, dweight, dweight_stride, dbias,
+                      int(grad_dtype)};
+    const Tile tile = tile_of(N, D, dtype);
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        if (tile.i == 256)
-            st = launch<T, 256, 256>(a, s);
+        constexpr int kLargeI = std::is_same<T, __nv_bfloat16>::value ? 256 : 128;
+        if (tile.j == 256)
+            st = launch<T, kLargeI, 256>(a, s);
         else if (tile.j == 128)
             st = launch<T, 128, 128>(a, s);
         else
             st = launch<T, 128, 64>(a, s);
     });
     if (st != SS_OK) return st;
-    if (splits > 1) {
-        const int64_t ctas = (int64_t(N) * D + N + 31) / 32;
-        SS_LAUNCH("k_dense_join", s, k_dense_join<<<int(ctas < sms * 16 ? ctas : sms * 16), 1024, 0, s>>>(a));
+    if (sh.splits > 1) {
+        const int64_t values = int64_t(N) * D + N;
+        if (sh.splits >= 16) {
+            const int64_t ctas = (values + 31) / 32;
+            SS_LAUNCH("k_dense_join_many", s,
+                      k_dense_join_many<<<int(ctas < sms * 16 ? ctas : sms * 16), 1024, 0, s>>>(a));
+        } else {
+            const int64_t ctas = (values + 255) / 256;
+            SS_LAUNCH("k_dense_join", s, k_dense_join<<<int(ctas < sms * 16 ? ctas : sms * 16), 256, 0, s>>>(a));
+        }
     }
     return check_launch(who);
 }

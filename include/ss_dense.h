@@ -22,8 +22,9 @@
 extern "C" {
 #endif
 
-/* Bytes of workspace ss_dense_grad8 needs; 0 for sizes outside the limits. */
-size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D);
+/* Bytes of workspace ss_dense_grad8 needs; 0 for sizes or types outside the limits. */
+size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D, ss_dtype dtype,
+                                      ss_dtype grad_dtype);
 
 /* dy: device [n][N] of `dtype`; *x: n rows of D; dweight: device [N][D] of
  * grad_dtype (SS_F32 or `dtype`), dbias: device [N] of grad_dtype, NULL if not

@@ -64,7 +64,7 @@ def test_gradient(ss, case):
     n, N, D, t, gt, fmt, pad, off = case
     dy, g = inputs(ss, n, N, D, t, fmt, pad, off)
     x64 = f64(g.rows.unpack(torch.empty(n, D, device="cuda")))
-    ws = torch.empty(ss.ss_dense_grad8_workspace_bytes(n, N, D), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    ws = torch.empty(ss.ss_dense_grad8_workspace_bytes(n, N, D, dtype(t), dtype(gt)), dtype=torch.uint8, device="cuda").fill_(0xFF)
     dw, buf = rows(np.zeros((N, D)), gt, pad, off, fill=-7.0)
     dw.fill_(5.0)
     db = torch.full((N,), 5.0, dtype=dtype(gt), device="cuda")

@@ -55,9 +55,12 @@ def test_workspace_sizes(lib):
         for n, D in [(-1, 1), (1 << 31, 1), (1, 0), (1, 65537)]:
             assert w(n, D) == 0
     w = lib.ss_dense_grad8_workspace_bytes
-    assert w(0, 1, 1) > 0 and w(10, 48, 48) > 0 and w((1 << 31) - 1, 65536, 65536) > 0
-    for n, N, D in [(-1, 1, 1), (1 << 31, 1, 1), (1, 0, 1), (1, 1, 0), (1, 65537, 1), (1, 1, 65537)]:
-        assert w(n, N, D) == 0
+    for t, g in ((F32, F32), (F16, F16), (BF16, F32)):
+        assert w(0, 1, 1, t, g) > 0 and w(10, 48, 48, t, g) > 0
+        assert w((1 << 31) - 1, 65536, 65536, t, g) > 65536 * 65536 * 4
+        for n, N, D in [(-1, 1, 1), (1 << 31, 1, 1), (1, 0, 1), (1, 1, 0), (1, 65537, 1), (1, 1, 65537)]:
+            assert w(n, N, D, t, g) == 0
+    assert w(1, 1, 1, 3, 0) == 0 and w(1, 1, 1, F32, F16) == 0 and w(1, 1, 1, F16, BF16) == 0
 
 
 def test_pack_and_unpack_refusals(lib):
@@ -128,7 +131,7 @@ def test_backward_refusals(lib):
 
 
 def test_dense_refusals(lib):
-    need = lib.ss_dense_grad8_workspace_bytes(4, 3, 8)
+    need = lib.ss_dense_grad8_workspace_bytes(4, 3, 8, F32, F32)
 
     def f(dy=A, dt=F32, dys=3, x=rows8(), n=4, N=3, D=8, dw=A, dws=8, db=A, gdt=F32, ws=A, nb=need):
         return lib.ss_dense_grad8(dy, dt, dys, x, n, N, D, dw, dws, db, gdt, ws, nb, None)
