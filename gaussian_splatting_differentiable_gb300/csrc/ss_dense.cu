@@ -60,7 +60,6 @@ struct DenseArgs {
     const void *dy;
     int64_t dys;
     Rows8 x;
-    int fmt;
     int64_t n;
     int32_t N, D;
     int64_t rows;         // of a split
@@ -114,72 +113,66 @@ __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint
 __device__ __forceinline__ void products_arrive(uint64_t *b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(b)) : "memory");
 }
-__device__ __forceinline__ void tensor_load16(uint32_t (&v)[16], uint32_t at) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                 "%14, %15}, [%16];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+__device__ __forceinline__ void tensor_load8(uint32_t (&v)[8], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "r"(at));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // ---- conversion
 
-// The part of a float32 that a bfloat16's bits hold, and the rest, which is exact; an infinity
-// has no rest.
-__device__ __forceinline__ float rest_of(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const float r = x - __uint_as_float(u & 0xffff0000u);
-    return (u & 0x7fffffffu) == 0x7f800000u ? 0.0f : r;
-}
+// A bfloat16 holds the upper half of a float32's bits; what is left of the value is exact.
 __device__ __forceinline__ uint32_t tops(F2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
+__device__ __forceinline__ F2 rests(F2 v) {
+    return add2(v, make_float2(-__uint_as_float(__float_as_uint(v.x) & 0xffff0000u),
+                               -__uint_as_float(__float_as_uint(v.y) & 0xffff0000u)));
+}
+// An infinity or a NaN among them?  0 x is neither for all other values.
+__device__ __forceinline__ bool any_special(const F2 (&f)[4]) {
+    const F2 o = both(0.0f);
+    const F2 z = fma2(f[0], o, fma2(f[1], o, fma2(f[2], o, mul2(f[3], o))));
+    return !(z.x + z.y == 0.0f);
+}
+// What hi holds of such values is all of them; a NaN keeps a bit that hi has.
+__device__ __noinline__ float special_of(float x, bool rest) {
+    const uint32_t u = __float_as_uint(x);
+    if ((u & 0x7f800000u) != 0x7f800000u) return rest ? x - __uint_as_float(u & 0xffff0000u) : x;
+    return rest ? 0.0f : ((u & 0x7fffffu) ? __uint_as_float(0x7fffffffu) : x);
+}
 
 __device__ __forceinline__ void store16(uint32_t at, const uint32_t (&w)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 template <int APART>
 __device__ __forceinline__ void store_parts(uint32_t at, const Raw<__nv_bfloat16> &r) { store16(at, r.w); }
-template <int APART>
-__device__ __forceinline__ void store_parts(uint32_t at, const Raw<__half> &r) {
-    F2 f[4];
-    floats_of(f, r);
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        hi[i] = tops(f[i]);
-        lo[i] = tops(make_float2(rest_of(f[i].x), rest_of(f[i].y)));
-    }
-    store16(at, hi);
-    store16(at + APART, lo);
-}
-template <int APART>
-__device__ __forceinline__ void store_parts(uint32_t at, const Raw<float> &r) {
+template <int APART, typename T>
+__device__ __forceinline__ void store_parts(uint32_t at, const Raw<T> &r) {
     F2 f[4];
     floats_of(f, r);
     uint32_t w[4];
+    const bool special = any_special(f);
+    if (special)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = tops(f[i]);
-        f[i] = make_float2(rest_of(f[i].x), rest_of(f[i].y));
-    }
-    store16(at, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = tops(f[i]);
-        f[i] = make_float2(f[i].x - __uint_as_float(__float_as_uint(f[i].x) & 0xffff0000u),
-                           f[i].y - __uint_as_float(__float_as_uint(f[i].y) & 0xffff0000u));
-    }
-    store16(at + APART, w);
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(special_of(f[i].x, false), special_of(f[i].y, false));
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = tops(f[i]);
+    store16(at, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = special ? make_float2(special_of(f[i].x, true), special_of(f[i].y, true)) : rests(f[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = tops(f[i]);
+    store16(at + APART, w);
+    if (sizeof(T) == 2) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = tops(rests(f[i]));
     store16(at + 2 * APART, w);
 }
-__device__ __forceinline__ void store_held(uint32_t at, const Held &h, int fmt) {
+template <int FMT>
+__device__ __forceinline__ void store_held(uint32_t at, const Held &h) {
     F2 f[4];
-    if (fmt == SS_INT8)
-        h.values<SS_INT8>(f);
-    else
-        h.values<SS_E4M3>(f);
+    h.values<FMT>(f);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack2<__nv_bfloat16>(f[i].x, f[i].y);
@@ -187,26 +180,32 @@ __device__ __forceinline__ void store_held(uint32_t at, const Held &h, int fmt) 
 }
 
 // Where a thread's units of a stage lie: `valid` units a row, the threads one
-// after the other along them, rows after rows.
+// after the other along them, rows after rows; turn k's are k * rows rows on.  A thread
+// without a unit has row kRows.
 struct Turns {
-    int unit, row, rows;     // rows: of a turn; unit < 0: none
+    int unit, row, rows;     // rows: of a turn
     __device__ __forceinline__ Turns(int threads, int valid) {
         rows = threads / valid;
         row = threadIdx.x / valid, unit = threadIdx.x - row * valid;
-        if (row >= rows) unit = -1, row = 0;
+        if (row >= rows) unit = 0, row = kRows;
+    }
+    // Of turn k's unit in an operand: 64 columns of a row, swizzled.
+    __device__ __forceinline__ uint32_t place(int k) const {
+        const int r = row + k * rows;
+        return (unit >> 3) * kBlock + r * 128 + (((unit ^ r) & 7) << 4);
     }
 };
 
-// 16 sums of a row of the tile (`count` of them the weight's): added to what is in
+// 8 sums of a row of the tile (`count` of them the weight's): added to what is in
 // part at `p` (if there is something), and stored there, or, at `e`, as dW.
-__device__ __forceinline__ void put_sums(const DenseArgs &a, size_t p, int64_t e, int count, uint32_t (&v)[16], bool add,
+__device__ __forceinline__ void put_sums(const DenseArgs &a, size_t p, int64_t e, int count, uint32_t (&v)[8], bool add,
                                          bool result) {
     float *part = a.part + p;
-    const bool vectors = count == 16 && (reinterpret_cast<uintptr_t>(part) & 15) == 0;
+    const bool vectors = count == 8 && (reinterpret_cast<uintptr_t>(part) & 15) == 0;
     if (add) {
         if (vectors)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
                 const float4 q = reinterpret_cast<const float4 *>(part)[k];
                 v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) + q.x);
                 v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) + q.y);
@@ -215,42 +214,41 @@ __device__ __forceinline__ void put_sums(const DenseArgs &a, size_t p, int64_t e
             }
         else
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+            for (int k = 0; k < 8; ++k)
                 if (k < count) v[k] = __float_as_uint(__uint_as_float(v[k]) + part[k]);
     }
     if (!result) {
         if (vectors)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 2; ++k)
                 reinterpret_cast<uint4 *>(part)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
         else
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+            for (int k = 0; k < 8; ++k)
                 if (k < count) part[k] = __uint_as_float(v[k]);
         return;
     }
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.dw) + e * (a.gdt == SS_F32 ? 4 : 2);
-    if (count < 16 || (at & 15) != 0) {
+    if (count < 8 || (at & 15) != 0) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+        for (int k = 0; k < 8; ++k)
             if (k < count) store_param(a.dw, a.gdt, e + k, __uint_as_float(v[k]));
     } else if (a.gdt == SS_F32) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
             reinterpret_cast<uint4 *>(at)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     } else {
-        uint32_t w[8];
+        uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
             const float x = __uint_as_float(v[2 * k]), y = __uint_as_float(v[2 * k + 1]);
             w[k] = a.gdt == SS_F16 ? pack2<__half>(x, y) : pack2<__nv_bfloat16>(x, y);
         }
-        reinterpret_cast<uint4 *>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4 *>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
-template <typename T, int TI, int TJ, bool ALIGNED>
+template <typename T, int TI, int TJ, int FMT, bool ALIGNED>
 __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>::kMinCtas) k_dense(DenseArgs a) {
     using C = Config<T, TI, TJ>;
     extern __shared__ uint8_t s_raw[];
@@ -295,7 +293,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
 
     // The sums of a chain out of the tensor memory: added to what the chains before left, and to their
     // place if it is the last.  A warp reads the 32 lanes (rows of dW) of its quarter, the warps of a
-    // quarter 16 columns in turn.
+    // quarter 8 columns in turn.
     auto drain = [&](bool first_chain, bool last_chain) {
         const int quarter = warp & 3;
         const bool failed = *static_cast<volatile uint32_t *>(&s_failed) != 0;
@@ -303,48 +301,48 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         for (int h = 0; h < TI / 128 && h * 128 < ni; ++h) {
             const int i = i0 + h * 128 + quarter * 32 + lane;
 #pragma unroll 1
-            for (int c = (warp >> 2) * 16; c < nj; c += C::kLoaders / 128 * 16) {
-                uint32_t v[16];
+            for (int c = (warp >> 2) * 8; c < nj; c += C::kLoaders / 128 * 8) {
+                uint32_t v[8];
                 const uint32_t at = tensor + (uint32_t(quarter * 32) << 16) + h * TJ + c;
                 __syncwarp();
-                tensor_load16(v, at);
+                tensor_load8(v, at);
                 if (C::kSums > 1) {
-                    uint32_t w[16];
-                    tensor_load16(w, at + C::kTile);
+                    uint32_t w[8];
+                    tensor_load8(w, at + C::kTile);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
+                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
                 }
                 if (stages == 0 || failed)      // a wait that ran out leaves NaN
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = failed ? 0x7fffffffu : 0u;
+                    for (int k = 0; k < 8; ++k) v[k] = failed ? 0x7fffffffu : 0u;
                 if (i < a.N)
                     put_sums(a, (size_t(blockIdx.x) * a.N + i) * a.D + j0 + c, int64_t(i) * a.dws + j0 + c,
-                             nj - c < 16 ? nj - c : 16, v, !first_chain, last_chain && a.splits == 1);
+                             nj - c < 8 ? nj - c : 8, v, !first_chain, last_chain && a.splits == 1);
             }
         }
     };
     if (warp < C::kLoaders / 32) {
         Raw<T> ra[C::kAhead][C::kTurnsA];
         Held rb[C::kAhead][C::kTurnsB];
-        const int ca = ta.unit < 0 ? 0 : (ni - ta.unit * kUnit < kUnit ? ni - ta.unit * kUnit : kUnit);
-        const T *pa = static_cast<const T *>(a.dy) + i0 + ta.unit * kUnit;
-        auto load = [&](Raw<T> (&va)[C::kTurnsA], Held (&vb)[C::kTurnsB], int stage) {
-            const int64_t m0 = first + int64_t(stage) * kRows;
+        const int ca = ni - ta.unit * kUnit < kUnit ? ni - ta.unit * kUnit : kUnit;
+        // the next stage to load: its units, and how many of its rows there are
+        const T *pa = static_cast<const T *>(a.dy) + (first + ta.row) * a.dys + i0 + ta.unit * kUnit;
+        const uint8_t *pq = a.x.q + (first + tb.row) * a.x.stride + j0 + tb.unit * kUnit;
+        const uint8_t *ps = a.x.scales + (first + tb.row) * a.x.scale_stride + j0 / kGroup + tb.unit / (kGroup / kUnit);
+        int64_t left = last - first;
+        auto load = [&](Raw<T> (&va)[C::kTurnsA], Held (&vb)[C::kTurnsB]) {
+            const int rows = left < kRows ? int(left) : kRows;
 #pragma unroll
-            for (int k = 0; k < C::kTurnsA; ++k) {
-                const int r = ta.row + k * ta.rows;
-                const bool here = r < kRows && m0 + r < last && stage < stages;
-                va[k] = load_unit<T, ALIGNED>(pa + (m0 + r) * a.dys, here ? ca : 0);
-            }
+            for (int k = 0; k < C::kTurnsA; ++k)
+                va[k] = load_unit<T, ALIGNED>(pa + k * ta.rows * a.dys, ta.row + k * ta.rows < rows ? ca : 0);
 #pragma unroll
-            for (int k = 0; k < C::kTurnsB; ++k) {
-                const int r = tb.row + k * tb.rows;
-                const bool here = tb.unit >= 0 && r < kRows && m0 + r < last && stage < stages;
-                vb[k].load(a.x, m0 + r, j0 / kUnit + tb.unit, here);
-            }
+            for (int k = 0; k < C::kTurnsB; ++k)
+                vb[k].load(pq + k * tb.rows * a.x.stride, ps + k * tb.rows * a.x.scale_stride, tb.row + k * tb.rows < rows);
+            pa += kRows * a.dys, pq += kRows * a.x.stride, ps += kRows * a.x.scale_stride;
+            left -= kRows;
         };
 #pragma unroll
-        for (int q = 0; q < C::kAhead; ++q) load(ra[q], rb[q], q);
+        for (int q = 0; q < C::kAhead; ++q) load(ra[q], rb[q]);
         int slot = 0, chains = 0;
         uint32_t parity = 1;
         bool ok = true, end;
@@ -361,9 +359,8 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                 const uint32_t at = ring + slot * C::kStageBytes;
 #pragma unroll
                 for (int k = 0; k < C::kTurnsA; ++k) {
-                    const int r = ta.row + k * ta.rows;
-                    if (ta.unit < 0 || r >= kRows) continue;
-                    store_parts<C::kABytes>(at + (ta.unit >> 3) * kBlock + r * 128 + (((ta.unit ^ r) & 7) << 4), ra[q][k]);
+                    if (ta.row + k * ta.rows >= kRows) continue;
+                    store_parts<C::kABytes>(at + ta.place(k), ra[q][k]);
                     if (bias) {
                         F2 f[4];
                         floats_of(f, ra[q][k]);
@@ -372,16 +369,12 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < C::kTurnsB; ++k) {
-                    const int r = tb.row + k * tb.rows;
-                    if (tb.unit < 0 || r >= kRows) continue;
-                    store_held(at + C::kParts * C::kABytes + (tb.unit >> 3) * kBlock + r * 128 + (((tb.unit ^ r) & 7) << 4),
-                               rb[q][k], a.fmt);
-                }
+                for (int k = 0; k < C::kTurnsB; ++k)
+                    if (tb.row + k * tb.rows < kRows) store_held<FMT>(at + C::kParts * C::kABytes + tb.place(k), rb[q][k]);
                 writes_to_async();
                 __syncwarp();
                 if (lane == 0) barrier_arrive(&s_full[slot]);
-                load(ra[q], rb[q], stage + C::kAhead);
+                load(ra[q], rb[q]);
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
             }
             base += C::kAhead;
@@ -438,14 +431,14 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         // the threads' sums of a column, in the order of their rows
         float *s = reinterpret_cast<float *>(ring_ptr);
         const int width = (ni + kUnit - 1) / kUnit * kUnit;
-        if (warp < C::kLoaders / 32 && ta.unit >= 0)
+        if (warp < C::kLoaders / 32 && ta.row < kRows)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 reinterpret_cast<float2 *>(s + size_t(ta.row) * width + ta.unit * kUnit)[i] = sums[i];
         __syncthreads();
         for (int j = threadIdx.x; j < ni; j += C::kThreads) {
             float t = 0.0f;
-            for (int r = 0; r < ta.rows; ++r) t += s[size_t(r) * width + j];
+            for (int r = 0; r < ta.rows && r < kRows; ++r) t += s[size_t(r) * width + j];
             if (a.splits > 1)
                 a.part_bias[size_t(blockIdx.x) * a.N + i0 + j] = t;
             else
@@ -533,14 +526,14 @@ Shares shares_of(int64_t n, int32_t N, int32_t D, int dtype, int gdt) {
     return {int(s), rows / kRows, s > 1 || n > rows};
 }
 
-template <typename T, int TI, int TJ>
+template <typename T, int TI, int TJ, int FMT>
 ss_status launch(const DenseArgs &a, cudaStream_t s) {
     using C = Config<T, TI, TJ>;
     const dim3 grid(a.splits, (a.D + TJ - 1) / TJ, (a.N + TI - 1) / TI);
     const bool aligned = units_aligned<T>(a.dy, a.dys);
-    auto kernel = aligned ? k_dense<T, TI, TJ, true> : k_dense<T, TI, TJ, false>;
+    auto kernel = aligned ? k_dense<T, TI, TJ, FMT, true> : k_dense<T, TI, TJ, FMT, false>;
     static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
-    const void *fn[2] = {(const void *)k_dense<T, TI, TJ, true>, (const void *)k_dense<T, TI, TJ, false>};
+    const void *fn[2] = {(const void *)k_dense<T, TI, TJ, FMT, true>, (const void *)k_dense<T, TI, TJ, FMT, false>};
     const ss_status st = ensure_dyn_smem(smem_ctx, fn, 2, C::kSmem, "k_dense");
     if (st != SS_OK) return st;
     SS_LAUNCH("k_dense", s, kernel<<<grid, C::kThreads, C::kSmem, s>>>(a));
@@ -586,19 +579,22 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
     const Shares sh = shares_of(n, N, D, dtype, grad_dtype);
     float *part = static_cast<float *>(workspace);
     const int64_t each = (n + sh.splits - 1) / sh.splits;
-    const DenseArgs a{dy, dy_stride, rows8_of(x), x ? x->format : 0, n, N, D, (each + kRows - 1) / kRows * kRows,
+    const DenseArgs a{dy, dy_stride, rows8_of(x), n, N, D, (each + kRows - 1) / kRows * kRows,
                       sh.splits, sh.chain, part, part + size_t(sh.splits) * N * D, dweight, dweight_stride, dbias,
                       int(grad_dtype)};
     const Tile tile = tile_of(N, D, dtype);
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int kLargeI = std::is_same<T, __nv_bfloat16>::value ? 256 : 128;
-        if (tile.j == 256)
-            st = launch<T, kLargeI, 256>(a, s);
-        else if (tile.j == 128)
-            st = launch<T, 128, 128>(a, s);
-        else
-            st = launch<T, 128, 64>(a, s);
+        with_format(x ? x->format : SS_INT8, [&](auto F) {
+            constexpr int FMT = decltype(F)::value;
+            if (tile.j == 256)
+                st = launch<T, kLargeI, 256, FMT>(a, s);
+            else if (tile.j == 128)
+                st = launch<T, 128, 128, FMT>(a, s);
+            else
+                st = launch<T, 128, 64, FMT>(a, s);
+        });
     });
     if (st != SS_OK) return st;
     if (sh.splits > 1) {

@@ -126,10 +126,13 @@ struct Held {
     uint2 q;
     uint32_t e;
     __device__ __forceinline__ void load(const Rows8 &in, int64_t row, int u, bool here) {
+        load(in.q + row * in.stride + u * kUnit, in.scales + row * in.scale_stride + u / (kGroup / kUnit), here);
+    }
+    __device__ __forceinline__ void load(const uint8_t *pq, const uint8_t *ps, bool here) {
         q = make_uint2(0u, 0u), e = 127u;
         if (!here) return;
-        q = *reinterpret_cast<const uint2 *>(in.q + row * in.stride + u * kUnit);
-        e = in.scales[row * in.scale_stride + u / (kGroup / kUnit)];
+        q = *reinterpret_cast<const uint2 *>(pq);
+        e = *ps;
     }
     template <int FMT>
     __device__ __forceinline__ void values(F2 (&f)[4]) const {
