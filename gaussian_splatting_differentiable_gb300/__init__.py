@@ -763,7 +763,8 @@ class Rows8:
         if not (0 <= n < 1 << 31 and 1 <= D <= 65536):
             raise ValueError("sizes out of range")
         self._n, self._D, self._format = n, D, format
-        stride, groups = (D + 7) // 8 * 8, (D + 31) // 32
+        piece = 16 if D > 32 else 8     # 16-byte rows where that adds little to them
+        stride, groups = (D + piece - 1) // piece * piece, (D + 31) // 32
         self._buf = torch.empty(n, stride, dtype=torch.uint8, device=d)
         self._q = self._buf.view(format)[:, :D]
         self._scales = torch.empty(n, groups, dtype=torch.uint8, device=d)

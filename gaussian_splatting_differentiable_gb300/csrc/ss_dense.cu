@@ -1,5 +1,6 @@
 // The weight gradient of a dense layer from its input kept in 8 bits (model:
 // include/ss_dense.h).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -26,13 +27,13 @@ namespace {
 // three times as often), and where dW is float32 the sums leave the tensor memory every
 // kChain32 rows and are added in float32.
 //
-// A CTA has a tile TI x TJ of dW over a range of rows.  Its loader warps keep
-// AHEAD stages of kRows rows on their way in registers, convert them and store them into
-// a ring in shared memory; one thread of the last warp issues the products; at the end of a
-// chain the loaders read the sums out of the tensor memory.
-constexpr int kRows = 32;              // of a stage
-constexpr int kStep = 16;              // of one product
-constexpr int kBlock = kRows * 128;    // bytes of 64 columns of a stage
+// A CTA has a tile TI x TJ of dW over a range of rows, stages of which go through a ring
+// in shared memory.  A bfloat16 dy needs no change: where it lies on 16-byte boundaries (FAST), a
+// thread has the copy engine bring it.  All else passes through the registers of
+// the loader warps, kAhead stages before it is converted and stored.  One thread of another
+// warp issues the products; at the end of a chain the loaders read the sums out of the tensor memory.
+constexpr int kStep = 16;              // rows of one product
+constexpr int kWide = 16;              // columns of x that a thread converts at a time
 
 template <typename T>
 constexpr int parts_of() { return sizeof(T) == 4 ? 3 : (std::is_same<T, __half>::value ? 2 : 1); }
@@ -43,14 +44,16 @@ struct Config {
     static constexpr bool kLarge = TJ == 256;
     static constexpr int kSums = kParts > 1 ? 2 : 1;
     static constexpr int kLoaders = kLarge ? 512 : 256;
-    static constexpr int kThreads = kLoaders + 32;
+    static constexpr int kThreads = kLoaders + 64;                  // and the warps of the products and of the copies
+    static constexpr int kRows = kParts == 3 && TJ > 64 ? 32 : 64;  // of a stage
+    static constexpr int kBlock = kRows * 128;                      // bytes of 64 columns of a stage
     static constexpr int kABytes = TI / 64 * kBlock, kBBytes = TJ / 64 * kBlock;
     static constexpr int kStageBytes = kParts * kABytes + kBBytes;
-    static constexpr int kStages = kLarge ? 200 * 1024 / kStageBytes : 2;
+    static constexpr int kStages = kLarge ? 200 * 1024 / kStageBytes : (kParts == 1 ? 3 : 2);
     static constexpr int kSmem = kStages * kStageBytes + 1024;      // and up to the first 1 KB boundary
-    static constexpr int kAhead = 2;
+    static constexpr int kAhead = kParts == 3 && !kLarge ? 1 : 2;
     static constexpr int kTurnsA = kRows * (TI / kUnit) / kLoaders;
-    static constexpr int kTurnsB = kRows * (TJ / kUnit) / kLoaders < 1 ? 1 : kRows * (TJ / kUnit) / kLoaders;
+    static constexpr int kTurnsB = kRows * (TJ / kWide) / kLoaders < 1 ? 1 : kRows * (TJ / kWide) / kLoaders;
     static constexpr int kTile = TI / 128 * TJ;                     // columns of tensor memory for one set of sums
     static constexpr int kColumns = kSums * kTile;
     static constexpr int kMinCtas = kLarge ? 1 : 2;
@@ -65,7 +68,7 @@ struct DenseArgs {
     int64_t rows;         // of a split
     int splits;
     int chain;            // stages of a chain of sums, a multiple of kAhead
-    float *part;          // [splits][N][D], then [splits][N]; not used by one split of one chain
+    float *part;          // [splits][N][D], then [splits][N]; not used by one split of one chain, or into float32
     float *part_bias;
     void *dw;
     int64_t dws;
@@ -95,10 +98,20 @@ __device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity) {
 }
 __device__ __forceinline__ void writes_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// A box of 64 columns (kRows rows) at (column, row), zeros outside the matrix.
+__device__ __forceinline__ void copy_box(uint32_t smem, const CUtensorMap *map, int column, int row, uint64_t *b) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(smem), "l"(map), "r"(column), "r"(row), "r"(smem_of(b)) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint64_t *b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(smem_of(b)), "r"(bytes) : "memory");
+}
+
 // 64 columns of 128 bytes a row, swizzled, columns side by side: blocks of 64
-// columns kBlock apart, groups of 8 rows 1 KB apart.
+// columns BLOCK apart, groups of 8 rows 1 KB apart.
+template <int BLOCK>
 __device__ __forceinline__ uint64_t operand_at(uint32_t smem) {
-    return uint64_t((smem & 0x3ffff) >> 4) | uint64_t(kBlock >> 4) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
+    return uint64_t((smem & 0x3ffff) >> 4) | uint64_t(BLOCK >> 4) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
            uint64_t(2) << 61;
 }
 // bfloat16 x bfloat16 into float32, both operands MN-major, 128 x n.
@@ -134,15 +147,26 @@ __device__ __forceinline__ bool any_special(const F2 (&f)[4]) {
     const F2 z = fma2(f[0], o, fma2(f[1], o, fma2(f[2], o, mul2(f[3], o))));
     return !(z.x + z.y == 0.0f);
 }
-// What hi holds of such values is all of them; a NaN keeps a bit that hi has.
-__device__ __noinline__ float special_of(float x, bool rest) {
-    const uint32_t u = __float_as_uint(x);
-    if ((u & 0x7f800000u) != 0x7f800000u) return rest ? x - __uint_as_float(u & 0xffff0000u) : x;
-    return rest ? 0.0f : ((u & 0x7fffffu) ? __uint_as_float(0x7fffffffu) : x);
-}
 
 __device__ __forceinline__ void store16(uint32_t at, const uint32_t (&w)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+// Such a unit: hi holds all of them, a NaN with a bit that hi has, and there is no rest.
+template <int APART, int PARTS>
+__device__ __noinline__ void store_special(uint32_t at, float2 f0, float2 f1, float2 f2, float2 f3) {
+    float f[8] = {f0.x, f0.y, f1.x, f1.y, f2.x, f2.y, f3.x, f3.y};
+    for (int p = 0; p < PARTS; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t u = __float_as_uint(f[i]);
+            if ((u & 0x7fffffffu) > 0x7f800000u) u = 0x7fffffffu;
+            const bool special = (u & 0x7f800000u) == 0x7f800000u;
+            w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | (u & 0xffff0000u) : u >> 16;
+            f[i] = special ? 0.0f : f[i] - __uint_as_float(u & 0xffff0000u);
+        }
+        store16(at + p * APART, w);
+    }
 }
 template <int APART>
 __device__ __forceinline__ void store_parts(uint32_t at, const Raw<__nv_bfloat16> &r) { store16(at, r.w); }
@@ -150,94 +174,135 @@ template <int APART, typename T>
 __device__ __forceinline__ void store_parts(uint32_t at, const Raw<T> &r) {
     F2 f[4];
     floats_of(f, r);
-    uint32_t w[4];
-    const bool special = any_special(f);
-    if (special)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = make_float2(special_of(f[i].x, false), special_of(f[i].y, false));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = tops(f[i]);
-    store16(at, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f[i] = special ? make_float2(special_of(f[i].x, true), special_of(f[i].y, true)) : rests(f[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = tops(f[i]);
-    store16(at + APART, w);
-    if (sizeof(T) == 2) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = tops(rests(f[i]));
-    store16(at + 2 * APART, w);
-}
-template <int FMT>
-__device__ __forceinline__ void store_held(uint32_t at, const Held &h) {
-    F2 f[4];
-    h.values<FMT>(f);
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack2<__nv_bfloat16>(f[i].x, f[i].y);
-    store16(at, w);
-}
-
-// Where a thread's units of a stage lie: `valid` units a row, the threads one
-// after the other along them, rows after rows; turn k's are k * rows rows on.  A thread
-// without a unit has row kRows.
-struct Turns {
-    int unit, row, rows;     // rows: of a turn
-    __device__ __forceinline__ Turns(int threads, int valid) {
-        rows = threads / valid;
-        row = threadIdx.x / valid, unit = threadIdx.x - row * valid;
-        if (row >= rows) unit = 0, row = kRows;
-    }
-    // Of turn k's unit in an operand: 64 columns of a row, swizzled.
-    __device__ __forceinline__ uint32_t place(int k) const {
-        const int r = row + k * rows;
-        return (unit >> 3) * kBlock + r * 128 + (((unit ^ r) & 7) << 4);
-    }
-};
-
-// 8 sums of a row of the tile (`count` of them the weight's): added to what is in
-// part at `p` (if there is something), and stored there, or, at `e`, as dW.
-__device__ __forceinline__ void put_sums(const DenseArgs &a, size_t p, int64_t e, int count, uint32_t (&v)[8], bool add,
-                                         bool result) {
-    float *part = a.part + p;
-    const bool vectors = count == 8 && (reinterpret_cast<uintptr_t>(part) & 15) == 0;
-    if (add) {
-        if (vectors)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 q = reinterpret_cast<const float4 *>(part)[k];
-                v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) + q.x);
-                v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) + q.y);
-                v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) + q.z);
-                v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) + q.w);
-            }
-        else
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < count) v[k] = __float_as_uint(__uint_as_float(v[k]) + part[k]);
-    }
-    if (!result) {
-        if (vectors)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                reinterpret_cast<uint4 *>(part)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        else
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < count) part[k] = __uint_as_float(v[k]);
+    if (any_special(f)) {
+        store_special<APART, parts_of<T>()>(at, f[0], f[1], f[2], f[3]);
         return;
     }
-    const uintptr_t at = reinterpret_cast<uintptr_t>(a.dw) + e * (a.gdt == SS_F32 ? 4 : 2);
-    if (count < 8 || (at & 15) != 0) {
+#pragma unroll
+    for (int p = 0; p < parts_of<T>(); ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = tops(f[i]);
+            if (p + 1 < parts_of<T>()) f[i] = rests(f[i]);
+        }
+        store16(at + p * APART, w);
+    }
+}
+
+// 16 columns of x as they are held, of which 8 or all are the row's.
+struct Wide {
+    uint32_t w[4], e;
+    template <bool FAST>
+    __device__ __forceinline__ void load(const uint8_t *pq, const uint8_t *ps, bool all) {
+        if (FAST && all) {
+            load_words(w, pq);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(pq);
+            uint2 v = make_uint2(0u, 0u);
+            if (all) v = *reinterpret_cast<const uint2 *>(pq + 8);
+            w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
+        }
+        e = *ps;
+    }
+};
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {      // pairs of bfloat16
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// x in bfloat16, every step exact.  SS_E4M3: the byte's exponent and mantissa in a bfloat16's places are
+// the value times 2^-120, subnormals too, which the scale makes good (in two factors where one
+// would be past bfloat16's range).  SS_INT8: the byte's lower seven bits as 128 .. 255, less 128, or
+// 256 with the sign bit.
+template <int FMT>
+__device__ __forceinline__ void store_held(uint32_t at, const Wide &h) {
+    uint32_t factor, more = 0;
+    if (FMT == SS_INT8) {
+        factor = h.e == kNanExponent ? 0x7fffu : (h.e == 0 ? 0x40u : h.e << 7);
+    } else {
+        const uint32_t e = h.e + 120u;
+        factor = e > 254u ? 254u << 7 : e << 7;
+        if (e > 254u) more = h.e == kNanExponent ? 0x7fffu : (e - 127u) << 7;
+    }
+    factor |= factor << 16, more |= more << 16;
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = h.w[i / 2];
+        if (FMT == SS_INT8) {
+            const uint32_t x = __byte_perm(w, 0u, i & 1 ? 0x4342 : 0x4140);
+            out[i] = minus((x & 0x007f007fu) | 0x43004300u, (x & 0x00800080u) | 0x43004300u);
+        } else {
+            const uint32_t x = __byte_perm(w, 0u, i & 1 ? 0x3424 : 0x1404);
+            out[i] = (x & 0x80008000u) | ((x & 0x7f007f00u) >> 4);
+        }
+        out[i] = times(out[i], factor);
+    }
+    if (FMT == SS_E4M3 && more)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = times(out[i], more);
+    const uint32_t a[4] = {out[0], out[1], out[2], out[3]}, b[4] = {out[4], out[5], out[6], out[7]};
+    store16(at, a);
+    store16(at ^ 16u, b);
+}
+
+// Where a thread's pieces of W columns of a stage lie: `valid` of them a row, the threads
+// one after the other along them, rows after rows; turn k's are k * rows rows on.  A
+// thread without a piece has row ROWS.
+template <int ROWS, int W>
+struct Turns {
+    int piece, row, rows;     // rows: of a turn
+    __device__ __forceinline__ Turns(int threads, int valid) {
+        rows = threads / valid;
+        row = threadIdx.x / valid, piece = threadIdx.x - row * valid;
+        if (row >= rows) piece = 0, row = ROWS;
+    }
+    // Of turn k's piece in an operand: 64 columns of a row, swizzled by 16 bytes.
+    __device__ __forceinline__ uint32_t place(int k) const {
+        const int r = row + k * rows, u = piece * (W / kUnit);
+        return (u >> 3) * (ROWS * 128) + r * 128 + (((u ^ r) & 7) << 4);
+    }
+    __device__ __forceinline__ bool has(int k, int of) const { return row + k * rows < of; }
+};
+
+// 8 sums of a row of the tile (`count` of them the weight's) to float32 values at p, added to
+// what is there or in its place.  No other thread has these, and a thread's additions to one
+// address come in its own order, so the sum's order is fixed, and nobody waits for what was there.
+__device__ __forceinline__ void put_sums(float *p, int count, const uint32_t (&v)[8], bool add) {
+    const bool vectors = count == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    if (vectors) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 4)
+            if (add)
+                asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + k), "f"(__uint_as_float(v[k])),
+                             "f"(__uint_as_float(v[k + 1])), "f"(__uint_as_float(v[k + 2])), "f"(__uint_as_float(v[k + 3]))
+                             : "memory");
+            else
+                *reinterpret_cast<uint4 *>(p + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+    } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (k < count) store_param(a.dw, a.gdt, e + k, __uint_as_float(v[k]));
-    } else if (a.gdt == SS_F32) {
+            if (k < count) {
+                if (add)
+                    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p + k), "f"(__uint_as_float(v[k])) : "memory");
+                else
+                    p[k] = __uint_as_float(v[k]);
+            }
+    }
+}
+// The same as dW of 16 bits, with what is in `part` added where there is something.
+__device__ __forceinline__ void put_rounded(const DenseArgs &a, int64_t e, const float *part, int count, uint32_t (&v)[8],
+                                            bool add) {
+    if (add)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            reinterpret_cast<uint4 *>(at)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    } else {
+        for (int k = 0; k < 8; ++k)
+            if (k < count) v[k] = __float_as_uint(__uint_as_float(v[k]) + part[k]);
+    uint16_t *at = static_cast<uint16_t *>(a.dw) + e;
+    if (count == 8 && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -245,14 +310,20 @@ __device__ __forceinline__ void put_sums(const DenseArgs &a, size_t p, int64_t e
             w[k] = a.gdt == SS_F16 ? pack2<__half>(x, y) : pack2<__nv_bfloat16>(x, y);
         }
         *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < count) store_param(a.dw, a.gdt, e + k, __uint_as_float(v[k]));
     }
 }
 
-template <typename T, int TI, int TJ, int FMT, bool ALIGNED>
-__global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>::kMinCtas) k_dense(DenseArgs a) {
+template <typename T, int TI, int TJ, int FMT, bool FAST>
+__global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>::kMinCtas)
+    k_dense(DenseArgs a, const __grid_constant__ CUtensorMap map) {
     using C = Config<T, TI, TJ>;
+    constexpr bool kCopies = FAST && C::kParts == 1;
     extern __shared__ uint8_t s_raw[];
-    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages], s_done, s_drained;
+    __shared__ uint64_t s_full[C::kStages], s_copied[C::kStages], s_empty[C::kStages], s_done, s_drained;
     __shared__ uint32_t s_tensor, s_failed;
     const uint32_t ring = (smem_of(s_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = s_raw + (ring - smem_of(s_raw));
@@ -261,12 +332,16 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
     const int ni = a.N - i0 < TI ? a.N - i0 : TI, nj = a.D - j0 < TJ ? a.D - j0 : TJ;
     const int64_t first = int64_t(blockIdx.x) * a.rows;
     const int64_t last = first + a.rows < a.n ? first + a.rows : a.n;
-    const int stages = last > first ? int((last - first + kRows - 1) / kRows) : 0;
+    const int stages = last > first ? int((last - first + C::kRows - 1) / C::kRows) : 0;
     const bool bias = blockIdx.y == 0 && a.db;
 
     if (threadIdx.x == 0) {
         s_failed = 0;
-        for (int k = 0; k < C::kStages; ++k) barrier_init(&s_full[k], C::kLoaders / 32), barrier_init(&s_empty[k], 1);
+        for (int k = 0; k < C::kStages; ++k) {
+            barrier_init(&s_full[k], C::kLoaders / 32);
+            barrier_init(&s_copied[k], 1);
+            barrier_init(&s_empty[k], 1);
+        }
         barrier_init(&s_done, 1);
         barrier_init(&s_drained, C::kLoaders / 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -289,7 +364,8 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
     F2 sums[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[i] = both(0.0f);
-    const Turns ta(C::kLoaders, (ni + kUnit - 1) / kUnit), tb(C::kLoaders, (nj + kUnit - 1) / kUnit);
+    const Turns<C::kRows, kUnit> ta(C::kLoaders, (ni + kUnit - 1) / kUnit);
+    const Turns<C::kRows, kWide> tb(C::kLoaders, (nj + kWide - 1) / kWide);
 
     // The sums of a chain out of the tensor memory: added to what the chains before left, and to their
     // place if it is the last.  A warp reads the 32 lanes (rows of dW) of its quarter, the warps of a
@@ -315,34 +391,55 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                 if (stages == 0 || failed)      // a wait that ran out leaves NaN
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] = failed ? 0x7fffffffu : 0u;
-                if (i < a.N)
-                    put_sums(a, (size_t(blockIdx.x) * a.N + i) * a.D + j0 + c, int64_t(i) * a.dws + j0 + c,
-                             nj - c < 8 ? nj - c : 8, v, !first_chain, last_chain && a.splits == 1);
+                if (i >= a.N) continue;
+                const int count = nj - c < 8 ? nj - c : 8;
+                const int64_t e = int64_t(i) * a.dws + j0 + c;
+                float *part = a.part + (size_t(blockIdx.x) * a.N + i) * a.D + j0 + c;
+                if (a.splits == 1 && a.gdt == SS_F32)
+                    put_sums(static_cast<float *>(a.dw) + e, count, v, !first_chain);
+                else if (a.splits == 1 && last_chain)
+                    put_rounded(a, e, part, count, v, !first_chain);
+                else
+                    put_sums(part, count, v, !first_chain);
             }
         }
     };
     if (warp < C::kLoaders / 32) {
         Raw<T> ra[C::kAhead][C::kTurnsA];
-        Held rb[C::kAhead][C::kTurnsB];
-        const int ca = ni - ta.unit * kUnit < kUnit ? ni - ta.unit * kUnit : kUnit;
-        // the next stage to load: its units, and how many of its rows there are
-        const T *pa = static_cast<const T *>(a.dy) + (first + ta.row) * a.dys + i0 + ta.unit * kUnit;
-        const uint8_t *pq = a.x.q + (first + tb.row) * a.x.stride + j0 + tb.unit * kUnit;
-        const uint8_t *ps = a.x.scales + (first + tb.row) * a.x.scale_stride + j0 / kGroup + tb.unit / (kGroup / kUnit);
+        Wide rb[C::kAhead][C::kTurnsB];
+        const int ca = ni - ta.piece * kUnit < kUnit ? ni - ta.piece * kUnit : kUnit;
+        const bool all = nj - tb.piece * kWide > kUnit;
+        // the next stage to load: its pieces, and how many of its rows there are
+        const T *pa = static_cast<const T *>(a.dy) + (first + ta.row) * a.dys + i0 + ta.piece * kUnit;
+        const uint8_t *pq = a.x.q + (first + tb.row) * a.x.stride + j0 + tb.piece * kWide;
+        const uint8_t *ps = a.x.scales + (first + tb.row) * a.x.scale_stride + j0 / kGroup + tb.piece / (kGroup / kWide);
         int64_t left = last - first;
-        auto load = [&](Raw<T> (&va)[C::kTurnsA], Held (&vb)[C::kTurnsB]) {
-            const int rows = left < kRows ? int(left) : kRows;
+        auto load = [&](Raw<T> (&va)[C::kTurnsA], Wide (&vb)[C::kTurnsB]) {
+            const int rows = left < C::kRows ? int(left) : C::kRows;
+            if (!kCopies)
 #pragma unroll
-            for (int k = 0; k < C::kTurnsA; ++k)
-                va[k] = load_unit<T, ALIGNED>(pa + k * ta.rows * a.dys, ta.row + k * ta.rows < rows ? ca : 0);
+                for (int k = 0; k < C::kTurnsA; ++k)
+                    if (ta.has(k, rows))
+                        va[k] = load_unit<T, FAST>(pa + k * ta.rows * a.dys, ca);
+                    else
+                        va[k].clear();
 #pragma unroll
             for (int k = 0; k < C::kTurnsB; ++k)
-                vb[k].load(pq + k * tb.rows * a.x.stride, ps + k * tb.rows * a.x.scale_stride, tb.row + k * tb.rows < rows);
-            pa += kRows * a.dys, pq += kRows * a.x.stride, ps += kRows * a.x.scale_stride;
-            left -= kRows;
+                if (tb.has(k, rows))
+                    vb[k].template load<FAST>(pq + k * tb.rows * a.x.stride, ps + k * tb.rows * a.x.scale_stride, all);
+                else
+                    vb[k] = Wide{{0u, 0u, 0u, 0u}, 127u};
+            pa += C::kRows * a.dys, pq += C::kRows * a.x.stride, ps += C::kRows * a.x.scale_stride;
+            left -= C::kRows;
         };
 #pragma unroll
         for (int q = 0; q < C::kAhead; ++q) load(ra[q], rb[q]);
+        auto add_bias = [&](const Raw<T> &r) {
+            F2 f[4];
+            floats_of(f, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums[i] = add2(sums[i], f[i]);
+        };
         int slot = 0, chains = 0;
         uint32_t parity = 1;
         bool ok = true, end;
@@ -350,27 +447,34 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         do {
 #pragma unroll
             for (int q = 0; q < C::kAhead; ++q) {
-                const int stage = base + q;
-                if (stage >= stages) break;
+                if (base + q >= stages) break;
                 if (!barrier_wait(&s_empty[slot], parity)) {
                     ok = false;
                     break;
                 }
                 const uint32_t at = ring + slot * C::kStageBytes;
+                if (!kCopies)
 #pragma unroll
-                for (int k = 0; k < C::kTurnsA; ++k) {
-                    if (ta.row + k * ta.rows >= kRows) continue;
-                    store_parts<C::kABytes>(at + ta.place(k), ra[q][k]);
-                    if (bias) {
-                        F2 f[4];
-                        floats_of(f, ra[q][k]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sums[i] = add2(sums[i], f[i]);
+                    for (int k = 0; k < C::kTurnsA; ++k) {
+                        if (!ta.has(k, C::kRows)) continue;
+                        store_parts<C::kABytes>(at + ta.place(k), ra[q][k]);
+                        if (bias) add_bias(ra[q][k]);
                     }
-                }
 #pragma unroll
                 for (int k = 0; k < C::kTurnsB; ++k)
-                    if (tb.row + k * tb.rows < kRows) store_held<FMT>(at + C::kParts * C::kABytes + tb.place(k), rb[q][k]);
+                    if (tb.has(k, C::kRows)) store_held<FMT>(at + C::kParts * C::kABytes + tb.place(k), rb[q][k]);
+                if constexpr (kCopies) if (bias) {       // the copy engine's rows, before the slot may be filled again
+                    if (!barrier_wait(&s_copied[slot], parity ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int k = 0; k < C::kTurnsA; ++k)
+                        if (ta.has(k, C::kRows)) {
+                            load_words(ra[q][k].w, ring_ptr + slot * C::kStageBytes + ta.place(k));
+                            add_bias(ra[q][k]);
+                        }
+                }
                 writes_to_async();
                 __syncwarp();
                 if (lane == 0) barrier_arrive(&s_full[slot]);
@@ -389,27 +493,28 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                 ++chains;
             }
         } while (!end);
-    } else {
+    } else if (warp == C::kLoaders / 32) {
         if (lane == 0) {
             const uint32_t what = product_of((nj + 15) / 16 * 16);
             int slot = 0, chains = 0, link = 0;
             uint32_t parity = 0;
             for (int stage = 0; stage < stages; ++stage) {
-                if (!barrier_wait(&s_full[slot], parity)) {
+                if (!barrier_wait(&s_full[slot], parity) || (kCopies && !barrier_wait(&s_copied[slot], parity))) {
                     s_failed = 1;
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;");
                 const uint32_t at = ring + slot * C::kStageBytes, bt = at + C::kParts * C::kABytes;
 #pragma unroll
-                for (int k = 0; k < kRows / kStep; ++k)
+                for (int k = 0; k < C::kRows / kStep; ++k)
 #pragma unroll
                     for (int p = 0; p < C::kParts; ++p)
 #pragma unroll
                         for (int h = 0; h < TI / 128; ++h)
                             if (h * 128 < ni)
-                                product(tensor + (p > 0 ? C::kTile : 0) + h * TJ, operand_at(at + p * C::kABytes + h * 2 * kBlock + k * kStep * 128),
-                                        operand_at(bt + k * kStep * 128), what, link > 0 || k > 0 || p > 1);
+                                product(tensor + (p > 0 ? C::kTile : 0) + h * TJ,
+                                        operand_at<C::kBlock>(at + p * C::kABytes + h * 2 * C::kBlock + k * kStep * 128),
+                                        operand_at<C::kBlock>(bt + k * kStep * 128), what, link > 0 || k > 0 || p > 1);
                 products_arrive(&s_empty[slot]);
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
                 if (++link == a.chain && stage + 1 < stages) {
@@ -425,20 +530,43 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
             if (!barrier_wait(&s_done, chains & 1)) s_failed = 1;    // the tensor memory is freed after them
         }
         __syncwarp();
+    } else {
+        if (kCopies && lane == 0) {
+            const int boxes = (ni + 63) / 64;
+            int slot = 0, stage = 0;
+            uint32_t parity = 1;
+            for (; stage < stages; ++stage) {
+                if (!barrier_wait(&s_empty[slot], parity)) {
+                    s_failed = 1;
+                    break;
+                }
+                barrier_expect(&s_copied[slot], boxes * C::kBlock);
+                for (int k = 0; k < boxes; ++k)
+                    copy_box(ring + slot * C::kStageBytes + k * C::kBlock, &map, i0 + 64 * k,
+                             int(first + int64_t(stage) * C::kRows), &s_copied[slot]);
+                if (++slot == C::kStages) slot = 0, parity ^= 1;
+            }
+            // every copy has come before the block ends
+            for (int k = stage < C::kStages ? stage : C::kStages; k > 0; --k) {
+                const int s = (stage - k) % C::kStages;
+                if (!barrier_wait(&s_copied[s], (stage - k) / C::kStages & 1)) s_failed = 1;
+            }
+        }
+        __syncwarp();
     }
     __syncthreads();
     if (bias) {
         // the threads' sums of a column, in the order of their rows
         float *s = reinterpret_cast<float *>(ring_ptr);
         const int width = (ni + kUnit - 1) / kUnit * kUnit;
-        if (warp < C::kLoaders / 32 && ta.row < kRows)
+        if (warp < C::kLoaders / 32 && ta.row < C::kRows)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                reinterpret_cast<float2 *>(s + size_t(ta.row) * width + ta.unit * kUnit)[i] = sums[i];
+                reinterpret_cast<float2 *>(s + size_t(ta.row) * width + ta.piece * kUnit)[i] = sums[i];
         __syncthreads();
         for (int j = threadIdx.x; j < ni; j += C::kThreads) {
             float t = 0.0f;
-            for (int r = 0; r < ta.rows && r < kRows; ++r) t += s[size_t(r) * width + j];
+            for (int r = 0; r < ta.rows && r < C::kRows; ++r) t += s[size_t(r) * width + j];
             if (a.splits > 1)
                 a.part_bias[size_t(blockIdx.x) * a.N + i0 + j] = t;
             else
@@ -507,36 +635,73 @@ Tile tile_of(int32_t N, int32_t D, int dtype) {
     return {128, 256, 1};      // two sets of sums
 }
 
-// How the rows are shared out: ranges with sums of their own, as many as fill the device, of
-// eight stages at least; and the chains of sums within a range.
+// How the rows are shared out: ranges with sums of their own, as many as fill the device; and the chains of sums within a range.
 constexpr int kSms = 152;
+constexpr int kLeastRows = 256;     // of a range
 constexpr int kChain32 = 2048, kChain16 = 16384;    // rows; dW in float32, in 16 bits
 struct Shares {
-    int splits, chain;
+    int splits, chain;     // chain: rows
     bool part;         // sums leave the tensor memory before they are done
 };
 Shares shares_of(int64_t n, int32_t N, int32_t D, int dtype, int gdt) {
     const Tile t = tile_of(N, D, dtype);
     const int64_t tiles = int64_t((N + t.i - 1) / t.i) * ((D + t.j - 1) / t.j);
     int64_t s = kSms * t.ctas / tiles;
-    const int64_t most = (n + 8 * kRows - 1) / (8 * kRows);
+    const int64_t most = (n + kLeastRows - 1) / kLeastRows;
     if (s > most) s = most;
     if (s < 1) s = 1;
     const int rows = gdt == SS_F32 ? kChain32 : kChain16;
-    return {int(s), rows / kRows, s > 1 || n > rows};
+    return {int(s), rows, s > 1 || (gdt != SS_F32 && n > rows)};
+}
+
+// The driver's function that describes a matrix to the copy engine.
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+ss_status encoder(EncodeFn *fn, const char *who) {
+    static std::atomic<EncodeFn> known{nullptr};
+    *fn = known.load(std::memory_order_acquire);
+    if (*fn) return SS_OK;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const ss_status st =
+        check_cuda(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q), who);
+    if (st != SS_OK) return st;
+    if (q != cudaDriverEntryPointSuccess || !p) return fail(SS_ERR_CUDA, "%s: the driver has no cuTensorMapEncodeTiled", who);
+    *fn = reinterpret_cast<EncodeFn>(p);
+    known.store(*fn, std::memory_order_release);
+    return SS_OK;
+}
+
+// dy [n][N] of bfloat16 in boxes of 64 columns x `rows` rows, swizzled as the products read them.
+ss_status map_of(CUtensorMap *map, const DenseArgs &a, int rows, const char *who) {
+    EncodeFn encode;
+    const ss_status st = encoder(&encode, who);
+    if (st != SS_OK) return st;
+    const cuuint64_t dims[2] = {cuuint64_t(a.N), cuuint64_t(a.n)}, strides[1] = {cuuint64_t(a.dys) * 2};
+    const cuuint32_t box[2] = {64, cuuint32_t(rows)}, each[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(a.dy), dims, strides, box, each,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SS_OK : fail(SS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", who, int(r));
 }
 
 template <typename T, int TI, int TJ, int FMT>
-ss_status launch(const DenseArgs &a, cudaStream_t s) {
+ss_status launch(DenseArgs a, cudaStream_t s, const char *who) {
     using C = Config<T, TI, TJ>;
+    const int64_t each = (a.n + a.splits - 1) / a.splits;
+    a.rows = (each + C::kRows - 1) / C::kRows * C::kRows;
+    a.chain /= C::kRows;
     const dim3 grid(a.splits, (a.D + TJ - 1) / TJ, (a.N + TI - 1) / TI);
-    const bool aligned = units_aligned<T>(a.dy, a.dys);
-    auto kernel = aligned ? k_dense<T, TI, TJ, FMT, true> : k_dense<T, TI, TJ, FMT, false>;
+    const bool fast = a.n > 0 && units_aligned<T>(a.dy, a.dys) && aligned_to(a.x.q, 16) && a.x.stride % 16 == 0;
     static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
     const void *fn[2] = {(const void *)k_dense<T, TI, TJ, FMT, true>, (const void *)k_dense<T, TI, TJ, FMT, false>};
-    const ss_status st = ensure_dyn_smem(smem_ctx, fn, 2, C::kSmem, "k_dense");
+    ss_status st = ensure_dyn_smem(smem_ctx, fn, 2, C::kSmem, who);
     if (st != SS_OK) return st;
-    SS_LAUNCH("k_dense", s, kernel<<<grid, C::kThreads, C::kSmem, s>>>(a));
+    CUtensorMap map = {};
+    if (fast && C::kParts == 1 && (st = map_of(&map, a, C::kRows, who)) != SS_OK) return st;
+    auto kernel = fast ? k_dense<T, TI, TJ, FMT, true> : k_dense<T, TI, TJ, FMT, false>;
+    SS_LAUNCH("k_dense", s, kernel<<<grid, C::kThreads, C::kSmem, s>>>(a, map));
     return SS_OK;
 }
 
@@ -578,10 +743,8 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
     cudaStream_t s = (cudaStream_t)stream;
     const Shares sh = shares_of(n, N, D, dtype, grad_dtype);
     float *part = static_cast<float *>(workspace);
-    const int64_t each = (n + sh.splits - 1) / sh.splits;
-    const DenseArgs a{dy, dy_stride, rows8_of(x), n, N, D, (each + kRows - 1) / kRows * kRows,
-                      sh.splits, sh.chain, part, part + size_t(sh.splits) * N * D, dweight, dweight_stride, dbias,
-                      int(grad_dtype)};
+    const DenseArgs a{dy, dy_stride, rows8_of(x), n, N, D, 0, sh.splits, sh.chain, part,
+                      part + size_t(sh.splits) * N * D, dweight, dweight_stride, dbias, int(grad_dtype)};
     const Tile tile = tile_of(N, D, dtype);
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
@@ -589,11 +752,11 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
         with_format(x ? x->format : SS_INT8, [&](auto F) {
             constexpr int FMT = decltype(F)::value;
             if (tile.j == 256)
-                st = launch<T, kLargeI, 256, FMT>(a, s);
+                st = launch<T, kLargeI, 256, FMT>(a, s, who);
             else if (tile.j == 128)
-                st = launch<T, 128, 128, FMT>(a, s);
+                st = launch<T, 128, 128, FMT>(a, s, who);
             else
-                st = launch<T, 128, 64, FMT>(a, s);
+                st = launch<T, 128, 64, FMT>(a, s, who);
         });
     });
     if (st != SS_OK) return st;
