@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) k_dense_convert(DenseArgs a, Convert
 template <int PARTS>
 struct Big {
     static constexpr int kTI = PARTS == 1 ? 256 : 128, kTJ = 256;
-    static constexpr int kRows = 32;                                // of a stage
+    static constexpr int kRows = 64;                                // of a stage, and of a copy (32: 272 us for 161)
     static constexpr int kBlock = kRows * 128;                      // bytes of 64 columns of a stage
     static constexpr int kABytes = kTI / 64 * kBlock, kBBytes = kTJ / 64 * kBlock;
     static constexpr int kStageBytes = PARTS * kABytes + kBBytes;
@@ -117,10 +117,13 @@ struct BigArgs {
     int64_t dy_row, dy_part;       // where the chunk begins in dy's map, and how far one part is from the next
     int width;                     // columns of a tile
     bool first, last;              // chunk
+    int bias;                      // the bias' sums: 0 not from here, 1 to part_bias from row bias_row on, 2 to db
+    int bias_row;
 };
 
 // CTA (range of the rows, tile of D, tile of N).  Warps 0 to 7 read the sums, one thread
-// of warp 8 issues the products, one of warp 9 the copies.
+// of warp 8 issues the products, one of warp 9 the copies.  Where dy is used as it lies, the CTAs of the
+// first columns of x have warps 0 to 7 add up its columns out of shared memory on the way.
 template <int PARTS>
 __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
     k_dense_big(DenseArgs a, BigArgs b, const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap x_map) {
@@ -135,10 +138,12 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
     const int64_t first = int64_t(blockIdx.x) * b.split_rows;
     const int64_t last = first + b.split_rows < b.rows ? first + b.split_rows : b.rows;
     const int stages = last > first ? int((last - first + C::kRows - 1) / C::kRows) : 0;
+    const bool bias = PARTS == 1 && b.bias && blockIdx.y == 0;
+    const uint8_t *ring_ptr = s_raw + (ring - smem_of(s_raw));
 
     if (threadIdx.x == 0) {
         s_failed = 0;
-        for (int k = 0; k < C::kStages; ++k) barrier_init(&s_full[k], 1), barrier_init(&s_empty[k], 1);
+        for (int k = 0; k < C::kStages; ++k) barrier_init(&s_full[k], 1), barrier_init(&s_empty[k], bias ? 9 : 1);
         barrier_init(&s_done, 1);
         barrier_init(&s_drained, C::kDrainers / 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -149,9 +154,38 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
     tensor_fence_after();
     const uint32_t tensor = s_tensor;
 
+    F2 sums[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sums[k] = both(0.0f);
     if (warp < 8) {
+        int slot = 0;
+        uint32_t parity = 0;
         const int chains = stages ? (stages + a.chain - 1) / a.chain : 1;
         for (int chain = 0; chain < chains; ++chain) {
+            if (bias) {
+                // warp w rows w, w + 8, ... of a stage, lane l columns 8 l to 8 l + 7
+                const int stop = (chain + 1) * a.chain < stages ? (chain + 1) * a.chain : stages;
+                for (int stage = chain * a.chain; stage < stop; ++stage) {
+                    if (!barrier_wait(&s_full[slot], parity)) {
+                        s_failed = 1;
+                        break;
+                    }
+                    const uint8_t *at = ring_ptr + slot * C::kStageBytes + (lane >> 3) * C::kBlock;
+                    if (lane * kUnit < ni)
+#pragma unroll
+                        for (int r = warp; r < C::kRows; r += 8) {
+                            Raw<__nv_bfloat16> v;
+                            load_words(v.w, at + r * 128 + (((lane ^ r) & 7) << 4));
+                            F2 f[4];
+                            floats_of(f, v);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) sums[k] = add2(sums[k], f[k]);
+                        }
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(&s_empty[slot]);
+                    if (++slot == C::kStages) slot = 0, parity ^= 1;
+                }
+            }
             if (!barrier_wait(&s_done, chain & 1)) s_failed = 1;
             tensor_fence_after();
             const bool begins = b.first && chain == 0, ends = b.last && chain == chains - 1;
@@ -254,6 +288,22 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
     tensor_fence_before();
     __syncthreads();
     if (warp == 8) tensor_free<512>(tensor);
+    if (!bias) return;
+    float *s = reinterpret_cast<float *>(s_raw + (ring - smem_of(s_raw)));     // [8][256]
+    if (warp < 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) reinterpret_cast<float2 *>(s + warp * 256 + lane * kUnit)[k] = sums[k];
+    __syncthreads();
+    for (int i = threadIdx.x; i < ni; i += C::kThreads) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += s[w * 256 + i];
+        if (s_failed) t = __uint_as_float(0x7fffffffu);
+        if (b.bias == 2)
+            store_param(a.db, a.gdt, i0 + i, t);
+        else
+            a.part_bias[size_t(b.bias_row + blockIdx.x) * a.N + i0 + i] = t;
+    }
 }
 
 // ------------------------------------------------------------------ shares
@@ -279,7 +329,7 @@ Plan plan_of(int64_t n, int32_t N, int32_t D, int dtype, int gdt) {
     Plan p{};
     p.x_stride = round_up(D, kUnit), p.dy_stride = round_up(N, kUnit);
     const int64_t each = 2 * (p.x_stride + parts * p.dy_stride);
-    p.chunk = int64_t(kConverted) / each / 64 * 64;
+    p.chunk = int64_t(kConverted) / each / 64 * 64;      // whole stages
     if (p.chunk < kLeastChunk) p.chunk = kLeastChunk;
     if (p.chunk > n) p.chunk = n < 1 ? 1 : n;
     const int64_t tiles_i = (N + ti - 1) / ti;
@@ -300,7 +350,7 @@ Plan plan_of(int64_t n, int32_t N, int32_t D, int dtype, int gdt) {
     const int chain = gdt == SS_F32 ? kChain32 : kChain16;
     p.part = p.splits > 1 || (gdt != SS_F32 && n > (p.chunk < chain ? p.chunk : chain));
     const size_t sums = p.part ? size_t(p.splits) * N * D * sizeof(float) : 0;
-    const int64_t chunks = (n + p.chunk - 1) / p.chunk, slabs = chunks * (round_up(p.chunk, 64) / kSlab + 1);
+    const int64_t chunks = (n + p.chunk - 1) / p.chunk, slabs = chunks * (round_up(p.chunk, 64) / kSlab + 1 + p.splits);
     const int64_t padded = round_up(p.chunk, 64);
     p.bias_at = round_up(sums, 256);
     p.x_at = p.bias_at + round_up(size_t(slabs) * N * sizeof(float), 256);
@@ -324,31 +374,35 @@ ss_status run(const char *who, DenseArgs a, const Plan &p, uint8_t *ws, cudaStre
     ss_status st = ensure_dyn_smem(smem_ctx, &fn, 1, C::kSmem, who);
     if (st != SS_OK) return st;
     a.bias_splits = 0;
+    bool bias_left = false;        // to be added up yet
     __nv_bfloat16 *xw = reinterpret_cast<__nv_bfloat16 *>(ws + p.x_at), *dyw = reinterpret_cast<__nv_bfloat16 *>(ws + p.dy_at);
     for (int64_t first = 0; first < a.n || first == 0; first += p.chunk) {
         const int64_t rows = a.n - first < p.chunk ? a.n - first : p.chunk, padded = round_up(rows, 64);
-        const bool wants_dy = !direct || a.db;
         const int x_blocks = (a.D + kXColumns - 1) / kXColumns;
         ConvertArgs c{first, rows, padded, xw, p.x_stride, direct ? nullptr : dyw, p.dy_stride, x_blocks,
-                      a.db ? a.part_bias + size_t(a.bias_splits) * a.N : nullptr};
+                      a.db && !direct ? a.part_bias + size_t(a.bias_splits) * a.N : nullptr};
         const int slabs = int((padded + kSlab - 1) / kSlab);
         CUtensorMap x_map = {}, dy_map = {};
         if (rows > 0) {
-            const dim3 grid(slabs, x_blocks + (wants_dy ? (a.N + kDyColumns - 1) / kDyColumns : 0));
+            const dim3 grid(slabs, x_blocks + (direct ? 0 : (a.N + kDyColumns - 1) / kDyColumns));
             auto kernel = aligned && q16 ? k_dense_convert<T, FMT, true> : k_dense_convert<T, FMT, false>;
             SS_LAUNCH("k_dense_convert", s, kernel<<<grid, kThreads, 0, s>>>(a, c));
             if ((st = map_of(&x_map, xw, padded, a.D, p.x_stride, C::kRows, who)) != SS_OK) return st;
             st = direct ? map_of(&dy_map, a.dy, a.n, a.N, a.dys, C::kRows, who)
                         : map_of(&dy_map, dyw, kParts * padded, a.N, p.dy_stride, C::kRows, who);
             if (st != SS_OK) return st;
-            a.bias_splits += slabs;
+            if (!direct) a.bias_splits += slabs;
         }
+        const int bias = !a.db || !direct ? 0 : (p.splits == 1 && a.n <= p.chunk ? 2 : 1);
+        bias_left |= a.db && bias != 2;
         const BigArgs b{rows, round_up((rows + p.splits - 1) / p.splits, C::kRows), direct ? first : 0, padded, p.width,
-                        first == 0, first + p.chunk >= a.n};
+                        first == 0, first + p.chunk >= a.n, bias, a.bias_splits};
+        if (direct) a.bias_splits += p.splits;
         const dim3 grid(p.splits, (a.D + p.width - 1) / p.width, (a.N + C::kTI - 1) / C::kTI);
         SS_LAUNCH("k_dense_big", s, k_dense_big<kParts><<<grid, C::kThreads, C::kSmem, s>>>(a, b, dy_map, x_map));
     }
-    if (a.splits > 1 || a.db) dense_join(a, a.splits > 1, s, sms);
+    if (!bias_left) a.db = nullptr;
+    if (a.splits > 1 || bias_left) dense_join(a, a.splits > 1, s, sms);
     return SS_OK;
 }
 
