@@ -23,7 +23,8 @@ namespace {
 // which go through a ring in shared memory.  A bfloat16 dy needs no change: where it lies on 16-byte
 // boundaries (FAST), a thread has the copy engine bring it.  All else passes through the
 // registers of the loader warps before it is converted and stored.  One thread of another
-// warp issues the products; at the end of a chain the loaders read the sums out of the tensor memory.
+// warp issues the products; at the end the loaders read the sums out of the tensor memory.  A range is one
+// chain.
 //
 // TI = 64 (N up to 64): two parts of dy side by side are the 128 rows of one product, so
 // a float32 takes two products and not three; the parts' sums are joined through shared memory.
@@ -33,7 +34,7 @@ struct Config {
     static constexpr bool kStacked = TI == 64;
     static constexpr int kLoaders = 256;
     static constexpr int kThreads = kLoaders + 64;                  // and the warps of the products and of the copies
-    static constexpr int kRows = 32;                                // of a stage
+    static constexpr int kRows = 64;                                // of a stage
     static constexpr int kBlock = kRows * 128;                      // bytes of 64 columns of a stage
     static constexpr int kABlocks = kStacked ? (kParts + 1) / 2 * 2 : 2 * kParts;
     static constexpr int kPart = TI / 64 * kBlock;                  // bytes from one part to the next
@@ -41,13 +42,13 @@ struct Config {
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kProducts = kABlocks / 2;                  // of 128 rows each, a step
     static constexpr int kSums = kStacked ? kProducts : (kParts > 1 ? 2 : 1);
-    static constexpr int kStages = kStacked ? 3 : (kParts == 3 ? 2 : 3);
+    static constexpr int kStages = 2;
     static constexpr int kSmem = kStages * kStageBytes + 1024;      // and up to the first 1 KB boundary
-    static constexpr int kAhead = kParts == 3 && !kStacked ? 1 : 2;
+    static constexpr int kAhead = kParts == 2 ? 2 : 1;
     static constexpr int kTurnsA = kRows * (TI / kUnit) / kLoaders;
     static constexpr int kTurnsB = kRows * (TJ / kWide) / kLoaders < 1 ? 1 : kRows * (TJ / kWide) / kLoaders;
     static constexpr int kColumns = kSums * TJ <= 64 ? 64 : (kSums * TJ <= 128 ? 128 : 256);   // of tensor memory
-    static constexpr int kMinCtas = kStacked ? 3 : 2;
+    static constexpr int kMinCtas = 2;
 };
 
 // Where a thread's pieces of W columns of a stage lie: `valid` of them a row, the threads
@@ -69,13 +70,45 @@ struct Turns {
     __device__ __forceinline__ bool has(int k, int of) const { return row + k * rows < of; }
 };
 
+// A unit of dy as bfloat16s, a part APART bytes from the one before.
+template <typename T, int APART>
+__device__ __noinline__ void store_parts_special(uint32_t at, Raw<T> r) {
+    uint32_t w[parts_of<T>()][4];
+    cut_parts_special(w, r);
+#pragma unroll
+    for (int p = 0; p < parts_of<T>(); ++p) store16(at + p * APART, w[p]);
+}
+template <typename T, int APART>
+__device__ __forceinline__ void store_parts(uint32_t at, const Raw<T> &r) {
+    if constexpr (parts_of<T>() == 1) {
+        store16(at, r.w);
+    } else {
+        F2 f[4];
+        floats_of(f, r);
+        if (any_special(f)) {
+            store_parts_special<T, APART>(at, r);
+            return;
+        }
+#pragma unroll
+        for (int p = 0; p < parts_of<T>(); ++p) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = tops(f[i]);
+                if (p + 1 < parts_of<T>()) f[i] = rests(f[i]);
+            }
+            store16(at + p * APART, w);
+        }
+    }
+}
+
 template <typename T, int TI, int TJ, int FMT, bool FAST>
 __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>::kMinCtas)
     k_dense(DenseArgs a, int64_t rows, const __grid_constant__ CUtensorMap map) {
     using C = Config<T, TI, TJ>;
     constexpr bool kCopies = FAST && C::kParts == 1;
     extern __shared__ uint8_t s_raw[];
-    __shared__ uint64_t s_full[C::kStages], s_copied[C::kStages], s_empty[C::kStages], s_done, s_drained;
+    __shared__ uint64_t s_full[C::kStages], s_copied[C::kStages], s_empty[C::kStages], s_done;
     __shared__ uint32_t s_tensor, s_failed;
     const uint32_t ring = (smem_of(s_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = s_raw + (ring - smem_of(s_raw));
@@ -94,7 +127,6 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
             barrier_init(&s_empty[k], 1);
         }
         barrier_init(&s_done, 1);
-        barrier_init(&s_drained, C::kLoaders / 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == C::kLoaders / 32) {
@@ -113,9 +145,9 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
     // x from the other end of the threads: neither of the two takes all of them
     const Turns<C::kRows, kWide> tb(C::kLoaders - 1 - int(threadIdx.x), C::kLoaders, (nj + kWide - 1) / kWide);
 
-    // The sums of a chain out of the tensor memory, to where they go.  A warp reads the 32 lanes
+    // The sums out of the tensor memory, to where they go.  A warp reads the 32 lanes
     // (rows of dW) of its quarter, the warps of a quarter 8 columns in turn.
-    auto drain = [&](bool first_chain, bool last_chain) {
+    auto drain = [&] {
         const int quarter = warp & 3;
         const bool failed = *static_cast<volatile uint32_t *>(&s_failed) != 0;
         auto checked = [&](uint32_t (&v)[8]) {
@@ -155,10 +187,9 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                         for (int p = 1; p < C::kParts; ++p) t += s[(p * 64 + i) * kPitch + c + k];
                         v[k] = __float_as_uint(t);
                     }
-                    put(a, blockIdx.x, i, c0 + c, nj - c0 - c < 8 ? nj - c0 - c : 8, v, first_chain, last_chain);
+                    put(a, blockIdx.x, i, c0 + c, nj - c0 - c < 8 ? nj - c0 - c : 8, v, true, true);
                 }
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(C::kLoaders) : "memory");
         } else {
             const int i = quarter * 32 + lane;
 #pragma unroll 1
@@ -173,7 +204,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                     for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
                 }
                 checked(v);
-                if (i < ni) put(a, blockIdx.x, i, c, nj - c < 8 ? nj - c : 8, v, first_chain, last_chain);
+                if (i < ni) put(a, blockIdx.x, i, c, nj - c < 8 ? nj - c : 8, v, true, true);
             }
         }
     };
@@ -213,11 +244,10 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
 #pragma unroll
             for (int i = 0; i < 4; ++i) sums[i] = add2(sums[i], f[i]);
         };
-        int slot = 0, chains = 0;
+        int slot = 0;
         uint32_t parity = 1;
-        bool ok = true, end;
-        int base = 0;
-        do {
+        bool ok = true;
+        for (int base = 0; base < stages && ok; base += C::kAhead)
 #pragma unroll
             for (int q = 0; q < C::kAhead; ++q) {
                 if (base + q >= stages) break;
@@ -230,10 +260,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
 #pragma unroll
                     for (int k = 0; k < C::kTurnsA; ++k) {
                         if (!ta.has(k, C::kRows)) continue;
-                        uint32_t w[C::kParts][4];
-                        cut_parts(w, ra[q][k]);
-#pragma unroll
-                        for (int p = 0; p < C::kParts; ++p) store16(at + p * C::kPart + ta.place(k), w[p]);
+                        store_parts<T, C::kPart>(at + ta.place(k), ra[q][k]);
                         if (bias) add_bias(ra[q][k]);
                     }
 #pragma unroll
@@ -263,22 +290,14 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                 load(ra[q], rb[q]);
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
             }
-            base += C::kAhead;
-            end = !ok || base >= stages;
-            if (end || base % a.chain == 0) {
-                if (!ok || !barrier_wait(&s_done, chains & 1)) s_failed = 1;
-                tensor_fence_after();
-                drain(chains == 0, end);
-                tensor_fence_before();
-                __syncwarp();
-                if (lane == 0) barrier_arrive(&s_drained);
-                ++chains;
-            }
-        } while (!end);
+        if (!ok || !barrier_wait(&s_done, 0)) s_failed = 1;
+        tensor_fence_after();
+        drain();
+        tensor_fence_before();
     } else if (warp == C::kLoaders / 32) {
         if (lane == 0) {
             const uint32_t what = product_of((nj + 15) / 16 * 16);
-            int slot = 0, chains = 0, link = 0;
+            int slot = 0;
             uint32_t parity = 0;
             for (int stage = 0; stage < stages; ++stage) {
                 if (!barrier_wait(&s_full[slot], parity) || (kCopies && !barrier_wait(&s_copied[slot], parity))) {
@@ -294,21 +313,13 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
                         const int set = C::kStacked ? p : (p > 0 ? 1 : 0);
                         product(tensor + set * TJ, operand_at<C::kBlock>(at + p * 2 * C::kBlock + k * kStep * 128),
                                 operand_at<C::kBlock>(bt + k * kStep * 128), what,
-                                link > 0 || k > 0 || (!C::kStacked && p > 1));
+                                stage > 0 || k > 0 || (!C::kStacked && p > 1));
                     }
                 products_arrive(&s_empty[slot]);
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
-                if (++link == a.chain && stage + 1 < stages) {
-                    products_arrive(&s_done);
-                    if (!barrier_wait(&s_drained, chains & 1)) {
-                        s_failed = 1;
-                        break;
-                    }
-                    link = 0, ++chains;
-                }
             }
             products_arrive(&s_done);
-            if (!barrier_wait(&s_done, chains & 1)) s_failed = 1;    // the tensor memory is freed after them
+            if (!barrier_wait(&s_done, 0)) s_failed = 1;    // the tensor memory is freed after them
         }
         __syncwarp();
     } else {
@@ -360,71 +371,53 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         tensor_free<C::kColumns>(tensor);
 }
 
-// The partial sums' totals, of [N][D] (where `weight`) and then of the bias.
-struct Joined {
-    const float *p;
-    int64_t apart;
-    int count;
-};
-__device__ __forceinline__ Joined joined(const DenseArgs &a, int64_t all, int64_t k) {
-    return k < all ? Joined{a.part + k, all, a.splits} : Joined{a.part_bias + (k - all), a.N, a.bias_splits};
-}
-__device__ __forceinline__ void put_result(const DenseArgs &a, int64_t all, int64_t k, float t) {
-    if (k < all)
-        store_param(a.dw, a.gdt, k / a.D * a.dws + k % a.D, t);
-    else
-        store_param(a.db, a.gdt, k - all, t);
-}
-
-// A thread a value: few partial sums of many values.
-__global__ void __launch_bounds__(256) k_dense_join(DenseArgs a, bool weight) {
-    const int64_t all = weight ? int64_t(a.N) * a.D : 0, count = all + (a.db ? a.N : 0);
-    for (int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x; k < count; k += int64_t(gridDim.x) * 256) {
-        const Joined j = joined(a, all, k);
-        float t = 0.0f;
+// The partial sums' totals.  SLICES warps of a CTA take the partial sums s, s + SLICES, ... of the
+// same 32 V values side by side, and the slices are added in order: many slices of few values, or 4
+// values a lane where there are enough to fill the device.  The first w_ctas CTAs have dW, the others the bias.
+template <int SLICES, int V>
+__global__ void __launch_bounds__(SLICES * 32) k_dense_join(DenseArgs a, int w_ctas) {
+    __shared__ float s_t[SLICES][32 * V + 1];
+    const bool weight = int(blockIdx.x) < w_ctas;
+    const int64_t all = weight ? int64_t(a.N) * a.D : a.N;
+    const int64_t first = int64_t(weight ? blockIdx.x : blockIdx.x - w_ctas) * (32 * V);
+    const int count = weight ? a.splits : a.bias_splits, lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const float *p = (weight ? a.part : a.part_bias) + first + lane;
+    float t[V] = {};
 #pragma unroll 4
-        for (int v = 0; v < j.count; ++v) t += j.p[v * j.apart];
-        put_result(a, all, k, t);
-    }
-}
-
-// 32 values by 32 slices of the partial sums side by side, then the slices in order.
-__global__ void __launch_bounds__(1024) k_dense_join_many(DenseArgs a, bool weight) {
-    __shared__ float s_t[32][33];
-    const int64_t all = weight ? int64_t(a.N) * a.D : 0, count = all + (a.db ? a.N : 0);
-    const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
-    for (int64_t base = int64_t(blockIdx.x) * 32; base < count; base += int64_t(gridDim.x) * 32) {
-        const int64_t k = base + c;
-        float t = 0.0f;
-        if (k < count) {
-            const Joined j = joined(a, all, k);
-#pragma unroll 4
-            for (int v = q; v < j.count; v += 32) t += j.p[v * j.apart];
-        }
-        __syncthreads();
-        s_t[q][c] = t;
-        __syncthreads();
-        t = s_t[c][q];
+    for (int v = q; v < count; v += SLICES)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        const int64_t e = base + q;
-        if (c == 0 && e < count) put_result(a, all, e, t);
+        for (int k = 0; k < V; ++k)
+            if (first + lane + 32 * k < all) t[k] += p[v * all + 32 * k];
+#pragma unroll
+    for (int k = 0; k < V; ++k) s_t[q][lane + 32 * k] = t[k];
+    __syncthreads();
+    for (int j = threadIdx.x; j < 32 * V; j += SLICES * 32) {
+        const int64_t e = first + j;
+        if (e >= all) break;
+        float u = 0.0f;
+#pragma unroll
+        for (int v = 0; v < SLICES; ++v) u += s_t[v][j];
+        if (weight)
+            store_param(a.dw, a.gdt, e / a.D * a.dws + e % a.D, u);
+        else
+            store_param(a.db, a.gdt, e, u);
     }
 }
 
-// Ranges of rows with sums of their own: as many as fill the device, of kLeastRows at least.
+// Ranges of rows with sums of their own: as many as fill the device, in as many rounds as it takes
+// for none to be longer than a chain; of kLeastRows at least.
 constexpr int kLeastRows = 128;
-int splits_of(int64_t n, int32_t N) {
-    const int64_t s = kSms * (N <= 64 ? 3 : 2), most = (n + kLeastRows - 1) / kLeastRows;
+int splits_of(int64_t n, int gdt) {
+    const int64_t once = kSms * 2, chain = gdt == SS_F32 ? kChain32 : kChain16;
+    const int64_t most = (n + kLeastRows - 1) / kLeastRows, rounds = (n + once * chain - 1) / (once * chain);
+    const int64_t s = once * rounds;
     return int(s < most ? s : (most < 1 ? 1 : most));
 }
-bool needs_part(int64_t n, int splits, int gdt) { return splits > 1 || (gdt != SS_F32 && n > kChain16); }
 
 template <typename T, int TI, int TJ, int FMT>
 ss_status launch(DenseArgs a, cudaStream_t s, const char *who) {
     using C = Config<T, TI, TJ>;
     const int64_t each = (a.n + a.splits - 1) / a.splits, rows = (each + C::kRows - 1) / C::kRows * C::kRows;
-    a.chain = (a.gdt == SS_F32 ? kChain32 : kChain16) / C::kRows;
     const bool fast = a.n > 0 && units_aligned<T>(a.dy, a.dys) && aligned_to(a.x.q, 16) && a.x.stride % 16 == 0;
     static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
     const void *fn[2] = {(const void *)k_dense<T, TI, TJ, FMT, true>, (const void *)k_dense<T, TI, TJ, FMT, false>};
@@ -442,16 +435,21 @@ bool dense_sizes_ok(int64_t n, int32_t N, int32_t D) { return row_sizes_ok(n, D)
 }  // namespace
 
 void dense_join(const DenseArgs &a, bool weight, cudaStream_t s, int sms) {
-    const int64_t values = (weight ? int64_t(a.N) * a.D : 0) + (a.db ? a.N : 0);
-    if (values == 0) return;
-    if (a.splits >= 16 || !weight) {
-        const int64_t ctas = (values + 31) / 32;
-        SS_LAUNCH("k_dense_join_many", s,
-                  k_dense_join_many<<<int(ctas < sms * 16 ? ctas : sms * 16), 1024, 0, s>>>(a, weight));
-    } else {
-        const int64_t ctas = (values + 255) / 256;
-        SS_LAUNCH("k_dense_join", s, k_dense_join<<<int(ctas < sms * 16 ? ctas : sms * 16), 256, 0, s>>>(a, weight));
+    int64_t values = weight ? int64_t(a.N) * a.D : 0, biases = a.db ? a.N : 0;
+    const bool wide = values >= int64_t(sms) * 256;
+    if (wide && biases && a.bias_splits > 64) {      // too many for few slices
+        dense_join(a, false, s, sms);
+        biases = 0;
     }
+    const int each = wide ? 128 : 32;
+    const int64_t w = (values + each - 1) / each, ctas = w + (biases + each - 1) / each;
+    if (ctas == 0) return;
+    if (wide && a.splits < 16)
+        SS_LAUNCH("k_dense_join", s, k_dense_join<4, 4><<<unsigned(ctas), 128, 0, s>>>(a, int(w)));
+    else if (wide)
+        SS_LAUNCH("k_dense_join", s, k_dense_join<8, 4><<<unsigned(ctas), 256, 0, s>>>(a, int(w)));
+    else
+        SS_LAUNCH("k_dense_join", s, k_dense_join<32, 1><<<unsigned(ctas), 1024, 0, s>>>(a, int(w)));
 }
 
 }  // namespace ss
@@ -463,8 +461,8 @@ extern "C" {
 size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D, ss_dtype dtype, ss_dtype grad_dtype) {
     if (!dense_sizes_ok(n, N, D) || !dtype_known(dtype) || (grad_dtype != SS_F32 && grad_dtype != dtype)) return 0;
     if (dense_is_big(N, D)) return dense_big_workspace(n, N, D, dtype, grad_dtype);
-    const int splits = splits_of(n, N);
-    return needs_part(n, splits, grad_dtype) ? size_t(splits) * N * (size_t(D) + 1) * sizeof(float) : 256;
+    const int splits = splits_of(n, grad_dtype);
+    return splits > 1 ? size_t(splits) * N * (size_t(D) + 1) * sizeof(float) : 256;
 }
 
 ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n, int32_t N,
@@ -495,7 +493,7 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
         st = dense_big(who, a, dtype, format, workspace, s, sms);
         return st != SS_OK ? st : check_launch(who);
     }
-    a.splits = a.bias_splits = splits_of(n, N);
+    a.splits = a.bias_splits = splits_of(n, grad_dtype);
     a.part = static_cast<float *>(workspace);
     a.part_bias = a.part + size_t(a.splits) * N * D;
     with_type(dtype, [&](auto t) {

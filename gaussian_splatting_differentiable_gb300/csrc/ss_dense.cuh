@@ -69,41 +69,40 @@ __device__ __forceinline__ void cut_parts(uint32_t (&w)[1][4], const Raw<__nv_bf
     for (int i = 0; i < 4; ++i) w[0][i] = r.w[i];
 }
 template <typename T>
+__device__ __forceinline__ void cut_parts_special(uint32_t (&w)[parts_of<T>()][4], const Raw<T> &r) {
+    F2 f[4];
+    floats_of(f, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v[2] = {f[i].x, f[i].y};
+#pragma unroll
+        for (int p = 0; p < parts_of<T>(); ++p) {
+            uint32_t top[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t u = __float_as_uint(v[k]);
+                if ((u & 0x7fffffffu) > 0x7f800000u) u = 0x7fffffffu;
+                top[k] = u >> 16;
+                v[k] = (u & 0x7f800000u) == 0x7f800000u ? 0.0f : v[k] - __uint_as_float(u & 0xffff0000u);
+            }
+            w[p][i] = top[0] | top[1] << 16;
+        }
+    }
+}
+template <typename T>
 __device__ __forceinline__ void cut_parts(uint32_t (&w)[parts_of<T>()][4], const Raw<T> &r) {
-    constexpr int kParts = parts_of<T>();
     F2 f[4];
     floats_of(f, r);
     if (any_special(f)) {
-#pragma unroll 1
-        for (int p = 0; p < kParts; ++p) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v[2] = {f[i].x, f[i].y};
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t u = __float_as_uint(v[k]);
-                    if ((u & 0x7fffffffu) > 0x7f800000u) u = 0x7fffffffu;
-                    const float rest = (u & 0x7f800000u) == 0x7f800000u ? 0.0f : v[k] - __uint_as_float(u & 0xffff0000u);
-                    v[k] = rest;
-                    o[i] = k ? o[i] | (u & 0xffff0000u) : u >> 16;
-                }
-                f[i] = make_float2(v[0], v[1]);
-            }
-#pragma unroll
-            for (int q = 0; q < kParts; ++q)
-                if (q == p)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[q][i] = o[i];
-        }
+        cut_parts_special(w, r);
         return;
     }
 #pragma unroll
-    for (int p = 0; p < kParts; ++p)
+    for (int p = 0; p < parts_of<T>(); ++p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             w[p][i] = tops(f[i]);
-            if (p + 1 < kParts) f[i] = rests(f[i]);
+            if (p + 1 < parts_of<T>()) f[i] = rests(f[i]);
         }
 }
 

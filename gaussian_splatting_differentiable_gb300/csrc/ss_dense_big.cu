@@ -25,8 +25,8 @@ namespace {
 // ------------------------------------------------------------------ conversion
 
 constexpr int kThreads = 256;
-constexpr int kSlab = 128;             // rows of a CTA
-constexpr int kXColumns = 512, kDyColumns = 256;
+constexpr int kSlab = 64;              // rows of a CTA
+constexpr int kDyColumns = 256;
 
 struct ConvertArgs {
     int64_t first, rows, padded;   // the chunk: its first row, its rows, and with rows of zeros a multiple of kRows
@@ -34,41 +34,60 @@ struct ConvertArgs {
     int64_t x_stride;
     __nv_bfloat16 *dy;             // [parts][padded][dy_stride], NULL: dy is used where it is
     int64_t dy_stride;
-    int x_blocks;                  // CTAs (y) for x; the others for dy
+    int x_ctas, dy_blocks;
     float *bias;                   // [slab][N] of this chunk, NULL: not wanted
 };
 
-// CTA (slab of rows, block of columns): x to bfloat16, or dy to its parts, with the
-// slab's sum of each column of dy.  Bound by memory.
+// The first x_ctas CTAs turn x into bfloat16, pieces of 16 columns one after the other along their threads,
+// four in flight; the others, by slabs of rows and blocks of columns, dy into its parts, with
+// the slab's sum of each column.  Bound by memory.
 template <typename T, int FMT, bool FAST>
 __global__ void __launch_bounds__(kThreads) k_dense_convert(DenseArgs a, ConvertArgs c) {
-    constexpr int kParts = parts_of<T>();
+    constexpr int kParts = parts_of<T>(), kAhead = 4;
     __shared__ float s_sum[kThreads / 32][kDyColumns];
-    const int64_t r0 = int64_t(blockIdx.x) * kSlab, r1 = r0 + kSlab < c.padded ? r0 + kSlab : c.padded;
-    if (int(blockIdx.y) < c.x_blocks) {
-        const int j = blockIdx.y * kXColumns + (threadIdx.x & 31) * kWide;
-        if (j >= a.D) return;
-        const bool all = a.D - j > kUnit;
-        for (int64_t r = r0 + (threadIdx.x >> 5); r < r1; r += kThreads / 32) {
-            Wide h{{0u, 0u, 0u, 0u}, 127u};
-            if (r < c.rows)
-                h.load<FAST>(a.x.q + (c.first + r) * a.x.stride + j, a.x.scales + (c.first + r) * a.x.scale_stride + j / kGroup, all);
-            uint32_t w[8];
-            convert<FMT>(w, h);
-            uint4 *to = reinterpret_cast<uint4 *>(c.x + r * c.x_stride + j);
-            to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            if (all) to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (int(blockIdx.x) < c.x_ctas) {
+        const int per_row = (a.D + kWide - 1) / kWide;
+        const int64_t step = int64_t(c.x_ctas) * kThreads, rows = step / per_row;
+        const int more = int(step - rows * per_row);
+        int64_t r = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / per_row;
+        int u = int(int64_t(blockIdx.x) * kThreads + threadIdx.x - r * per_row);
+        while (r < c.padded) {
+            Wide h[kAhead];
+            __nv_bfloat16 *to[kAhead];
+            bool all[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int j = u * kWide;
+                to[k] = r < c.padded ? c.x + r * c.x_stride + j : nullptr, all[k] = a.D - j > kUnit;
+                h[k] = Wide{{0u, 0u, 0u, 0u}, 127u};
+                if (r < c.rows)
+                    h[k].template load<FAST>(a.x.q + (c.first + r) * a.x.stride + j,
+                                             a.x.scales + (c.first + r) * a.x.scale_stride + j / kGroup, all[k]);
+                r += rows, u += more;
+                if (u >= per_row) u -= per_row, ++r;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (!to[k]) continue;
+                uint32_t w[8];
+                convert<FMT>(w, h[k]);
+                uint4 *p = reinterpret_cast<uint4 *>(to[k]);
+                p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                if (all[k]) p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
         }
         return;
     }
+    const int slab = (int(blockIdx.x) - c.x_ctas) / c.dy_blocks, block = (int(blockIdx.x) - c.x_ctas) % c.dy_blocks;
+    const int64_t r0 = int64_t(slab) * kSlab, r1 = r0 + kSlab < c.padded ? r0 + kSlab : c.padded;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i0 = (blockIdx.y - c.x_blocks) * kDyColumns, i = i0 + lane * kUnit;
+    const int i0 = block * kDyColumns, i = i0 + lane * kUnit;
     const int count = a.N - i < kUnit ? a.N - i : kUnit;
     F2 sums[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) sums[k] = both(0.0f);
     if (count > 0)
-#pragma unroll 2
+#pragma unroll 4
         for (int64_t r = r0 + warp; r < r1; r += kThreads / 32) {
             const Raw<T> v = load_unit<T, FAST>(static_cast<const T *>(a.dy) + (c.first + r) * a.dys + i, r < c.rows ? count : 0);
             F2 f[4];
@@ -92,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) k_dense_convert(DenseArgs a, Convert
     float t = 0.0f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) t += s_sum[w][threadIdx.x];
-    c.bias[size_t(blockIdx.x) * a.N + j] = t;
+    c.bias[size_t(slab) * a.N + j] = t;
 }
 
 // ------------------------------------------------------------------ products
@@ -378,15 +397,16 @@ ss_status run(const char *who, DenseArgs a, const Plan &p, uint8_t *ws, cudaStre
     __nv_bfloat16 *xw = reinterpret_cast<__nv_bfloat16 *>(ws + p.x_at), *dyw = reinterpret_cast<__nv_bfloat16 *>(ws + p.dy_at);
     for (int64_t first = 0; first < a.n || first == 0; first += p.chunk) {
         const int64_t rows = a.n - first < p.chunk ? a.n - first : p.chunk, padded = round_up(rows, 64);
-        const int x_blocks = (a.D + kXColumns - 1) / kXColumns;
-        ConvertArgs c{first, rows, padded, xw, p.x_stride, direct ? nullptr : dyw, p.dy_stride, x_blocks,
+        const int64_t pieces = (padded * ((a.D + kWide - 1) / kWide) + 4 * kThreads - 1) / (4 * kThreads);
+        const int x_ctas = int(pieces < sms * 8 ? pieces : sms * 8), dy_blocks = (a.N + kDyColumns - 1) / kDyColumns;
+        ConvertArgs c{first, rows, padded, xw, p.x_stride, direct ? nullptr : dyw, p.dy_stride, x_ctas, dy_blocks,
                       a.db && !direct ? a.part_bias + size_t(a.bias_splits) * a.N : nullptr};
         const int slabs = int((padded + kSlab - 1) / kSlab);
         CUtensorMap x_map = {}, dy_map = {};
         if (rows > 0) {
-            const dim3 grid(slabs, x_blocks + (direct ? 0 : (a.N + kDyColumns - 1) / kDyColumns));
+            const int64_t grid = x_ctas + (direct ? 0 : int64_t(slabs) * dy_blocks);
             auto kernel = aligned && q16 ? k_dense_convert<T, FMT, true> : k_dense_convert<T, FMT, false>;
-            SS_LAUNCH("k_dense_convert", s, kernel<<<grid, kThreads, 0, s>>>(a, c));
+            SS_LAUNCH("k_dense_convert", s, kernel<<<unsigned(grid), kThreads, 0, s>>>(a, c));
             if ((st = map_of(&x_map, xw, padded, a.D, p.x_stride, C::kRows, who)) != SS_OK) return st;
             st = direct ? map_of(&dy_map, a.dy, a.n, a.N, a.dys, C::kRows, who)
                         : map_of(&dy_map, dyw, kParts * padded, a.N, p.dy_stride, C::kRows, who);
