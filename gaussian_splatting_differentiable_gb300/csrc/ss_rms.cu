@@ -27,10 +27,15 @@ struct Rows {
 
 // A row's place in the threads.  `lanes` threads share it, thread l of them
 // holding units l, l + lanes, ... (NV of them) in registers, so the row is read
-// once.  Narrow rows (MULTI false) take a power of two of lanes inside a warp, four at
-// least, and reduce by shuffles; wide ones take whole warps and reduce through
+// once.  Narrow rows (MULTI false) take a power of two of lanes inside a warp and reduce
+// by shuffles; wide ones take whole warps and reduce through
 // shared memory and a barrier of their own.  Groups of 32 columns are four lanes side
-// by side in both.
+// by side in both (fewer where the row ends with them).
+//
+// Rows that start off their blocks' boundaries, all tensors' alike (kShifted): units lie on the
+// boundaries, head elements of the first not being the row's; a group of lanes takes every
+// step-th row with step a multiple of the rows after which starts repeat, so its columns stay
+// fixed.
 constexpr int kMaxRowThreads = 512;    // x 2 units = 8192 columns, the widest row held in registers
 constexpr int kMaxGroups = 4;          // rows of several warps side by side in a CTA: of two warps at least
 constexpr int kRowWarps = kMaxRowThreads / 32;
@@ -42,19 +47,20 @@ struct Place {
 };
 
 bool in_registers(int32_t D) { return D <= kMaxRowThreads * 2 * kUnit; }
+bool shifted_in_registers(int32_t D) { return D + 2 * (kUnit - 1) < kMaxRowThreads * 2 * kUnit; }
 
 // Up to 32 lanes a unit each; a warp with two units a lane up to 64; from there on
 // whole warps.
-Place place_of(int32_t D, int *nv, bool *multi) {
+Place place_of(int32_t D, bool shifted, int *nv, bool *multi) {
     Place pl{};
-    pl.units = units_of(D);
+    pl.units = units_of(shifted ? D + kUnit - 1 : D);
     *nv = pl.units <= 32 ? 1 : 2;
     *multi = pl.units > 64;
     if (*multi) {
         pl.lanes = (pl.units + 63) / 64 * 32;
         pl.groups = pl.lanes < kThreads ? kThreads / pl.lanes : 1;
     } else {
-        pl.lanes = 4, pl.shift = 2;
+        pl.lanes = 1, pl.shift = 0;
         while (pl.lanes * *nv < pl.units) pl.lanes <<= 1, ++pl.shift;
         pl.groups = kThreads / pl.lanes;
     }
@@ -91,22 +97,38 @@ __device__ __forceinline__ void row_sum(float (&v)[K], const Place &pl, int grou
 
 // Where a thread's units lie.
 struct Units {
-    int lane, lanes;
+    int lane, lanes, head;
     int32_t D;
     bool first, last;    // of the lanes of a warp that share a row
     __device__ __forceinline__ int at(int k) const { return lane + k * lanes; }
-    // Elements of unit k that are a row's.
-    __device__ __forceinline__ int count(int k) const {
-        const int c = D - at(k) * kUnit;
+    // Elements of unit k that are the row's: from lo on, up to hi.
+    __device__ __forceinline__ int lo(int k) const { return at(k) == 0 ? head : 0; }
+    __device__ __forceinline__ int hi(int k) const {
+        const int c = D + head - at(k) * kUnit;
         return c <= 0 ? 0 : (c < kUnit ? c : kUnit);
     }
-    __device__ __forceinline__ bool prev() const { return !first; }
+    // The column of its element 0.
+    __device__ __forceinline__ int column(int k) const { return at(k) * kUnit - head; }
     __device__ __forceinline__ bool next(int k) const { return !last && (at(k) + 1) * kUnit < D; }
 };
 template <bool MULTI>
-__device__ __forceinline__ Units units_at(int lane, const Place &pl, int32_t D) {
+__device__ __forceinline__ Units units_at(int lane, const Place &pl, int32_t D, int head) {
     const int l = MULTI ? lane & 31 : lane;
-    return Units{lane, pl.lanes, D, l == 0, l == (MULTI ? 31 : pl.lanes - 1)};
+    return Units{lane, pl.lanes, head, D, l == 0, l == (MULTI ? 31 : pl.lanes - 1)};
+}
+
+// Unit k of the row at p (`here`: there is such a row).
+template <typename T, Lie LIE>
+__device__ __forceinline__ Raw<T> load_of(const T *p, const Units &c, int k, bool here) {
+    if constexpr (LIE == kShifted) return load_block(p + c.column(k), c.lo(k), here ? c.hi(k) : 0);
+    return load_unit<T, LIE == kAligned>(p + c.column(k), here ? c.hi(k) : 0);
+}
+template <typename T, Lie LIE>
+__device__ __forceinline__ void store_of(T *p, const Raw<T> &r, const Units &c, int k, bool here) {
+    if constexpr (LIE == kShifted)
+        store_block(p + c.column(k), r, here ? c.lo(k) : 0, here ? c.hi(k) : 0);
+    else
+        store_unit<T, LIE == kAligned>(p + c.column(k), r, here ? c.hi(k) : 0, !c.first, c.next(k));
 }
 
 // A thread's weights in float32 (1 where there are none, and past the row).
@@ -115,9 +137,9 @@ __device__ __forceinline__ void load_weights(F2 (&g)[NV][4], const void *w, int 
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         float f[kUnit];
-        const int j = c.at(k) * kUnit, n = w ? c.count(k) : 0;
+        const int j = c.column(k), lo = c.lo(k), hi = w ? c.hi(k) : 0;
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) f[i] = i < n ? load_param(w, pdt, j + i) : 1.0f;
+        for (int i = 0; i < kUnit; ++i) f[i] = i >= lo && i < hi ? load_param(w, pdt, j + i) : 1.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[k][i] = make_float2(f[2 * i], f[2 * i + 1]);
     }
@@ -154,19 +176,19 @@ __device__ __forceinline__ void put_group(int fmt, const Rows8 &out, int64_t row
 // A unit into 8 bits; all lanes of a warp together.  What lies past the row is whatever the
 // unit has there, and counts for nothing.
 template <int FMT>
-__device__ __forceinline__ void put_held(const Rows8 &out, int64_t row, int u, int count, const F2 (&v)[4]) {
+__device__ __forceinline__ void put_held(const Rows8 &out, int64_t row, int u, int count, const F2 (&v)[4], int lanes) {
     F2 f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         f[i] = make_float2(2 * i < count ? v[i].x : 0.0f, 2 * i + 1 < count ? v[i].y : 0.0f);
-    const uint32_t e = group_exponent<FMT>(f);
+    const uint32_t e = group_exponent<FMT>(f, lanes);
     if (count > 0) put_unit<FMT>(out, row, u, e, f);
 }
-__device__ __forceinline__ void put_held(int fmt, const Rows8 &out, int64_t row, int u, int count, const F2 (&v)[4]) {
+__device__ __forceinline__ void put_held(int fmt, const Rows8 &out, int64_t row, int u, int count, const F2 (&v)[4], int lanes) {
     if (fmt == SS_INT8)
-        put_held<SS_INT8>(out, row, u, count, v);
+        put_held<SS_INT8>(out, row, u, count, v, lanes);
     else
-        put_held<SS_E4M3>(out, row, u, count, v);
+        put_held<SS_E4M3>(out, row, u, count, v, lanes);
 }
 
 struct FwdArgs {
@@ -188,25 +210,22 @@ struct FwdArgs {
 };
 
 // A row from registers: its sum with the residual, its square's mean, and every
-// output that is wanted.  The next row's loads are in flight meanwhile.
-template <typename T, int NV, bool MULTI, bool ALIGNED, bool RES>
+// output that is wanted.  The next row's loads are in flight meanwhile.  (kShifted: without
+// outputs in 8 bits, whose groups begin with the row.)
+template <typename T, int NV, bool MULTI, Lie LIE, bool RES>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_rms_fwd(FwdArgs a, Place pl) {
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][1][kRowWarps];
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
     const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
-    const Units c = units_at<MULTI>(lane, pl, a.D);
     const int64_t step = int64_t(gridDim.x) * pl.groups, row0 = int64_t(blockIdx.x) * pl.groups + group;
-    int count[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) count[k] = c.count(k);
+    const Units c = units_at<MULTI>(lane, pl, a.D, LIE == kShifted ? head_of<T>(static_cast<const T *>(a.x) + row0 * a.xs) : 0);
     Raw<T> x[NV], res[NV];
     auto load = [&](int64_t row) {
         const T *px = static_cast<const T *>(a.x) + row * a.xs, *pr = static_cast<const T *>(a.residual) + row * a.rs;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int n = row < a.n ? count[k] : 0;
-            x[k] = load_unit<T, ALIGNED>(px + c.at(k) * kUnit, n);
-            if (RES) res[k] = load_unit<T, ALIGNED>(pr + c.at(k) * kUnit, n);
+            x[k] = load_of<T, LIE>(px, c, k, row < a.n);
+            if (RES) res[k] = load_of<T, LIE>(pr, c, k, row < a.n);
         }
     };
     load(row0);
@@ -234,8 +253,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_rms_fwd(F
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[k][i] = add2(h[k][i], q[i]);
                 const Raw<T> r = raw_of<T>(h[k]);
-                store_unit<T, ALIGNED>(static_cast<T *>(a.sum) + row * a.ss_ + c.at(k) * kUnit, r, here ? count[k] : 0,
-                                       c.prev(), c.next(k));
+                store_of<T, LIE>(static_cast<T *>(a.sum) + row * a.ss_, r, c, k, here);
                 floats_of(h[k], r);
             }
 #pragma unroll
@@ -248,14 +266,13 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_rms_fwd(F
         const F2 rr = both(r);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int n = here ? count[k] : 0;
-            if (a.kept_fmt >= 0) put_held(a.kept_fmt, a.kept, row, c.at(k), n, h[k]);
+            if (LIE != kShifted && a.kept_fmt >= 0)
+                put_held(a.kept_fmt, a.kept, row, c.at(k), here ? c.hi(k) : 0, h[k], pl.lanes);
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[k][i] = mul2(mul2(h[k][i], rr), g[k][i]);
-            if (a.y)
-                store_unit<T, ALIGNED>(static_cast<T *>(a.y) + row * a.ys + c.at(k) * kUnit, raw_of<T>(h[k]), n,
-                                       c.prev(), c.next(k));
-            if (a.out_fmt >= 0) put_held(a.out_fmt, a.out, row, c.at(k), n, h[k]);
+            if (a.y) store_of<T, LIE>(static_cast<T *>(a.y) + row * a.ys, raw_of<T>(h[k]), c, k, here);
+            if (LIE != kShifted && a.out_fmt >= 0)
+                put_held(a.out_fmt, a.out, row, c.at(k), here ? c.hi(k) : 0, h[k], pl.lanes);
         }
         if (here && lane == 0 && a.rstd) a.rstd[row] = r;
     }
@@ -368,21 +385,20 @@ __global__ void __launch_bounds__(kThreads) k_norm8_bwd_rows_wide(BwdArgs a) {
 // row's loads are in flight meanwhile.  The weights' sums stay in registers over all of a
 // CTA's rows and leave one partial sum a CTA in a.part (none where it is NULL), or, where one CTA
 // has all rows, the gradients themselves.
-template <typename T, int NV, bool MULTI, bool ALIGNED, bool CENTRED, bool HELD>
+template <typename T, int NV, bool MULTI, Lie LIE, bool CENTRED, bool HELD>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd(BwdArgs a, Place pl, bool alone) {
     constexpr int kSums = CENTRED ? 2 : 1;
     extern __shared__ float4 s_gamma[];      // [2 NV][threads]; at the end the sums
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][kSums][kRowWarps];
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
     const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
-    const Units c = units_at<MULTI>(lane, pl, a.D);
     const int64_t step = int64_t(gridDim.x) * pl.groups, row0 = int64_t(blockIdx.x) * pl.groups + group;
-    int count[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) count[k] = c.count(k);
+    const Units c =
+        units_at<MULTI>(lane, pl, a.D, LIE == kShifted ? head_of<T>(static_cast<const T *>(a.dy) + row0 * a.dys) : 0);
+    using HeldUnit = typename std::conditional<LIE == kShifted, HeldAcross, Held>::type;
     struct Row {
         Raw<T> dy[NV], dsum[NV], x[HELD ? 1 : NV];
-        Held q[HELD ? NV : 1];
+        HeldUnit q[HELD ? NV : 1];
         float mu, r;
     };
     auto load = [&](Row &w, int64_t row) {
@@ -391,20 +407,26 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
                 *px = static_cast<const T *>(a.h) + row * a.hs;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int n = here ? count[k] : 0, j = c.at(k) * kUnit;
-            w.dy[k] = load_unit<T, ALIGNED>(pd + j, n);
-            if (!CENTRED && a.dsum) w.dsum[k] = load_unit<T, ALIGNED>(ps + j, n);
-            if constexpr (HELD)
-                w.q[k].load(a.kept, row, c.at(k), n > 0);
+            w.dy[k] = load_of<T, LIE>(pd, c, k, here);
+            if (!CENTRED && a.dsum) w.dsum[k] = load_of<T, LIE>(ps, c, k, here);
+            if constexpr (!HELD)
+                w.x[k] = load_of<T, LIE>(px, c, k, here);
+            else if constexpr (LIE == kShifted)
+                w.q[k].load(a.kept, row, c.column(k), a.D, here && c.hi(k) > 0);
             else
-                w.x[k] = load_unit<T, ALIGNED>(px + j, n);
+                w.q[k].load(a.kept, row, c.at(k), here && c.hi(k) > 0);
         }
         w.mu = CENTRED && here ? a.mean[row] : 0.0f;
         w.r = here ? a.rstd[row] : 0.0f;
     };
-    // g = (h - mean) r of unit k, zeros past the row
+    // g = (h - mean) r of unit k; what is not the row's meets zeros of dy
     auto normed = [&](F2 (&g)[4], const Row &w, int k) {
-        if constexpr (HELD) {
+        if constexpr (HELD && LIE == kShifted) {
+            if (a.fmt == SS_INT8)
+                w.q[k].template values<SS_INT8>(g, c.column(k));
+            else
+                w.q[k].template values<SS_E4M3>(g, c.column(k));
+        } else if constexpr (HELD) {
             if (a.fmt == SS_INT8)
                 w.q[k].template values<SS_INT8>(g);
             else
@@ -491,21 +513,21 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
 #pragma unroll
                 for (int i = 0; i < 4; ++i) d[i] = add2(d[i], u[i]);
             }
-            store_unit<T, ALIGNED>(static_cast<T *>(a.dx) + row * a.dxs + c.at(k) * kUnit, raw_of<T>(d),
-                                   row < a.n ? count[k] : 0, c.prev(), c.next(k));
+            store_of<T, LIE>(static_cast<T *>(a.dx) + row * a.dxs, raw_of<T>(d), c, k, row < a.n);
         }
     }
     start_dependents();
     if (!a.part) return;
-    // The CTA's sums, in fixed order: the rows of a warp are joined by shuffles
-    // (!MULTI), then the warps or groups in turn, in gamma's place.
+    // The CTA's sums, in fixed order: the rows of a warp are joined by shuffles where their columns
+    // are the same (!MULTI, not kShifted), then the warps or groups in turn, in gamma's place.
     __syncthreads();                       // gamma has been read
+    constexpr bool kFold = !MULTI && LIE != kShifted;
     const int cols = kSums * a.D;
-    const int slots = MULTI ? pl.groups : kThreads / 32;
+    const int slots = kFold ? kThreads / 32 : pl.groups;
     float *s_sum = reinterpret_cast<float *>(s_gamma);
     float *part = a.part + size_t(blockIdx.x) * cols;
     const bool direct = slots == 1 && !alone;
-    float *mine = direct ? part : s_sum + size_t(MULTI ? group : threadIdx.x >> 5) * cols;
+    float *mine = direct ? part : s_sum + size_t(kFold ? threadIdx.x >> 5 : group) * cols;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -514,9 +536,10 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
             for (int i = 0; i < kUnit; ++i) {
                 const F2 t = q ? db[k][i / 2] : dg[k][i / 2];
                 float v = i & 1 ? t.y : t.x;
-                if (!MULTI)
+                if (kFold)
                     for (int o = pl.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (i < count[k] && (MULTI || (threadIdx.x & 31) < pl.lanes)) mine[q * a.D + c.at(k) * kUnit + i] = v;
+                if (i >= c.lo(k) && i < c.hi(k) && (!kFold || (threadIdx.x & 31) < pl.lanes))
+                    mine[q * a.D + c.column(k) + i] = v;
             }
     if (direct) return;
     __syncthreads();
@@ -560,15 +583,16 @@ __global__ void __launch_bounds__(1024) k_norm8_bwd_final(const float *part, int
 // Partial sums of the weights' gradients that the workspace has room for.
 constexpr int kMaxSmem = 200 * 1024;
 constexpr int kMaxParts = 1024;
-int64_t weight_parts(int64_t n) { return n < 1 ? 1 : (n < kMaxParts ? n : kMaxParts); }
+int64_t weight_parts(int64_t n) { return n + kUnit < kMaxParts ? n + kUnit : kMaxParts; }   // a grid is rounded up to a period
 int wide_grid(int64_t n, int sms) { return int(n < int64_t(sms) * 8 ? n : int64_t(sms) * 8); }
 
 // As many CTAs as fit the device at once (times `waves` where each would have many
 // rows of few values: the later ones even out what the memory's two halves
-// take), and no more than share the rows evenly.
+// take), and no more than share the rows evenly; a multiple of the period where rows start
+// differently.
 template <typename K>
-int grid_of(std::atomic<unsigned long long> *known, K kernel, int threads, size_t smem, int64_t n, int groups, int waves,
-            int most, int sms) {
+int grid_of(std::atomic<unsigned long long> *known, K kernel, int threads, size_t smem, int64_t n, int groups, int period,
+            int waves, int most, int sms) {
     // the last answer, by what it depends on (one kernel, one architecture)
     const unsigned long long key = (unsigned long long)(threads) << 40 | (unsigned long long)(smem) << 8;
     const unsigned long long k = known->load(std::memory_order_relaxed);
@@ -582,7 +606,9 @@ int grid_of(std::atomic<unsigned long long> *known, K kernel, int threads, size_
     if (n >= fit * groups * 48) fit *= waves;
     if (fit > most) fit = most;
     const int64_t turns = (n + fit * groups - 1) / (fit * groups);
-    const int64_t grid = (n + turns * groups - 1) / (turns * groups);
+    int64_t grid = (n + turns * groups - 1) / (turns * groups);
+    const int p = groups % period == 0 ? 1 : period;
+    grid = (grid + p - 1) / p * p;
     return int(grid < 1 ? 1 : grid);
 }
 
@@ -595,6 +621,15 @@ void with_place(int nv, bool multi, F &&f) {
         f(std::integral_constant<int, 2>(), std::false_type());
     else
         f(std::integral_constant<int, 1>(), std::false_type());
+}
+template <typename F>
+void with_lie(Lie lie, F &&f) {
+    if (lie == kAligned)
+        f(std::integral_constant<Lie, kAligned>());
+    else if (lie == kShifted)
+        f(std::integral_constant<Lie, kShifted>());
+    else
+        f(std::integral_constant<Lie, kAnyhow>());
 }
 template <typename F>
 void with_flag(bool b, F &&f) {
@@ -613,16 +648,19 @@ void launch_fwd(const FwdArgs &a, int sms, cudaStream_t s) {
     const bool aligned = units_aligned<T>(a.x, a.xs) &&
                          (!a.residual || (units_aligned<T>(a.residual, a.rs) && units_aligned<T>(a.sum, a.ss_))) &&
                          (!a.y || units_aligned<T>(a.y, a.ys));
+    const bool alike = (!a.residual || (start_alike<T>(a.x, a.xs, a.residual, a.rs) && start_alike<T>(a.x, a.xs, a.sum, a.ss_))) &&
+                       (!a.y || start_alike<T>(a.x, a.xs, a.y, a.ys)) && a.kept_fmt < 0 && a.out_fmt < 0;
+    const Lie lie = aligned ? kAligned : (alike && shifted_in_registers(a.D) ? kShifted : kAnyhow);
     int nv;
     bool multi;
-    const Place pl = place_of(a.D, &nv, &multi);
-    const int threads = multi ? pl.lanes * pl.groups : kThreads;
+    const Place pl = place_of(a.D, lie == kShifted, &nv, &multi);
+    const int threads = multi ? pl.lanes * pl.groups : kThreads, period = lie == kShifted ? period_of(a.xs) : 1;
     with_place(nv, multi, [&](auto NV, auto MULTI) {
-        with_flag(aligned, [&](auto ALIGNED) {
+        with_lie(lie, [&](auto LIE) {
             with_flag(a.residual != nullptr, [&](auto RES) {
-                auto kernel = k_rms_fwd<T, NV(), MULTI(), ALIGNED(), RES()>;
+                auto kernel = k_rms_fwd<T, NV(), MULTI(), LIE(), RES()>;
                 static std::atomic<unsigned long long> known{0};
-                const int grid = grid_of(&known, kernel, threads, 0, a.n, pl.groups, multi ? 1 : 8, 1 << 30, sms);
+                const int grid = grid_of(&known, kernel, threads, 0, a.n, pl.groups, period, multi ? 1 : 8, 1 << 30, sms);
                 SS_LAUNCH("k_rms_fwd", s, kernel<<<grid, threads, 0, s>>>(a, pl));
             });
         });
@@ -648,17 +686,20 @@ ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
     }
     const bool aligned = units_aligned<T>(a.dy, a.dys) && units_aligned<T>(a.dx, a.dxs) &&
                          (HELD || units_aligned<T>(a.h, a.hs)) && (!a.dsum || units_aligned<T>(a.dsum, a.dss));
+    const bool alike = start_alike<T>(a.dy, a.dys, a.dx, a.dxs) && (HELD || start_alike<T>(a.dy, a.dys, a.h, a.hs)) &&
+                       (!a.dsum || start_alike<T>(a.dy, a.dys, a.dsum, a.dss));
+    const Lie lie = aligned ? kAligned : (alike && shifted_in_registers(a.D) ? kShifted : kAnyhow);
     int nv;
     bool multi;
-    const Place pl = place_of(a.D, &nv, &multi);
-    const int threads = multi ? pl.lanes * pl.groups : kThreads;
+    const Place pl = place_of(a.D, lie == kShifted, &nv, &multi);
+    const int threads = multi ? pl.lanes * pl.groups : kThreads, period = lie == kShifted ? period_of(a.dys) : 1;
     // what one CTA takes at once needs no launch that adds up several CTAs' sums
     const bool alone = a.n <= pl.groups;
     ss_status st = SS_OK;
     with_place(nv, multi, [&](auto NV, auto MULTI) {
-        with_flag(aligned, [&](auto ALIGNED) {
-            auto kernel = k_norm8_bwd<T, NV(), MULTI(), ALIGNED(), CENTRED, HELD>;
-            const int slots = MULTI() ? pl.groups : kThreads / 32;
+        with_lie(lie, [&](auto LIE) {
+            auto kernel = k_norm8_bwd<T, NV(), MULTI(), LIE(), CENTRED, HELD>;
+            const int slots = MULTI() || LIE() == kShifted ? pl.groups : kThreads / 32;
             size_t smem = size_t(2 * NV()) * threads * sizeof(float4);
             const size_t sums = a.dgamma && (slots > 1 || alone) ? size_t(slots) * cols * sizeof(float) : 0;
             if (smem < sums) smem = sums;
@@ -666,7 +707,7 @@ ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
             const void *fn = (const void *)kernel;
             if ((st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "k_norm8_bwd")) != SS_OK) return;
             static std::atomic<unsigned long long> known{0};
-            const int grid = alone ? 1 : grid_of(&known, kernel, threads, smem, a.n, pl.groups, 1, kMaxParts, sms);
+            const int grid = alone ? 1 : grid_of(&known, kernel, threads, smem, a.n, pl.groups, period, 1, kMaxParts - kUnit, sms);
             BwdArgs b = a;
             if (!a.dgamma) b.part = nullptr;
             SS_LAUNCH("k_norm8_bwd", s, kernel<<<grid, threads, smem, s>>>(b, pl, alone));

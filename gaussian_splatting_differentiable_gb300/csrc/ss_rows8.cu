@@ -71,29 +71,40 @@ __device__ __forceinline__ F2 held_to<__half>(F2 v) {
                        isnan(v.y) ? v.y : fminf(fmaxf(v.y, -65504.0f), 65504.0f));
 }
 
+// Where x's rows start off their blocks' boundaries, units lie on them all the same, and take what
+// is held from two units (one more of them a row then).
 template <typename T, int FMT, bool ALIGNED, int AHEAD>
 __global__ void __launch_bounds__(kThreads) k_rows8_unpack(Rows8 in, int64_t n, int32_t D, T *x, int64_t xs) {
-    Walk w(n, D);
-    const int lane = threadIdx.x & 31;
-    while (__any_sync(0xffffffffu, w.row < n)) {
-        Held h[AHEAD];
+    Walk w(n, ALIGNED ? D : D + kUnit - 1);
+    typename std::conditional<ALIGNED, Held, HeldAcross>::type h[AHEAD];
+    while (w.row < n) {
         T *p[AHEAD];
-        int u[AHEAD], count[AHEAD];
+        int lo[AHEAD], hi[AHEAD], column[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            u[k] = w.u, count[k] = w.count(D);
-            h[k].load(in, w.row, u[k], count[k] > 0);
-            p[k] = x + w.row * xs + u[k] * kUnit;
+            T *at = x + w.row * xs;
+            const int head = ALIGNED ? 0 : head_of<T>(at);
+            column[k] = w.u * kUnit - head, p[k] = at + column[k];
+            lo[k] = w.u == 0 ? head : 0;
+            const int c = D - column[k];
+            hi[k] = w.row >= n || c <= 0 ? 0 : (c < kUnit ? c : kUnit);
+            if constexpr (ALIGNED)
+                h[k].load(in, w.row, w.u, hi[k] > 0);
+            else
+                h[k].load(in, w.row, column[k], D, hi[k] > 0);
             w.next();
         }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
+            if (hi[k] <= 0) continue;
             F2 f[4];
-            h[k].template values<FMT>(f);
+            if constexpr (ALIGNED)
+                h[k].template values<FMT>(f);
+            else
+                h[k].template values<FMT>(f, column[k]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = held_to<T>(f[i]);
-            store_unit<T, ALIGNED>(p[k], raw_of<T>(f), count[k], u[k] > 0 && lane > 0,
-                                   (u[k] + 1) * kUnit < D && lane < 31);
+            store_block(p[k], raw_of<T>(f), lo[k], hi[k]);
         }
     }
 }

@@ -92,17 +92,17 @@ __device__ __forceinline__ float decode1(uint8_t q) {
     return a.x;
 }
 
-// Of a group whose 32 values four lanes side by side hold, 8 each (zeros past the row): the biased
-// exponent of its scale, in all four.
+// Of a group whose 32 values four lanes side by side hold, 8 each (zeros past the row; fewer
+// lanes where the row has fewer columns): the biased exponent of its scale, in all of them.
 template <int FMT>
-__device__ __forceinline__ uint32_t group_exponent(const F2 (&f)[4]) {
+__device__ __forceinline__ uint32_t group_exponent(const F2 (&f)[4], int lanes = 4) {
     // as whole numbers: NaN is the largest magnitude of all
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         m = max(m, max(__float_as_uint(f[i].x) & 0x7fffffffu, __float_as_uint(f[i].y) & 0x7fffffffu));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (lanes > 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    if (lanes > 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     return exponent_of<FMT>(m);
 }
 
@@ -141,6 +141,37 @@ struct Held {
         const F2 s = both(scale_of(e));
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], s);
+    }
+};
+
+// Eight elements from column j on (j down to -7, where the first are not the row's and read as anything
+// finite that the row's first group holds), which need not begin with a unit: bytes of two
+// units, and scales of two groups where `edge`, the column where the second begins, is among them.
+struct HeldAcross {
+    uint2 a, b;
+    uint32_t e0, e1;
+    __device__ __forceinline__ void load(const Rows8 &in, int64_t row, int j, int32_t D, bool here) {
+        a = b = make_uint2(0u, 0u), e0 = e1 = 127u;
+        if (!here) return;
+        const uint8_t *q = in.q + row * in.stride, *s = in.scales + row * in.scale_stride;
+        const int u = j >> 3, last = (D - 1) / kUnit;              // units u and u + 1
+        if (u >= 0) a = *reinterpret_cast<const uint2 *>(q + u * kUnit);
+        if ((j & 7) && u < last) b = *reinterpret_cast<const uint2 *>(q + (u + 1) * kUnit);
+        const int g = j < 0 ? 0 : j / kGroup, h = (j + kUnit - 1) / kGroup, most = (D - 1) / kGroup;
+        e0 = s[g], e1 = s[h < most ? h : most];
+    }
+    template <int FMT>
+    __device__ __forceinline__ void values(F2 (&f)[4], int j) const {
+        const int off = j & 7, bits = 8 * (off & 3);
+        const bool up = off & 4;
+        const uint32_t w0 = up ? a.y : a.x, w1 = up ? b.x : a.y, w2 = up ? b.y : b.x;
+        decode4<FMT>(f[0], f[1], __funnelshift_r(w0, w1, bits));
+        decode4<FMT>(f[2], f[3], __funnelshift_r(w1, w2, bits));
+        const float s0 = scale_of(e0), s1 = scale_of(e1);
+        const int edge = kGroup - (j & (kGroup - 1));              // elements from here on are the second group's
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = mul2(f[i], make_float2(2 * i < edge ? s0 : s1, 2 * i + 1 < edge ? s0 : s1));
     }
 };
 

@@ -3,8 +3,10 @@
 // 16-bit row, 32 of a float32 row; four of them, in four lanes side by side,
 // share a scale.
 //
-// Rows start anywhere (to their type's alignment).  ALIGNED: every unit starts on
-// a boundary of its size, and is one load or store.  Otherwise a unit is cut out of
+// Rows start anywhere (to their type's alignment).  kAligned: every unit starts on
+// a boundary of its size, and is one load or store.  kShifted: rows do not, but all tensors'
+// rows alike; units lie on the boundaries, and the first and the last of a row are partly its.
+// kAnyhow: units begin with the row, and a unit is cut out of
 // the 16-byte vectors that hold it, the lanes of a warp side by side reading each
 // vector twice (the second time from L1); and a store goes by vectors too, each
 // put together from a lane's first elements and the lane before's last.
@@ -20,6 +22,8 @@ namespace ss {
 
 constexpr int kUnit = 8;
 __host__ __device__ inline int units_of(int32_t D) { return (D + kUnit - 1) / kUnit; }
+
+enum Lie { kAligned, kShifted, kAnyhow };
 
 template <typename T>
 struct Raw {
@@ -153,6 +157,43 @@ __device__ __forceinline__ void store_element(T *p, const Raw<T> &r, int i) {
     }
 }
 
+// Four, two and one elements from element i on, a multiple of as many, at a place aligned for them.
+template <typename T>
+__device__ __forceinline__ void store_four(T *p, const Raw<T> &r, bool upper) {
+    constexpr int H = Raw<T>::kWords / 2;
+    if constexpr (H == 4)
+        *reinterpret_cast<uint4 *>(p) = upper ? make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]) : make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else
+        *reinterpret_cast<uint2 *>(p) = upper ? make_uint2(r.w[2], r.w[3]) : make_uint2(r.w[0], r.w[1]);
+}
+template <typename T>
+__device__ __forceinline__ void store_two(T *p, const Raw<T> &r, int i) {
+    const bool u = i & 4, m = i & 2;
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t a = m ? (u ? r.w[6] : r.w[2]) : (u ? r.w[4] : r.w[0]), b = m ? (u ? r.w[7] : r.w[3]) : (u ? r.w[5] : r.w[1]);
+        *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+    } else {
+        *reinterpret_cast<uint32_t *>(p) = m ? (u ? r.w[3] : r.w[1]) : (u ? r.w[2] : r.w[0]);
+    }
+}
+// Elements [lo, hi) of the unit on the boundary p: of a part that begins or ends with the unit at most
+// three pieces.
+template <typename T>
+__device__ __forceinline__ void store_range(T *p, const Raw<T> &r, int lo, int hi) {
+    if (lo == 0) {
+        if (hi & 4) store_four(p, r, false);
+        if (hi & 2) store_two(p + (hi & 4), r, hi & 4);
+        if (hi & 1) store_element(p, r, hi - 1);
+    } else if (hi == kUnit) {
+        if (lo & 1) store_element(p, r, lo);
+        const int two = (lo + 1) & 6;                 // the even element from lo on
+        if ((two & 2) != 0) store_two(p + two, r, two);
+        if (lo <= 4) store_four(p + 4, r, true);
+    } else {
+        for (int i = lo; i < hi; ++i) store_element(p, r, i);
+    }
+}
+
 // Stores the first `count` elements (0 .. 8) of the unit to p.  Every lane of the warp
 // calls it, lanes without a unit with count 0.  prev, next: the lane before holds
 // the row's unit before this one, the lane after the one after (with count > 0).
@@ -162,8 +203,8 @@ __device__ __forceinline__ void store_unit(T *p, const Raw<T> &r, int count, boo
     if (ALIGNED) {
         if (count == kUnit)
             store_words(p, r.w);
-        else
-            for (int i = 0; i < count; ++i) store_element(p, r, i);
+        else if (count > 0)
+            store_range(p, r, 0, count);
         return;
     }
     uint32_t before[4];
@@ -217,6 +258,51 @@ __device__ __forceinline__ void store_unit(T *p, const Raw<T> &r, int count, boo
     // next unit, and all of a short unit's
     const int last = next ? kUnit - o / kSize : count;
     for (int i = first; i < last; ++i) store_element(p, r, i);
+}
+
+// The unit on the boundary p, of which elements [lo, hi) are the row's; the others read as zeros.
+template <typename T>
+__device__ __forceinline__ Raw<T> load_block(const T *p, int lo, int hi) {
+    Raw<T> r;
+    if (lo >= hi) {
+        r.clear();
+        return r;
+    }
+    load_words(r.w, p);
+    if (hi - lo < kUnit) {
+#pragma unroll
+        for (int i = 0; i < Raw<T>::kWords; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                if (i < lo || i >= hi) r.w[i] = 0u;
+            } else {
+                if (2 * i < lo || 2 * i >= hi) r.w[i] &= 0xffff0000u;
+                if (2 * i + 1 < lo || 2 * i + 1 >= hi) r.w[i] &= 0xffffu;
+            }
+        }
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_block(T *p, const Raw<T> &r, int lo, int hi) {
+    if (hi - lo == kUnit)
+        store_words(p, r.w);
+    else if (lo < hi)
+        store_range(p, r, lo, hi);
+}
+
+// How far into its block of a unit's bytes p lies, in elements.
+template <typename T>
+__host__ __device__ inline int head_of(const void *p) {
+    return int(reinterpret_cast<uintptr_t>(p) & (kUnit * sizeof(T) - 1)) / int(sizeof(T));
+}
+// Whether the rows of both start alike within blocks, and the rows after which starts repeat.
+template <typename T>
+inline bool start_alike(const void *a, int64_t as, const void *b, int64_t bs) {
+    return head_of<T>(a) == head_of<T>(b) && (as - bs) % kUnit == 0;
+}
+inline int period_of(int64_t stride) {
+    const int r = int(stride % kUnit);
+    return r == 0 ? 1 : kUnit / (r & -r);
 }
 
 // Where rows of T allow units of one load or store.

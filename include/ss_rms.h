@@ -18,8 +18,10 @@
  *
  * Statistics and sums are float32; a result is rounded once, when it is stored,
  * and an output in 8 bits comes from the float32 y.  Squares past float32's range make r
- * zero.  The weights' sums run along splits that depend on the sizes, on how the rows are
- * aligned and on the device: with those the same, the same inputs give the same bits.
+ * zero.  A row's sum runs in an order that depends on how the rows are aligned and, where they do not
+ * start on 32-byte (16-bit types: 16-byte) boundaries, on whether outputs in 8 bits are wanted; the weights' sums along
+ * splits that depend on the sizes, the alignment and the device: with those the same, the same
+ * inputs give the same bits.
  *
  * Conventions are those of ss.h; rows and strides those of ss_embed.h.
  */

@@ -111,13 +111,17 @@ def fwd_case(ss, n, D, t, p, pad, off, residual=True, affine=True, fmts=("e4m3",
         assert np.array_equal(got, O.held(f64(y), fmts[0])[0])
     lim = np.abs(want) + ey
     assert_close(got, want, half_step(lim, scales_of(lim, fmts[0]), fmts[0]) + ey, "y in 8 bits")
-    # each output by itself gives the same bits, and in place
+    # the 8-bit outputs by themselves give the same bits; y without them may sum a row that does not
+    # start on a boundary in another order, and then both are as near as they have to be; in place the same bits
     y0, o0 = y.clone(), out.rows.q.float().clone()
     only = Guarded(ss, n, D, fmts[0])
     ss.ss_rms_norm_fwd(x, res, g, eps, sm if residual else None, out=only.rows)
     assert torch.equal(only.rows.q.float(), o0) and torch.equal(only.rows.scales, out.rows.scales)
     ss.ss_rms_norm_fwd(x, res, g, eps, sm if residual else None, y)
-    assert torch.equal(y, y0)
+    assert_close(y, want, ey + uT(t) * np.abs(want) + TINY[t], "y alone")
+    if D * y.element_size() % 32 == 0 and pad % 8 == 0 and off % 8 == 0:
+        assert torch.equal(y, y0)
+    y0 = y.clone()
     if residual:
         s0 = sm.clone()
         x2, r2 = rows(x0, t, pad, off)[0], rows(res, t, pad, off)[0]
