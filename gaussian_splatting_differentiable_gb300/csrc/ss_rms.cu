@@ -380,68 +380,144 @@ __global__ void __launch_bounds__(kThreads) k_norm8_bwd_rows_wide(BwdArgs a) {
     }
 }
 
-// A row's dy and h (HELD: kept in 8 bits) from registers, as they were loaded: widened once
-// for the sums and once more for the result, they take half the registers.  The next
-// row's loads are in flight meanwhile.  The weights' sums stay in registers over all of a
-// CTA's rows and leave one partial sum a CTA in a.part (none where it is NULL), or, where one CTA
-// has all rows, the gradients themselves.
-template <typename T, int NV, bool MULTI, Lie LIE, bool CENTRED, bool HELD>
+__device__ __forceinline__ void copy16(uint32_t smem, const void *p) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t smem, const void *p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// What a stage of the backward's ring has of each thread, tensor after tensor, [units][16 bytes][threads]:
+// dy, dsum (not CENTRED), and h or what is held of it (two units' bytes where they are shifted).
+template <typename T, int NV, Lie LIE, bool CENTRED, bool HELD>
+struct Ring {
+    static constexpr int kVecs = kUnit * int(sizeof(T)) / 16;       // of a unit
+    static constexpr int kRows = NV * kVecs * (CENTRED ? 1 : 2);
+    static constexpr int kHeld = HELD ? (LIE == kShifted ? 2 * NV : NV) * 8 : NV * kVecs * 16;   // bytes a thread
+    static constexpr int kBytes = kRows * 16 + kHeld;               // a thread and stage
+    static constexpr int kStages = kBytes > 96 ? 2 : 3;
+};
+
+// A row's dy and h (FMT >= 0: kept in 8 bits) through a ring in shared memory, asynchronously, kStages
+// - 1 rows ahead: every thread copies into slots of its own and reads only those, so the
+// ring needs no barrier and the copies in flight no registers.  The weights' sums stay in
+// registers over all of a CTA's rows and leave one partial sum a CTA in a.part (none where it is
+// NULL), or, where one CTA has all rows, the gradients themselves.
+template <typename T, int NV, bool MULTI, Lie LIE, bool CENTRED, int FMT>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd(BwdArgs a, Place pl, bool alone) {
     constexpr int kSums = CENTRED ? 2 : 1;
-    extern __shared__ float4 s_gamma[];      // [2 NV][threads]; at the end the sums
+    constexpr bool HELD = FMT >= 0;
+    using R = Ring<T, NV, LIE, CENTRED, HELD>;
+    constexpr int kStages = R::kStages;
+    extern __shared__ uint4 s_ring[];        // the ring, then gamma [2 NV][threads]; at the end the sums
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][kSums][kRowWarps];
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
     const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
     const int64_t step = int64_t(gridDim.x) * pl.groups, row0 = int64_t(blockIdx.x) * pl.groups + group;
     const Units c =
         units_at<MULTI>(lane, pl, a.D, LIE == kShifted ? head_of<T>(static_cast<const T *>(a.dy) + row0 * a.dys) : 0);
-    using HeldUnit = typename std::conditional<LIE == kShifted, HeldAcross, Held>::type;
-    struct Row {
-        Raw<T> dy[NV], dsum[NV], x[HELD ? 1 : NV];
-        HeldUnit q[HELD ? NV : 1];
-        float mu, r;
+    const int apart = blockDim.x;
+    const int stage_vecs = R::kBytes / 8 * apart / 2;        // 16-byte vectors of a stage
+    uint4 *slot = s_ring + threadIdx.x;
+    int lo[NV], hi[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) lo[k] = c.lo(k), hi[k] = c.hi(k);
+    // the rows to fetch next
+    const T *pd = static_cast<const T *>(a.dy) + row0 * a.dys + c.column(0),
+            *ps = static_cast<const T *>(a.dsum) + row0 * a.dss + c.column(0),
+            *px = static_cast<const T *>(a.h) + row0 * a.hs + c.column(0);
+    const uint8_t *pq = a.kept.q + row0 * a.kept.stride;
+    const int held_units = units_of(a.D);
+    // unit k of a tensor into its slot
+    auto fetch_unit = [&](uint4 *to, const T *p, int k) {
+        if (LIE == kAnyhow) {
+            const Raw<T> r = load_unit<T, false>(p + k * c.lanes * kUnit, hi[k]);
+#pragma unroll
+            for (int v = 0; v < R::kVecs; ++v)
+                to[v * apart] = make_uint4(r.w[4 * v], r.w[4 * v + 1], r.w[4 * v + 2], r.w[4 * v + 3]);
+        } else if (hi[k] > lo[k]) {
+#pragma unroll
+            for (int v = 0; v < R::kVecs; ++v)
+                copy16(uint32_t(__cvta_generic_to_shared(to + v * apart)),
+                       reinterpret_cast<const uint4 *>(p + k * c.lanes * kUnit) + v);
+        }
     };
-    auto load = [&](Row &w, int64_t row) {
-        const bool here = row < a.n;
-        const T *pd = static_cast<const T *>(a.dy) + row * a.dys, *ps = static_cast<const T *>(a.dsum) + row * a.dss,
-                *px = static_cast<const T *>(a.h) + row * a.hs;
+    // Row `row` of all tensors into a stage; a row past the last as zeros.
+    auto fetch = [&](int stage, int64_t row) {
+        uint4 *to = slot + stage * stage_vecs;
+        uint2 *held = reinterpret_cast<uint2 *>(s_ring + stage * stage_vecs + R::kRows * apart) + threadIdx.x;
+        if (row < a.n) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                fetch_unit(to + k * R::kVecs * apart, pd, k);
+                if (!CENTRED && a.dsum) fetch_unit(to + (NV + k) * R::kVecs * apart, ps, k);
+                if constexpr (!HELD) {
+                    fetch_unit(to + (R::kRows + k * R::kVecs) * apart, px, k);
+                } else if constexpr (LIE == kShifted) {
+                    const int j = c.column(k), u = j >> 3;
+                    if (hi[k] > 0 && u >= 0)
+                        copy8(uint32_t(__cvta_generic_to_shared(held + 2 * k * apart)), pq + u * kUnit);
+                    if (hi[k] > 0 && (j & 7) && u + 1 < held_units)
+                        copy8(uint32_t(__cvta_generic_to_shared(held + (2 * k + 1) * apart)), pq + (u + 1) * kUnit);
+                } else {
+                    if (hi[k] > 0) copy8(uint32_t(__cvta_generic_to_shared(held + k * apart)), pq + c.at(k) * kUnit);
+                }
+            }
+        } else {
+            for (int v = 0; v < R::kRows + (HELD ? 0 : NV * R::kVecs); ++v) to[v * apart] = make_uint4(0u, 0u, 0u, 0u);
+            if (HELD)
+                for (int v = 0; v < R::kHeld / 8; ++v) held[v * apart] = make_uint2(0u, 0u);
+        }
+        copies_commit();
+        pd += step * a.dys, ps += step * a.dss, px += step * a.hs, pq += step * a.kept.stride;
+    };
+    // slots that no copy fills stay zeros (a copy is not ordered after a store before it)
+#pragma unroll
+    for (int q = 0; q < kStages; ++q) {
+        uint4 *to = slot + q * stage_vecs;
+        uint2 *held = reinterpret_cast<uint2 *>(s_ring + q * stage_vecs + R::kRows * apart) + threadIdx.x;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            w.dy[k] = load_of<T, LIE>(pd, c, k, here);
-            if (!CENTRED && a.dsum) w.dsum[k] = load_of<T, LIE>(ps, c, k, here);
-            if constexpr (!HELD)
-                w.x[k] = load_of<T, LIE>(px, c, k, here);
-            else if constexpr (LIE == kShifted)
-                w.q[k].load(a.kept, row, c.column(k), a.D, here && c.hi(k) > 0);
-            else
-                w.q[k].load(a.kept, row, c.at(k), here && c.hi(k) > 0);
-        }
-        w.mu = CENTRED && here ? a.mean[row] : 0.0f;
-        w.r = here ? a.rstd[row] : 0.0f;
-    };
-    // g = (h - mean) r of unit k; what is not the row's meets zeros of dy
-    auto normed = [&](F2 (&g)[4], const Row &w, int k) {
-        if constexpr (HELD && LIE == kShifted) {
-            if (a.fmt == SS_INT8)
-                w.q[k].template values<SS_INT8>(g, c.column(k));
-            else
-                w.q[k].template values<SS_E4M3>(g, c.column(k));
-        } else if constexpr (HELD) {
-            if (a.fmt == SS_INT8)
-                w.q[k].template values<SS_INT8>(g);
-            else
-                w.q[k].template values<SS_E4M3>(g);
-        } else {
-            floats_of(g, w.x[k]);
-        }
-        const F2 rr = both(w.r), neg = both(-w.mu);
+            if (LIE != kAnyhow && hi[k] <= lo[k])
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g[i] = mul2(CENTRED ? add2(g[i], neg) : g[i], rr);
+                for (int v = 0; v < R::kVecs; ++v) {
+                    to[(k * R::kVecs + v) * apart] = make_uint4(0u, 0u, 0u, 0u);
+                    if (!CENTRED) to[((NV + k) * R::kVecs + v) * apart] = make_uint4(0u, 0u, 0u, 0u);
+                    if (!HELD) to[(R::kRows + k * R::kVecs + v) * apart] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            if constexpr (HELD && LIE == kShifted) {
+                const int j = c.column(k), u = j >> 3;
+                if (hi[k] <= 0 || u < 0) held[2 * k * apart] = make_uint2(0u, 0u);
+                if (hi[k] <= 0 || !(j & 7) || u + 1 >= held_units) held[(2 * k + 1) * apart] = make_uint2(0u, 0u);
+            } else if constexpr (HELD) {
+                if (hi[k] <= 0) held[k * apart] = make_uint2(0u, 0u);
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kStages - 1; ++q) fetch(q, row0 + q * step);
+    // what a row needs beside them, a row ahead
+    float mu, r;
+    uint32_t e0[NV], e1[NV];
+    auto load = [&](int64_t row) {
+        const bool here = row < a.n;
+        mu = CENTRED && here ? a.mean[row] : 0.0f, r = here ? a.rstd[row] : 0.0f;
+        if (HELD) {
+            const uint8_t *s = a.kept.scales + row * a.kept.scale_stride;
+            const int most = (a.D - 1) / kGroup;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int j = c.column(k), g = j < 0 ? 0 : j / kGroup, h = (j + kUnit - 1) / kGroup;
+                e0[k] = here && hi[k] > 0 ? s[g] : 127u;
+                if (LIE == kShifted) e1[k] = here && hi[k] > 0 ? s[h < most ? h : most] : 127u;
+            }
+        }
     };
-    Row w, ahead;
-    load(ahead, row0);
-    float4 *plane = s_gamma + threadIdx.x;
-    const int apart = blockDim.x;
+    load(row0);
+    float4 *plane = reinterpret_cast<float4 *>(s_ring + kStages * stage_vecs) + threadIdx.x;
     {
         F2 g[NV][4];
         load_weights<NV>(g, a.gamma, a.pdt, c);
@@ -451,13 +527,6 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
             for (int i = 0; i < 2; ++i)
                 plane[(2 * k + i) * apart] = make_float4(g[k][2 * i].x, g[k][2 * i].y, g[k][2 * i + 1].x, g[k][2 * i + 1].y);
     }
-    auto weights = [&](F2 (&g)[4], int k) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 q = plane[(2 * k + i) * apart];
-            g[2 * i] = make_float2(q.x, q.y), g[2 * i + 1] = make_float2(q.z, q.w);
-        }
-    };
     if (MULTI) {
         for (int e = threadIdx.x; e < kMaxGroups * 2 * kSums * kRowWarps; e += blockDim.x) (&s_red[0][0][0][0])[e] = 0.0f;
         __syncthreads();
@@ -468,63 +537,95 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = both(0.0f);
-    int flip = 0;
+    int flip = 0, stage = 0;
     const int64_t lead = MULTI ? row0 : row0 - ((threadIdx.x & 31) >> pl.shift);
-    for (int64_t base = lead; base < a.n; base += step) {
+    T *pdx = static_cast<T *>(a.dx) + row0 * a.dxs;
+    // unit k as a stage has it, of which [lo, hi) are the row's; others as zeros
+    auto unit_in = [&](const uint4 *at, int k) {
+        Raw<T> u;
+#pragma unroll
+        for (int v = 0; v < R::kVecs; ++v) {
+            const uint4 q = at[v * apart];
+            u.w[4 * v] = q.x, u.w[4 * v + 1] = q.y, u.w[4 * v + 2] = q.z, u.w[4 * v + 3] = q.w;
+        }
+        if (LIE != kAnyhow && hi[k] - lo[k] < kUnit) cut(u, lo[k], hi[k]);
+        return u;
+    };
+    for (int64_t base = lead; base < a.n; base += step, pdx += step * a.dxs) {
         const int64_t row = base + (row0 - lead);
-        w = ahead;
-        load(ahead, row + step);
-        F2 s0 = both(0.0f), s1 = both(0.0f);
+        copies_wait<kStages - 2>();
+        const uint4 *from = slot + stage * stage_vecs;
+        const uint2 *held = reinterpret_cast<const uint2 *>(s_ring + stage * stage_vecs + R::kRows * apart) + threadIdx.x;
+        F2 d[NV][4], g[NV][4], s0 = both(0.0f), s1 = both(0.0f);
+        const F2 rr = both(r), neg = both(-mu);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            F2 d[4], g[4], wt[4];
-            floats_of(d, w.dy[k]);
-            normed(g, w, k);
-            weights(wt, k);
+            F2 wt[4];
+            floats_of(d[k], unit_in(from + k * R::kVecs * apart, k));
+            // g = (h - mean) r; what is not the row's meets zeros of dy
+            if constexpr (!HELD) {
+                floats_of(g[k], unit_in(from + (R::kRows + k * R::kVecs) * apart, k));
+            } else if constexpr (LIE == kShifted) {
+                const HeldAcross h{held[2 * k * apart], held[(2 * k + 1) * apart], e0[k], e1[k]};
+                h.template values<FMT>(g[k], c.column(k));
+            } else {
+                const Held h{held[k * apart], e0[k]};
+                h.template values<FMT>(g[k]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 q = plane[(2 * k + i) * apart];
+                wt[2 * i] = make_float2(q.x, q.y), wt[2 * i + 1] = make_float2(q.z, q.w);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                dg[k][i] = fma2(d[i], g[i], dg[k][i]);
-                if (CENTRED) db[k][i] = add2(db[k][i], d[i]);
-                d[i] = mul2(d[i], wt[i]);
-                if (CENTRED) s1 = add2(s1, d[i]);
-                s0 = fma2(d[i], g[i], s0);
+                g[k][i] = mul2(CENTRED ? add2(g[k][i], neg) : g[k][i], rr);
+                dg[k][i] = fma2(d[k][i], g[k][i], dg[k][i]);
+                if (CENTRED) db[k][i] = add2(db[k][i], d[k][i]);
+                d[k][i] = mul2(d[k][i], wt[i]);
+                if (CENTRED) s1 = add2(s1, d[k][i]);
+                s0 = fma2(d[k][i], g[k][i], s0);
             }
         }
+        Raw<T> up[NV];
+        const bool sums = !CENTRED && a.dsum;
+        if (sums)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) up[k] = unit_in(from + (NV + k) * R::kVecs * apart, k);
         float sum[kSums];
         sum[0] = sum_of(s0);
         if (CENTRED) sum[kSums - 1] = sum_of(s1);
+        load(row + step);
+        fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);   // the slots read one row ago
+        stage = stage == kStages - 1 ? 0 : stage + 1;
         row_sum<kSums, MULTI>(sum, pl, group, lane, s_red[MULTI ? group : 0], flip);
-        const F2 mag = both(-sum[0] * inv), ma = both(CENTRED ? -sum[kSums - 1] * inv : 0.0f), rr = both(w.r);
+        const F2 mag = both(-sum[0] * inv), ma = both(CENTRED ? -sum[kSums - 1] * inv : 0.0f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            F2 d[4], g[4], wt[4];
-            floats_of(d, w.dy[k]);
-            normed(g, w, k);
-            weights(wt, k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                d[i] = mul2(d[i], wt[i]);
-                if (CENTRED) d[i] = add2(d[i], ma);
-                d[i] = mul2(fma2(g[i], mag, d[i]), rr);
+                if (CENTRED) d[k][i] = add2(d[k][i], ma);
+                d[k][i] = mul2(fma2(g[k][i], mag, d[k][i]), rr);
             }
-            if (!CENTRED && a.dsum) {
+            if (sums) {
                 F2 u[4];
-                floats_of(u, w.dsum[k]);
+                floats_of(u, up[k]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] = add2(d[i], u[i]);
+                for (int i = 0; i < 4; ++i) d[k][i] = add2(d[k][i], u[i]);
             }
-            store_of<T, LIE>(static_cast<T *>(a.dx) + row * a.dxs, raw_of<T>(d), c, k, row < a.n);
+            store_of<T, LIE>(pdx, raw_of<T>(d[k]), c, k, row < a.n);
         }
     }
+    copies_wait<0>();
     start_dependents();
     if (!a.part) return;
     // The CTA's sums, in fixed order: the rows of a warp are joined by shuffles where their columns
-    // are the same (!MULTI, not kShifted), then the warps or groups in turn, in gamma's place.
-    __syncthreads();                       // gamma has been read
+    // are the same (!MULTI, not kShifted), then the warps or groups in turn, in the ring's place.
+    __syncthreads();                       // the last rows' slots and gamma have been read
     constexpr bool kFold = !MULTI && LIE != kShifted;
     const int cols = kSums * a.D;
     const int slots = kFold ? kThreads / 32 : pl.groups;
-    float *s_sum = reinterpret_cast<float *>(s_gamma);
+    float *s_sum = reinterpret_cast<float *>(s_ring);
     float *part = a.part + size_t(blockIdx.x) * cols;
     const bool direct = slots == 1 && !alone;
     float *mine = direct ? part : s_sum + size_t(kFold ? threadIdx.x >> 5 : group) * cols;
@@ -581,7 +682,7 @@ __global__ void __launch_bounds__(1024) k_norm8_bwd_final(const float *part, int
 }
 
 // Partial sums of the weights' gradients that the workspace has room for.
-constexpr int kMaxSmem = 200 * 1024;
+constexpr int kMaxSmem = 225 * 1024;   // 227 KB less 2 KB of static buffers
 constexpr int kMaxParts = 1024;
 int64_t weight_parts(int64_t n) { return n + kUnit < kMaxParts ? n + kUnit : kMaxParts; }   // a grid is rounded up to a period
 int wide_grid(int64_t n, int sms) { return int(n < int64_t(sms) * 8 ? n : int64_t(sms) * 8); }
@@ -667,8 +768,9 @@ void launch_fwd(const FwdArgs &a, int sms, cudaStream_t s) {
     });
 }
 
-template <typename T, bool CENTRED, bool HELD>
+template <typename T, bool CENTRED, int FMT>
 ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
+    constexpr bool HELD = FMT >= 0;
     const int cols = CENTRED ? 2 * a.D : a.D;
     const dim3 final_grid((cols + 31) / 32);
     if (a.n == 0 || !in_registers(a.D)) {
@@ -698,9 +800,10 @@ ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
     ss_status st = SS_OK;
     with_place(nv, multi, [&](auto NV, auto MULTI) {
         with_lie(lie, [&](auto LIE) {
-            auto kernel = k_norm8_bwd<T, NV(), MULTI(), LIE(), CENTRED, HELD>;
+            auto kernel = k_norm8_bwd<T, NV(), MULTI(), LIE(), CENTRED, FMT>;
+            using R = Ring<T, NV(), LIE(), CENTRED, HELD>;
             const int slots = MULTI() || LIE() == kShifted ? pl.groups : kThreads / 32;
-            size_t smem = size_t(2 * NV()) * threads * sizeof(float4);
+            size_t smem = (size_t(R::kStages) * R::kBytes + 2 * NV() * sizeof(float4)) * threads;
             const size_t sums = a.dgamma && (slots > 1 || alone) ? size_t(slots) * cols * sizeof(float) : 0;
             if (smem < sums) smem = sums;
             static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
@@ -725,11 +828,11 @@ ss_status backward(const char *who, const BwdArgs &a, int dtype, int sms, cudaSt
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
         if (a.centred)
-            st = launch_bwd<T, true, true>(a, sms, s);
+            with_format(a.fmt, [&](auto F) { st = launch_bwd<T, true, decltype(F)::value>(a, sms, s); });
         else if (a.fmt >= 0)
-            st = launch_bwd<T, false, true>(a, sms, s);
+            with_format(a.fmt, [&](auto F) { st = launch_bwd<T, false, decltype(F)::value>(a, sms, s); });
         else
-            st = launch_bwd<T, false, false>(a, sms, s);
+            st = launch_bwd<T, false, -1>(a, sms, s);
     });
     return st != SS_OK ? st : check_launch(who);
 }

@@ -260,6 +260,19 @@ __device__ __forceinline__ void store_unit(T *p, const Raw<T> &r, int count, boo
     for (int i = first; i < last; ++i) store_element(p, r, i);
 }
 
+// Clears all but elements [lo, hi).
+template <typename T>
+__device__ __forceinline__ void cut(Raw<T> &r, int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < Raw<T>::kWords; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            if (i < lo || i >= hi) r.w[i] = 0u;
+        } else {
+            if (2 * i < lo || 2 * i >= hi) r.w[i] &= 0xffff0000u;
+            if (2 * i + 1 < lo || 2 * i + 1 >= hi) r.w[i] &= 0xffffu;
+        }
+    }
+}
 // The unit on the boundary p, of which elements [lo, hi) are the row's; the others read as zeros.
 template <typename T>
 __device__ __forceinline__ Raw<T> load_block(const T *p, int lo, int hi) {
@@ -269,17 +282,7 @@ __device__ __forceinline__ Raw<T> load_block(const T *p, int lo, int hi) {
         return r;
     }
     load_words(r.w, p);
-    if (hi - lo < kUnit) {
-#pragma unroll
-        for (int i = 0; i < Raw<T>::kWords; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                if (i < lo || i >= hi) r.w[i] = 0u;
-            } else {
-                if (2 * i < lo || 2 * i >= hi) r.w[i] &= 0xffff0000u;
-                if (2 * i + 1 < lo || 2 * i + 1 >= hi) r.w[i] &= 0xffffu;
-            }
-        }
-    }
+    if (hi - lo < kUnit) cut(r, lo, hi);
     return r;
 }
 template <typename T>
