@@ -397,13 +397,16 @@ struct Ring {
     static constexpr int kVecs = kUnit * int(sizeof(T)) / 16;       // of a unit
     static constexpr int kRows = NV * kVecs * (CENTRED ? 1 : 2);
     static constexpr int kHeld = HELD ? (LIE == kShifted ? 2 * NV : NV) * 8 : NV * kVecs * 16;   // bytes a thread
-    static constexpr int kBytes = kRows * 16 + kHeld;               // a thread and stage
+    static constexpr bool kUsed = sizeof(T) == 2;                   // (float32: see below)
+    static constexpr int kBytes = kUsed ? kRows * 16 + kHeld : 0;   // a thread and stage
     static constexpr int kStages = kBytes > 96 ? 2 : 3;
 };
 
 // A row's dy and h (FMT >= 0: kept in 8 bits) through a ring in shared memory, asynchronously, kStages
 // - 1 rows ahead: every thread copies into slots of its own and reads only those, so the
-// ring needs no barrier and the copies in flight no registers.  The weights' sums stay in
+// ring needs no barrier and the copies in flight no registers.  A unit of float32 would be two
+// such copies, each of half of every 32-byte sector, which L2 reads twice (2M x 48: 283 us); these come by
+// one load of 32 bytes into registers, a row ahead (227).  The weights' sums stay in
 // registers over all of a CTA's rows and leave one partial sum a CTA in a.part (none where it is
 // NULL), or, where one CTA has all rows, the gradients themselves.
 template <typename T, int NV, bool MULTI, Lie LIE, bool CENTRED, int FMT>
@@ -445,8 +448,31 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
                        reinterpret_cast<const uint4 *>(p + k * c.lanes * kUnit) + v);
         }
     };
-    // Row `row` of all tensors into a stage; a row past the last as zeros.
+    using HeldUnit = typename std::conditional<LIE == kShifted, HeldAcross, Held>::type;
+    struct Ahead {
+        Raw<T> dy[NV], dsum[NV], x[HELD ? 1 : NV];
+        HeldUnit q[HELD ? NV : 1];
+    };
+    Ahead ahead;
+    // Row `row` of all tensors into a stage (or registers); a row past the last as zeros.
     auto fetch = [&](int stage, int64_t row) {
+        if constexpr (!R::kUsed) {
+            const bool here = row < a.n;
+            const int64_t skip = c.column(0);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                ahead.dy[k] = load_of<T, LIE>(pd - skip, c, k, here);
+                if (!CENTRED && a.dsum) ahead.dsum[k] = load_of<T, LIE>(ps - skip, c, k, here);
+                if constexpr (!HELD)
+                    ahead.x[k] = load_of<T, LIE>(px - skip, c, k, here);
+                else if constexpr (LIE == kShifted)
+                    ahead.q[k].load(a.kept, row, c.column(k), a.D, here && hi[k] > 0);
+                else
+                    ahead.q[k].load(a.kept, row, c.at(k), here && hi[k] > 0);
+            }
+            pd += step * a.dys, ps += step * a.dss, px += step * a.hs;
+            return;
+        }
         uint4 *to = slot + stage * stage_vecs;
         uint2 *held = reinterpret_cast<uint2 *>(s_ring + stage * stage_vecs + R::kRows * apart) + threadIdx.x;
         if (row < a.n) {
@@ -476,7 +502,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
     };
     // slots that no copy fills stay zeros (a copy is not ordered after a store before it)
 #pragma unroll
-    for (int q = 0; q < kStages; ++q) {
+    for (int q = 0; q < (R::kUsed ? kStages : 0); ++q) {
         uint4 *to = slot + q * stage_vecs;
         uint2 *held = reinterpret_cast<uint2 *>(s_ring + q * stage_vecs + R::kRows * apart) + threadIdx.x;
 #pragma unroll
@@ -498,14 +524,14 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
         }
     }
 #pragma unroll
-    for (int q = 0; q < kStages - 1; ++q) fetch(q, row0 + q * step);
+    for (int q = 0; q < (R::kUsed ? kStages - 1 : 1); ++q) fetch(q, row0 + q * step);
     // what a row needs beside them, a row ahead
     float mu, r;
     uint32_t e0[NV], e1[NV];
     auto load = [&](int64_t row) {
         const bool here = row < a.n;
         mu = CENTRED && here ? a.mean[row] : 0.0f, r = here ? a.rstd[row] : 0.0f;
-        if (HELD) {
+        if (HELD && R::kUsed) {
             const uint8_t *s = a.kept.scales + row * a.kept.scale_stride;
             const int most = (a.D - 1) / kGroup;
 #pragma unroll
@@ -553,7 +579,13 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
     };
     for (int64_t base = lead; base < a.n; base += step, pdx += step * a.dxs) {
         const int64_t row = base + (row0 - lead);
-        copies_wait<kStages - 2>();
+        Ahead now;
+        if constexpr (R::kUsed) {
+            copies_wait<kStages - 2>();
+        } else {
+            now = ahead;
+            fetch(0, row + step);
+        }
         const uint4 *from = slot + stage * stage_vecs;
         const uint2 *held = reinterpret_cast<const uint2 *>(s_ring + stage * stage_vecs + R::kRows * apart) + threadIdx.x;
         F2 d[NV][4], g[NV][4], s0 = both(0.0f), s1 = both(0.0f);
@@ -561,10 +593,14 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             F2 wt[4];
-            floats_of(d[k], unit_in(from + k * R::kVecs * apart, k));
+            floats_of(d[k], R::kUsed ? unit_in(from + k * R::kVecs * apart, k) : now.dy[k]);
             // g = (h - mean) r; what is not the row's meets zeros of dy
             if constexpr (!HELD) {
-                floats_of(g[k], unit_in(from + (R::kRows + k * R::kVecs) * apart, k));
+                floats_of(g[k], R::kUsed ? unit_in(from + (R::kRows + k * R::kVecs) * apart, k) : now.x[k]);
+            } else if constexpr (!R::kUsed && LIE == kShifted) {
+                now.q[k].template values<FMT>(g[k], c.column(k));
+            } else if constexpr (!R::kUsed) {
+                now.q[k].template values<FMT>(g[k]);
             } else if constexpr (LIE == kShifted) {
                 const HeldAcross h{held[2 * k * apart], held[(2 * k + 1) * apart], e0[k], e1[k]};
                 h.template values<FMT>(g[k], c.column(k));
@@ -591,12 +627,12 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd
         const bool sums = !CENTRED && a.dsum;
         if (sums)
 #pragma unroll
-            for (int k = 0; k < NV; ++k) up[k] = unit_in(from + (NV + k) * R::kVecs * apart, k);
+            for (int k = 0; k < NV; ++k) up[k] = R::kUsed ? unit_in(from + (NV + k) * R::kVecs * apart, k) : now.dsum[k];
         float sum[kSums];
         sum[0] = sum_of(s0);
         if (CENTRED) sum[kSums - 1] = sum_of(s1);
         load(row + step);
-        fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);   // the slots read one row ago
+        if (R::kUsed) fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);   // the slots read one row ago
         stage = stage == kStages - 1 ? 0 : stage + 1;
         row_sum<kSums, MULTI>(sum, pl, group, lane, s_red[MULTI ? group : 0], flip);
         const F2 mag = both(-sum[0] * inv), ma = both(CENTRED ? -sum[kSums - 1] * inv : 0.0f);
