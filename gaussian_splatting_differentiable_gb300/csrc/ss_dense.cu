@@ -20,21 +20,23 @@ namespace {
 
 // A weight of one tile, up to 128 x 128: rows come in faster than they are worked on, so all of
 // dy and x pass once, and are converted on the way.  A CTA has a range of rows, stages of
-// which go through a ring in shared memory.  A bfloat16 dy needs no change: where it lies on 16-byte
-// boundaries (FAST), a thread has the copy engine bring it.  All else passes through the
-// registers of the loader warps before it is converted and stored.  One thread of another
+// which go through a ring in shared memory.  Where dy and x lie on 16-byte boundaries (FAST), a thread
+// has the copy engine bring them: a bfloat16 dy, which needs no change, to its place, all
+// else to a ring of its own, out of which the loader warps convert it (loads into their
+// registers, which are what other rows take, leave them waiting: 2M x 48 x 48 float32
+// 145 us).  One thread of another
 // warp issues the products; at the end the loaders read the sums out of the tensor memory.  A range is one
 // chain.
 //
 // TI = 64 (N up to 64): two parts of dy side by side are the 128 rows of one product, so
 // a float32 takes two products and not three; the parts' sums are joined through shared memory.
-template <typename T, int TI, int TJ>
+template <typename T, int TI, int TJ, int ROWS>
 struct Config {
     static constexpr int kParts = parts_of<T>();
     static constexpr bool kStacked = TI == 64;
     static constexpr int kLoaders = 256;
     static constexpr int kThreads = kLoaders + 64;                  // and the warps of the products and of the copies
-    static constexpr int kRows = 64;                                // of a stage
+    static constexpr int kRows = ROWS;                              // of a stage
     static constexpr int kBlock = kRows * 128;                      // bytes of 64 columns of a stage
     static constexpr int kABlocks = kStacked ? (kParts + 1) / 2 * 2 : 2 * kParts;
     static constexpr int kPart = TI / 64 * kBlock;                  // bytes from one part to the next
@@ -43,9 +45,8 @@ struct Config {
     static constexpr int kProducts = kABlocks / 2;                  // of 128 rows each, a step
     static constexpr int kSums = kStacked ? kProducts : (kParts > 1 ? 2 : 1);
     static constexpr int kStages = 2;
-    static constexpr int kSmem = kStages * kStageBytes + 1024;      // and up to the first 1 KB boundary
-    static constexpr int kAhead = kParts == 2 ? 2 : 1;
-    static constexpr int kTurnsA = kRows * (TI / kUnit) / kLoaders;
+    static constexpr int kRawStages = 2;
+    static constexpr int kTurnsA = kRows * (TI / kUnit) / kLoaders < 1 ? 1 : kRows * (TI / kUnit) / kLoaders;
     static constexpr int kTurnsB = kRows * (TJ / kWide) / kLoaders < 1 ? 1 : kRows * (TJ / kWide) / kLoaders;
     static constexpr int kColumns = kSums * TJ <= 64 ? 64 : (kSums * TJ <= 128 ? 128 : 256);   // of tensor memory
     static constexpr int kMinCtas = 2;
@@ -102,16 +103,24 @@ __device__ __forceinline__ void store_parts(uint32_t at, const Raw<T> &r) {
     }
 }
 
-template <typename T, int TI, int TJ, int FMT, bool FAST>
-__global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>::kMinCtas)
-    k_dense(DenseArgs a, int64_t rows, const __grid_constant__ CUtensorMap map) {
-    using C = Config<T, TI, TJ>;
+// A stage of the ring of what is to be converted: rows of dy (in several parts), then of x.
+struct RawStage {
+    int dy_pitch, x_pitch, bytes;
+};
+
+template <typename T, int TI, int TJ, int ROWS, int FMT, bool FAST>
+__global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, TI, TJ, ROWS>::kMinCtas)
+    k_dense(DenseArgs a, int64_t rows, RawStage raw, const __grid_constant__ CUtensorMap dy_map,
+            const __grid_constant__ CUtensorMap x_map) {
+    using C = Config<T, TI, TJ, ROWS>;
     constexpr bool kCopies = FAST && C::kParts == 1;
     extern __shared__ uint8_t s_raw[];
     __shared__ uint64_t s_full[C::kStages], s_copied[C::kStages], s_empty[C::kStages], s_done;
+    __shared__ uint64_t s_raw_full[C::kRawStages], s_raw_empty[C::kRawStages];
     __shared__ uint32_t s_tensor, s_failed;
     const uint32_t ring = (smem_of(s_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = s_raw + (ring - smem_of(s_raw));
+    const uint8_t *raw_ring = ring_ptr + C::kStages * C::kStageBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ni = a.N, nj = a.D;
     const int64_t first = int64_t(blockIdx.x) * rows;
@@ -126,6 +135,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
             barrier_init(&s_copied[k], 1);
             barrier_init(&s_empty[k], 1);
         }
+        for (int k = 0; k < C::kRawStages; ++k) barrier_init(&s_raw_full[k], 1), barrier_init(&s_raw_empty[k], C::kLoaders / 32);
         barrier_init(&s_done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -209,70 +219,93 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         }
     };
     if (warp < C::kLoaders / 32) {
-        Raw<T> ra[C::kAhead][C::kTurnsA];
-        Wide rb[C::kAhead][C::kTurnsB];
+        Raw<T> ra[C::kTurnsA];
+        Wide rb[C::kTurnsB];
         const int ca = ni - ta.piece * kUnit < kUnit ? ni - ta.piece * kUnit : kUnit;
         const bool all = nj - tb.piece * kWide > kUnit;
-        // the next stage to load: its pieces, and how many of its rows there are
+        // the next stage to load: its pieces (FAST: x's scales), and how many of its rows there are
         const T *pa = static_cast<const T *>(a.dy) + (first + ta.row) * a.dys + ta.piece * kUnit;
         const uint8_t *pq = a.x.q + (first + tb.row) * a.x.stride + tb.piece * kWide;
         const uint8_t *ps = a.x.scales + (first + tb.row) * a.x.scale_stride + tb.piece / (kGroup / kWide);
         int64_t left = last - first;
-        auto load = [&](Raw<T> (&va)[C::kTurnsA], Wide (&vb)[C::kTurnsB]) {
-            const int rows = left < C::kRows ? int(left) : C::kRows;
-            if (!kCopies)
+        auto load = [&] {
+            const int there = left < C::kRows ? int(left) : C::kRows;
+            if (!FAST)
 #pragma unroll
                 for (int k = 0; k < C::kTurnsA; ++k)
-                    if (ta.has(k, rows))
-                        va[k] = load_unit<T, FAST>(pa + k * ta.rows * a.dys, ca);
+                    if (ta.has(k, there))
+                        ra[k] = load_unit<T, false>(pa + k * ta.rows * a.dys, ca);
                     else
-                        va[k].clear();
+                        ra[k].clear();
 #pragma unroll
-            for (int k = 0; k < C::kTurnsB; ++k)
-                if (tb.has(k, rows))
-                    vb[k].template load<FAST>(pq + k * tb.rows * a.x.stride, ps + k * tb.rows * a.x.scale_stride, all);
+            for (int k = 0; k < C::kTurnsB; ++k) {
+                if (FAST)
+                    rb[k].e = tb.has(k, there) ? ps[k * tb.rows * a.x.scale_stride] : 127u;
+                else if (tb.has(k, there))
+                    rb[k].template load<false>(pq + k * tb.rows * a.x.stride, ps + k * tb.rows * a.x.scale_stride, all);
                 else
-                    vb[k] = Wide{{0u, 0u, 0u, 0u}, 127u};
+                    rb[k] = Wide{{0u, 0u, 0u, 0u}, 127u};
+            }
             pa += C::kRows * a.dys, pq += C::kRows * a.x.stride, ps += C::kRows * a.x.scale_stride;
             left -= C::kRows;
         };
-#pragma unroll
-        for (int q = 0; q < C::kAhead; ++q) load(ra[q], rb[q]);
+        load();
         auto add_bias = [&](const Raw<T> &r) {
             F2 f[4];
             floats_of(f, r);
 #pragma unroll
             for (int i = 0; i < 4; ++i) sums[i] = add2(sums[i], f[i]);
         };
-        int slot = 0;
-        uint32_t parity = 1;
+        int slot = 0, raw_slot = 0;
+        uint32_t parity = 1, raw_parity = 0;
         bool ok = true;
-        for (int base = 0; base < stages && ok; base += C::kAhead)
-#pragma unroll
-            for (int q = 0; q < C::kAhead; ++q) {
-                if (base + q >= stages) break;
-                if (!barrier_wait(&s_empty[slot], parity)) {
+        for (int stage = 0; stage < stages; ++stage) {
+            if (FAST) {
+                if (!barrier_wait(&s_raw_full[raw_slot], raw_parity)) {
                     ok = false;
                     break;
                 }
-                const uint32_t at = ring + slot * C::kStageBytes;
-                if (!kCopies)
+                const uint8_t *from = raw_ring + raw_slot * raw.bytes;
+                if (!kCopies) {
 #pragma unroll
-                    for (int k = 0; k < C::kTurnsA; ++k) {
-                        if (!ta.has(k, C::kRows)) continue;
-                        store_parts<T, C::kPart>(at + ta.place(k), ra[q][k]);
-                        if (bias) add_bias(ra[q][k]);
-                    }
+                    for (int k = 0; k < C::kTurnsA; ++k)
+                        if (ta.has(k, C::kRows)) {
+                            const uint8_t *at = from + (ta.row + k * ta.rows) * raw.dy_pitch + ta.piece * int(kUnit * sizeof(T));
+#pragma unroll
+                            for (int v = 0; v < Raw<T>::kWords / 4; ++v) {
+                                const uint4 u = reinterpret_cast<const uint4 *>(at)[v];
+                                ra[k].w[4 * v] = u.x, ra[k].w[4 * v + 1] = u.y, ra[k].w[4 * v + 2] = u.z, ra[k].w[4 * v + 3] = u.w;
+                            }
+                        }
+                    from += C::kRows * raw.dy_pitch;
+                }
 #pragma unroll
                 for (int k = 0; k < C::kTurnsB; ++k)
-                    if (tb.has(k, C::kRows)) {
-                        uint32_t w[8];
-                        convert<FMT>(w, rb[q][k]);
-                        const uint32_t to = at + C::kABytes + tb.place(k);
-                        store16(to, {w[0], w[1], w[2], w[3]});
-                        store16(to ^ 16u, {w[4], w[5], w[6], w[7]});
-                    }
-                if constexpr (kCopies) if (bias) {       // the copy engine's rows, before the slot may be filled again
+                    if (tb.has(k, C::kRows)) load_words(rb[k].w, from + (tb.row + k * tb.rows) * raw.x_pitch + tb.piece * kWide);
+            }
+            if (!barrier_wait(&s_empty[slot], parity)) {
+                ok = false;
+                break;
+            }
+            const uint32_t at = ring + slot * C::kStageBytes;
+            if (!kCopies)
+#pragma unroll
+                for (int k = 0; k < C::kTurnsA; ++k) {
+                    if (!ta.has(k, C::kRows)) continue;
+                    store_parts<T, C::kPart>(at + ta.place(k), ra[k]);
+                    if (bias) add_bias(ra[k]);
+                }
+#pragma unroll
+            for (int k = 0; k < C::kTurnsB; ++k)
+                if (tb.has(k, C::kRows)) {
+                    uint32_t w[8];
+                    convert<FMT>(w, rb[k]);
+                    const uint32_t to = at + C::kABytes + tb.place(k);
+                    store16(to, {w[0], w[1], w[2], w[3]});
+                    store16(to ^ 16u, {w[4], w[5], w[6], w[7]});
+                }
+            if constexpr (kCopies)
+                if (bias) {       // the copy engine's rows, before the slot may be filled again
                     if (!barrier_wait(&s_copied[slot], parity ^ 1)) {
                         ok = false;
                         break;
@@ -280,16 +313,20 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
 #pragma unroll
                     for (int k = 0; k < C::kTurnsA; ++k)
                         if (ta.has(k, C::kRows)) {
-                            load_words(ra[q][k].w, ring_ptr + slot * C::kStageBytes + ta.place(k));
-                            add_bias(ra[q][k]);
+                            load_words(ra[k].w, ring_ptr + slot * C::kStageBytes + ta.place(k));
+                            add_bias(ra[k]);
                         }
                 }
-                writes_to_async();
-                __syncwarp();
-                if (lane == 0) barrier_arrive(&s_full[slot]);
-                load(ra[q], rb[q]);
-                if (++slot == C::kStages) slot = 0, parity ^= 1;
+            writes_to_async();
+            __syncwarp();
+            if (lane == 0) {
+                barrier_arrive(&s_full[slot]);
+                if (FAST) barrier_arrive(&s_raw_empty[raw_slot]);
             }
+            load();
+            if (++slot == C::kStages) slot = 0, parity ^= 1;
+            if (++raw_slot == C::kRawStages) raw_slot = 0, raw_parity ^= 1;
+        }
         if (!ok || !barrier_wait(&s_done, 0)) s_failed = 1;
         tensor_fence_after();
         drain();
@@ -323,26 +360,43 @@ __global__ void __launch_bounds__(Config<T, TI, TJ>::kThreads, Config<T, TI, TJ>
         }
         __syncwarp();
     } else {
-        if (kCopies && lane == 0) {
+        if (FAST && lane == 0) {
             const int boxes = (ni + 63) / 64;
-            int slot = 0, stage = 0;
-            uint32_t parity = 1;
+            const uint32_t raw_at = ring + C::kStages * C::kStageBytes;
+            int slot = 0, raw_slot = 0, stage = 0, copied = 0;
+            uint32_t parity = 1, raw_parity = 1;
             for (; stage < stages; ++stage) {
-                if (!barrier_wait(&s_empty[slot], parity)) {
+                const int row = int(first + int64_t(stage) * C::kRows);
+                if (!barrier_wait(&s_raw_empty[raw_slot], raw_parity)) {
                     s_failed = 1;
                     break;
                 }
-                barrier_expect(&s_copied[slot], boxes * C::kBlock);
-                for (int k = 0; k < boxes; ++k)
-                    copy_box(ring + slot * C::kStageBytes + k * C::kBlock, &map, 64 * k,
-                             int(first + int64_t(stage) * C::kRows), &s_copied[slot]);
-                if (++slot == C::kStages) slot = 0, parity ^= 1;
+                uint32_t to = raw_at + raw_slot * raw.bytes;
+                barrier_expect(&s_raw_full[raw_slot], raw.bytes);
+                if (!kCopies) {
+                    copy_box(to, &dy_map, 0, row, &s_raw_full[raw_slot]);
+                    to += C::kRows * raw.dy_pitch;
+                }
+                copy_box(to, &x_map, 0, row, &s_raw_full[raw_slot]);
+                if (++raw_slot == C::kRawStages) raw_slot = 0, raw_parity ^= 1;
+                if (kCopies) {
+                    if (!barrier_wait(&s_empty[slot], parity)) {
+                        s_failed = 1;
+                        ++stage;
+                        break;
+                    }
+                    barrier_expect(&s_copied[slot], boxes * C::kBlock);
+                    for (int k = 0; k < boxes; ++k)
+                        copy_box(ring + slot * C::kStageBytes + k * C::kBlock, &dy_map, 64 * k, row, &s_copied[slot]);
+                    ++copied;
+                    if (++slot == C::kStages) slot = 0, parity ^= 1;
+                }
             }
             // every copy has come before the block ends
-            for (int k = stage < C::kStages ? stage : C::kStages; k > 0; --k) {
-                const int s = (stage - k) % C::kStages;
-                if (!barrier_wait(&s_copied[s], (stage - k) / C::kStages & 1)) s_failed = 1;
-            }
+            for (int k = copied < C::kStages ? copied : C::kStages; k > 0; --k)
+                if (!barrier_wait(&s_copied[(copied - k) % C::kStages], (copied - k) / C::kStages & 1)) s_failed = 1;
+            for (int k = stage < C::kRawStages ? stage : C::kRawStages; k > 0; --k)
+                if (!barrier_wait(&s_raw_full[(stage - k) % C::kRawStages], (stage - k) / C::kRawStages & 1)) s_failed = 1;
         }
         __syncwarp();
     }
@@ -406,6 +460,7 @@ __global__ void __launch_bounds__(SLICES * 32) k_dense_join(DenseArgs a, int w_c
 
 // Ranges of rows with sums of their own: as many as fill the device, in as many rounds as it takes
 // for none to be longer than a chain; of kLeastRows at least.
+constexpr int kMostSmem = 113 * 1024, kTwoSmem = 112 * 1024 + 512;     // two CTAs of an SM
 constexpr int kLeastRows = 128;
 int splits_of(int64_t n, int gdt) {
     const int64_t once = kSms * 2, chain = gdt == SS_F32 ? kChain32 : kChain16;
@@ -414,19 +469,54 @@ int splits_of(int64_t n, int gdt) {
     return int(s < most ? s : (most < 1 ? 1 : most));
 }
 
-template <typename T, int TI, int TJ, int FMT>
-ss_status launch(DenseArgs a, cudaStream_t s, const char *who) {
-    using C = Config<T, TI, TJ>;
+template <typename T, int TI, int TJ, int ROWS, int FMT>
+ss_status launch(DenseArgs a, const RawStage &raw, bool fast, size_t smem, cudaStream_t s, const char *who) {
+    using C = Config<T, TI, TJ, ROWS>;
     const int64_t each = (a.n + a.splits - 1) / a.splits, rows = (each + C::kRows - 1) / C::kRows * C::kRows;
-    const bool fast = a.n > 0 && units_aligned<T>(a.dy, a.dys) && aligned_to(a.x.q, 16) && a.x.stride % 16 == 0;
     static std::atomic<unsigned long long> smem_ctx[kMaxDevices];   // see ensure_dyn_smem
-    const void *fn[2] = {(const void *)k_dense<T, TI, TJ, FMT, true>, (const void *)k_dense<T, TI, TJ, FMT, false>};
-    ss_status st = ensure_dyn_smem(smem_ctx, fn, 2, C::kSmem, who);
+    const void *fn[2] = {(const void *)k_dense<T, TI, TJ, ROWS, FMT, true>, (const void *)k_dense<T, TI, TJ, ROWS, FMT, false>};
+    ss_status st = ensure_dyn_smem(smem_ctx, fn, 2, kMostSmem, who);
     if (st != SS_OK) return st;
-    CUtensorMap map = {};
-    if (fast && C::kParts == 1 && (st = map_of(&map, a.dy, a.n, a.N, a.dys, C::kRows, who)) != SS_OK) return st;
-    auto kernel = fast ? k_dense<T, TI, TJ, FMT, true> : k_dense<T, TI, TJ, FMT, false>;
-    SS_LAUNCH("k_dense", s, kernel<<<a.splits, C::kThreads, C::kSmem, s>>>(a, rows, map));
+    CUtensorMap dy_map = {}, x_map = {};
+    if (fast) {
+        constexpr int kSize = int(sizeof(T));
+        st = C::kParts == 1 ? map_of(&dy_map, a.dy, a.n, a.N, a.dys, C::kRows, who)
+                            : map_of(&dy_map, kSize == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.dy, a.n,
+                                     a.N, a.dys * kSize, raw.dy_pitch / kSize, C::kRows, false, who);
+        if (st != SS_OK) return st;
+        st = map_of(&x_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x.q, a.n, units_of(a.D) * kUnit, a.x.stride, raw.x_pitch, C::kRows, false,
+                    who);
+        if (st != SS_OK) return st;
+    }
+    auto kernel = fast ? k_dense<T, TI, TJ, ROWS, FMT, true> : k_dense<T, TI, TJ, ROWS, FMT, false>;
+    SS_LAUNCH("k_dense", s, kernel<<<a.splits, C::kThreads, smem, s>>>(a, rows, raw, dy_map, x_map));
+    return SS_OK;
+}
+
+// Stages of 64 rows where two CTAs of an SM have room for them, else of 32.
+template <typename T, int TI, int TJ, int FMT>
+ss_status launch(const DenseArgs &a, cudaStream_t s, const char *who) {
+    const bool fast = a.n > 0 && aligned_to(a.dy, 16) && a.dys * int64_t(sizeof(T)) % 16 == 0 && aligned_to(a.x.q, 16) &&
+                      a.x.stride % 16 == 0;
+    RawStage raw{parts_of<T>() == 1 ? 0 : (a.N * int(sizeof(T)) + 15) / 16 * 16, (a.D + 15) / 16 * 16, 0};
+    raw.bytes = raw.dy_pitch + raw.x_pitch;       // of a row
+    using C64 = Config<T, TI, TJ, 64>;
+    using C32 = Config<T, TI, TJ, 32>;
+    // what the widest rows take; float32 of up to 64 x 64 goes by its own
+    constexpr int kWidest = C64::kStages * C64::kStageBytes + C64::kRawStages * 64 * (TI * (parts_of<T>() == 1 ? 0 : int(sizeof(T))) + TJ);
+    constexpr bool kBoth = parts_of<T>() == 3 && TI == 64 && TJ == 64;
+    if constexpr (kBoth || kWidest <= kTwoSmem) {
+        const size_t smem = C64::kStages * C64::kStageBytes + (fast ? C64::kRawStages * 64 * raw.bytes : 0) + 1280;
+        if (!kBoth || smem <= kTwoSmem) {
+            raw.bytes *= 64;
+            return launch<T, TI, TJ, 64, FMT>(a, raw, fast, smem, s, who);
+        }
+    }
+    if constexpr (kBoth || kWidest > kTwoSmem) {
+        const size_t smem = C32::kStages * C32::kStageBytes + (fast ? C32::kRawStages * 32 * raw.bytes : 0) + 1280;
+        raw.bytes *= 32;
+        return launch<T, TI, TJ, 32, FMT>(a, raw, fast, smem, s, who);
+    }
     return SS_OK;
 }
 

@@ -38,27 +38,16 @@ struct Walk {
     }
 };
 
-// Bound by memory.  AHEAD units' loads are in flight in a thread.
-template <typename T, int FMT, bool ALIGNED, int AHEAD>
+// Bound by memory.  A unit at a time and many warps (2M x 48 float32: 82 us; two units' loads in
+// flight 87, four 92, with the registers that they take).
+template <typename T, int FMT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_rows8_pack(const T *x, int64_t xs, int64_t n, int32_t D, Rows8 out) {
-    Walk w(n, D);
-    while (__any_sync(0xffffffffu, w.row < n)) {
-        Raw<T> r[AHEAD];
-        int64_t row[AHEAD];
-        int u[AHEAD], count[AHEAD];
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            row[k] = w.row, u[k] = w.u, count[k] = w.count(D);
-            r[k] = load_unit<T, ALIGNED>(x + row[k] * xs + u[k] * kUnit, count[k]);
-            w.next();
-        }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            F2 f[4];
-            floats_of(f, r[k]);
-            const uint32_t e = group_exponent<FMT>(f);
-            if (count[k] > 0) put_unit<FMT>(out, row[k], u[k], e, f);
-        }
+    for (Walk w(n, D); __any_sync(0xffffffffu, w.row < n); w.next()) {
+        const int count = w.count(D);
+        F2 f[4];
+        floats_of(f, load_unit<T, ALIGNED>(x + w.row * xs + w.u * kUnit, count));
+        const uint32_t e = group_exponent<FMT>(f);
+        if (count > 0) put_unit<FMT>(out, w.row, w.u, e, f);
     }
 }
 
@@ -73,39 +62,25 @@ __device__ __forceinline__ F2 held_to<__half>(F2 v) {
 
 // Where x's rows start off their blocks' boundaries, units lie on them all the same, and take what
 // is held from two units (one more of them a row then).
-template <typename T, int FMT, bool ALIGNED, int AHEAD>
+template <typename T, int FMT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_rows8_unpack(Rows8 in, int64_t n, int32_t D, T *x, int64_t xs) {
-    Walk w(n, ALIGNED ? D : D + kUnit - 1);
-    typename std::conditional<ALIGNED, Held, HeldAcross>::type h[AHEAD];
-    while (w.row < n) {
-        T *p[AHEAD];
-        int lo[AHEAD], hi[AHEAD], column[AHEAD];
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            T *at = x + w.row * xs;
-            const int head = ALIGNED ? 0 : head_of<T>(at);
-            column[k] = w.u * kUnit - head, p[k] = at + column[k];
-            lo[k] = w.u == 0 ? head : 0;
-            const int c = D - column[k];
-            hi[k] = w.row >= n || c <= 0 ? 0 : (c < kUnit ? c : kUnit);
-            if constexpr (ALIGNED)
-                h[k].load(in, w.row, w.u, hi[k] > 0);
-            else
-                h[k].load(in, w.row, column[k], D, hi[k] > 0);
-            w.next();
+    for (Walk w(n, ALIGNED ? D : D + kUnit - 1); w.row < n; w.next()) {
+        T *at = x + w.row * xs;
+        const int head = ALIGNED ? 0 : head_of<T>(at), column = w.u * kUnit - head;
+        if (column >= D) continue;
+        F2 f[4];
+        if constexpr (ALIGNED) {
+            Held h;
+            h.load(in, w.row, w.u, true);
+            h.values<FMT>(f);
+        } else {
+            HeldAcross h;
+            h.load(in, w.row, column, D, true);
+            h.values<FMT>(f, column);
         }
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            if (hi[k] <= 0) continue;
-            F2 f[4];
-            if constexpr (ALIGNED)
-                h[k].template values<FMT>(f);
-            else
-                h[k].template values<FMT>(f, column[k]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = held_to<T>(f[i]);
-            store_block(p[k], raw_of<T>(f), lo[k], hi[k]);
-        }
+        for (int i = 0; i < 4; ++i) f[i] = held_to<T>(f[i]);
+        store_block(at + column, raw_of<T>(f), w.u == 0 ? head : 0, D - column < kUnit ? D - column : kUnit);
     }
 }
 
@@ -143,9 +118,9 @@ ss_status ss_rows8_pack(const void *x, ss_dtype dtype, int64_t x_stride, int64_t
         with_format(out->format, [&](auto F) {
             constexpr int FMT = decltype(F)::value;
             if (aligned)
-                SS_LAUNCH("k_rows8_pack", s, k_rows8_pack<T, FMT, true, 2><<<grid, kThreads, 0, s>>>(p, x_stride, n, D, o));
+                SS_LAUNCH("k_rows8_pack", s, k_rows8_pack<T, FMT, true><<<grid, kThreads, 0, s>>>(p, x_stride, n, D, o));
             else
-                SS_LAUNCH("k_rows8_pack", s, k_rows8_pack<T, FMT, false, 2><<<grid, kThreads, 0, s>>>(p, x_stride, n, D, o));
+                SS_LAUNCH("k_rows8_pack", s, k_rows8_pack<T, FMT, false><<<grid, kThreads, 0, s>>>(p, x_stride, n, D, o));
         });
     });
     return check_launch(who);
@@ -173,9 +148,9 @@ ss_status ss_rows8_unpack(const ss_rows8 *in, int64_t n, int32_t D, void *x, ss_
         with_format(in->format, [&](auto F) {
             constexpr int FMT = decltype(F)::value;
             if (aligned)
-                SS_LAUNCH("k_rows8_unpack", s, k_rows8_unpack<T, FMT, true, 4><<<grid, kThreads, 0, s>>>(r, n, D, p, x_stride));
+                SS_LAUNCH("k_rows8_unpack", s, k_rows8_unpack<T, FMT, true><<<grid, kThreads, 0, s>>>(r, n, D, p, x_stride));
             else
-                SS_LAUNCH("k_rows8_unpack", s, k_rows8_unpack<T, FMT, false, 2><<<grid, kThreads, 0, s>>>(r, n, D, p, x_stride));
+                SS_LAUNCH("k_rows8_unpack", s, k_rows8_unpack<T, FMT, false><<<grid, kThreads, 0, s>>>(r, n, D, p, x_stride));
         });
     });
     return check_launch(who);

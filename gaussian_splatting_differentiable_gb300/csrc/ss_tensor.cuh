@@ -99,19 +99,23 @@ inline ss_status encoder(EncodeFn *fn, const char *who) {
     return SS_OK;
 }
 
-// A matrix of bfloat16 (rows of `columns`, `stride` elements apart) in boxes of 64 columns x
-// `box_rows` rows, swizzled as the products read them.
-inline ss_status map_of(CUtensorMap *map, const void *p, int64_t rows, int64_t columns, int64_t stride, int box_rows,
-                        const char *who) {
+// A matrix (rows of `columns`, `stride` bytes apart) in boxes of box_columns x box_rows, side by side
+// as they lie, or (64 columns of bfloat16) swizzled as the products read them.
+inline ss_status map_of(CUtensorMap *map, CUtensorMapDataType type, const void *p, int64_t rows, int64_t columns, int64_t stride,
+                        int box_columns, int box_rows, bool swizzled, const char *who) {
     EncodeFn encode;
     const ss_status st = encoder(&encode, who);
     if (st != SS_OK) return st;
-    const cuuint64_t dims[2] = {cuuint64_t(columns), cuuint64_t(rows)}, strides[1] = {cuuint64_t(stride) * 2};
-    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, each[2] = {1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, each,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t dims[2] = {cuuint64_t(columns), cuuint64_t(rows)}, strides[1] = {cuuint64_t(stride)};
+    const cuuint32_t box[2] = {cuuint32_t(box_columns), cuuint32_t(box_rows)}, each[2] = {1, 1};
+    const CUresult r = encode(map, type, 2, const_cast<void *>(p), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SS_OK : fail(SS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", who, int(r));
+}
+inline ss_status map_of(CUtensorMap *map, const void *p, int64_t rows, int64_t columns, int64_t stride, int box_rows,
+                        const char *who) {
+    return map_of(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, rows, columns, stride * 2, 64, box_rows, true, who);
 }
 
 }  // namespace ss
