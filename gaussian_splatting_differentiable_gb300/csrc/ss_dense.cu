@@ -459,14 +459,15 @@ __global__ void __launch_bounds__(SLICES * 32) k_dense_join(DenseArgs a, int w_c
 }
 
 // Ranges of rows with sums of their own: as many as fill the device, in as many rounds as it takes
-// for none to be longer than a chain; of kLeastRows at least.
+// for none to be longer than a chain; of kLeastRows at least, and one where it spares the launch that
+// joins them.
 constexpr int kMostSmem = 113 * 1024, kTwoSmem = 112 * 1024 + 512;     // two CTAs of an SM
-constexpr int kLeastRows = 128;
+constexpr int kLeastRows = 128, kOneRange = 256;
 int splits_of(int64_t n, int gdt) {
     const int64_t once = kSms * 2, chain = gdt == SS_F32 ? kChain32 : kChain16;
     const int64_t most = (n + kLeastRows - 1) / kLeastRows, rounds = (n + once * chain - 1) / (once * chain);
     const int64_t s = once * rounds;
-    return int(s < most ? s : (most < 1 ? 1 : most));
+    return n <= kOneRange ? 1 : int(s < most ? s : most);
 }
 
 template <typename T, int TI, int TJ, int ROWS, int FMT>
