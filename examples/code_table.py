@@ -1,6 +1,6 @@
 """Train a splat scene whose colours come from a learned code table.
 
-    python examples/code_table.py [--splats N] [--codes V] [--steps K]
+    python examples/code_table.py [--splats N] [--codes V] [--steps K] [--keep int8|e4m3]
 
 Every splat names a row of a table of V codes of 48 values.  A step looks the
 rows up and scales them, normalises each (layer norm with learned weights),
@@ -8,8 +8,9 @@ takes the result as the splat's degree-3 colour coefficients, projects and
 rasterizes the splats, compares the image with a target (L1 + SSIM), sends the
 gradients all the way back (rasterizer, projection, layer norm, table), clips
 the gradients of everything that is learned by their common norm, and moves
-against them.  The target is the same scene with colours of its own; all data
-is synthetic.
+against them.  With --keep, what the norm's backward pass needs of its input is
+kept in 8 bits from the forward on.  The target is the same scene with colours of
+its own; all data is synthetic.
 """
 from __future__ import annotations
 
@@ -25,6 +26,7 @@ import gaussian_splatting_differentiable_gb300 as ss  # noqa: E402
 from synth.scene3d import make_scene3d  # noqa: E402
 
 COEFFICIENTS = 16     # of degree 3, for each of 3 colours
+FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 RATES = {"table": 2.0, "gamma": 0.5, "beta": 0.5, "opacity": 0.2, "mean3": 1e-4, "scale": 1e-4,
          "quat": 1e-3}
 
@@ -32,7 +34,8 @@ RATES = {"table": 2.0, "gamma": 0.5, "beta": 0.5, "opacity": 0.2, "mean3": 1e-4,
 class CodeTableScene:
     """A scene's parameters, the buffers of every step, and the step itself."""
 
-    def __init__(self, scene, codes: int, max_norm: float = 0.03, seed: int = 0, device="cuda"):
+    def __init__(self, scene, codes: int, max_norm: float = 0.03, seed: int = 0, device="cuda",
+                 keep=None):
         d = torch.device(device)
         g = torch.Generator(device=d).manual_seed(seed)
         n, D = scene.n, 3 * COEFFICIENTS
@@ -51,6 +54,7 @@ class CodeTableScene:
         self.ids = torch.where(torch.arange(n, device=d) % 64 == 63, -1, ids)
         self.lookup = ss.Embedding(n, codes, D, scale=D ** 0.5, device=d)
         self.norm = ss.LayerNorm(n, D, device=d)
+        self.kept = None if keep is None else ss.Rows8(n, D, keep, device=d)
         self.projector = ss.Projector(n, 3, d)
         self.raster = ss.Rasterizer(scene.W, scene.H, n, 8 * n, device=d)
         self.loss = ss.SsimLoss(3, scene.H, scene.W, device=d)
@@ -65,6 +69,8 @@ class CodeTableScene:
     def render(self) -> torch.Tensor:
         codes = self.lookup.forward(self.params["table"], self.ids)
         coef = self.norm.forward(codes, self.params["gamma"], self.params["beta"])
+        if self.kept is not None:
+            self.kept.pack(codes)
         self.splats.sh.view(coef.shape[1], -1).copy_(coef.t())     # [16, 3, n]
         self.projector.forward(self.splats, self.cam)
         self.flat = self.projector.splats2d(self.params["opacity"])
@@ -77,7 +83,8 @@ class CodeTableScene:
         r = self.raster.grads
         self.projector.backward(self.splats, self.cam, r["dmean2d"], r["dconic"], r["drgb"])
         self.dcoef.copy_(self.projector.grads["dsh"].view(self.dcoef.shape[1], -1).t())
-        dcodes = self.norm.backward(self.dcoef, self.lookup.out, self.params["gamma"])
+        codes = self.lookup.out if self.kept is None else self.kept
+        dcodes = self.norm.backward(self.dcoef, codes, self.params["gamma"])
         self.lookup.backward(dcodes, self.ids)
 
     def step(self, target: torch.Tensor) -> torch.Tensor:
@@ -109,10 +116,11 @@ def main() -> None:
     ap.add_argument("--splats", type=int, default=5207)
     ap.add_argument("--codes", type=int, default=256)
     ap.add_argument("--steps", type=int, default=100)
+    ap.add_argument("--keep", choices=sorted(FORMATS))
     a = ap.parse_args()
     scene = make_scene3d(11, n=a.splats, W=256, H=256)
     target = target_of(scene)
-    model = CodeTableScene(scene, a.codes)
+    model = CodeTableScene(scene, a.codes, keep=FORMATS.get(a.keep))
     losses = [model.step(target) for _ in range(a.steps)]
     for k in sorted({0, a.steps // 4, a.steps // 2, a.steps - 1}):
         print("step %4d: loss %.5f" % (k, float(losses[k])))
