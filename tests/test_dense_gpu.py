@@ -55,7 +55,11 @@ SHAPES = [(1, 1, 1, "f32", "f32", "int8", 0, 0), (0, 5, 7, "f32", "f32", "int8",
           (2049, 200, 33, "f32", "f32", "e4m3", 0, 0), (40, 1001, 333, "bf16", "bf16", "int8", 0, 0),
           (4097, 65, 1, "bf16", "f32", "int8", 0, 0), (3001, 1, 300, "f32", "f32", "e4m3", 0, 0),
           (5000, 59, 48, "f32", "f32", "int8", 0, 0), (20000, 7, 9, "f16", "f32", "int8", 0, 0),
-          (700, 384, 640, "f16", "f16", "e4m3", 0, 0), (70, 2503, 31, "bf16", "f32", "int8", 0, 0)]
+          (700, 384, 640, "f16", "f16", "e4m3", 0, 0), (70, 2503, 31, "bf16", "f32", "int8", 0, 0),
+          (256, 48, 48, "f32", "f32", "int8", 0, 0), (255, 16, 30, "f16", "f32", "e4m3", 8, 0),
+          (300, 60, 100, "f32", "f32", "int8", 4, 0), (310, 100, 60, "f32", "f32", "e4m3", 8, 8),
+          (320, 120, 128, "f16", "f32", "int8", 0, 0), (3, 65536, 1, "bf16", "bf16", "int8", 0, 0),
+          (2, 1, 65536, "f32", "f32", "e4m3", 0, 0), (5, 300, 20000, "f16", "f32", "int8", 0, 0)]
 
 
 @pytest.mark.parametrize("case", SHAPES, ids=lambda c: "-".join(map(str, c)))
@@ -141,7 +145,8 @@ def test_range_ends(ss):
     (200000, 48, 48, "f32", "f32"), (60000, 130, 70, "bf16", "f32"), (3000, 1500, 1100, "f16", "f32"),
     (1700000, 16, 24, "f16", "f32"), (300000, 100, 128, "bf16", "f32"), (100000, 60, 128, "f32", "f32"),
     (9000, 2500, 2300, "bf16", "f32"), (300000, 200, 200, "f32", "f32"), (7000, 2000, 2100, "f32", "f32"),
-    (18000, 2400, 2500, "bf16", "bf16"), (20000, 1700, 1800, "f16", "f16")])
+    (18000, 2400, 2500, "bf16", "bf16"), (20000, 1700, 1800, "f16", "f16"),
+    (270000, 200, 200, "bf16", "f32"), (270000, 200, 216, "bf16", "bf16")])
 def test_long_sums(ss, n, N, D, t, gt):
     """Sums of many rows keep float32's accuracy, far below the bound that the number of
     rows gives.  The summands' signs are random: no partial sum is past 6 times their root sum of
@@ -170,26 +175,32 @@ def test_long_sums(ss, n, N, D, t, gt):
     assert float((off / dy.double().square().sum(0).sqrt()).max()) <= limit * (1 + u)
 
 
-def test_offsets_past_32_bits(ss):
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [64, 200])
+def test_offsets_past_32_bits(ss, N, t):
     import torch
     stride = (1 << 30) + 8
-    buf = torch.empty(3 * stride + 64, dtype=torch.bfloat16, device="cuda")
-    big = torch.as_strided(buf, (4, 64), (stride, 1))
-    small = torch.randn(4, 64, device="cuda").bfloat16()
+    buf = torch.empty(3 * stride + N, dtype=dtype(t), device="cuda")
+    big = torch.as_strided(buf, (4, N), (stride, 1))
+    small = torch.randn(4, N, device="cuda").to(dtype(t))
     big.copy_(small)
-    far = torch.empty(3 * stride + 64, dtype=torch.uint8, device="cuda")
+    far = torch.empty(3 * (stride + 8) + 64, dtype=torch.uint8, device="cuda")
     x = torch.randn(4, 64, device="cuda")
     a, b = ss.Rows8(4, 64).pack(x), ss.Rows8(4, 64)
     b._c.q, b._c.q_stride = far.data_ptr(), stride
     b.pack(x)
-    m, k = (ss.DenseGrad(4, 64, 64, dtype=torch.bfloat16) for _ in range(2))
-    assert torch.equal(m.backward(small, a), k.backward(big, b))
+    m, k = (ss.DenseGrad(4, N, 64, dtype=dtype(t)) for _ in range(2))
+    want = m.backward(small, a)
+    assert torch.equal(want, k.backward(big, a)) and torch.equal(want, k.backward(small, b))
+    b._c.q_stride = stride + 8                       # rows on 16-byte boundaries
+    assert torch.equal(want, k.backward(big, b.pack(x)))
 
 
-def test_another_stream_and_a_captured_graph(ss):
+@pytest.mark.parametrize("N,t", [(48, "f32"), (48, "bf16"), (300, "f16"), (300, "bf16")])
+def test_another_stream_and_a_captured_graph(ss, N, t):
     import torch
-    dy, x = torch.randn(3000, 48, device="cuda"), torch.randn(3000, 100, device="cuda")
-    r, m = ss.Rows8(3000, 100), ss.DenseGrad(3000, 48, 100)
+    dy, x = torch.randn(3000, N, device="cuda").to(dtype(t)), torch.randn(3000, 100, device="cuda")
+    r, m = ss.Rows8(3000, 100), ss.DenseGrad(3000, N, 100, dtype=dtype(t))
     m.backward(dy, r.pack(x))
     have = tuple(m.grads.values())
     want = [v.clone() for v in have]

@@ -245,7 +245,8 @@ def bwd_case(ss, n, D, t, p, pad, off, kind="rms", source="int8", dsum=True, aff
     assert ((buf == 0) | (buf == -7.0)).all()
 
 
-MORE = [(5000, 48, "f32", "f32", 0, 0), (6001, 7, "bf16", "bf16", 0, 0), (2000, 1000, "bf16", "bf16", 0, 0),
+MORE = [(0, 48, "bf16", "bf16", 0, 0), (5000, 48, "f32", "f32", 0, 0), (4000, 35, "bf16", "f32", 0, 0), (900, 505, "f16", "f16", 0, 1),
+        (300, 8185, "bf16", "f32", 0, 0), (250, 4100, "f32", "f32", 4, 0), (40, 8184, "f32", "f32", 8, 0), (6001, 7, "bf16", "bf16", 0, 0), (2000, 1000, "bf16", "bf16", 0, 0),
         (701, 513, "f32", "f32", 0, 0), (1500, 1001, "bf16", "bf16", 0, 0), (3000, 90, "f16", "f32", 3, 1)]
 
 
