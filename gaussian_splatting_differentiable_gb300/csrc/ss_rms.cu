@@ -209,11 +209,19 @@ struct FwdArgs {
     float *rstd;
 };
 
+// CTAs an SM that the registers are held down for, of narrow rows (0: wide ones as the compiler has them in CTAs of
+// up to 512).  Forward: 700,000 x 87 float16 with five 193 us, with four 207; 2M x 48 float32 with four 228, with
+// five 236; 60,000 x 500 float16 (two units a lane) with three 58, with two 71.
+constexpr int fwd_ctas(int bytes, int nv, bool multi) { return multi ? 0 : (nv == 2 ? 3 : (bytes == 2 ? 5 : 4)); }
+// Backward: 2M x 48 float32 with two 224 us, with three 282 (spills); 2M x 48 bfloat16 with three 142, with two
+// 169; 60,000 x 500 float32 with one 123, with two 144.
+constexpr int bwd_ctas(int bytes, int nv, bool multi) { return multi ? 0 : (nv == 2 ? (bytes == 2 ? 2 : 1) : (bytes == 2 ? 3 : 2)); }
+
 // A row from registers: its sum with the residual, its square's mean, and every
 // output that is wanted.  The next row's loads are in flight meanwhile.  (kShifted: without
 // outputs in 8 bits, whose groups begin with the row.)
 template <typename T, int NV, bool MULTI, Lie LIE, bool RES>
-__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_rms_fwd(FwdArgs a, Place pl) {
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(sizeof(T), NV, MULTI)) k_rms_fwd(FwdArgs a, Place pl) {
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][1][kRowWarps];
     const int group = MULTI ? threadIdx.x / pl.lanes : threadIdx.x >> pl.shift;
     const int lane = MULTI ? threadIdx.x - group * pl.lanes : threadIdx.x & (pl.lanes - 1);
@@ -410,7 +418,7 @@ struct Ring {
 // registers over all of a CTA's rows and leave one partial sum a CTA in a.part (none where it is
 // NULL), or, where one CTA has all rows, the gradients themselves.
 template <typename T, int NV, bool MULTI, Lie LIE, bool CENTRED, int FMT>
-__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads) k_norm8_bwd(BwdArgs a, Place pl, bool alone) {
+__global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, bwd_ctas(sizeof(T), NV, MULTI)) k_norm8_bwd(BwdArgs a, Place pl, bool alone) {
     constexpr int kSums = CENTRED ? 2 : 1;
     constexpr bool HELD = FMT >= 0;
     using R = Ring<T, NV, LIE, CENTRED, HELD>;
