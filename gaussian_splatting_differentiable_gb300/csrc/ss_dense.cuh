@@ -8,8 +8,8 @@
 // a float16's 11.  The tensor cores cut every addition off at float32's last place, towards
 // zero, so a long chain of them loses a little of each sum: after 2048 rows 5e-7 of it, after 4096
 // 1.2e-6.  So the products of mid and lo have sums of their own (with hi's they would cut those off
-// three times as often), and where dW is float32 the sums leave the tensor memory every
-// kChain32 rows and are added in float32.
+// three times as often), and no sum stays in the tensor memory for more than a chain of rows,
+// kChain32 where dW is float32; what it held then is added in float32.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -37,7 +37,7 @@ struct DenseArgs {
     int64_t n;
     int32_t N, D;
     int splits, bias_splits;
-    int chain;            // stages of a chain of sums
+    int chain;            // stages of a chain of sums (weights past one tile)
     float *part;          // [splits][N][D], where sums leave the tensor memory before they are done
     float *part_bias;     // [bias_splits][N]
     void *dw;

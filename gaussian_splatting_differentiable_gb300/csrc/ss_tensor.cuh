@@ -19,8 +19,8 @@ __device__ __forceinline__ void barrier_init(uint64_t *b, uint32_t count) {
 __device__ __forceinline__ void barrier_arrive(uint64_t *b) {
     asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(smem_of(b)) : "memory");
 }
-// Waits for the phase of that parity to end; false after some seconds, when something has gone
-// wrong.
+// Waits for the phase of that parity to end; false after a million tries, each of which may
+// itself wait: something has gone wrong then.
 __device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity) {
     for (uint32_t k = 0; k < (1u << 20); ++k) {
         uint32_t done;
@@ -32,7 +32,7 @@ __device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity) {
 }
 __device__ __forceinline__ void writes_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// A box of 64 columns (kRows rows) at (column, row), zeros outside the matrix.
+// A map's box at (column, row), zeros outside the matrix.
 __device__ __forceinline__ void copy_box(uint32_t smem, const CUtensorMap *map, int column, int row, uint64_t *b) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(smem), "l"(map), "r"(column), "r"(row), "r"(smem_of(b)) : "memory");

@@ -4,10 +4,13 @@
  *
  *   dW[i][j] = sum over rows m of dy[m][i] x[m][j],   db[i] = sum of dy[m][i]
  *
- * x[m][j] is q s as it is held; every product is exact in the sums' terms
- * (x in bfloat16, dy as the sum of one, two or three bfloat16 values), and sums are float32 along
- * splits of the rows that depend on the sizes: with those the same, the same inputs
- * give the same bits.
+ * x[m][j] is q s as it is held.  Every product is exact (x in bfloat16, dy as the sum of one,
+ * two or three bfloat16 values, which float16 and float32 values are); sums are float32,
+ * in the tensor cores for up to 2816 rows (16,384 where dweight has 16 bits), which cut
+ * off what float32's last place does not hold, and rounded to nearest from there on.  The rows
+ * are split by the sizes, the types and the alignment: with those the same, the same
+ * inputs give the same bits.  (Scales below 2^-111, which packing does not make, may leave x
+ * bfloat16's subnormals.)  Should one of the kernels' waits run out, dweight reads NaN.
  *
  * Conventions are those of ss.h; rows and strides those of ss_embed.h.
  */
