@@ -50,14 +50,16 @@ bool in_registers(int32_t D) { return D <= kMaxRowThreads * 2 * kUnit; }
 bool shifted_in_registers(int32_t D) { return D + 2 * (kUnit - 1) < kMaxRowThreads * 2 * kUnit; }
 
 // Up to 32 lanes a unit each; a warp with two units a lane up to 64; from there on
-// whole warps.
-Place place_of(int32_t D, bool shifted, int *nv, bool *multi) {
+// whole warps.  `single`: whole warps with a unit a lane as far as they go, for the gradients of float32 rows, whose
+// two units take more registers than there are (8191 x 4096: 131 us for 80; of 16-bit rows 49 for 66).
+Place place_of(int32_t D, bool shifted, bool single, int *nv, bool *multi) {
     Place pl{};
     pl.units = units_of(shifted ? D + kUnit - 1 : D);
     *nv = pl.units <= 32 ? 1 : 2;
     *multi = pl.units > 64;
+    if (single && pl.units > 32 && pl.units <= kMaxRowThreads) *nv = 1, *multi = true;
     if (*multi) {
-        pl.lanes = (pl.units + 63) / 64 * 32;
+        pl.lanes = (pl.units + 32 * *nv - 1) / (32 * *nv) * 32;
         pl.groups = pl.lanes < kThreads ? kThreads / pl.lanes : 1;
     } else {
         pl.lanes = 1, pl.shift = 0;
@@ -214,8 +216,8 @@ struct FwdArgs {
 // five 236; 60,000 x 500 float16 (two units a lane) with three 58, with two 71.
 constexpr int fwd_ctas(int bytes, int nv, bool multi) { return multi ? 0 : (nv == 2 ? 3 : (bytes == 2 ? 5 : 4)); }
 // Backward: 2M x 48 float32 with two 224 us, with three 282 (spills); 2M x 48 bfloat16 with three 142, with two
-// 169; 60,000 x 500 float32 with one 123, with two 144.
-constexpr int bwd_ctas(int bytes, int nv, bool multi) { return multi ? 0 : (nv == 2 ? (bytes == 2 ? 2 : 1) : (bytes == 2 ? 3 : 2)); }
+// 169.
+constexpr int bwd_ctas(int bytes, int nv, bool multi) { return multi ? 0 : (bytes == 4 || nv == 2 ? 2 : 3); }
 
 // A row from registers: its sum with the residual, its square's mean, and every
 // output that is wanted.  The next row's loads are in flight meanwhile.  (kShifted: without
@@ -764,14 +766,18 @@ int grid_of(std::atomic<unsigned long long> *known, K kernel, int threads, size_
 }
 
 // f(NV, MULTI) of a place, as constants.
-template <typename F>
+template <bool SINGLE, typename F>
 void with_place(int nv, bool multi, F &&f) {
-    if (multi)
+    if (multi && nv == 2) {
         f(std::integral_constant<int, 2>(), std::true_type());
-    else if (nv == 2)
-        f(std::integral_constant<int, 2>(), std::false_type());
-    else
-        f(std::integral_constant<int, 1>(), std::false_type());
+        return;
+    }
+    if constexpr (SINGLE) {
+        if (multi) return f(std::integral_constant<int, 1>(), std::true_type());
+    } else {
+        if (nv == 2) return f(std::integral_constant<int, 2>(), std::false_type());
+    }
+    f(std::integral_constant<int, 1>(), std::false_type());
 }
 template <typename F>
 void with_lie(Lie lie, F &&f) {
@@ -804,9 +810,9 @@ void launch_fwd(const FwdArgs &a, int sms, cudaStream_t s) {
     const Lie lie = aligned ? kAligned : (alike && shifted_in_registers(a.D) ? kShifted : kAnyhow);
     int nv;
     bool multi;
-    const Place pl = place_of(a.D, lie == kShifted, &nv, &multi);
+    const Place pl = place_of(a.D, lie == kShifted, false, &nv, &multi);
     const int threads = multi ? pl.lanes * pl.groups : kThreads, period = lie == kShifted ? period_of(a.xs) : 1;
-    with_place(nv, multi, [&](auto NV, auto MULTI) {
+    with_place<false>(nv, multi, [&](auto NV, auto MULTI) {
         with_lie(lie, [&](auto LIE) {
             with_flag(a.residual != nullptr, [&](auto RES) {
                 auto kernel = k_rms_fwd<T, NV(), MULTI(), LIE(), RES()>;
@@ -843,12 +849,12 @@ ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
     const Lie lie = aligned ? kAligned : (alike && shifted_in_registers(a.D) ? kShifted : kAnyhow);
     int nv;
     bool multi;
-    const Place pl = place_of(a.D, lie == kShifted, &nv, &multi);
+    const Place pl = place_of(a.D, lie == kShifted, sizeof(T) == 4, &nv, &multi);
     const int threads = multi ? pl.lanes * pl.groups : kThreads, period = lie == kShifted ? period_of(a.dys) : 1;
     // what one CTA takes at once needs no launch that adds up several CTAs' sums
     const bool alone = a.n <= pl.groups;
     ss_status st = SS_OK;
-    with_place(nv, multi, [&](auto NV, auto MULTI) {
+    with_place<sizeof(T) == 4>(nv, multi, [&](auto NV, auto MULTI) {
         with_lie(lie, [&](auto LIE) {
             auto kernel = k_norm8_bwd<T, NV(), MULTI(), LIE(), CENTRED, FMT>;
             using R = Ring<T, NV(), LIE(), CENTRED, HELD>;

@@ -104,13 +104,14 @@ def test_products_are_exact(ss, t):
         assert np.array_equal(f64(m.grads["dbias"]), f64(dy)[0])
 
 
+@pytest.mark.parametrize("N,pad", [(40, 0), (40, 3), (200, 0), (200, 1)])
 @pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
-def test_values_that_are_not_finite(ss, t):
+def test_values_that_are_not_finite(ss, t, N, pad):
     """An infinity gives infinities of the product's sign (NaN beside zeros); NaN and
     rows that read as NaN give NaN; nothing else changes."""
     import torch
-    n, N, D = 100, 40, 64
-    dy = torch.ones(n, N, dtype=dtype(t), device="cuda")
+    n, D = 100, 64
+    dy, _ = rows(np.ones((n, N)), t, pad)
     dy[3, 5], dy[4, 6], dy[7, 8] = float("inf"), float("-inf"), float("nan")
     xv = torch.ones(n, D, device="cuda")
     xv[3, 10] = 0.0
@@ -127,16 +128,17 @@ def test_values_that_are_not_finite(ss, t):
     assert db[5] == float("inf") and db[6] == float("-inf") and torch.isnan(db[8]) and (db[rest] == n).all()
 
 
-def test_range_ends(ss):
+@pytest.mark.parametrize("N", [3, 129])
+def test_range_ends(ss, N):
     """The largest float32 and bfloat16 gradients, and scales at both ends."""
     import torch
     big = float(np.finfo(np.float32).max)
     x = torch.ones(2, 32, device="cuda")
     x[0] = 2.0 ** -90
     r = ss.Rows8(2, 32, torch.float8_e4m3fn).pack(x)
-    dy = torch.zeros(2, 3, device="cuda")
+    dy = torch.zeros(2, N, device="cuda")
     dy[0, 0], dy[0, 1], dy[1, 2] = big, -big, 2.0 ** -100
-    m = ss.DenseGrad(2, 3, 32)
+    m = ss.DenseGrad(2, N, 32)
     want = f64(dy).T @ f64(x)
     assert (np.abs(f64(m.backward(dy, r)) - want) <= 6 * U32 * np.abs(want)).all()
 
