@@ -1,6 +1,6 @@
 // The weight gradient of a dense layer from its input kept in 8 bits (model:
-// include/ss_dense.h; the method: ss_dense.cuh): weights of one tile, and the joining of
-// partial sums.
+// include/ss_dense.h; the method: ss_dense.cuh): weights of one tile or a few, and the
+// joining of partial sums.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -526,6 +526,33 @@ ss_status launch(const DenseArgs &a, cudaStream_t s, const char *who) {
     return SS_OK;
 }
 
+template <typename T, int FMT>
+ss_status tile(const DenseArgs &a, cudaStream_t s, const char *who) {
+    if (a.N <= 64 && a.D <= 64) return launch<T, 64, 64, FMT>(a, s, who);
+    if (a.N <= 64) return launch<T, 64, 128, FMT>(a, s, who);
+    if (a.D <= 64) return launch<T, 128, 64, FMT>(a, s, who);
+    return launch<T, 128, 128, FMT>(a, s, who);
+}
+
+// A weight past one tile goes to the kernel of large ones, but for one of up to eight tiles in a row or a
+// column and many rows of dy in float32 or float16: that kernel writes dy's parts to memory and
+// reads them back, here dy is read once, and a tile's two launches cost 20 us (200,000 x 256 x 128 float32: 98 us
+// for 229, 400,000 x 48 x 256 float16: 88 for 252; 16384 rows of 512 x 48 float32: 60 for 45, of 256 x 128
+// float16: 37 for 35).  bfloat16 needs no parts (131,072 x 1024 x 32: 172 for 92), and 2 x 2 tiles read both twice.
+constexpr int32_t kSide = 128, kMostTiles = 8;
+constexpr int64_t kTileRows = 32768;
+bool dense_is_big(int64_t n, int32_t N, int32_t D, int dtype) {
+    const int64_t tiles = int64_t((N + kSide - 1) / kSide) * ((D + kSide - 1) / kSide);
+    if (tiles == 1) return false;
+    return dtype == SS_BF16 || (N > kSide && D > kSide) || tiles > kMostTiles || n < tiles * kTileRows;
+}
+
+// A tile's partial sums, the bias's behind them.
+size_t tile_workspace(int splits, int32_t N, int32_t D) {
+    const size_t rows = N < kSide ? N : kSide, columns = D < kSide ? D : kSide;
+    return splits > 1 ? size_t(splits) * rows * (columns + 1) * sizeof(float) : 256;
+}
+
 bool dense_sizes_ok(int64_t n, int32_t N, int32_t D) { return row_sizes_ok(n, D) && N >= 1 && N <= kMaxWidth; }
 
 }  // namespace
@@ -556,9 +583,8 @@ extern "C" {
 
 size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D, ss_dtype dtype, ss_dtype grad_dtype) {
     if (!dense_sizes_ok(n, N, D) || !dtype_known(dtype) || (grad_dtype != SS_F32 && grad_dtype != dtype)) return 0;
-    if (dense_is_big(N, D)) return dense_big_workspace(n, N, D, dtype, grad_dtype);
-    const int splits = splits_of(n, grad_dtype);
-    return splits > 1 ? size_t(splits) * N * (size_t(D) + 1) * sizeof(float) : 256;
+    if (dense_is_big(n, N, D, dtype)) return dense_big_workspace(n, N, D, dtype, grad_dtype);
+    return tile_workspace(splits_of(n, grad_dtype), N, D);
 }
 
 ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n, int32_t N,
@@ -585,29 +611,29 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
     DenseArgs a{dy, dy_stride, rows8_of(x), n, N, D, 1, 1, 0, nullptr, nullptr, dweight, dweight_stride, dbias,
                 int(grad_dtype)};
     const int format = x ? x->format : SS_INT8;
-    if (dense_is_big(N, D)) {
+    if (dense_is_big(n, N, D, dtype)) {
         st = dense_big(who, a, dtype, format, workspace, s, sms);
         return st != SS_OK ? st : check_launch(who);
     }
+    // tile after tile, all in the same workspace
     a.splits = a.bias_splits = splits_of(n, grad_dtype);
     a.part = static_cast<float *>(workspace);
-    a.part_bias = a.part + size_t(a.splits) * N * D;
-    with_type(dtype, [&](auto t) {
-        using T = decltype(t);
-        with_format(format, [&](auto F) {
-            constexpr int FMT = decltype(F)::value;
-            if (N <= 64 && D <= 64)
-                st = launch<T, 64, 64, FMT>(a, s, who);
-            else if (N <= 64)
-                st = launch<T, 64, 128, FMT>(a, s, who);
-            else if (D <= 64)
-                st = launch<T, 128, 64, FMT>(a, s, who);
-            else
-                st = launch<T, 128, 128, FMT>(a, s, who);
-        });
-    });
-    if (st != SS_OK) return st;
-    if (a.splits > 1) dense_join(a, true, s, sms);
+    const size_t size = dtype_bytes(dtype), out_size = dtype_bytes(grad_dtype);
+    for (int32_t i = 0; i < N; i += kSide)
+        for (int32_t j = 0; j < D; j += kSide) {
+            DenseArgs t = a;
+            t.N = N - i < kSide ? N - i : kSide, t.D = D - j < kSide ? D - j : kSide;
+            t.dy = static_cast<const char *>(dy) + i * size;
+            t.x.q += j, t.x.scales += j / kGroup;
+            t.dw = static_cast<char *>(dweight) + (i * dweight_stride + j) * out_size;
+            t.db = dbias && j == 0 ? static_cast<char *>(dbias) + i * out_size : nullptr;
+            t.part_bias = t.part + size_t(t.splits) * t.N * t.D;
+            with_type(dtype, [&](auto v) {
+                with_format(format, [&](auto F) { st = tile<decltype(v), decltype(F)::value>(t, s, who); });
+            });
+            if (st != SS_OK) return st;
+            if (t.splits > 1) dense_join(t, true, s, sms);
+        }
     return check_launch(who);
 }
 

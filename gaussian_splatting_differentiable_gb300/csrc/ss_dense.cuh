@@ -223,7 +223,6 @@ __device__ __forceinline__ void put(const DenseArgs &a, int split, int i, int j,
 }
 
 // For weights past one tile (ss_dense_big.cu).
-bool dense_is_big(int32_t N, int32_t D);
 size_t dense_big_workspace(int64_t n, int32_t N, int32_t D, int dtype, int gdt);
 ss_status dense_big(const char *who, DenseArgs a, int dtype, int format, void *workspace, cudaStream_t s, int sms);
 // Adds up a.part and a.part_bias into the results, where they are there.

@@ -430,8 +430,6 @@ ss_status run(const char *who, DenseArgs a, const Plan &p, uint8_t *ws, cudaStre
 
 }  // namespace
 
-bool dense_is_big(int32_t N, int32_t D) { return N > 128 || D > 128; }
-
 size_t dense_big_workspace(int64_t n, int32_t N, int32_t D, int dtype, int gdt) {
     return plan_of(n, N, D, dtype, gdt).bytes;
 }

@@ -148,7 +148,9 @@ def test_range_ends(ss, N):
     (1700000, 16, 24, "f16", "f32"), (300000, 100, 128, "bf16", "f32"), (100000, 60, 128, "f32", "f32"),
     (9000, 2500, 2300, "bf16", "f32"), (300000, 200, 200, "f32", "f32"), (7000, 2000, 2100, "f32", "f32"),
     (18000, 2400, 2500, "bf16", "bf16"), (20000, 1700, 1800, "f16", "f16"),
-    (270000, 200, 200, "bf16", "f32"), (270000, 200, 216, "bf16", "bf16")])
+    (270000, 200, 200, "bf16", "f32"), (270000, 200, 216, "bf16", "bf16"),
+    (70000, 250, 48, "f32", "f32"), (70000, 40, 200, "f16", "f32"), (300000, 1000, 1, "f32", "f32"),
+    (280000, 3, 1021, "f16", "f16")])
 def test_long_sums(ss, n, N, D, t, gt):
     """Sums of many rows keep float32's accuracy, far below the bound that the number of
     rows gives.  The summands' signs are random: no partial sum is past 6 times their root sum of
@@ -175,6 +177,38 @@ def test_long_sums(ss, n, N, D, t, gt):
     wb = dy.double().sum(0)
     off = (m.grads["dbias"].double() - wb).abs() - u * wb.abs()
     assert float((off / dy.double().square().sum(0).sqrt()).max()) <= limit * (1 + u)
+
+
+@pytest.mark.parametrize("n,N,D,t,gt,pad", [
+    (65536, 256, 48, "f32", "f32", 0), (65541, 129, 33, "f32", "f32", 1), (98304, 7, 300, "f16", "f16", 8),
+    (131072, 500, 128, "f16", "f32", 3), (98311, 64, 257, "f32", "f32", 1)])
+def test_tiles_of_many_rows(ss, n, N, D, t, gt, pad):
+    """A weight that takes one tile after another has each tile's own bits, in place, and
+    nothing past the results and the workspace is written."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(n)
+    dy = torch.randn(n, N + pad, generator=g, device="cuda").to(dtype(t))[:, :N]
+    x = torch.randn(n, D, generator=g, device="cuda")
+    r = ss.Rows8(n, D).pack(x)
+    need = ss.ss_dense_grad8_workspace_bytes(n, N, D, dtype(t), dtype(gt))
+    room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    buf = torch.full((N, D + pad), -7.0, dtype=dtype(gt), device="cuda")
+    db = torch.full((N + 64,), -7.0, dtype=dtype(gt), device="cuda")
+    dw = buf[:, :D]
+    ss.ss_dense_grad8(dy, r, dw, db[:N], room[:need])
+    assert (room[need:] == 0xA5).all() and (buf[:, D:] == -7.0).all() and (db[N:] == -7.0).all()
+    for i in range(0, N, 128):
+        for j in range(0, D, 128):
+            part = x[:, j:j + 128].contiguous()
+            m = ss.DenseGrad(n, min(128, N - i), part.shape[1], dtype=dtype(t), grad_dtype=dtype(gt))
+            m.backward(dy[:, i:i + 128], ss.Rows8(n, part.shape[1]).pack(part))
+            assert torch.equal(m.grads["dweight"], dw[i:i + 128, j:j + 128])
+            # the bias is the first tile's of a row; tiles of other widths may add its
+            # rows up in ranges of another length (of whole stages of 64 rows, or of 32)
+            assert j > 0 or torch.equal(m.grads["dbias"], db[i:min(i + 128, N)])
+    dw.fill_(3.0)
+    ss.ss_dense_grad8(dy, r, dw, None, room[:need])
+    assert torch.equal(m.grads["dweight"], dw[i:, j:]) and (db[N:] == -7.0).all()
 
 
 @pytest.mark.parametrize("t", ["bf16", "f32"])
