@@ -25,7 +25,8 @@
 extern "C" {
 #endif
 
-/* Bytes of workspace ss_dense_grad8 needs; 0 for sizes or types outside the limits. */
+/* Bytes of workspace ss_dense_grad8 needs for these sizes (fewer rows may need more);
+ * 0 for sizes or types outside the limits. */
 size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D, ss_dtype dtype,
                                       ss_dtype grad_dtype);
 
