@@ -132,17 +132,20 @@ __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
 }
 // x in bfloat16, every step exact.  SS_E4M3: the byte's exponent and mantissa in a bfloat16's places are
 // the value times 2^-120, subnormals too, which the scale makes good (in two factors where one
-// would be past bfloat16's range).  SS_INT8: the byte's lower seven bits as 128 .. 255, less 128, or
+// would be past bfloat16's range); the format's NaN, seven ones, would be 480 so, and is put in afterwards, where a
+// carry into bit 7 shows that there is one.  SS_INT8: the byte's lower seven bits as 128 .. 255, less 128, or
 // 256 with the sign bit.
 template <int FMT>
 __device__ __forceinline__ void convert(uint32_t (&out)[8], const Wide &h) {
-    uint32_t factor, more = 0;
+    uint32_t factor, more = 0, carries = 0;
     if (FMT == SS_INT8) {
         factor = h.e == kNanExponent ? 0x7fffu : (h.e == 0 ? 0x40u : h.e << 7);
     } else {
         const uint32_t e = h.e + 120u;
         factor = e > 254u ? 254u << 7 : e << 7;
         if (e > 254u) more = h.e == kNanExponent ? 0x7fffu : (e - 127u) << 7;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) carries |= (h.w[i] & 0x7f7f7f7fu) + 0x01010101u;
     }
     factor |= factor << 16, more |= more << 16;
 #pragma unroll
@@ -160,6 +163,13 @@ __device__ __forceinline__ void convert(uint32_t (&out)[8], const Wide &h) {
     if (FMT == SS_E4M3 && more)
 #pragma unroll
         for (int i = 0; i < 8; ++i) out[i] = times(out[i], more);
+    if (FMT == SS_E4M3 && (carries & 0x80808080u))
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t c = ((h.w[i / 2] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            const uint32_t x = __byte_perm(c, 0u, i & 1 ? 0x3424 : 0x1404);    // 0x8000 in the NaNs' places
+            out[i] |= x - (x >> 9);
+        }
 }
 
 // 8 sums of a row of the tile (`count` of them the weight's) to float32 values at p, added to

@@ -11,6 +11,8 @@
  *       floats with 4 exponent bits and 3 of mantissa (1 sign; no infinities)
  * A group that holds an infinity or a NaN has e = 255 and q = 0, and reads as
  * NaN throughout.
+ * Rows that were not packed are read by the same formula: any q (-128 and the
+ * 8-bit floats' NaN, 0x7f and 0xff, too) times 2^(e - 127), NaN where e = 255.
  *
  * A division by a power of two is exact, so an element is rounded once:
  * |q s - x| <= s / 2 (SS_INT8), or the larger of |x| 2^-4 and s 2^-10
