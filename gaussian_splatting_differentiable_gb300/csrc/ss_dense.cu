@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
                     for (int k = 0; k < 8; ++k) {
                         float t = s[i * kPitch + c + k];
 #pragma unroll
-                        for (int p = 1; p < C::kParts; ++p) t += s[(p * 64 + i) * kPitch + c + k];
+                        for (int p = 1; p < C::kParts; ++p) t = joined(t, s[(p * 64 + i) * kPitch + c + k]);
                         v[k] = __float_as_uint(t);
                     }
                     put(a, blockIdx.x, i, c0 + c, nj - c0 - c < 8 ? nj - c0 - c : 8, v, true, true);
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
                     uint32_t w[8];
                     tensor_load8(w, tensor + (uint32_t(quarter * 32) << 16) + TJ + c);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
+                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(joined(__uint_as_float(v[k]), __uint_as_float(w[k])));
                 }
                 checked(v);
                 if (i < ni) put(a, blockIdx.x, i, c, nj - c < 8 ? nj - c : 8, v, true, true);

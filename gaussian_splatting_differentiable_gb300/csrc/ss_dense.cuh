@@ -172,6 +172,11 @@ __device__ __forceinline__ void convert(uint32_t (&out)[8], const Wide &h) {
         }
 }
 
+// A sum of products with dy's hi and those with its rests together.  A rest that is 0 makes NaN of an infinite x,
+// where dy x is infinite; hi, which is 0, infinite or NaN where dy is (below 2^-133 it is 0), has it right, and
+// whatever its sum reads as that is not finite, dW does too.
+__device__ __forceinline__ float joined(float hi, float rests) { return isfinite(hi) ? hi + rests : hi; }
+
 // 8 sums of a row of the tile (`count` of them the weight's) to float32 values at p, added to
 // what is there or in its place.  No other thread has these, and a thread's additions to one
 // address come in its own order, so the sum's order is fixed, and nobody waits for what was there.

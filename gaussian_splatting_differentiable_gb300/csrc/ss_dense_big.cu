@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
                             tensor_load8(w, at + C::kTJ);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
+                                v[k] = __float_as_uint(joined(__uint_as_float(v[k]), __uint_as_float(w[k])));
                         }
                         if (stages == 0 || failed)      // a wait that ran out leaves NaN
 #pragma unroll

@@ -53,7 +53,7 @@ def test_the_formats_nan_reads_as_nan(ss, t, N, D, pad):
 
 
 @pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("scale", [16, 1, 0, 150])
+@pytest.mark.parametrize("scale", [16, 1, 0, 150, 254])
 def test_every_e4m3_byte_reads_as_its_value(ss, t, scale):
     """One row against dy = 1: the gradient is x, each of the 256 bytes at the ends of the
     scales too (zero where a product is below float32's least normal: sums may lose that)."""
@@ -70,3 +70,32 @@ def test_every_e4m3_byte_reads_as_its_value(ss, t, scale):
     for i in range(3):
         assert np.array_equal(got[i][normal], want[normal], equal_nan=True)
         assert (np.abs(got[i][~normal].astype(np.float64) - want[~normal]) < 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("N,D,pad", SHAPES)
+@pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
+def test_rows_that_read_as_infinities(ss, t, N, D, pad, fmt):
+    """Values at float32's end are rounded past it.  An infinity times dy is one of the product's
+    sign, whether dy has 1, 8 or more significant bits, and NaN where dy is 0 or two meet."""
+    import torch
+    n, big = 90, float(np.finfo(np.float32).max)
+    v = torch.ones(n, D, device="cuda")
+    v[3, 10], v[3, 33], v[60, 5], v[60, 33] = big, big, -big, -big
+    x = ss.Rows8(n, D, torch_format(fmt)).pack(v)
+    dy = torch.full((n, N + pad), 0.75, device="cuda").to(dtype(t))[:, :N]
+    values = [1.0, -1.0, 1.0 + 2.0 ** -7, -1.25 - 2.0 ** -10, 2.0 ** -14, 1.0 + 2.0 ** -20, 0.0, -0.0, 3.0 + 2.0 ** -15]
+    for k, d in enumerate(values):
+        dy[3, k] = d
+        dy[60, k + 11] = d
+    held = f64(x.unpack(torch.empty(n, D, device="cuda")))
+    assert held[3, 10] == np.inf and held[3, 33] == np.inf and held[60, 5] == -np.inf and held[60, 33] == -np.inf
+    got = gradient(ss, dy, x).double().numpy()
+    d64 = f64(dy)
+    with np.errstate(invalid="ignore"):
+        terms = d64[:, :, None] * held[:, None, :]
+        want = terms.sum(0)
+    special = ~np.isfinite(want)
+    assert special.any() and np.isnan(want).any() and np.array_equal(got[special], want[special], equal_nan=True)
+    tol = 2 * (n + 16) * U32 * np.abs(terms).sum(0)[~special] + (U[t] if t != "f32" else 0.0) * np.abs(want[~special])
+    assert (np.abs(got[~special] - want[~special]) <= tol).all()
