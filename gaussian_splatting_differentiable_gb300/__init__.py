@@ -995,6 +995,14 @@ def ss_dense_grad8(dy, x, dweight, dbias, workspace, stream=None) -> None:
         _check(st, "ss_dense_grad8")
 
 
+def ss_test_dense_wait_timeout(dy, x, dweight, dbias, workspace, stream=None) -> None:
+    """ss_dense_grad8 with waits that run out (tests)."""
+    _check(_L.ss_test_dense_wait_timeout(
+        dy.data_ptr(), _dtype(dy, "dy"), dy.stride(0), x.c, dy.shape[0], dy.shape[1], x.D,
+        dweight.data_ptr(), dweight.stride(0), dbias.data_ptr(), DTYPE_CODES[dweight.dtype],
+        *_scratch(workspace), _stream(stream)), "ss_test_dense_wait_timeout")
+
+
 class DenseGrad:
     """Buffers of the weight gradient of a dense layer y = x W^T + b over n rows,
     W [N, D], whose input was kept in 8 bits: `grads` (dweight [N, D], dbias [N]

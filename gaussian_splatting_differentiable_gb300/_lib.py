@@ -143,6 +143,8 @@ ROWS8_PROTOTYPES = {
                                           P, SZ, P]),
     "ss_dense_grad8_workspace_bytes": (SZ, [I64, I32, I32, I32, I32]),
     "ss_dense_grad8": (ctypes.c_int, [P, I32, I64, R8, I64, I32, I32, P, I64, P, I32, P, SZ, P]),
+    "ss_test_dense_wait_timeout": (ctypes.c_int, [P, I32, I64, R8, I64, I32, I32, P, I64, P, I32, P,
+                                                  SZ, P]),
 }
 
 _lib = None

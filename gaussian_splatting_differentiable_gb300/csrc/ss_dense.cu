@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cstdint>
 #include <type_traits>
 
@@ -266,10 +267,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
         bool ok = true;
         for (int stage = 0; stage < stages; ++stage) {
             if (FAST) {
-                if (!barrier_wait(&s_raw_full[raw_slot], raw_parity)) {
-                    ok = false;
-                    break;
-                }
+                ok &= barrier_wait(&s_raw_full[raw_slot], raw_parity, a.tries);
                 const uint8_t *from = raw_ring + raw_slot * raw.bytes;
                 if (!kCopies) {
 #pragma unroll
@@ -288,7 +286,9 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
                 for (int k = 0; k < C::kTurnsB; ++k)
                     if (tb.has(k, C::kRows)) load_words(rb[k].w, from + (tb.row + k * tb.rows) * raw.x_pitch + tb.piece * kWide);
             }
-            if (!barrier_wait(&s_empty[slot], parity)) {
+            // a warp's lanes go on together, or leave
+            ok &= barrier_wait(&s_empty[slot], parity, a.tries);
+            if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
@@ -311,9 +311,9 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
                 }
             if constexpr (kCopies)
                 if (bias) {       // the copy engine's rows, before the slot may be filled again
-                    if (!barrier_wait(&s_copied[slot], parity ^ 1)) {
+                    if (!barrier_wait(&s_copied[slot], parity ^ 1, a.tries)) {
                         ok = false;
-                        break;
+                        s_failed = 1;
                     }
 #pragma unroll
                     for (int k = 0; k < C::kTurnsA; ++k)
@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
             if (++slot == C::kStages) slot = 0, parity ^= 1;
             if (++raw_slot == C::kRawStages) raw_slot = 0, raw_parity ^= 1;
         }
-        if (!ok || !barrier_wait(&s_done, 0)) s_failed = 1;
+        if (!barrier_wait(&s_done, 0, a.tries) || !ok) s_failed = 1;
+        __syncwarp();
         tensor_fence_after();
         drain();
         tensor_fence_before();
@@ -342,8 +343,9 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
             int slot = 0;
             uint32_t parity = 0;
             for (int stage = 0; stage < stages; ++stage) {
-                if (!barrier_wait(&s_full[slot], parity) || (kCopies && !barrier_wait(&s_copied[slot], parity))) {
+                if (!barrier_wait(&s_full[slot], parity, a.tries) || (kCopies && !barrier_wait(&s_copied[slot], parity, a.tries))) {
                     s_failed = 1;
+                    __threadfence_block();      // before those that wait for s_done look at it
                     break;
                 }
                 tensor_fence_after();
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
             }
             products_arrive(&s_done);
-            if (!barrier_wait(&s_done, 0)) s_failed = 1;    // the tensor memory is freed after them
+            if (!barrier_wait(&s_done, 0, a.tries)) s_failed = 1;    // the tensor memory is freed after them
         }
         __syncwarp();
     } else {
@@ -370,9 +372,9 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
             const uint32_t raw_at = ring + C::kStages * C::kStageBytes;
             int slot = 0, raw_slot = 0, stage = 0, copied = 0;
             uint32_t parity = 1, raw_parity = 1;
-            for (; stage < stages; ++stage) {
+            for (; stage < stages && stage < a.sent; ++stage) {
                 const int row = int(first + int64_t(stage) * C::kRows);
-                if (!barrier_wait(&s_raw_empty[raw_slot], raw_parity)) {
+                if (!barrier_wait(&s_raw_empty[raw_slot], raw_parity, a.tries)) {
                     s_failed = 1;
                     break;
                 }
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
                 copy_box(to, &x_map, 0, row, &s_raw_full[raw_slot]);
                 if (++raw_slot == C::kRawStages) raw_slot = 0, raw_parity ^= 1;
                 if (kCopies) {
-                    if (!barrier_wait(&s_empty[slot], parity)) {
+                    if (!barrier_wait(&s_empty[slot], parity, a.tries)) {
                         s_failed = 1;
                         ++stage;
                         break;
@@ -399,9 +401,9 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
             }
             // every copy has come before the block ends
             for (int k = copied < C::kStages ? copied : C::kStages; k > 0; --k)
-                if (!barrier_wait(&s_copied[(copied - k) % C::kStages], (copied - k) / C::kStages & 1)) s_failed = 1;
+                if (!barrier_wait(&s_copied[(copied - k) % C::kStages], (copied - k) / C::kStages & 1, a.tries)) s_failed = 1;
             for (int k = stage < C::kRawStages ? stage : C::kRawStages; k > 0; --k)
-                if (!barrier_wait(&s_raw_full[(stage - k) % C::kRawStages], (stage - k) / C::kRawStages & 1)) s_failed = 1;
+                if (!barrier_wait(&s_raw_full[(stage - k) % C::kRawStages], (stage - k) / C::kRawStages & 1, a.tries)) s_failed = 1;
         }
         __syncwarp();
     }
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(Config<T, TI, TJ, ROWS>::kThreads, Config<T, T
         for (int j = threadIdx.x; j < ni; j += C::kThreads) {
             float t = 0.0f;
             for (int r = 0; r < ta.rows && r < C::kRows; ++r) t += s[size_t(r) * width + j];
+            if (s_failed) t = __uint_as_float(0x7fffffffu);
             if (a.splits > 1)
                 a.part_bias[size_t(blockIdx.x) * a.N + j] = t;
             else
@@ -579,19 +582,10 @@ void dense_join(const DenseArgs &a, bool weight, cudaStream_t s, int sms) {
 
 using namespace ss;
 
-extern "C" {
-
-size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D, ss_dtype dtype, ss_dtype grad_dtype) {
-    if (!dense_sizes_ok(n, N, D) || !dtype_known(dtype) || (grad_dtype != SS_F32 && grad_dtype != dtype)) return 0;
-    if (dense_is_big(n, N, D, dtype)) return dense_big_workspace(n, N, D, dtype, grad_dtype);
-    return tile_workspace(splits_of(n, grad_dtype), N, D);
-}
-
-ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n, int32_t N,
-                         int32_t D, void *dweight, int64_t dweight_stride, void *dbias, ss_dtype grad_dtype,
-                         void *workspace, size_t workspace_bytes, ss_stream_t stream) {
+static ss_status dense_grad8(const char *who, const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n,
+                          int32_t N, int32_t D, void *dweight, int64_t dweight_stride, void *dbias, ss_dtype grad_dtype,
+                          void *workspace, size_t workspace_bytes, uint32_t tries, int sent, ss_stream_t stream) {
     clear_error();
-    const char *who = "ss_dense_grad8";
     if (!dense_sizes_ok(n, N, D))
         return fail(SS_ERR_UNSUPPORTED, "%s: %lld rows, %d x %d outside 0..2^31-1, 1..%d", who, (long long)n, N, D,
                     kMaxWidth);
@@ -606,10 +600,10 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
     if ((st = check_workspace(who, workspace, workspace_bytes, ss_dense_grad8_workspace_bytes(n, N, D, dtype, grad_dtype))) != SS_OK)
         return st;
     int dev = 0, sms = 0;
-    if ((st = current_device(&dev, &sms, "ss_dense_grad8: device query")) != SS_OK) return st;
+    if ((st = current_device(&dev, &sms, who)) != SS_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     DenseArgs a{dy, dy_stride, rows8_of(x), n, N, D, 1, 1, 0, nullptr, nullptr, dweight, dweight_stride, dbias,
-                int(grad_dtype)};
+                int(grad_dtype), tries, sent};
     const int format = x ? x->format : SS_INT8;
     if (dense_is_big(n, N, D, dtype)) {
         st = dense_big(who, a, dtype, format, workspace, s, sms);
@@ -635,6 +629,30 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
             if (t.splits > 1) dense_join(t, true, s, sms);
         }
     return check_launch(who);
+}
+
+extern "C" {
+
+size_t ss_dense_grad8_workspace_bytes(int64_t n, int32_t N, int32_t D, ss_dtype dtype, ss_dtype grad_dtype) {
+    if (!dense_sizes_ok(n, N, D) || !dtype_known(dtype) || (grad_dtype != SS_F32 && grad_dtype != dtype)) return 0;
+    if (dense_is_big(n, N, D, dtype)) return dense_big_workspace(n, N, D, dtype, grad_dtype);
+    return tile_workspace(splits_of(n, grad_dtype), N, D);
+}
+
+ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n, int32_t N,
+                         int32_t D, void *dweight, int64_t dweight_stride, void *dbias, ss_dtype grad_dtype,
+                         void *workspace, size_t workspace_bytes, ss_stream_t stream) {
+    return dense_grad8("ss_dense_grad8", dy, dtype, dy_stride, x, n, N, D, dweight, dweight_stride, dbias, grad_dtype,
+                       workspace, workspace_bytes, kWaitTries, INT_MAX, stream);
+}
+
+// A test's: nothing else differs from ss_dense_grad8.  Each wait ends after 4096 tries; the copies that have
+// been issued are waited for and the tensor memory is given back as ever.
+ss_status ss_test_dense_wait_timeout(const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n,
+                                     int32_t N, int32_t D, void *dweight, int64_t dweight_stride, void *dbias,
+                                     ss_dtype grad_dtype, void *workspace, size_t workspace_bytes, ss_stream_t stream) {
+    return dense_grad8("ss_test_dense_wait_timeout", dy, dtype, dy_stride, x, n, N, D, dweight, dweight_stride, dbias,
+                       grad_dtype, workspace, workspace_bytes, 4096, 1, stream);
 }
 
 }  // extern "C"

@@ -44,6 +44,8 @@ struct DenseArgs {
     int64_t dws;
     void *db;
     int gdt;
+    uint32_t tries;       // of a wait, after which it has run out
+    int sent;             // stages that the copies stop after (a test's: none for all others)
 };
 
 // A bfloat16 holds the upper half of a float32's bits; what is left of the value is exact.

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
                 // warp w rows w, w + 8, ... of a stage, lane l columns 8 l to 8 l + 7
                 const int stop = (chain + 1) * a.chain < stages ? (chain + 1) * a.chain : stages;
                 for (int stage = chain * a.chain; stage < stop; ++stage) {
-                    if (!barrier_wait(&s_full[slot], parity)) {
+                    if (!warp_wait(&s_full[slot], parity, a.tries)) {
                         s_failed = 1;
                         break;
                     }
@@ -207,10 +207,11 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
                     if (++slot == C::kStages) slot = 0, parity ^= 1;
                 }
             }
-            if (!barrier_wait(&s_done, chain & 1)) s_failed = 1;
+            if (!barrier_wait(&s_done, chain & 1, a.tries)) s_failed = 1;
             tensor_fence_after();
-            const bool begins = b.first && chain == 0, ends = b.last && chain == chains - 1;
-            const bool failed = *static_cast<volatile uint32_t *>(&s_failed) != 0;
+            // a wait that ran out leaves NaN, and no other chain is waited for
+            const bool failed = __any_sync(0xffffffffu, *static_cast<volatile uint32_t *>(&s_failed) != 0);
+            const bool begins = b.first && chain == 0, ends = b.last && (failed || chain == chains - 1);
             // a warp reads the 32 lanes (rows of dW) of its quarter, the two warps of a quarter 8
             // columns in turn
             const int quarter = warp & 3;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
                             for (int k = 0; k < 8; ++k)
                                 v[k] = __float_as_uint(joined(__uint_as_float(v[k]), __uint_as_float(w[k])));
                         }
-                        if (stages == 0 || failed)      // a wait that ran out leaves NaN
+                        if (stages == 0 || failed)
 #pragma unroll
                             for (int k = 0; k < 8; ++k) v[k] = failed ? 0x7fffffffu : 0u;
                         if (i < a.N) put(a, blockIdx.x, i, j0 + c, nj - c < 8 ? nj - c : 8, v, begins, ends);
@@ -240,15 +241,18 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
             tensor_fence_before();
             __syncwarp();
             if (lane == 0) barrier_arrive(&s_drained);
+            if (failed) break;
         }
     } else if (warp == 8) {
         if (lane == 0) {
             const uint32_t what = product_of((nj + 15) / 16 * 16);
             int slot = 0, chains = 0, link = 0;
             uint32_t parity = 0;
+            bool told = false;         // s_done of this chain
             for (int stage = 0; stage < stages; ++stage) {
-                if (!barrier_wait(&s_full[slot], parity)) {
+                if (!barrier_wait(&s_full[slot], parity, a.tries)) {
                     s_failed = 1;
+                    __threadfence_block();      // before those that wait for s_done look at it
                     break;
                 }
                 tensor_fence_after();
@@ -267,16 +271,17 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
                 if (++link == a.chain && stage + 1 < stages) {
                     products_arrive(&s_done);
-                    if (!barrier_wait(&s_drained, chains & 1)) {
+                    if (!barrier_wait(&s_drained, chains & 1, a.tries)) {
                         s_failed = 1;
+                        told = true;
                         break;
                     }
                     link = 0, ++chains;
                     tensor_fence_after();
                 }
             }
-            products_arrive(&s_done);
-            if (!barrier_wait(&s_done, chains & 1)) s_failed = 1;    // the tensor memory is freed after them
+            if (!told) products_arrive(&s_done);
+            if (!barrier_wait(&s_done, chains & 1, a.tries)) s_failed = 1;    // the tensor memory is freed after them
         }
         __syncwarp();
     } else {
@@ -284,8 +289,8 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
             const int a_boxes = (ni + 63) / 64, b_boxes = (nj + 63) / 64;
             int slot = 0, stage = 0;
             uint32_t parity = 1;
-            for (; stage < stages; ++stage) {
-                if (!barrier_wait(&s_empty[slot], parity)) {
+            for (; stage < stages && stage < a.sent; ++stage) {
+                if (!barrier_wait(&s_empty[slot], parity, a.tries)) {
                     s_failed = 1;
                     break;
                 }
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(Big<PARTS>::kThreads, 1)
             }
             // every copy has come before the block ends
             for (int k = stage < C::kStages ? stage : C::kStages; k > 0; --k)
-                if (!barrier_wait(&s_full[(stage - k) % C::kStages], (stage - k) / C::kStages & 1)) s_failed = 1;
+                if (!barrier_wait(&s_full[(stage - k) % C::kStages], (stage - k) / C::kStages & 1, a.tries)) s_failed = 1;
         }
         __syncwarp();
     }

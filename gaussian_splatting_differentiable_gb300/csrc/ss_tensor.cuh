@@ -19,16 +19,23 @@ __device__ __forceinline__ void barrier_init(uint64_t *b, uint32_t count) {
 __device__ __forceinline__ void barrier_arrive(uint64_t *b) {
     asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(smem_of(b)) : "memory");
 }
-// Waits for the phase of that parity to end; false after a million tries, each of which may
+// Waits for the phase of that parity to end; false after so many tries, each of which may
 // itself wait: something has gone wrong then.
-__device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity) {
-    for (uint32_t k = 0; k < (1u << 20); ++k) {
-        uint32_t done;
-        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-                     : "=r"(done) : "r"(smem_of(b)), "r"(parity) : "memory");
-        if (done) return true;
-    }
-    return false;
+constexpr uint32_t kWaitTries = 1u << 20;
+__device__ __forceinline__ bool barrier_try(uint64_t *b, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done) : "r"(smem_of(b)), "r"(parity) : "memory");
+    return done;
+}
+__device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity, uint32_t tries) {
+    while (!barrier_try(b, parity))
+        if (--tries == 0) return false;
+    return true;
+}
+// The same by a whole warp, with one answer for all of its lanes: they go on together.
+__device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, uint32_t tries) {
+    return __all_sync(0xffffffffu, barrier_wait(b, parity, tries));
 }
 __device__ __forceinline__ void writes_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

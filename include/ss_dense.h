@@ -11,7 +11,8 @@
  * off what float32's last place does not hold, and rounded to nearest from there on.  The rows
  * are split by the sizes, the types and the alignment: with those the same, the same
  * inputs give the same bits.  (Scales below 2^-111, which packing does not make, may leave x
- * bfloat16's subnormals.)  Should one of the kernels' waits run out, dweight reads NaN.
+ * bfloat16's subnormals.)  Should one of the kernels' waits run out, dweight and
+ * dbias read NaN where it was, which nothing else tells of.
  *
  * Conventions are those of ss.h; rows and strides those of ss_embed.h.
  */
@@ -42,6 +43,16 @@ ss_status ss_dense_grad8(const void *dy, ss_dtype dtype, int64_t dy_stride, cons
                          int64_t n, int32_t N, int32_t D, void *dweight, int64_t dweight_stride,
                          void *dbias, ss_dtype grad_dtype, void *workspace,
                          size_t workspace_bytes, ss_stream_t stream);
+
+/* Test hook for failure detection, not part of the path: ss_dense_grad8 with copies
+ * that stop after the first stage of each range of rows (32 or 64 of them), so that the waits
+ * for the next one give up, after a few thousand tries; rows that no copies bring (dy or x
+ * off 16-byte boundaries, in weights of one tile) are worked on as ever. */
+ss_status ss_test_dense_wait_timeout(const void *dy, ss_dtype dtype, int64_t dy_stride,
+                                     const ss_rows8 *x, int64_t n, int32_t N, int32_t D,
+                                     void *dweight, int64_t dweight_stride, void *dbias,
+                                     ss_dtype grad_dtype, void *workspace, size_t workspace_bytes,
+                                     ss_stream_t stream);
 
 #ifdef __cplusplus
 }
