@@ -573,6 +573,10 @@ def ss_layer_norm_workspace_bytes(n: int, D: int) -> int:
     return int(_L.ss_layer_norm_workspace_bytes(n, D))
 
 
+def ss_layer_norm_bwd8_workspace_bytes(n: int, D: int) -> int:
+    return int(_L.ss_layer_norm_bwd8_workspace_bytes(n, D))
+
+
 def _param(t, name: str, D: int, code: int, dtype) -> tuple:
     """(pointer, type code) of a parameter vector of the rows' type or float32."""
     p = _vector(t, name, D)
@@ -637,6 +641,11 @@ def ss_layer_norm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace,
         _check(st, "ss_layer_norm_bwd")
 
 
+def _layer_norm_scratch(n: int, D: int) -> int:
+    """Bytes that serve both of LayerNorm's backward calls, 0 for sizes out of range."""
+    return max(ss_layer_norm_workspace_bytes(n, D), ss_layer_norm_bwd8_workspace_bytes(n, D))
+
+
 class LayerNorm:
     """Buffers of the layer norm of n rows of D values: `y`, `mean`, `rstd`
     of the forward, `dx` and `grads` (dgamma, dbeta) of the backward.  They
@@ -658,7 +667,7 @@ class LayerNorm:
             self._mean = torch.empty(n, dtype=torch.float32, device=d)
             self._rstd = torch.empty(n, dtype=torch.float32, device=d)
         if backward:
-            nb = ss_layer_norm_workspace_bytes(n, D)
+            nb = _layer_norm_scratch(n, D)
             if nb == 0:
                 raise ValueError("sizes out of range")
             self._dx = torch.empty(n, D, dtype=dtype, device=d)
