@@ -5,11 +5,15 @@
 // as they lie, 64 columns (128 bytes) to a row of a swizzled 8-row atom of 1 KB.
 // x becomes bfloat16 on the way, which holds it exactly.  dy is one bfloat16, or is cut into
 // as many as hold it exactly: hi, mid and lo of a float32's 24 bits, hi and lo of
-// a float16's 11.  The tensor cores cut every addition off at float32's last place, towards
-// zero, so a long chain of them loses a little of each sum: after 2048 rows 5e-7 of it, after 4096
-// 1.2e-6.  So the products of mid and lo have sums of their own (with hi's they would cut those off
-// three times as often), and no sum stays in the tensor memory for more than a chain of rows,
-// kChain32 where dW is float32; what it held then is added in float32.
+// a float16's 11.  The tensor cores add a step's 16 products to a sum and cut it off at float32's last place, towards
+// zero, so a long chain of steps loses a little of each sum: of summands of one sign and of many exponents 3.0e-6 after
+// 2048 rows, in step with their number (of a few bits 1.7e-6 after 2048, 2.5e-6 after 2816, 7.6e-6 after 5632), of
+// random signs 4.8e-7 after 2048 and 1.2e-6 after 4096; a float32 product by PyTorch is off by 1.0e-6 at most, to either
+// side.  So the products of mid and lo have sums of their own (with hi's they would cut those off three times as
+// often), and no sum stays in the tensor memory for more than a chain of rows, kChain32 where dW is float32; what it held
+// then is added in float32.  That takes time: 150 us for 145 with chains of 2816 rows (2M x 48 x 48 float32), 249 for
+// 228 (8191 x 4096 x 4096 bfloat16 into float32).  Where dW has 16 bits, chains of kChain16 lose up to 2.4e-5, which
+// the rounding to 16 bits hides but for one value in several hundred that lies next to a border.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -24,7 +28,7 @@ namespace ss {
 
 constexpr int kStep = 16;              // rows of one product
 constexpr int kWide = 16;              // columns of x that a thread converts at a time
-constexpr int kChain32 = 2816, kChain16 = 16384;    // rows of a chain; dW in float32, in 16 bits
+constexpr int kChain32 = 2048, kChain16 = 16384;    // rows of a chain; dW in float32, in 16 bits
 constexpr int kSms = 152;
 
 template <typename T>

@@ -7,7 +7,7 @@
  * x[m][j] is q s as it is held.  Every product is exact (x in bfloat16, dy as the sum of one,
  * two or three bfloat16 values, which float16 and float32 values are but for what a float32 has
  * below 2^-133, which is left out), infinite and NaN where dy x is; sums are float32,
- * in the tensor cores for up to 2816 rows (16,384 where dweight has 16 bits), which cut
+ * in the tensor cores for up to 2048 rows (16,384 where dweight has 16 bits), which cut
  * off what float32's last place does not hold, and rounded to nearest from there on.  The rows
  * are split by the sizes, the types and the alignment: with those the same, the same
  * inputs give the same bits.  (Scales below 2^-111, which packing does not make, may leave x
