@@ -9,8 +9,9 @@ rasterizes the splats, compares the image with a target (L1 + SSIM), sends the
 gradients all the way back (rasterizer, projection, layer norm, table), clips
 the gradients of everything that is learned by their common norm, and moves
 against them.  With --keep, what the norm's backward pass needs of its input is
-kept in 8 bits from the forward on.  The target is the same scene with colours of
-its own; all data is synthetic.
+kept in 8 bits from the forward on, as layers in between would have it; the lookup's
+rows are a buffer of its own and stay, so this one norm saves no memory by it.  The target is
+the same scene with colours of its own; all data is synthetic.
 """
 from __future__ import annotations
 

@@ -874,11 +874,17 @@ class RMSNorm:
     (int8 or float8_e4m3fn), the Rows8 `out`; the Rows8 `kept` (the sum, or x, in 8
     bits) where `keep` names one; `rstd`.  The backward's: `dx` and `grads`
     (dgamma).  They belong to one stream at a time, as Embedding's do.  param_dtype
-    is that of gamma and its gradient."""
+    is that of gamma and its gradient.
+
+    inplace=True, for the layers of a stack: the forward writes the sum over the
+    residual's rows, the backward writes dx over dsum's (over dy's where there is
+    no dsum), and the object has neither `sum` nor `dx`.  With `keep` and `out` a
+    layer then holds its rows in 8 bits alone."""
 
     def __init__(self, n: int, D: int, eps: float = 1e-5, dtype=torch.float32,
                  param_dtype=torch.float32, device="cuda", forward: bool = True,
-                 backward: bool = True, residual: bool = False, out=None, keep=None):
+                 backward: bool = True, residual: bool = False, out=None, keep=None,
+                 inplace: bool = False):
         d = _device(device)
         self.n, self.D, self.eps = n, D, float(eps)
         self.dtype, self._code = dtype, _code(dtype, "dtype")
@@ -890,11 +896,12 @@ class RMSNorm:
             raise ValueError("sizes out of range")
         if not forward and (residual or out is not None or keep is not None):
             raise ValueError("residual, out and keep are the forward's")
-        self._forward, self._residual = forward, bool(residual)
+        self._forward, self._residual, self._backward = forward, bool(residual), backward
+        self._inplace = bool(inplace)
         self._sum = self._y = self._out = self._kept = self._rstd = None
         self._dx = self._workspace = self.grads = None
         if forward:
-            if residual:
+            if residual and not inplace:
                 self._sum = torch.empty(n, D, dtype=dtype, device=d)
             if out is None:
                 self._y = torch.empty(n, D, dtype=dtype, device=d)
@@ -904,7 +911,7 @@ class RMSNorm:
                 self._kept = Rows8(n, D, keep, d)
             self._rstd = torch.empty(n, dtype=torch.float32, device=d)
         if backward:
-            self._dx = torch.empty(n, D, dtype=dtype, device=d)
+            self._dx = None if inplace else torch.empty(n, D, dtype=dtype, device=d)
             self._dgamma = torch.empty(D, dtype=param_dtype, device=d)
             self.grads = {"dgamma": self._dgamma}
             self._workspace = _workspace(nb, d)
@@ -933,8 +940,9 @@ class RMSNorm:
         rp, rs = (None, 0) if residual is None else self._input(residual, "residual")
         gp = None if gamma is None else _vector(gamma, "gamma", D, self.param_dtype)
         h, y, o, k = self._sum, self._y, self._out, self._kept
+        hp, hs = (rp, rs) if h is None else (h.data_ptr(), D)
         st = _L.ss_rms_norm_fwd(xp, self._code, xs, rp, rs, self.n, D, gp, self._param_code,
-                                self.eps, None if h is None else h.data_ptr(), D,
+                                self.eps, hp, hs,
                                 None if y is None else y.data_ptr(), D,
                                 None if o is None else o._c, None if k is None else k._c,
                                 self._rstd.data_ptr(), _stream(stream))
@@ -946,10 +954,10 @@ class RMSNorm:
         """x: the forward's sum (x without a residual) as rows or as the Rows8 that
         keeps it, this object's own `kept` or else `sum` if not given; dsum: the
         gradient of the sum's other use, None for none; rstd: the forward's, this
-        object's own if not given."""
+        object's own if not given.  Returns dx (inplace: dsum, or dy)."""
         n, D = self.n, self.D
         dx, ws = self._dx, self._workspace
-        if dx is None:
+        if not self._backward:
             raise ValueError("this RMSNorm was made without backward=True")
         if x is None:
             x = self._sum if self._kept is None else self._kept
@@ -967,8 +975,14 @@ class RMSNorm:
         gp = None if gamma is None else _vector(gamma, "gamma", D, self.param_dtype)
         sp, ss_ = (None, 0) if dsum is None else self._input(dsum, "dsum")
         rp = self._rstd.data_ptr() if rstd is None else _vector(rstd, "rstd", n, torch.float32)
+        if dx is not None:
+            dxp, dxs = dx.data_ptr(), D
+        elif dsum is not None:
+            dx, dxp, dxs = dsum, sp, ss_
+        else:
+            dx, dxp, dxs = dy, dyp, dys
         st = _L.ss_rms_norm_bwd(dyp, dys, xp, xs, kp, self._code, n, D, gp, self._param_code, rp,
-                                sp, ss_, dx.data_ptr(), D, self._dgamma.data_ptr(), ws.data_ptr(),
+                                sp, ss_, dxp, dxs, self._dgamma.data_ptr(), ws.data_ptr(),
                                 ws.nbytes, _stream(stream))
         if st:
             _check(st, "ss_rms_norm_bwd")
