@@ -8,6 +8,7 @@
 
 #include "ss_internal.h"
 #include "ss_launch.cuh"
+#include "ss_norm.cuh"
 #include "ss_norm.h"
 #include "ss_profile.h"
 #include "ss_vec.cuh"
@@ -15,7 +16,7 @@
 namespace ss {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kNormThreads;
 constexpr int32_t kMaxD = 65536;
 
 // A row's place in the threads.  `lanes` threads share it, thread l of them
@@ -35,7 +36,6 @@ constexpr int32_t kMaxD = 65536;
 // step-th row with step a multiple of the period after which rows start
 // alike, so its columns stay fixed.
 constexpr int kPerThread = 16;       // elements of a row in one thread's vectors
-constexpr int kMaxRowThreads = 512;  // x 16 = the widest row held in registers
 constexpr int kMaxGroups = 8;        // of two warps at least
 
 struct Place {
@@ -54,43 +54,6 @@ struct Rows {
 
 // Rows ahead by what they take: 16 bytes a vector, thread and tensor.
 constexpr int stages_of(int vectors) { return vectors <= 2 ? 4 : 3; }
-
-__device__ __forceinline__ void copy16(void *smem, const void *gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(smem))), "l"(gmem)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Sums K values over the row's lanes; every lane gets the same sums (one
-// fixed order).  MULTI alternates two buffers, so one barrier a sum is enough;
-// their slots past the row's warps hold zeros.
-constexpr int kRowWarps = kMaxRowThreads / 32;
-template <int K, bool MULTI>
-__device__ __forceinline__ void row_sum(float (&v)[K], const Place &pl, int group, int lane,
-                                        float (*s_red)[K][kRowWarps], int &flip) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        if (MULTI || o < pl.lanes)
-#pragma unroll
-            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (!MULTI) return;
-    if ((lane & 31) == 0)
-#pragma unroll
-        for (int k = 0; k < K; ++k) s_red[flip][k][lane >> 5] = v[k];
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(pl.lanes) : "memory");
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const float4 *q = reinterpret_cast<const float4 *>(s_red[flip][k]);
-        v[k] = 0.0f;
-        for (int w = 0; w < pl.lanes; w += 128) {
-            const float4 t = q[w >> 7];
-            v[k] += (t.x + t.y) + (t.z + t.w);
-        }
-    }
-    flip ^= 1;
-}
 
 // Rounding of the mean.  1 / sqrt(var + eps) multiplies it: a row of one value
 // 1e4 and a mean one unit of its last place off give y = 0.3 for 0.
@@ -351,7 +314,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
             }
             pe += xstep;
         }
-        row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
+        row_sum<1, MULTI>(sum, pl.lanes, group, c.lane, s_red[MULTI ? group : 0], flip);
         float mu = kAgain ? sum[0] * inv : quotient(sum[0], width, inv);
         const F2 neg = both(-mu);
         acc = both(0.0f);
@@ -372,7 +335,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
                 ec[u] = col[u] >= 0 ? ec[u] - mu : 0.0f;
                 sum[0] = fmaf(ec[u], ec[u], sum[0]);
             }
-        row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
+        row_sum<1, MULTI>(sum, pl.lanes, group, c.lane, s_red[MULTI ? group : 0], flip);
         float v = fmaf(sum[0], inv, eps);
         const bool again = kAgain && far_off(mu, v);
         // (a row's lanes agree; and one branch for what few rows are)
@@ -388,7 +351,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(VE
             if (SHIFT)
 #pragma unroll
                 for (int u = 0; u < kX; ++u) sum[0] += ec[u];
-            row_sum<1, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
+            row_sum<1, MULTI>(sum, pl.lanes, group, c.lane, s_red[MULTI ? group : 0], flip);
             const float off = again ? sum[0] / width : 0.0f;    // (a product with 1 / D would leave a rounding)
             if (again) v = fmaxf(fmaf(-off, off, var), 0.0f) + eps;
             mu += off;
@@ -538,7 +501,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
         load(row + step);
         fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);   // the slots read one row ago
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        row_sum<2, MULTI>(sum, pl, group, c.lane, s_red[MULTI ? group : 0], flip);
+        row_sum<2, MULTI>(sum, pl.lanes, group, c.lane, s_red[MULTI ? group : 0], flip);
         if (row >= n) continue;
         const F2 ma = both(-sum[0] * inv), mah = both(-sum[1] * inv);
 #pragma unroll
@@ -613,41 +576,14 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, MULTI ? 1 :
     }
 }
 
-// The CTAs' partial sums of 32 columns of [dgamma | dbeta]: 32 slices of the
-// CTAs side by side, then the slices in order.  Its launch begins while
+// The CTAs' partial sums of 32 columns of [dgamma | dbeta].  Its launch begins while
 // k_norm_bwd ends; bound by latency.
 __global__ void __launch_bounds__(1024) k_norm_bwd_final(const float *part, int parts, int32_t D, void *dgamma,
                                                          void *dbeta, int pdt) {
-    __shared__ float s_t[32][33];
-    wait_for_previous();
-    const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
-    const int j = blockIdx.x * 32 + c;
-    float t = 0.0f;
-    if (j < 2 * D)
-#pragma unroll 4
-        for (int p = q; p < parts; p += 32) t += part[size_t(p) * 2 * D + j];
-    s_t[q][c] = t;
-    __syncthreads();
-    t = s_t[c][q];                         // column q of the 32, slice c
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const int col = blockIdx.x * 32 + q;
-    if (c == 0 && col < 2 * D) store_param(col < D ? dgamma : dbeta, pdt, col < D ? col : col - D, t);
+    add_up_parts(part, parts, D, 2 * D, dgamma, dbeta, pdt);
 }
 
 // ------------------------------------------------------------------ rows wider than the registers
-
-// Sum over the CTA, the same value in every thread (fixed order).
-__device__ __forceinline__ float block_sum(float v, float *s_red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.0f;
-    for (int w = 0; w < kThreads / 32; ++w) t += s_red[w];
-    return t;
-}
 
 // A CTA a row, which is read three times (the second and third from L1 or L2),
 // an element a thread: rows past too_wide() have work enough for
@@ -759,12 +695,6 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows_wide(const T *dy, in
     }
 }
 
-// Partial sums of the weights' gradients that the workspace has room for: at
-// most one for each row, and up to kMaxPeriod - 1 more where the grid is rounded up
-// to a multiple of the period of the rows' starts.
-constexpr int kMaxPeriod = 8, kMaxParts = 1024;
-int64_t weight_parts(int64_t n) { return n + kMaxPeriod < kMaxParts ? n + kMaxPeriod : kMaxParts; }
-
 int pow2_at_least(int v) {
     int p = 1;
     while (p < v) p <<= 1;
@@ -800,31 +730,10 @@ int period_of(int64_t stride, int bytes) {
     return r == 0 ? 1 : 16 / (r & -r);
 }
 
-// As many CTAs as fit the device at once, and no more than share the rows
-// evenly; a multiple of the period where rows start differently.  `waves`
-// times as many where each would have many rows of few values: the device
-// hands out the later ones as the first end, which evens out what the
-// memory's two halves take (2M x 48 float32: 115 us, 131 in one wave).
 template <typename Tag, typename K>
 int grid_of(K kernel, int threads, size_t smem, int64_t n, int groups, int period, int waves, int most, int sms) {
-    // the last answer, by what it depends on (one kernel, one architecture)
     static std::atomic<unsigned long long> known{0};
-    const unsigned long long key = (unsigned long long)(threads) << 40 | (unsigned long long)(smem) << 8;
-    const unsigned long long k = known.load(std::memory_order_relaxed);
-    int per_sm = int(k & 255);
-    if ((k ^ key) >> 8) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
-            per_sm = 1;
-        known.store(key | per_sm, std::memory_order_relaxed);
-    }
-    int64_t fit = int64_t(sms) * per_sm;
-    if (n >= fit * groups * 48) fit *= waves;
-    if (fit > most) fit = most;
-    const int64_t turns = (n + fit * groups - 1) / (fit * groups);
-    int64_t grid = (n + turns * groups - 1) / (turns * groups);
-    const int p = groups % period == 0 ? 1 : period;
-    grid = (grid + p - 1) / p * p;
-    return int(grid < 1 ? 1 : grid);
+    return ss::grid_of(&known, kernel, threads, smem, n, groups, period, waves, most, sms);
 }
 
 bool sizes_ok(int64_t n, int32_t D) { return n >= 0 && n < (int64_t(1) << 31) && D >= 1 && D <= kMaxD; }
@@ -989,8 +898,6 @@ bool too_wide(int32_t D) {
     constexpr int kVec = 16 / sizeof(T);
     return D / kVec > kMaxRowThreads * (kPerThread / kVec);
 }
-
-int wide_grid(int64_t n, int sms) { return int(n < int64_t(sms) * 8 ? n : int64_t(sms) * 8); }
 
 template <typename T>
 ss_status launch_fwd(const FwdArgs &a, int sms, cudaStream_t s) {

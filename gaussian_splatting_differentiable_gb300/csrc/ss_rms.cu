@@ -9,6 +9,7 @@
 
 #include "ss_internal.h"
 #include "ss_launch.cuh"
+#include "ss_norm.cuh"
 #include "ss_profile.h"
 #include "ss_rms.h"
 #include "ss_rows8.cuh"
@@ -17,7 +18,7 @@
 namespace ss {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kNormThreads;
 
 template <typename T>
 struct Rows {
@@ -36,9 +37,7 @@ struct Rows {
 // boundaries, head elements of the first not being the row's; a group of lanes takes every
 // step-th row with step a multiple of the rows after which starts repeat, so its columns stay
 // fixed.
-constexpr int kMaxRowThreads = 512;    // x 2 units = 8192 columns, the widest row held in registers
 constexpr int kMaxGroups = 4;          // rows of several warps side by side in a CTA: of two warps at least
-constexpr int kRowWarps = kMaxRowThreads / 32;
 
 struct Place {
     int lanes, shift;   // lanes = 1 << shift where !MULTI
@@ -67,34 +66,6 @@ Place place_of(int32_t D, bool shifted, bool single, int *nv, bool *multi) {
         pl.groups = kThreads / pl.lanes;
     }
     return pl;
-}
-
-// Sums K values over the row's lanes; every lane gets the same sums (one
-// fixed order).  MULTI alternates two buffers, so one barrier a sum is enough;
-// their slots past the row's warps hold zeros.
-template <int K, bool MULTI>
-__device__ __forceinline__ void row_sum(float (&v)[K], const Place &pl, int group, int lane,
-                                        float (*s_red)[K][kRowWarps], int &flip) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        if (MULTI || o < pl.lanes)
-#pragma unroll
-            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (!MULTI) return;
-    if ((lane & 31) == 0)
-#pragma unroll
-        for (int k = 0; k < K; ++k) s_red[flip][k][lane >> 5] = v[k];
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(pl.lanes) : "memory");
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const float4 *q = reinterpret_cast<const float4 *>(s_red[flip][k]);
-        v[k] = 0.0f;
-        for (int w = 0; w < pl.lanes; w += 128) {
-            const float4 t = q[w >> 7];
-            v[k] += (t.x + t.y) + (t.z + t.w);
-        }
-    }
-    flip ^= 1;
 }
 
 // Where a thread's units lie.
@@ -145,18 +116,6 @@ __device__ __forceinline__ void load_weights(F2 (&g)[NV][4], const void *w, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[k][i] = make_float2(f[2 * i], f[2 * i + 1]);
     }
-}
-
-// Sum over the CTA, the same value in every thread (fixed order).
-__device__ __forceinline__ float block_sum(float v, float *s_red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.0f;
-    for (int w = 0; w < kThreads / 32; ++w) t += s_red[w];
-    return t;
 }
 
 // What a warp's 32 consecutive columns hold, into 8 bits (v: 0 past the row).
@@ -273,7 +232,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(si
         }
         load(row + step);
         float sum[1] = {sum_of(acc)};
-        row_sum<1, MULTI>(sum, pl, group, lane, s_red[MULTI ? group : 0], flip);
+        row_sum<1, MULTI>(sum, pl.lanes, group, lane, s_red[MULTI ? group : 0], flip);
         const float r = __frsqrt_rn(__fdiv_rn(sum[0], width) + a.eps);
         const F2 rr = both(r);
 #pragma unroll
@@ -392,16 +351,9 @@ __global__ void __launch_bounds__(kThreads) k_norm8_bwd_rows_wide(BwdArgs a) {
     }
 }
 
-__device__ __forceinline__ void copy16(uint32_t smem, const void *p) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
-}
 __device__ __forceinline__ void copy8(uint32_t smem, const void *p) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem), "l"(p) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // What a stage of the backward's ring has of each thread, tensor after tensor, [units][16 bytes][threads]:
 // dy, dsum (not CENTRED), and h or what is held of it (two units' bytes where they are shifted).
 template <typename T, int NV, Lie LIE, bool CENTRED, bool HELD>
@@ -460,8 +412,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, bwd_ctas(si
         } else if (hi[k] > lo[k]) {
 #pragma unroll
             for (int v = 0; v < R::kVecs; ++v)
-                copy16(uint32_t(__cvta_generic_to_shared(to + v * apart)),
-                       reinterpret_cast<const uint4 *>(p + k * c.lanes * kUnit) + v);
+                copy16(to + v * apart, reinterpret_cast<const uint4 *>(p + k * c.lanes * kUnit) + v);
         }
     };
     using HeldUnit = typename std::conditional<LIE == kShifted, HeldAcross, Held>::type;
@@ -650,7 +601,7 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, bwd_ctas(si
         load(row + step);
         if (R::kUsed) fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * step);   // the slots read one row ago
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        row_sum<kSums, MULTI>(sum, pl, group, lane, s_red[MULTI ? group : 0], flip);
+        row_sum<kSums, MULTI>(sum, pl.lanes, group, lane, s_red[MULTI ? group : 0], flip);
         const F2 mag = both(-sum[0] * inv), ma = both(CENTRED ? -sum[kSums - 1] * inv : 0.0f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -708,62 +659,14 @@ __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, bwd_ctas(si
     }
 }
 
-// The partial sums of 32 columns of [dgamma | dbeta]: 32 slices of them side by
-// side, then the slices in order.
+// The partial sums of 32 columns of [dgamma | dbeta], or of dgamma alone.
 __global__ void __launch_bounds__(1024) k_norm8_bwd_final(const float *part, int parts, int32_t D, int cols,
                                                           void *dgamma, void *dbeta, int pdt) {
-    __shared__ float s_t[32][33];
-    wait_for_previous();
-    const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
-    const int j = blockIdx.x * 32 + c;
-    float t = 0.0f;
-    if (j < cols)
-#pragma unroll 4
-        for (int p = q; p < parts; p += 32) t += part[size_t(p) * cols + j];
-    s_t[q][c] = t;
-    __syncthreads();
-    t = s_t[c][q];                         // column q of the 32, slice c
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const int col = blockIdx.x * 32 + q;
-    if (c != 0 || col >= cols) return;
-    if (col < D)
-        store_param(dgamma, pdt, col, t);
-    else
-        store_param(dbeta, pdt, col - D, t);
+    add_up_parts(part, parts, D, cols, dgamma, dbeta, pdt);
 }
 
-// Partial sums of the weights' gradients that the workspace has room for.
 constexpr int kMaxSmem = 225 * 1024;   // 227 KB less 2 KB of static buffers
-constexpr int kMaxParts = 1024;
-int64_t weight_parts(int64_t n) { return n + kUnit < kMaxParts ? n + kUnit : kMaxParts; }   // a grid is rounded up to a period
-int wide_grid(int64_t n, int sms) { return int(n < int64_t(sms) * 8 ? n : int64_t(sms) * 8); }
-
-// As many CTAs as fit the device at once (times `waves` where each would have many
-// rows of few values: the later ones even out what the memory's two halves
-// take), and no more than share the rows evenly; a multiple of the period where rows start
-// differently.
-template <typename K>
-int grid_of(std::atomic<unsigned long long> *known, K kernel, int threads, size_t smem, int64_t n, int groups, int period,
-            int waves, int most, int sms) {
-    // the last answer, by what it depends on (one kernel, one architecture)
-    const unsigned long long key = (unsigned long long)(threads) << 40 | (unsigned long long)(smem) << 8;
-    const unsigned long long k = known->load(std::memory_order_relaxed);
-    int per_sm = int(k & 255);
-    if ((k ^ key) >> 8) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
-            per_sm = 1;
-        known->store(key | per_sm, std::memory_order_relaxed);
-    }
-    int64_t fit = int64_t(sms) * per_sm;
-    if (n >= fit * groups * 48) fit *= waves;
-    if (fit > most) fit = most;
-    const int64_t turns = (n + fit * groups - 1) / (fit * groups);
-    int64_t grid = (n + turns * groups - 1) / (turns * groups);
-    const int p = groups % period == 0 ? 1 : period;
-    grid = (grid + p - 1) / p * p;
-    return int(grid < 1 ? 1 : grid);
-}
+static_assert(kUnit == kMaxPeriod, "rows' starts repeat after a unit's elements at most");
 
 // f(NV, MULTI) of a place, as constants.
 template <bool SINGLE, typename F>
@@ -866,7 +769,7 @@ ss_status launch_bwd(const BwdArgs &a, int sms, cudaStream_t s) {
             const void *fn = (const void *)kernel;
             if ((st = ensure_dyn_smem(smem_ctx, &fn, 1, kMaxSmem, "k_norm8_bwd")) != SS_OK) return;
             static std::atomic<unsigned long long> known{0};
-            const int grid = alone ? 1 : grid_of(&known, kernel, threads, smem, a.n, pl.groups, period, 1, kMaxParts - kUnit, sms);
+            const int grid = alone ? 1 : grid_of(&known, kernel, threads, smem, a.n, pl.groups, period, 1, kMaxParts - kMaxPeriod, sms);
             BwdArgs b = a;
             if (!a.dgamma) b.part = nullptr;
             SS_LAUNCH("k_norm8_bwd", s, kernel<<<grid, threads, smem, s>>>(b, pl, alone));
