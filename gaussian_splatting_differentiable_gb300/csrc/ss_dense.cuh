@@ -29,6 +29,8 @@ namespace ss {
 constexpr int kStep = 16;              // rows of one product
 constexpr int kWide = 16;              // columns of x that a thread converts at a time
 constexpr int kChain32 = 2048, kChain16 = 16384;    // rows of a chain; dW in float32, in 16 bits
+// The split of the rows goes by this device's SMs as written down, and not as asked for: so the workspace's
+// size, which is asked for without a device, and a result's bits depend on the sizes and types alone.
 constexpr int kSms = 152;
 
 template <typename T>

@@ -171,11 +171,14 @@ struct FwdArgs {
 };
 
 // CTAs an SM that the registers are held down for, of narrow rows (0: wide ones as the compiler has them in CTAs of
-// up to 512).  Forward: 700,000 x 87 float16 with five 193 us, with four 207; 2M x 48 float32 with four 228, with
-// five 236; 60,000 x 500 float16 (two units a lane) with three 58, with two 71.
+// up to 512).  Forward, us: 700,000 x 87 float16 with five 193, with four 207; 2M x 48 float32 with four 228, with
+// five 236; two units a lane with three, two and four: 60,000 x 500 float32 89, 97 and 95 (three spill 72 to 232
+// bytes, two none), 60,000 x 512 float32 86, 83 and 92, 60,000 x 500 float16 60, 73 and 61, 60,000 x 501 bfloat16 79,
+// 101 and 74.
 constexpr int fwd_ctas(int bytes, int nv, bool multi) { return multi ? 0 : (nv == 2 ? 3 : (bytes == 2 ? 5 : 4)); }
-// Backward: 2M x 48 float32 with two 224 us, with three 282 (spills); 2M x 48 bfloat16 with three 142, with two
-// 169.
+// Backward: 2M x 48 float32 with two 224, with three 282 (spills); 2M x 48 bfloat16 with three 142, with two
+// 169; two units a lane (16 bits) with two, three and one: 60,000 x 500 float16 57, 116 and 78, 60,000 x 512
+// bfloat16 47, 79 and 56, the layer norm's 41, 93 and 52.
 constexpr int bwd_ctas(int bytes, int nv, bool multi) { return multi ? 0 : (bytes == 4 || nv == 2 ? 2 : 3); }
 
 // A row from registers: its sum with the residual, its square's mean, and every
