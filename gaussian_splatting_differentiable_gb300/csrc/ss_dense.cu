@@ -28,8 +28,8 @@ namespace {
 // warp issues the products; at the end the loaders read the sums out of the tensor memory.  A range is one
 // chain.
 //
-// 2M x 48 x 48 (484 MB float32, 292 bfloat16): 134 us and 84, at 3.6 TB/s; through registers 145 and 86.  Without
-// the conversions 95 and 77: what bounds it is the way of a stage through copies, barriers and
+// 2M x 48 x 48 (484 MB float32, 292 bfloat16): 135 us and 92 by ncu, at 3.7 and 3.3 TB/s.  In chains of 2816 rows 134
+// and 84; there, through registers 145 and 86, without the conversions 95 and 77: what bounds it is the way of a stage through copies, barriers and
 // products, of which shared memory has room for four at a time on an SM, and then the conversions.
 // (Stages of 32 rows: 156 us and more; three or four of them of raw rows ahead, or 128, 384 or 512
 // loaders: nothing gained.)
@@ -542,9 +542,9 @@ ss_status tile(const DenseArgs &a, cudaStream_t s, const char *who) {
 
 // A weight past one tile goes to the kernel of large ones, but for one of up to eight tiles in a row or a
 // column and many rows of dy in float32 or float16: that kernel writes dy's parts to memory and
-// reads them back, here dy is read once, and a tile's two launches cost 20 us (200,000 x 256 x 128 float32: 98 us
-// for 229, 400,000 x 48 x 256 float16: 88 for 252; 16384 rows of 512 x 48 float32: 60 for 45, of 256 x 128
-// float16: 37 for 35).  bfloat16 needs no parts (131,072 x 1024 x 32: 172 for 92), and 2 x 2 tiles read both twice.
+// reads them back, here dy is read once, and a tile's two launches cost 20 us (200,000 x 256 x 128 float32: 104 us
+// for 227, 400,000 x 48 x 256 float16: 88 for 252; 16384 rows of 512 x 48 float32: 60 for 45, of 256 x 128
+// float16: 37 for 35).  bfloat16 needs no parts (131,072 x 1024 x 32: 172 for 90), and 2 x 2 tiles read both twice.
 constexpr int32_t kSide = 128, kMostTiles = 8;
 constexpr int64_t kTileRows = 32768;
 bool dense_is_big(int64_t n, int32_t N, int32_t D, int dtype) {

@@ -5,9 +5,10 @@
 // anew would take longer than the products (8191 x 4096 x 4096 in tiles of 256 x 256: 285
 // us, of which the products 140).  So x, and dy where it is not bfloat16 on 16-byte boundaries, are
 // converted once, a chunk of rows at a time, into the workspace, and the products' kernel
-// has the copy engine bring both.  8191 x 4096 x 4096 bfloat16: 22 us and 162; the products' tiles come at 60
-// bytes a clock and SM (of 64 KB a stage, for 1024 clocks of products), the tensor cores are busy 73 % of
-// the time (304 tiles of 256 x 224, two to an SM).
+// has the copy engine bring both.  8191 x 4096 x 4096 bfloat16: 21 us and 158 by ncu; the products' tiles come at 62
+// bytes a clock and SM (of 64 KB a stage, for 1024 clocks of products), the tensor cores are busy 74 % of
+// the time (304 tiles of 256 x 224, two to an SM).  Into float32 223: the products wait while a chain leaves the tensor
+// memory.
 #include <cuda_runtime.h>
 
 #include <atomic>

@@ -1,5 +1,6 @@
 // Root-mean-square norm, and the gradients of both norms from rows kept in 8
-// bits (model: include/ss_rms.h).
+// bits (model: include/ss_rms.h).  Times that stand alone are a kernel's by ncu; where two
+// are compared they are both calls', some microseconds more.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -183,9 +184,9 @@ constexpr int bwd_ctas(int bytes, int nv, bool multi) { return multi ? 0 : (byte
 
 // A row from registers: its sum with the residual, its square's mean, and every
 // output that is wanted.  The next row's loads are in flight meanwhile.  (kShifted: without
-// outputs in 8 bits, whose groups begin with the row.)  2M x 48 float32 (1.54 GB): 224 us, at a
-// copy's rate; 8191 x 4096 bfloat16 into e4m3 (235 MB) 50 (35), with 57 % of the issue slots taken by 15 warps
-// an SM; 16384 x 1001 bfloat16 33 (20).
+// outputs in 8 bits, whose groups begin with the row.)  2M x 48 float32 (1.54 GB): 222 us, at a
+// copy's rate; 8191 x 4096 bfloat16 into e4m3 (235 MB) 52 (35), with 57 % of the issue slots taken by 15 warps
+// an SM; 16384 x 1001 bfloat16 a call 33 (20).
 template <typename T, int NV, bool MULTI, Lie LIE, bool RES>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, fwd_ctas(sizeof(T), NV, MULTI)) k_rms_fwd(FwdArgs a, Place pl) {
     __shared__ alignas(16) float s_red[MULTI ? kMaxGroups : 1][2][1][kRowWarps];
@@ -372,14 +373,14 @@ struct Ring {
 // A row's dy and h (FMT >= 0: kept in 8 bits) through a ring in shared memory, asynchronously, kStages
 // - 1 rows ahead: every thread copies into slots of its own and reads only those, so the
 // ring needs no barrier and the copies in flight no registers.  A unit of float32 would be two
-// such copies, each of half of every 32-byte sector, which L2 reads twice (2M x 48: 283 us); these come by
-// one load of 32 bytes into registers, a row ahead (227).  The weights' sums stay in
+// such copies, each of half of every 32-byte sector, which L2 reads twice; these come by
+// one load of 32 bytes into registers, a row ahead (2M x 48: 227 us a call for 283).  The weights' sums stay in
 // registers over all of a CTA's rows and leave one partial sum a CTA in a.part (none where it is
 // NULL), or, where one CTA has all rows, the gradients themselves.
 //
-// 2M x 48 float32 from int8 (1.26 GB): 220 us at 5.7 TB/s; 8191 x 4096 bfloat16 from e4m3 (236 MB) 45 (35 at a
-// copy's rate), 16384 x 1001 bfloat16 from int8 (83 MB) 32 (12): both have 15 warps an SM for the registers that
-// x, dy and the weights' sums take, and wait on one another's instructions, 54 and 58 % of the issue slots taken.
+// 2M x 48 float32 from int8 (1.26 GB): 222 us at 5.6 TB/s; 8191 x 4096 bfloat16 from e4m3 (236 MB) 46 (35 at a
+// copy's rate), 16384 x 1001 bfloat16 from int8 (83 MB) 34 (12): both have 15 warps an SM for the registers that
+// x, dy and the weights' sums take, and wait on one another's instructions, 52 and 58 % of the issue slots taken.
 template <typename T, int NV, bool MULTI, Lie LIE, bool CENTRED, int FMT>
 __global__ void __launch_bounds__(MULTI ? kMaxRowThreads : kThreads, bwd_ctas(sizeof(T), NV, MULTI)) k_norm8_bwd(BwdArgs a, Place pl, bool alone) {
     constexpr int kSums = CENTRED ? 2 : 1;

@@ -38,8 +38,8 @@ struct Walk {
     }
 };
 
-// Bound by memory.  A unit at a time and many warps (2M x 48 float32: 82 us; two units' loads in
-// flight 87, four 92, with the registers that they take).
+// Bound by memory.  A unit at a time and many warps (2M x 48 float32: 79 us by ncu; a call 82, with
+// two units' loads in flight 87, four 92, with the registers that they take).
 template <typename T, int FMT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_rows8_pack(const T *x, int64_t xs, int64_t n, int32_t D, Rows8 out) {
     for (Walk w(n, D); __any_sync(0xffffffffu, w.row < n); w.next()) {
@@ -60,8 +60,8 @@ __device__ __forceinline__ F2 held_to<__half>(F2 v) {
                        isnan(v.y) ? v.y : fminf(fmaxf(v.y, -65504.0f), 65504.0f));
 }
 
-// 2M x 48 to float32 (484 MB, four fifths of it stores): 74 us.  Where x's rows start off their blocks' boundaries, units lie on them all the same, and take what
-// is held from two units (one more of them a row then).
+// 2M x 48 to float32 (484 MB, four fifths of it stores): 75 us by ncu.  Where x's rows start off their blocks' boundaries,
+// units lie on them all the same, and take what is held from two units (one more of them a row then).
 template <typename T, int FMT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_rows8_unpack(Rows8 in, int64_t n, int32_t D, T *x, int64_t xs) {
     for (Walk w(n, ALIGNED ? D : D + kUnit - 1); w.row < n; w.next()) {
