@@ -29,9 +29,9 @@ namespace {
 // chain.
 //
 // 2M x 48 x 48 (484 MB float32, 292 bfloat16): 135 us and 92 by ncu, at 3.7 and 3.3 TB/s.  In chains of 2816 rows 134
-// and 84; there, through registers 145 and 86, without the conversions 95 and 77: what bounds it is the way of a stage through copies, barriers and
-// products, of which shared memory has room for four at a time on an SM, and then the conversions.
-// (Stages of 32 rows: 156 us and more; three or four of them of raw rows ahead, or 128, 384 or 512
+// and 84; there, through registers 145 and 86, without the conversions 95 and 77: what bounds it is the way of a stage
+// through copies, barriers and products, of which shared memory has room for four at a time on an SM, and then the
+// conversions.  (Stages of 32 rows: 156 us and more; three or four of them of raw rows ahead, or 128, 384 or 512
 // loaders: nothing gained.)
 //
 // TI = 64 (N up to 64): two parts of dy side by side are the 128 rows of one product, so
@@ -586,8 +586,8 @@ void dense_join(const DenseArgs &a, bool weight, cudaStream_t s, int sms) {
 using namespace ss;
 
 static ss_status dense_grad8(const char *who, const void *dy, ss_dtype dtype, int64_t dy_stride, const ss_rows8 *x, int64_t n,
-                          int32_t N, int32_t D, void *dweight, int64_t dweight_stride, void *dbias, ss_dtype grad_dtype,
-                          void *workspace, size_t workspace_bytes, uint32_t tries, int sent, ss_stream_t stream) {
+                             int32_t N, int32_t D, void *dweight, int64_t dweight_stride, void *dbias, ss_dtype grad_dtype,
+                             void *workspace, size_t workspace_bytes, uint32_t tries, int sent, ss_stream_t stream) {
     clear_error();
     if (!dense_sizes_ok(n, N, D))
         return fail(SS_ERR_UNSUPPORTED, "%s: %lld rows, %d x %d outside 0..2^31-1, 1..%d", who, (long long)n, N, D,
