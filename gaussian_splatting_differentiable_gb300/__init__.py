@@ -775,6 +775,8 @@ class Rows8:
         piece = 16 if D > 32 else 8     # 16-byte rows where that adds little to them
         stride, groups = (D + piece - 1) // piece * piece, (D + 31) // 32
         self._buf = torch.empty(n, stride, dtype=torch.uint8, device=d)
+        # what a caller does not reach through q (packing writes zeros there, too, whichever comes first)
+        self._buf[:, D:(D + 7) // 8 * 8].zero_()
         self._q = self._buf.view(format)[:, :D]
         self._scales = torch.empty(n, groups, dtype=torch.uint8, device=d)
         self._c = _lib.SsRows8(self._buf.data_ptr(), stride, self._scales.data_ptr(), groups, code,

@@ -41,7 +41,8 @@ typedef enum {
 
 /* Rows of D values in 8 bits; a HOST struct, read during the call.  Row i's
  * values begin at q + i * q_stride and take D bytes, rounded up to whole 8 (the
- * bytes past D are written as zeros); its scales are the bytes
+ * bytes past D are written as zeros, and whoever fills rows without packing writes
+ * zeros there, too: the norms' gradients read them); its scales are the bytes
  * scales + i * scale_stride + (0 .. (D + 31) / 32 - 1). */
 typedef struct {
     void *q;              /* device, 8-byte aligned */
